@@ -112,7 +112,8 @@ def work(c):
         return {"bytes": kv * c["Hkv"] * 2 * D * el + c["B"] * c["Hq"] * (4 * D + 4), "flops": 4 * D * c["Hq"] * sum(lens)}
     if c["kind"] == "fork":
         tiles = -(-(c["L"] % c["ps"]) // TILE)
-        return {"bytes": 2 * c["n"] * c["layers"] * c["Hkv"] * tiles * 2 * TILE * D * el + 16 * c["n"] * _pages(c["L"], c["ps"])}
+        # one parent: its page in use is read once, and written n times
+        return {"bytes": (1 + c["n"]) * c["layers"] * c["Hkv"] * tiles * 2 * TILE * D * el + 8 * (1 + c["n"]) * _pages(c["L"], c["ps"])}
     if c["kind"] == "compact":
         return {"bytes": 2 * c["moves"] * c["layers"] * c["Hkv"] * c["ps"] * 2 * D * el + 8 * c["B"] * c["max_pages"]}
     T = c["B"] if c["kind"] == "append" else c["tokens"]
