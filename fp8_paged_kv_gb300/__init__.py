@@ -68,6 +68,27 @@ SIGNATURES = {
                                            _I32, _P]),
     "fpk_decode_step_bf16": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P,
                                             _SZ, _I32, _F, _I32, _I32, _I32, _I32, _I32, _I32, _P]),
+    "fpk_prefix_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "fpk_paged_decode_attn_fp8_prefix": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _I32,
+                                                        _P, _P, _P, _SZ, _F, _I32, _I32, _I32, _I32,
+                                                        _I32, _I32, _P]),
+    "fpk_paged_decode_attn_bf16_prefix": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _P, _P, _I32,
+                                                         _P, _P, _P, _SZ, _F, _I32, _I32, _I32, _I32,
+                                                         _I32, _I32, _P]),
+    "fpk_rope_append_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _P, _P,
+                                           _I32, _I32, _F, _I32, _I32, _I32, _I32, _I32, _I32, _P]),
+    "fpk_rope_append_bf16": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _P, _P,
+                                            _I32, _I32, _F, _I32, _I32, _I32, _I32, _I32, _I32, _P]),
+    "fpk_rope_prefill_fp8": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _I32,
+                                            _P, _P, _P, _I32, _I32, _F, _I32, _I32, _I32, _I32, _I32,
+                                            _I32, _P]),
+    "fpk_rope_prefill_bf16": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _I32,
+                                             _P, _P, _P, _I32, _I32, _F, _I32, _I32, _I32, _I32, _I32,
+                                             _I32, _P]),
+    "fpk_kv_fork": (ctypes.c_int, [_P, _I32, _I32, _I64, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _I32,
+                                   _I32, _I32, _I32, _I32, _I32, _P]),
+    "fpk_kv_compact": (ctypes.c_int, [_P, _I32, _I32, _I64, _P, _I32, _P, _P, _P, _P, _P, _I32,
+                                      _I32, _I32, _I32, _I32, _I32, _P]),
     "fpk_decode_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32), _P]),
     "fpk_w4_quantize": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _P]),
     "fpk_w4_gemv": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I32, _I32, _P]),
@@ -126,6 +147,29 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+def _expect(t, name, shape):
+    """The tensor's shape, where the call's other arguments settle it (None: an argument left out)."""
+    if t is not None and tuple(t.shape) != shape:
+        raise FpkError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _expect_pool(kv_pool, layers, num_pages, Hkv, page_size, D):
+    want = 2 * layers * num_pages * Hkv * page_size * D
+    if layers < 1 or kv_pool.numel() != want:
+        raise FpkError(f"kv_pool has {kv_pool.numel()} elements, expected {want}")
+
+
+def _same_device(*tensors):
+    """Every tensor is on the current device: the launch goes to that device's stream."""
+    dev = None
+    for t in tensors:
+        if t is None or not t.is_cuda:
+            continue  # host tensors are refused by name when their pointer is taken
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise FpkError(f"tensor on device {t.get_device()}, the current device is {dev}")
 
 
 _U8 = torch.uint8
@@ -343,6 +387,203 @@ def fpk_paged_decode_attn_fp8_noalloc(q, kv_pool, k_scale, v_scale, page_table, 
         _ptr(abort_mask, _U8, "abort_mask", True), _ptr(out, _F32, "out"),
         _ptr(lse, _F32, "lse", True), num_splits, sm_scale, B, Hq, Hkv, D, page_size, num_pages,
         _stream(stream)), "fpk_paged_decode_attn_fp8_noalloc")
+
+
+# ---------------------------------------------------------- shared prefixes
+def fpk_prefix_workspace_bytes(B, Hq, Hkv, D=128) -> int:
+    n = load_library().fpk_prefix_workspace_bytes(B, Hq, Hkv, D)
+    if n == 0 and B > 0:
+        raise FpkError("fpk_prefix_workspace_bytes: invalid shape or no CUDA device")
+    return int(n)
+
+
+def _groups(group_starts, prefix_lens):
+    n = prefix_lens.numel()
+    if group_starts.numel() != n + 1:
+        raise FpkError(f"group_starts has {group_starts.numel()} entries, expected {n + 1} "
+                       "(one more than prefix_lens)")
+    return n
+
+
+def _attn_shapes(q, page_table, seq_lens, abort_mask, out, lse):
+    B, Hq, D = q.shape
+    _expect(page_table, "page_table", (B, page_table.shape[-1]))
+    _expect(seq_lens, "seq_lens", (B,))
+    _expect(abort_mask, "abort_mask", (B,))
+    _expect(out, "out", (B, Hq, D))
+    _expect(lse, "lse", (B, Hq))
+    return B, Hq, D
+
+
+def fpk_paged_decode_attn_fp8_prefix(q, kv_pool, k_scale, v_scale, page_table, seq_lens, abort_mask,
+                                     group_starts, prefix_lens, out, lse, workspace, *, Hkv, page_size,
+                                     num_pages, sm_scale, stream=None):
+    """Decode attention that reads each group's shared prefix once (out: bf16)."""
+    B, Hq, D = _attn_shapes(q, page_table, seq_lens, abort_mask, out, lse)
+    n_groups = _groups(group_starts, prefix_lens)
+    _expect_pool(kv_pool, 1, num_pages, Hkv, page_size, D)
+    _same_device(q, kv_pool, k_scale, v_scale, page_table, seq_lens, abort_mask, group_starts,
+                 prefix_lens, out, lse, workspace)
+    _check(load_library().fpk_paged_decode_attn_fp8_prefix(
+        _ptr(q, _BF16, "q"), _ptr(kv_pool, _U8, "kv_pool"),
+        _ptr(k_scale, _F32, "k_scale"), _ptr(v_scale, _F32, "v_scale"),
+        _ptr(page_table, _I32T, "page_table"), page_table.shape[1], _ptr(seq_lens, _I32T, "seq_lens"),
+        _ptr(abort_mask, _U8, "abort_mask", True), _ptr(group_starts, _I32T, "group_starts"),
+        _ptr(prefix_lens, _I32T, "prefix_lens"), n_groups,
+        _ptr(out, _BF16, "out"), _ptr(lse, _F32, "lse", True), _ptr(workspace, _U8, "workspace"),
+        workspace.numel(), sm_scale, B, Hq, Hkv, D, page_size, num_pages, _stream(stream)),
+        "fpk_paged_decode_attn_fp8_prefix")
+
+
+def fpk_paged_decode_attn_bf16_prefix(q, kv_pool, page_table, seq_lens, abort_mask, group_starts,
+                                      prefix_lens, out, lse, workspace, *, Hkv, page_size, num_pages,
+                                      sm_scale, stream=None):
+    """BF16-cache variant of fpk_paged_decode_attn_fp8_prefix."""
+    B, Hq, D = _attn_shapes(q, page_table, seq_lens, abort_mask, out, lse)
+    n_groups = _groups(group_starts, prefix_lens)
+    _expect_pool(kv_pool, 1, num_pages, Hkv, page_size, D)
+    _same_device(q, kv_pool, page_table, seq_lens, abort_mask, group_starts, prefix_lens, out, lse,
+                 workspace)
+    _check(load_library().fpk_paged_decode_attn_bf16_prefix(
+        _ptr(q, _BF16, "q"), _ptr(kv_pool, _BF16_LIKE, "kv_pool"),
+        _ptr(page_table, _I32T, "page_table"), page_table.shape[1], _ptr(seq_lens, _I32T, "seq_lens"),
+        _ptr(abort_mask, _U8, "abort_mask", True), _ptr(group_starts, _I32T, "group_starts"),
+        _ptr(prefix_lens, _I32T, "prefix_lens"), n_groups,
+        _ptr(out, _BF16, "out"), _ptr(lse, _F32, "lse", True), _ptr(workspace, _U8, "workspace"),
+        workspace.numel(), sm_scale, B, Hq, Hkv, D, page_size, num_pages, _stream(stream)),
+        "fpk_paged_decode_attn_bf16_prefix")
+
+
+# --------------------------------------------------------- rotary positions
+def _rope_shapes(q, k, v, inv_freq, q_out, page_table, live_tags, expected_tags, abort_mask, Hkv,
+                 rot_dim, rows):
+    T, _, D = k.shape
+    _expect(k, "k", (T, Hkv, D))
+    _expect(v, "v", (T, Hkv, D))
+    Hq = 0 if q is None else q.shape[1]
+    if q is not None:
+        _expect(q, "q", (T, Hq, D))
+        _expect(q_out, "q_out", (T, Hq, D))
+    _expect(inv_freq, "inv_freq", (rot_dim // 2,))
+    B = page_table.shape[0]
+    if rows is not None and T != B:
+        raise FpkError(f"k has {T} rows for {B} requests")
+    _expect(expected_tags, "expected_tags", tuple(page_table.shape))
+    _expect(abort_mask, "abort_mask", (B,))
+    _same_device(q, k, v, inv_freq, q_out, page_table, live_tags, expected_tags, abort_mask)
+    return T, B, Hq, D
+
+
+def _rope(name, fp8, q, k, v, pos, inv_freq, q_out, kv_pool, scales, page_table, live_tags,
+          expected_tags, abort_mask, Hkv, page_size, num_pages, rot_dim, interleaved, rot_scale,
+          stream):
+    """pos: (seq_lens,) of an append or (cu_seqlens, start_pos) of a prefill."""
+    append = len(pos) == 1
+    T, B, Hq, D = _rope_shapes(q, k, v, inv_freq, q_out, page_table, live_tags, expected_tags,
+                               abort_mask, Hkv, rot_dim, pos[0] if append else None)
+    _expect_pool(kv_pool, 1, num_pages, Hkv, page_size, D)
+    _expect(live_tags, "live_tags", (num_pages,))
+    _same_device(kv_pool, *pos, *scales)
+    if append:
+        _expect(pos[0], "seq_lens", (B,))
+        mid, places = [], [_ptr(pos[0], _I32T, "seq_lens")]
+    else:
+        _expect(pos[0], "cu_seqlens", (B + 1,))
+        _expect(pos[1], "start_pos", (B,))
+        mid, places = [_ptr(pos[0], _I32T, "cu_seqlens"), T, _ptr(pos[1], _I32T, "start_pos", True)], []
+    _check(getattr(load_library(), name)(
+        _ptr(q, _BF16, "q", True), _ptr(k, _BF16, "k"), _ptr(v, _BF16, "v"), *mid,
+        _ptr(inv_freq, _F32, "inv_freq"), _ptr(q_out, _BF16, "q_out", True),
+        _ptr(kv_pool, _U8 if fp8 else _BF16_LIKE, "kv_pool"),
+        *(_ptr(s, _F32, n) for s, n in zip(scales, ("k_scale", "v_scale"))),
+        _ptr(page_table, _I32T, "page_table"), page_table.shape[1], *places,
+        _ptr(live_tags, _TAGS, "live_tags", True), _ptr(expected_tags, _TAGS, "expected_tags", True),
+        _ptr(abort_mask, _U8, "abort_mask", True), rot_dim, int(interleaved), rot_scale, B, Hq, Hkv, D,
+        page_size, num_pages, _stream(stream)), name)
+
+
+def fpk_rope_append_fp8(q, k_new, v_new, inv_freq, q_out, kv_pool, k_scale, v_scale, page_table,
+                        seq_lens, live_tags=None, expected_tags=None, abort_mask=None, *, Hkv,
+                        page_size, num_pages, rot_dim, interleaved=False, rot_scale=1.0, stream=None):
+    _rope("fpk_rope_append_fp8", True, q, k_new, v_new, (seq_lens,), inv_freq, q_out, kv_pool,
+          (k_scale, v_scale), page_table, live_tags, expected_tags, abort_mask, Hkv, page_size,
+          num_pages, rot_dim, interleaved, rot_scale, stream)
+
+
+def fpk_rope_append_bf16(q, k_new, v_new, inv_freq, q_out, kv_pool, page_table, seq_lens,
+                         live_tags=None, expected_tags=None, abort_mask=None, *, Hkv, page_size,
+                         num_pages, rot_dim, interleaved=False, rot_scale=1.0, stream=None):
+    _rope("fpk_rope_append_bf16", False, q, k_new, v_new, (seq_lens,), inv_freq, q_out, kv_pool, (),
+          page_table, live_tags, expected_tags, abort_mask, Hkv, page_size, num_pages, rot_dim,
+          interleaved, rot_scale, stream)
+
+
+def fpk_rope_prefill_fp8(q, k, v, cu_seqlens, start_pos, inv_freq, q_out, kv_pool, k_scale, v_scale,
+                         page_table, live_tags=None, expected_tags=None, abort_mask=None, *, Hkv,
+                         page_size, num_pages, rot_dim, interleaved=False, rot_scale=1.0, stream=None):
+    _rope("fpk_rope_prefill_fp8", True, q, k, v, (cu_seqlens, start_pos), inv_freq, q_out, kv_pool,
+          (k_scale, v_scale), page_table, live_tags, expected_tags, abort_mask, Hkv, page_size,
+          num_pages, rot_dim, interleaved, rot_scale, stream)
+
+
+def fpk_rope_prefill_bf16(q, k, v, cu_seqlens, start_pos, inv_freq, q_out, kv_pool, page_table,
+                          live_tags=None, expected_tags=None, abort_mask=None, *, Hkv, page_size,
+                          num_pages, rot_dim, interleaved=False, rot_scale=1.0, stream=None):
+    _rope("fpk_rope_prefill_bf16", False, q, k, v, (cu_seqlens, start_pos), inv_freq, q_out, kv_pool,
+          (), page_table, live_tags, expected_tags, abort_mask, Hkv, page_size, num_pages, rot_dim,
+          interleaved, rot_scale, stream)
+
+
+# ---------------------------------------------------------- forks and moves
+def _pool_layers(kv_pool, layers, num_pages, Hkv, page_size, D):
+    """(element bytes, bytes from one layer's pool to the next)"""
+    _expect_pool(kv_pool, layers, num_pages, Hkv, page_size, D)
+    el = kv_pool.element_size()
+    return el, 2 * num_pages * Hkv * page_size * D * el
+
+
+def _table_shapes(page_table, expected_tags, seq_lens, live_tags, abort_mask, num_pages):
+    B, max_pages = page_table.shape
+    _expect(expected_tags, "expected_tags", (B, max_pages))
+    _expect(seq_lens, "seq_lens", (B,))
+    _expect(live_tags, "live_tags", (num_pages,))
+    _expect(abort_mask, "abort_mask", (B,))
+    return B, max_pages
+
+
+def fpk_kv_fork(kv_pool, page_table, expected_tags, seq_lens, live_tags, abort_mask, parent, child,
+                fresh, *, layers=1, Hkv, D, page_size, num_pages, stream=None):
+    """Rows child[i] take over rows parent[i]: full pages shared, the page in use
+    copied to fresh[i] in all layers of kv_pool ([layers][one pool], contiguous)."""
+    B, max_pages = _table_shapes(page_table, expected_tags, seq_lens, live_tags, abort_mask, num_pages)
+    el, stride = _pool_layers(kv_pool, layers, num_pages, Hkv, page_size, D)
+    n = parent.numel()
+    _expect(child, "child", (n,))
+    _expect(fresh, "fresh", (n,))
+    _same_device(kv_pool, page_table, expected_tags, seq_lens, live_tags, abort_mask, parent, child, fresh)
+    _check(load_library().fpk_kv_fork(
+        _ptr(kv_pool, (_U8, *_BF16_LIKE), "kv_pool"), el, layers, stride,
+        _ptr(page_table, _I32T, "page_table"), max_pages, _ptr(expected_tags, _TAGS, "expected_tags"),
+        _ptr(seq_lens, _I32T, "seq_lens"), _ptr(live_tags, _TAGS, "live_tags"),
+        _ptr(abort_mask, _U8, "abort_mask", True), _ptr(parent, _I32T, "parent"),
+        _ptr(child, _I32T, "child"), _ptr(fresh, _I32T, "fresh"), n, B, Hkv, D, page_size, num_pages,
+        _stream(stream)), "fpk_kv_fork")
+
+
+def fpk_kv_compact(kv_pool, page_table, expected_tags, seq_lens, live_tags, src, dst, *, layers=1,
+                   Hkv, D, page_size, num_pages, stream=None):
+    """Pages src[i] (ascending) move to dst[i] in all layers of kv_pool; tables and tags follow."""
+    B, max_pages = _table_shapes(page_table, expected_tags, seq_lens, live_tags, None, num_pages)
+    el, stride = _pool_layers(kv_pool, layers, num_pages, Hkv, page_size, D)
+    n = src.numel()
+    _expect(dst, "dst", (n,))
+    _same_device(kv_pool, page_table, expected_tags, seq_lens, live_tags, src, dst)
+    _check(load_library().fpk_kv_compact(
+        _ptr(kv_pool, (_U8, *_BF16_LIKE), "kv_pool"), el, layers, stride,
+        _ptr(page_table, _I32T, "page_table"), max_pages, _ptr(expected_tags, _TAGS, "expected_tags"),
+        _ptr(seq_lens, _I32T, "seq_lens"), _ptr(live_tags, _TAGS, "live_tags"),
+        _ptr(src, _I32T, "src"), _ptr(dst, _I32T, "dst"), n, B, Hkv, D, page_size, num_pages,
+        _stream(stream)), "fpk_kv_compact")
 
 
 def fpk_decode_status(workspace, stream=None) -> int:

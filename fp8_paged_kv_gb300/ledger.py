@@ -12,6 +12,11 @@ matches.  The ledger is that bookkeeping for one layer's pool:
   the ledger orders is applied on the device by ``fpk_page_tags_bump``);
 * per request, the table row (page ids) and the expected tags.
 
+Requests may share pages: ``fork`` makes one request hold another's full pages
+(``fpk_kv_fork`` applies it on the device) and ``release`` frees a page when its
+last holder leaves.  ``compact`` plans the moves that bring all pages in use to
+the front of the pool (``fpk_kv_compact`` applies them).
+
 Every allocation is a reallocation and bumps the page's tag; the pages
 returned by ``allocate`` are the bump list for that step.  The ledger does no
 GPU work itself and holds none of the kernels' arithmetic beyond the +1 it
@@ -36,13 +41,18 @@ class PageLedger:
         self.page_table = np.full((B, max_pages), -1, np.int32)
         self.expected = np.zeros((B, max_pages), np.uint32)
         self.lens = np.zeros(B, np.int32)
-        self.owner = np.full(num_pages, -1, np.int64)
+        self.owner = np.full(num_pages, -1, np.int64)      # one of a page's holders, -1: free
+        self.held = [set() for _ in range(B)]               # pages each request holds
+        self.refs = np.zeros(num_pages, np.int64)           # holders of each page
         if page_table is not None:
             self.page_table[:] = page_table
             m = page_table >= 0
             self.expected[m] = self.tags[page_table[m]]
             rows, _ = np.nonzero(m)
             self.owner[page_table[m]] = rows
+            for r, p in zip(rows, page_table[m]):
+                self.held[r].add(int(p))
+            np.add.at(self.refs, page_table[m], 1)
             self.lens[:] = seq_lens
         self.free = deque(int(p) for p in np.flatnonzero(self.owner < 0))
 
@@ -61,6 +71,8 @@ class PageLedger:
         for i, p in enumerate(got):
             self.tags[p] = self.tags[p] + np.uint32(1)
             self.owner[p] = r
+            self.refs[p] = 1
+            self.held[r].add(p)
             self.page_table[r, have + i] = p
             self.expected[r, have + i] = self.tags[p]
         return got
@@ -70,12 +82,20 @@ class PageLedger:
         return int(np.count_nonzero(row >= 0))
 
     def release(self, r: int) -> list[int]:
-        """Request r finished (or was aborted): its pages return to the free list."""
+        """Request r finished (or was aborted): its pages return to the free list, but
+        for those that another request still holds.  Returns the pages freed."""
         row = self.page_table[r]
-        pages = [int(p) for p in row[row >= 0] if 0 <= p < self.num_pages and self.owner[p] == r]
-        for p in pages:
-            self.owner[p] = -1
-            self.free.append(p)
+        mine = [int(p) for p in row[row >= 0] if int(p) in self.held[r]]
+        self.held[r].clear()
+        pages = []
+        for p in mine:
+            self.refs[p] -= 1
+            if self.refs[p] == 0:
+                self.owner[p] = -1
+                self.free.append(p)
+                pages.append(p)
+            elif self.owner[p] == r:
+                self.owner[p] = next(i for i in range(self.B) if p in self.held[i])
         self.page_table[r] = -1
         self.expected[r] = 0
         self.lens[r] = 0
@@ -92,6 +112,50 @@ class PageLedger:
         self.lens[r] += 1
         need = self.pages_of(r) - self.pages_of_table(r)
         return self.allocate(r, need) if need > 0 else []
+
+    # -------------------------------------------------- sharing and moving
+    def fork(self, parent: int, child: int) -> int:
+        """Empty slot `child` takes over request `parent`: its full pages are shared,
+        and where its last page is not full the child gets a page of its own, to
+        which fpk_kv_fork copies it.  Returns that page (-1: none was needed)."""
+        assert self.pages_of_table(child) == 0, "slot still holds pages"
+        L = int(self.lens[parent])
+        full = L // self.page_size
+        row = self.page_table[parent, :full]
+        if not all(int(p) in self.held[parent] for p in row):
+            raise RuntimeError(f"request {parent}: a page it maps is not its own")
+        if L % self.page_size and not self.free:
+            raise RuntimeError("pool exhausted")
+        self.page_table[child, :full] = row
+        self.expected[child, :full] = self.expected[parent, :full]
+        self.held[child].update(int(p) for p in row)
+        self.refs[row] += 1
+        self.lens[child] = L
+        return self.allocate(child, 1)[0] if L % self.page_size else -1
+
+    def compact(self) -> tuple[np.ndarray, np.ndarray]:
+        """Moves (src ascending, dst) after which the pages in use are the pool's
+        first ones.  Tables, tags and holders follow, as fpk_kv_compact leaves
+        them on the device; stale entries stay."""
+        used = np.flatnonzero(self.refs > 0)
+        src = used[used >= used.size].astype(np.int32)
+        dst = np.flatnonzero(self.refs[:used.size] == 0).astype(np.int32)
+        to = np.arange(self.num_pages, dtype=np.int32)
+        to[src] = dst
+        at = self.page_table
+        held = np.arange(self.max_pages) < -(-self.lens[:, None] // self.page_size)
+        known = held & (at >= 0) & (at < self.num_pages)
+        safe = np.where(known, at, 0)
+        moved = known & (to[safe] != safe) & (self.expected == self.tags[safe])
+        self.tags[dst] += np.uint32(1)
+        at[moved] = to[safe[moved]]
+        self.expected[moved] = self.tags[at[moved]]
+        self.refs[dst], self.owner[dst] = self.refs[src], self.owner[src]
+        self.refs[src], self.owner[src] = 0, -1
+        self.held = [{int(to[p]) for p in h} for h in self.held]
+        taken = set(dst.tolist())
+        self.free = deque([p for p in self.free if p not in taken] + src.tolist())
+        return src, dst
 
     # ------------------------------------------------------ stale mappings
     def corrupt(self, r: int, rng: np.random.Generator) -> tuple[int, str]:

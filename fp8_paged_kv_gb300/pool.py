@@ -16,9 +16,11 @@ import torch
 
 from . import (fpk_decode_append_check_bf16, fpk_decode_append_check_fp8, fpk_decode_step_bf16,
                fpk_decode_step_fp8, fpk_decode_workspace_bytes, fpk_kv_append_bf16, fpk_kv_append_fp8,
-               fpk_kv_prefill_bf16, fpk_kv_prefill_fp8, fpk_page_tags_bump,
-               fpk_page_tags_validate, fpk_paged_decode_attn_bf16, fpk_paged_decode_attn_fp8,
-               fpk_paged_decode_attn_fp8_tc)
+               fpk_kv_compact, fpk_kv_fork, fpk_kv_prefill_bf16, fpk_kv_prefill_fp8,
+               fpk_page_tags_bump, fpk_page_tags_validate, fpk_paged_decode_attn_bf16,
+               fpk_paged_decode_attn_bf16_prefix, fpk_paged_decode_attn_fp8,
+               fpk_paged_decode_attn_fp8_prefix, fpk_paged_decode_attn_fp8_tc,
+               fpk_prefix_workspace_bytes, fpk_rope_append_bf16, fpk_rope_append_fp8)
 
 NAN_E4M3 = 0x7F          # e4m3 NaN code: fills slots no token was written to
 NAN_BF16 = 0x7FC0
@@ -82,6 +84,7 @@ class DecodePool:
         ws = fpk_decode_workspace_bytes(wl.B, wl.Hq, wl.Hkv, wl.D, self.num_splits)
         self.workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=dev)
         self.count_aborts = True
+        self.out16 = self.prefix_workspace = None  # made by the first attend_shared()
 
     def _new_io(self):
         wl, dev = self.wl, self.device
@@ -185,6 +188,52 @@ class DecodePool:
         else:
             fpk_paged_decode_attn_bf16(self.q, self.kv_pool, self.page_table,
                                        self.seq_lens, mask, self.out, self.lse, self.workspace, **kw)
+
+    def attend_shared(self, group_starts, prefix_lens, use_mask: bool = True, stream=None):
+        """Attention that reads each group's shared prefix once; bf16 results in out16,
+        lse as attend().  group_starts int32 [n + 1] and prefix_lens int32 [n] on the
+        device: requests [group_starts[g], group_starts[g + 1]) share their first
+        prefix_lens[g] tokens' pages."""
+        wl = self.wl
+        if self.out16 is None:
+            self.out16 = torch.zeros((wl.B, wl.Hq, wl.D), dtype=torch.bfloat16, device=self.device)
+            ws = fpk_prefix_workspace_bytes(wl.B, wl.Hq, wl.Hkv, wl.D)
+            self.prefix_workspace = torch.zeros(ws, dtype=torch.uint8, device=self.device)
+        mask = self.abort_mask if use_mask else None
+        args = (self.page_table, self.seq_lens, mask, group_starts, prefix_lens, self.out16, self.lse,
+                self.prefix_workspace)
+        kw = dict(Hkv=wl.Hkv, page_size=wl.page_size, num_pages=wl.num_pages, sm_scale=wl.sm_scale,
+                  stream=stream)
+        if self.fp8:
+            fpk_paged_decode_attn_fp8_prefix(self.q, self.kv_pool, self.k_scale, self.v_scale, *args, **kw)
+        else:
+            fpk_paged_decode_attn_bf16_prefix(self.q, self.kv_pool, *args, **kw)
+
+    # ------------------------------------------------ forks, moves, rotations
+    def fork(self, parent, child, fresh, stream=None):
+        """Rows child[i] take over rows parent[i] (int32 device tensors; fresh: PageLedger.fork)."""
+        fpk_kv_fork(self.kv_pool, self.page_table, self.expected_tags, self.seq_lens, self.live_tags,
+                    self.abort_mask, parent, child, fresh, stream=stream, **self.kw)
+
+    def compact(self, src, dst, stream=None):
+        """Pages src[i] move to dst[i] (int32 device tensors from PageLedger.compact)."""
+        fpk_kv_compact(self.kv_pool, self.page_table, self.expected_tags, self.seq_lens, self.live_tags,
+                       src, dst, stream=stream, **self.kw)
+
+    def rope_append(self, inv_freq, *, rot_dim=None, interleaved=False, rot_scale=1.0, guard=True,
+                    stream=None):
+        """append() with rotary positions: q is rotated in place, k_new on its way into the cache."""
+        wl = self.wl
+        tags = (self.live_tags, self.expected_tags, self.abort_mask) if guard else (None, None, None)
+        kw = dict(Hkv=wl.Hkv, page_size=wl.page_size, num_pages=wl.num_pages,
+                  rot_dim=wl.D if rot_dim is None else rot_dim, interleaved=interleaved,
+                  rot_scale=rot_scale, stream=stream)
+        if self.fp8:
+            fpk_rope_append_fp8(self.q, self.k_new, self.v_new, inv_freq, self.q, self.kv_pool,
+                                self.k_scale, self.v_scale, self.page_table, self.seq_lens, *tags, **kw)
+        else:
+            fpk_rope_append_bf16(self.q, self.k_new, self.v_new, inv_freq, self.q, self.kv_pool,
+                                 self.page_table, self.seq_lens, *tags, **kw)
 
     def append_check(self, stream=None):
         """The step's cache write and batched tag check in one launch."""

@@ -190,6 +190,110 @@ int fpk_kv_prefill_bf16(const void* k, const void* v, const int32_t* cu_seqlens,
                         int32_t page_size, int32_t num_pages, void* stream);
 
 /*
+ * Rotary positions with the cache write: rotates the queries and keys of new
+ * tokens by their positions and writes the rotated keys and the values into
+ * the pages, in one launch.  The pages' models use rotary positions; the pages
+ * do not describe the step, layouts and order are this library's own.
+ *
+ * A head's first rot_dim values form rot_dim/2 pairs: (x_i, x_{i+rot_dim/2})
+ * (interleaved == 0) or (x_{2i}, x_{2i+1}) (interleaved != 0).  At position p
+ * pair i becomes rot_scale * (x cos a - y sin a, y cos a + x sin a) with
+ * a = p * inv_freq[i]; the other D - rot_dim values stay.  Angles are reduced
+ * in extended precision: the error of cos and sin is below 2^-20 for every
+ * int32 position and |inv_freq| <= 1.  The rotation runs in fp32 and is
+ * rounded once: queries to bf16, keys to the cache (e4m3(rotated / *k_scale),
+ * or bf16), values as fpk_kv_append_* writes them.
+ *   append : one token per request, position seq_lens[r] - 1 (seq_lens counts
+ *            it); requests with seq_lens[r] <= 0 are left alone, q_out too.
+ *   prefill: rows cu_seqlens[r] .. cu_seqlens[r+1]-1 are request r's tokens at
+ *            positions start_pos[r], start_pos[r] + 1, ... (start_pos NULL: 0;
+ *            a token at a negative position fails the guard).
+ * Guard: as fpk_kv_append_fp8, per token's page -- a refused token's key and
+ * value are not written and abort_mask[r] is set; its query is rotated all the
+ * same.
+ *   q        : bf16 [tokens][Hq][D]; q_out: the same shape, may be q itself,
+ *              else no overlap.  k, v: bf16 [tokens][Hkv][D].  16-byte aligned.
+ *   inv_freq : float [rot_dim/2] (device), finite
+ *   rot_dim  : multiple of 16 in [16, D], else FPK_EUNSUPPORTED; Hq >= 0 (0:
+ *              keys and values only; q and q_out may then be NULL)
+ */
+int fpk_rope_append_fp8(const void* q, const void* k_new, const void* v_new, const float* inv_freq,
+                        void* q_out, uint8_t* kv_pool, const float* k_scale, const float* v_scale,
+                        const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                        const uint32_t* live_tags, const uint32_t* expected_tags,
+                        uint8_t* abort_mask, int32_t rot_dim, int32_t interleaved, float rot_scale,
+                        int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
+                        int32_t num_pages, void* stream);
+int fpk_rope_append_bf16(const void* q, const void* k_new, const void* v_new, const float* inv_freq,
+                         void* q_out, void* kv_pool, const int32_t* page_table, int32_t max_pages,
+                         const int32_t* seq_lens, const uint32_t* live_tags,
+                         const uint32_t* expected_tags, uint8_t* abort_mask, int32_t rot_dim,
+                         int32_t interleaved, float rot_scale, int32_t B, int32_t Hq, int32_t Hkv,
+                         int32_t D, int32_t page_size, int32_t num_pages, void* stream);
+int fpk_rope_prefill_fp8(const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
+                         int32_t n_tokens, const int32_t* start_pos, const float* inv_freq,
+                         void* q_out, uint8_t* kv_pool, const float* k_scale, const float* v_scale,
+                         const int32_t* page_table, int32_t max_pages, const uint32_t* live_tags,
+                         const uint32_t* expected_tags, uint8_t* abort_mask, int32_t rot_dim,
+                         int32_t interleaved, float rot_scale, int32_t B, int32_t Hq, int32_t Hkv,
+                         int32_t D, int32_t page_size, int32_t num_pages, void* stream);
+int fpk_rope_prefill_bf16(const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
+                          int32_t n_tokens, const int32_t* start_pos, const float* inv_freq,
+                          void* q_out, void* kv_pool, const int32_t* page_table, int32_t max_pages,
+                          const uint32_t* live_tags, const uint32_t* expected_tags,
+                          uint8_t* abort_mask, int32_t rot_dim, int32_t interleaved,
+                          float rot_scale, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                          int32_t page_size, int32_t num_pages, void* stream);
+
+/*
+ * Fork: request child[i] takes over the context of request parent[i], i < n
+ * (several samples of one prompt).  Full pages are shared: the child's table
+ * and expected tags name the parent's pages.  The page in use, where
+ * L = seq_lens[parent] is no multiple of page_size, is copied (its tiles that
+ * hold tokens) in every layer to page fresh[i], which the host has allocated:
+ * live_tags[fresh[i]] += 1 (a reallocation) and the child's entry expects the
+ * new tag.  seq_lens[child] = L; the child's entries behind its pages become
+ * -1 with tag 0.  Where L is a multiple of page_size fresh[i] is not touched.
+ * Refused (fail closed), leaving the child empty (all entries -1, tags 0,
+ * seq_lens 0) and abort_mask[child] = 1: a parent outside [0, B), or equal to
+ * its child; a parent whose context exceeds its table, names a page outside
+ * [0, num_pages) or expects a tag that is not live; a needed fresh page outside
+ * [0, num_pages).  A refused fork may have written to its fresh page, whose tag
+ * then stays.  A child outside [0, B) is ignored.  No row may be a child twice,
+ * or a child and a parent, in one call; the fresh pages are distinct and in no
+ * row; what such entries get is unspecified (nothing out of range is touched).
+ *   kv_pool    : layer l's pool starts at kv_pool + l * layer_stride bytes
+ *                (layer_stride a multiple of 16; all layers share the table)
+ *   elem_bytes : 1 (e4m3) or 2 (bf16)
+ *   seq_lens   : int32 [B]; abort_mask: uint8 [B], nullable
+ *   parent, child, fresh : int32 [n]
+ */
+int fpk_kv_fork(void* kv_pool, int32_t elem_bytes, int32_t layers, int64_t layer_stride,
+                int32_t* page_table, int32_t max_pages, uint32_t* expected_tags, int32_t* seq_lens,
+                uint32_t* live_tags, uint8_t* abort_mask, const int32_t* parent,
+                const int32_t* child, const int32_t* fresh, int32_t n, int32_t B, int32_t Hkv,
+                int32_t D, int32_t page_size, int32_t num_pages, void* stream);
+
+/*
+ * Compaction: page src[i] moves to page dst[i] in every layer, i < n (a pool
+ * whose tail is to be free, or handed back).  live_tags[dst[i]] += 1 (a
+ * reallocation).  Every table entry among a request's first
+ * ceil(seq_lens / page_size) that names src[i] and expects its live tag is
+ * made to name dst[i] and to expect the new tag, in all rows that share the
+ * page.  Stale entries (another expected tag) stay as they are, and so stay
+ * stale; src's bytes and tag are untouched.
+ * src is ascending; no page is listed twice, or in both lists.  Moves with a
+ * page outside [0, num_pages) are ignored.  (An unsorted src leaves entries
+ * unmoved, other breaches leave unspecified bytes; nothing out of range is
+ * touched.)  Arguments as fpk_kv_fork; src, dst: int32 [n].
+ */
+int fpk_kv_compact(void* kv_pool, int32_t elem_bytes, int32_t layers, int64_t layer_stride,
+                   int32_t* page_table, int32_t max_pages, uint32_t* expected_tags,
+                   const int32_t* seq_lens, uint32_t* live_tags, const int32_t* src,
+                   const int32_t* dst, int32_t n, int32_t B, int32_t Hkv, int32_t D,
+                   int32_t page_size, int32_t num_pages, void* stream);
+
+/*
  * Element-wise quantiser: out[i] = e4m3(x[i] / *scale) for i < n, with the
  * same division and rounding as the append.  x: float [n], out: uint8 [n].
  */
@@ -370,6 +474,67 @@ int fpk_paged_decode_attn_bf16(const void* q, const void* kv_pool,
                                int32_t num_splits, float sm_scale, int32_t B, int32_t Hq,
                                int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
                                void* stream);
+
+/*
+ * Decode attention of a batch whose requests share prefixes: each shared
+ * prefix is read once for all requests that hold it, not once per request.
+ * Sources: as fpk_paged_decode_attn_fp8; the pages do not describe sharing --
+ * forked requests (fpk_kv_fork) and one system prompt for many requests map
+ * the same physical pages in their tables, and this call uses it.
+ *
+ * The result is that of fpk_paged_decode_attn_fp8 on the same tables, context
+ * lengths and mask, in bf16 (the input type of the weight GEMV):
+ *   out[r][h][:] = bf16(sum_j exp(s_j - m) decode(V_j) *v_scale / sum_j exp(s_j - m)),
+ *   lse[r][h] = m + ln(sum_j exp(s_j - m)), s_j = sm_scale sum_d q[d] decode(K_j[d]) *k_scale.
+ * Group g holds the requests [group_starts[g], group_starts[g + 1]), whose
+ * page tables agree over the first prefix_lens[g] tokens.  Requests before
+ * group_starts[0] or from group_starts[n_groups] on share nothing.  What is
+ * shared in effect is the largest number of whole pages within prefix_lens[g]
+ * and within the context of every live request of the group; tokens behind it
+ * are read through each request's own table.  A group of one live or dead
+ * request shares nothing.
+ *   q            : bf16 [B][Hq][D]
+ *   group_starts : int32 [n_groups + 1], non-decreasing, within [0, B] (values
+ *                  outside are clamped, one below an earlier one counts as that one)
+ *   prefix_lens  : int32 [n_groups]; negative counts as 0
+ *   out          : bf16 [B][Hq][D], 32-byte aligned; lse: float [B][Hq], nullable
+ *   workspace    : >= fpk_prefix_workspace_bytes(...) bytes for the current
+ *                  device, 256-byte aligned, owned by the caller, zeroed ONCE
+ *                  after allocating (its first 4 bytes are a status word as in
+ *                  fpk_paged_decode_attn_fp8; everything else is rewritten by
+ *                  every call).  Calls that share a workspace must not overlap
+ *                  on the GPU.
+ * Dead requests (L <= 0, abort_mask[r] != 0, L > max_pages * page_size, a page
+ * id outside [0, num_pages) among the first ceil(L / page_size) entries) get
+ * out = 0 and lse = -inf, as does a request whose table does not agree with
+ * its group's over the shared pages: no request is answered from pages that
+ * its own table does not name.  The first live request of a group stands for
+ * the group's table.
+ * Precision: scores and sums in fp32; the query enters the tensor cores exactly
+ * in bf16, or for the e4m3 cache as two e4m3 parts (what they leave out is below
+ * 2^-17 of the largest |q| of the head); softmax weights are rounded to f16
+ * (e4m3 cache) or bf16 (bf16 cache), values enter exactly.  Repeated calls
+ * on the same inputs give identical bits.
+ * D == 128, page_size a multiple of 16 in [16, 256], 1 <= Hq / Hkv <= 8, else
+ * FPK_EUNSUPPORTED; n_groups > 0 needs both group arrays (FPK_EINVAL).
+ */
+size_t fpk_prefix_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D);
+int fpk_paged_decode_attn_fp8_prefix(const void* q, const uint8_t* kv_pool, const float* k_scale,
+                                     const float* v_scale, const int32_t* page_table,
+                                     int32_t max_pages, const int32_t* seq_lens,
+                                     const uint8_t* abort_mask, const int32_t* group_starts,
+                                     const int32_t* prefix_lens, int32_t n_groups, void* out,
+                                     float* lse, void* workspace, size_t workspace_bytes,
+                                     float sm_scale, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                     int32_t page_size, int32_t num_pages, void* stream);
+int fpk_paged_decode_attn_bf16_prefix(const void* q, const void* kv_pool,
+                                      const int32_t* page_table, int32_t max_pages,
+                                      const int32_t* seq_lens, const uint8_t* abort_mask,
+                                      const int32_t* group_starts, const int32_t* prefix_lens,
+                                      int32_t n_groups, void* out, float* lse, void* workspace,
+                                      size_t workspace_bytes, float sm_scale, int32_t B, int32_t Hq,
+                                      int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                                      void* stream);
 
 /*
  * One whole decode step: fpk_decode_append_check_fp8 (the new token's write
