@@ -1,5 +1,42 @@
-// prefix_attn.cu -- decode attention of a batch whose requests share prefixes.
-#include "common.cuh"
+// prefix_attn.cu -- decode attention of a batch whose requests share prefixes,
+// on the fifth-generation tensor cores.
+//
+// A group's shared prefix is a matrix product: the rows are the queries of all
+// its requests that read one kv head (requests x GQA group), the columns the
+// prefix's tokens.  What a request has of its own is the same product with the
+// few rows of its GQA group.  Both are units of one work list:
+//
+// * prefix unit: (group, kv head, up to 256 query rows) over the shared pages;
+//   own unit: (request, kv head), its G rows over its own pages.
+// * Units are laid end to end in cost (blocks of 128 tokens, dearer for units of
+//   more than 128 rows) and the line is cut into one equal range per CTA; a CTA
+//   runs a piece of a unit after another.  Every piece writes its partial
+//   (m, l, O); a second kernel merges a row's partials by log-sum-exp in a fixed
+//   order, so repeated calls give the same bits.  A planning kernel of one CTA
+//   finds the groups' shared pages and every CTA's first unit.
+//
+// Piece pipeline (one CTA per SM, 16 warps), per block of 128 tokens:
+//   warp 12     lands K rows (128-byte swizzle) and V tiles by tensor maps
+//   warps 8-11  e4m3 cache: V codes to f16 core matrices (exact), so that softmax
+//               weights enter the second product in f16; both caches: zeroes
+//               where no token lies (an unwritten slot may hold NaN, and 0 NaN = NaN)
+//   warp 13     issues S = Q K^T and O += P V (tcgen05.mma, M = N = 128)
+//   warps 0-3, 4-7: softmax of row tile 0 and 1, a thread per row: no shuffles,
+//               the row's maximum, sum and rescale are the thread's own.  P
+//               replaces S in tensor memory as the A operand of the second product.
+// Units of more than 128 rows use both tiles on every block; smaller ones give
+// the two tiles alternate blocks of the same rows, each with its own partial.
+//
+// Precision.  bf16 cache: q, K, P and V in bf16.  e4m3 cache: K enters as it
+// lies; q x 2^e (its largest value in [128, 256)) as two e4m3 parts c0 + c1: a
+// bf16's eight bits fill exactly two parts of four, but for values below 2^-9
+// of the largest, which lose at most 2^-17 of it; the MMAs' K runs over both
+// parts against the same K rows, at the rate of one f16 product.  Scores, sums and
+// O stay in fp32.  O is rescaled only when a row's maximum has grown by more than
+// 2^8 since the last time: weights are then at most 2^8, far inside f16.
+#include <atomic>
+
+#include "tcgen05.cuh"
 
 namespace fpk {
 namespace {
@@ -7,12 +44,32 @@ namespace {
 constexpr int kPfTile = 16;
 constexpr int kPfDim = 128;
 constexpr int kPfGroupMax = 8;
+constexpr int kPfBlk = 128;                    // tokens of a block
+constexpr int kPfBlkTiles = kPfBlk / kPfTile;
+constexpr int kPfUnitRows = 256;               // query rows of a prefix unit: two MMA tiles
 constexpr float kPfLog2e = 1.4426950408889634f;
 constexpr float kPfLn2 = 0.6931471805599453f;
+constexpr float kPfGrow = 8.f;                 // log2 growth of a maximum that rescales O
+// Cost of a block in the work list, with both tiles at work and with one.
+constexpr int kPfCostPair = 3;
+constexpr int kPfCostSolo = 2;
 
-struct PrefixArgs {
+constexpr int kPfThreads = 512;
+constexpr int kPfVWarp = 8, kPfLoadWarp = 12, kPfMmaWarp = 13, kPfCheckWarp = 14;
+constexpr int kPfPlanThreads = 1024;
+constexpr int kPfMergeWarps = 4;
+
+// What the planning kernel finds of each request.
+struct PfReq {
+  int64_t y0;      // place of its units in the work list (the group's prefix units first, at its first request)
+  int32_t ptiles;  // tiles of the shared prefix
+  int32_t stok;    // tokens behind it; 0 for a dead request
+  int32_t gfirst, gcount, leader;
+  int32_t pad;
+};
+
+struct PfArgs {
   const uint16_t* q;
-  const uint8_t* kv_pool;
   const float* k_scale;
   const float* v_scale;
   const int32_t* page_table;
@@ -22,120 +79,1027 @@ struct PrefixArgs {
   const int32_t* prefix_lens;
   uint16_t* out;
   float* lse;
-  int n_groups, B, Hq, Hkv, G, page_size, num_pages, max_pages;
+  uint32_t* status;
+  int64_t* total;    // length of the work list
+  int32_t* gstart;   // [n_groups + 1] group starts, clamped and non-decreasing
+  int32_t* first;    // [ctas] request in whose units a CTA's range begins
+  int32_t* dead;     // [B]
+  PfReq* req;        // [B]
+  float2* part_ml;   // partials: 4 per (request, query head), then 256 rows per CTA
+  float* part_o;
+  int n_groups, B, Hq, Hkv, G, page_size, num_pages, max_pages, ctas, zbox;
   float sm_scale_log2;
 };
 
+// Shared-memory map of the main kernel, from a 1024-byte aligned base.
+template <bool kFp8>
+struct PfCfg {
+  static constexpr int kElem = kFp8 ? 1 : 2;
+  static constexpr int kQTile = 128 * 256;                     // parts (or halves) of a tile's queries
+  static constexpr int kKStage = kPfBlk * kPfDim * kElem;
+  static constexpr int kVStage = kKStage;
+  static constexpr int kKStages = kFp8 ? 3 : 2;
+  static constexpr int kVStages = 3;
+  static constexpr int kV16 = kPfBlk * kPfDim * 2;             // converted V block
+  static constexpr int kV16Bufs = kFp8 ? 2 : 0;
+  static constexpr int kOffK = 2 * kQTile;
+  static constexpr int kOffV = kOffK + kKStages * kKStage;
+  static constexpr int kOffV16 = kOffV + kVStages * kVStage;
+  static constexpr int kOffBars = kOffV16 + kV16Bufs * kV16;
+  // barriers
+  static constexpr int kReady = kFp8 ? kV16Bufs : kVStages;    // V blocks ready for the MMA
+  static constexpr int kBarKFull = 0;
+  static constexpr int kBarKFree = kBarKFull + kKStages;
+  static constexpr int kBarVFull = kBarKFree + kKStages;
+  static constexpr int kBarVFree = kBarVFull + kVStages;
+  static constexpr int kBarReady = kBarVFree + kVStages;
+  static constexpr int kBarUsed = kBarReady + kReady;          // e4m3: converted block read by the MMA
+  static constexpr int kBarS = kBarUsed + kV16Bufs;            // [2]
+  static constexpr int kBarP = kBarS + 2;                      // [2]
+  static constexpr int kBarO = kBarP + 2;                      // [2]
+  static constexpr int kBarQ = kBarO + 2;
+  static constexpr int kBarQFree = kBarQ + 1;
+  static constexpr int kBarDone = kBarQFree + 1;               // every MMA of the CTA completed
+  static constexpr int kBars = kBarDone + 1;
+  static constexpr int kOffMisc = kOffBars + 8 * kBars;        // tensor memory base, failure flag
+  static constexpr int kSmem = kOffMisc + 16 + 1024;
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
+};
+
 // Context length of request r if it is alive by its length and abort flag, else 0.
-__device__ __forceinline__ int live_length(const PrefixArgs& a, int r) {
+__device__ __forceinline__ int live_length(const PfArgs& a, int r) {
   const int L = __ldg(a.seq_lens + r);
   if (L <= 0 || static_cast<int64_t>(L) > static_cast<int64_t>(a.max_pages) * a.page_size) return 0;
   if (a.abort_mask != nullptr && __ldg(a.abort_mask + r) != 0) return 0;
   return L;
 }
 
-template <bool kFp8>
-__device__ __forceinline__ float pool_value(const uint8_t* pool, int64_t i) {
-  if (kFp8) {
-    const uint32_t h = e4m3x2_to_f16x2(pool[i]);
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
-  }
-  return bf16_bits_to_float(reinterpret_cast<const uint16_t*>(pool)[i]);
+// ---------------------------------------------------------------------------
+// work list
+// ---------------------------------------------------------------------------
+// Prefix units of a group, per kv head: `units` of up to 256 rows, all but the
+// last of cost kPfCostPair per block, the last of cost `wlast`.
+struct PfPrefix {
+  int blocks, units, wlast;
+  int64_t head_cost;
+};
+__device__ __forceinline__ PfPrefix prefix_shape(int ptiles, int gcount, int G) {
+  PfPrefix p;
+  const int rows = gcount * G;
+  p.blocks = (ptiles + kPfBlkTiles - 1) / kPfBlkTiles;
+  p.units = (rows + kPfUnitRows - 1) / kPfUnitRows;
+  p.wlast = rows - (p.units - 1) * kPfUnitRows > 128 ? kPfCostPair : kPfCostSolo;
+  p.head_cost = static_cast<int64_t>(p.blocks) * (static_cast<int64_t>(kPfCostPair) * (p.units - 1) + p.wlast);
+  return p;
+}
+__device__ __forceinline__ int own_blocks(int stok) { return stok > 0 ? (stok - 1) / kPfBlk + 1 : 0; }
+
+// CTA c owns the blocks that start in [range_begin(c), range_begin(c + 1)).
+__device__ __forceinline__ int64_t range_begin(int64_t c, int64_t T, int64_t n) { return c * T / n; }
+__device__ __forceinline__ int owner_of(int64_t y, int64_t T, int64_t n) {
+  return static_cast<int>(((y + 1) * n - 1) / T);
+}
+// Blocks [i0, i1) of a unit at y with n blocks of cost w that a range [b0, b1) owns.
+__device__ __forceinline__ void owned_blocks(int64_t y, int n, int w, int64_t b0, int64_t b1, int& i0, int& i1) {
+  const int64_t lo = b0 <= y ? 0 : (b0 - y + w - 1) / w;
+  const int64_t hi = b1 <= y ? 0 : (b1 - y + w - 1) / w;
+  i0 = static_cast<int>(lo < n ? lo : n);
+  i1 = static_cast<int>(hi < n ? hi : n);
 }
 
-// One CTA per (request, kv head), one thread per dim.
-template <bool kFp8>
-__global__ void __launch_bounds__(kPfDim) prefix_simple_kernel(const PrefixArgs a) {
-  __shared__ float s_q[kPfGroupMax][kPfDim];
-  __shared__ float s_s[kPfGroupMax][kPfTile];
-  const int r = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, t = threadIdx.x;
-  const int64_t row0 = static_cast<int64_t>(r) * a.Hq + h * a.G;
-  const int L = live_length(a, r);
-  // the request's group, what it shares, and the row that stands for it
-  int shared_pages = 0, leader = r;
-  for (int g = 0; g < a.n_groups; ++g) {
-    const int lo = min(max(__ldg(a.group_starts + g), 0), a.B), hi = min(max(__ldg(a.group_starts + g + 1), 0), a.B);
-    if (r < lo || r >= hi || hi - lo < 2) continue;
-    int least = max(__ldg(a.prefix_lens + g), 0);
-    leader = -1;
-    for (int i = lo; i < hi; ++i) {
-      const int Li = live_length(a, i);
-      if (Li == 0) continue;
-      if (leader < 0) leader = i;
-      least = min(least, Li);
+struct PfPiece {
+  bool prefix;
+  int r;           // request whose table is read (prefix: the leader)
+  int h;
+  int row0, rows;  // prefix: rows of the group; own: rows [0, G)
+  int gfirst;      // request of row 0
+  int i0, i1;      // blocks of the unit
+  int tile0;       // table tile of the unit's first token
+  int tokens;      // of the unit
+};
+
+struct PfCursor {
+  PfReq q;
+  int r, h, u;  // u: prefix unit of the head, -1 in a request's own units
+  int64_t y, b0, b1;
+};
+
+__device__ __forceinline__ PfReq load_req(const PfArgs& a, int r) {
+  PfReq q;
+  const int4* p = reinterpret_cast<const int4*>(a.req + r);
+  const int4 x = __ldcg(p), z = __ldcg(p + 1);
+  q.y0 = static_cast<int64_t>((static_cast<uint64_t>(static_cast<uint32_t>(x.y)) << 32) | static_cast<uint32_t>(x.x));
+  q.ptiles = x.z;
+  q.stok = x.w;
+  q.gfirst = z.x;
+  q.gcount = z.y;
+  q.leader = z.z;
+  return q;
+}
+
+__device__ __forceinline__ void enter_request(const PfArgs& a, PfCursor& c) {
+  c.q = load_req(a, c.r);
+  c.h = 0;
+  c.u = c.q.ptiles > 0 && c.q.gfirst == c.r ? 0 : -1;
+  c.y = c.q.y0;
+}
+
+__device__ __forceinline__ PfCursor begin_range(const PfArgs& a, int64_t b0, int64_t b1) {
+  PfCursor c;
+  c.b0 = b0;
+  c.b1 = b1;
+  c.r = __ldcg(a.first + blockIdx.x);
+  enter_request(a, c);
+  int64_t at = b0 - c.y;
+  if (c.u == 0) {
+    const PfPrefix p = prefix_shape(c.q.ptiles, c.q.gcount, a.G);
+    const int64_t all = p.head_cost * a.Hkv;
+    if (at < all) {
+      c.h = static_cast<int>(at / p.head_cost);
+      const int64_t step = static_cast<int64_t>(kPfCostPair) * p.blocks;
+      const int64_t u = at % p.head_cost / step;
+      c.u = static_cast<int>(u < p.units ? u : p.units - 1);
+      c.y += c.h * p.head_cost + c.u * step;
+      return c;
     }
-    shared_pages = leader < 0 ? 0 : least / a.page_size;
+    c.u = -1;
+    c.y += all;
+    at -= all;
   }
-  int bad = L == 0;
-  if (!bad) {
-    const int32_t* row = a.page_table + static_cast<int64_t>(r) * a.max_pages;
-    const int32_t* lead = a.page_table + static_cast<int64_t>(max(leader, 0)) * a.max_pages;
-    for (int i = t; i < (L + a.page_size - 1) / a.page_size; i += kPfDim) {
-      const int p = __ldg(row + i);
-      if (p < 0 || p >= a.num_pages || (i < shared_pages && p != __ldg(lead + i))) bad = 1;
+  const int64_t cost = static_cast<int64_t>(kPfCostSolo) * own_blocks(c.q.stok);
+  if (cost > 0) {
+    const int64_t h = at / cost;
+    c.h = static_cast<int>(h < a.Hkv ? h : a.Hkv);
+    c.y += c.h * cost;
+  }
+  return c;
+}
+
+__device__ __forceinline__ bool next_piece(const PfArgs& a, PfCursor& c, PfPiece& p) {
+  for (;;) {
+    if (c.y >= c.b1) return false;
+    int n, w;
+    if (c.u >= 0) {
+      const PfPrefix s = prefix_shape(c.q.ptiles, c.q.gcount, a.G);
+      n = s.blocks;
+      w = c.u == s.units - 1 ? s.wlast : kPfCostPair;
+      p.prefix = true;
+      p.r = c.q.leader;
+      p.row0 = c.u * kPfUnitRows;
+      p.rows = min(kPfUnitRows, c.q.gcount * a.G - p.row0);
+      p.tile0 = 0;
+      p.tokens = c.q.ptiles * kPfTile;
+      p.h = c.h;
+      p.gfirst = c.q.gfirst;
+      owned_blocks(c.y, n, w, c.b0, c.b1, p.i0, p.i1);
+      c.y += static_cast<int64_t>(n) * w;
+      if (++c.u == s.units) {
+        c.u = 0;
+        if (++c.h == a.Hkv) {
+          c.h = 0;
+          c.u = -1;
+        }
+      }
+    } else {
+      n = own_blocks(c.q.stok);
+      if (n == 0 || c.h >= a.Hkv) {
+        if (++c.r >= a.B) return false;
+        enter_request(a, c);
+        continue;
+      }
+      p.prefix = false;
+      p.r = c.r;
+      p.row0 = 0;
+      p.rows = a.G;
+      p.tile0 = c.q.ptiles;
+      p.tokens = c.q.stok;
+      p.h = c.h;
+      p.gfirst = c.r;
+      owned_blocks(c.y, n, kPfCostSolo, c.b0, c.b1, p.i0, p.i1);
+      c.y += static_cast<int64_t>(n) * kPfCostSolo;
+      ++c.h;
     }
+    if (p.i0 < p.i1) return true;
   }
-  bad = __syncthreads_or(bad);
-  if (bad) {
-    for (int g = 0; g < a.G; ++g) {
-      a.out[(row0 + g) * kPfDim + t] = 0;
-      if (t == 0 && a.lse != nullptr) a.lse[row0 + g] = -INFINITY;
-    }
-    return;
-  }
-  for (int g = 0; g < kPfGroupMax; ++g)
-    s_q[g][t] = g < a.G ? bf16_bits_to_float(a.q[(row0 + g) * kPfDim + t]) : 0.f;
-  __syncthreads();
-  const float kmul = (kFp8 ? __ldg(a.k_scale) : 1.f) * a.sm_scale_log2;
+}
+
+// One CTA: group ranges, shared pages and leaders, the work list and every CTA's
+// first request.
+__global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const PfArgs a) {
+  __shared__ int64_t s_sum[kPfPlanThreads / 32];
+  __shared__ int s_max[kPfPlanThreads / 32];
+  griddep_launch_dependents();
+  const unsigned kFull = 0xffffffffu;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int tpp = a.page_size >> 4;
-  float m[kPfGroupMax], l[kPfGroupMax], o[kPfGroupMax];
-  for (int g = 0; g < kPfGroupMax; ++g) {
-    m[g] = -INFINITY;
-    l[g] = o[g] = 0.f;
-  }
-  for (int tile = 0; tile * kPfTile < L; ++tile) {
-    const int page = __ldg(a.page_table + static_cast<int64_t>(r) * a.max_pages + tile / tpp);
-    const int64_t kb = ((static_cast<int64_t>(page) * a.Hkv + h) * tpp + tile % tpp) * 2 * kPfTile * kPfDim;
-    const int n = min(kPfTile, L - tile * kPfTile);
-    const int sg = t >> 4, st = t & 15;
-    float s = -INFINITY;
-    if (st < n) {
-      s = 0.f;
-      for (int d = 0; d < kPfDim; ++d) s = fmaf(s_q[sg][d], pool_value<kFp8>(a.kv_pool, kb + st * kPfDim + d), s);
-      s *= kmul;
+  // group starts: clamped, then the running maximum
+  int carry = 0;
+  for (int base = 0; a.n_groups > 0 && base <= a.n_groups; base += kPfPlanThreads) {
+    const int i = base + t;
+    int v = i <= a.n_groups ? min(max(__ldg(a.group_starts + i), 0), a.B) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, v, o);
+      if (lane >= o) v = max(v, x);
     }
-    s_s[sg][st] = s;
+    if (lane == 31) s_max[warp] = v;
     __syncthreads();
-    float v[kPfTile];
-    for (int j = 0; j < n; ++j) v[j] = pool_value<kFp8>(a.kv_pool, kb + kPfTile * kPfDim + t * kPfTile + j);
-    for (int g = 0; g < a.G; ++g) {
-      float mn = m[g];
-      for (int j = 0; j < n; ++j) mn = fmaxf(mn, s_s[g][j]);
-      const float f = m[g] == -INFINITY ? 0.f : exp2f(m[g] - mn);
-      o[g] *= f;
-      l[g] *= f;
-      m[g] = mn;
-      for (int j = 0; j < n; ++j) {
-        const float p = mn == -INFINITY ? 0.f : exp2f(s_s[g][j] - mn);
-        l[g] += p;
-        o[g] = fmaf(p, v[j], o[g]);
+    int before = carry;
+    for (int k = 0; k < kPfPlanThreads / 32; ++k) {
+      if (k < warp) before = max(before, s_max[k]);
+      carry = max(carry, s_max[k]);
+    }
+    if (i <= a.n_groups) a.gstart[i] = max(v, before);
+    __syncthreads();
+  }
+  for (int r = t; r < a.B; r += kPfPlanThreads) {
+    const int L = live_length(a, r);
+    PfReq& q = a.req[r];
+    q.ptiles = 0;
+    q.stok = L;
+    q.gfirst = r;
+    q.gcount = 1;
+    q.leader = r;
+    a.dead[r] = L == 0;
+  }
+  __syncthreads();
+  // what each group shares: whole pages of the prefix that every live request holds
+  for (int g = warp; g < a.n_groups; g += kPfPlanThreads / 32) {
+    const int lo = a.gstart[g], hi = a.gstart[g + 1];
+    if (hi - lo < 2) continue;
+    int least = 0x7fffffff, leader = 0x7fffffff;
+    for (int r = lo + lane; r < hi; r += 32) {
+      const int L = a.req[r].stok;
+      if (L > 0) {
+        least = min(least, L);
+        leader = min(leader, r);
       }
     }
-    __syncthreads();
+    least = __reduce_min_sync(kFull, least);
+    leader = __reduce_min_sync(kFull, leader);
+    const int pre = __ldg(a.prefix_lens + g);
+    const int ptiles = leader == 0x7fffffff ? 0 : max(0, min(pre, least)) / a.page_size * tpp;
+    if (ptiles == 0) continue;
+    for (int r = lo + lane; r < hi; r += 32) {
+      PfReq& q = a.req[r];
+      q.ptiles = ptiles;
+      q.stok = max(0, q.stok - ptiles * kPfTile);
+      q.gfirst = lo;
+      q.gcount = hi - lo;
+      q.leader = leader;
+    }
   }
-  const float vmul = kFp8 ? __ldg(a.v_scale) : 1.f;
-  for (int g = 0; g < a.G; ++g) {
-    const bool none = l[g] == 0.f;
-    const __nv_bfloat16 y = __float2bfloat16_rn(none ? 0.f : o[g] * vmul / l[g]);
-    a.out[(row0 + g) * kPfDim + t] = __bfloat16_as_ushort(y);
-    if (t == 0 && a.lse != nullptr) a.lse[row0 + g] = none ? -INFINITY : (m[g] + log2f(l[g])) * kPfLn2;
+  __syncthreads();
+  // places in the work list
+  const int chunk = (a.B + kPfPlanThreads - 1) / kPfPlanThreads;
+  const int rb = min(a.B, t * chunk), re = min(a.B, rb + chunk);
+  auto cost_of = [&](int r) -> int64_t {
+    const PfReq& q = a.req[r];
+    int64_t c = static_cast<int64_t>(kPfCostSolo) * own_blocks(q.stok);
+    if (q.ptiles > 0 && q.gfirst == r) c += prefix_shape(q.ptiles, q.gcount, a.G).head_cost;
+    return c * a.Hkv;
+  };
+  int64_t mine = 0;
+  for (int r = rb; r < re; ++r) mine += cost_of(r);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int64_t y = incl - mine, T = 0;
+  for (int k = 0; k < kPfPlanThreads / 32; ++k) {
+    if (k < warp) y += s_sum[k];
+    T += s_sum[k];
+  }
+  if (t == 0) *a.total = T;
+  const int64_t n = a.ctas;
+  for (int r = rb; r < re; ++r) {
+    const int64_t c = cost_of(r);
+    a.req[r].y0 = y;
+    if (c > 0)  // the CTAs whose ranges begin within [y, y + c)
+      for (int64_t k = (y * n + T - 1) / T; k < n && range_begin(k, T, n) < y + c; ++k) a.first[k] = r;
+    y += c;
   }
 }
 
-size_t prefix_workspace(int32_t B, int32_t Hq) {
-  (void)B;
-  (void)Hq;
-  return 256;
+// ---------------------------------------------------------------------------
+// tcgen05
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+// Instruction descriptors, M = N = 128, both operands K-major, D in fp32.
+constexpr uint32_t kPfShape = (1u << 4) | (static_cast<uint32_t>(128 >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+constexpr uint32_t kPfE4m3 = kPfShape;                            // kind::f8f6f4, E4M3 x E4M3
+constexpr uint32_t kPfF16 = kPfShape;                             // kind::f16, F16 x F16
+constexpr uint32_t kPfBf16 = kPfShape | (1u << 7) | (1u << 10);   // kind::f16, BF16 x BF16
+
+// S = Q K^T: both operands from shared memory.
+template <bool kFp8>
+__device__ __forceinline__ void mma_s(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t acc) {
+  if (kFp8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(kPfE4m3), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(kPfBf16), "r"(acc)
+        : "memory");
+}
+
+// O += P V: P from tensor memory.
+template <bool kFp8>
+__device__ __forceinline__ void mma_o(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(kFp8 ? kPfF16 : kPfBf16), "r"(acc)
+      : "memory");
+}
+
+// 32 consecutive columns of this thread's tensor memory lane, waited for.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A wait that gives up once any wait of the CTA has: control flow then runs on
+// to the end without waiting (every address stays in range; the results are
+// void and the status word says so), so that no barrier is left waiting.
+__device__ __forceinline__ void pf_wait(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* failed) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((it & 255u) == 0u) {
+      if (*failed) return;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        *failed = 1;
+        atomicOr(status, kStatusWaitTimeout);
+        return;
+      }
+    }
+  }
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kPfThreads, 1)
+    prefix_attn_kernel(const PfArgs a, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap) {
+  using C = PfCfg<kFp8>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  uint8_t* const sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const uint32_t sbase = smem_addr(sm);
+  auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8 * i; };
+  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
+  volatile int* const s_failed = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned kFull = 0xffffffffu;
+
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kBars; ++i) {
+      int arrivals = 1;
+      if (i >= C::kBarReady && i < C::kBarReady + C::kReady) arrivals = 4;             // V warps
+      if (kFp8 && i >= C::kBarVFree && i < C::kBarVFree + C::kVStages) arrivals = 4;   // V warps
+      if (i >= C::kBarP && i < C::kBarP + 2) arrivals = 4;                             // a tile's softmax warps
+      if (i == C::kBarQ) arrivals = 8;                                                 // all softmax warps
+      mbar_init(bar(i), arrivals);
+    }
+    *s_failed = 0;
+    fence_barrier_init();
+  }
+  if (warp == kPfMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();  // the plan is there
+  const uint32_t tmem = *s_tmem;
+  const int64_t T = __ldcg(a.total);
+  const int64_t b0 = range_begin(blockIdx.x, T, a.ctas), b1 = range_begin(blockIdx.x + 1, T, a.ctas);
+  auto wait = [&](int i, uint32_t parity) { pf_wait(bar(i), parity & 1u, a.status, s_failed); };
+
+  if (b0 < b1) {
+    PfCursor cur = begin_range(a, b0, b1);
+    PfPiece p;
+    const int tpp = a.page_size >> 4;
+    if (warp == kPfLoadWarp) {
+      // ===================== K and V blocks into their rings =====================
+      // Lane c + 8 k copies box c of a block (zbox tiles, within a page), k = 0: K (bf16:
+      // its first 64 dims), 1: V (bf16: K's other dims), 2: bf16 V.
+      const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
+      const int c = lane & 7, part = lane >> 3;
+      const int boxes = kPfBlkTiles / a.zbox;
+      uint32_t j = 0;
+      while (next_piece(a, cur, p)) {
+        const int32_t* row = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
+        const int tiles = (p.tokens + kPfTile - 1) / kPfTile;
+        auto page_of = [&](int i) -> int {  // page of box c of block i, -2: no such box
+          const int t = i * kPfBlkTiles + c * a.zbox;
+          return c < boxes && t < tiles && i < p.i1 ? __ldg(row + (p.tile0 + t) / tpp) : -2;
+        };
+        int next = page_of(p.i0);
+        const uint64_t pol = p.prefix ? again : once;
+        for (int i = p.i0; i < p.i1; ++i, ++j) {
+          const int pg = next;
+          next = page_of(i + 1);
+          const uint32_t ks = j % C::kKStages, vs = j % C::kVStages;
+          if (j >= static_cast<uint32_t>(C::kKStages)) wait(C::kBarKFree + ks, j / C::kKStages - 1);
+          if (j >= static_cast<uint32_t>(C::kVStages)) wait(C::kBarVFree + vs, j / C::kVStages - 1);
+          const bool good = pg >= 0 && pg < a.num_pages;
+          // a page outside the pool: the request is dead (a group's are told apart by the check warp)
+          if (!good && pg != -2 && !p.prefix) a.dead[p.r] = 1;
+          const int n = __popc(__ballot_sync(kFull, good && part == 0));
+          if (lane == 0) {
+            const uint32_t bytes = static_cast<uint32_t>(n * a.zbox) * kPfTile * kPfDim * C::kElem;
+            if (bytes == 0) {
+              mbar_arrive(bar(C::kBarKFull + ks));
+              mbar_arrive(bar(C::kBarVFull + vs));
+            } else {
+              mbar_arrive_expect_tx(bar(C::kBarKFull + ks), bytes);
+              mbar_arrive_expect_tx(bar(C::kBarVFull + vs), bytes);
+            }
+          }
+          __syncwarp();
+          if (good) {
+            const int tile = p.tile0 + i * kPfBlkTiles + c * a.zbox;
+            const int z = (pg * a.Hkv + p.h) * tpp + tile % tpp;
+            const uint32_t kdst = sbase + C::kOffK + ks * C::kKStage + c * a.zbox * kPfTile * 128;
+            const uint32_t vdst = sbase + C::kOffV + vs * C::kVStage + c * a.zbox * kPfTile * kPfDim * C::kElem;
+            if (part == 0) tma_load_3d(kdst, &kmap, 0, 0, z, bar(C::kBarKFull + ks), pol);
+            if (!kFp8 && part == 1) tma_load_3d(kdst + kPfBlk * 128, &kmap, 64, 0, z, bar(C::kBarKFull + ks), pol);
+            if (part == (kFp8 ? 1 : 2)) tma_load_3d(vdst, &vmap, 0, kFp8 ? 16 : 128, z, bar(C::kBarVFull + vs), pol);
+          }
+        }
+      }
+      // every copy has landed before the CTA ends, even if a wait gave up
+      if (lane == 0) {
+        for (uint32_t b = j > C::kKStages ? j - C::kKStages : 0; b < j; ++b)
+          mbar_wait(bar(C::kBarKFull + b % C::kKStages), (b / C::kKStages) & 1, a.status);
+        for (uint32_t b = j > C::kVStages ? j - C::kVStages : 0; b < j; ++b)
+          mbar_wait(bar(C::kBarVFull + b % C::kVStages), (b / C::kVStages) & 1, a.status);
+      }
+    } else if (warp >= kPfVWarp && warp < kPfVWarp + 4) {
+      // ===================== V blocks made ready for the MMA =====================
+      const int d = threadIdx.x - kPfVWarp * 32;  // this thread's dim
+      uint32_t j = 0;
+      while (next_piece(a, cur, p)) {
+        for (int i = p.i0; i < p.i1; ++i, ++j) {
+          const int nv = min(kPfBlk, p.tokens - i * kPfBlk);
+          const uint32_t vs = j % C::kVStages;
+          uint8_t* const v = sm + C::kOffV + vs * C::kVStage;
+          wait(C::kBarVFull + vs, j / C::kVStages);
+          if (kFp8) {
+            const uint32_t buf = j & 1;
+            if (j >= 2) wait(C::kBarUsed + buf, (j >> 1) - 1);
+            uint8_t* const o = sm + C::kOffV16 + buf * C::kV16 + d * 16;
+#pragma unroll
+            for (int t = 0; t < kPfBlkTiles; ++t) {
+              // codes of dim d, tokens 16 t .. 16 t + 15, to two rows of 8 f16
+              const uint4 x = *reinterpret_cast<const uint4*>(v + t * kPfTile * kPfDim + d * 16);
+              uint32_t y[8];
+              e4m3x4_to_f16x4(x.x, y[0], y[1]);
+              e4m3x4_to_f16x4(x.y, y[2], y[3]);
+              e4m3x4_to_f16x4(x.z, y[4], y[5]);
+              e4m3x4_to_f16x4(x.w, y[6], y[7]);
+              if (nv < (t + 1) * kPfTile) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int left = nv - t * kPfTile - 2 * k;  // tokens of this pair that exist
+                  if (left <= 0) y[k] = 0;
+                  else if (left == 1) y[k] &= 0xFFFFu;
+                }
+              }
+              uint4* const w = reinterpret_cast<uint4*>(o + t * kPfTile * kPfDim * 2);
+              w[0] = make_uint4(y[0], y[1], y[2], y[3]);
+              w[128] = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(C::kBarReady + buf));
+              mbar_arrive(bar(C::kBarVFree + vs));
+            }
+          } else {
+            if (nv < kPfBlk) {
+              // rows of 16 tokens with the 32-byte swizzle: the two 16-byte halves change places
+              // in every other group of four rows
+              for (int k = nv; k < kPfBlk; ++k) {
+                const int half = ((k >> 3) & 1) ^ ((d >> 2) & 1);
+                *reinterpret_cast<uint16_t*>(v + (k >> 4) * kPfTile * kPfDim * 2 + d * 32 + half * 16 + (k & 7) * 2) = 0;
+              }
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kBarReady + vs));
+          }
+        }
+      }
+    } else if (warp == kPfMmaWarp) {
+      // ===================== MMA issue (one thread) =====================
+      if (lane == 0) {
+        uint32_t jb = 0;               // blocks of earlier pieces
+        uint32_t np[2] = {0, 0};       // P blocks taken of each tile
+        uint32_t piece = 0;
+        auto issue_s = [&](int t, int qt, uint32_t j) {
+          const uint32_t q = sbase + qt * C::kQTile;
+          const uint32_t k = sbase + C::kOffK + (j % C::kKStages) * C::kKStage;
+          // e4m3: two query parts against the same K rows; bf16: two halves of the dims
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const uint64_t ad = smem_desc(q + (x >> 2) * 16384 + (x & 3) * 32, 16, 1024, 2);
+            const uint64_t bd = smem_desc(k + (kFp8 ? 0 : (x >> 2) * 16384) + (x & 3) * 32, 16, 1024, 2);
+            mma_s<kFp8>(tmem + t * 128, ad, bd, x > 0);
+          }
+          mma_commit(bar(C::kBarS + t));
+        };
+        auto wait_ready = [&](uint32_t j) { wait(C::kBarReady + j % C::kReady, j / C::kReady); };
+        auto issue_o = [&](int t, uint32_t j, bool acc) {
+          wait(C::kBarP + t, np[t]);
+          ++np[t];
+          tc_fence_after();
+          const uint32_t v = kFp8 ? sbase + C::kOffV16 + (j & 1) * C::kV16
+                                  : sbase + C::kOffV + (j % C::kVStages) * C::kVStage;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            // 16 tokens: e4m3 as two columns of core matrices (8 dims x 8 tokens, 128 B apart along the
+            // dims, 2 KiB along the tokens), bf16 as rows of 32 bytes with the 32-byte swizzle
+            const uint64_t bd = kFp8 ? smem_desc(v + x * 4096, 2048, 128, 0) : smem_desc(v + x * 4096, 16, 256, 6);
+            mma_o<kFp8>(tmem + 256 + t * 128, tmem + t * 128 + x * 8, bd, acc || x > 0);
+          }
+          mma_commit(bar(C::kBarO + t));
+        };
+        auto free_v = [&](uint32_t j) {
+          mma_commit(bar(kFp8 ? C::kBarUsed + (j & 1) : C::kBarVFree + j % C::kVStages));
+        };
+        while (next_piece(a, cur, p)) {
+          const int nb = p.i1 - p.i0;
+          const bool pair = p.rows > 128;
+          const int lag = pair ? 1 : 2;  // blocks between S and its PV
+          wait(C::kBarQ, piece);
+          tc_fence_after();
+          for (int i = 0; i < nb + lag; ++i) {
+            if (pair) {
+              for (int t = 0; t < 2; ++t) {
+                if (i >= 1) {
+                  if (t == 0) wait_ready(jb + i - 1);
+                  issue_o(t, jb + i - 1, i > 1);
+                  if (t == 1) free_v(jb + i - 1);
+                }
+                if (i < nb) {
+                  if (t == 0) wait(C::kBarKFull + (jb + i) % C::kKStages, (jb + i) / C::kKStages);
+                  tc_fence_after();
+                  issue_s(t, t, jb + i);
+                  if (t == 1) mma_commit(bar(C::kBarKFree + (jb + i) % C::kKStages));
+                }
+              }
+            } else {
+              const int t = i & 1;
+              if (i >= 2) {
+                wait_ready(jb + i - 2);
+                issue_o(t, jb + i - 2, i > 3);
+                free_v(jb + i - 2);
+              }
+              if (i < nb) {
+                wait(C::kBarKFull + (jb + i) % C::kKStages, (jb + i) / C::kKStages);
+                tc_fence_after();
+                issue_s(t, 0, jb + i);
+                mma_commit(bar(C::kBarKFree + (jb + i) % C::kKStages));
+              }
+            }
+            if (i == nb - 1) mma_commit(bar(C::kBarQFree));
+          }
+          jb += nb;
+          ++piece;
+        }
+        // every product and every arrival it owes is done before the CTA ends
+        mma_commit(bar(C::kBarDone));
+        mbar_wait(bar(C::kBarDone), 0, a.status);
+      }
+      __syncwarp();
+    } else if (warp == kPfCheckWarp) {
+      // ===================== tables of a group agree =====================
+      // The units of kv head 0 cover every shared page once per 256 rows: each request of
+      // the unit must name the leader's pages, and they must be in the pool.
+      while (next_piece(a, cur, p)) {
+        if (!p.prefix || p.h != 0) continue;
+        const int p0 = p.i0 * kPfBlkTiles / tpp;
+        const int p1 = (min(p.i1 * kPfBlkTiles, p.tokens / kPfTile) + tpp - 1) / tpp;
+        const int32_t* lead = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
+        const int r0 = p.gfirst + p.row0 / a.G, r1 = p.gfirst + (p.row0 + p.rows - 1) / a.G;
+        for (int i = p0 + lane; i < p1; i += 32) {
+          const int want = __ldg(lead + i);
+          const bool in = want >= 0 && want < a.num_pages;
+#pragma unroll 4
+          for (int r = r0; r <= r1; ++r)
+            if (!in || __ldg(a.page_table + static_cast<int64_t>(r) * a.max_pages + i) != want) a.dead[r] = 1;
+        }
+      }
+    } else if (warp < 8) {
+      // ===================== softmax, a thread per row =====================
+      const int t = warp >> 2;                       // row tile
+      const int row = threadIdx.x & 127;
+      const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+      const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * 128 + lanes;
+      const float kscale = kFp8 ? __ldg(a.k_scale) : 1.f, vscale = kFp8 ? __ldg(a.v_scale) : 1.f;
+      const bool negate = a.sm_scale_log2 < 0.f;     // the sign goes to the query: maxima of raw scores are then those of scaled ones
+      const float base_mult = fabsf(a.sm_scale_log2) * kscale;
+      uint32_t ns = 0, piece = 0;                    // S blocks taken of this tile
+      while (next_piece(a, cur, p)) {
+        const bool pair = p.rows > 128;
+        const int lrow = pair ? t * 128 + row : row;  // row of the unit
+        const bool valid = lrow < p.rows;
+        const int grow = p.row0 + lrow;
+        const int64_t qrow = valid ? static_cast<int64_t>(p.gfirst + grow / a.G) * a.Hq + p.h * a.G + grow % a.G : 0;
+        const bool busy = __any_sync(kFull, valid);
+        // ---- the row's query into shared memory
+        if (piece > 0) wait(C::kBarQFree, piece - 1);
+        float mult = base_mult;
+        if (valid) {
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + qrow * kPfDim);
+          uint4 x[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = __ldg(src + k);
+          if (negate) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              x[k].x ^= 0x80008000u;
+              x[k].y ^= 0x80008000u;
+              x[k].z ^= 0x80008000u;
+              x[k].w ^= 0x80008000u;
+            }
+          }
+          uint8_t* const dst = sm + (pair ? t : 0) * C::kQTile + row * 128;
+          if (kFp8) {
+            uint32_t top = 0;  // largest |q|: bf16 magnitudes order as integers
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+            }
+            const float amax = bf16_bits_to_float(static_cast<uint16_t>(top));
+            int e = 0;
+            if (amax > 0.f && isfinite(amax)) e = min(max(7 - ilogbf(amax), -126), 126);
+            const float up = __int_as_float((127 + e) << 23);
+            mult = isfinite(amax) ? base_mult * __int_as_float((127 - e) << 23) : __int_as_float(0x7fffffff);
+            if (pair || t == 0) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t w[8] = {x[2 * k].x, x[2 * k].y, x[2 * k].z, x[2 * k].w,
+                                       x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
+                uint32_t c0[4], c1[4];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float lo = __uint_as_float(w[i] << 16) * up, hi = __uint_as_float(w[i] & 0xFFFF0000u) * up;
+                  const uint32_t h = f32x2_to_e4m3x2(lo, hi);
+                  const float2 f = e4m3x2_to_float2(h);
+                  const uint32_t g = f32x2_to_e4m3x2(lo - f.x, hi - f.y);
+                  if (i & 1) {
+                    c0[i >> 1] |= h << 16;
+                    c1[i >> 1] |= g << 16;
+                  } else {
+                    c0[i >> 1] = h;
+                    c1[i >> 1] = g;
+                  }
+                }
+                const int at = (k ^ (row & 7)) << 4;
+                *reinterpret_cast<uint4*>(dst + at) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
+                *reinterpret_cast<uint4*>(dst + 16384 + at) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+              }
+            }
+          } else if (pair || t == 0) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              *reinterpret_cast<uint4*>(dst + (k >> 3) * 16384 + (((k & 7) ^ (row & 7)) << 4)) = x[k];
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kBarQ));
+        // ---- blocks
+        float m = -INFINITY, l = 0.f;
+        bool any = false;
+        const int nb = p.i1 - p.i0;
+        for (int i = pair ? 0 : t; i < nb; i += pair ? 1 : 2) {
+          wait(C::kBarS + t, ns);
+          ++ns;
+          tc_fence_after();
+          if (busy) {
+            const int nv = min(kPfBlk, p.tokens - (p.i0 + i) * kPfBlk);
+            float s[32];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32(ts + 32 * c, s);
+              if (nv < kPfBlk) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (32 * c + k >= nv) s[k] = -INFINITY;
+              }
+#pragma unroll
+              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, s[k]);
+            }
+            const float mb = mx == -INFINITY ? -INFINITY : mx * mult;
+            const bool grow_row = mb > m + kPfGrow || (m == -INFINITY && mb != -INFINITY);
+            if (__any_sync(kFull, grow_row)) {
+              const float f = !grow_row ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - mb);
+              if (grow_row) m = mb;
+              l *= f;
+              if (any) {  // O of the blocks before, once their products are done
+                wait(C::kBarO + t, ns - 2);
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                  float o[32];
+                  tmem_ld32(to + 32 * c, o);
+                  uint32_t z[16];
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) z[k] = __float_as_uint(o[k] * f);
+                  tmem_st16(to + 32 * c, z);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) z[k] = __float_as_uint(o[16 + k] * f);
+                  tmem_st16(to + 32 * c + 16, z);
+                }
+              }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32(ts + 32 * c, s);
+              if (nv < kPfBlk) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (32 * c + k >= nv) s[k] = -INFINITY;
+              }
+              uint32_t w[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                float p0 = fast_exp2(fmaf(s[2 * k], mult, -ref)), p1 = fast_exp2(fmaf(s[2 * k + 1], mult, -ref));
+                if (nv < kPfBlk) {
+                  if (32 * c + 2 * k >= nv) p0 = 0.f;  // mult may be 0
+                  if (32 * c + 2 * k + 1 >= nv) p1 = 0.f;
+                }
+                sum[k & 3] += p0 + p1;
+                w[k] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+              }
+              tmem_st16(ts + 16 * c, w);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+          }
+          any = true;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kBarP + t));
+        }
+        // ---- the row's partial: pieces at a unit's start by row, others by CTA
+        int64_t slot = 0;
+        if (p.i0 == 0)
+          slot = static_cast<int64_t>((p.prefix ? 0 : 2) + (pair ? 0 : t)) * a.B * a.Hq + qrow;
+        else
+          slot = static_cast<int64_t>(4) * a.B * a.Hq + static_cast<int64_t>(blockIdx.x) * kPfUnitRows + t * 128 + row;
+        if (any) {
+          wait(C::kBarO + t, ns - 1);
+          tc_fence_after();
+          if (busy) {
+            float* const dst = a.part_o + slot * kPfDim;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float o[32];
+              tmem_ld32(to + 32 * c, o);
+              if (valid) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  *reinterpret_cast<float4*>(dst + 32 * c + 4 * k) =
+                      make_float4(o[4 * k] * vscale, o[4 * k + 1] * vscale, o[4 * k + 2] * vscale, o[4 * k + 3] * vscale);
+              }
+            }
+          }
+        }
+        if (valid) a.part_ml[slot] = make_float2(m, l);
+        ++piece;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPfMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// merge
+// ---------------------------------------------------------------------------
+// One warp per (request, query head): its partials are those of the prefix
+// unit's pieces and of its own unit's, in the order of the work list.  A lane
+// finds one partial (row in the partial arrays, m, l), then all lanes add its O.
+__global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const PfArgs a) {
+  griddep_wait();
+  const unsigned kFull = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kPfMergeWarps + (threadIdx.x >> 5);
+  if (row >= static_cast<int64_t>(a.B) * a.Hq) return;
+  const int r = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
+  const int h = hq / a.G, g = hq % a.G;
+  uint2* const out = reinterpret_cast<uint2*>(a.out + row * kPfDim) + lane;
+  const int64_t T = __ldcg(a.total), n = a.ctas, rows = static_cast<int64_t>(a.B) * a.Hq;
+  float M = -INFINITY, W = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool dead = __ldcg(a.dead + r) != 0;
+  if (!dead) {
+    const PfReq q = load_req(a, r);
+    int64_t own_y = q.y0;
+    auto merge_unit = [&](int64_t y, int blocks, int w, int kind, int subs, int lrow) {
+      const int c0 = owner_of(y, T, n), c1 = owner_of(y + static_cast<int64_t>(blocks - 1) * w, T, n);
+      const int cands = (c1 - c0 + 1) * subs;
+      for (int base = 0; base < cands; base += 32) {
+        const int k = base + lane;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        int64_t slot = 0;
+        if (k < cands) {
+          const int c = c0 + k / subs, sub = k % subs;
+          int i0, i1;
+          owned_blocks(y, blocks, w, range_begin(c, T, n), range_begin(c + 1, T, n), i0, i1);
+          slot = i0 == 0 ? static_cast<int64_t>(kind + sub) * rows + row
+                         : 4 * rows + static_cast<int64_t>(c) * kPfUnitRows + sub * 128 + lrow;
+          if (i0 < i1) ml = __ldcg(a.part_ml + slot);
+        }
+        float mx = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+        const float mn = fmaxf(M, mx);
+        const bool has = ml.x != -INFINITY;  // a NaN maximum counts
+        const float f = has ? fast_exp2(ml.x - mn) : 0.f;
+        float ws = ml.y * f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(kFull, ws, o);
+        const float old = M == -INFINITY ? 0.f : fast_exp2(M - mn);
+        W = W * old + ws;
+        acc.x *= old;
+        acc.y *= old;
+        acc.z *= old;
+        acc.w *= old;
+        M = mn;
+        unsigned todo = __ballot_sync(kFull, has);
+        while (todo) {
+          float fk[4];
+          float4 o[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int src = todo ? __ffs(todo) - 1 : 0;
+            const float fx = __shfl_sync(kFull, f, src);
+            const int64_t sx = __shfl_sync(kFull, slot, src);
+            fk[x] = todo ? fx : 0.f;
+            o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (todo) o[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + sx * kPfDim) + lane);
+            todo &= todo - 1;
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            acc.x = fmaf(o[x].x, fk[x], acc.x);
+            acc.y = fmaf(o[x].y, fk[x], acc.y);
+            acc.z = fmaf(o[x].z, fk[x], acc.z);
+            acc.w = fmaf(o[x].w, fk[x], acc.w);
+          }
+        }
+      }
+    };
+    if (q.ptiles > 0) {
+      const PfPrefix s = prefix_shape(q.ptiles, q.gcount, a.G);
+      const int64_t gy = q.gfirst == r ? q.y0 : load_req(a, q.gfirst).y0;
+      const int i = (r - q.gfirst) * a.G + g, u = i / kPfUnitRows;
+      const int w = u == s.units - 1 ? s.wlast : kPfCostPair;
+      merge_unit(gy + h * s.head_cost + static_cast<int64_t>(u) * kPfCostPair * s.blocks, s.blocks, w, 0,
+                 w == kPfCostPair ? 1 : 2, i % kPfUnitRows);
+      if (q.gfirst == r) own_y += s.head_cost * a.Hkv;
+    }
+    const int nb = own_blocks(q.stok);
+    if (nb > 0) merge_unit(own_y + static_cast<int64_t>(h) * nb * kPfCostSolo, nb, kPfCostSolo, 2, 2, g);
+  }
+  dead = dead || W == 0.f;
+  const float inv = dead ? 0.f : 1.f / W;
+  *out = dead ? make_uint2(0, 0)
+              : make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = dead ? -INFINITY : (M + __log2f(W)) * kPfLn2;
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+constexpr int kPfMaxDevices = 64;
+std::atomic<int> g_pf_ready[2][kPfMaxDevices];
+
+template <bool kFp8>
+int prepare_prefix(int dev) {
+  std::atomic<int>& slot = g_pf_ready[kFp8][dev];
+  if (slot.load(std::memory_order_relaxed) > 0) return FPK_OK;
+  if (cudaFuncSetAttribute(prefix_attn_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           PfCfg<kFp8>::kSmem) != cudaSuccess)
+    return FPK_ECUDA;
+  slot.store(1, std::memory_order_relaxed);
+  return FPK_OK;
+}
+
+struct PfLayout {
+  size_t gstart, first, dead, req, ml, o, total;
+};
+PfLayout prefix_layout(int64_t B, int64_t Hq, int64_t ctas) {
+  auto up = [](int64_t x) { return (static_cast<size_t>(x) + 255) & ~static_cast<size_t>(255); };
+  const int64_t slots = 4 * B * Hq + ctas * kPfUnitRows;
+  PfLayout l;
+  l.gstart = 256;
+  l.first = l.gstart + up((B + 1) * 4);
+  l.dead = l.first + up(ctas * 4);
+  l.req = l.dead + up(B * 4);
+  l.ml = l.req + up(B * static_cast<int64_t>(sizeof(PfReq)));
+  l.o = l.ml + up(slots * 8);
+  l.total = l.o + up(slots * kPfDim * 4);
+  return l;
+}
+
+// The pool as tiles of rows: K rows come first, V behind them; boxes of zbox tiles.
+int encode_prefix_map(CUtensorMap* m, const void* pool, int64_t tiles, bool fp8, bool v, int zbox) {
+  EncodeTiled enc = tensor_map_encoder();
+  if (enc == nullptr) return FPK_ECUDA;
+  const bool narrow = v && !fp8;  // bf16 V: rows of 16 tokens
+  const cuuint64_t inner = narrow ? 16 : 128, rows = narrow ? 256 : 32, el = fp8 ? 1 : 2;
+  const cuuint64_t dims[3] = {inner, rows, static_cast<cuuint64_t>(tiles)};
+  const cuuint64_t strides[2] = {inner * el, inner * el * rows};
+  const cuuint32_t box[3] = {narrow ? 16u : fp8 ? 128u : 64u, narrow ? 128u : 16u, static_cast<cuuint32_t>(zbox)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapSwizzle sw = !v ? CU_TENSOR_MAP_SWIZZLE_128B : fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_32B;
+  const CUresult r = enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                         const_cast<void*>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FPK_OK : FPK_ECUDA;
+}
+
+// Launches `kernel` as a programmatic dependent of the kernel before it.
+template <typename... Exp, typename... Act>
+int launch_dependent(void (*kernel)(Exp...), int grid, int threads, size_t smem, cudaStream_t s, Act&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Act&&>(args)...) != cudaSuccess) return FPK_ECUDA;
+  return checked_launch_status();
 }
 
 template <bool kFp8>
@@ -150,18 +1114,34 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
     return FPK_EINVAL;
   const int G = Hq / Hkv;
   if (D != kPfDim || G > kPfGroupMax || page_size % kPfTile != 0 || page_size > 256) return FPK_EUNSUPPORTED;
-  if (static_cast<int64_t>(B) * Hq > 0x7fffffff / 4) return FPK_EUNSUPPORTED;
+  const int tpp = page_size / kPfTile;
+  const int64_t tiles = static_cast<int64_t>(num_pages) * Hkv * tpp;
+  // tile numbers are 32-bit tensor-map coordinates; rows are counted in 31 bits
+  if (tiles > 0x7fffffff || static_cast<int64_t>(B) * Hq > 0x7fffffff / 4) return FPK_EUNSUPPORTED;
   if (B == 0) return FPK_OK;
   if (!q || !kv_pool || !page_table || !seq_lens || !out || !workspace) return FPK_EINVAL;
   if (kFp8 && (!k_scale || !v_scale)) return FPK_EINVAL;
-  if (n_groups > 0 && (!group_starts || !prefix_lens)) return FPK_EINVAL;
+  if (n_groups > B || (n_groups > 0 && (!group_starts || !prefix_lens))) return FPK_EINVAL;
   if (!aligned16(q) || !aligned16(kv_pool) || (reinterpret_cast<uintptr_t>(out) & 31u) != 0 ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return FPK_EINVAL;
-  if (workspace_bytes < prefix_workspace(B, Hq)) return FPK_ENOSPC;
-  PrefixArgs a;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kPfMaxDevices) return FPK_ECUDA;
+  const int ctas = device_sm_count(dev);
+  if (ctas <= 0) return FPK_ECUDA;
+  const PfLayout l = prefix_layout(B, Hq, ctas);
+  if (workspace_bytes < l.total) return FPK_ENOSPC;
+  const int st = prepare_prefix<kFp8>(dev);
+  if (st != FPK_OK) return st;
+  int zbox = 1;  // tiles per copy: a power of two that divides a page and a block
+  while (zbox < kPfBlkTiles && tpp % (2 * zbox) == 0) zbox *= 2;
+  CUtensorMap kmap, vmap;
+  if (encode_prefix_map(&kmap, kv_pool, tiles > 0 ? tiles : 1, kFp8, false, zbox) != FPK_OK ||
+      encode_prefix_map(&vmap, kv_pool, tiles > 0 ? tiles : 1, kFp8, true, zbox) != FPK_OK)
+    return FPK_ECUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PfArgs a;
   a.q = static_cast<const uint16_t*>(q);
-  a.kv_pool = static_cast<const uint8_t*>(kv_pool);
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.page_table = page_table;
@@ -171,6 +1151,14 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   a.prefix_lens = prefix_lens;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.total = reinterpret_cast<int64_t*>(ws + 8);
+  a.gstart = reinterpret_cast<int32_t*>(ws + l.gstart);
+  a.first = reinterpret_cast<int32_t*>(ws + l.first);
+  a.dead = reinterpret_cast<int32_t*>(ws + l.dead);
+  a.req = reinterpret_cast<PfReq*>(ws + l.req);
+  a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
+  a.part_o = reinterpret_cast<float*>(ws + l.o);
   a.n_groups = n_groups;
   a.B = B;
   a.Hq = Hq;
@@ -179,9 +1167,16 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   a.page_size = page_size;
   a.num_pages = num_pages;
   a.max_pages = max_pages;
+  a.ctas = ctas;
+  a.zbox = zbox;
   a.sm_scale_log2 = sm_scale * kPfLog2e;
-  prefix_simple_kernel<kFp8><<<B * Hkv, kPfDim, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return checked_launch_status();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  prefix_plan_kernel<<<1, kPfPlanThreads, 0, s>>>(a);
+  if (checked_launch_status() != FPK_OK) return FPK_ECUDA;
+  if (launch_dependent(prefix_attn_kernel<kFp8>, ctas, kPfThreads, PfCfg<kFp8>::kSmem, s, a, kmap, vmap) != FPK_OK)
+    return FPK_ECUDA;
+  const int merge = static_cast<int>((static_cast<int64_t>(B) * Hq + kPfMergeWarps - 1) / kPfMergeWarps);
+  return launch_dependent(prefix_merge_kernel, merge, 32 * kPfMergeWarps, 0, s, a);
 }
 
 }  // namespace
@@ -189,7 +1184,10 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
 
 extern "C" size_t fpk_prefix_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > fpk::kPfGroupMax || D != fpk::kPfDim) return 0;
-  return fpk::prefix_workspace(B, Hq);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= fpk::kPfMaxDevices) return 0;
+  const int ctas = fpk::device_sm_count(dev);
+  return ctas > 0 ? fpk::prefix_layout(B, Hq, ctas).total : 0;
 }
 
 extern "C" int fpk_paged_decode_attn_fp8_prefix(const void* q, const uint8_t* kv_pool, const float* k_scale,

@@ -516,7 +516,8 @@ int fpk_paged_decode_attn_bf16(const void* q, const void* kv_pool,
  * (e4m3 cache) or bf16 (bf16 cache), values enter exactly.  Repeated calls
  * on the same inputs give identical bits.
  * D == 128, page_size a multiple of 16 in [16, 256], 1 <= Hq / Hkv <= 8, else
- * FPK_EUNSUPPORTED; n_groups > 0 needs both group arrays (FPK_EINVAL).
+ * FPK_EUNSUPPORTED; n_groups is at most B, and above 0 it needs both group arrays
+ * (FPK_EINVAL).
  */
 size_t fpk_prefix_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D);
 int fpk_paged_decode_attn_fp8_prefix(const void* q, const uint8_t* kv_pool, const float* k_scale,

@@ -31,7 +31,7 @@ def test_prefix(lib, fp8):
         return f(q, kv, *sc, pt, mp, lens, None, gs, pl, n, out, None, ws, wsb, 0.1, B, Hq, Hkv, D, ps, pages, None)
 
     assert call(B=0, q=None, kv=None, out=None, ws=None, gs=None) == OK
-    for bad in (dict(B=-1), dict(Hq=0), dict(Hkv=0), dict(Hq=15), dict(n=-1), dict(mp=-1), dict(pages=-1),
+    for bad in (dict(B=-1), dict(Hq=0), dict(Hkv=0), dict(Hq=15), dict(n=-1), dict(n=3), dict(mp=-1), dict(pages=-1),
                 dict(ps=0), dict(q=None), dict(kv=None), dict(pt=None), dict(lens=None), dict(out=None),
                 dict(ws=None), dict(gs=None), dict(pl=None), dict(q=A + 2), dict(kv=A + 8), dict(out=A + 16),
                 dict(ws=A + 128)) + ((dict(ks=None), dict(vs=None)) if fp8 else ()):
