@@ -44,28 +44,32 @@ namespace {
 constexpr int kPfTile = 16;
 constexpr int kPfDim = 128;
 constexpr int kPfGroupMax = 8;
-constexpr int kPfBlk = 128;                    // tokens of a block
+constexpr int kPfBlk = 64;                     // tokens of a block
 constexpr int kPfBlkTiles = kPfBlk / kPfTile;
 constexpr int kPfUnitRows = 256;               // query rows of a prefix unit: two MMA tiles
 constexpr float kPfLog2e = 1.4426950408889634f;
 constexpr float kPfLn2 = 0.6931471805599453f;
 constexpr float kPfGrow = 8.f;                 // log2 growth of a maximum that rescales O
+// A row's scale is not taken below this (a scale of 0 leaves weights of 1 all the same): -inf times
+// it is -inf still.
+constexpr float kPfMinMult = 1e-37f;
 // Cost of a block in the work list, with both tiles at work and with one.
-constexpr int kPfCostPair = 3;
-constexpr int kPfCostSolo = 2;
+constexpr int kPfCostPair = 2;
+constexpr int kPfCostSolo = 1;
 
 constexpr int kPfThreads = 512;
-constexpr int kPfVWarp = 8, kPfLoadWarp = 12, kPfMmaWarp = 13, kPfCheckWarp = 14;
+constexpr int kPfVWarp = 8, kPfKLoadWarp = 12, kPfMmaWarp = 13, kPfVLoadWarp = 14, kPfPlanWarp = 15;
+constexpr int kPfPieces = 4;                   // pieces known ahead
 constexpr int kPfPlanThreads = 1024;
 constexpr int kPfMergeWarps = 4;
 
 // What the planning kernel finds of each request.
 struct PfReq {
-  int64_t y0;      // place of its units in the work list (the group's prefix units first, at its first request)
+  int32_t y0;      // place of its units in the work list (the group's prefix units first, at its first request)
   int32_t ptiles;  // tiles of the shared prefix
   int32_t stok;    // tokens behind it; 0 for a dead request
   int32_t gfirst, gcount, leader;
-  int32_t pad;
+  int32_t pad[2];
 };
 
 struct PfArgs {
@@ -80,9 +84,9 @@ struct PfArgs {
   uint16_t* out;
   float* lse;
   uint32_t* status;
-  int64_t* total;    // length of the work list
+  int32_t* total;    // length of the work list (the host has made sure that it fits)
+  PfReq* start;      // [ctas] the request in whose units a CTA's range begins: its record, pad = {r, total}
   int32_t* gstart;   // [n_groups + 1] group starts, clamped and non-decreasing
-  int32_t* first;    // [ctas] request in whose units a CTA's range begins
   int32_t* dead;     // [B]
   PfReq* req;        // [B]
   float2* part_ml;   // partials: 4 per (request, query head), then 256 rows per CTA
@@ -98,15 +102,17 @@ struct PfCfg {
   static constexpr int kQTile = 128 * 256;                     // parts (or halves) of a tile's queries
   static constexpr int kKStage = kPfBlk * kPfDim * kElem;
   static constexpr int kVStage = kKStage;
-  static constexpr int kKStages = kFp8 ? 3 : 2;
-  static constexpr int kVStages = 3;
+  static constexpr int kKStages = kFp8 ? 6 : 4;
+  static constexpr int kVStages = 6;
   static constexpr int kV16 = kPfBlk * kPfDim * 2;             // converted V block
-  static constexpr int kV16Bufs = kFp8 ? 2 : 0;
+  static constexpr int kV16Bufs = kFp8 ? 4 : 0;
   static constexpr int kOffK = 2 * kQTile;
   static constexpr int kOffV = kOffK + kKStages * kKStage;
   static constexpr int kOffV16 = kOffV + kVStages * kVStage;
-  static constexpr int kOffBars = kOffV16 + kV16Bufs * kV16;
-  // barriers
+  static constexpr int kOffMult = kOffV16 + kV16Bufs * kV16;   // score multiplier of each query row
+  static constexpr int kOffPiece = kOffMult + 2 * 128 * 4;
+  static constexpr int kOffBars = kOffPiece + kPfPieces * 48;
+  // barriers; a tile's S and P have one per buffer
   static constexpr int kReady = kFp8 ? kV16Bufs : kVStages;    // V blocks ready for the MMA
   static constexpr int kBarKFull = 0;
   static constexpr int kBarKFree = kBarKFull + kKStages;
@@ -114,12 +120,15 @@ struct PfCfg {
   static constexpr int kBarVFree = kBarVFull + kVStages;
   static constexpr int kBarReady = kBarVFree + kVStages;
   static constexpr int kBarUsed = kBarReady + kReady;          // e4m3: converted block read by the MMA
-  static constexpr int kBarS = kBarUsed + kV16Bufs;            // [2]
-  static constexpr int kBarP = kBarS + 2;                      // [2]
-  static constexpr int kBarO = kBarP + 2;                      // [2]
-  static constexpr int kBarQ = kBarO + 2;
-  static constexpr int kBarQFree = kBarQ + 1;
-  static constexpr int kBarDone = kBarQFree + 1;               // every MMA of the CTA completed
+  static constexpr int kBarS = kBarUsed + kV16Bufs;            // [tile][buffer]
+  static constexpr int kBarP = kBarS + 4;                      // [tile][buffer]
+  static constexpr int kBarO = kBarP + 4;                      // [tile][buffer] a product added to O
+  static constexpr int kBarOFree = kBarO + 4;                  // [tile] O of a piece read
+  static constexpr int kBarQ = kBarOFree + 2;                  // [buffer] queries staged
+  static constexpr int kBarQFree = kBarQ + 2;                  // [buffer] queries and multipliers of a piece read
+  static constexpr int kBarPiece = kBarQFree + 2;              // [kPfPieces] piece known
+  static constexpr int kBarPieceFree = kBarPiece + kPfPieces;  // [kPfPieces] piece read by every warp
+  static constexpr int kBarDone = kBarPieceFree + kPfPieces;   // every MMA of the CTA completed
   static constexpr int kBars = kBarDone + 1;
   static constexpr int kOffMisc = kOffBars + 8 * kBars;        // tensor memory base, failure flag
   static constexpr int kSmem = kOffMisc + 16 + 1024;
@@ -140,8 +149,7 @@ __device__ __forceinline__ int live_length(const PfArgs& a, int r) {
 // Prefix units of a group, per kv head: `units` of up to 256 rows, all but the
 // last of cost kPfCostPair per block, the last of cost `wlast`.
 struct PfPrefix {
-  int blocks, units, wlast;
-  int64_t head_cost;
+  int blocks, units, wlast, head_cost;
 };
 __device__ __forceinline__ PfPrefix prefix_shape(int ptiles, int gcount, int G) {
   PfPrefix p;
@@ -149,76 +157,90 @@ __device__ __forceinline__ PfPrefix prefix_shape(int ptiles, int gcount, int G) 
   p.blocks = (ptiles + kPfBlkTiles - 1) / kPfBlkTiles;
   p.units = (rows + kPfUnitRows - 1) / kPfUnitRows;
   p.wlast = rows - (p.units - 1) * kPfUnitRows > 128 ? kPfCostPair : kPfCostSolo;
-  p.head_cost = static_cast<int64_t>(p.blocks) * (static_cast<int64_t>(kPfCostPair) * (p.units - 1) + p.wlast);
+  p.head_cost = p.blocks * (kPfCostPair * (p.units - 1) + p.wlast);
   return p;
 }
 __device__ __forceinline__ int own_blocks(int stok) { return stok > 0 ? (stok - 1) / kPfBlk + 1 : 0; }
 
-// CTA c owns the blocks that start in [range_begin(c), range_begin(c + 1)).
-__device__ __forceinline__ int64_t range_begin(int64_t c, int64_t T, int64_t n) { return c * T / n; }
-__device__ __forceinline__ int owner_of(int64_t y, int64_t T, int64_t n) {
-  return static_cast<int>(((y + 1) * n - 1) / T);
+// CTA c owns the blocks that start in [begin(c), begin(c + 1)): T / n each, one
+// more for the first T mod n CTAs.
+struct PfRanges {
+  int share, more;
+  __device__ __forceinline__ int begin(int c) const { return c * share + min(c, more); }
+  __device__ __forceinline__ int owner(int y) const {
+    const int big = more * (share + 1);
+    return y < big ? y / (share + 1) : more + (y - big) / share;
+  }
+};
+__device__ __forceinline__ PfRanges ranges_of(int T, int n) {
+  PfRanges r;
+  r.share = T / n;
+  r.more = T - r.share * n;
+  return r;
 }
 // Blocks [i0, i1) of a unit at y with n blocks of cost w that a range [b0, b1) owns.
-__device__ __forceinline__ void owned_blocks(int64_t y, int n, int w, int64_t b0, int64_t b1, int& i0, int& i1) {
-  const int64_t lo = b0 <= y ? 0 : (b0 - y + w - 1) / w;
-  const int64_t hi = b1 <= y ? 0 : (b1 - y + w - 1) / w;
-  i0 = static_cast<int>(lo < n ? lo : n);
-  i1 = static_cast<int>(hi < n ? hi : n);
+__device__ __forceinline__ void owned_blocks(int y, int n, int w, int b0, int b1, int& i0, int& i1) {
+  i0 = min(n, b0 <= y ? 0 : (b0 - y + w - 1) / w);
+  i1 = min(n, b1 <= y ? 0 : (b1 - y + w - 1) / w);
 }
 
-struct PfPiece {
-  bool prefix;
+struct alignas(16) PfPiece {
+  int prefix;
   int r;           // request whose table is read (prefix: the leader)
   int h;
   int row0, rows;  // prefix: rows of the group; own: rows [0, G)
   int gfirst;      // request of row 0
-  int i0, i1;      // blocks of the unit
+  int i0, i1;      // blocks of the unit; none: the end
   int tile0;       // table tile of the unit's first token
   int tokens;      // of the unit
+  int qbuf;        // query buffer of a unit of one row tile
+  int pad;
+  __device__ __forceinline__ bool pair() const { return rows > 128; }
 };
+static_assert(sizeof(PfPiece) == 48, "slot of the piece ring");
 
 struct PfCursor {
   PfReq q;
   int r, h, u;  // u: prefix unit of the head, -1 in a request's own units
-  int64_t y, b0, b1;
+  int y, b0, b1;
 };
 
-__device__ __forceinline__ PfReq load_req(const PfArgs& a, int r) {
+__device__ __forceinline__ PfReq load_req(const PfReq* at) {
   PfReq q;
-  const int4* p = reinterpret_cast<const int4*>(a.req + r);
+  const int4* p = reinterpret_cast<const int4*>(at);
   const int4 x = __ldcg(p), z = __ldcg(p + 1);
-  q.y0 = static_cast<int64_t>((static_cast<uint64_t>(static_cast<uint32_t>(x.y)) << 32) | static_cast<uint32_t>(x.x));
-  q.ptiles = x.z;
-  q.stok = x.w;
-  q.gfirst = z.x;
-  q.gcount = z.y;
-  q.leader = z.z;
+  q.y0 = x.x;
+  q.ptiles = x.y;
+  q.stok = x.z;
+  q.gfirst = x.w;
+  q.gcount = z.x;
+  q.leader = z.y;
+  q.pad[0] = z.z;
+  q.pad[1] = z.w;
   return q;
 }
 
-__device__ __forceinline__ void enter_request(const PfArgs& a, PfCursor& c) {
-  c.q = load_req(a, c.r);
+__device__ __forceinline__ void enter_request(PfCursor& c, int r, const PfReq& q) {
+  c.q = q;
+  c.r = r;
   c.h = 0;
   c.u = c.q.ptiles > 0 && c.q.gfirst == c.r ? 0 : -1;
   c.y = c.q.y0;
 }
 
-__device__ __forceinline__ PfCursor begin_range(const PfArgs& a, int64_t b0, int64_t b1) {
+__device__ __forceinline__ PfCursor begin_range(const PfArgs& a, const PfReq& q, int b0, int b1) {
   PfCursor c;
   c.b0 = b0;
   c.b1 = b1;
-  c.r = __ldcg(a.first + blockIdx.x);
-  enter_request(a, c);
-  int64_t at = b0 - c.y;
+  enter_request(c, q.pad[0], q);
+  int at = b0 - c.y;
   if (c.u == 0) {
     const PfPrefix p = prefix_shape(c.q.ptiles, c.q.gcount, a.G);
-    const int64_t all = p.head_cost * a.Hkv;
+    const int all = p.head_cost * a.Hkv;
     if (at < all) {
-      c.h = static_cast<int>(at / p.head_cost);
-      const int64_t step = static_cast<int64_t>(kPfCostPair) * p.blocks;
-      const int64_t u = at % p.head_cost / step;
-      c.u = static_cast<int>(u < p.units ? u : p.units - 1);
+      c.h = at / p.head_cost;
+      const int step = kPfCostPair * p.blocks;
+      c.u = min((at - c.h * p.head_cost) / step, p.units - 1);
       c.y += c.h * p.head_cost + c.u * step;
       return c;
     }
@@ -226,10 +248,9 @@ __device__ __forceinline__ PfCursor begin_range(const PfArgs& a, int64_t b0, int
     c.y += all;
     at -= all;
   }
-  const int64_t cost = static_cast<int64_t>(kPfCostSolo) * own_blocks(c.q.stok);
+  const int cost = kPfCostSolo * own_blocks(c.q.stok);
   if (cost > 0) {
-    const int64_t h = at / cost;
-    c.h = static_cast<int>(h < a.Hkv ? h : a.Hkv);
+    c.h = min(at / cost, a.Hkv);
     c.y += c.h * cost;
   }
   return c;
@@ -243,7 +264,7 @@ __device__ __forceinline__ bool next_piece(const PfArgs& a, PfCursor& c, PfPiece
       const PfPrefix s = prefix_shape(c.q.ptiles, c.q.gcount, a.G);
       n = s.blocks;
       w = c.u == s.units - 1 ? s.wlast : kPfCostPair;
-      p.prefix = true;
+      p.prefix = 1;
       p.r = c.q.leader;
       p.row0 = c.u * kPfUnitRows;
       p.rows = min(kPfUnitRows, c.q.gcount * a.G - p.row0);
@@ -252,7 +273,7 @@ __device__ __forceinline__ bool next_piece(const PfArgs& a, PfCursor& c, PfPiece
       p.h = c.h;
       p.gfirst = c.q.gfirst;
       owned_blocks(c.y, n, w, c.b0, c.b1, p.i0, p.i1);
-      c.y += static_cast<int64_t>(n) * w;
+      c.y += n * w;
       if (++c.u == s.units) {
         c.u = 0;
         if (++c.h == a.Hkv) {
@@ -263,11 +284,11 @@ __device__ __forceinline__ bool next_piece(const PfArgs& a, PfCursor& c, PfPiece
     } else {
       n = own_blocks(c.q.stok);
       if (n == 0 || c.h >= a.Hkv) {
-        if (++c.r >= a.B) return false;
-        enter_request(a, c);
+        if (c.r + 1 >= a.B) return false;
+        enter_request(c, c.r + 1, load_req(a.req + c.r + 1));
         continue;
       }
-      p.prefix = false;
+      p.prefix = 0;
       p.r = c.r;
       p.row0 = 0;
       p.rows = a.G;
@@ -276,7 +297,7 @@ __device__ __forceinline__ bool next_piece(const PfArgs& a, PfCursor& c, PfPiece
       p.h = c.h;
       p.gfirst = c.r;
       owned_blocks(c.y, n, kPfCostSolo, c.b0, c.b1, p.i0, p.i1);
-      c.y += static_cast<int64_t>(n) * kPfCostSolo;
+      c.y += n * kPfCostSolo;
       ++c.h;
     }
     if (p.i0 < p.i1) return true;
@@ -286,7 +307,7 @@ __device__ __forceinline__ bool next_piece(const PfArgs& a, PfCursor& c, PfPiece
 // One CTA: group ranges, shared pages and leaders, the work list and every CTA's
 // first request.
 __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const PfArgs a) {
-  __shared__ int64_t s_sum[kPfPlanThreads / 32];
+  __shared__ int s_sum[kPfPlanThreads / 32];
   __shared__ int s_max[kPfPlanThreads / 32];
   griddep_launch_dependents();
   const unsigned kFull = 0xffffffffu;
@@ -353,35 +374,46 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
   // places in the work list
   const int chunk = (a.B + kPfPlanThreads - 1) / kPfPlanThreads;
   const int rb = min(a.B, t * chunk), re = min(a.B, rb + chunk);
-  auto cost_of = [&](int r) -> int64_t {
+  auto cost_of = [&](int r) -> int {
     const PfReq& q = a.req[r];
-    int64_t c = static_cast<int64_t>(kPfCostSolo) * own_blocks(q.stok);
+    int c = kPfCostSolo * own_blocks(q.stok);
     if (q.ptiles > 0 && q.gfirst == r) c += prefix_shape(q.ptiles, q.gcount, a.G).head_cost;
     return c * a.Hkv;
   };
-  int64_t mine = 0;
+  int mine = 0;
   for (int r = rb; r < re; ++r) mine += cost_of(r);
-  int64_t incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(kFull, incl, o);
+    const int v = __shfl_up_sync(kFull, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) s_sum[warp] = incl;
   __syncthreads();
-  int64_t y = incl - mine, T = 0;
+  int y = incl - mine, T = 0;
   for (int k = 0; k < kPfPlanThreads / 32; ++k) {
     if (k < warp) y += s_sum[k];
     T += s_sum[k];
   }
   if (t == 0) *a.total = T;
-  const int64_t n = a.ctas;
   for (int r = rb; r < re; ++r) {
-    const int64_t c = cost_of(r);
     a.req[r].y0 = y;
-    if (c > 0)  // the CTAs whose ranges begin within [y, y + c)
-      for (int64_t k = (y * n + T - 1) / T; k < n && range_begin(k, T, n) < y + c; ++k) a.first[k] = r;
-    y += c;
+    y += cost_of(r);
+  }
+  __syncthreads();
+  // every CTA's first request: the last one whose units start at or before its range
+  const PfRanges rg = ranges_of(T, a.ctas);
+  for (int c = t; c < a.ctas; c += kPfPlanThreads) {
+    const int b0 = rg.begin(c);
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.req[mid].y0 <= b0) lo = mid; else hi = mid - 1;
+    }
+    PfReq q = a.req[lo];
+    q.pad[0] = lo;
+    q.pad[1] = T;
+    a.start[c] = q;
   }
 }
 
@@ -403,11 +435,14 @@ __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
   return pol;
 }
 
-// Instruction descriptors, M = N = 128, both operands K-major, D in fp32.
-constexpr uint32_t kPfShape = (1u << 4) | (static_cast<uint32_t>(128 >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
-constexpr uint32_t kPfE4m3 = kPfShape;                            // kind::f8f6f4, E4M3 x E4M3
-constexpr uint32_t kPfF16 = kPfShape;                             // kind::f16, F16 x F16
-constexpr uint32_t kPfBf16 = kPfShape | (1u << 7) | (1u << 10);   // kind::f16, BF16 x BF16
+// Instruction descriptors: M = 128, both operands K-major, D in fp32; S has N = 64 (tokens), O
+// N = 128 (dims).
+constexpr uint32_t pf_idesc(int n, uint32_t type) {
+  return (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(128 >> 4) << 24);
+}
+constexpr uint32_t kPfSE4m3 = pf_idesc(kPfBlk, 0), kPfSBf16 = pf_idesc(kPfBlk, 1);  // kind::f8f6f4, kind::f16
+constexpr uint32_t kPfOF16 = pf_idesc(kPfDim, 0), kPfOBf16 = pf_idesc(kPfDim, 1);   // kind::f16
 
 // S = Q K^T: both operands from shared memory.
 template <bool kFp8>
@@ -416,13 +451,13 @@ __device__ __forceinline__ void mma_s(uint32_t d, uint64_t adesc, uint64_t bdesc
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(kPfE4m3), "r"(acc)
+        "l"(adesc), "l"(bdesc), "r"(kPfSE4m3), "r"(acc)
         : "memory");
   else
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(kPfBf16), "r"(acc)
+        "l"(adesc), "l"(bdesc), "r"(kPfSBf16), "r"(acc)
         : "memory");
 }
 
@@ -432,7 +467,7 @@ __device__ __forceinline__ void mma_o(uint32_t d, uint32_t a, uint64_t bdesc, ui
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(kFp8 ? kPfF16 : kPfBf16), "r"(acc)
+      "r"(a), "l"(bdesc), "r"(kFp8 ? kPfOF16 : kPfOBf16), "r"(acc)
       : "memory");
 }
 
@@ -440,8 +475,9 @@ __device__ __forceinline__ void mma_o(uint32_t d, uint32_t a, uint64_t bdesc, ui
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+      "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32]; "
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
@@ -453,15 +489,75 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+// 64 consecutive columns of this thread's tensor memory lane, waited for.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+      "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, "
+      "%42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+      "%62, %63}, [%64]; "
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+      "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32}; "
+      ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+
+// Packed fp32 pairs and the three-input maximum: one instruction each on sm_103a.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// One lane of the (converged) warp: tcgen05 instructions of an elected lane keep
+// their operands in uniform registers, which those of `if (lane == 0)` do not.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
 
 // A wait that gives up once any wait of the CTA has: control flow then runs on
 // to the end without waiting (every address stays in range; the results are
@@ -492,24 +588,27 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   uint8_t* const sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const uint32_t sbase = smem_addr(sm);
   auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8 * i; };
+  float* const s_mult = reinterpret_cast<float*>(sm + C::kOffMult);
+  PfPiece* const s_piece = reinterpret_cast<PfPiece*>(sm + C::kOffPiece);
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
   volatile int* const s_failed = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned kFull = 0xffffffffu;
+  const int warp = __shfl_sync(kFull, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   griddep_launch_dependents();
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kBars; ++i) {
-      int arrivals = 1;
-      if (i >= C::kBarReady && i < C::kBarReady + C::kReady) arrivals = 4;             // V warps
-      if (kFp8 && i >= C::kBarVFree && i < C::kBarVFree + C::kVStages) arrivals = 4;   // V warps
-      if (i >= C::kBarP && i < C::kBarP + 2) arrivals = 4;                             // a tile's softmax warps
-      if (i == C::kBarQ) arrivals = 8;                                                 // all softmax warps
-      mbar_init(bar(i), arrivals);
-    }
-    *s_failed = 0;
+  if (threadIdx.x < C::kBars) {
+    const int i = threadIdx.x;
+    int arrivals = 1;
+    if (i >= C::kBarReady && i < C::kBarReady + C::kReady) arrivals = 4;             // V warps
+    if (kFp8 && i >= C::kBarVFree && i < C::kBarVFree + C::kVStages) arrivals = 4;   // V warps
+    if (i >= C::kBarP && i < C::kBarP + 4) arrivals = 4;                             // a tile's softmax warps
+    if (i >= C::kBarOFree && i < C::kBarQFree) arrivals = 4;                         // (also Q)
+    if (i >= C::kBarQFree && i < C::kBarQFree + 2) arrivals = 9;                     // the MMA, all softmax warps
+    if (i >= C::kBarPieceFree && i < C::kBarPieceFree + kPfPieces) arrivals = 15;    // every other warp
+    mbar_init(bar(i), arrivals);
     fence_barrier_init();
   }
+  if (threadIdx.x == 0) *s_failed = 0;
   if (warp == kPfMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)),
                  "r"(512)
@@ -521,83 +620,203 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   tc_fence_after();
   griddep_wait();  // the plan is there
   const uint32_t tmem = *s_tmem;
-  const int64_t T = __ldcg(a.total);
-  const int64_t b0 = range_begin(blockIdx.x, T, a.ctas), b1 = range_begin(blockIdx.x + 1, T, a.ctas);
+  const PfReq first = load_req(a.start + blockIdx.x);
+  const PfRanges rg = ranges_of(first.pad[1], a.ctas);
+  const int b0 = rg.begin(blockIdx.x), b1 = rg.begin(blockIdx.x + 1);
   auto wait = [&](int i, uint32_t parity) { pf_wait(bar(i), parity & 1u, a.status, s_failed); };
+  // the next piece, from the planning warp; false at the end
+  uint32_t pn = 0;
+  auto take_piece = [&](PfPiece& p) -> bool {
+    wait(C::kBarPiece + pn % kPfPieces, pn / kPfPieces);
+    p = s_piece[pn % kPfPieces];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::kBarPieceFree + pn % kPfPieces));
+    ++pn;
+    return p.i0 < p.i1 && !*s_failed;
+  };
+  // query rows [row, row + n) of a unit, by one warp, into rows `at`.. of a query buffer: half a warp per row
+  // (a lane: 8 dims), the next rows' loads ahead
+  auto stage_rows = [&](const PfPiece& p, int buf, int row, int at, int n) {
+    const int c = lane & 15;
+    auto load = [&](int k) -> uint4 {
+      const int i = k + (lane >> 4), g = p.row0 + row + i;
+      if (i >= n) return make_uint4(0, 0, 0, 0);
+      return __ldg(reinterpret_cast<const uint4*>(
+                       a.q + (static_cast<int64_t>(p.gfirst + g / a.G) * a.Hq + p.h * a.G + g % a.G) * kPfDim) + c);
+    };
+    const float base = fabsf(a.sm_scale_log2) * (kFp8 ? __ldg(a.k_scale) : 1.f);
+    // a negative scale's sign goes to the query: maxima of raw scores are then those of scaled ones
+    const uint32_t flip = a.sm_scale_log2 < 0.f ? 0x80008000u : 0u;
+    uint4 x0 = load(0), x1 = load(2), x2 = load(4), x3 = load(6);
+#pragma unroll 1
+    for (int k = 0; k < n; k += 2) {
+      const uint32_t w[4] = {x0.x ^ flip, x0.y ^ flip, x0.z ^ flip, x0.w ^ flip};
+      x0 = x1;
+      x1 = x2;
+      x2 = x3;
+      x3 = load(k + 8);
+      const int rr = at + k + (lane >> 4);
+      uint8_t* const dst = sm + buf * C::kQTile + rr * 128;
+      if (kFp8) {
+        uint32_t top = 0;  // largest |q|: bf16 magnitudes order as integers
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+        // e4m3 parts of q 2^e with its largest value in [128, 256): e = 134 - its exponent
+        const int ex = static_cast<int>(top >> 7);
+        const int e = ex == 0 ? (top == 0 ? 0 : 126) : min(max(134 - ex, -126), 126);
+        const float up = __int_as_float((127 + e) << 23);
+        uint32_t c0[2], c1[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float lo = __uint_as_float(w[i] << 16) * up, hi = __uint_as_float(w[i] & 0xFFFF0000u) * up;
+          const uint32_t u = f32x2_to_e4m3x2(lo, hi);
+          const float2 f = e4m3x2_to_float2(u);
+          const uint32_t v = f32x2_to_e4m3x2(lo - f.x, hi - f.y);
+          if (i & 1) {
+            c0[i >> 1] |= u << 16;
+            c1[i >> 1] |= v << 16;
+          } else {
+            c0[i >> 1] = u;
+            c1[i >> 1] = v;
+          }
+        }
+        if (rr < at + n) {
+          uint8_t* const d = dst + (((c >> 1) ^ (rr & 7)) << 4) + (c & 1) * 8;
+          *reinterpret_cast<uint2*>(d) = make_uint2(c0[0], c0[1]);
+          *reinterpret_cast<uint2*>(d + 16384) = make_uint2(c1[0], c1[1]);
+          if (c == 0)
+            s_mult[buf * 128 + rr] =
+                ex == 255 ? __int_as_float(0x7fffffff) : fmaxf(base * __int_as_float((127 - e) << 23), kPfMinMult);
+        }
+      } else if (rr < at + n) {
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (c == 0) s_mult[buf * 128 + rr] = fmaxf(base, kPfMinMult);
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
 
   if (b0 < b1) {
-    PfCursor cur = begin_range(a, b0, b1);
     PfPiece p;
     const int tpp = a.page_size >> 4;
-    if (warp == kPfLoadWarp) {
-      // ===================== K and V blocks into their rings =====================
-      // Lane c + 8 k copies box c of a block (zbox tiles, within a page), k = 0: K (bf16:
-      // its first 64 dims), 1: V (bf16: K's other dims), 2: bf16 V.
+    if (warp == kPfPlanWarp) {
+      // ===================== pieces, ahead of the other warps =====================
+      // Also the queries of own units (a few rows), and the check that a group's tables agree: the
+      // prefix units of kv head 0 cover every shared page once per 256 rows, and each request of the
+      // unit must name the leader's pages, which must be in the pool.
+      PfCursor cur = begin_range(a, first, b0, b1);
+      uint32_t n = 0, uses[2] = {0, 0};
+      int qbuf = 1;
+      for (bool more = true; more; ++n) {
+        more = next_piece(a, cur, p);
+        if (!more) p.i0 = p.i1 = 0;
+        const bool pair = p.pair();
+        qbuf ^= 1;
+        p.qbuf = qbuf;
+        if (n >= kPfPieces) wait(C::kBarPieceFree + n % kPfPieces, n / kPfPieces - 1);
+        if (lane == 0) {
+          s_piece[n % kPfPieces] = p;
+          mbar_arrive(bar(C::kBarPiece + n % kPfPieces));
+        }
+        __syncwarp();
+        if (!more) break;
+        // (every use of a buffer is waited for in turn, whoever stages it: a barrier's parity tells
+        // neighbouring phases apart, no others)
+        if (uses[qbuf] > 0) wait(C::kBarQFree + qbuf, uses[qbuf] - 1);
+        if (pair && uses[qbuf ^ 1] > 0) wait(C::kBarQFree + (qbuf ^ 1), uses[qbuf ^ 1] - 1);
+        if (!p.prefix) {
+          stage_rows(p, qbuf, 0, 0, p.rows);
+          if (lane < 4) mbar_arrive(bar(C::kBarQ + qbuf));
+        }
+        ++uses[qbuf];
+        if (pair) ++uses[qbuf ^ 1];
+        if (p.prefix && p.h == 0) {
+          const int p0 = p.i0 * kPfBlkTiles / tpp;
+          const int p1 = (min(p.i1 * kPfBlkTiles, p.tokens / kPfTile) + tpp - 1) / tpp;
+          const int32_t* lead = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
+          const int r0 = p.gfirst + p.row0 / a.G, r1 = p.gfirst + (p.row0 + p.rows - 1) / a.G;
+          for (int i = p0 + lane; i < p1; i += 32) {
+            const int want = __ldg(lead + i);
+            const bool in = want >= 0 && want < a.num_pages;
+#pragma unroll 4
+            for (int r = r0; r <= r1; ++r)
+              if (!in || __ldg(a.page_table + static_cast<int64_t>(r) * a.max_pages + i) != want) a.dead[r] = 1;
+          }
+        }
+      }
+    } else if (warp == kPfKLoadWarp || warp == kPfVLoadWarp) {
+      // ===================== K rows, V tiles into their rings =====================
+      // Lane c copies box c of a block (zbox tiles, within a page); bf16 K: lanes 4 + c the other 64 dims.
+      const bool kw = warp == kPfKLoadWarp;
       const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
-      const int c = lane & 7, part = lane >> 3;
+      const int c = lane & 3, part = lane >> 2;
       const int boxes = kPfBlkTiles / a.zbox;
-      uint32_t j = 0;
-      while (next_piece(a, cur, p)) {
+      const int stages = kw ? C::kKStages : C::kVStages;
+      const int full = kw ? C::kBarKFull : C::kBarVFull, free = kw ? C::kBarKFree : C::kBarVFree;
+      const int parts = kw && !kFp8 ? 2 : 1;
+      const uint32_t ring = sbase + (kw ? C::kOffK : C::kOffV);
+      uint32_t j = 0, st = 0, round = 0;
+      while (take_piece(p)) {
         const int32_t* row = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
         const int tiles = (p.tokens + kPfTile - 1) / kPfTile;
         auto page_of = [&](int i) -> int {  // page of box c of block i, -2: no such box
           const int t = i * kPfBlkTiles + c * a.zbox;
           return c < boxes && t < tiles && i < p.i1 ? __ldg(row + (p.tile0 + t) / tpp) : -2;
         };
-        int next = page_of(p.i0);
+        int next = page_of(p.i0), next2 = page_of(p.i0 + 1);
         const uint64_t pol = p.prefix ? again : once;
         for (int i = p.i0; i < p.i1; ++i, ++j) {
           const int pg = next;
-          next = page_of(i + 1);
-          const uint32_t ks = j % C::kKStages, vs = j % C::kVStages;
-          if (j >= static_cast<uint32_t>(C::kKStages)) wait(C::kBarKFree + ks, j / C::kKStages - 1);
-          if (j >= static_cast<uint32_t>(C::kVStages)) wait(C::kBarVFree + vs, j / C::kVStages - 1);
+          next = next2;
+          next2 = page_of(i + 2);
+          if (round > 0) wait(free + st, round - 1);
           const bool good = pg >= 0 && pg < a.num_pages;
-          // a page outside the pool: the request is dead (a group's are told apart by the check warp)
+          // a page outside the pool: the request is dead (a group's are told apart by the planning warp)
           if (!good && pg != -2 && !p.prefix) a.dead[p.r] = 1;
           const int n = __popc(__ballot_sync(kFull, good && part == 0));
+          const uint32_t f = bar(full + st);
           if (lane == 0) {
             const uint32_t bytes = static_cast<uint32_t>(n * a.zbox) * kPfTile * kPfDim * C::kElem;
-            if (bytes == 0) {
-              mbar_arrive(bar(C::kBarKFull + ks));
-              mbar_arrive(bar(C::kBarVFull + vs));
-            } else {
-              mbar_arrive_expect_tx(bar(C::kBarKFull + ks), bytes);
-              mbar_arrive_expect_tx(bar(C::kBarVFull + vs), bytes);
-            }
+            if (bytes == 0) mbar_arrive(f);
+            else mbar_arrive_expect_tx(f, bytes);
           }
           __syncwarp();
-          if (good) {
+          if (good && part < parts) {
             const int tile = p.tile0 + i * kPfBlkTiles + c * a.zbox;
             const int z = (pg * a.Hkv + p.h) * tpp + tile % tpp;
-            const uint32_t kdst = sbase + C::kOffK + ks * C::kKStage + c * a.zbox * kPfTile * 128;
-            const uint32_t vdst = sbase + C::kOffV + vs * C::kVStage + c * a.zbox * kPfTile * kPfDim * C::kElem;
-            if (part == 0) tma_load_3d(kdst, &kmap, 0, 0, z, bar(C::kBarKFull + ks), pol);
-            if (!kFp8 && part == 1) tma_load_3d(kdst + kPfBlk * 128, &kmap, 64, 0, z, bar(C::kBarKFull + ks), pol);
-            if (part == (kFp8 ? 1 : 2)) tma_load_3d(vdst, &vmap, 0, kFp8 ? 16 : 128, z, bar(C::kBarVFull + vs), pol);
+            const uint32_t dst = ring + st * C::kKStage;
+            if (kw)
+              tma_load_3d(dst + part * kPfBlk * 128 + c * a.zbox * kPfTile * 128, &kmap, part * 64, 0, z, f, pol);
+            else
+              tma_load_3d(dst + c * a.zbox * kPfTile * kPfDim * C::kElem, &vmap, 0, kFp8 ? 16 : 128, z, f, pol);
+          }
+          if (++st == static_cast<uint32_t>(stages)) {
+            st = 0;
+            ++round;
           }
         }
       }
       // every copy has landed before the CTA ends, even if a wait gave up
       if (lane == 0) {
-        for (uint32_t b = j > C::kKStages ? j - C::kKStages : 0; b < j; ++b)
-          mbar_wait(bar(C::kBarKFull + b % C::kKStages), (b / C::kKStages) & 1, a.status);
-        for (uint32_t b = j > C::kVStages ? j - C::kVStages : 0; b < j; ++b)
-          mbar_wait(bar(C::kBarVFull + b % C::kVStages), (b / C::kVStages) & 1, a.status);
+        for (uint32_t b = j > static_cast<uint32_t>(stages) ? j - stages : 0; b < j; ++b)
+          mbar_wait(bar(full + b % stages), (b / stages) & 1, a.status);
       }
     } else if (warp >= kPfVWarp && warp < kPfVWarp + 4) {
       // ===================== V blocks made ready for the MMA =====================
       const int d = threadIdx.x - kPfVWarp * 32;  // this thread's dim
       uint32_t j = 0;
-      while (next_piece(a, cur, p)) {
+      while (take_piece(p)) {
         for (int i = p.i0; i < p.i1; ++i, ++j) {
           const int nv = min(kPfBlk, p.tokens - i * kPfBlk);
           const uint32_t vs = j % C::kVStages;
           uint8_t* const v = sm + C::kOffV + vs * C::kVStage;
           wait(C::kBarVFull + vs, j / C::kVStages);
           if (kFp8) {
-            const uint32_t buf = j & 1;
-            if (j >= 2) wait(C::kBarUsed + buf, (j >> 1) - 1);
+            const uint32_t buf = j % C::kReady;
+            if (j >= static_cast<uint32_t>(C::kReady)) wait(C::kBarUsed + buf, j / C::kReady - 1);
             uint8_t* const o = sm + C::kOffV16 + buf * C::kV16 + d * 16;
 #pragma unroll
             for (int t = 0; t < kPfBlkTiles; ++t) {
@@ -608,17 +827,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               e4m3x4_to_f16x4(x.y, y[2], y[3]);
               e4m3x4_to_f16x4(x.z, y[4], y[5]);
               e4m3x4_to_f16x4(x.w, y[6], y[7]);
-              if (nv < (t + 1) * kPfTile) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const int left = nv - t * kPfTile - 2 * k;  // tokens of this pair that exist
-                  if (left <= 0) y[k] = 0;
-                  else if (left == 1) y[k] &= 0xFFFFu;
-                }
-              }
               uint4* const w = reinterpret_cast<uint4*>(o + t * kPfTile * kPfDim * 2);
               w[0] = make_uint4(y[0], y[1], y[2], y[3]);
               w[128] = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+            if (nv < kPfBlk) {  // f16 of token k, dim d: tile k / 16, row of 8 tokens (k / 8) % 2
+              for (int k = nv; k < kPfBlk; ++k)
+                *reinterpret_cast<uint16_t*>(o + (k >> 4) * 4096 + ((k >> 3) & 1) * 2048 + (k & 7) * 2) = 0;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -642,275 +857,240 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
       }
     } else if (warp == kPfMmaWarp) {
-      // ===================== MMA issue (one thread) =====================
-      if (lane == 0) {
-        uint32_t jb = 0;               // blocks of earlier pieces
-        uint32_t np[2] = {0, 0};       // P blocks taken of each tile
-        uint32_t piece = 0;
-        auto issue_s = [&](int t, int qt, uint32_t j) {
-          const uint32_t q = sbase + qt * C::kQTile;
-          const uint32_t k = sbase + C::kOffK + (j % C::kKStages) * C::kKStage;
-          // e4m3: two query parts against the same K rows; bf16: two halves of the dims
+      // ===================== MMA issue =====================
+      // The warp runs as one, an elected lane issues.  One loop polls for whatever can go out next (its
+      // code has to stay small: it is all fetched once per block): the oldest PV that is owed, and the
+      // next S.  S runs ahead of PV by two blocks of a tile (its two S buffers), across pieces; owed PVs
+      // wait in a queue in the order of their S, an entry being block << 3 | last of its block << 2 |
+      // first of its tile in the piece << 1 | tile.
+      const uint64_t qdesc = smem_desc(sbase, 16, 1024, 2);
+      const uint64_t kdesc = smem_desc(sbase + C::kOffK, 16, 1024, 2);
+      // V, 16 tokens a step: e4m3 as two columns of core matrices (8 dims x 8 tokens, 128 B apart along
+      // the dims, 2 KiB along the tokens), bf16 as rows of 32 bytes with the 32-byte swizzle
+      const uint64_t vdesc = kFp8 ? smem_desc(sbase + C::kOffV16, 2048, 128, 0) : smem_desc(sbase + C::kOffV, 16, 256, 6);
+      uint32_t j = 0;                       // K blocks taken
+      uint32_t ns[2] = {0, 0};              // S issued of each tile
+      uint32_t np[2] = {0, 0};              // PV issued of each tile
+      uint32_t begun[2] = {0, 0};           // pieces begun in each tile's O
+      uint32_t uses[2] = {0, 0};            // query buffers taken
+      uint32_t q0 = 0, q1 = 0, q2 = 0, q3 = 0, owed = 0;
+      bool have = false, more = true, q_ok = false, k_ok = false, pair = false;
+      int i = 0, nb = 0;
+      uint32_t t = 0, idle = 0;             // tile of the next S
+      uint64_t since = 0;
+      auto test = [&](int b, uint32_t phase) { return mbar_test(bar(b), phase & 1); };
+      while (have || more || owed > 0) {
+        ++idle;
+        if (owed > 0) {
+          const uint32_t ot = q0 & 1, vj = q0 >> 3;
+          const bool begins = (q0 & 2) != 0;
+          const uint32_t n = ot ? np[1] : np[0], k = ot ? begun[1] : begun[0];
+          if (__all_sync(kFull, test(C::kBarP + 2 * ot + (n & 1), n >> 1) &&
+                                    test(C::kBarReady + vj % C::kReady, vj / C::kReady) &&
+                                    (!begins || k == 0 || test(C::kBarOFree + ot, k - 1)))) {
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t vd = vdesc + (vj % C::kReady) * ((kFp8 ? C::kV16 : C::kVStage) >> 4);
+              const uint32_t pt = tmem + ot * 128 + (n & 1) * 64;
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const uint64_t ad = smem_desc(q + (x >> 2) * 16384 + (x & 3) * 32, 16, 1024, 2);
-            const uint64_t bd = smem_desc(k + (kFp8 ? 0 : (x >> 2) * 16384) + (x & 3) * 32, 16, 1024, 2);
-            mma_s<kFp8>(tmem + t * 128, ad, bd, x > 0);
-          }
-          mma_commit(bar(C::kBarS + t));
-        };
-        auto wait_ready = [&](uint32_t j) { wait(C::kBarReady + j % C::kReady, j / C::kReady); };
-        auto issue_o = [&](int t, uint32_t j, bool acc) {
-          wait(C::kBarP + t, np[t]);
-          ++np[t];
-          tc_fence_after();
-          const uint32_t v = kFp8 ? sbase + C::kOffV16 + (j & 1) * C::kV16
-                                  : sbase + C::kOffV + (j % C::kVStages) * C::kVStage;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            // 16 tokens: e4m3 as two columns of core matrices (8 dims x 8 tokens, 128 B apart along the
-            // dims, 2 KiB along the tokens), bf16 as rows of 32 bytes with the 32-byte swizzle
-            const uint64_t bd = kFp8 ? smem_desc(v + x * 4096, 2048, 128, 0) : smem_desc(v + x * 4096, 16, 256, 6);
-            mma_o<kFp8>(tmem + 256 + t * 128, tmem + t * 128 + x * 8, bd, acc || x > 0);
-          }
-          mma_commit(bar(C::kBarO + t));
-        };
-        auto free_v = [&](uint32_t j) {
-          mma_commit(bar(kFp8 ? C::kBarUsed + (j & 1) : C::kBarVFree + j % C::kVStages));
-        };
-        while (next_piece(a, cur, p)) {
-          const int nb = p.i1 - p.i0;
-          const bool pair = p.rows > 128;
-          const int lag = pair ? 1 : 2;  // blocks between S and its PV
-          wait(C::kBarQ, piece);
-          tc_fence_after();
-          for (int i = 0; i < nb + lag; ++i) {
-            if (pair) {
-              for (int t = 0; t < 2; ++t) {
-                if (i >= 1) {
-                  if (t == 0) wait_ready(jb + i - 1);
-                  issue_o(t, jb + i - 1, i > 1);
-                  if (t == 1) free_v(jb + i - 1);
-                }
-                if (i < nb) {
-                  if (t == 0) wait(C::kBarKFull + (jb + i) % C::kKStages, (jb + i) / C::kKStages);
-                  tc_fence_after();
-                  issue_s(t, t, jb + i);
-                  if (t == 1) mma_commit(bar(C::kBarKFree + (jb + i) % C::kKStages));
-                }
-              }
-            } else {
-              const int t = i & 1;
-              if (i >= 2) {
-                wait_ready(jb + i - 2);
-                issue_o(t, jb + i - 2, i > 3);
-                free_v(jb + i - 2);
-              }
-              if (i < nb) {
-                wait(C::kBarKFull + (jb + i) % C::kKStages, (jb + i) / C::kKStages);
-                tc_fence_after();
-                issue_s(t, 0, jb + i);
-                mma_commit(bar(C::kBarKFree + (jb + i) % C::kKStages));
-              }
+              for (int x = 0; x < kPfBlkTiles; ++x)
+                mma_o<kFp8>(tmem + 256 + ot * 128, pt + x * 8, vd + x * (4096 >> 4), !begins || x > 0);
+              mma_commit(bar(C::kBarO + 2 * ot + (n & 1)));
+              if (q0 & 4) mma_commit(bar((kFp8 ? C::kBarUsed : C::kBarVFree) + vj % C::kReady));
             }
-            if (i == nb - 1) mma_commit(bar(C::kBarQFree));
+            __syncwarp();
+            if (ot) {
+              ++np[1];
+              begun[1] += begins;
+            } else {
+              ++np[0];
+              begun[0] += begins;
+            }
+            q0 = q1;
+            q1 = q2;
+            q2 = q3;
+            --owed;
+            idle = 0;
           }
-          jb += nb;
-          ++piece;
         }
-        // every product and every arrival it owes is done before the CTA ends
-        mma_commit(bar(C::kBarDone));
-        mbar_wait(bar(C::kBarDone), 0, a.status);
-      }
-      __syncwarp();
-    } else if (warp == kPfCheckWarp) {
-      // ===================== tables of a group agree =====================
-      // The units of kv head 0 cover every shared page once per 256 rows: each request of
-      // the unit must name the leader's pages, and they must be in the pool.
-      while (next_piece(a, cur, p)) {
-        if (!p.prefix || p.h != 0) continue;
-        const int p0 = p.i0 * kPfBlkTiles / tpp;
-        const int p1 = (min(p.i1 * kPfBlkTiles, p.tokens / kPfTile) + tpp - 1) / tpp;
-        const int32_t* lead = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
-        const int r0 = p.gfirst + p.row0 / a.G, r1 = p.gfirst + (p.row0 + p.rows - 1) / a.G;
-        for (int i = p0 + lane; i < p1; i += 32) {
-          const int want = __ldg(lead + i);
-          const bool in = want >= 0 && want < a.num_pages;
-#pragma unroll 4
-          for (int r = r0; r <= r1; ++r)
-            if (!in || __ldg(a.page_table + static_cast<int64_t>(r) * a.max_pages + i) != want) a.dead[r] = 1;
+        if (have) {
+          if (!q_ok)
+            q_ok = __all_sync(kFull, (!(pair || p.qbuf == 0) || test(C::kBarQ, uses[0])) &&
+                                         (!(pair || p.qbuf == 1) || test(C::kBarQ + 1, uses[1])));
+          const uint32_t ks = j % C::kKStages, n = t ? ns[1] : ns[0];
+          if (!k_ok) k_ok = __all_sync(kFull, test(C::kBarKFull + ks, j / C::kKStages));
+          if (q_ok && k_ok && n - (t ? np[1] : np[0]) < 2) {
+            const bool last_of_block = !pair || t == 1, last = last_of_block && i == nb - 1;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t qd = qdesc + (pair ? t : static_cast<uint32_t>(p.qbuf)) * (C::kQTile >> 4);
+              const uint64_t kd = kdesc + ks * (C::kKStage >> 4);
+              // e4m3: two query parts against the same K rows; bf16: two halves of the dims
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                mma_s<kFp8>(tmem + t * 128 + (n & 1) * 64, qd + (x >> 2) * (16384 >> 4) + (x & 3) * 2,
+                            kd + (kFp8 ? 0 : (x >> 2) * (kPfBlk * 128 >> 4)) + (x & 3) * 2, x > 0);
+              mma_commit(bar(C::kBarS + 2 * t + (n & 1)));
+              if (last_of_block) mma_commit(bar(C::kBarKFree + ks));
+              if (last && (pair || p.qbuf == 0)) mma_commit(bar(C::kBarQFree));
+              if (last && (pair || p.qbuf == 1)) mma_commit(bar(C::kBarQFree + 1));
+            }
+            __syncwarp();
+            const uint32_t e = j << 3 | (last_of_block ? 4u : 0u) | (i < (pair ? 1 : 2) ? 2u : 0u) | t;
+            if (owed == 0) q0 = e;
+            else if (owed == 1) q1 = e;
+            else if (owed == 2) q2 = e;
+            else q3 = e;
+            ++owed;
+            if (t) ++ns[1]; else ++ns[0];
+            if (last_of_block) {
+              ++j;
+              ++i;
+              k_ok = false;
+            }
+            t ^= 1;
+            if (last) {
+              have = false;
+              if (pair || p.qbuf == 0) ++uses[0];
+              if (pair || p.qbuf == 1) ++uses[1];
+            }
+            idle = 0;
+          }
+        }
+        if (!have && more && __all_sync(kFull, test(C::kBarPiece + pn % kPfPieces, pn / kPfPieces))) {
+          more = have = take_piece(p);
+          q_ok = k_ok = false;
+          pair = p.pair();
+          nb = p.i1 - p.i0;
+          i = 0;
+          t = 0;
+          idle = 0;
+        }
+        // as every wait: bounded, and over once any other has given up
+        if ((idle & 255u) == 255u) {
+          if (*s_failed) break;
+          if (idle == 255u) since = global_timer_ns();
+          else if (global_timer_ns() - since > kWaitLimitNs) {
+            *s_failed = 1;
+            if (lane == 0) atomicOr(a.status, kStatusWaitTimeout);
+            break;
+          }
         }
       }
-    } else if (warp < 8) {
+      // every product and every arrival it owes is done before the CTA ends
+      if (elect_one()) mma_commit(bar(C::kBarDone));
+      mbar_wait(bar(C::kBarDone), 0, a.status);
+    } else {
       // ===================== softmax, a thread per row =====================
       const int t = warp >> 2;                       // row tile
       const int row = threadIdx.x & 127;
       const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
       const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * 128 + lanes;
-      const float kscale = kFp8 ? __ldg(a.k_scale) : 1.f, vscale = kFp8 ? __ldg(a.v_scale) : 1.f;
-      const bool negate = a.sm_scale_log2 < 0.f;     // the sign goes to the query: maxima of raw scores are then those of scaled ones
-      const float base_mult = fabsf(a.sm_scale_log2) * kscale;
-      uint32_t ns = 0, piece = 0;                    // S blocks taken of this tile
-      while (next_piece(a, cur, p)) {
-        const bool pair = p.rows > 128;
+      uint32_t ns = 0;                               // S blocks taken of this tile
+      uint32_t uses[2] = {0, 0};                     // query buffers taken
+      while (take_piece(p)) {
+        const bool pair = p.pair();
+        const int nb = p.i1 - p.i0;
         const int lrow = pair ? t * 128 + row : row;  // row of the unit
         const bool valid = lrow < p.rows;
-        const int grow = p.row0 + lrow;
-        const int64_t qrow = valid ? static_cast<int64_t>(p.gfirst + grow / a.G) * a.Hq + p.h * a.G + grow % a.G : 0;
-        const bool busy = __any_sync(kFull, valid);
-        // ---- the row's query into shared memory
-        if (piece > 0) wait(C::kBarQFree, piece - 1);
-        float mult = base_mult;
-        if (valid) {
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + qrow * kPfDim);
-          uint4 x[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = __ldg(src + k);
-          if (negate) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              x[k].x ^= 0x80008000u;
-              x[k].y ^= 0x80008000u;
-              x[k].z ^= 0x80008000u;
-              x[k].w ^= 0x80008000u;
-            }
-          }
-          uint8_t* const dst = sm + (pair ? t : 0) * C::kQTile + row * 128;
-          if (kFp8) {
-            uint32_t top = 0;  // largest |q|: bf16 magnitudes order as integers
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-            }
-            const float amax = bf16_bits_to_float(static_cast<uint16_t>(top));
-            int e = 0;
-            if (amax > 0.f && isfinite(amax)) e = min(max(7 - ilogbf(amax), -126), 126);
-            const float up = __int_as_float((127 + e) << 23);
-            mult = isfinite(amax) ? base_mult * __int_as_float((127 - e) << 23) : __int_as_float(0x7fffffff);
-            if (pair || t == 0) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint32_t w[8] = {x[2 * k].x, x[2 * k].y, x[2 * k].z, x[2 * k].w,
-                                       x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
-                uint32_t c0[4], c1[4];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float lo = __uint_as_float(w[i] << 16) * up, hi = __uint_as_float(w[i] & 0xFFFF0000u) * up;
-                  const uint32_t h = f32x2_to_e4m3x2(lo, hi);
-                  const float2 f = e4m3x2_to_float2(h);
-                  const uint32_t g = f32x2_to_e4m3x2(lo - f.x, hi - f.y);
-                  if (i & 1) {
-                    c0[i >> 1] |= h << 16;
-                    c1[i >> 1] |= g << 16;
-                  } else {
-                    c0[i >> 1] = h;
-                    c1[i >> 1] = g;
-                  }
-                }
-                const int at = (k ^ (row & 7)) << 4;
-                *reinterpret_cast<uint4*>(dst + at) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
-                *reinterpret_cast<uint4*>(dst + 16384 + at) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
-              }
-            }
-          } else if (pair || t == 0) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              *reinterpret_cast<uint4*>(dst + (k >> 3) * 16384 + (((k & 7) ^ (row & 7)) << 4)) = x[k];
-          }
+        const bool busy = lrow - lane < p.rows;       // some row of the warp's is
+        const int buf = pair ? t : p.qbuf;
+        // ---- the queries of a prefix unit into shared memory (own units': the planning warp)
+        if (p.prefix && (pair || t == 0)) {
+          const uint32_t u = buf ? uses[1] : uses[0];
+          if (u > 0) wait(C::kBarQFree + buf, u - 1);
+          if (busy) stage_rows(p, buf, lrow - lane, row - lane, min(32, p.rows - (lrow - lane)));
+          if (lane == 0) mbar_arrive(bar(C::kBarQ + buf));
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
+        wait(C::kBarQ + buf, buf ? uses[1] : uses[0]);
+        const float mult = s_mult[buf * 128 + row];   // (whatever lies there for a row that is none)
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::kBarQ));
+        if (pair || p.qbuf == 0) {
+          ++uses[0];
+          if (lane == 0) mbar_arrive(bar(C::kBarQFree));
+        }
+        if (pair || p.qbuf == 1) {
+          ++uses[1];
+          if (lane == 0) mbar_arrive(bar(C::kBarQFree + 1));
+        }
         // ---- blocks
         float m = -INFINITY, l = 0.f;
         bool any = false;
-        const int nb = p.i1 - p.i0;
+#pragma unroll 1
         for (int i = pair ? 0 : t; i < nb; i += pair ? 1 : 2) {
-          wait(C::kBarS + t, ns);
-          ++ns;
+          wait(C::kBarS + 2 * t + (ns & 1), ns >> 1);
           tc_fence_after();
           if (busy) {
             const int nv = min(kPfBlk, p.tokens - (p.i0 + i) * kPfBlk);
-            float s[32];
-            float mx = -INFINITY;
+            const uint32_t tb = ts + (ns & 1) * 64;
+            float s[64];
+            tmem_ld64(tb, s);
+            if (nv < kPfBlk) {  // columns behind the last token
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32(ts + 32 * c, s);
-              if (nv < kPfBlk) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (32 * c + k >= nv) s[k] = -INFINITY;
-              }
-#pragma unroll
-              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, s[k]);
+              for (int k = 0; k < 64; ++k)
+                if (k >= nv) s[k] = -INFINITY;
             }
+            float m4[4] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
+#pragma unroll
+            for (int k = 8; k < 64; k += 8)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) m4[x] = max3(m4[x], s[k + 2 * x], s[k + 2 * x + 1]);
+            const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
             const float mb = mx == -INFINITY ? -INFINITY : mx * mult;
-            const bool grow_row = mb > m + kPfGrow || (m == -INFINITY && mb != -INFINITY);
-            if (__any_sync(kFull, grow_row)) {
-              const float f = !grow_row ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - mb);
-              if (grow_row) m = mb;
+            const bool grown = mb > m + kPfGrow || (m == -INFINITY && mb != -INFINITY);
+            if (__any_sync(kFull, grown)) {
+              const float f = !grown ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - mb);
+              if (grown) m = mb;
               l *= f;
               if (any) {  // O of the blocks before, once their products are done
-                wait(C::kBarO + t, ns - 2);
+                wait(C::kBarO + 2 * t + ((ns - 1) & 1), (ns - 1) >> 1);
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                   float o[32];
                   tmem_ld32(to + 32 * c, o);
-                  uint32_t z[16];
+                  uint32_t z[32];
 #pragma unroll
-                  for (int k = 0; k < 16; ++k) z[k] = __float_as_uint(o[k] * f);
-                  tmem_st16(to + 32 * c, z);
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) z[k] = __float_as_uint(o[16 + k] * f);
-                  tmem_st16(to + 32 * c + 16, z);
+                  for (int k = 0; k < 32; ++k) z[k] = __float_as_uint(o[k] * f);
+                  tmem_st32(to + 32 * c, z);
                 }
               }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 mult2 = make_float2(mult, mult), ref2 = make_float2(-ref, -ref);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            uint32_t w[32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32(ts + 32 * c, s);
-              if (nv < kPfBlk) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (32 * c + k >= nv) s[k] = -INFINITY;
-              }
-              uint32_t w[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                float p0 = fast_exp2(fmaf(s[2 * k], mult, -ref)), p1 = fast_exp2(fmaf(s[2 * k + 1], mult, -ref));
-                if (nv < kPfBlk) {
-                  if (32 * c + 2 * k >= nv) p0 = 0.f;  // mult may be 0
-                  if (32 * c + 2 * k + 1 >= nv) p1 = 0.f;
-                }
-                sum[k & 3] += p0 + p1;
-                w[k] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-              }
-              tmem_st16(ts + 16 * c, w);
+            for (int k = 0; k < 32; ++k) {
+              float2 e = fma2(make_float2(s[2 * k], s[2 * k + 1]), mult2, ref2);
+              e.x = fast_exp2(e.x);
+              e.y = fast_exp2(e.y);
+              sum[k & 1] = add2(sum[k & 1], e);
+              w[k] = kFp8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_st32(tb, w);
             tmem_wait_st();
           }
           any = true;
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::kBarP + t));
+          if (lane == 0) mbar_arrive(bar(C::kBarP + 2 * t + (ns & 1)));
+          ++ns;
         }
         // ---- the row's partial: pieces at a unit's start by row, others by CTA
-        int64_t slot = 0;
-        if (p.i0 == 0)
-          slot = static_cast<int64_t>((p.prefix ? 0 : 2) + (pair ? 0 : t)) * a.B * a.Hq + qrow;
-        else
-          slot = static_cast<int64_t>(4) * a.B * a.Hq + static_cast<int64_t>(blockIdx.x) * kPfUnitRows + t * 128 + row;
+        const int grow = p.row0 + lrow;
+        int64_t slot = static_cast<int64_t>(4) * a.B * a.Hq + static_cast<int64_t>(blockIdx.x) * kPfUnitRows + t * 128 + row;
+        if (p.i0 == 0 && valid)
+          slot = static_cast<int64_t>((p.prefix ? 0 : 2) + (pair ? 0 : t)) * a.B * a.Hq +
+                 static_cast<int64_t>(p.gfirst + grow / a.G) * a.Hq + p.h * a.G + grow % a.G;
         if (any) {
-          wait(C::kBarO + t, ns - 1);
+          // (the last two products: the MMAs of the last block's S came behind the others')
+          if (ns > 1) wait(C::kBarO + 2 * t + (ns & 1), (ns - 2) >> 1);
+          wait(C::kBarO + 2 * t + ((ns - 1) & 1), (ns - 1) >> 1);
           tc_fence_after();
           if (busy) {
+            const float vscale = kFp8 ? __ldg(a.v_scale) : 1.f;
             float* const dst = a.part_o + slot * kPfDim;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -924,9 +1104,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               }
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kBarOFree + t));
         }
         if (valid) a.part_ml[slot] = make_float2(m, l);
-        ++piece;
       }
     }
   }
@@ -953,15 +1135,16 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
   const int r = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
   const int h = hq / a.G, g = hq % a.G;
   uint2* const out = reinterpret_cast<uint2*>(a.out + row * kPfDim) + lane;
-  const int64_t T = __ldcg(a.total), n = a.ctas, rows = static_cast<int64_t>(a.B) * a.Hq;
+  const PfRanges rg = ranges_of(__ldcg(a.total), a.ctas);
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
   float M = -INFINITY, W = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   bool dead = __ldcg(a.dead + r) != 0;
   if (!dead) {
-    const PfReq q = load_req(a, r);
-    int64_t own_y = q.y0;
-    auto merge_unit = [&](int64_t y, int blocks, int w, int kind, int subs, int lrow) {
-      const int c0 = owner_of(y, T, n), c1 = owner_of(y + static_cast<int64_t>(blocks - 1) * w, T, n);
+    const PfReq q = load_req(a.req + r);
+    int own_y = q.y0;
+    auto merge_unit = [&](int y, int blocks, int w, int kind, int subs, int lrow) {
+      const int c0 = rg.owner(y), c1 = rg.owner(y + (blocks - 1) * w);
       const int cands = (c1 - c0 + 1) * subs;
       for (int base = 0; base < cands; base += 32) {
         const int k = base + lane;
@@ -970,7 +1153,7 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
         if (k < cands) {
           const int c = c0 + k / subs, sub = k % subs;
           int i0, i1;
-          owned_blocks(y, blocks, w, range_begin(c, T, n), range_begin(c + 1, T, n), i0, i1);
+          owned_blocks(y, blocks, w, rg.begin(c), rg.begin(c + 1), i0, i1);
           slot = i0 == 0 ? static_cast<int64_t>(kind + sub) * rows + row
                          : 4 * rows + static_cast<int64_t>(c) * kPfUnitRows + sub * 128 + lrow;
           if (i0 < i1) ml = __ldcg(a.part_ml + slot);
@@ -1017,15 +1200,15 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
     };
     if (q.ptiles > 0) {
       const PfPrefix s = prefix_shape(q.ptiles, q.gcount, a.G);
-      const int64_t gy = q.gfirst == r ? q.y0 : load_req(a, q.gfirst).y0;
+      const int gy = q.gfirst == r ? q.y0 : load_req(a.req + q.gfirst).y0;
       const int i = (r - q.gfirst) * a.G + g, u = i / kPfUnitRows;
       const int w = u == s.units - 1 ? s.wlast : kPfCostPair;
-      merge_unit(gy + h * s.head_cost + static_cast<int64_t>(u) * kPfCostPair * s.blocks, s.blocks, w, 0,
+      merge_unit(gy + h * s.head_cost + u * kPfCostPair * s.blocks, s.blocks, w, 0,
                  w == kPfCostPair ? 1 : 2, i % kPfUnitRows);
       if (q.gfirst == r) own_y += s.head_cost * a.Hkv;
     }
     const int nb = own_blocks(q.stok);
-    if (nb > 0) merge_unit(own_y + static_cast<int64_t>(h) * nb * kPfCostSolo, nb, kPfCostSolo, 2, 2, g);
+    if (nb > 0) merge_unit(own_y + h * nb * kPfCostSolo, nb, kPfCostSolo, 2, 2, g);
   }
   dead = dead || W == 0.f;
   const float inv = dead ? 0.f : 1.f / W;
@@ -1052,15 +1235,15 @@ int prepare_prefix(int dev) {
 }
 
 struct PfLayout {
-  size_t gstart, first, dead, req, ml, o, total;
+  size_t gstart, start, dead, req, ml, o, total;
 };
 PfLayout prefix_layout(int64_t B, int64_t Hq, int64_t ctas) {
   auto up = [](int64_t x) { return (static_cast<size_t>(x) + 255) & ~static_cast<size_t>(255); };
   const int64_t slots = 4 * B * Hq + ctas * kPfUnitRows;
   PfLayout l;
   l.gstart = 256;
-  l.first = l.gstart + up((B + 1) * 4);
-  l.dead = l.first + up(ctas * 4);
+  l.start = l.gstart + up((B + 1) * 4);
+  l.dead = l.start + up(ctas * static_cast<int64_t>(sizeof(PfReq)));
   l.req = l.dead + up(B * 4);
   l.ml = l.req + up(B * static_cast<int64_t>(sizeof(PfReq)));
   l.o = l.ml + up(slots * 8);
@@ -1116,8 +1299,12 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   if (D != kPfDim || G > kPfGroupMax || page_size % kPfTile != 0 || page_size > 256) return FPK_EUNSUPPORTED;
   const int tpp = page_size / kPfTile;
   const int64_t tiles = static_cast<int64_t>(num_pages) * Hkv * tpp;
-  // tile numbers are 32-bit tensor-map coordinates; rows are counted in 31 bits
-  if (tiles > 0x7fffffff || static_cast<int64_t>(B) * Hq > 0x7fffffff / 4) return FPK_EUNSUPPORTED;
+  // tile numbers are 32-bit tensor-map coordinates; rows and the work list's length (at most a prefix
+  // unit and an own unit of the table's width per request and kv head) are counted in 31 bits
+  const int64_t width = (static_cast<int64_t>(max_pages) * page_size + kPfBlk - 1) / kPfBlk;
+  if (tiles > 0x7fffffff || static_cast<int64_t>(B) * Hq > 0x7fffffff / 4 ||
+      width > (int64_t(1) << 24) || width * B > (int64_t(1) << 31) / ((kPfCostPair + kPfCostSolo) * Hkv))
+    return FPK_EUNSUPPORTED;
   if (B == 0) return FPK_OK;
   if (!q || !kv_pool || !page_table || !seq_lens || !out || !workspace) return FPK_EINVAL;
   if (kFp8 && (!k_scale || !v_scale)) return FPK_EINVAL;
@@ -1152,9 +1339,9 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = reinterpret_cast<uint32_t*>(ws);
-  a.total = reinterpret_cast<int64_t*>(ws + 8);
+  a.total = reinterpret_cast<int32_t*>(ws + 8);
   a.gstart = reinterpret_cast<int32_t*>(ws + l.gstart);
-  a.first = reinterpret_cast<int32_t*>(ws + l.first);
+  a.start = reinterpret_cast<PfReq*>(ws + l.start);
   a.dead = reinterpret_cast<int32_t*>(ws + l.dead);
   a.req = reinterpret_cast<PfReq*>(ws + l.req);
   a.part_ml = reinterpret_cast<float2*>(ws + l.ml);

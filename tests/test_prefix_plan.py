@@ -6,7 +6,7 @@ import random
 
 import pytest
 
-PAIR, SOLO, ROWS, BLK = 3, 2, 256, 8
+PAIR, SOLO, ROWS, BLK = 2, 1, 256, 4
 
 
 def prefix_shape(ptiles, gcount, G):
@@ -17,13 +17,22 @@ def prefix_shape(ptiles, gcount, G):
 
 
 def own_blocks(stok):
-    return -(-stok // 128)
+    return -(-stok // 64)
 
 
 def owned(y, n, w, b0, b1):
     lo = 0 if b0 <= y else (b0 - y + w - 1) // w
     hi = 0 if b1 <= y else (b1 - y + w - 1) // w
     return min(lo, n), min(hi, n)
+
+
+def begin(c, T, n):
+    return c * (T // n) + min(c, T % n)
+
+
+def owner(y, T, n):
+    share, more = divmod(T, n)
+    return y // (share + 1) if y < more * (share + 1) else more + (y - more * (share + 1)) // share
 
 
 def plan(groups, G, Hkv, ctas):
@@ -37,19 +46,14 @@ def plan(groups, G, Hkv, ctas):
                 cost += prefix_shape(ptiles, len(own), G)[3]
             reqs.append((y, ptiles, stok, first, len(own)))
             y += cost * Hkv
-    T, start = y, {}
-    ends = [q[0] for q in reqs[1:]] + [T]
-    for r, (y0, *_) in enumerate(reqs):
-        if ends[r] > y0:
-            k = -(-y0 * ctas // T)
-            while k < ctas and k * T // ctas < ends[r]:
-                start[k] = r
-                k += 1
+    T = y
+    # the last request whose units start at or before the range
+    start = [max(r for r, q in enumerate(reqs) if q[0] <= begin(c, T, ctas)) for c in range(ctas)]
     return reqs, T, start
 
 
 def pieces(reqs, T, start, G, Hkv, ctas, c):
-    b0, b1 = c * T // ctas, (c + 1) * T // ctas
+    b0, b1 = begin(c, T, ctas), begin(c + 1, T, ctas)
     if b0 >= b1:
         return
     r = start[c]
@@ -113,9 +117,8 @@ def merge(reqs, T, G, Hkv, ctas, r, h, g):
     own = y0
 
     def unit(y, n, w, name, subs):
-        owner = lambda x: ((x + 1) * ctas - 1) // T  # noqa: E731
-        for c in range(owner(y), owner(y + (n - 1) * w) + 1):
-            i0, i1 = owned(y, n, w, c * T // ctas, (c + 1) * T // ctas)
+        for c in range(owner(y, T, ctas), owner(y + (n - 1) * w, T, ctas) + 1):
+            i0, i1 = owned(y, n, w, begin(c, T, ctas), begin(c + 1, T, ctas))
             for sub in range(subs):
                 if i0 < i1:
                     yield name, ("start" if i0 == 0 else c), sub
