@@ -44,7 +44,7 @@ namespace {
 constexpr int kPfTile = 16;
 constexpr int kPfDim = 128;
 constexpr int kPfGroupMax = 8;
-constexpr int kPfBlk = 64;                     // tokens of a block
+constexpr int kPfBlk = 128;                    // tokens of a block
 constexpr int kPfBlkTiles = kPfBlk / kPfTile;
 constexpr int kPfUnitRows = 256;               // query rows of a prefix unit: two MMA tiles
 constexpr float kPfLog2e = 1.4426950408889634f;
@@ -58,7 +58,7 @@ constexpr int kPfCostPair = 2;
 constexpr int kPfCostSolo = 1;
 
 constexpr int kPfThreads = 512;
-constexpr int kPfVWarp = 8, kPfKLoadWarp = 12, kPfMmaWarp = 13, kPfVLoadWarp = 14, kPfPlanWarp = 15;
+constexpr int kPfVWarp = 8, kPfLoadWarp = 12, kPfMmaWarp = 13, kPfPlanWarp = 15;  // two MMA warps
 constexpr int kPfPieces = 4;                   // pieces known ahead
 constexpr int kPfPlanThreads = 1024;
 constexpr int kPfMergeWarps = 4;
@@ -102,17 +102,17 @@ struct PfCfg {
   static constexpr int kQTile = 128 * 256;                     // parts (or halves) of a tile's queries
   static constexpr int kKStage = kPfBlk * kPfDim * kElem;
   static constexpr int kVStage = kKStage;
-  static constexpr int kKStages = kFp8 ? 6 : 4;
-  static constexpr int kVStages = 6;
+  static constexpr int kKStages = kFp8 ? 3 : 2;
+  static constexpr int kVStages = 3;
   static constexpr int kV16 = kPfBlk * kPfDim * 2;             // converted V block
-  static constexpr int kV16Bufs = kFp8 ? 4 : 0;
+  static constexpr int kV16Bufs = kFp8 ? 2 : 0;
   static constexpr int kOffK = 2 * kQTile;
   static constexpr int kOffV = kOffK + kKStages * kKStage;
   static constexpr int kOffV16 = kOffV + kVStages * kVStage;
   static constexpr int kOffMult = kOffV16 + kV16Bufs * kV16;   // score multiplier of each query row
   static constexpr int kOffPiece = kOffMult + 2 * 128 * 4;
   static constexpr int kOffBars = kOffPiece + kPfPieces * 48;
-  // barriers; a tile's S and P have one per buffer
+  // barriers
   static constexpr int kReady = kFp8 ? kV16Bufs : kVStages;    // V blocks ready for the MMA
   static constexpr int kBarKFull = 0;
   static constexpr int kBarKFree = kBarKFull + kKStages;
@@ -120,16 +120,17 @@ struct PfCfg {
   static constexpr int kBarVFree = kBarVFull + kVStages;
   static constexpr int kBarReady = kBarVFree + kVStages;
   static constexpr int kBarUsed = kBarReady + kReady;          // e4m3: converted block read by the MMA
-  static constexpr int kBarS = kBarUsed + kV16Bufs;            // [tile][buffer]
-  static constexpr int kBarP = kBarS + 4;                      // [tile][buffer]
-  static constexpr int kBarO = kBarP + 4;                      // [tile][buffer] a product added to O
-  static constexpr int kBarOFree = kBarO + 4;                  // [tile] O of a piece read
+  static constexpr int kBarS = kBarUsed + kV16Bufs;            // [tile]
+  static constexpr int kBarP = kBarS + 2;                      // [tile][half of the block]
+  static constexpr int kBarO = kBarP + 4;                      // [tile] a product added to O
+  static constexpr int kBarOFree = kBarO + 2;                  // [tile] O of a piece read
   static constexpr int kBarQ = kBarOFree + 2;                  // [buffer] queries staged
   static constexpr int kBarQFree = kBarQ + 2;                  // [buffer] queries and multipliers of a piece read
   static constexpr int kBarPiece = kBarQFree + 2;              // [kPfPieces] piece known
   static constexpr int kBarPieceFree = kBarPiece + kPfPieces;  // [kPfPieces] piece read by every warp
-  static constexpr int kBarDone = kBarPieceFree + kPfPieces;   // every MMA of the CTA completed
-  static constexpr int kBars = kBarDone + 1;
+  static constexpr int kBarDone = kBarPieceFree + kPfPieces;   // [2] every MMA of a warp completed
+  static constexpr int kBarTurn = kBarDone + 2;                // [tile] the other tile's products of a turn are out
+  static constexpr int kBars = kBarTurn + 2;
   static constexpr int kOffMisc = kOffBars + 8 * kBars;        // tensor memory base, failure flag
   static constexpr int kSmem = kOffMisc + 16 + 1024;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -435,8 +436,7 @@ __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
   return pol;
 }
 
-// Instruction descriptors: M = 128, both operands K-major, D in fp32; S has N = 64 (tokens), O
-// N = 128 (dims).
+// Instruction descriptors: M = N = 128, both operands K-major, D in fp32.
 constexpr uint32_t pf_idesc(int n, uint32_t type) {
   return (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(128 >> 4) << 24);
@@ -444,30 +444,43 @@ constexpr uint32_t pf_idesc(int n, uint32_t type) {
 constexpr uint32_t kPfSE4m3 = pf_idesc(kPfBlk, 0), kPfSBf16 = pf_idesc(kPfBlk, 1);  // kind::f8f6f4, kind::f16
 constexpr uint32_t kPfOF16 = pf_idesc(kPfDim, 0), kPfOBf16 = pf_idesc(kPfDim, 1);   // kind::f16
 
-// S = Q K^T: both operands from shared memory.
-template <bool kFp8>
-__device__ __forceinline__ void mma_s(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t acc) {
-  if (kFp8)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(kPfSE4m3), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(kPfSBf16), "r"(acc)
-        : "memory");
+// One elected lane of the (converged) warp issues; everything is predicated, not branched, so that the
+// operands stay in uniform registers.
+#define PF_COMMIT "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
+// Arrives on `bar` once every product that this warp's elected lane has issued is done.
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e " PF_COMMIT "[%0];\n\t}" ::"r"(bar) : "memory");
 }
 
-// O += P V: P from tensor memory.
+// S = Q K^T, both operands from shared memory: eight steps of 32 bytes of K, four per atom of 128
+// bytes (e4m3: two query parts against the same K rows; bf16: two halves of the dims, K's %4 apart).
+#define PF_S_STEP(kind, x, first)                                                             \
+  "add.s64 a, %1, " #x ";\n\tadd.s64 b, k, " #x ";\n\t@e tcgen05.mma.cta_group::1.kind::" kind \
+  " [%0], a, b, %3, " first ";\n\t"
+#define PF_S(kind)                                                                                             \
+  "{\n\t.reg .pred e, no, yes;\n\t.reg .b64 a, b, k;\n\telect.sync _|e, 0xffffffff;\n\t"                       \
+  "setp.ne.u32 no, 0, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\tmov.b64 k, %2;\n\t" PF_S_STEP(kind, 0, "no")             \
+      PF_S_STEP(kind, 2, "yes") PF_S_STEP(kind, 4, "yes") PF_S_STEP(kind, 6, "yes")                            \
+  "add.s64 k, %2, %4;\n\tsub.s64 k, k, 1024;\n\t" PF_S_STEP(kind, 1024, "yes") PF_S_STEP(kind, 1026, "yes")    \
+      PF_S_STEP(kind, 1028, "yes") PF_S_STEP(kind, 1030, "yes") "}"
 template <bool kFp8>
-__device__ __forceinline__ void mma_o(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t acc) {
+__device__ __forceinline__ void issue_s(uint32_t d, uint64_t qdesc, uint64_t kdesc) {
+  if (kFp8)
+    asm volatile(PF_S("f8f6f4")::"r"(d), "l"(qdesc), "l"(kdesc), "r"(kPfSE4m3), "n"(0) : "memory");
+  else
+    asm volatile(PF_S("f16")::"r"(d), "l"(qdesc), "l"(kdesc), "r"(kPfSBf16), "n"(kPfBlk * 128 >> 4) : "memory");
+}
+
+// O += P V over half a block, P from tensor memory: a step is 16 tokens, 8 columns of P and 4 KiB of V.
+#define PF_O_STEP(pcol, voff, acc)                                                                  \
+  "add.u32 p, %1, " #pcol ";\n\tadd.s64 b, %2, " #voff ";\n\t@e tcgen05.mma.cta_group::1.kind::f16" \
+  " [%0], [p], b, %3, " acc ";\n\t"
+__device__ __forceinline__ void issue_o(uint32_t d, uint32_t p, uint64_t vdesc, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(kFp8 ? kPfOF16 : kPfOBf16), "r"(acc)
+      "{\n\t.reg .pred e, first, yes;\n\t.reg .b32 p;\n\t.reg .b64 b;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.u32 first, %4, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t" PF_O_STEP(0, 0, "first") PF_O_STEP(8, 256, "yes")
+          PF_O_STEP(16, 512, "yes") PF_O_STEP(24, 768, "yes") "}" ::"r"(d),
+      "r"(p), "l"(vdesc), "r"(idesc), "r"(acc)
       : "memory");
 }
 
@@ -549,15 +562,15 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// One lane of the (converged) warp: tcgen05 instructions of an elected lane keep
-// their operands in uniform registers, which those of `if (lane == 0)` do not.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-  return ok != 0;
+__device__ __forceinline__ void tmem_fill1(uint32_t taddr, float x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
 }
+__device__ __forceinline__ void tmem_fill8(uint32_t taddr, float x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(taddr),
+               "r"(__float_as_uint(x))
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A wait that gives up once any wait of the CTA has: control flow then runs on
 // to the end without waiting (every address stays in range; the results are
@@ -599,12 +612,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   if (threadIdx.x < C::kBars) {
     const int i = threadIdx.x;
     int arrivals = 1;
+    if (i < C::kBarVFull && i >= C::kBarKFree) arrivals = 2;                         // MMA warps
+    if (i >= (kFp8 ? C::kBarUsed : C::kBarVFree) && i < (kFp8 ? C::kBarS : C::kBarReady)) arrivals = 2;
     if (i >= C::kBarReady && i < C::kBarReady + C::kReady) arrivals = 4;             // V warps
     if (kFp8 && i >= C::kBarVFree && i < C::kBarVFree + C::kVStages) arrivals = 4;   // V warps
     if (i >= C::kBarP && i < C::kBarP + 4) arrivals = 4;                             // a tile's softmax warps
     if (i >= C::kBarOFree && i < C::kBarQFree) arrivals = 4;                         // (also Q)
-    if (i >= C::kBarQFree && i < C::kBarQFree + 2) arrivals = 9;                     // the MMA, all softmax warps
-    if (i >= C::kBarPieceFree && i < C::kBarPieceFree + kPfPieces) arrivals = 15;    // every other warp
+    if (i >= C::kBarQFree && i < C::kBarQFree + 2) arrivals = 10;                    // MMA and softmax warps
+    if (i >= C::kBarPieceFree && i < C::kBarPieceFree + kPfPieces) arrivals = 16;    // every other warp; K's and V's half of one
     mbar_init(bar(i), arrivals);
     fence_barrier_init();
   }
@@ -626,13 +641,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   auto wait = [&](int i, uint32_t parity) { pf_wait(bar(i), parity & 1u, a.status, s_failed); };
   // the next piece, from the planning warp; false at the end
   uint32_t pn = 0;
-  auto take_piece = [&](PfPiece& p) -> bool {
+  auto take_piece = [&](PfPiece& p, unsigned group = 0xffffffffu, bool leads = false) -> bool {
     wait(C::kBarPiece + pn % kPfPieces, pn / kPfPieces);
     p = s_piece[pn % kPfPieces];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(C::kBarPieceFree + pn % kPfPieces));
+    __syncwarp(group);
+    if (lane == 0 || leads) mbar_arrive(bar(C::kBarPieceFree + pn % kPfPieces));
     ++pn;
-    return p.i0 < p.i1 && !*s_failed;
+    return __all_sync(group, p.i0 < p.i1 && !*s_failed);
   };
   // query rows [row, row + n) of a unit, by one warp, into rows `at`.. of a query buffer: half a warp per row
   // (a lane: 8 dims), the next rows' loads ahead
@@ -747,19 +762,22 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
         }
       }
-    } else if (warp == kPfKLoadWarp || warp == kPfVLoadWarp) {
+    } else if (warp == kPfLoadWarp) {
       // ===================== K rows, V tiles into their rings =====================
-      // Lane c copies box c of a block (zbox tiles, within a page); bf16 K: lanes 4 + c the other 64 dims.
-      const bool kw = warp == kPfKLoadWarp;
+      // The half-warps run apart, one for K and one for V (their rings drain at different times).  Lane
+      // c copies box c of a block (zbox tiles, within a page); bf16 K: lanes 8 + c the other 64 dims.
+      const bool kw = lane < 16;
+      const unsigned group = kw ? 0xffffu : 0xffff0000u;
+      const bool leads = (lane & 15) == 0;
       const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
-      const int c = lane & 3, part = lane >> 2;
+      const int c = lane & 7, part = (lane & 15) >> 3;
       const int boxes = kPfBlkTiles / a.zbox;
       const int stages = kw ? C::kKStages : C::kVStages;
       const int full = kw ? C::kBarKFull : C::kBarVFull, free = kw ? C::kBarKFree : C::kBarVFree;
       const int parts = kw && !kFp8 ? 2 : 1;
       const uint32_t ring = sbase + (kw ? C::kOffK : C::kOffV);
       uint32_t j = 0, st = 0, round = 0;
-      while (take_piece(p)) {
+      while (take_piece(p, group, leads)) {
         const int32_t* row = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
         const int tiles = (p.tokens + kPfTile - 1) / kPfTile;
         auto page_of = [&](int i) -> int {  // page of box c of block i, -2: no such box
@@ -776,14 +794,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const bool good = pg >= 0 && pg < a.num_pages;
           // a page outside the pool: the request is dead (a group's are told apart by the planning warp)
           if (!good && pg != -2 && !p.prefix) a.dead[p.r] = 1;
-          const int n = __popc(__ballot_sync(kFull, good && part == 0));
+          const int n = __popc(__ballot_sync(group, good && part == 0));
           const uint32_t f = bar(full + st);
-          if (lane == 0) {
+          if (leads) {
             const uint32_t bytes = static_cast<uint32_t>(n * a.zbox) * kPfTile * kPfDim * C::kElem;
             if (bytes == 0) mbar_arrive(f);
             else mbar_arrive_expect_tx(f, bytes);
           }
-          __syncwarp();
+          __syncwarp(group);
           if (good && part < parts) {
             const int tile = p.tile0 + i * kPfBlkTiles + c * a.zbox;
             const int z = (pg * a.Hkv + p.h) * tpp + tile % tpp;
@@ -800,7 +818,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
       }
       // every copy has landed before the CTA ends, even if a wait gave up
-      if (lane == 0) {
+      if (leads) {
         for (uint32_t b = j > static_cast<uint32_t>(stages) ? j - stages : 0; b < j; ++b)
           mbar_wait(bar(full + b % stages), (b / stages) & 1, a.status);
       }
@@ -831,9 +849,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               w[0] = make_uint4(y[0], y[1], y[2], y[3]);
               w[128] = make_uint4(y[4], y[5], y[6], y[7]);
             }
-            if (nv < kPfBlk) {  // f16 of token k, dim d: tile k / 16, row of 8 tokens (k / 8) % 2
-              for (int k = nv; k < kPfBlk; ++k)
-                *reinterpret_cast<uint16_t*>(o + (k >> 4) * 4096 + ((k >> 3) & 1) * 2048 + (k & 7) * 2) = 0;
+            if (nv < kPfBlk) {  // f16 of token k, dim d: rows of 8 tokens, 2 KiB apart
+#pragma unroll 1
+              for (int k = nv; k < kPfBlk; k = (k | 7) + 1)
+                for (uint8_t* e = o + (k >> 3) * 2048 + (k & 7) * 2; e < o + (k >> 3) * 2048 + 16; e += 2)
+                  *reinterpret_cast<uint16_t*>(e) = 0;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -845,9 +865,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             if (nv < kPfBlk) {
               // rows of 16 tokens with the 32-byte swizzle: the two 16-byte halves change places
               // in every other group of four rows
-              for (int k = nv; k < kPfBlk; ++k) {
-                const int half = ((k >> 3) & 1) ^ ((d >> 2) & 1);
-                *reinterpret_cast<uint16_t*>(v + (k >> 4) * kPfTile * kPfDim * 2 + d * 32 + half * 16 + (k & 7) * 2) = 0;
+#pragma unroll 1
+              for (int k = nv; k < kPfBlk; k = (k | 7) + 1) {
+                uint8_t* const x = v + (k >> 4) * kPfTile * kPfDim * 2 + d * 32 + (((k >> 3) & 1) ^ ((d >> 2) & 1)) * 16;
+                for (uint8_t* e = x + (k & 7) * 2; e < x + 16; e += 2) *reinterpret_cast<uint16_t*>(e) = 0;
               }
               fence_proxy_async_smem();
             }
@@ -856,130 +877,79 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
         }
       }
-    } else if (warp == kPfMmaWarp) {
-      // ===================== MMA issue =====================
-      // The warp runs as one, an elected lane issues.  One loop polls for whatever can go out next (its
-      // code has to stay small: it is all fetched once per block): the oldest PV that is owed, and the
-      // next S.  S runs ahead of PV by two blocks of a tile (its two S buffers), across pieces; owed PVs
-      // wait in a queue in the order of their S, an entry being block << 3 | last of its block << 2 |
-      // first of its tile in the piece << 1 | tile.
-      const uint64_t qdesc = smem_desc(sbase, 16, 1024, 2);
-      const uint64_t kdesc = smem_desc(sbase + C::kOffK, 16, 1024, 2);
+    } else if (warp == kPfMmaWarp || warp == kPfMmaWarp + 1) {
+      // ===================== MMA issue, a warp per row tile =====================
+      // The warp runs as one, an elected lane issues.  A tile's products alternate: S of a block, PV of the
+      // same block in halves as the softmax hands P over, S of the next (which overwrites S and P: the
+      // products of one thread run in order).  While a tile's softmax runs the other tile has the tensor
+      // cores; on a unit of both tiles the warps take turns (PV and the next S), or else the two would run
+      // in step, their softmaxes too, and leave the tensor cores idle.  Both warps see and free every
+      // block, the other tile's too: a barrier's parity tells neighbouring phases apart, no others.
+      const int t = warp - kPfMmaWarp;
+      const uint32_t base = __reduce_max_sync(kFull, sbase), tm = __reduce_max_sync(kFull, tmem);  // uniform registers
+      const uint32_t bars = base + C::kOffBars;
+      const uint64_t qdesc = smem_desc(base, 16, 1024, 2), kdesc = smem_desc(base + C::kOffK, 16, 1024, 2);
       // V, 16 tokens a step: e4m3 as two columns of core matrices (8 dims x 8 tokens, 128 B apart along
       // the dims, 2 KiB along the tokens), bf16 as rows of 32 bytes with the 32-byte swizzle
-      const uint64_t vdesc = kFp8 ? smem_desc(sbase + C::kOffV16, 2048, 128, 0) : smem_desc(sbase + C::kOffV, 16, 256, 6);
-      uint32_t j = 0;                       // K blocks taken
-      uint32_t ns[2] = {0, 0};              // S issued of each tile
-      uint32_t np[2] = {0, 0};              // PV issued of each tile
-      uint32_t begun[2] = {0, 0};           // pieces begun in each tile's O
-      uint32_t uses[2] = {0, 0};            // query buffers taken
-      uint32_t q0 = 0, q1 = 0, q2 = 0, q3 = 0, owed = 0;
-      bool have = false, more = true, q_ok = false, k_ok = false, pair = false;
-      int i = 0, nb = 0;
-      uint32_t t = 0, idle = 0;             // tile of the next S
-      uint64_t since = 0;
-      auto test = [&](int b, uint32_t phase) { return mbar_test(bar(b), phase & 1); };
-      while (have || more || owed > 0) {
-        ++idle;
-        if (owed > 0) {
-          const uint32_t ot = q0 & 1, vj = q0 >> 3;
-          const bool begins = (q0 & 2) != 0;
-          const uint32_t n = ot ? np[1] : np[0], k = ot ? begun[1] : begun[0];
-          if (__all_sync(kFull, test(C::kBarP + 2 * ot + (n & 1), n >> 1) &&
-                                    test(C::kBarReady + vj % C::kReady, vj / C::kReady) &&
-                                    (!begins || k == 0 || test(C::kBarOFree + ot, k - 1)))) {
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t vd = vdesc + (vj % C::kReady) * ((kFp8 ? C::kV16 : C::kVStage) >> 4);
-              const uint32_t pt = tmem + ot * 128 + (n & 1) * 64;
+      const uint64_t vdesc = kFp8 ? smem_desc(base + C::kOffV16, 2048, 128, 0) : smem_desc(base + C::kOffV, 16, 256, 6);
+      uint32_t ks = 0, kph = 0, vs = 0, vph = 0, n = 0, begun = 0, uses0 = 0, uses1 = 0, turns = 0;
+      while (take_piece(p)) {
+        const bool pair = __any_sync(kFull, p.pair());
+        const uint32_t nb = __reduce_max_sync(kFull, p.i1 - p.i0), qb = __reduce_max_sync(kFull, p.qbuf);
+        if (pair || qb == 0) wait(C::kBarQ, uses0++);
+        if (pair || qb == 1) wait(C::kBarQ + 1, uses1++);
+        const uint64_t qd = qdesc + (pair ? t : qb) * (C::kQTile >> 4);
+        bool begins = true;
+        for (uint32_t i = 0; i <= nb; ++i) {
+          // PV of block i - 1, S of block i
+          if (pair && (t == 1 || i > 0)) wait(C::kBarTurn + t, turns++);
+          if (i > 0) {
+            wait(C::kBarReady + vs, vph);
+            if (pair || ((i - 1) & 1) == static_cast<uint32_t>(t)) {
+              if (begins && begun > 0) wait(C::kBarOFree + t, begun - 1);  // O of the piece before has been read
+              const uint64_t vd = vdesc + vs * ((kFp8 ? C::kV16 : C::kVStage) >> 4);
 #pragma unroll
-              for (int x = 0; x < kPfBlkTiles; ++x)
-                mma_o<kFp8>(tmem + 256 + ot * 128, pt + x * 8, vd + x * (4096 >> 4), !begins || x > 0);
-              mma_commit(bar(C::kBarO + 2 * ot + (n & 1)));
-              if (q0 & 4) mma_commit(bar((kFp8 ? C::kBarUsed : C::kBarVFree) + vj % C::kReady));
+              for (int h = 0; h < 2; ++h) {
+                wait(C::kBarP + 2 * t + h, n);
+                tc_fence_after();
+                issue_o(tm + 256 + t * 128, tm + t * 128 + 32 * h, vd + h * 1024, kFp8 ? kPfOF16 : kPfOBf16,
+                        !begins || h > 0);
+              }
+              ++n;
+              begun += begins;
+              begins = false;
+              commit_elected(bars + 8 * (C::kBarO + t));
+              commit_elected(bars + 8 * ((kFp8 ? C::kBarUsed : C::kBarVFree) + vs));
+            } else if (lane == 0) {
+              mbar_arrive(bar((kFp8 ? C::kBarUsed : C::kBarVFree) + vs));
             }
-            __syncwarp();
-            if (ot) {
-              ++np[1];
-              begun[1] += begins;
-            } else {
-              ++np[0];
-              begun[0] += begins;
-            }
-            q0 = q1;
-            q1 = q2;
-            q2 = q3;
-            --owed;
-            idle = 0;
+            if (++vs == C::kReady) vs = 0, vph ^= 1;
           }
-        }
-        if (have) {
-          if (!q_ok)
-            q_ok = __all_sync(kFull, (!(pair || p.qbuf == 0) || test(C::kBarQ, uses[0])) &&
-                                         (!(pair || p.qbuf == 1) || test(C::kBarQ + 1, uses[1])));
-          const uint32_t ks = j % C::kKStages, n = t ? ns[1] : ns[0];
-          if (!k_ok) k_ok = __all_sync(kFull, test(C::kBarKFull + ks, j / C::kKStages));
-          if (q_ok && k_ok && n - (t ? np[1] : np[0]) < 2) {
-            const bool last_of_block = !pair || t == 1, last = last_of_block && i == nb - 1;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t qd = qdesc + (pair ? t : static_cast<uint32_t>(p.qbuf)) * (C::kQTile >> 4);
-              const uint64_t kd = kdesc + ks * (C::kKStage >> 4);
-              // e4m3: two query parts against the same K rows; bf16: two halves of the dims
-#pragma unroll
-              for (int x = 0; x < 8; ++x)
-                mma_s<kFp8>(tmem + t * 128 + (n & 1) * 64, qd + (x >> 2) * (16384 >> 4) + (x & 3) * 2,
-                            kd + (kFp8 ? 0 : (x >> 2) * (kPfBlk * 128 >> 4)) + (x & 3) * 2, x > 0);
-              mma_commit(bar(C::kBarS + 2 * t + (n & 1)));
-              if (last_of_block) mma_commit(bar(C::kBarKFree + ks));
-              if (last && (pair || p.qbuf == 0)) mma_commit(bar(C::kBarQFree));
-              if (last && (pair || p.qbuf == 1)) mma_commit(bar(C::kBarQFree + 1));
+          if (i < nb) {
+            wait(C::kBarKFull + ks, kph);
+            if (pair || (i & 1) == static_cast<uint32_t>(t)) {
+              tc_fence_after();
+              issue_s<kFp8>(tm + t * 128, qd, kdesc + ks * (C::kKStage >> 4));
+              commit_elected(bars + 8 * (C::kBarS + t));
+              commit_elected(bars + 8 * (C::kBarKFree + ks));
+            } else if (lane == 0) {
+              mbar_arrive(bar(C::kBarKFree + ks));
             }
-            __syncwarp();
-            const uint32_t e = j << 3 | (last_of_block ? 4u : 0u) | (i < (pair ? 1 : 2) ? 2u : 0u) | t;
-            if (owed == 0) q0 = e;
-            else if (owed == 1) q1 = e;
-            else if (owed == 2) q2 = e;
-            else q3 = e;
-            ++owed;
-            if (t) ++ns[1]; else ++ns[0];
-            if (last_of_block) {
-              ++j;
-              ++i;
-              k_ok = false;
-            }
-            t ^= 1;
-            if (last) {
-              have = false;
-              if (pair || p.qbuf == 0) ++uses[0];
-              if (pair || p.qbuf == 1) ++uses[1];
-            }
-            idle = 0;
+            if (++ks == C::kKStages) ks = 0, kph ^= 1;
           }
+          if (pair && lane == 0 && (t == 0 || i < nb)) mbar_arrive(bar(C::kBarTurn + (t ^ 1)));
         }
-        if (!have && more && __all_sync(kFull, test(C::kBarPiece + pn % kPfPieces, pn / kPfPieces))) {
-          more = have = take_piece(p);
-          q_ok = k_ok = false;
-          pair = p.pair();
-          nb = p.i1 - p.i0;
-          i = 0;
-          t = 0;
-          idle = 0;
-        }
-        // as every wait: bounded, and over once any other has given up
-        if ((idle & 255u) == 255u) {
-          if (*s_failed) break;
-          if (idle == 255u) since = global_timer_ns();
-          else if (global_timer_ns() - since > kWaitLimitNs) {
-            *s_failed = 1;
-            if (lane == 0) atomicOr(a.status, kStatusWaitTimeout);
-            break;
-          }
+        // the queries: both warps' S of a buffer are done
+        if (pair) {
+          commit_elected(bars + 8 * (C::kBarQFree + t));
+          commit_elected(bars + 8 * (C::kBarQFree + t));
+        } else {
+          commit_elected(bars + 8 * (C::kBarQFree + qb));
         }
       }
       // every product and every arrival it owes is done before the CTA ends
-      if (elect_one()) mma_commit(bar(C::kBarDone));
-      mbar_wait(bar(C::kBarDone), 0, a.status);
+      commit_elected(bars + 8 * (C::kBarDone + t));
+      mbar_wait(bar(C::kBarDone + t), 0, a.status);
     } else {
       // ===================== softmax, a thread per row =====================
       const int t = warp >> 2;                       // row tile
@@ -1018,33 +988,44 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         bool any = false;
 #pragma unroll 1
         for (int i = pair ? 0 : t; i < nb; i += pair ? 1 : 2) {
-          wait(C::kBarS + 2 * t + (ns & 1), ns >> 1);
+          wait(C::kBarS + t, ns);
+          if (ns > 0) wait(C::kBarO + t, ns - 1);  // (over already: S came behind that product)
           tc_fence_after();
           if (busy) {
-            const int nv = min(kPfBlk, p.tokens - (p.i0 + i) * kPfBlk);
-            const uint32_t tb = ts + (ns & 1) * 64;
-            float s[64];
-            tmem_ld64(tb, s);
-            if (nv < kPfBlk) {  // columns behind the last token
-#pragma unroll
-              for (int k = 0; k < 64; ++k)
-                if (k >= nv) s[k] = -INFINITY;
+            const int nv = p.tokens - (p.i0 + i) * kPfBlk;
+            if (nv < kPfBlk) {
+              // columns behind the last token: -inf, written to tensor memory by a short loop (selects
+              // on registers would be a second copy of the code below, fetched anew for every tail)
+#pragma unroll 1
+              for (int k = nv; k < kPfBlk;) {
+                if (k & 7) {
+                  tmem_fill1(ts + k, -INFINITY);
+                  ++k;
+                } else {
+                  tmem_fill8(ts + k, -INFINITY);
+                  k += 8;
+                }
+              }
+              tmem_wait_st();
             }
-            float m4[4] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
+            float s[64], mx = -INFINITY;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              tmem_ld64(ts + 64 * h, s);
+              float m4[4] = {max3(mx, s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
 #pragma unroll
-            for (int k = 8; k < 64; k += 8)
+              for (int k = 8; k < 64; k += 8)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) m4[x] = max3(m4[x], s[k + 2 * x], s[k + 2 * x + 1]);
-            const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+                for (int x = 0; x < 4; ++x) m4[x] = max3(m4[x], s[k + 2 * x], s[k + 2 * x + 1]);
+              mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+            }
             const float mb = mx == -INFINITY ? -INFINITY : mx * mult;
             const bool grown = mb > m + kPfGrow || (m == -INFINITY && mb != -INFINITY);
             if (__any_sync(kFull, grown)) {
               const float f = !grown ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - mb);
               if (grown) m = mb;
               l *= f;
-              if (any) {  // O of the blocks before, once their products are done
-                wait(C::kBarO + 2 * t + ((ns - 1) & 1), (ns - 1) >> 1);
-                tc_fence_after();
+              if (any) {  // O of the blocks before
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                   float o[32];
@@ -1058,24 +1039,35 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
             const float ref = m == -INFINITY ? 0.f : m;
             const float2 mult2 = make_float2(mult, mult), ref2 = make_float2(-ref, -ref);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            uint32_t w[32];
+            float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              tmem_ld64(ts + 64 * h, s);
+              uint32_t w[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              float2 e = fma2(make_float2(s[2 * k], s[2 * k + 1]), mult2, ref2);
-              e.x = fast_exp2(e.x);
-              e.y = fast_exp2(e.y);
-              sum[k & 1] = add2(sum[k & 1], e);
-              w[k] = kFp8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+              for (int k = 0; k < 32; ++k) {
+                float2 e = fma2(make_float2(s[2 * k], s[2 * k + 1]), mult2, ref2);
+                e.x = fast_exp2(e.x);
+                e.y = fast_exp2(e.y);
+                sum[k & 1] = add2(sum[k & 1], e);
+                w[k] = kFp8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+              }
+              tmem_st32(ts + 32 * h, w);  // over columns that have been read
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(C::kBarP + 2 * t + h));
             }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            tmem_st32(tb, w);
-            tmem_wait_st();
+            l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(C::kBarP + 2 * t));
+              mbar_arrive(bar(C::kBarP + 2 * t + 1));
+            }
           }
           any = true;
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::kBarP + 2 * t + (ns & 1)));
           ++ns;
         }
         // ---- the row's partial: pieces at a unit's start by row, others by CTA
@@ -1085,9 +1077,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           slot = static_cast<int64_t>((p.prefix ? 0 : 2) + (pair ? 0 : t)) * a.B * a.Hq +
                  static_cast<int64_t>(p.gfirst + grow / a.G) * a.Hq + p.h * a.G + grow % a.G;
         if (any) {
-          // (the last two products: the MMAs of the last block's S came behind the others')
-          if (ns > 1) wait(C::kBarO + 2 * t + (ns & 1), (ns - 2) >> 1);
-          wait(C::kBarO + 2 * t + ((ns - 1) & 1), (ns - 1) >> 1);
+          wait(C::kBarO + t, ns - 1);
           tc_fence_after();
           if (busy) {
             const float vscale = kFp8 ? __ldg(a.v_scale) : 1.f;

@@ -6,7 +6,7 @@ import random
 
 import pytest
 
-PAIR, SOLO, ROWS, BLK = 2, 1, 256, 4
+PAIR, SOLO, ROWS, BLK = 2, 1, 256, 8
 
 
 def prefix_shape(ptiles, gcount, G):
@@ -17,7 +17,7 @@ def prefix_shape(ptiles, gcount, G):
 
 
 def own_blocks(stok):
-    return -(-stok // 64)
+    return -(-stok // 128)
 
 
 def owned(y, n, w, b0, b1):
