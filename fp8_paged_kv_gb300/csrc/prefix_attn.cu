@@ -64,12 +64,13 @@ constexpr int kPfPlanThreads = 1024;
 constexpr int kPfMergeWarps = 4;
 
 // What the planning kernel finds of each request.
-struct PfReq {
+struct alignas(16) PfReq {
   int32_t y0;      // place of its units in the work list (the group's prefix units first, at its first request)
   int32_t ptiles;  // tiles of the shared prefix
   int32_t stok;    // tokens behind it; 0 for a dead request
   int32_t gfirst, gcount, leader;
-  int32_t pad[2];
+  int32_t r, b0, b1;  // (of a CTA's first request: its number, the CTA's range)
+  int32_t pad[3];
 };
 
 struct PfArgs {
@@ -85,13 +86,14 @@ struct PfArgs {
   float* lse;
   uint32_t* status;
   int32_t* total;    // length of the work list (the host has made sure that it fits)
-  PfReq* start;      // [ctas] the request in whose units a CTA's range begins: its record, pad = {r, total}
+  PfReq* start;      // [ctas] the request in whose units a CTA's range begins: its record, number and the CTA's range
   int32_t* gstart;   // [n_groups + 1] group starts, clamped and non-decreasing
   int32_t* dead;     // [B]
   PfReq* req;        // [B]
   float2* part_ml;   // partials: 4 per (request, query head), then 256 rows per CTA
   float* part_o;
   int n_groups, B, Hq, Hkv, G, page_size, num_pages, max_pages, ctas, zbox;
+  uint32_t by_g, by_tpp;  // ceil(2^32 / G), ceil(2^32 / tiles of a page); 0 for 1
   float sm_scale_log2;
 };
 
@@ -135,6 +137,11 @@ struct PfCfg {
   static constexpr int kSmem = kOffMisc + 16 + 1024;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
+
+// x / d for d <= 16 by its reciprocal `by`: exact while x (by d - 2^32) < 2^32, that is for x < 2^28.
+__device__ __forceinline__ int quotient(int x, uint32_t by) {
+  return by == 0 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), by));
+}
 
 // Context length of request r if it is alive by its length and abort flag, else 0.
 __device__ __forceinline__ int live_length(const PfArgs& a, int r) {
@@ -181,8 +188,9 @@ __device__ __forceinline__ PfRanges ranges_of(int T, int n) {
 }
 // Blocks [i0, i1) of a unit at y with n blocks of cost w that a range [b0, b1) owns.
 __device__ __forceinline__ void owned_blocks(int y, int n, int w, int b0, int b1, int& i0, int& i1) {
-  i0 = min(n, b0 <= y ? 0 : (b0 - y + w - 1) / w);
-  i1 = min(n, b1 <= y ? 0 : (b1 - y + w - 1) / w);
+  const int lo = max(b0 - y, 0) + w - 1, hi = max(b1 - y, 0) + w - 1;
+  i0 = min(n, w == kPfCostPair ? lo / kPfCostPair : lo / kPfCostSolo);
+  i1 = min(n, w == kPfCostPair ? hi / kPfCostPair : hi / kPfCostSolo);
 }
 
 struct alignas(16) PfPiece {
@@ -206,18 +214,13 @@ struct PfCursor {
   int y, b0, b1;
 };
 
+static_assert(sizeof(PfReq) == 48, "three 16-byte words");
 __device__ __forceinline__ PfReq load_req(const PfReq* at) {
   PfReq q;
   const int4* p = reinterpret_cast<const int4*>(at);
-  const int4 x = __ldcg(p), z = __ldcg(p + 1);
-  q.y0 = x.x;
-  q.ptiles = x.y;
-  q.stok = x.z;
-  q.gfirst = x.w;
-  q.gcount = z.x;
-  q.leader = z.y;
-  q.pad[0] = z.z;
-  q.pad[1] = z.w;
+  *reinterpret_cast<int4*>(&q.y0) = __ldcg(p);
+  *reinterpret_cast<int4*>(&q.gcount) = __ldcg(p + 1);
+  *reinterpret_cast<int4*>(&q.b1) = __ldcg(p + 2);
   return q;
 }
 
@@ -229,12 +232,12 @@ __device__ __forceinline__ void enter_request(PfCursor& c, int r, const PfReq& q
   c.y = c.q.y0;
 }
 
-__device__ __forceinline__ PfCursor begin_range(const PfArgs& a, const PfReq& q, int b0, int b1) {
+__device__ __forceinline__ PfCursor begin_range(const PfArgs& a, const PfReq& q) {
   PfCursor c;
-  c.b0 = b0;
-  c.b1 = b1;
-  enter_request(c, q.pad[0], q);
-  int at = b0 - c.y;
+  c.b0 = q.b0;
+  c.b1 = q.b1;
+  enter_request(c, q.r, q);
+  int at = q.b0 - c.y;
   if (c.u == 0) {
     const PfPrefix p = prefix_shape(c.q.ptiles, c.q.gcount, a.G);
     const int all = p.head_cost * a.Hkv;
@@ -316,24 +319,29 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
   const int tpp = a.page_size >> 4;
   // group starts: clamped, then the running maximum
   int carry = 0;
+#pragma unroll 1
   for (int base = 0; a.n_groups > 0 && base <= a.n_groups; base += kPfPlanThreads) {
     const int i = base + t;
     int v = i <= a.n_groups ? min(max(__ldg(a.group_starts + i), 0), a.B) : 0;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(kFull, v, o);
       if (lane >= o) v = max(v, x);
     }
     if (lane == 31) s_max[warp] = v;
     __syncthreads();
-    int before = carry;
-    for (int k = 0; k < kPfPlanThreads / 32; ++k) {
-      if (k < warp) before = max(before, s_max[k]);
-      carry = max(carry, s_max[k]);
+    int w = s_max[lane];  // the warps' maxima, then those of the warps up to each
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, w, o);
+      if (lane >= o) w = max(w, x);
     }
-    if (i <= a.n_groups) a.gstart[i] = max(v, before);
+    const int before = __shfl_sync(kFull, w, max(warp - 1, 0));
+    if (i <= a.n_groups) a.gstart[i] = max(max(v, carry), warp > 0 ? before : 0);
+    carry = max(carry, __shfl_sync(kFull, w, 31));
     __syncthreads();
   }
+#pragma unroll 1
   for (int r = t; r < a.B; r += kPfPlanThreads) {
     const int L = live_length(a, r);
     PfReq& q = a.req[r];
@@ -346,10 +354,12 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
   }
   __syncthreads();
   // what each group shares: whole pages of the prefix that every live request holds
+#pragma unroll 1
   for (int g = warp; g < a.n_groups; g += kPfPlanThreads / 32) {
     const int lo = a.gstart[g], hi = a.gstart[g + 1];
     if (hi - lo < 2) continue;
     int least = 0x7fffffff, leader = 0x7fffffff;
+#pragma unroll 1
     for (int r = lo + lane; r < hi; r += 32) {
       const int L = a.req[r].stok;
       if (L > 0) {
@@ -362,6 +372,7 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
     const int pre = __ldg(a.prefix_lens + g);
     const int ptiles = leader == 0x7fffffff ? 0 : max(0, min(pre, least)) / a.page_size * tpp;
     if (ptiles == 0) continue;
+#pragma unroll 1
     for (int r = lo + lane; r < hi; r += 32) {
       PfReq& q = a.req[r];
       q.ptiles = ptiles;
@@ -382,21 +393,27 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
     return c * a.Hkv;
   };
   int mine = 0;
+#pragma unroll 1
   for (int r = rb; r < re; ++r) mine += cost_of(r);
   int incl = mine;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(kFull, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) s_sum[warp] = incl;
   __syncthreads();
-  int y = incl - mine, T = 0;
-  for (int k = 0; k < kPfPlanThreads / 32; ++k) {
-    if (k < warp) y += s_sum[k];
-    T += s_sum[k];
+  int sums = s_sum[lane];
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kFull, sums, o);
+    if (lane >= o) sums += x;
   }
+  const int below = __shfl_sync(kFull, sums, max(warp - 1, 0));
+  const int T = __shfl_sync(kFull, sums, 31);
+  int y = incl - mine + (warp > 0 ? below : 0);
   if (t == 0) *a.total = T;
+#pragma unroll 1
   for (int r = rb; r < re; ++r) {
     a.req[r].y0 = y;
     y += cost_of(r);
@@ -404,16 +421,19 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
   __syncthreads();
   // every CTA's first request: the last one whose units start at or before its range
   const PfRanges rg = ranges_of(T, a.ctas);
+#pragma unroll 1
   for (int c = t; c < a.ctas; c += kPfPlanThreads) {
     const int b0 = rg.begin(c);
     int lo = 0, hi = a.B - 1;
+#pragma unroll 1
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (a.req[mid].y0 <= b0) lo = mid; else hi = mid - 1;
     }
     PfReq q = a.req[lo];
-    q.pad[0] = lo;
-    q.pad[1] = T;
+    q.r = lo;
+    q.b0 = b0;
+    q.b1 = rg.begin(c + 1);
     a.start[c] = q;
   }
 }
@@ -575,8 +595,7 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // A wait that gives up once any wait of the CTA has: control flow then runs on
 // to the end without waiting (every address stays in range; the results are
 // void and the status word says so), so that no barrier is left waiting.
-__device__ __forceinline__ void pf_wait(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* failed) {
-  if (mbar_try_wait(bar, parity)) return;
+__device__ __noinline__ void pf_wait_long(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* failed) {
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return;
@@ -589,6 +608,17 @@ __device__ __forceinline__ void pf_wait(uint32_t bar, uint32_t parity, uint32_t*
       }
     }
   }
+}
+__device__ __forceinline__ void pf_wait(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* failed) {
+  if (!mbar_try_wait(bar, parity)) pf_wait_long(bar, parity, status, failed);
+}
+
+// A value the compiler does not know to be a loop's invariant: a loop is not copied for each of its
+// cases.  Code is kept small all over: 16 warps run six programs, and what the instruction caches do not
+// hold is fetched anew at some ten cycles an instruction.
+__device__ __forceinline__ int varying(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
 }
 
 template <bool kFp8>
@@ -636,8 +666,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   griddep_wait();  // the plan is there
   const uint32_t tmem = *s_tmem;
   const PfReq first = load_req(a.start + blockIdx.x);
-  const PfRanges rg = ranges_of(first.pad[1], a.ctas);
-  const int b0 = rg.begin(blockIdx.x), b1 = rg.begin(blockIdx.x + 1);
   auto wait = [&](int i, uint32_t parity) { pf_wait(bar(i), parity & 1u, a.status, s_failed); };
   // the next piece, from the planning warp; false at the end
   uint32_t pn = 0;
@@ -656,8 +684,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     auto load = [&](int k) -> uint4 {
       const int i = k + (lane >> 4), g = p.row0 + row + i;
       if (i >= n) return make_uint4(0, 0, 0, 0);
+      const int r = quotient(g, a.by_g);
       return __ldg(reinterpret_cast<const uint4*>(
-                       a.q + (static_cast<int64_t>(p.gfirst + g / a.G) * a.Hq + p.h * a.G + g % a.G) * kPfDim) + c);
+                       a.q + (static_cast<int64_t>(p.gfirst + r) * a.Hq + p.h * a.G + g - r * a.G) * kPfDim) + c);
     };
     const float base = fabsf(a.sm_scale_log2) * (kFp8 ? __ldg(a.k_scale) : 1.f);
     // a negative scale's sign goes to the query: maxima of raw scores are then those of scaled ones
@@ -714,7 +743,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     __syncwarp();
   };
 
-  if (b0 < b1) {
+  if (first.b0 < first.b1) {
     PfPiece p;
     const int tpp = a.page_size >> 4;
     if (warp == kPfPlanWarp) {
@@ -722,9 +751,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // Also the queries of own units (a few rows), and the check that a group's tables agree: the
       // prefix units of kv head 0 cover every shared page once per 256 rows, and each request of the
       // unit must name the leader's pages, which must be in the pool.
-      PfCursor cur = begin_range(a, first, b0, b1);
+      PfCursor cur = begin_range(a, first);
       uint32_t n = 0, uses[2] = {0, 0};
       int qbuf = 1;
+#pragma unroll 1
       for (bool more = true; more; ++n) {
         more = next_piece(a, cur, p);
         if (!more) p.i0 = p.i1 = 0;
@@ -749,14 +779,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         ++uses[qbuf];
         if (pair) ++uses[qbuf ^ 1];
         if (p.prefix && p.h == 0) {
-          const int p0 = p.i0 * kPfBlkTiles / tpp;
-          const int p1 = (min(p.i1 * kPfBlkTiles, p.tokens / kPfTile) + tpp - 1) / tpp;
+          const int p0 = quotient(p.i0 * kPfBlkTiles, a.by_tpp);
+          const int p1 = quotient(min(p.i1 * kPfBlkTiles, p.tokens / kPfTile) + tpp - 1, a.by_tpp);
           const int32_t* lead = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
-          const int r0 = p.gfirst + p.row0 / a.G, r1 = p.gfirst + (p.row0 + p.rows - 1) / a.G;
+          const int r0 = p.gfirst + quotient(p.row0, a.by_g), r1 = p.gfirst + quotient(p.row0 + p.rows - 1, a.by_g);
+#pragma unroll 1
           for (int i = p0 + lane; i < p1; i += 32) {
             const int want = __ldg(lead + i);
             const bool in = want >= 0 && want < a.num_pages;
-#pragma unroll 4
+#pragma unroll 2
             for (int r = r0; r <= r1; ++r)
               if (!in || __ldg(a.page_table + static_cast<int64_t>(r) * a.max_pages + i) != want) a.dead[r] = 1;
           }
@@ -782,14 +813,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int tiles = (p.tokens + kPfTile - 1) / kPfTile;
         auto page_of = [&](int i) -> int {  // page of box c of block i, -2: no such box
           const int t = i * kPfBlkTiles + c * a.zbox;
-          return c < boxes && t < tiles && i < p.i1 ? __ldg(row + (p.tile0 + t) / tpp) : -2;
+          return c < boxes && t < tiles && i < p.i1 ? __ldg(row + quotient(p.tile0 + t, a.by_tpp)) : -2;
         };
-        int next = page_of(p.i0), next2 = page_of(p.i0 + 1);
+        int next = page_of(p.i0);
         const uint64_t pol = p.prefix ? again : once;
+#pragma unroll 1
         for (int i = p.i0; i < p.i1; ++i, ++j) {
           const int pg = next;
-          next = next2;
-          next2 = page_of(i + 2);
+          next = page_of(i + 1);
           if (round > 0) wait(free + st, round - 1);
           const bool good = pg >= 0 && pg < a.num_pages;
           // a page outside the pool: the request is dead (a group's are told apart by the planning warp)
@@ -804,9 +835,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           __syncwarp(group);
           if (good && part < parts) {
             const int tile = p.tile0 + i * kPfBlkTiles + c * a.zbox;
-            const int z = (pg * a.Hkv + p.h) * tpp + tile % tpp;
+            const int z = (pg * a.Hkv + p.h) * tpp + tile - quotient(tile, a.by_tpp) * tpp;
             const uint32_t dst = ring + st * C::kKStage;
-            if (kw)
+            if (varying(kw))
               tma_load_3d(dst + part * kPfBlk * 128 + c * a.zbox * kPfTile * 128, &kmap, part * 64, 0, z, f, pol);
             else
               tma_load_3d(dst + c * a.zbox * kPfTile * kPfDim * C::kElem, &vmap, 0, kFp8 ? 16 : 128, z, f, pol);
@@ -819,6 +850,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       // every copy has landed before the CTA ends, even if a wait gave up
       if (leads) {
+#pragma unroll 1
         for (uint32_t b = j > static_cast<uint32_t>(stages) ? j - stages : 0; b < j; ++b)
           mbar_wait(bar(full + b % stages), (b / stages) & 1, a.status);
       }
@@ -827,6 +859,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const int d = threadIdx.x - kPfVWarp * 32;  // this thread's dim
       uint32_t j = 0;
       while (take_piece(p)) {
+#pragma unroll 1
         for (int i = p.i0; i < p.i1; ++i, ++j) {
           const int nv = min(kPfBlk, p.tokens - i * kPfBlk);
           const uint32_t vs = j % C::kVStages;
@@ -836,7 +869,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const uint32_t buf = j % C::kReady;
             if (j >= static_cast<uint32_t>(C::kReady)) wait(C::kBarUsed + buf, j / C::kReady - 1);
             uint8_t* const o = sm + C::kOffV16 + buf * C::kV16 + d * 16;
-#pragma unroll
+#pragma unroll 2
             for (int t = 0; t < kPfBlkTiles; ++t) {
               // codes of dim d, tokens 16 t .. 16 t + 15, to two rows of 8 f16
               const uint4 x = *reinterpret_cast<const uint4*>(v + t * kPfTile * kPfDim + d * 16);
@@ -894,21 +927,23 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const uint64_t vdesc = kFp8 ? smem_desc(base + C::kOffV16, 2048, 128, 0) : smem_desc(base + C::kOffV, 16, 256, 6);
       uint32_t ks = 0, kph = 0, vs = 0, vph = 0, n = 0, begun = 0, uses0 = 0, uses1 = 0, turns = 0;
       while (take_piece(p)) {
-        const bool pair = __any_sync(kFull, p.pair());
+        const int pair_in = __any_sync(kFull, p.pair());
         const uint32_t nb = __reduce_max_sync(kFull, p.i1 - p.i0), qb = __reduce_max_sync(kFull, p.qbuf);
-        if (pair || qb == 0) wait(C::kBarQ, uses0++);
-        if (pair || qb == 1) wait(C::kBarQ + 1, uses1++);
-        const uint64_t qd = qdesc + (pair ? t : qb) * (C::kQTile >> 4);
+        if (pair_in || qb == 0) wait(C::kBarQ, uses0++);
+        if (pair_in || qb == 1) wait(C::kBarQ + 1, uses1++);
+        const uint64_t qd = qdesc + (pair_in ? t : qb) * (C::kQTile >> 4);
         bool begins = true;
+#pragma unroll 1
         for (uint32_t i = 0; i <= nb; ++i) {
           // PV of block i - 1, S of block i
+          const bool pair = varying(pair_in) != 0;
           if (pair && (t == 1 || i > 0)) wait(C::kBarTurn + t, turns++);
           if (i > 0) {
             wait(C::kBarReady + vs, vph);
             if (pair || ((i - 1) & 1) == static_cast<uint32_t>(t)) {
               if (begins && begun > 0) wait(C::kBarOFree + t, begun - 1);  // O of the piece before has been read
               const uint64_t vd = vdesc + vs * ((kFp8 ? C::kV16 : C::kVStage) >> 4);
-#pragma unroll
+#pragma unroll 1
               for (int h = 0; h < 2; ++h) {
                 wait(C::kBarP + 2 * t + h, n);
                 tc_fence_after();
@@ -940,12 +975,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (pair && lane == 0 && (t == 0 || i < nb)) mbar_arrive(bar(C::kBarTurn + (t ^ 1)));
         }
         // the queries: both warps' S of a buffer are done
-        if (pair) {
-          commit_elected(bars + 8 * (C::kBarQFree + t));
-          commit_elected(bars + 8 * (C::kBarQFree + t));
-        } else {
-          commit_elected(bars + 8 * (C::kBarQFree + qb));
-        }
+#pragma unroll 1
+        for (int k = 0; k <= pair_in; ++k) commit_elected(bars + 8 * (C::kBarQFree + (pair_in ? t : qb)));
       }
       // every product and every arrival it owes is done before the CTA ends
       commit_elected(bars + 8 * (C::kBarDone + t));
@@ -1071,11 +1102,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           ++ns;
         }
         // ---- the row's partial: pieces at a unit's start by row, others by CTA
-        const int grow = p.row0 + lrow;
+        const int grow = p.row0 + lrow, rq = quotient(grow, a.by_g);
         int64_t slot = static_cast<int64_t>(4) * a.B * a.Hq + static_cast<int64_t>(blockIdx.x) * kPfUnitRows + t * 128 + row;
         if (p.i0 == 0 && valid)
           slot = static_cast<int64_t>((p.prefix ? 0 : 2) + (pair ? 0 : t)) * a.B * a.Hq +
-                 static_cast<int64_t>(p.gfirst + grow / a.G) * a.Hq + p.h * a.G + grow % a.G;
+                 static_cast<int64_t>(p.gfirst + rq) * a.Hq + p.h * a.G + grow - rq * a.G;
         if (any) {
           wait(C::kBarO + t, ns - 1);
           tc_fence_after();
@@ -1132,16 +1163,38 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
   bool dead = __ldcg(a.dead + r) != 0;
   if (!dead) {
     const PfReq q = load_req(a.req + r);
-    int own_y = q.y0;
-    auto merge_unit = [&](int y, int blocks, int w, int kind, int subs, int lrow) {
+    // the units that hold the row's partials: (place, blocks, cost of a block, row in a CTA's slots)
+    const int nb = own_blocks(q.stok);
+    int own_y = q.y0, y = 0, blocks = 0, w = kPfCostSolo, lrow = 0;
+    if (q.ptiles > 0) {
+      const PfPrefix s = prefix_shape(q.ptiles, q.gcount, a.G);
+      const int gy = q.gfirst == r ? q.y0 : load_req(a.req + q.gfirst).y0;
+      const int i = (r - q.gfirst) * a.G + g, u = i / kPfUnitRows;
+      blocks = s.blocks;
+      w = u == s.units - 1 ? s.wlast : kPfCostPair;
+      lrow = i % kPfUnitRows;
+      y = gy + h * s.head_cost + u * kPfCostPair * blocks;
+      if (q.gfirst == r) own_y += s.head_cost * a.Hkv;
+    }
+#pragma unroll 1
+    for (int kind = 0; kind < 4; kind += 2) {
+      if (kind == 2) {
+        blocks = nb;
+        w = kPfCostSolo;
+        lrow = g;
+        y = own_y + h * nb * kPfCostSolo;
+      }
+      if (blocks == 0) continue;
+      const int subs = w == kPfCostPair ? 0 : 1;  // log2 of the row tiles with a partial each
       const int c0 = rg.owner(y), c1 = rg.owner(y + (blocks - 1) * w);
-      const int cands = (c1 - c0 + 1) * subs;
+      const int cands = (c1 - c0 + 1) << subs;
+#pragma unroll 1
       for (int base = 0; base < cands; base += 32) {
         const int k = base + lane;
         float2 ml = make_float2(-INFINITY, 0.f);
         int64_t slot = 0;
         if (k < cands) {
-          const int c = c0 + k / subs, sub = k % subs;
+          const int c = c0 + (k >> subs), sub = k & subs;
           int i0, i1;
           owned_blocks(y, blocks, w, rg.begin(c), rg.begin(c + 1), i0, i1);
           slot = i0 == 0 ? static_cast<int64_t>(kind + sub) * rows + row
@@ -1149,13 +1202,13 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
           if (i0 < i1) ml = __ldcg(a.part_ml + slot);
         }
         float mx = ml.x;
-#pragma unroll
+#pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
         const float mn = fmaxf(M, mx);
         const bool has = ml.x != -INFINITY;  // a NaN maximum counts
         const float f = has ? fast_exp2(ml.x - mn) : 0.f;
         float ws = ml.y * f;
-#pragma unroll
+#pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(kFull, ws, o);
         const float old = M == -INFINITY ? 0.f : fast_exp2(M - mn);
         W = W * old + ws;
@@ -1165,6 +1218,7 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
         acc.w *= old;
         M = mn;
         unsigned todo = __ballot_sync(kFull, has);
+#pragma unroll 1
         while (todo) {
           float fk[4];
           float4 o[4];
@@ -1187,18 +1241,7 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
           }
         }
       }
-    };
-    if (q.ptiles > 0) {
-      const PfPrefix s = prefix_shape(q.ptiles, q.gcount, a.G);
-      const int gy = q.gfirst == r ? q.y0 : load_req(a.req + q.gfirst).y0;
-      const int i = (r - q.gfirst) * a.G + g, u = i / kPfUnitRows;
-      const int w = u == s.units - 1 ? s.wlast : kPfCostPair;
-      merge_unit(gy + h * s.head_cost + u * kPfCostPair * s.blocks, s.blocks, w, 0,
-                 w == kPfCostPair ? 1 : 2, i % kPfUnitRows);
-      if (q.gfirst == r) own_y += s.head_cost * a.Hkv;
     }
-    const int nb = own_blocks(q.stok);
-    if (nb > 0) merge_unit(own_y + h * nb * kPfCostSolo, nb, kPfCostSolo, 2, 2, g);
   }
   dead = dead || W == 0.f;
   const float inv = dead ? 0.f : 1.f / W;
@@ -1346,6 +1389,8 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   a.max_pages = max_pages;
   a.ctas = ctas;
   a.zbox = zbox;
+  a.by_g = G == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + G - 1) / G);
+  a.by_tpp = tpp == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + tpp - 1) / tpp);
   a.sm_scale_log2 = sm_scale * kPfLog2e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prefix_plan_kernel<<<1, kPfPlanThreads, 0, s>>>(a);
