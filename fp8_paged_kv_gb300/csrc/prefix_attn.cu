@@ -59,7 +59,7 @@ constexpr int kPfCostSolo = 1;
 
 constexpr int kPfThreads = 512;
 constexpr int kPfVWarp = 8, kPfLoadWarp = 12, kPfMmaWarp = 13, kPfPlanWarp = 15;  // two MMA warps
-constexpr int kPfPieces = 4;                   // pieces known ahead
+constexpr int kPfPieces = 4, kPfPieceBytes = 80;  // pieces known ahead
 constexpr int kPfPlanThreads = 1024;
 constexpr int kPfMergeWarps = 4;
 
@@ -113,7 +113,7 @@ struct PfCfg {
   static constexpr int kOffV16 = kOffV + kVStages * kVStage;
   static constexpr int kOffMult = kOffV16 + kV16Bufs * kV16;   // score multiplier of each query row
   static constexpr int kOffPiece = kOffMult + 2 * 128 * 4;
-  static constexpr int kOffBars = kOffPiece + kPfPieces * 48;
+  static constexpr int kOffBars = kOffPiece + kPfPieces * kPfPieceBytes;
   // barriers
   static constexpr int kReady = kFp8 ? kV16Bufs : kVStages;    // V blocks ready for the MMA
   static constexpr int kBarKFull = 0;
@@ -206,7 +206,11 @@ struct alignas(16) PfPiece {
   int pad;
   __device__ __forceinline__ bool pair() const { return rows > 128; }
 };
-static_assert(sizeof(PfPiece) == 48, "slot of the piece ring");
+struct alignas(16) PfSlot {
+  PfPiece piece;
+  int pages[kPfBlkTiles];  // of the first block's tiles, -1 where the unit has none
+};
+static_assert(sizeof(PfSlot) == kPfPieceBytes, "slot of the piece ring");
 
 struct PfCursor {
   PfReq q;
@@ -216,11 +220,18 @@ struct PfCursor {
 
 static_assert(sizeof(PfReq) == 48, "three 16-byte words");
 __device__ __forceinline__ PfReq load_req(const PfReq* at) {
-  PfReq q;
   const int4* p = reinterpret_cast<const int4*>(at);
-  *reinterpret_cast<int4*>(&q.y0) = __ldcg(p);
-  *reinterpret_cast<int4*>(&q.gcount) = __ldcg(p + 1);
-  *reinterpret_cast<int4*>(&q.b1) = __ldcg(p + 2);
+  const int4 x = __ldcg(p), y = __ldcg(p + 1), z = __ldcg(p + 2);
+  PfReq q;
+  q.y0 = x.x;
+  q.ptiles = x.y;
+  q.stok = x.z;
+  q.gfirst = x.w;
+  q.gcount = y.x;
+  q.leader = y.y;
+  q.r = y.z;
+  q.b0 = y.w;
+  q.b1 = z.x;
   return q;
 }
 
@@ -590,6 +601,13 @@ __device__ __forceinline__ void tmem_fill8(uint32_t taddr, float x) {
                "r"(__float_as_uint(x))
                : "memory");
 }
+__device__ __forceinline__ void tmem_fill32(uint32_t taddr, float x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, "
+      "%1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(taddr),
+      "r"(__float_as_uint(x))
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A wait that gives up once any wait of the CTA has: control flow then runs on
@@ -632,7 +650,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const uint32_t sbase = smem_addr(sm);
   auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8 * i; };
   float* const s_mult = reinterpret_cast<float*>(sm + C::kOffMult);
-  PfPiece* const s_piece = reinterpret_cast<PfPiece*>(sm + C::kOffPiece);
+  PfSlot* const s_piece = reinterpret_cast<PfSlot*>(sm + C::kOffPiece);
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
   volatile int* const s_failed = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 4);
   const unsigned kFull = 0xffffffffu;
@@ -647,7 +665,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (i >= C::kBarReady && i < C::kBarReady + C::kReady) arrivals = 4;             // V warps
     if (kFp8 && i >= C::kBarVFree && i < C::kBarVFree + C::kVStages) arrivals = 4;   // V warps
     if (i >= C::kBarP && i < C::kBarP + 4) arrivals = 4;                             // a tile's softmax warps
-    if (i >= C::kBarOFree && i < C::kBarQFree) arrivals = 4;                         // (also Q)
+    if (i >= C::kBarOFree && i < C::kBarOFree + 2) arrivals = 4;                     // a tile's softmax warps
+    if (i >= C::kBarQ && i < C::kBarQ + 2) arrivals = 5;                             // those, or the planning warp for them; and it
     if (i >= C::kBarQFree && i < C::kBarQFree + 2) arrivals = 10;                    // MMA and softmax warps
     if (i >= C::kBarPieceFree && i < C::kBarPieceFree + kPfPieces) arrivals = 16;    // every other warp; K's and V's half of one
     mbar_init(bar(i), arrivals);
@@ -669,13 +688,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   auto wait = [&](int i, uint32_t parity) { pf_wait(bar(i), parity & 1u, a.status, s_failed); };
   // the next piece, from the planning warp; false at the end
   uint32_t pn = 0;
-  auto take_piece = [&](PfPiece& p, unsigned group = 0xffffffffu, bool leads = false) -> bool {
+  auto take_piece = [&](PfPiece& p) -> bool {
     wait(C::kBarPiece + pn % kPfPieces, pn / kPfPieces);
-    p = s_piece[pn % kPfPieces];
-    __syncwarp(group);
-    if (lane == 0 || leads) mbar_arrive(bar(C::kBarPieceFree + pn % kPfPieces));
+    p = s_piece[pn % kPfPieces].piece;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::kBarPieceFree + pn % kPfPieces));
     ++pn;
-    return __all_sync(group, p.i0 < p.i1 && !*s_failed);
+    return __all_sync(kFull, p.i0 < p.i1 && !*s_failed);
   };
   // query rows [row, row + n) of a unit, by one warp, into rows `at`.. of a query buffer: half a warp per row
   // (a lane: 8 dims), the next rows' loads ahead
@@ -751,33 +770,56 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // Also the queries of own units (a few rows), and the check that a group's tables agree: the
       // prefix units of kv head 0 cover every shared page once per 256 rows, and each request of the
       // unit must name the leader's pages, which must be in the pool.
+      // Pieces are published as far ahead as the ring allows, queries staged as far as the two buffers do.
       PfCursor cur = begin_range(a, first);
-      uint32_t n = 0, uses[2] = {0, 0};
-      int qbuf = 1;
+      uint32_t n = 0, staged = 0, uses[2] = {0, 0};
+      int qbuf = 0;
+      bool more = true;
 #pragma unroll 1
-      for (bool more = true; more; ++n) {
-        more = next_piece(a, cur, p);
-        if (!more) p.i0 = p.i1 = 0;
+      for (;;) {
+#pragma unroll 1
+        while (more && (n == 0 || (staged > 0 && n - staged < kPfPieces))) {
+          if (n >= kPfPieces) {
+            const uint32_t phase = n / kPfPieces - 1;
+            if (staged == n) wait(C::kBarPieceFree + n % kPfPieces, phase);
+            else if (!__all_sync(kFull, mbar_test(bar(C::kBarPieceFree + n % kPfPieces), phase & 1))) break;
+          }
+          more = next_piece(a, cur, p);
+          if (!more) p.i0 = p.i1 = 0;
+          p.qbuf = qbuf;
+          qbuf ^= 1;
+          // the first block's pages: the loads of a new piece need not wait for the table
+          const int tile = p.i0 * kPfBlkTiles + lane;
+          const bool some = more && lane < kPfBlkTiles && tile * kPfTile < p.tokens;
+          const int page = some ? max(-1, __ldg(a.page_table + static_cast<int64_t>(p.r) * a.max_pages +
+                                                quotient(p.tile0 + tile, a.by_tpp))) : -1;
+          PfSlot* const at = s_piece + n % kPfPieces;
+          if (lane < kPfBlkTiles) at->pages[lane] = page;
+          if (lane == 0) at->piece = p;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kBarPiece + n % kPfPieces));
+          ++n;
+        }
+        p = s_piece[staged % kPfPieces].piece;
+        __syncwarp();
+        ++staged;
+        if (p.i0 >= p.i1) break;
         const bool pair = p.pair();
-        qbuf ^= 1;
-        p.qbuf = qbuf;
-        if (n >= kPfPieces) wait(C::kBarPieceFree + n % kPfPieces, n / kPfPieces - 1);
-        if (lane == 0) {
-          s_piece[n % kPfPieces] = p;
-          mbar_arrive(bar(C::kBarPiece + n % kPfPieces));
+        // (every use of a buffer is waited for in turn and announced here, whoever stages it: a barrier's
+        // parity tells neighbouring phases apart, no others, so nobody may run two uses ahead of this warp)
+        if (uses[p.qbuf] > 0) wait(C::kBarQFree + p.qbuf, uses[p.qbuf] - 1);
+        if (pair && uses[p.qbuf ^ 1] > 0) wait(C::kBarQFree + (p.qbuf ^ 1), uses[p.qbuf ^ 1] - 1);
+        if (!p.prefix) {
+          stage_rows(p, p.qbuf, 0, 0, p.rows);
+          if (lane < 4) mbar_arrive(bar(C::kBarQ + p.qbuf));
         }
         __syncwarp();
-        if (!more) break;
-        // (every use of a buffer is waited for in turn, whoever stages it: a barrier's parity tells
-        // neighbouring phases apart, no others)
-        if (uses[qbuf] > 0) wait(C::kBarQFree + qbuf, uses[qbuf] - 1);
-        if (pair && uses[qbuf ^ 1] > 0) wait(C::kBarQFree + (qbuf ^ 1), uses[qbuf ^ 1] - 1);
-        if (!p.prefix) {
-          stage_rows(p, qbuf, 0, 0, p.rows);
-          if (lane < 4) mbar_arrive(bar(C::kBarQ + qbuf));
+        ++uses[p.qbuf];
+        if (lane == 0) mbar_arrive(bar(C::kBarQ + p.qbuf));
+        if (pair) {
+          ++uses[p.qbuf ^ 1];
+          if (lane == 0) mbar_arrive(bar(C::kBarQ + (p.qbuf ^ 1)));
         }
-        ++uses[qbuf];
-        if (pair) ++uses[qbuf ^ 1];
         if (p.prefix && p.h == 0) {
           const int p0 = quotient(p.i0 * kPfBlkTiles, a.by_tpp);
           const int p1 = quotient(min(p.i1 * kPfBlkTiles, p.tokens / kPfTile) + tpp - 1, a.by_tpp);
@@ -795,64 +837,84 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
     } else if (warp == kPfLoadWarp) {
       // ===================== K rows, V tiles into their rings =====================
-      // The half-warps run apart, one for K and one for V (their rings drain at different times).  Lane
-      // c copies box c of a block (zbox tiles, within a page); bf16 K: lanes 8 + c the other 64 dims.
+      // The lower half-warp copies K, the upper one V, each with its own piece and place (the rings drain
+      // at different times), in one loop that looks at both and waits for neither.  Lane c of a half
+      // copies box c of a block (zbox tiles, within a page); bf16 K: lanes 8 + c the other 64 dims.
       const bool kw = lane < 16;
       const unsigned group = kw ? 0xffffu : 0xffff0000u;
       const bool leads = (lane & 15) == 0;
       const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
-      const int c = lane & 7, part = (lane & 15) >> 3;
-      const int boxes = kPfBlkTiles / a.zbox;
-      const int stages = kw ? C::kKStages : C::kVStages;
-      const int full = kw ? C::kBarKFull : C::kBarVFull, free = kw ? C::kBarKFree : C::kBarVFree;
-      const int parts = kw && !kFp8 ? 2 : 1;
-      const uint32_t ring = sbase + (kw ? C::kOffK : C::kOffV);
-      uint32_t j = 0, st = 0, round = 0;
-      while (take_piece(p, group, leads)) {
-        const int32_t* row = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
-        const int tiles = (p.tokens + kPfTile - 1) / kPfTile;
-        auto page_of = [&](int i) -> int {  // page of box c of block i, -2: no such box
-          const int t = i * kPfBlkTiles + c * a.zbox;
-          return c < boxes && t < tiles && i < p.i1 ? __ldg(row + quotient(p.tile0 + t, a.by_tpp)) : -2;
-        };
-        int next = page_of(p.i0);
-        const uint64_t pol = p.prefix ? again : once;
-#pragma unroll 1
-        for (int i = p.i0; i < p.i1; ++i, ++j) {
+      const int c = lane & 7;
+      const int box_t = c * a.zbox;                        // first tile of the box in a block
+      const bool copies = c < kPfBlkTiles / a.zbox && ((lane & 8) == 0 || (kw && !kFp8));
+      const uint32_t stages = kw ? C::kKStages : C::kVStages;
+      const uint32_t full = bar(kw ? C::kBarKFull : C::kBarVFull), free = bar(kw ? C::kBarKFree : C::kBarVFree);
+      const uint32_t ring = sbase + (kw ? C::kOffK : C::kOffV) +
+                            (kw ? (lane & 8) / 8 * kPfBlk * 128 + box_t * kPfTile * 128 : box_t * kPfTile * kPfDim * C::kElem);
+      const void* const map = kw ? &kmap : &vmap;
+      const int mx = kw ? (lane & 8) * 8 : 0, my = kw ? 0 : kFp8 ? 16 : 128;
+      auto all_of_half = [&](bool x) -> bool { return (__ballot_sync(kFull, x) & group) == group; };
+      const int32_t* row = nullptr;
+      int i = 0, tiles = 0, next = -2;
+      uint64_t pol = 0;
+      uint32_t j = 0, st = 0, round = 0, idle = 0;
+      bool have = false, done = false;
+      // page of this lane's box of block i, -2: no such box
+      auto page_of = [&](int i) -> int {
+        const int t = i * kPfBlkTiles + box_t;
+        return copies && t < tiles && i < p.i1 ? max(-1, __ldg(row + quotient(p.tile0 + t, a.by_tpp))) : -2;
+      };
+      while (!__all_sync(kFull, done)) {
+        ++idle;
+        if (all_of_half(!have && !done && mbar_test(bar(C::kBarPiece + pn % kPfPieces), pn / kPfPieces & 1))) {
+          const PfSlot& slot = s_piece[pn % kPfPieces];
+          p = slot.piece;
+          next = slot.pages[box_t & (kPfBlkTiles - 1)];
+          __syncwarp(group);
+          if (leads) mbar_arrive(bar(C::kBarPieceFree + pn % kPfPieces));
+          ++pn;
+          have = p.i0 < p.i1;
+          done = !have;
+          i = p.i0;
+          row = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
+          tiles = (p.tokens + kPfTile - 1) / kPfTile;
+          pol = p.prefix ? again : once;
+          if (!copies || i * kPfBlkTiles + box_t >= tiles) next = -2;
+          idle = 0;
+        }
+        const bool goes = all_of_half(have && (round == 0 || mbar_test(free + 8 * st, (round - 1) & 1)));
+        const bool good = goes && next >= 0 && next < a.num_pages;
+        const uint32_t boxes = __popc(__ballot_sync(kFull, good) & group);
+        if (goes) {
           const int pg = next;
           next = page_of(i + 1);
-          if (round > 0) wait(free + st, round - 1);
-          const bool good = pg >= 0 && pg < a.num_pages;
           // a page outside the pool: the request is dead (a group's are told apart by the planning warp)
           if (!good && pg != -2 && !p.prefix) a.dead[p.r] = 1;
-          const int n = __popc(__ballot_sync(group, good && part == 0));
-          const uint32_t f = bar(full + st);
+          const uint32_t f = full + 8 * st;
           if (leads) {
-            const uint32_t bytes = static_cast<uint32_t>(n * a.zbox) * kPfTile * kPfDim * C::kElem;
+            const uint32_t bytes = boxes * a.zbox * (kPfTile * (kw ? 128 : kPfDim * C::kElem));
             if (bytes == 0) mbar_arrive(f);
             else mbar_arrive_expect_tx(f, bytes);
           }
           __syncwarp(group);
-          if (good && part < parts) {
-            const int tile = p.tile0 + i * kPfBlkTiles + c * a.zbox;
-            const int z = (pg * a.Hkv + p.h) * tpp + tile - quotient(tile, a.by_tpp) * tpp;
-            const uint32_t dst = ring + st * C::kKStage;
-            if (varying(kw))
-              tma_load_3d(dst + part * kPfBlk * 128 + c * a.zbox * kPfTile * 128, &kmap, part * 64, 0, z, f, pol);
-            else
-              tma_load_3d(dst + c * a.zbox * kPfTile * kPfDim * C::kElem, &vmap, 0, kFp8 ? 16 : 128, z, f, pol);
+          if (good) {
+            const int tile = p.tile0 + i * kPfBlkTiles + box_t;
+            tma_load_3d(ring + st * C::kKStage, map, mx, my,
+                        (pg * a.Hkv + p.h) * tpp + tile - quotient(tile, a.by_tpp) * tpp, f, pol);
           }
-          if (++st == static_cast<uint32_t>(stages)) {
-            st = 0;
-            ++round;
-          }
+          if (++st == stages) st = 0, ++round;
+          ++j;
+          if (++i == p.i1) have = false;
+          idle = 0;
         }
+        // (whoever waits for a copy gives up in time)
+        if (__any_sync(kFull, (idle & 255u) == 255u && *s_failed != 0)) done = true;
       }
-      // every copy has landed before the CTA ends, even if a wait gave up
+      // every copy has landed before the CTA ends
       if (leads) {
 #pragma unroll 1
-        for (uint32_t b = j > static_cast<uint32_t>(stages) ? j - stages : 0; b < j; ++b)
-          mbar_wait(bar(full + b % stages), (b / stages) & 1, a.status);
+        for (uint32_t b = j > stages ? j - stages : 0; b < j; ++b)
+          mbar_wait(full + 8 * (b % stages), (b / stages) & 1, a.status);
       }
     } else if (warp >= kPfVWarp && warp < kPfVWarp + 4) {
       // ===================== V blocks made ready for the MMA =====================
@@ -1006,14 +1068,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         wait(C::kBarQ + buf, buf ? uses[1] : uses[0]);
         const float mult = s_mult[buf * 128 + row];   // (whatever lies there for a row that is none)
         __syncwarp();
-        if (pair || p.qbuf == 0) {
-          ++uses[0];
-          if (lane == 0) mbar_arrive(bar(C::kBarQFree));
-        }
-        if (pair || p.qbuf == 1) {
-          ++uses[1];
-          if (lane == 0) mbar_arrive(bar(C::kBarQFree + 1));
-        }
+        if (pair || p.qbuf == 0) ++uses[0];
+        if (pair || p.qbuf == 1) ++uses[1];
+        // (of a pair each tile's warps answer for their own buffer, twice: they have seen no other filled)
+        if (lane <= (pair ? 1 : 0)) mbar_arrive(bar(C::kBarQFree + buf));
         // ---- blocks
         float m = -INFINITY, l = 0.f;
         bool any = false;
@@ -1032,9 +1090,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 if (k & 7) {
                   tmem_fill1(ts + k, -INFINITY);
                   ++k;
-                } else {
+                } else if (k & 31) {
                   tmem_fill8(ts + k, -INFINITY);
                   k += 8;
+                } else {
+                  tmem_fill32(ts + k, -INFINITY);
+                  k += 32;
                 }
               }
               tmem_wait_st();

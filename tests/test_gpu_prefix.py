@@ -247,7 +247,7 @@ def test_aborted_leader_and_members(fp8):
 @BOTH
 def test_bad_pages(fp8):
     c = make([(200, [210, 300, 260]), (64, [100, 90])], fp8=fp8)
-    for r, j, p in ((0, 2, -1), (1, 15, c["P"]), (2, 16, -9), (4, 5, 1 << 30)):
+    for r, j, p in ((0, 2, -1), (1, 15, c["P"]), (2, 16, -9), (4, 5, 1 << 30), (3, 4, -2), (1, 12, -2)):
         table = c["table"].copy()
         table[r, j] = p
         ref = reference(c, table=table)

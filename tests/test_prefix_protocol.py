@@ -1,0 +1,299 @@
+"""CPU model of the barriers inside the shared-prefix attention kernel: its warps as
+coroutines that run in a random order, products and copies that finish late, and
+barriers that tell a waiter no more than a phase's parity.  Every run has to end,
+and every read has to find what it waits for: the block, the piece and the queries
+that the reader is at."""
+import random
+
+import pytest
+
+KST, VST, V16, PIECES = 3, 3, 2, 4
+
+
+class Bar:
+    def __init__(self, count):
+        self.count = self.left = count
+        self.phase = 0
+
+    def arrive(self, n=1):
+        for _ in range(n):
+            self.left -= 1
+            if self.left == 0:
+                self.left, self.phase = self.count, self.phase + 1
+
+    def done(self, phase):
+        return (self.phase & 1) != (phase & 1)
+
+
+def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
+    """pieces: [(prefix, pair, blocks)]; slow: a warp that hardly ever gets its turn"""
+    rng = random.Random(seed)
+    kst, ready_n = (KST, V16) if fp8 else (2, VST)
+    B = dict(kfull=[Bar(1) for _ in range(kst)], kfree=[Bar(2) for _ in range(kst)],
+             vfull=[Bar(1) for _ in range(VST)], vfree=[Bar(4 if fp8 else 2) for _ in range(VST)],
+             ready=[Bar(4) for _ in range(ready_n)], used=[Bar(2) for _ in range(V16)],
+             S=[Bar(1), Bar(1)], P=[[Bar(4), Bar(4)], [Bar(4), Bar(4)]], O=[Bar(1), Bar(1)],
+             ofree=[Bar(4), Bar(4)], Q=[Bar(5), Bar(5)], qfree=[Bar(10), Bar(10)],
+             piece=[Bar(1) for _ in range(pieces_ring)], piecefree=[Bar(16) for _ in range(pieces_ring)],
+             turn=[Bar(1), Bar(1)])
+    late = []                       # (order in its queue, effect)
+    queues = {}
+    slots = [None] * pieces_ring
+    qof = [None, None]              # piece whose queries a buffer holds
+    kof, vof, cof = [None] * kst, [None] * VST, [None] * ready_n
+    sof, oof = [None, None], [None, None]
+    nb = len(pieces)
+
+    def later(queue, effect):
+        queues.setdefault(queue, []).append(effect)
+
+    def wait(bar, phase):
+        while not bar.done(phase):
+            yield
+
+    def take(pn):
+        yield from wait(B["piece"][pn % pieces_ring], pn // pieces_ring)
+        assert slots[pn % pieces_ring] is not None and slots[pn % pieces_ring][0] == pn, "piece slot"
+        p = slots[pn % pieces_ring]
+        yield
+        B["piecefree"][pn % pieces_ring].arrive()
+        return p
+
+    def plan():
+        n = staged = 0
+        uses, qbuf, more = [0, 0], 0, True
+        while True:
+            while more and n - staged < pieces_ring:
+                if n >= pieces_ring:
+                    ph = n // pieces_ring - 1
+                    if staged == n:
+                        yield from wait(B["piecefree"][n % pieces_ring], ph)
+                    elif not B["piecefree"][n % pieces_ring].done(ph):
+                        break
+                more = n < nb
+                slots[n % pieces_ring] = (n, qbuf) + (pieces[n] if more else (0, 0, 0))
+                qbuf ^= 1
+                yield
+                B["piece"][n % pieces_ring].arrive()
+                n += 1
+                yield
+            k, qb, prefix, pair, blocks = slots[staged % pieces_ring]
+            assert k == staged
+            staged += 1
+            if not blocks:
+                return
+            for b in ([qb, qb ^ 1] if pair else [qb]):
+                if uses[b] > 0:
+                    yield from wait(B["qfree"][b], uses[b] - 1)
+            if not prefix:
+                qof[qb] = k
+                yield
+                B["Q"][qb].arrive(4)
+            for b in ([qb, qb ^ 1] if pair else [qb]):
+                uses[b] += 1
+                B["Q"][b].arrive()
+            yield
+
+    def loader(full, free, stages, hold, name):
+        j = pn = 0
+        while True:
+            k, qb, prefix, pair, blocks = yield from take(pn)
+            pn += 1
+            if not blocks:
+                return
+            for i in range(blocks):
+                s, r = j % stages, j // stages
+                if r > 0:
+                    yield from wait(free[s], r - 1)
+
+                def land(s=s, at=(k, i)):
+                    hold[s] = at
+                    full[s].arrive()
+                later((name, s), land)
+                j += 1
+                yield
+
+    def vwarp():
+        j = pn = 0
+        while True:
+            k, qb, prefix, pair, blocks = yield from take(pn)
+            pn += 1
+            if not blocks:
+                return
+            for i in range(blocks):
+                vs = j % VST
+                yield from wait(B["vfull"][vs], j // VST)
+                assert vof[vs] == (k, i), "V block"
+                if fp8:
+                    buf = j % V16
+                    if j >= V16:
+                        yield from wait(B["used"][buf], j // V16 - 1)
+                    cof[buf] = (k, i)
+                    yield
+                    B["ready"][buf].arrive()
+                    B["vfree"][vs].arrive()
+                else:
+                    cof[vs] = (k, i)
+                    B["ready"][vs].arrive()
+                j += 1
+                yield
+
+    def mma(t):
+        ks = kr = vs = vr = n = begun = turns = pn = 0
+        uses = [0, 0]
+        q = ("mma", t)
+        while True:
+            k, qb, prefix, pair, blocks = yield from take(pn)
+            pn += 1
+            if not blocks:
+                return
+            for b in (0, 1):
+                if pair or qb == b:
+                    yield from wait(B["Q"][b], uses[b])
+                    uses[b] += 1
+            mine_buf = t if pair else qb
+            begins = True
+            for i in range(blocks + 1):
+                if pair and (t == 1 or i > 0):
+                    yield from wait(B["turn"][t], turns)
+                    turns += 1
+                if i > 0:
+                    yield from wait(B["ready"][vs], vr)
+                    assert cof[vs] == (k, i - 1), "converted block"
+                    freed = (B["used"] if fp8 else B["vfree"])[vs]
+                    if pair or (i - 1) % 2 == t:
+                        if begins and begun > 0:
+                            yield from wait(B["ofree"][t], begun - 1)
+                        for h in (0, 1):
+                            yield from wait(B["P"][t][h], n)
+                        n += 1
+                        begun += begins
+                        begins = False
+
+                        def pv(at=(k, i - 1), vs=vs, freed=freed):
+                            assert cof[vs] == at, "V under a product"
+                            oof[t] = at
+                            B["O"][t].arrive()
+                            freed.arrive()
+                        later(q, pv)
+                    else:
+                        freed.arrive()
+                    vs += 1
+                    if vs == ready_n:
+                        vs, vr = 0, vr + 1
+                if i < blocks:
+                    yield from wait(B["kfull"][ks], kr)
+                    assert kof[ks] == (k, i), "K block"
+                    if pair or i % 2 == t:
+                        def s(at=(k, i), ks=ks, b=mine_buf):
+                            assert kof[ks] == at and qof[b] == at[0], "operands of S"
+                            sof[t] = at
+                            B["S"][t].arrive()
+                            B["kfree"][ks].arrive()
+                        later(q, s)
+                    else:
+                        B["kfree"][ks].arrive()
+                    ks += 1
+                    if ks == kst:
+                        ks, kr = 0, kr + 1
+                if pair and (t == 0 or i < blocks):
+                    B["turn"][t ^ 1].arrive()
+                yield
+            later(q, lambda b=mine_buf, c=2 if pair else 1: B["qfree"][b].arrive(c))
+
+    def softmax(t):
+        ns = pn = 0
+        uses = [0, 0]
+        while True:
+            k, qb, prefix, pair, blocks = yield from take(pn)
+            pn += 1
+            if not blocks:
+                return
+            b = t if pair else qb
+            if prefix and (pair or t == 0):
+                if uses[b] > 0:
+                    yield from wait(B["qfree"][b], uses[b] - 1)
+                qof[b] = k
+                yield
+                B["Q"][b].arrive()
+            yield from wait(B["Q"][b], uses[b])
+            assert qof[b] == k, "multipliers"
+            yield
+            for x in (0, 1):
+                if pair or qb == x:
+                    uses[x] += 1
+            B["qfree"][b].arrive(2 if pair else 1)
+            some = False
+            for i in range(0 if pair else t, blocks, 1 if pair else 2):
+                yield from wait(B["S"][t], ns)
+                if ns > 0:
+                    yield from wait(B["O"][t], ns - 1)
+                assert sof[t] == (k, i), "S"
+                for h in (0, 1):
+                    yield
+                    B["P"][t][h].arrive()
+                ns += 1
+                some = True
+            if some:
+                yield from wait(B["O"][t], ns - 1)
+                assert oof[t][0] == k, "O"
+                yield
+                B["ofree"][t].arrive()
+
+    tasks = [plan(), loader(B["kfull"], B["kfree"], kst, kof, "k"), loader(B["vfull"], B["vfree"], VST, vof, "v"),
+             mma(0), mma(1)] + [vwarp() for _ in range(4)] + [softmax(t) for t in (0, 1) for _ in range(4)]
+    weight = [0.002 if i == slow else rng.choice([1, 1, 3, 20]) for i in range(len(tasks))]
+    def state():
+        return [b.phase * 1000 + b.left for v in B.values() for x in v for b in (x if isinstance(x, list) else [x])]
+
+    def step(i):
+        try:
+            next(tasks[i])
+        except StopIteration:
+            tasks[i] = None
+
+    while any(tasks):
+        before = state()
+        for _ in range(300):
+            if queues and rng.random() < 0.3:
+                key = rng.choice(list(queues))
+                queues[key].pop(0)()
+                if not queues[key]:
+                    del queues[key]
+                continue
+            i = rng.choices(range(len(tasks)), weight)[0]
+            if tasks[i]:
+                step(i)
+        if state() == before:
+            # everybody has its turn: something has to move
+            for i in list(range(len(tasks))) * 8:
+                if tasks[i]:
+                    step(i)
+            assert queues or state() != before or not any(tasks), f"{sum(map(bool, tasks))} warps wait for ever"
+    while queues:
+        key = next(iter(queues))
+        queues[key].pop(0)()
+        if not queues[key]:
+            del queues[key]
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("kind", ["own", "pairs", "solo", "mixed", "long"])
+def test_every_run_ends(fp8, kind):
+    for seed in range(18):
+        rng = random.Random(seed * 7 + len(kind))
+        many = rng.randint(5, 9)
+        if kind == "own":
+            pieces = [(0, 0, rng.choice([1, 1, 2, 3, 5])) for _ in range(many)]
+        elif kind == "pairs":
+            pieces = [(1, 1, rng.choice([1, 1, 2, 3])) for _ in range(many)]
+        elif kind == "solo":
+            pieces = [(1, 0, rng.choice([1, 1, 2, 4])) for _ in range(many)]
+        elif kind == "long":
+            pieces = [(1, rng.randint(0, 1), 9), (0, 0, 8)]
+        else:
+            pieces = []
+            for _ in range(many):
+                prefix = rng.randint(0, 1)
+                pieces.append((prefix, prefix and rng.randint(0, 1), rng.choice([1, 1, 2, 3, 4])))
+        simulate(pieces, fp8, seed, slow=seed - 1)  # each warp held back in turn
