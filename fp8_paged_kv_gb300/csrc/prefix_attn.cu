@@ -59,7 +59,7 @@ constexpr int kPfCostSolo = 1;
 
 constexpr int kPfThreads = 512;
 constexpr int kPfVWarp = 8, kPfLoadWarp = 12, kPfMmaWarp = 13, kPfPlanWarp = 15;  // two MMA warps
-constexpr int kPfPieces = 4, kPfPieceBytes = 80;  // pieces known ahead
+constexpr int kPfPieces = 4, kPfPieceBytes = 176;  // pieces known ahead
 constexpr int kPfPlanThreads = 1024;
 constexpr int kPfMergeWarps = 4;
 
@@ -134,7 +134,7 @@ struct PfCfg {
   static constexpr int kBarTurn = kBarDone + 2;                // [tile] the other tile's products of a turn are out
   static constexpr int kBars = kBarTurn + 2;
   static constexpr int kOffMisc = kOffBars + 8 * kBars;        // tensor memory base, failure flag
-  static constexpr int kSmem = kOffMisc + 16 + 1024;
+  static constexpr int kSmem = kOffMisc + 16;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
@@ -208,7 +208,7 @@ struct alignas(16) PfPiece {
 };
 struct alignas(16) PfSlot {
   PfPiece piece;
-  int pages[kPfBlkTiles];  // of the first block's tiles, -1 where the unit has none
+  int pages[32];  // of the first four blocks' tiles, -1 where the unit has none
 };
 static_assert(sizeof(PfSlot) == kPfPieceBytes, "slot of the piece ring");
 
@@ -645,9 +645,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                        const __grid_constant__ CUtensorMap vmap) {
   using C = PfCfg<kFp8>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t raw = smem_addr(smem_raw);
-  uint8_t* const sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* const sm = smem_raw;
   const uint32_t sbase = smem_addr(sm);
+  if (sbase & 1023u) {  // (cannot happen: the array is aligned, and there is no other shared memory)
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusBadStart);
+    return;
+  }
   auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8 * i; };
   float* const s_mult = reinterpret_cast<float*>(sm + C::kOffMult);
   PfSlot* const s_piece = reinterpret_cast<PfSlot*>(sm + C::kOffPiece);
@@ -788,13 +791,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (!more) p.i0 = p.i1 = 0;
           p.qbuf = qbuf;
           qbuf ^= 1;
-          // the first block's pages: the loads of a new piece need not wait for the table
+          // the first blocks' pages: copies need not wait for the table, which may come from far
           const int tile = p.i0 * kPfBlkTiles + lane;
-          const bool some = more && lane < kPfBlkTiles && tile * kPfTile < p.tokens;
+          const bool some = more && tile * kPfTile < p.tokens;
           const int page = some ? max(-1, __ldg(a.page_table + static_cast<int64_t>(p.r) * a.max_pages +
                                                 quotient(p.tile0 + tile, a.by_tpp))) : -1;
           PfSlot* const at = s_piece + n % kPfPieces;
-          if (lane < kPfBlkTiles) at->pages[lane] = page;
+          at->pages[lane] = page;
           if (lane == 0) at->piece = p;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kBarPiece + n % kPfPieces));
@@ -859,17 +862,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       uint64_t pol = 0;
       uint32_t j = 0, st = 0, round = 0, idle = 0;
       bool have = false, done = false;
-      // page of this lane's box of block i, -2: no such box
-      auto page_of = [&](int i) -> int {
-        const int t = i * kPfBlkTiles + box_t;
-        return copies && t < tiles && i < p.i1 ? max(-1, __ldg(row + quotient(p.tile0 + t, a.by_tpp))) : -2;
-      };
+      int ids[4] = {-2, -2, -2, -2};  // pages of this lane's box of the next four blocks (once it is there)
+      auto have_box = [&](int i) -> bool { return copies && i < p.i1 && i * kPfBlkTiles + box_t < tiles; };
       while (!__all_sync(kFull, done)) {
         ++idle;
         if (all_of_half(!have && !done && mbar_test(bar(C::kBarPiece + pn % kPfPieces), pn / kPfPieces & 1))) {
           const PfSlot& slot = s_piece[pn % kPfPieces];
           p = slot.piece;
-          next = slot.pages[box_t & (kPfBlkTiles - 1)];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ids[k] = slot.pages[(k * kPfBlkTiles + box_t) & 31];
           __syncwarp(group);
           if (leads) mbar_arrive(bar(C::kBarPieceFree + pn % kPfPieces));
           ++pn;
@@ -879,7 +880,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           row = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
           tiles = (p.tokens + kPfTile - 1) / kPfTile;
           pol = p.prefix ? again : once;
-          if (!copies || i * kPfBlkTiles + box_t >= tiles) next = -2;
+          // (the slot may be written anew from here on: the ids are taken now)
+          next = have_box(i) ? ids[0] : -2;
           idle = 0;
         }
         const bool goes = all_of_half(have && (round == 0 || mbar_test(free + 8 * st, (round - 1) & 1)));
@@ -887,7 +889,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const uint32_t boxes = __popc(__ballot_sync(kFull, good) & group);
         if (goes) {
           const int pg = next;
-          next = page_of(i + 1);
+          ids[0] = ids[1];
+          ids[1] = ids[2];
+          ids[2] = ids[3];
+          if (have_box(i + 4)) ids[3] = max(-1, __ldg(row + quotient(p.tile0 + (i + 4) * kPfBlkTiles + box_t, a.by_tpp)));
+          next = have_box(i + 1) ? ids[0] : -2;
           // a page outside the pool: the request is dead (a group's are told apart by the planning warp)
           if (!good && pg != -2 && !p.prefix) a.dead[p.r] = 1;
           const uint32_t f = full + 8 * st;
