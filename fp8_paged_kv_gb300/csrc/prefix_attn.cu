@@ -53,9 +53,10 @@ constexpr float kPfGrow = 8.f;                 // log2 growth of a maximum that 
 // A row's scale is not taken below this (a scale of 0 leaves weights of 1 all the same): -inf times
 // it is -inf still.
 constexpr float kPfMinMult = 1e-37f;
-// Cost of a block in the work list, with both tiles at work and with one.
-constexpr int kPfCostPair = 2;
-constexpr int kPfCostSolo = 1;
+// Costs in the work list, in some 600 cycles: of a block with both tiles at work and with one, and
+// of a unit's start (queries, first products, partials).
+constexpr int kPfCostPair = 6, kPfCostSolo = 2;
+constexpr int kPfStartPair = 12, kPfStartSolo = 5;
 
 constexpr int kPfThreads = 512;
 constexpr int kPfVWarp = 8, kPfLoadWarp = 12, kPfMmaWarp = 13, kPfPlanWarp = 15;  // two MMA warps
@@ -154,10 +155,12 @@ __device__ __forceinline__ int live_length(const PfArgs& a, int r) {
 // ---------------------------------------------------------------------------
 // work list
 // ---------------------------------------------------------------------------
+// The part of a unit's place that its start takes; its blocks lie behind.
+__device__ __forceinline__ int start_cost(int w) { return w == kPfCostPair ? kPfStartPair : kPfStartSolo; }
 // Prefix units of a group, per kv head: `units` of up to 256 rows, all but the
-// last of cost kPfCostPair per block, the last of cost `wlast`.
+// last of cost kPfCostPair per block (`step` each), the last of cost `wlast`.
 struct PfPrefix {
-  int blocks, units, wlast, head_cost;
+  int blocks, units, wlast, step, head_cost;
 };
 __device__ __forceinline__ PfPrefix prefix_shape(int ptiles, int gcount, int G) {
   PfPrefix p;
@@ -165,10 +168,12 @@ __device__ __forceinline__ PfPrefix prefix_shape(int ptiles, int gcount, int G) 
   p.blocks = (ptiles + kPfBlkTiles - 1) / kPfBlkTiles;
   p.units = (rows + kPfUnitRows - 1) / kPfUnitRows;
   p.wlast = rows - (p.units - 1) * kPfUnitRows > 128 ? kPfCostPair : kPfCostSolo;
-  p.head_cost = p.blocks * (kPfCostPair * (p.units - 1) + p.wlast);
+  p.step = kPfStartPair + kPfCostPair * p.blocks;
+  p.head_cost = p.step * (p.units - 1) + start_cost(p.wlast) + p.wlast * p.blocks;
   return p;
 }
 __device__ __forceinline__ int own_blocks(int stok) { return stok > 0 ? (stok - 1) / kPfBlk + 1 : 0; }
+__device__ __forceinline__ int own_cost(int stok) { return stok > 0 ? kPfStartSolo + kPfCostSolo * own_blocks(stok) : 0; }
 
 // CTA c owns the blocks that start in [begin(c), begin(c + 1)): T / n each, one
 // more for the first T mod n CTAs.
@@ -186,7 +191,7 @@ __device__ __forceinline__ PfRanges ranges_of(int T, int n) {
   r.more = T - r.share * n;
   return r;
 }
-// Blocks [i0, i1) of a unit at y with n blocks of cost w that a range [b0, b1) owns.
+// Blocks [i0, i1) that a range [b0, b1) owns of the n blocks of cost w of a unit, the first block at y.
 __device__ __forceinline__ void owned_blocks(int y, int n, int w, int b0, int b1, int& i0, int& i1) {
   const int lo = max(b0 - y, 0) + w - 1, hi = max(b1 - y, 0) + w - 1;
   i0 = min(n, w == kPfCostPair ? lo / kPfCostPair : lo / kPfCostSolo);
@@ -203,7 +208,7 @@ struct alignas(16) PfPiece {
   int tile0;       // table tile of the unit's first token
   int tokens;      // of the unit
   int qbuf;        // query buffer of a unit of one row tile
-  int pad;
+  int t0;          // tile of the first block of such a unit; the others take turns
   __device__ __forceinline__ bool pair() const { return rows > 128; }
 };
 struct alignas(16) PfSlot {
@@ -254,16 +259,15 @@ __device__ __forceinline__ PfCursor begin_range(const PfArgs& a, const PfReq& q)
     const int all = p.head_cost * a.Hkv;
     if (at < all) {
       c.h = at / p.head_cost;
-      const int step = kPfCostPair * p.blocks;
-      c.u = min((at - c.h * p.head_cost) / step, p.units - 1);
-      c.y += c.h * p.head_cost + c.u * step;
+      c.u = min((at - c.h * p.head_cost) / p.step, p.units - 1);
+      c.y += c.h * p.head_cost + c.u * p.step;
       return c;
     }
     c.u = -1;
     c.y += all;
     at -= all;
   }
-  const int cost = kPfCostSolo * own_blocks(c.q.stok);
+  const int cost = own_cost(c.q.stok);
   if (cost > 0) {
     c.h = min(at / cost, a.Hkv);
     c.y += c.h * cost;
@@ -287,8 +291,8 @@ __device__ __forceinline__ bool next_piece(const PfArgs& a, PfCursor& c, PfPiece
       p.tokens = c.q.ptiles * kPfTile;
       p.h = c.h;
       p.gfirst = c.q.gfirst;
-      owned_blocks(c.y, n, w, c.b0, c.b1, p.i0, p.i1);
-      c.y += n * w;
+      owned_blocks(c.y + start_cost(w), n, w, c.b0, c.b1, p.i0, p.i1);
+      c.y += start_cost(w) + n * w;
       if (++c.u == s.units) {
         c.u = 0;
         if (++c.h == a.Hkv) {
@@ -311,8 +315,8 @@ __device__ __forceinline__ bool next_piece(const PfArgs& a, PfCursor& c, PfPiece
       p.tokens = c.q.stok;
       p.h = c.h;
       p.gfirst = c.r;
-      owned_blocks(c.y, n, kPfCostSolo, c.b0, c.b1, p.i0, p.i1);
-      c.y += n * kPfCostSolo;
+      owned_blocks(c.y + kPfStartSolo, n, kPfCostSolo, c.b0, c.b1, p.i0, p.i1);
+      c.y += own_cost(c.q.stok);
       ++c.h;
     }
     if (p.i0 < p.i1) return true;
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
   const int rb = min(a.B, t * chunk), re = min(a.B, rb + chunk);
   auto cost_of = [&](int r) -> int {
     const PfReq& q = a.req[r];
-    int c = kPfCostSolo * own_blocks(q.stok);
+    int c = own_cost(q.stok);
     if (q.ptiles > 0 && q.gfirst == r) c += prefix_shape(q.ptiles, q.gcount, a.G).head_cost;
     return c * a.Hkv;
   };
@@ -776,7 +780,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // Pieces are published as far ahead as the ring allows, queries staged as far as the two buffers do.
       PfCursor cur = begin_range(a, first);
       uint32_t n = 0, staged = 0, uses[2] = {0, 0};
-      int qbuf = 0;
+      int qbuf = 0, t0 = 0;
       bool more = true;
 #pragma unroll 1
       for (;;) {
@@ -791,6 +795,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (!more) p.i0 = p.i1 = 0;
           p.qbuf = qbuf;
           qbuf ^= 1;
+          p.t0 = t0;
+          if (!p.pair()) t0 ^= (p.i1 - p.i0) & 1;
           // the first blocks' pages: copies need not wait for the table, which may come from far
           const int tile = p.i0 * kPfBlkTiles + lane;
           const bool some = more && tile * kPfTile < p.tokens;
@@ -937,8 +943,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const uint32_t buf = j % C::kReady;
             if (j >= static_cast<uint32_t>(C::kReady)) wait(C::kBarUsed + buf, j / C::kReady - 1);
             uint8_t* const o = sm + C::kOffV16 + buf * C::kV16 + d * 16;
+            const int tiles = (nv + kPfTile - 1) / kPfTile;
 #pragma unroll 2
-            for (int t = 0; t < kPfBlkTiles; ++t) {
+            for (int t = 0; t < tiles; ++t) {
               // codes of dim d, tokens 16 t .. 16 t + 15, to two rows of 8 f16
               const uint4 x = *reinterpret_cast<const uint4*>(v + t * kPfTile * kPfDim + d * 16);
               uint32_t y[8];
@@ -952,7 +959,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
             if (nv < kPfBlk) {  // f16 of token k, dim d: rows of 8 tokens, 2 KiB apart
 #pragma unroll 1
-              for (int k = nv; k < kPfBlk; k = (k | 7) + 1)
+              for (int k = nv; k & 63; k = (k | 7) + 1)
                 for (uint8_t* e = o + (k >> 3) * 2048 + (k & 7) * 2; e < o + (k >> 3) * 2048 + 16; e += 2)
                   *reinterpret_cast<uint16_t*>(e) = 0;
             }
@@ -967,7 +974,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               // rows of 16 tokens with the 32-byte swizzle: the two 16-byte halves change places
               // in every other group of four rows
 #pragma unroll 1
-              for (int k = nv; k < kPfBlk; k = (k | 7) + 1) {
+              for (int k = nv; k & 63; k = (k | 7) + 1) {
                 uint8_t* const x = v + (k >> 4) * kPfTile * kPfDim * 2 + d * 32 + (((k >> 3) & 1) ^ ((d >> 2) & 1)) * 16;
                 for (uint8_t* e = x + (k & 7) * 2; e < x + 16; e += 2) *reinterpret_cast<uint16_t*>(e) = 0;
               }
@@ -993,10 +1000,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // V, 16 tokens a step: e4m3 as two columns of core matrices (8 dims x 8 tokens, 128 B apart along
       // the dims, 2 KiB along the tokens), bf16 as rows of 32 bytes with the 32-byte swizzle
       const uint64_t vdesc = kFp8 ? smem_desc(base + C::kOffV16, 2048, 128, 0) : smem_desc(base + C::kOffV, 16, 256, 6);
-      uint32_t ks = 0, kph = 0, vs = 0, vph = 0, n = 0, begun = 0, uses0 = 0, uses1 = 0, turns = 0;
+      uint32_t ks = 0, kph = 0, vs = 0, vph = 0, n0 = 0, n1 = 0, begun = 0, uses0 = 0, uses1 = 0, turns = 0;
       while (take_piece(p)) {
         const int pair_in = __any_sync(kFull, p.pair());
         const uint32_t nb = __reduce_max_sync(kFull, p.i1 - p.i0), qb = __reduce_max_sync(kFull, p.qbuf);
+        const uint32_t t0 = __reduce_max_sync(kFull, p.t0);
+        const uint32_t halves = __reduce_max_sync(kFull, (p.tokens - p.i0 * kPfBlk + 63) / 64);  // of the piece, and behind it
         if (pair_in || qb == 0) wait(C::kBarQ, uses0++);
         if (pair_in || qb == 1) wait(C::kBarQ + 1, uses1++);
         const uint64_t qd = qdesc + (pair_in ? t : qb) * (C::kQTile >> 4);
@@ -1008,17 +1017,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (pair && (t == 1 || i > 0)) wait(C::kBarTurn + t, turns++);
           if (i > 0) {
             wait(C::kBarReady + vs, vph);
-            if (pair || ((i - 1) & 1) == static_cast<uint32_t>(t)) {
+            if (pair || ((i - 1 + t0) & 1) == static_cast<uint32_t>(t)) {
               if (begins && begun > 0) wait(C::kBarOFree + t, begun - 1);  // O of the piece before has been read
               const uint64_t vd = vdesc + vs * ((kFp8 ? C::kV16 : C::kVStage) >> 4);
 #pragma unroll 1
-              for (int h = 0; h < 2; ++h) {
-                wait(C::kBarP + 2 * t + h, n);
+              for (int h = 0; h < 2 && 2 * (i - 1) + h < halves; ++h) {
+                wait(C::kBarP + 2 * t + h, h ? n1++ : n0++);
                 tc_fence_after();
                 issue_o(tm + 256 + t * 128, tm + t * 128 + 32 * h, vd + h * 1024, kFp8 ? kPfOF16 : kPfOBf16,
                         !begins || h > 0);
               }
-              ++n;
               begun += begins;
               begins = false;
               commit_elected(bars + 8 * (C::kBarO + t));
@@ -1030,7 +1038,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
           if (i < nb) {
             wait(C::kBarKFull + ks, kph);
-            if (pair || (i & 1) == static_cast<uint32_t>(t)) {
+            if (pair || ((i + t0) & 1) == static_cast<uint32_t>(t)) {
               tc_fence_after();
               issue_s<kFp8>(tm + t * 128, qd, kdesc + ks * (C::kKStage >> 4));
               commit_elected(bars + 8 * (C::kBarS + t));
@@ -1082,17 +1090,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         float m = -INFINITY, l = 0.f;
         bool any = false;
 #pragma unroll 1
-        for (int i = pair ? 0 : t; i < nb; i += pair ? 1 : 2) {
+        for (int i = pair ? 0 : t ^ p.t0; i < nb; i += pair ? 1 : 2) {
           wait(C::kBarS + t, ns);
           if (ns > 0) wait(C::kBarO + t, ns - 1);  // (over already: S came behind that product)
           tc_fence_after();
+          const int nv = p.tokens - (p.i0 + i) * kPfBlk, halves = nv > 64 ? 2 : 1;  // (a half without tokens is left out)
           if (busy) {
-            const int nv = p.tokens - (p.i0 + i) * kPfBlk;
             if (nv < kPfBlk) {
               // columns behind the last token: -inf, written to tensor memory by a short loop (selects
               // on registers would be a second copy of the code below, fetched anew for every tail)
 #pragma unroll 1
-              for (int k = nv; k < kPfBlk;) {
+              for (int k = nv; k & 63;) {
                 if (k & 7) {
                   tmem_fill1(ts + k, -INFINITY);
                   ++k;
@@ -1108,7 +1116,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
             float s[64], mx = -INFINITY;
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < halves; ++h) {
               tmem_ld64(ts + 64 * h, s);
               float m4[4] = {max3(mx, s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
 #pragma unroll
@@ -1139,7 +1147,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const float2 mult2 = make_float2(mult, mult), ref2 = make_float2(-ref, -ref);
             float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < halves; ++h) {
               tmem_ld64(ts + 64 * h, s);
               uint32_t w[32];
 #pragma unroll
@@ -1162,7 +1170,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(bar(C::kBarP + 2 * t));
-              mbar_arrive(bar(C::kBarP + 2 * t + 1));
+              if (halves == 2) mbar_arrive(bar(C::kBarP + 2 * t + 1));
             }
           }
           any = true;
@@ -1181,13 +1189,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const float vscale = kFp8 ? __ldg(a.v_scale) : 1.f;
             float* const dst = a.part_o + slot * kPfDim;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              float o[32];
-              tmem_ld32(to + 32 * c, o);
+            for (int c = 0; c < 2; ++c) {
+              float o[64];
+              tmem_ld64(to + 64 * c, o);
               if (valid) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  *reinterpret_cast<float4*>(dst + 32 * c + 4 * k) =
+                for (int k = 0; k < 16; ++k)
+                  *reinterpret_cast<float4*>(dst + 64 * c + 4 * k) =
                       make_float4(o[4 * k] * vscale, o[4 * k + 1] * vscale, o[4 * k + 2] * vscale, o[4 * k + 3] * vscale);
               }
             }
@@ -1240,7 +1248,7 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
       blocks = s.blocks;
       w = u == s.units - 1 ? s.wlast : kPfCostPair;
       lrow = i % kPfUnitRows;
-      y = gy + h * s.head_cost + u * kPfCostPair * blocks;
+      y = gy + h * s.head_cost + u * s.step + start_cost(w);
       if (q.gfirst == r) own_y += s.head_cost * a.Hkv;
     }
 #pragma unroll 1
@@ -1249,7 +1257,7 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
         blocks = nb;
         w = kPfCostSolo;
         lrow = g;
-        y = own_y + h * nb * kPfCostSolo;
+        y = own_y + h * own_cost(q.stok) + kPfStartSolo;
       }
       if (blocks == 0) continue;
       const int subs = w == kPfCostPair ? 0 : 1;  // log2 of the row tiles with a partial each
@@ -1402,8 +1410,9 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   // tile numbers are 32-bit tensor-map coordinates; rows and the work list's length (at most a prefix
   // unit and an own unit of the table's width per request and kv head) are counted in 31 bits
   const int64_t width = (static_cast<int64_t>(max_pages) * page_size + kPfBlk - 1) / kPfBlk;
-  if (tiles > 0x7fffffff || static_cast<int64_t>(B) * Hq > 0x7fffffff / 4 ||
-      width > (int64_t(1) << 24) || width * B > (int64_t(1) << 31) / ((kPfCostPair + kPfCostSolo) * Hkv))
+  const int64_t longest = width * (kPfCostPair + kPfCostSolo) + kPfStartPair + kPfStartSolo;
+  if (tiles > 0x7fffffff || static_cast<int64_t>(B) * Hq > 0x7fffffff / 4 || width > (int64_t(1) << 24) ||
+      longest > 0x7fffffff / (static_cast<int64_t>(B > 0 ? B : 1) * Hkv))
     return FPK_EUNSUPPORTED;
   if (B == 0) return FPK_OK;
   if (!q || !kv_pool || !page_table || !seq_lens || !out || !workspace) return FPK_EINVAL;

@@ -6,14 +6,23 @@ import random
 
 import pytest
 
-PAIR, SOLO, ROWS, BLK = 2, 1, 256, 8
+PAIR, SOLO, START_PAIR, START_SOLO, ROWS, BLK = 6, 2, 12, 5, 256, 8
 
 
 def prefix_shape(ptiles, gcount, G):
     rows = gcount * G
     blocks, units = -(-ptiles // BLK), -(-rows // ROWS)
     wlast = PAIR if rows - (units - 1) * ROWS > 128 else SOLO
-    return blocks, units, wlast, blocks * (PAIR * (units - 1) + wlast)
+    step = START_PAIR + PAIR * blocks
+    return blocks, units, wlast, step, step * (units - 1) + start_cost(wlast) + wlast * blocks
+
+
+def start_cost(w):
+    return START_PAIR if w == PAIR else START_SOLO
+
+
+def own_cost(stok):
+    return START_SOLO + SOLO * own_blocks(stok) if stok > 0 else 0
 
 
 def own_blocks(stok):
@@ -41,9 +50,9 @@ def plan(groups, G, Hkv, ctas):
     for ptiles, own in groups:
         first = len(reqs)
         for i, stok in enumerate(own):
-            cost = SOLO * own_blocks(stok)
+            cost = own_cost(stok)
             if ptiles and i == 0:
-                cost += prefix_shape(ptiles, len(own), G)[3]
+                cost += prefix_shape(ptiles, len(own), G)[4]
             reqs.append((y, ptiles, stok, first, len(own)))
             y += cost * Hkv
     T = y
@@ -67,29 +76,29 @@ def pieces(reqs, T, start, G, Hkv, ctas, c):
     assert at >= 0
     skip_own = True
     if u == 0:
-        blocks, units, wlast, head = prefix_shape(reqs[r][1], reqs[r][4], G)
+        blocks, units, wlast, step, head = prefix_shape(reqs[r][1], reqs[r][4], G)
         if at < head * Hkv:
             h = at // head
-            u = min(at % head // (PAIR * blocks), units - 1)
-            y += h * head + u * PAIR * blocks
+            u = min(at % head // step, units - 1)
+            y += h * head + u * step
             skip_own = False
         else:
             u, y, at = -1, y + head * Hkv, at - head * Hkv
     if skip_own:
-        cost = SOLO * own_blocks(reqs[r][2])
+        cost = own_cost(reqs[r][2])
         if cost:
             h = min(at // cost, Hkv)
             y += h * cost
     while y < b1:
         y0, ptiles, stok, gfirst, gcount = reqs[r]
         if u >= 0:
-            blocks, units, wlast, head = prefix_shape(ptiles, gcount, G)
+            blocks, units, wlast, step, head = prefix_shape(ptiles, gcount, G)
             w = wlast if u == units - 1 else PAIR
-            i0, i1 = owned(y, blocks, w, b0, b1)
+            i0, i1 = owned(y + start_cost(w), blocks, w, b0, b1)
             unit = ("prefix", gfirst, h, u)
             pair = min(ROWS, gcount * G - u * ROWS) > 128
             assert pair == (w == PAIR)
-            y += blocks * w
+            y += start_cost(w) + blocks * w
             u += 1
             if u == units:
                 u, h = 0, h + 1
@@ -103,9 +112,9 @@ def pieces(reqs, T, start, G, Hkv, ctas, c):
                     return
                 h, u, y = enter(r)
                 continue
-            i0, i1 = owned(y, n, SOLO, b0, b1)
+            i0, i1 = owned(y + START_SOLO, n, SOLO, b0, b1)
             unit, pair = ("own", r, h, 0), False
-            y += n * SOLO
+            y += own_cost(stok)
             h += 1
         if i0 < i1:
             yield unit, i0, i1, pair
@@ -124,17 +133,17 @@ def merge(reqs, T, G, Hkv, ctas, r, h, g):
                     yield name, ("start" if i0 == 0 else c), sub
 
     if ptiles:
-        blocks, units, wlast, head = prefix_shape(ptiles, gcount, G)
+        blocks, units, wlast, step, head = prefix_shape(ptiles, gcount, G)
         i = (r - gfirst) * G + g
         u = i // ROWS
         w = wlast if u == units - 1 else PAIR
-        yield from unit(reqs[gfirst][0] + h * head + u * PAIR * blocks, blocks, w, ("prefix", gfirst, h, u),
+        yield from unit(reqs[gfirst][0] + h * head + u * step + start_cost(w), blocks, w, ("prefix", gfirst, h, u),
                         1 if w == PAIR else 2)
         if gfirst == r:
             own += head * Hkv
     n = own_blocks(stok)
     if n:
-        yield from unit(own + h * n * SOLO, n, SOLO, ("own", r, h, 0), 2)
+        yield from unit(own + h * own_cost(stok) + START_SOLO, n, SOLO, ("own", r, h, 0), 2)
 
 
 @pytest.mark.parametrize("seed", range(60))

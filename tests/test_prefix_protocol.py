@@ -26,7 +26,7 @@ class Bar:
 
 
 def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
-    """pieces: [(prefix, pair, blocks)]; slow: a warp that hardly ever gets its turn"""
+    """pieces: [(prefix, pair, blocks, halves of the last block)]; slow: a warp that hardly ever gets its turn"""
     rng = random.Random(seed)
     kst, ready_n = (KST, V16) if fp8 else (2, VST)
     B = dict(kfull=[Bar(1) for _ in range(kst)], kfree=[Bar(2) for _ in range(kst)],
@@ -61,7 +61,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
 
     def plan():
         n = staged = 0
-        uses, qbuf, more = [0, 0], 0, True
+        uses, qbuf, tile, more = [0, 0], 0, 0, True
         while True:
             while more and n - staged < pieces_ring:
                 if n >= pieces_ring:
@@ -71,13 +71,15 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
                     elif not B["piecefree"][n % pieces_ring].done(ph):
                         break
                 more = n < nb
-                slots[n % pieces_ring] = (n, qbuf) + (pieces[n] if more else (0, 0, 0))
+                slots[n % pieces_ring] = (n, qbuf, tile) + (pieces[n] if more else (0, 0, 0, 0))
                 qbuf ^= 1
+                if more and not pieces[n][1]:
+                    tile ^= pieces[n][2] & 1
                 yield
                 B["piece"][n % pieces_ring].arrive()
                 n += 1
                 yield
-            k, qb, prefix, pair, blocks = slots[staged % pieces_ring]
+            k, qb, t0, prefix, pair, blocks, tail = slots[staged % pieces_ring]
             assert k == staged
             staged += 1
             if not blocks:
@@ -97,7 +99,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
     def loader(full, free, stages, hold, name):
         j = pn = 0
         while True:
-            k, qb, prefix, pair, blocks = yield from take(pn)
+            k, qb, t0, prefix, pair, blocks, tail = yield from take(pn)
             pn += 1
             if not blocks:
                 return
@@ -116,7 +118,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
     def vwarp():
         j = pn = 0
         while True:
-            k, qb, prefix, pair, blocks = yield from take(pn)
+            k, qb, t0, prefix, pair, blocks, tail = yield from take(pn)
             pn += 1
             if not blocks:
                 return
@@ -139,11 +141,12 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
                 yield
 
     def mma(t):
-        ks = kr = vs = vr = n = begun = turns = pn = 0
+        ks = kr = vs = vr = begun = turns = pn = 0
+        n = [0, 0]
         uses = [0, 0]
         q = ("mma", t)
         while True:
-            k, qb, prefix, pair, blocks = yield from take(pn)
+            k, qb, t0, prefix, pair, blocks, tail = yield from take(pn)
             pn += 1
             if not blocks:
                 return
@@ -161,12 +164,12 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
                     yield from wait(B["ready"][vs], vr)
                     assert cof[vs] == (k, i - 1), "converted block"
                     freed = (B["used"] if fp8 else B["vfree"])[vs]
-                    if pair or (i - 1) % 2 == t:
+                    if pair or (i - 1 + t0) % 2 == t:
                         if begins and begun > 0:
                             yield from wait(B["ofree"][t], begun - 1)
-                        for h in (0, 1):
-                            yield from wait(B["P"][t][h], n)
-                        n += 1
+                        for h in range(tail if i == blocks else 2):
+                            yield from wait(B["P"][t][h], n[h])
+                            n[h] += 1
                         begun += begins
                         begins = False
 
@@ -184,7 +187,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
                 if i < blocks:
                     yield from wait(B["kfull"][ks], kr)
                     assert kof[ks] == (k, i), "K block"
-                    if pair or i % 2 == t:
+                    if pair or (i + t0) % 2 == t:
                         def s(at=(k, i), ks=ks, b=mine_buf):
                             assert kof[ks] == at and qof[b] == at[0], "operands of S"
                             sof[t] = at
@@ -205,7 +208,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
         ns = pn = 0
         uses = [0, 0]
         while True:
-            k, qb, prefix, pair, blocks = yield from take(pn)
+            k, qb, t0, prefix, pair, blocks, tail = yield from take(pn)
             pn += 1
             if not blocks:
                 return
@@ -224,12 +227,12 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
                     uses[x] += 1
             B["qfree"][b].arrive(2 if pair else 1)
             some = False
-            for i in range(0 if pair else t, blocks, 1 if pair else 2):
+            for i in range(0 if pair else t ^ t0, blocks, 1 if pair else 2):
                 yield from wait(B["S"][t], ns)
                 if ns > 0:
                     yield from wait(B["O"][t], ns - 1)
                 assert sof[t] == (k, i), "S"
-                for h in (0, 1):
+                for h in range(tail if i == blocks - 1 else 2):
                     yield
                     B["P"][t][h].arrive()
                 ns += 1
@@ -296,4 +299,5 @@ def test_every_run_ends(fp8, kind):
             for _ in range(many):
                 prefix = rng.randint(0, 1)
                 pieces.append((prefix, prefix and rng.randint(0, 1), rng.choice([1, 1, 2, 3, 4])))
+        pieces = [x + (rng.randint(1, 2),) for x in pieces]
         simulate(pieces, fp8, seed, slow=seed - 1)  # each warp held back in turn
