@@ -105,8 +105,8 @@ struct PfCfg {
   static constexpr int kQTile = 128 * 256;                     // parts (or halves) of a tile's queries
   static constexpr int kKStage = kPfBlk * kPfDim * kElem;
   static constexpr int kVStage = kKStage;
-  static constexpr int kKStages = kFp8 ? 3 : 2;
-  static constexpr int kVStages = 3;
+  static constexpr int kKStages = kFp8 ? 4 : 2;
+  static constexpr int kVStages = kFp8 ? 2 : 3;
   static constexpr int kV16 = kPfBlk * kPfDim * 2;             // converted V block
   static constexpr int kV16Bufs = kFp8 ? 2 : 0;
   static constexpr int kOffK = 2 * kQTile;
@@ -208,7 +208,7 @@ struct alignas(16) PfPiece {
   int tile0;       // table tile of the unit's first token
   int tokens;      // of the unit
   int qbuf;        // query buffer of a unit of one row tile
-  int t0;          // tile of the first block of such a unit; the others take turns
+  int t0;          // parity of the blocks before, and tile of the first one of a unit of one row tile
   __device__ __forceinline__ bool pair() const { return rows > 128; }
 };
 struct alignas(16) PfSlot {
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           p.qbuf = qbuf;
           qbuf ^= 1;
           p.t0 = t0;
-          if (!p.pair()) t0 ^= (p.i1 - p.i0) & 1;
+          t0 ^= (p.i1 - p.i0) & 1;
           // the first blocks' pages: copies need not wait for the table, which may come from far
           const int tile = p.i0 * kPfBlkTiles + lane;
           const bool some = more && tile * kPfTile < p.tokens;
@@ -991,8 +991,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // same block in halves as the softmax hands P over, S of the next (which overwrites S and P: the
       // products of one thread run in order).  While a tile's softmax runs the other tile has the tensor
       // cores; on a unit of both tiles the warps take turns (PV and the next S), or else the two would run
-      // in step, their softmaxes too, and leave the tensor cores idle.  Both warps see and free every
-      // block, the other tile's too: a barrier's parity tells neighbouring phases apart, no others.
+      // in step, their softmaxes too, and leave the tensor cores idle.
+      //
+      // On a unit of one row tile block j belongs to tile j mod 2.  A barrier's parity tells neighbouring
+      // phases apart, no others, so a warp has to see every phase of a barrier it waits for: where the
+      // number of slots is even, a tile has its own slots and sees all of theirs; bf16 V has three slots,
+      // and both warps see and free every block.  (A unit of both tiles begins when all blocks before
+      // it are over: its queries are staged by the softmax warps of both.)
       const int t = warp - kPfMmaWarp;
       const uint32_t base = __reduce_max_sync(kFull, sbase), tm = __reduce_max_sync(kFull, tmem);  // uniform registers
       const uint32_t bars = base + C::kOffBars;
@@ -1000,56 +1005,72 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // V, 16 tokens a step: e4m3 as two columns of core matrices (8 dims x 8 tokens, 128 B apart along
       // the dims, 2 KiB along the tokens), bf16 as rows of 32 bytes with the 32-byte swizzle
       const uint64_t vdesc = kFp8 ? smem_desc(base + C::kOffV16, 2048, 128, 0) : smem_desc(base + C::kOffV, 16, 256, 6);
-      uint32_t ks = 0, kph = 0, vs = 0, vph = 0, n0 = 0, n1 = 0, begun = 0, uses0 = 0, uses1 = 0, turns = 0;
+      uint32_t j0 = 0, v3 = 0, v3ph = 0, n0 = 0, n1 = 0, begun = 0, uses0 = 0, uses1 = 0, turns = 0;
+      static_assert(C::kKStages % 2 == 0 && (!kFp8 || C::kReady == 2), "slots that tiles own");
       while (take_piece(p)) {
         const int pair_in = __any_sync(kFull, p.pair());
         const uint32_t nb = __reduce_max_sync(kFull, p.i1 - p.i0), qb = __reduce_max_sync(kFull, p.qbuf);
-        const uint32_t t0 = __reduce_max_sync(kFull, p.t0);
         const uint32_t halves = __reduce_max_sync(kFull, (p.tokens - p.i0 * kPfBlk + 63) / 64);  // of the piece, and behind it
+        const uint32_t step = pair_in ? 1 : 2;
         if (pair_in || qb == 0) wait(C::kBarQ, uses0++);
         if (pair_in || qb == 1) wait(C::kBarQ + 1, uses1++);
         const uint64_t qd = qdesc + (pair_in ? t : qb) * (C::kQTile >> 4);
         bool begins = true;
+        uint32_t passed = 0;  // bf16: V blocks seen
+        // the other tile's bf16 V blocks up to block m
+        auto pass_v = [&](uint32_t m) {
+          if (kFp8) return;
 #pragma unroll 1
-        for (uint32_t i = 0; i <= nb; ++i) {
-          // PV of block i - 1, S of block i
+          for (; passed < m; ++passed) {
+            wait(C::kBarReady + v3, v3ph);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kBarVFree + v3));
+            if (++v3 == C::kReady) v3 = 0, v3ph ^= 1;
+          }
+        };
+#pragma unroll 1
+        for (uint32_t i = pair_in ? 0 : (j0 ^ t) & 1; i < nb + step; i += step) {
+          // PV of this tile's block before, S of block i
           const bool pair = varying(pair_in) != 0;
           if (pair && (t == 1 || i > 0)) wait(C::kBarTurn + t, turns++);
-          if (i > 0) {
-            wait(C::kBarReady + vs, vph);
-            if (pair || ((i - 1 + t0) & 1) == static_cast<uint32_t>(t)) {
-              if (begins && begun > 0) wait(C::kBarOFree + t, begun - 1);  // O of the piece before has been read
-              const uint64_t vd = vdesc + vs * ((kFp8 ? C::kV16 : C::kVStage) >> 4);
+          if (i >= step) {
+            const uint32_t m = i - step, jm = j0 + m;
+            pass_v(m);
+            const uint32_t vs = kFp8 ? jm % C::kReady : v3;
+            wait(C::kBarReady + vs, kFp8 ? jm / C::kReady : v3ph);
+            if (begins && begun > 0) wait(C::kBarOFree + t, begun - 1);  // O of the piece before has been read
+            const uint64_t vd = vdesc + vs * ((kFp8 ? C::kV16 : C::kVStage) >> 4);
 #pragma unroll 1
-              for (int h = 0; h < 2 && 2 * (i - 1) + h < halves; ++h) {
-                wait(C::kBarP + 2 * t + h, h ? n1++ : n0++);
-                tc_fence_after();
-                issue_o(tm + 256 + t * 128, tm + t * 128 + 32 * h, vd + h * 1024, kFp8 ? kPfOF16 : kPfOBf16,
-                        !begins || h > 0);
-              }
-              begun += begins;
-              begins = false;
-              commit_elected(bars + 8 * (C::kBarO + t));
-              commit_elected(bars + 8 * ((kFp8 ? C::kBarUsed : C::kBarVFree) + vs));
-            } else if (lane == 0) {
-              mbar_arrive(bar((kFp8 ? C::kBarUsed : C::kBarVFree) + vs));
+            for (int h = 0; h < 2 && 2 * m + h < halves; ++h) {
+              wait(C::kBarP + 2 * t + h, h ? n1++ : n0++);
+              tc_fence_after();
+              issue_o(tm + 256 + t * 128, tm + t * 128 + 32 * h, vd + h * 1024, kFp8 ? kPfOF16 : kPfOBf16,
+                      !begins || h > 0);
             }
-            if (++vs == C::kReady) vs = 0, vph ^= 1;
+            begun += begins;
+            begins = false;
+            commit_elected(bars + 8 * (C::kBarO + t));
+            const uint32_t bv = bars + 8 * ((kFp8 ? C::kBarUsed : C::kBarVFree) + vs);
+            commit_elected(bv);
+            if (kFp8 && !pair) commit_elected(bv);  // for the other tile too
+            if (!kFp8) {
+              ++passed;
+              if (++v3 == C::kReady) v3 = 0, v3ph ^= 1;
+            }
           }
           if (i < nb) {
-            wait(C::kBarKFull + ks, kph);
-            if (pair || ((i + t0) & 1) == static_cast<uint32_t>(t)) {
-              tc_fence_after();
-              issue_s<kFp8>(tm + t * 128, qd, kdesc + ks * (C::kKStage >> 4));
-              commit_elected(bars + 8 * (C::kBarS + t));
-              commit_elected(bars + 8 * (C::kBarKFree + ks));
-            } else if (lane == 0) {
-              mbar_arrive(bar(C::kBarKFree + ks));
-            }
-            if (++ks == C::kKStages) ks = 0, kph ^= 1;
+            const uint32_t ks = (j0 + i) % C::kKStages;
+            wait(C::kBarKFull + ks, (j0 + i) / C::kKStages);
+            tc_fence_after();
+            issue_s<kFp8>(tm + t * 128, qd, kdesc + ks * (C::kKStage >> 4));
+            commit_elected(bars + 8 * (C::kBarS + t));
+            commit_elected(bars + 8 * (C::kBarKFree + ks));
+            if (!pair) commit_elected(bars + 8 * (C::kBarKFree + ks));
           }
           if (pair && lane == 0 && (t == 0 || i < nb)) mbar_arrive(bar(C::kBarTurn + (t ^ 1)));
         }
+        pass_v(nb);
+        j0 += nb;
         // the queries: both warps' S of a buffer are done
 #pragma unroll 1
         for (int k = 0; k <= pair_in; ++k) commit_elected(bars + 8 * (C::kBarQFree + (pair_in ? t : qb)));

@@ -7,7 +7,7 @@ import random
 
 import pytest
 
-KST, VST, V16, PIECES = 3, 3, 2, 4
+PIECES = 4
 
 
 class Bar:
@@ -28,7 +28,8 @@ class Bar:
 def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
     """pieces: [(prefix, pair, blocks, halves of the last block)]; slow: a warp that hardly ever gets its turn"""
     rng = random.Random(seed)
-    kst, ready_n = (KST, V16) if fp8 else (2, VST)
+    KST, VST, V16 = (4, 2, 2) if fp8 else (2, 3, 0)
+    kst, ready_n = KST, V16 if fp8 else VST
     B = dict(kfull=[Bar(1) for _ in range(kst)], kfree=[Bar(2) for _ in range(kst)],
              vfull=[Bar(1) for _ in range(VST)], vfree=[Bar(4 if fp8 else 2) for _ in range(VST)],
              ready=[Bar(4) for _ in range(ready_n)], used=[Bar(2) for _ in range(V16)],
@@ -73,7 +74,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
                 more = n < nb
                 slots[n % pieces_ring] = (n, qbuf, tile) + (pieces[n] if more else (0, 0, 0, 0))
                 qbuf ^= 1
-                if more and not pieces[n][1]:
+                if more:
                     tile ^= pieces[n][2] & 1
                 yield
                 B["piece"][n % pieces_ring].arrive()
@@ -141,7 +142,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
                 yield
 
     def mma(t):
-        ks = kr = vs = vr = begun = turns = pn = 0
+        j0 = v3 = v3r = begun = turns = pn = 0
         n = [0, 0]
         uses = [0, 0]
         q = ("mma", t)
@@ -150,58 +151,73 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
             pn += 1
             if not blocks:
                 return
+            assert t0 == j0 % 2
             for b in (0, 1):
                 if pair or qb == b:
                     yield from wait(B["Q"][b], uses[b])
                     uses[b] += 1
             mine_buf = t if pair else qb
-            begins = True
-            for i in range(blocks + 1):
+            begins, step, passed = True, 1 if pair else 2, 0
+
+            def pass_v(m):
+                nonlocal passed, v3, v3r
+                while not fp8 and passed < m:
+                    yield from wait(B["ready"][v3], v3r)
+                    assert cof[v3] == (k, passed), "V block passed"
+                    yield
+                    B["vfree"][v3].arrive()
+                    passed += 1
+                    v3 += 1
+                    if v3 == VST:
+                        v3, v3r = 0, v3r + 1
+
+            i = 0 if pair else (j0 ^ t) & 1
+            while i < blocks + step:
                 if pair and (t == 1 or i > 0):
                     yield from wait(B["turn"][t], turns)
                     turns += 1
-                if i > 0:
+                if i >= step:
+                    m = i - step
+                    yield from pass_v(m)
+                    vs, vr = ((j0 + m) % V16, (j0 + m) // V16) if fp8 else (v3, v3r)
                     yield from wait(B["ready"][vs], vr)
-                    assert cof[vs] == (k, i - 1), "converted block"
-                    freed = (B["used"] if fp8 else B["vfree"])[vs]
-                    if pair or (i - 1 + t0) % 2 == t:
-                        if begins and begun > 0:
-                            yield from wait(B["ofree"][t], begun - 1)
-                        for h in range(tail if i == blocks else 2):
-                            yield from wait(B["P"][t][h], n[h])
-                            n[h] += 1
-                        begun += begins
-                        begins = False
+                    assert cof[vs] == (k, m), "converted block"
+                    if begins and begun > 0:
+                        yield from wait(B["ofree"][t], begun - 1)
+                    for h in range(tail if m == blocks - 1 else 2):
+                        yield from wait(B["P"][t][h], n[h])
+                        n[h] += 1
+                    begun += begins
+                    begins = False
 
-                        def pv(at=(k, i - 1), vs=vs, freed=freed):
-                            assert cof[vs] == at, "V under a product"
-                            oof[t] = at
-                            B["O"][t].arrive()
-                            freed.arrive()
-                        later(q, pv)
-                    else:
-                        freed.arrive()
-                    vs += 1
-                    if vs == ready_n:
-                        vs, vr = 0, vr + 1
+                    def pv(at=(k, m), vs=vs, freed=(B["used"] if fp8 else B["vfree"])[vs], c=2 if fp8 and not pair else 1):
+                        assert cof[vs] == at, "V under a product"
+                        oof[t] = at
+                        B["O"][t].arrive()
+                        freed.arrive(c)
+                    later(q, pv)
+                    if not fp8:
+                        passed += 1
+                        v3 += 1
+                        if v3 == VST:
+                            v3, v3r = 0, v3r + 1
                 if i < blocks:
-                    yield from wait(B["kfull"][ks], kr)
+                    ks = (j0 + i) % kst
+                    yield from wait(B["kfull"][ks], (j0 + i) // kst)
                     assert kof[ks] == (k, i), "K block"
-                    if pair or (i + t0) % 2 == t:
-                        def s(at=(k, i), ks=ks, b=mine_buf):
-                            assert kof[ks] == at and qof[b] == at[0], "operands of S"
-                            sof[t] = at
-                            B["S"][t].arrive()
-                            B["kfree"][ks].arrive()
-                        later(q, s)
-                    else:
-                        B["kfree"][ks].arrive()
-                    ks += 1
-                    if ks == kst:
-                        ks, kr = 0, kr + 1
+
+                    def s(at=(k, i), ks=ks, b=mine_buf, c=1 if pair else 2):
+                        assert kof[ks] == at and qof[b] == at[0], "operands of S"
+                        sof[t] = at
+                        B["S"][t].arrive()
+                        B["kfree"][ks].arrive(c)
+                    later(q, s)
                 if pair and (t == 0 or i < blocks):
                     B["turn"][t ^ 1].arrive()
                 yield
+                i += step
+            yield from pass_v(blocks)
+            j0 += blocks
             later(q, lambda b=mine_buf, c=2 if pair else 1: B["qfree"][b].arrive(c))
 
     def softmax(t):
