@@ -3,25 +3,28 @@
 //
 // A group's shared prefix is a matrix product: the rows are the queries of all
 // its requests that read one kv head (requests x GQA group), the columns the
-// prefix's tokens.  What a request has of its own is the same product with the
-// few rows of its GQA group.  Both are units of one work list:
+// prefix's tokens.  What a request has of its own is decode attention as ever
+// (paged_decode_split_kernel, over the tables behind the shared pages): it is
+// bound by HBM, and that kernel keeps twice as many bytes in flight as fit
+// beside the products here.  Four launches: a plan, the own parts, the
+// prefixes, and a merge of each row's partials by log-sum-exp.
 //
-// * prefix unit: (group, kv head, up to 256 query rows) over the shared pages;
-//   own unit: (request, kv head), its G rows over its own pages.
+// * Unit: (group, kv head, up to 256 query rows) over the group's shared pages.
 // * Units are laid end to end in cost (blocks of 128 tokens, dearer for units of
-//   more than 128 rows) and the line is cut into one equal range per CTA; a CTA
-//   runs a piece of a unit after another.  Every piece writes its partial
-//   (m, l, O); a second kernel merges a row's partials by log-sum-exp in a fixed
-//   order, so repeated calls give the same bits.  A planning kernel of one CTA
-//   finds the groups' shared pages and every CTA's first unit.
+//   more than 128 rows, and a start) and the line is cut into one equal range per
+//   CTA; a CTA runs a piece of a unit after another.  Every piece writes its partial
+//   (m, l, O); the merge takes a row's partials in a fixed order, so repeated calls
+//   give the same bits.
 //
 // Piece pipeline (one CTA per SM, 16 warps), per block of 128 tokens:
+//   warp 15     finds the pieces ahead of the others
 //   warp 12     lands K rows (128-byte swizzle) and V tiles by tensor maps
 //   warps 8-11  e4m3 cache: V codes to f16 core matrices (exact), so that softmax
 //               weights enter the second product in f16; both caches: zeroes
-//               where no token lies (an unwritten slot may hold NaN, and 0 NaN = NaN)
-//   warp 13     issues S = Q K^T and O += P V (tcgen05.mma, M = N = 128)
-//   warps 0-3, 4-7: softmax of row tile 0 and 1, a thread per row: no shuffles,
+//               where no token lies (stale shared memory may hold NaN, and 0 NaN = NaN)
+//   warps 13, 14  issue S = Q K^T and O += P V (tcgen05.mma, M = N = 128) of row
+//               tile 0 and 1
+//   warps 0-3, 4-7  softmax of row tile 0 and 1, a thread per row: no shuffles,
 //               the row's maximum, sum and rescale are the thread's own.  P
 //               replaces S in tensor memory as the A operand of the second product.
 // Units of more than 128 rows use both tiles on every block; smaller ones give
@@ -36,6 +39,7 @@
 // 2^8 since the last time: weights are then at most 2^8, far inside f16.
 #include <atomic>
 
+#include "own_attn.cuh"
 #include "tcgen05.cuh"
 
 namespace fpk {
@@ -64,15 +68,14 @@ constexpr int kPfPieces = 4, kPfPieceBytes = 176;  // pieces known ahead
 constexpr int kPfPlanThreads = 1024;
 constexpr int kPfMergeWarps = 4;
 
-// What the planning kernel finds of each request.
-struct alignas(16) PfReq {
-  int32_t y0;      // place of its units in the work list (the group's prefix units first, at its first request)
+// What the planning kernel finds of each group.
+struct alignas(16) PfGroup {
+  int32_t y0;      // place of its units in the work list
   int32_t ptiles;  // tiles of the shared prefix
-  int32_t stok;    // tokens behind it; 0 for a dead request
-  int32_t gfirst, gcount, leader;
-  int32_t r, b0, b1;  // (of a CTA's first request: its number, the CTA's range)
-  int32_t pad[3];
+  int32_t first, count, leader;
+  int32_t g, b0, b1;  // (of a CTA's first group: its number, the CTA's range)
 };
+static_assert(sizeof(PfGroup) == 32, "two 16-byte words");
 
 struct PfArgs {
   const uint16_t* q;
@@ -86,14 +89,19 @@ struct PfArgs {
   uint16_t* out;
   float* lse;
   uint32_t* status;
-  int32_t* total;    // length of the work list (the host has made sure that it fits)
-  PfReq* start;      // [ctas] the request in whose units a CTA's range begins: its record, number and the CTA's range
   int32_t* gstart;   // [n_groups + 1] group starts, clamped and non-decreasing
+  PfGroup* group;    // [n_groups]
+  PfGroup* start;    // [ctas] the group in whose units a CTA's range begins: its record, number and the CTA's range
+  int32_t* group_of; // [B], -1: none
+  int32_t* own_len;  // [B] tokens behind the shared prefix; 0 for a dead request
+  int32_t* skip;     // [B] pages of the shared prefix
   int32_t* dead;     // [B]
-  PfReq* req;        // [B]
-  float2* part_ml;   // partials: 4 per (request, query head), then 256 rows per CTA
+  uint4* counters;   // of the own parts' attention, to be zeroed
+  const float* own_out;  // [B][Hq][D], [B][Hq]: attention over the own tokens
+  const float* own_lse;
+  float2* part_ml;   // partials: 2 per (request, query head), then 256 rows per CTA
   float* part_o;
-  int n_groups, B, Hq, Hkv, G, page_size, num_pages, max_pages, ctas, zbox;
+  int n_groups, B, Hq, Hkv, G, page_size, num_pages, max_pages, ctas, zbox, n_counters;
   uint32_t by_g, by_tpp;  // ceil(2^32 / G), ceil(2^32 / tiles of a page); 0 for 1
   float sm_scale_log2;
 };
@@ -172,8 +180,6 @@ __device__ __forceinline__ PfPrefix prefix_shape(int ptiles, int gcount, int G) 
   p.head_cost = p.step * (p.units - 1) + start_cost(p.wlast) + p.wlast * p.blocks;
   return p;
 }
-__device__ __forceinline__ int own_blocks(int stok) { return stok > 0 ? (stok - 1) / kPfBlk + 1 : 0; }
-__device__ __forceinline__ int own_cost(int stok) { return stok > 0 ? kPfStartSolo + kPfCostSolo * own_blocks(stok) : 0; }
 
 // CTA c owns the blocks that start in [begin(c), begin(c + 1)): T / n each, one
 // more for the first T mod n CTAs.
@@ -199,16 +205,15 @@ __device__ __forceinline__ void owned_blocks(int y, int n, int w, int b0, int b1
 }
 
 struct alignas(16) PfPiece {
-  int prefix;
-  int r;           // request whose table is read (prefix: the leader)
+  int r;           // request whose table is read: the leader
   int h;
-  int row0, rows;  // prefix: rows of the group; own: rows [0, G)
+  int row0, rows;  // rows of the group
   int gfirst;      // request of row 0
   int i0, i1;      // blocks of the unit; none: the end
-  int tile0;       // table tile of the unit's first token
   int tokens;      // of the unit
   int qbuf;        // query buffer of a unit of one row tile
   int t0;          // parity of the blocks before, and tile of the first one of a unit of one row tile
+  int pad[2];
   __device__ __forceinline__ bool pair() const { return rows > 128; }
 };
 struct alignas(16) PfSlot {
@@ -218,113 +223,70 @@ struct alignas(16) PfSlot {
 static_assert(sizeof(PfSlot) == kPfPieceBytes, "slot of the piece ring");
 
 struct PfCursor {
-  PfReq q;
-  int r, h, u;  // u: prefix unit of the head, -1 in a request's own units
+  PfGroup q;
+  int g, h, u;  // u: unit of the head
   int y, b0, b1;
 };
 
-static_assert(sizeof(PfReq) == 48, "three 16-byte words");
-__device__ __forceinline__ PfReq load_req(const PfReq* at) {
+__device__ __forceinline__ PfGroup load_group(const PfGroup* at) {
   const int4* p = reinterpret_cast<const int4*>(at);
-  const int4 x = __ldcg(p), y = __ldcg(p + 1), z = __ldcg(p + 2);
-  PfReq q;
+  const int4 x = __ldcg(p), y = __ldcg(p + 1);
+  PfGroup q;
   q.y0 = x.x;
   q.ptiles = x.y;
-  q.stok = x.z;
-  q.gfirst = x.w;
-  q.gcount = y.x;
-  q.leader = y.y;
-  q.r = y.z;
-  q.b0 = y.w;
-  q.b1 = z.x;
+  q.first = x.z;
+  q.count = x.w;
+  q.leader = y.x;
+  q.g = y.y;
+  q.b0 = y.z;
+  q.b1 = y.w;
   return q;
 }
 
-__device__ __forceinline__ void enter_request(PfCursor& c, int r, const PfReq& q) {
-  c.q = q;
-  c.r = r;
-  c.h = 0;
-  c.u = c.q.ptiles > 0 && c.q.gfirst == c.r ? 0 : -1;
-  c.y = c.q.y0;
-}
-
-__device__ __forceinline__ PfCursor begin_range(const PfArgs& a, const PfReq& q) {
+__device__ __forceinline__ PfCursor begin_range(const PfArgs& a, const PfGroup& q) {
   PfCursor c;
+  c.q = q;
+  c.g = q.g;
   c.b0 = q.b0;
   c.b1 = q.b1;
-  enter_request(c, q.r, q);
-  int at = q.b0 - c.y;
-  if (c.u == 0) {
-    const PfPrefix p = prefix_shape(c.q.ptiles, c.q.gcount, a.G);
-    const int all = p.head_cost * a.Hkv;
-    if (at < all) {
-      c.h = at / p.head_cost;
-      c.u = min((at - c.h * p.head_cost) / p.step, p.units - 1);
-      c.y += c.h * p.head_cost + c.u * p.step;
-      return c;
-    }
-    c.u = -1;
-    c.y += all;
-    at -= all;
-  }
-  const int cost = own_cost(c.q.stok);
-  if (cost > 0) {
-    c.h = min(at / cost, a.Hkv);
-    c.y += c.h * cost;
-  }
+  const PfPrefix p = prefix_shape(q.ptiles, q.count, a.G);
+  const int at = q.b0 - q.y0;
+  c.h = at / p.head_cost;
+  c.u = min((at - c.h * p.head_cost) / p.step, p.units - 1);
+  c.y = q.y0 + c.h * p.head_cost + c.u * p.step;
   return c;
 }
 
 __device__ __forceinline__ bool next_piece(const PfArgs& a, PfCursor& c, PfPiece& p) {
   for (;;) {
     if (c.y >= c.b1) return false;
-    int n, w;
-    if (c.u >= 0) {
-      const PfPrefix s = prefix_shape(c.q.ptiles, c.q.gcount, a.G);
-      n = s.blocks;
-      w = c.u == s.units - 1 ? s.wlast : kPfCostPair;
-      p.prefix = 1;
-      p.r = c.q.leader;
-      p.row0 = c.u * kPfUnitRows;
-      p.rows = min(kPfUnitRows, c.q.gcount * a.G - p.row0);
-      p.tile0 = 0;
-      p.tokens = c.q.ptiles * kPfTile;
-      p.h = c.h;
-      p.gfirst = c.q.gfirst;
-      owned_blocks(c.y + start_cost(w), n, w, c.b0, c.b1, p.i0, p.i1);
-      c.y += start_cost(w) + n * w;
-      if (++c.u == s.units) {
-        c.u = 0;
-        if (++c.h == a.Hkv) {
-          c.h = 0;
-          c.u = -1;
-        }
-      }
-    } else {
-      n = own_blocks(c.q.stok);
-      if (n == 0 || c.h >= a.Hkv) {
-        if (c.r + 1 >= a.B) return false;
-        enter_request(c, c.r + 1, load_req(a.req + c.r + 1));
-        continue;
-      }
-      p.prefix = 0;
-      p.r = c.r;
-      p.row0 = 0;
-      p.rows = a.G;
-      p.tile0 = c.q.ptiles;
-      p.tokens = c.q.stok;
-      p.h = c.h;
-      p.gfirst = c.r;
-      owned_blocks(c.y + kPfStartSolo, n, kPfCostSolo, c.b0, c.b1, p.i0, p.i1);
-      c.y += own_cost(c.q.stok);
+    if (c.q.ptiles == 0 || c.h == a.Hkv) {
+      if (++c.g >= a.n_groups) return false;
+      c.q = load_group(a.group + c.g);
+      c.h = c.u = 0;
+      c.y = c.q.y0;
+      continue;
+    }
+    const PfPrefix s = prefix_shape(c.q.ptiles, c.q.count, a.G);
+    const int w = c.u == s.units - 1 ? s.wlast : kPfCostPair;
+    p.r = c.q.leader;
+    p.h = c.h;
+    p.row0 = c.u * kPfUnitRows;
+    p.rows = min(kPfUnitRows, c.q.count * a.G - p.row0);
+    p.gfirst = c.q.first;
+    p.tokens = c.q.ptiles * kPfTile;
+    owned_blocks(c.y + start_cost(w), s.blocks, w, c.b0, c.b1, p.i0, p.i1);
+    c.y += start_cost(w) + s.blocks * w;
+    if (++c.u == s.units) {
+      c.u = 0;
       ++c.h;
     }
     if (p.i0 < p.i1) return true;
   }
 }
 
-// One CTA: group ranges, shared pages and leaders, the work list and every CTA's
-// first request.
+// One CTA: group ranges, shared pages and leaders, what the requests have of their
+// own, the work list and every CTA's first group.
 __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const PfArgs a) {
   __shared__ int s_sum[kPfPlanThreads / 32];
   __shared__ int s_max[kPfPlanThreads / 32];
@@ -332,6 +294,8 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
   const unsigned kFull = 0xffffffffu;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int tpp = a.page_size >> 4;
+#pragma unroll 1
+  for (int i = t; i < a.n_counters; i += kPfPlanThreads) a.counters[i] = make_uint4(0, 0, 0, 0);
   // group starts: clamped, then the running maximum
   int carry = 0;
 #pragma unroll 1
@@ -359,12 +323,9 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
 #pragma unroll 1
   for (int r = t; r < a.B; r += kPfPlanThreads) {
     const int L = live_length(a, r);
-    PfReq& q = a.req[r];
-    q.ptiles = 0;
-    q.stok = L;
-    q.gfirst = r;
-    q.gcount = 1;
-    q.leader = r;
+    a.own_len[r] = L;
+    a.skip[r] = 0;
+    a.group_of[r] = -1;
     a.dead[r] = L == 0;
   }
   __syncthreads();
@@ -372,11 +333,10 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
 #pragma unroll 1
   for (int g = warp; g < a.n_groups; g += kPfPlanThreads / 32) {
     const int lo = a.gstart[g], hi = a.gstart[g + 1];
-    if (hi - lo < 2) continue;
     int least = 0x7fffffff, leader = 0x7fffffff;
 #pragma unroll 1
     for (int r = lo + lane; r < hi; r += 32) {
-      const int L = a.req[r].stok;
+      const int L = a.own_len[r];
       if (L > 0) {
         least = min(least, L);
         leader = min(leader, r);
@@ -384,32 +344,33 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
     }
     least = __reduce_min_sync(kFull, least);
     leader = __reduce_min_sync(kFull, leader);
-    const int pre = __ldg(a.prefix_lens + g);
-    const int ptiles = leader == 0x7fffffff ? 0 : max(0, min(pre, least)) / a.page_size * tpp;
-    if (ptiles == 0) continue;
+    const int pages = hi - lo < 2 || leader == 0x7fffffff ? 0 : max(0, min(__ldg(a.prefix_lens + g), least)) / a.page_size;
+    if (lane == 0) {
+      PfGroup& q = a.group[g];
+      q.ptiles = pages * tpp;
+      q.first = lo;
+      q.count = hi - lo;
+      q.leader = leader;
+    }
+    if (pages == 0) continue;
 #pragma unroll 1
     for (int r = lo + lane; r < hi; r += 32) {
-      PfReq& q = a.req[r];
-      q.ptiles = ptiles;
-      q.stok = max(0, q.stok - ptiles * kPfTile);
-      q.gfirst = lo;
-      q.gcount = hi - lo;
-      q.leader = leader;
+      a.own_len[r] = max(0, a.own_len[r] - pages * a.page_size);
+      a.skip[r] = pages;
+      a.group_of[r] = g;
     }
   }
   __syncthreads();
   // places in the work list
-  const int chunk = (a.B + kPfPlanThreads - 1) / kPfPlanThreads;
-  const int rb = min(a.B, t * chunk), re = min(a.B, rb + chunk);
-  auto cost_of = [&](int r) -> int {
-    const PfReq& q = a.req[r];
-    int c = own_cost(q.stok);
-    if (q.ptiles > 0 && q.gfirst == r) c += prefix_shape(q.ptiles, q.gcount, a.G).head_cost;
-    return c * a.Hkv;
+  const int chunk = (a.n_groups + kPfPlanThreads - 1) / kPfPlanThreads;
+  const int gb = min(a.n_groups, t * chunk), ge = min(a.n_groups, gb + chunk);
+  auto cost_of = [&](int g) -> int {
+    const PfGroup& q = a.group[g];
+    return q.ptiles > 0 ? prefix_shape(q.ptiles, q.count, a.G).head_cost * a.Hkv : 0;
   };
   int mine = 0;
 #pragma unroll 1
-  for (int r = rb; r < re; ++r) mine += cost_of(r);
+  for (int g = gb; g < ge; ++g) mine += cost_of(g);
   int incl = mine;
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
@@ -427,26 +388,25 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
   const int below = __shfl_sync(kFull, sums, max(warp - 1, 0));
   const int T = __shfl_sync(kFull, sums, 31);
   int y = incl - mine + (warp > 0 ? below : 0);
-  if (t == 0) *a.total = T;
 #pragma unroll 1
-  for (int r = rb; r < re; ++r) {
-    a.req[r].y0 = y;
-    y += cost_of(r);
+  for (int g = gb; g < ge; ++g) {
+    a.group[g].y0 = y;
+    y += cost_of(g);
   }
   __syncthreads();
-  // every CTA's first request: the last one whose units start at or before its range
+  // every CTA's first group: the last one whose units start at or before its range
   const PfRanges rg = ranges_of(T, a.ctas);
 #pragma unroll 1
   for (int c = t; c < a.ctas; c += kPfPlanThreads) {
     const int b0 = rg.begin(c);
-    int lo = 0, hi = a.B - 1;
+    int lo = 0, hi = a.n_groups - 1;
 #pragma unroll 1
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (a.req[mid].y0 <= b0) lo = mid; else hi = mid - 1;
+      if (a.group[mid].y0 <= b0) lo = mid; else hi = mid - 1;
     }
-    PfReq q = a.req[lo];
-    q.r = lo;
+    PfGroup q = a.group[lo];
+    q.g = lo;
     q.b0 = b0;
     q.b1 = rg.begin(c + 1);
     a.start[c] = q;
@@ -673,7 +633,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (kFp8 && i >= C::kBarVFree && i < C::kBarVFree + C::kVStages) arrivals = 4;   // V warps
     if (i >= C::kBarP && i < C::kBarP + 4) arrivals = 4;                             // a tile's softmax warps
     if (i >= C::kBarOFree && i < C::kBarOFree + 2) arrivals = 4;                     // a tile's softmax warps
-    if (i >= C::kBarQ && i < C::kBarQ + 2) arrivals = 5;                             // those, or the planning warp for them; and it
+    if (i >= C::kBarQ && i < C::kBarQ + 2) arrivals = 4;                             // those
     if (i >= C::kBarQFree && i < C::kBarQFree + 2) arrivals = 10;                    // MMA and softmax warps
     if (i >= C::kBarPieceFree && i < C::kBarPieceFree + kPfPieces) arrivals = 16;    // every other warp; K's and V's half of one
     mbar_init(bar(i), arrivals);
@@ -691,7 +651,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   tc_fence_after();
   griddep_wait();  // the plan is there
   const uint32_t tmem = *s_tmem;
-  const PfReq first = load_req(a.start + blockIdx.x);
+  const PfGroup first = load_group(a.start + blockIdx.x);
   auto wait = [&](int i, uint32_t parity) { pf_wait(bar(i), parity & 1u, a.status, s_failed); };
   // the next piece, from the planning warp; false at the end
   uint32_t pn = 0;
@@ -774,71 +734,39 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int tpp = a.page_size >> 4;
     if (warp == kPfPlanWarp) {
       // ===================== pieces, ahead of the other warps =====================
-      // Also the queries of own units (a few rows), and the check that a group's tables agree: the
-      // prefix units of kv head 0 cover every shared page once per 256 rows, and each request of the
-      // unit must name the leader's pages, which must be in the pool.
-      // Pieces are published as far ahead as the ring allows, queries staged as far as the two buffers do.
+      // And the check that a group's tables agree: the units of kv head 0 cover every shared page once per
+      // 256 rows, and each request of the unit must name the leader's pages, which must be in the pool.
       PfCursor cur = begin_range(a, first);
-      uint32_t n = 0, staged = 0, uses[2] = {0, 0};
       int qbuf = 0, t0 = 0;
       bool more = true;
 #pragma unroll 1
-      for (;;) {
-#pragma unroll 1
-        while (more && (n == 0 || (staged > 0 && n - staged < kPfPieces))) {
-          if (n >= kPfPieces) {
-            const uint32_t phase = n / kPfPieces - 1;
-            if (staged == n) wait(C::kBarPieceFree + n % kPfPieces, phase);
-            else if (!__all_sync(kFull, mbar_test(bar(C::kBarPieceFree + n % kPfPieces), phase & 1))) break;
-          }
-          more = next_piece(a, cur, p);
-          if (!more) p.i0 = p.i1 = 0;
-          p.qbuf = qbuf;
-          qbuf ^= 1;
-          p.t0 = t0;
-          t0 ^= (p.i1 - p.i0) & 1;
-          // the first blocks' pages: copies need not wait for the table, which may come from far
-          const int tile = p.i0 * kPfBlkTiles + lane;
-          const bool some = more && tile * kPfTile < p.tokens;
-          const int page = some ? max(-1, __ldg(a.page_table + static_cast<int64_t>(p.r) * a.max_pages +
-                                                quotient(p.tile0 + tile, a.by_tpp))) : -1;
-          PfSlot* const at = s_piece + n % kPfPieces;
-          at->pages[lane] = page;
-          if (lane == 0) at->piece = p;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::kBarPiece + n % kPfPieces));
-          ++n;
-        }
-        p = s_piece[staged % kPfPieces].piece;
+      for (uint32_t n = 0; more; ++n) {
+        more = next_piece(a, cur, p);
+        if (!more) p.i0 = p.i1 = 0;
+        p.qbuf = qbuf;
+        qbuf ^= 1;
+        p.t0 = t0;
+        t0 ^= (p.i1 - p.i0) & 1;
+        // the first blocks' pages: copies need not wait for the table, which may come from far
+        const int tile = p.i0 * kPfBlkTiles + lane;
+        const bool some = more && tile * kPfTile < p.tokens;
+        const int32_t* lead = a.page_table + static_cast<int64_t>(more ? p.r : 0) * a.max_pages;
+        const int page = some ? max(-1, __ldg(lead + quotient(tile, a.by_tpp))) : -1;
+        if (n >= kPfPieces) wait(C::kBarPieceFree + n % kPfPieces, n / kPfPieces - 1);
+        PfSlot* const at = s_piece + n % kPfPieces;
+        at->pages[lane] = page;
+        if (lane == 0) at->piece = p;
         __syncwarp();
-        ++staged;
-        if (p.i0 >= p.i1) break;
-        const bool pair = p.pair();
-        // (every use of a buffer is waited for in turn and announced here, whoever stages it: a barrier's
-        // parity tells neighbouring phases apart, no others, so nobody may run two uses ahead of this warp)
-        if (uses[p.qbuf] > 0) wait(C::kBarQFree + p.qbuf, uses[p.qbuf] - 1);
-        if (pair && uses[p.qbuf ^ 1] > 0) wait(C::kBarQFree + (p.qbuf ^ 1), uses[p.qbuf ^ 1] - 1);
-        if (!p.prefix) {
-          stage_rows(p, p.qbuf, 0, 0, p.rows);
-          if (lane < 4) mbar_arrive(bar(C::kBarQ + p.qbuf));
-        }
-        __syncwarp();
-        ++uses[p.qbuf];
-        if (lane == 0) mbar_arrive(bar(C::kBarQ + p.qbuf));
-        if (pair) {
-          ++uses[p.qbuf ^ 1];
-          if (lane == 0) mbar_arrive(bar(C::kBarQ + (p.qbuf ^ 1)));
-        }
-        if (p.prefix && p.h == 0) {
+        if (lane == 0) mbar_arrive(bar(C::kBarPiece + n % kPfPieces));
+        if (more && p.h == 0) {
           const int p0 = quotient(p.i0 * kPfBlkTiles, a.by_tpp);
           const int p1 = quotient(min(p.i1 * kPfBlkTiles, p.tokens / kPfTile) + tpp - 1, a.by_tpp);
-          const int32_t* lead = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
           const int r0 = p.gfirst + quotient(p.row0, a.by_g), r1 = p.gfirst + quotient(p.row0 + p.rows - 1, a.by_g);
 #pragma unroll 1
           for (int i = p0 + lane; i < p1; i += 32) {
             const int want = __ldg(lead + i);
             const bool in = want >= 0 && want < a.num_pages;
-#pragma unroll 2
+#pragma unroll 4
             for (int r = r0; r <= r1; ++r)
               if (!in || __ldg(a.page_table + static_cast<int64_t>(r) * a.max_pages + i) != want) a.dead[r] = 1;
           }
@@ -852,7 +780,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const bool kw = lane < 16;
       const unsigned group = kw ? 0xffffu : 0xffff0000u;
       const bool leads = (lane & 15) == 0;
-      const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
+      const uint64_t pol = l2_policy_evict_normal();  // (other units and CTAs read the same pages)
       const int c = lane & 7;
       const int box_t = c * a.zbox;                        // first tile of the box in a block
       const bool copies = c < kPfBlkTiles / a.zbox && ((lane & 8) == 0 || (kw && !kFp8));
@@ -865,7 +793,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       auto all_of_half = [&](bool x) -> bool { return (__ballot_sync(kFull, x) & group) == group; };
       const int32_t* row = nullptr;
       int i = 0, tiles = 0, next = -2;
-      uint64_t pol = 0;
       uint32_t j = 0, st = 0, round = 0, idle = 0;
       bool have = false, done = false;
       int ids[4] = {-2, -2, -2, -2};  // pages of this lane's box of the next four blocks (once it is there)
@@ -884,8 +811,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           done = !have;
           i = p.i0;
           row = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
-          tiles = (p.tokens + kPfTile - 1) / kPfTile;
-          pol = p.prefix ? again : once;
+          tiles = p.tokens / kPfTile;
           // (the slot may be written anew from here on: the ids are taken now)
           next = have_box(i) ? ids[0] : -2;
           idle = 0;
@@ -894,14 +820,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const bool good = goes && next >= 0 && next < a.num_pages;
         const uint32_t boxes = __popc(__ballot_sync(kFull, good) & group);
         if (goes) {
-          const int pg = next;
+          const int pg = next;  // (one outside the pool is not copied: the check has it)
           ids[0] = ids[1];
           ids[1] = ids[2];
           ids[2] = ids[3];
-          if (have_box(i + 4)) ids[3] = max(-1, __ldg(row + quotient(p.tile0 + (i + 4) * kPfBlkTiles + box_t, a.by_tpp)));
+          if (have_box(i + 4)) ids[3] = max(-1, __ldg(row + quotient((i + 4) * kPfBlkTiles + box_t, a.by_tpp)));
           next = have_box(i + 1) ? ids[0] : -2;
-          // a page outside the pool: the request is dead (a group's are told apart by the planning warp)
-          if (!good && pg != -2 && !p.prefix) a.dead[p.r] = 1;
           const uint32_t f = full + 8 * st;
           if (leads) {
             const uint32_t bytes = boxes * a.zbox * (kPfTile * (kw ? 128 : kPfDim * C::kElem));
@@ -910,7 +834,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
           __syncwarp(group);
           if (good) {
-            const int tile = p.tile0 + i * kPfBlkTiles + box_t;
+            const int tile = i * kPfBlkTiles + box_t;
             tma_load_3d(ring + st * C::kKStage, map, mx, my,
                         (pg * a.Hkv + p.h) * tpp + tile - quotient(tile, a.by_tpp) * tpp, f, pol);
           }
@@ -1019,13 +943,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         uint32_t passed = 0;  // bf16: V blocks seen
         // the other tile's bf16 V blocks up to block m
         auto pass_v = [&](uint32_t m) {
-          if (kFp8) return;
 #pragma unroll 1
-          for (; passed < m; ++passed) {
+          while (!kFp8 && passed < m) {
             wait(C::kBarReady + v3, v3ph);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::kBarVFree + v3));
             if (++v3 == C::kReady) v3 = 0, v3ph ^= 1;
+            ++passed;
           }
         };
 #pragma unroll 1
@@ -1093,8 +1017,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const bool valid = lrow < p.rows;
         const bool busy = lrow - lane < p.rows;       // some row of the warp's is
         const int buf = pair ? t : p.qbuf;
-        // ---- the queries of a prefix unit into shared memory (own units': the planning warp)
-        if (p.prefix && (pair || t == 0)) {
+        // ---- the queries into shared memory
+        if (pair || t == 0) {
           const uint32_t u = buf ? uses[1] : uses[0];
           if (u > 0) wait(C::kBarQFree + buf, u - 1);
           if (busy) stage_rows(p, buf, lrow - lane, row - lane, min(32, p.rows - (lrow - lane)));
@@ -1199,9 +1123,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         // ---- the row's partial: pieces at a unit's start by row, others by CTA
         const int grow = p.row0 + lrow, rq = quotient(grow, a.by_g);
-        int64_t slot = static_cast<int64_t>(4) * a.B * a.Hq + static_cast<int64_t>(blockIdx.x) * kPfUnitRows + t * 128 + row;
+        int64_t slot = static_cast<int64_t>(2) * a.B * a.Hq + static_cast<int64_t>(blockIdx.x) * kPfUnitRows + t * 128 + row;
         if (p.i0 == 0 && valid)
-          slot = static_cast<int64_t>((p.prefix ? 0 : 2) + (pair ? 0 : t)) * a.B * a.Hq +
+          slot = static_cast<int64_t>(pair ? 0 : t) * a.B * a.Hq +
                  static_cast<int64_t>(p.gfirst + rq) * a.Hq + p.h * a.G + grow - rq * a.G;
         if (any) {
           wait(C::kBarO + t, ns - 1);
@@ -1240,49 +1164,39 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 // ---------------------------------------------------------------------------
 // merge
 // ---------------------------------------------------------------------------
-// One warp per (request, query head): its partials are those of the prefix
-// unit's pieces and of its own unit's, in the order of the work list.  A lane
+// One warp per (request, query head): attention over the own tokens, and the
+// partials of the pieces of the row's unit in the order of the work list.  A lane
 // finds one partial (row in the partial arrays, m, l), then all lanes add its O.
 __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const PfArgs a) {
-  griddep_wait();
   const unsigned kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kPfMergeWarps + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(a.B) * a.Hq) return;
-  const int r = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
-  const int h = hq / a.G, g = hq % a.G;
-  uint2* const out = reinterpret_cast<uint2*>(a.out + row * kPfDim) + lane;
-  const PfRanges rg = ranges_of(__ldcg(a.total), a.ctas);
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
-  float M = -INFINITY, W = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  bool dead = __ldcg(a.dead + r) != 0;
-  if (!dead) {
-    const PfReq q = load_req(a.req + r);
-    // the units that hold the row's partials: (place, blocks, cost of a block, row in a CTA's slots)
-    const int nb = own_blocks(q.stok);
-    int own_y = q.y0, y = 0, blocks = 0, w = kPfCostSolo, lrow = 0;
-    if (q.ptiles > 0) {
-      const PfPrefix s = prefix_shape(q.ptiles, q.gcount, a.G);
-      const int gy = q.gfirst == r ? q.y0 : load_req(a.req + q.gfirst).y0;
-      const int i = (r - q.gfirst) * a.G + g, u = i / kPfUnitRows;
-      blocks = s.blocks;
-      w = u == s.units - 1 ? s.wlast : kPfCostPair;
-      lrow = i % kPfUnitRows;
-      y = gy + h * s.head_cost + u * s.step + start_cost(w);
-      if (q.gfirst == r) own_y += s.head_cost * a.Hkv;
-    }
-#pragma unroll 1
-    for (int kind = 0; kind < 4; kind += 2) {
-      if (kind == 2) {
-        blocks = nb;
-        w = kPfCostSolo;
-        lrow = g;
-        y = own_y + h * own_cost(q.stok) + kPfStartSolo;
-      }
-      if (blocks == 0) continue;
+  griddep_wait();
+  if (row >= rows) return;
+  uint2* const out = reinterpret_cast<uint2*>(a.out + row * kPfDim) + lane;
+  const int r = static_cast<int>(row / a.Hq), hq = static_cast<int>(row - static_cast<int64_t>(r) * a.Hq);
+  const float own_lse = __ldcg(a.own_lse + row);
+  float4 acc = __ldcg(reinterpret_cast<const float4*>(a.own_out + row * kPfDim) + lane);
+  bool dead = false;
+  float M = own_lse * kPfLog2e, W = own_lse == -INFINITY ? 0.f : 1.f;
+  if (W == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.n_groups > 0) {
+    // own tokens without a result: a page of theirs is outside the pool
+    dead = __ldcg(a.dead + r) != 0 || (own_lse == -INFINITY && __ldcg(a.own_len + r) > 0);
+    const int gi = __ldcg(a.group_of + r);
+    if (!dead && gi >= 0) {
+      const PfGroup q = load_group(a.group + gi);
+      const PfRanges rg = [&] {  // from the last CTA's range: its end is the list's
+        return ranges_of(load_group(a.start + a.ctas - 1).b1, a.ctas);
+      }();
+      const PfPrefix s = prefix_shape(q.ptiles, q.count, a.G);
+      const int h = quotient(hq, a.by_g);
+      const int i = (r - q.first) * a.G + hq - h * a.G, u = i / kPfUnitRows, lrow = i % kPfUnitRows;
+      const int w = u == s.units - 1 ? s.wlast : kPfCostPair;
+      const int y = q.y0 + h * s.head_cost + u * s.step + start_cost(w);
       const int subs = w == kPfCostPair ? 0 : 1;  // log2 of the row tiles with a partial each
-      const int c0 = rg.owner(y), c1 = rg.owner(y + (blocks - 1) * w);
+      const int c0 = rg.owner(y), c1 = rg.owner(y + (s.blocks - 1) * w);
       const int cands = (c1 - c0 + 1) << subs;
 #pragma unroll 1
       for (int base = 0; base < cands; base += 32) {
@@ -1292,9 +1206,8 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
         if (k < cands) {
           const int c = c0 + (k >> subs), sub = k & subs;
           int i0, i1;
-          owned_blocks(y, blocks, w, rg.begin(c), rg.begin(c + 1), i0, i1);
-          slot = i0 == 0 ? static_cast<int64_t>(kind + sub) * rows + row
-                         : 4 * rows + static_cast<int64_t>(c) * kPfUnitRows + sub * 128 + lrow;
+          owned_blocks(y, s.blocks, w, rg.begin(c), rg.begin(c + 1), i0, i1);
+          slot = i0 == 0 ? sub * rows + row : 2 * rows + static_cast<int64_t>(c) * kPfUnitRows + sub * 128 + lrow;
           if (i0 < i1) ml = __ldcg(a.part_ml + slot);
         }
         float mx = ml.x;
@@ -1364,17 +1277,20 @@ int prepare_prefix(int dev) {
 }
 
 struct PfLayout {
-  size_t gstart, start, dead, req, ml, o, total;
+  size_t gstart, group, start, per_request, own_out, own_lse, ml, o, total;
 };
-PfLayout prefix_layout(int64_t B, int64_t Hq, int64_t ctas) {
+// Behind the workspace of the own parts' attention (whose first word is the status word of both).
+PfLayout prefix_layout(int64_t B, int64_t Hq, int64_t ctas, size_t own_bytes) {
   auto up = [](int64_t x) { return (static_cast<size_t>(x) + 255) & ~static_cast<size_t>(255); };
-  const int64_t slots = 4 * B * Hq + ctas * kPfUnitRows;
+  const int64_t slots = 2 * B * Hq + ctas * kPfUnitRows;
   PfLayout l;
-  l.gstart = 256;
-  l.start = l.gstart + up((B + 1) * 4);
-  l.dead = l.start + up(ctas * static_cast<int64_t>(sizeof(PfReq)));
-  l.req = l.dead + up(B * 4);
-  l.ml = l.req + up(B * static_cast<int64_t>(sizeof(PfReq)));
+  l.gstart = up(static_cast<int64_t>(own_bytes));
+  l.group = l.gstart + up((B + 1) * 4);
+  l.start = l.group + up(B * static_cast<int64_t>(sizeof(PfGroup)));
+  l.per_request = l.start + up(ctas * static_cast<int64_t>(sizeof(PfGroup)));
+  l.own_out = l.per_request + up(4 * B * 4);
+  l.own_lse = l.own_out + up(B * Hq * kPfDim * 4);
+  l.ml = l.own_lse + up(B * Hq * 4);
   l.o = l.ml + up(slots * 8);
   l.total = l.o + up(slots * kPfDim * 4);
   return l;
@@ -1428,10 +1344,10 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   if (D != kPfDim || G > kPfGroupMax || page_size % kPfTile != 0 || page_size > 256) return FPK_EUNSUPPORTED;
   const int tpp = page_size / kPfTile;
   const int64_t tiles = static_cast<int64_t>(num_pages) * Hkv * tpp;
-  // tile numbers are 32-bit tensor-map coordinates; rows and the work list's length (at most a prefix
-  // unit and an own unit of the table's width per request and kv head) are counted in 31 bits
+  // tile numbers are 32-bit tensor-map coordinates; rows and the work list's length (at most a unit
+  // of the table's width per request and kv head) are counted in 31 bits
   const int64_t width = (static_cast<int64_t>(max_pages) * page_size + kPfBlk - 1) / kPfBlk;
-  const int64_t longest = width * (kPfCostPair + kPfCostSolo) + kPfStartPair + kPfStartSolo;
+  const int64_t longest = width * kPfCostPair + kPfStartPair;
   if (tiles > 0x7fffffff || static_cast<int64_t>(B) * Hq > 0x7fffffff / 4 || width > (int64_t(1) << 24) ||
       longest > 0x7fffffff / (static_cast<int64_t>(B > 0 ? B : 1) * Hkv))
     return FPK_EUNSUPPORTED;
@@ -1446,7 +1362,9 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kPfMaxDevices) return FPK_ECUDA;
   const int ctas = device_sm_count(dev);
   if (ctas <= 0) return FPK_ECUDA;
-  const PfLayout l = prefix_layout(B, Hq, ctas);
+  const size_t own_bytes = own_attention_bytes(B, Hq, Hkv);
+  if (own_bytes == 0) return FPK_ECUDA;
+  const PfLayout l = prefix_layout(B, Hq, ctas, own_bytes);
   if (workspace_bytes < l.total) return FPK_ENOSPC;
   const int st = prepare_prefix<kFp8>(dev);
   if (st != FPK_OK) return st;
@@ -1469,11 +1387,15 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = reinterpret_cast<uint32_t*>(ws);
-  a.total = reinterpret_cast<int32_t*>(ws + 8);
   a.gstart = reinterpret_cast<int32_t*>(ws + l.gstart);
-  a.start = reinterpret_cast<PfReq*>(ws + l.start);
-  a.dead = reinterpret_cast<int32_t*>(ws + l.dead);
-  a.req = reinterpret_cast<PfReq*>(ws + l.req);
+  a.group = reinterpret_cast<PfGroup*>(ws + l.group);
+  a.start = reinterpret_cast<PfGroup*>(ws + l.start);
+  a.group_of = reinterpret_cast<int32_t*>(ws + l.per_request);
+  a.own_len = a.group_of + B;
+  a.skip = a.own_len + B;
+  a.dead = a.skip + B;
+  a.own_out = reinterpret_cast<float*>(ws + l.own_out);
+  a.own_lse = reinterpret_cast<float*>(ws + l.own_lse);
   a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
   a.part_o = reinterpret_cast<float*>(ws + l.o);
   a.n_groups = n_groups;
@@ -1490,9 +1412,23 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   a.by_tpp = tpp == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + tpp - 1) / tpp);
   a.sm_scale_log2 = sm_scale * kPfLog2e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  prefix_plan_kernel<<<1, kPfPlanThreads, 0, s>>>(a);
-  if (checked_launch_status() != FPK_OK) return FPK_ECUDA;
-  if (launch_dependent(prefix_attn_kernel<kFp8>, ctas, kPfThreads, PfCfg<kFp8>::kSmem, s, a, kmap, vmap) != FPK_OK)
+  const bool groups = n_groups > 0;
+  size_t from = 0, to = 0;
+  own_attention_counters(B, Hq, Hkv, &from, &to);
+  a.counters = reinterpret_cast<uint4*>(ws + from);
+  a.n_counters = static_cast<int>((to - from) / sizeof(uint4));
+  if (!groups && cudaMemsetAsync(ws + from, 0, to - from, s) != cudaSuccess) return FPK_ECUDA;
+  if (groups) {
+    prefix_plan_kernel<<<1, kPfPlanThreads, 0, s>>>(a);
+    if (checked_launch_status() != FPK_OK) return FPK_ECUDA;
+  }
+  // without groups the own parts are all there is, and their kernel knows dead requests by itself
+  const int own = own_attention(kFp8, q, kv_pool, k_scale, v_scale, page_table, max_pages, groups ? a.own_len : seq_lens,
+                                groups ? a.skip : nullptr, groups ? nullptr : abort_mask,
+                                reinterpret_cast<float*>(ws + l.own_out), reinterpret_cast<float*>(ws + l.own_lse), ws,
+                                own_bytes, sm_scale, B, Hq, Hkv, page_size, num_pages, stream);
+  if (own != FPK_OK) return own;
+  if (groups && launch_dependent(prefix_attn_kernel<kFp8>, ctas, kPfThreads, PfCfg<kFp8>::kSmem, s, a, kmap, vmap) != FPK_OK)
     return FPK_ECUDA;
   const int merge = static_cast<int>((static_cast<int64_t>(B) * Hq + kPfMergeWarps - 1) / kPfMergeWarps);
   return launch_dependent(prefix_merge_kernel, merge, 32 * kPfMergeWarps, 0, s, a);
@@ -1506,7 +1442,8 @@ extern "C" size_t fpk_prefix_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv,
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= fpk::kPfMaxDevices) return 0;
   const int ctas = fpk::device_sm_count(dev);
-  return ctas > 0 ? fpk::prefix_layout(B, Hq, ctas).total : 0;
+  const size_t own = fpk::own_attention_bytes(B, Hq, Hkv);
+  return ctas > 0 && own > 0 ? fpk::prefix_layout(B, Hq, ctas, own).total : 0;
 }
 
 extern "C" int fpk_paged_decode_attn_fp8_prefix(const void* q, const uint8_t* kv_pool, const float* k_scale,

@@ -26,7 +26,7 @@ class Bar:
 
 
 def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
-    """pieces: [(prefix, pair, blocks, halves of the last block)]; slow: a warp that hardly ever gets its turn"""
+    """pieces: [(pair, blocks, halves of the last block)]; slow: a warp that hardly ever gets its turn"""
     rng = random.Random(seed)
     KST, VST, V16 = (4, 2, 2) if fp8 else (2, 3, 0)
     kst, ready_n = KST, V16 if fp8 else VST
@@ -34,7 +34,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
              vfull=[Bar(1) for _ in range(VST)], vfree=[Bar(4 if fp8 else 2) for _ in range(VST)],
              ready=[Bar(4) for _ in range(ready_n)], used=[Bar(2) for _ in range(V16)],
              S=[Bar(1), Bar(1)], P=[[Bar(4), Bar(4)], [Bar(4), Bar(4)]], O=[Bar(1), Bar(1)],
-             ofree=[Bar(4), Bar(4)], Q=[Bar(5), Bar(5)], qfree=[Bar(10), Bar(10)],
+             ofree=[Bar(4), Bar(4)], Q=[Bar(4), Bar(4)], qfree=[Bar(10), Bar(10)],
              piece=[Bar(1) for _ in range(pieces_ring)], piecefree=[Bar(16) for _ in range(pieces_ring)],
              turn=[Bar(1), Bar(1)])
     late = []                       # (order in its queue, effect)
@@ -61,46 +61,22 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
         return p
 
     def plan():
-        n = staged = 0
-        uses, qbuf, tile, more = [0, 0], 0, 0, True
-        while True:
-            while more and n - staged < pieces_ring:
-                if n >= pieces_ring:
-                    ph = n // pieces_ring - 1
-                    if staged == n:
-                        yield from wait(B["piecefree"][n % pieces_ring], ph)
-                    elif not B["piecefree"][n % pieces_ring].done(ph):
-                        break
-                more = n < nb
-                slots[n % pieces_ring] = (n, qbuf, tile) + (pieces[n] if more else (0, 0, 0, 0))
-                qbuf ^= 1
-                if more:
-                    tile ^= pieces[n][2] & 1
-                yield
-                B["piece"][n % pieces_ring].arrive()
-                n += 1
-                yield
-            k, qb, t0, prefix, pair, blocks, tail = slots[staged % pieces_ring]
-            assert k == staged
-            staged += 1
-            if not blocks:
-                return
-            for b in ([qb, qb ^ 1] if pair else [qb]):
-                if uses[b] > 0:
-                    yield from wait(B["qfree"][b], uses[b] - 1)
-            if not prefix:
-                qof[qb] = k
-                yield
-                B["Q"][qb].arrive(4)
-            for b in ([qb, qb ^ 1] if pair else [qb]):
-                uses[b] += 1
-                B["Q"][b].arrive()
+        qbuf = tile = 0
+        for n in range(nb + 1):
+            slot = (n, qbuf, tile) + (pieces[n] if n < nb else (0, 0, 0))
+            qbuf ^= 1
+            tile ^= slot[4] & 1
+            if n >= pieces_ring:
+                yield from wait(B["piecefree"][n % pieces_ring], n // pieces_ring - 1)
+            slots[n % pieces_ring] = slot
+            yield
+            B["piece"][n % pieces_ring].arrive()
             yield
 
     def loader(full, free, stages, hold, name):
         j = pn = 0
         while True:
-            k, qb, t0, prefix, pair, blocks, tail = yield from take(pn)
+            k, qb, t0, pair, blocks, tail = yield from take(pn)
             pn += 1
             if not blocks:
                 return
@@ -119,7 +95,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
     def vwarp():
         j = pn = 0
         while True:
-            k, qb, t0, prefix, pair, blocks, tail = yield from take(pn)
+            k, qb, t0, pair, blocks, tail = yield from take(pn)
             pn += 1
             if not blocks:
                 return
@@ -147,7 +123,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
         uses = [0, 0]
         q = ("mma", t)
         while True:
-            k, qb, t0, prefix, pair, blocks, tail = yield from take(pn)
+            k, qb, t0, pair, blocks, tail = yield from take(pn)
             pn += 1
             if not blocks:
                 return
@@ -224,12 +200,12 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
         ns = pn = 0
         uses = [0, 0]
         while True:
-            k, qb, t0, prefix, pair, blocks, tail = yield from take(pn)
+            k, qb, t0, pair, blocks, tail = yield from take(pn)
             pn += 1
             if not blocks:
                 return
             b = t if pair else qb
-            if prefix and (pair or t == 0):
+            if pair or t == 0:
                 if uses[b] > 0:
                     yield from wait(B["qfree"][b], uses[b] - 1)
                 qof[b] = k
@@ -297,23 +273,14 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
 
 
 @pytest.mark.parametrize("fp8", [True, False])
-@pytest.mark.parametrize("kind", ["own", "pairs", "solo", "mixed", "long"])
+@pytest.mark.parametrize("kind", ["pairs", "solo", "mixed", "long"])
 def test_every_run_ends(fp8, kind):
     for seed in range(18):
         rng = random.Random(seed * 7 + len(kind))
         many = rng.randint(5, 9)
-        if kind == "own":
-            pieces = [(0, 0, rng.choice([1, 1, 2, 3, 5])) for _ in range(many)]
-        elif kind == "pairs":
-            pieces = [(1, 1, rng.choice([1, 1, 2, 3])) for _ in range(many)]
-        elif kind == "solo":
-            pieces = [(1, 0, rng.choice([1, 1, 2, 4])) for _ in range(many)]
-        elif kind == "long":
-            pieces = [(1, rng.randint(0, 1), 9), (0, 0, 8)]
+        if kind == "long":
+            pieces = [(rng.randint(0, 1), 9), (rng.randint(0, 1), 8)]
         else:
-            pieces = []
-            for _ in range(many):
-                prefix = rng.randint(0, 1)
-                pieces.append((prefix, prefix and rng.randint(0, 1), rng.choice([1, 1, 2, 3, 4])))
-        pieces = [x + (rng.randint(1, 2),) for x in pieces]
-        simulate(pieces, fp8, seed, slow=seed - 1)  # each warp held back in turn
+            pieces = [({"pairs": 1, "solo": 0}.get(kind, rng.randint(0, 1)), rng.choice([1, 1, 2, 3, 4])) for _ in range(many)]
+        # each warp held back in turn
+        simulate([p + (rng.randint(1, 2),) for p in pieces], fp8, seed, slow=seed - 1)
