@@ -48,7 +48,6 @@
 #include <atomic>
 
 #include "attn_plan.cuh"
-#include "own_attn.cuh"
 #include "common.cuh"
 #include "step_ops.cuh"
 
@@ -109,7 +108,6 @@ struct AttnArgs {
   const float* v_scale;
   const int32_t* page_table;
   const int32_t* seq_lens;
-  const int32_t* skip_pages;  // nullable: columns of each request's table that lie before its tokens
   const uint8_t* abort_mask;
   float* out;
   float* lse;
@@ -455,7 +453,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
     bool ab = false;
     while (ok && next_piece(cur, a, T, W, p)) {
       const int32_t* ptrow = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
-      if (a.skip_pages != nullptr) ptrow += __ldg(a.skip_pages + p.r);
       const int nst = (p.t1 - p.t0 + 1) >> 1;
       auto load_id = [&](int k0) {
         int pg = -1;
@@ -1397,8 +1394,7 @@ int attn_entry(const void* q, const void* kv_pool, const float* k_scale,
                const int32_t* seq_lens, const uint8_t* abort_mask, float* out, float* lse,
                void* workspace, size_t workspace_bytes, int32_t num_splits, float sm_scale,
                int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
-               int32_t num_pages, void* stream, AttnLaunch mode = AttnLaunch::kPlain,
-               const int32_t* skip_pages = nullptr) {
+               int32_t num_pages, void* stream, AttnLaunch mode = AttnLaunch::kPlain) {
   int st = check_attn_args<kFp8>(q, kv_pool, k_scale, v_scale, page_table, max_pages, seq_lens, out,
                                  workspace, true, num_splits, B, Hq, Hkv, D, page_size, num_pages);
   if (st != FPK_OK || B == 0) return st;
@@ -1425,7 +1421,6 @@ int attn_entry(const void* q, const void* kv_pool, const float* k_scale,
   a.v_scale = v_scale;
   a.page_table = page_table;
   a.seq_lens = seq_lens;
-  a.skip_pages = skip_pages;
   a.abort_mask = abort_mask;
   a.out = out;
   a.lse = lse;
@@ -1452,29 +1447,6 @@ int attn_entry(const void* q, const void* kv_pool, const float* k_scale,
 }
 
 }  // namespace
-
-size_t own_attention_bytes(int32_t B, int32_t Hq, int32_t Hkv) { return fpk_decode_workspace_bytes(B, Hq, Hkv, kDim, 0); }
-
-void own_attention_counters(int32_t B, int32_t Hq, int32_t Hkv, size_t* from, size_t* to) {
-  int dev = 0;
-  const int W = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? auto_workers(dev) : 1;
-  // the layout of any split count up to the automatic one has its counters within this one's
-  const WsLayout l = layout(B, Hkv, Hq / Hkv, W > 0 ? W : 1);
-  *from = l.seg_count;
-  *to = l.part_ml;
-}
-
-int own_attention(bool fp8, const void* q, const void* kv_pool, const float* k_scale, const float* v_scale,
-                  const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
-                  const int32_t* skip_pages, const uint8_t* abort_mask, float* out, float* lse, void* workspace,
-                  size_t workspace_bytes, float sm_scale, int32_t B, int32_t Hq, int32_t Hkv, int32_t page_size,
-                  int32_t num_pages, void* stream) {
-  auto entry = fp8 ? attn_entry<true> : attn_entry<false>;
-  return entry(q, kv_pool, k_scale, v_scale, page_table, max_pages, seq_lens, abort_mask, out, lse, workspace,
-               workspace_bytes, 0, sm_scale, B, Hq, Hkv, kDim, page_size, num_pages, stream, AttnLaunch::kPlain,
-               skip_pages);
-}
-
 }  // namespace fpk
 
 extern "C" size_t fpk_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D,

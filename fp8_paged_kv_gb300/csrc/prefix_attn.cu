@@ -3,11 +3,10 @@
 //
 // A group's shared prefix is a matrix product: the rows are the queries of all
 // its requests that read one kv head (requests x GQA group), the columns the
-// prefix's tokens.  What a request has of its own is decode attention as ever
-// (paged_decode_split_kernel, over the tables behind the shared pages): it is
-// bound by HBM, and that kernel keeps twice as many bytes in flight as fit
-// beside the products here.  Four launches: a plan, the own parts, the
-// prefixes, and a merge of each row's partials by log-sum-exp.
+// prefix's tokens.  What a request has of its own is decode attention, bound by
+// HBM.  Four launches: a plan, the own parts, the prefixes, and a merge of each
+// row's partials by log-sum-exp.  (Without groups: paged_decode_split_kernel and
+// the merge, which then only rounds.)
 //
 // * Unit: (group, kv head, up to 256 query rows) over the group's shared pages.
 // * Units are laid end to end in cost (blocks of 128 tokens, dearer for units of
@@ -39,7 +38,7 @@
 // 2^8 since the last time: weights are then at most 2^8, far inside f16.
 #include <atomic>
 
-#include "own_attn.cuh"
+#include "attn_plan.cuh"
 #include "tcgen05.cuh"
 
 namespace fpk {
@@ -94,14 +93,13 @@ struct PfArgs {
   PfGroup* start;    // [ctas] the group in whose units a CTA's range begins: its record, number and the CTA's range
   int32_t* group_of; // [B], -1: none
   int32_t* own_len;  // [B] tokens behind the shared prefix; 0 for a dead request
-  int32_t* skip;     // [B] pages of the shared prefix
   int32_t* dead;     // [B]
-  uint4* counters;   // of the own parts' attention, to be zeroed
-  const float* own_out;  // [B][Hq][D], [B][Hq]: attention over the own tokens
-  const float* own_lse;
-  float2* part_ml;   // partials: 2 per (request, query head), then 256 rows per CTA
+  const uint8_t* kv_pool;
+  const float* all_out;  // without groups: [B][Hq][D], [B][Hq], attention over all tokens
+  const float* all_lse;
+  float2* part_ml;   // partials: prefixes' 2 per (request, query head) and 256 rows per CTA, then own parts' osplits
   float* part_o;
-  int n_groups, B, Hq, Hkv, G, page_size, num_pages, max_pages, ctas, zbox, n_counters;
+  int n_groups, B, Hq, Hkv, G, page_size, num_pages, max_pages, ctas, zbox, osplits;
   uint32_t by_g, by_tpp;  // ceil(2^32 / G), ceil(2^32 / tiles of a page); 0 for 1
   float sm_scale_log2;
 };
@@ -294,8 +292,6 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
   const unsigned kFull = 0xffffffffu;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int tpp = a.page_size >> 4;
-#pragma unroll 1
-  for (int i = t; i < a.n_counters; i += kPfPlanThreads) a.counters[i] = make_uint4(0, 0, 0, 0);
   // group starts: clamped, then the running maximum
   int carry = 0;
 #pragma unroll 1
@@ -324,7 +320,6 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
   for (int r = t; r < a.B; r += kPfPlanThreads) {
     const int L = live_length(a, r);
     a.own_len[r] = L;
-    a.skip[r] = 0;
     a.group_of[r] = -1;
     a.dead[r] = L == 0;
   }
@@ -356,7 +351,6 @@ __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const Pf
 #pragma unroll 1
     for (int r = lo + lane; r < hi; r += 32) {
       a.own_len[r] = max(0, a.own_len[r] - pages * a.page_size);
-      a.skip[r] = pages;
       a.group_of[r] = g;
     }
   }
@@ -1162,11 +1156,317 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
+// own parts
+// ---------------------------------------------------------------------------
+// A request's own tokens, kv head by kv head, in up to osplits splits of at
+// least 256 tokens: a CTA of four warps per split, a warp taking every fourth
+// tile of 16 tokens straight from the pool into registers (mma.sync: the rows
+// are the at most eight heads of a GQA group, which is too few for a tcgen05
+// tile, and the work is reading).  The layout of the pool suits the fragments
+// with the dims of K and the tokens of V permuted: lane (g, c) = (lane / 4,
+// lane % 4) holds dims 32 c .. 32 c + 31 of its K tokens -- step kk of S takes
+// 32 c + 4 kk .. + 3 of q and K alike -- and tokens 4 c .. 4 c + 3 of its V dims,
+// which are the very tokens of the scores that the lane holds for head g: P
+// enters the second product from the registers where S left it.
+constexpr int kOwnWarps = 4;
+constexpr int kOwnMinTiles = 16;  // of a split
+constexpr float kOwnFails = -1.f;  // sum of a split with a page outside the pool
+__device__ __forceinline__ int own_splits(int tiles, int most) {
+  return min(most, (tiles + kOwnMinTiles - 1) / kOwnMinTiles);
+}
+// First slot of the own parts' partials: split z of row i is at own_slot0 + z rows + i.
+__device__ __forceinline__ int64_t own_slot0(const PfArgs& a) {
+  return static_cast<int64_t>(2) * a.B * a.Hq + static_cast<int64_t>(a.ctas) * kPfUnitRows;
+}
+
+// K and V words of one tile as the lane needs them: K 8 (16) words of two tokens, V 16 quads of tokens.
+template <bool kFp8>
+struct OwnTile {
+  uint4 k[2][kFp8 ? 2 : 4];
+  uint32_t v[kFp8 ? 16 : 32];
+};
+
+template <bool kFp8>
+__device__ __forceinline__ void own_load(OwnTile<kFp8>& x, const uint8_t* tile, int lane) {
+  constexpr int el = kFp8 ? 1 : 2;
+  const int g = lane >> 2, c = lane & 3;
+  const int tok = 4 * (g >> 1) + (g & 1);  // scores' column g of either half: tokens tok, tok + 2
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int i = 0; i < 2 * el; ++i)
+      x.k[n][i] = __ldg(reinterpret_cast<const uint4*>(tile + ((tok + 2 * n) * kPfDim + 32 * c) * el) + i);
+  const uint8_t* v = tile + kPfTile * kPfDim * el + (g * kPfTile + 4 * c) * el;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (kFp8) {
+      x.v[i] = __ldg(reinterpret_cast<const uint32_t*>(v + i * 8 * kPfTile));
+    } else {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(v + i * 8 * kPfTile * 2));
+      x.v[2 * i] = w.x;
+      x.v[2 * i + 1] = w.y;
+    }
+  }
+}
+
+template <bool kFp8>
+__device__ __forceinline__ void own_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (kFp8) mma_f16(d, a, b0, b1);
+  else mma_bf16(d, a, b0, b1);
+}
+
+// The pages that request r shares, found by one CTA on its own (as the planning kernel finds them for all):
+// its group ends at the first start above r.
+__device__ __forceinline__ int shared_pages(const PfArgs& a, int r) {
+  __shared__ int s_first[kOwnWarps], s_lo[kOwnWarps], s_least[kOwnWarps];
+  const unsigned kFull = 0xffffffffu;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  auto start = [&](int i) -> int { return min(max(__ldg(a.group_starts + i), 0), a.B); };
+  int first = 0x7fffffff;
+#pragma unroll 1
+  for (int i = t; i <= a.n_groups && first == 0x7fffffff; i += 32 * kOwnWarps)
+    if (start(i) > r) first = i;
+  first = __reduce_min_sync(kFull, first);
+  if (lane == 0) s_first[warp] = first;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kOwnWarps; ++w) first = min(first, s_first[w]);
+  if (first == 0 || first > a.n_groups) return 0;
+  int lo = 0;
+#pragma unroll 1
+  for (int i = t; i < first; i += 32 * kOwnWarps) lo = max(lo, start(i));
+  lo = __reduce_max_sync(kFull, lo);
+  if (lane == 0) s_lo[warp] = lo;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kOwnWarps; ++w) lo = max(lo, s_lo[w]);
+  const int hi = start(first);
+  if (hi - lo < 2) return 0;
+  int least = 0x7fffffff;
+#pragma unroll 1
+  for (int i = lo + t; i < hi; i += 32 * kOwnWarps) {
+    const int L = live_length(a, i);
+    if (L > 0) least = min(least, L);
+  }
+  least = __reduce_min_sync(kFull, least);
+  if (lane == 0) s_least[warp] = least;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kOwnWarps; ++w) least = min(least, s_least[w]);
+  return max(0, min(__ldg(a.prefix_lens + first - 1), least)) / a.page_size;
+}
+
+template <bool kFp8>
+__device__ __forceinline__ void own_part(const PfArgs& a) {
+  __shared__ float s_o[kOwnWarps][kPfGroupMax][kPfDim + 4];
+  __shared__ float2 s_ml[kOwnWarps][kPfGroupMax];
+  const unsigned kFull = 0xffffffffu;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const int z = static_cast<int>(blockIdx.x) % a.osplits, seg = static_cast<int>(blockIdx.x) / a.osplits;
+  const int r = seg / a.Hkv, h = seg - r * a.Hkv;
+  const int live = live_length(a, r), skip = shared_pages(a, r);
+  const int L = max(0, live - skip * a.page_size);
+  const int tiles = (L + kPfTile - 1) / kPfTile, n = own_splits(tiles, a.osplits);
+  if (z >= n) return;
+  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * z / n);
+  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (z + 1) / n);
+  const int tpp = a.page_size >> 4;
+  constexpr int tile_bytes = 2 * kPfTile * kPfDim * (kFp8 ? 1 : 2);
+  const int32_t* row = a.page_table + static_cast<int64_t>(r) * a.max_pages + skip;
+  auto page_of = [&](int t) -> int { return t < t1 ? __ldg(row + quotient(t, a.by_tpp)) : -1; };
+  auto good = [&](int page) -> bool { return page >= 0 && page < a.num_pages; };
+  auto at = [&](int t, int page) -> const uint8_t* {
+    return a.kv_pool +
+           ((static_cast<int64_t>(page) * a.Hkv + h) * tpp + t - quotient(t, a.by_tpp) * tpp) * tile_bytes;
+  };
+  int t = t0 + warp;
+  int page = page_of(t), next = page_of(t + kOwnWarps);
+  OwnTile<kFp8> x;
+  bool have = good(page);
+  if (have) own_load<kFp8>(x, at(t, page), lane);
+  // ---- queries of the GQA group (head g): A fragments, rows 8 .. 15 zero; e4m3: f16 of q 2^e
+  uint32_t qa[8][2];
+  float mult = fabsf(a.sm_scale_log2) * (kFp8 ? __ldg(a.k_scale) : 1.f);
+  {
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = g < a.G ? __ldg(reinterpret_cast<const uint4*>(
+                                 a.q + (static_cast<int64_t>(r) * a.Hq + h * a.G + g) * kPfDim + 32 * c) + i)
+                     : make_uint4(0, 0, 0, 0);
+    const uint32_t flip = a.sm_scale_log2 < 0.f ? 0x80008000u : 0u;
+    uint32_t q[16] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w,
+                      w[2].x, w[2].y, w[2].z, w[2].w, w[3].x, w[3].y, w[3].z, w[3].w};
+    if (kFp8) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = max(top, max(q[i] & 0x7FFFu, (q[i] >> 16) & 0x7FFFu));
+      top = max(top, __shfl_xor_sync(kFull, top, 1));
+      top = max(top, __shfl_xor_sync(kFull, top, 2));
+      const int ex = static_cast<int>(top >> 7);
+      const int e = ex == 0 ? (top == 0 ? 0 : 126) : min(max(134 - ex, -126), 126);
+      const float up = __int_as_float((127 + e) << 23);
+      mult = ex == 255 ? __int_as_float(0x7fffffff) : mult * __int_as_float((127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        q[i] = pack_f16x2(__uint_as_float(q[i] << 16) * up, __uint_as_float(q[i] & 0xFFFF0000u) * up);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      qa[i][0] = q[2 * i] ^ flip;
+      qa[i][1] = q[2 * i + 1] ^ flip;
+    }
+  }
+  float m = -INFINITY, l = 0.f, o[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+  bool bad = false;
+#pragma unroll 1
+  for (; t < t1; t += kOwnWarps) {
+    if (!have) {
+      bad = true;  // a page outside the pool
+      page = next;
+      next = page_of(t + 2 * kOwnWarps);
+      have = good(page);
+      if (have) own_load<kFp8>(x, at(t + kOwnWarps, page), lane);
+      continue;
+    }
+    // ---- scores of head g, tokens 4 c .. 4 c + 3
+    float s[2][4] = {};
+#pragma unroll
+    for (int n2 = 0; n2 < 2; ++n2) {
+      const uint32_t* kw = reinterpret_cast<const uint32_t*>(x.k[n2]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t b0, b1;
+        if (kFp8) {
+          e4m3x4_to_f16x4(kw[i], b0, b1);
+        } else {
+          b0 = kw[2 * i];
+          b1 = kw[2 * i + 1];
+        }
+        const uint32_t af[4] = {qa[i][0], 0u, qa[i][1], 0u};
+        own_mma<kFp8>(s[n2], af, b0, b1);
+      }
+    }
+    uint32_t v[16][2];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (kFp8) {
+        e4m3x4_to_f16x4(x.v[i], v[i][0], v[i][1]);
+      } else {
+        v[i][0] = x.v[2 * i];
+        v[i][1] = x.v[2 * i + 1];
+      }
+    }
+    // ---- the next tile's loads under this one's softmax and second product
+    page = next;
+    next = page_of(t + 2 * kOwnWarps);
+    have = good(page);
+    if (have) own_load<kFp8>(x, at(t + kOwnWarps, page), lane);
+    float e[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};
+    const int left = L - t * kPfTile - 4 * c;  // tokens of this lane's four that exist
+    if (L - t * kPfTile < kPfTile) {
+      // an unwritten slot may hold NaN: no score, and no value
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k >= left) e[k] = -INFINITY;
+      const uint32_t m01 = left >= 2 ? 0xFFFFFFFFu : left == 1 ? 0xFFFFu : 0u;
+      const uint32_t m23 = left >= 4 ? 0xFFFFFFFFu : left == 3 ? 0xFFFFu : 0u;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        v[i][0] &= m01;
+        v[i][1] &= m23;
+      }
+    }
+    float mx = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+    const float scale = fmaxf(mult, kPfMinMult);
+    const float mb = mx == -INFINITY ? -INFINITY : mx * (mult != mult ? mult : scale);
+    const bool grown = mb > m || (m == -INFINITY && mb != -INFINITY);
+    if (__any_sync(kFull, grown)) {
+      const float f = !grown ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - mb);
+      if (grown) m = mb;
+      l *= f;
+      // O's columns are heads 2 c, 2 c + 1
+      const float f0 = __shfl_sync(kFull, f, 8 * c), f1 = __shfl_sync(kFull, f, 8 * c + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i][0] *= f0;
+        o[i][1] *= f1;
+        o[i][2] *= f0;
+        o[i][3] *= f1;
+      }
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    const float mul = mult != mult ? mult : scale;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      e[k] = fast_exp2(fmaf(e[k], mul, -ref));
+      l += e[k];
+    }
+    const uint32_t p0 = kFp8 ? pack_f16x2(e[0], e[1]) : pack_bf16x2(e[0], e[1]);
+    const uint32_t p1 = kFp8 ? pack_f16x2(e[2], e[3]) : pack_bf16x2(e[2], e[3]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t af[4] = {v[2 * i][0], v[2 * i + 1][0], v[2 * i][1], v[2 * i + 1][1]};
+      own_mma<kFp8>(o[i], af, p0, p1);
+    }
+  }
+  // ---- the four warps' states
+  l += __shfl_xor_sync(kFull, l, 1);
+  l += __shfl_xor_sync(kFull, l, 2);
+  if (c == 0) s_ml[warp][g] = make_float2(m, l);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    s_o[warp][2 * c][16 * i + g] = o[i][0];
+    s_o[warp][2 * c + 1][16 * i + g] = o[i][1];
+    s_o[warp][2 * c][16 * i + 8 + g] = o[i][2];
+    s_o[warp][2 * c + 1][16 * i + 8 + g] = o[i][3];
+  }
+  const bool fails = __syncthreads_or(bad);
+  const float vscale = kFp8 ? __ldg(a.v_scale) : 1.f;
+  const int64_t slot = own_slot0(a) + static_cast<int64_t>(z) * a.B * a.Hq + static_cast<int64_t>(r) * a.Hq + h * a.G;
+  for (int hd = warp; hd < a.G; hd += kOwnWarps) {
+    float M = -INFINITY, W = 0.f;
+#pragma unroll
+    for (int w = 0; w < kOwnWarps; ++w) M = fmaxf(M, s_ml[w][hd].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kOwnWarps; ++w) {
+      const float2 ml = s_ml[w][hd];
+      if (ml.x == -INFINITY) continue;
+      const float f = fast_exp2(ml.x - M);
+      const float4 y = *reinterpret_cast<const float4*>(&s_o[w][hd][4 * lane]);
+      W = fmaf(ml.y, f, W);
+      acc.x = fmaf(y.x, f, acc.x);
+      acc.y = fmaf(y.y, f, acc.y);
+      acc.z = fmaf(y.z, f, acc.z);
+      acc.w = fmaf(y.w, f, acc.w);
+    }
+    *reinterpret_cast<float4*>(a.part_o + (slot + hd) * kPfDim + 4 * lane) =
+        make_float4(acc.x * vscale, acc.y * vscale, acc.z * vscale, acc.w * vscale);
+    if (lane == 0) a.part_ml[slot + hd] = fails ? make_float2(0.f, kOwnFails) : make_float2(M, W);
+  }
+}
+
+// Runs beside the planning kernel: it needs nothing of it.  Its end implies that kernel's, though: one CTA waits.
+template <bool kFp8>
+__global__ void __launch_bounds__(32 * kOwnWarps, kFp8 ? 4 : 3) prefix_own_kernel(const PfArgs a) {
+  griddep_launch_dependents();
+  own_part<kFp8>(a);
+  if (blockIdx.x == 0) griddep_wait();
+}
+
+// ---------------------------------------------------------------------------
 // merge
 // ---------------------------------------------------------------------------
-// One warp per (request, query head): attention over the own tokens, and the
-// partials of the pieces of the row's unit in the order of the work list.  A lane
-// finds one partial (row in the partial arrays, m, l), then all lanes add its O.
+// One warp per (request, query head): the partials of its own splits and those
+// of the pieces of its unit, in that order.  A lane finds one partial (its row in
+// the partial arrays, m, l), then all lanes add its O.
 __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const PfArgs a) {
   const unsigned kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31;
@@ -1175,79 +1475,87 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
   griddep_wait();
   if (row >= rows) return;
   uint2* const out = reinterpret_cast<uint2*>(a.out + row * kPfDim) + lane;
+  if (a.n_groups == 0) {
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(a.all_out + row * kPfDim) + lane);
+    *out = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    if (lane == 0 && a.lse != nullptr) a.lse[row] = __ldcg(a.all_lse + row);
+    return;
+  }
   const int r = static_cast<int>(row / a.Hq), hq = static_cast<int>(row - static_cast<int64_t>(r) * a.Hq);
-  const float own_lse = __ldcg(a.own_lse + row);
-  float4 acc = __ldcg(reinterpret_cast<const float4*>(a.own_out + row * kPfDim) + lane);
-  bool dead = false;
-  float M = own_lse * kPfLog2e, W = own_lse == -INFINITY ? 0.f : 1.f;
-  if (W == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (a.n_groups > 0) {
-    // own tokens without a result: a page of theirs is outside the pool
-    dead = __ldcg(a.dead + r) != 0 || (own_lse == -INFINITY && __ldcg(a.own_len + r) > 0);
-    const int gi = __ldcg(a.group_of + r);
-    if (!dead && gi >= 0) {
+  const int L = __ldcg(a.own_len + r), gi = __ldcg(a.group_of + r);
+  bool dead = __ldcg(a.dead + r) != 0;
+  float M = -INFINITY, W = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!dead) {
+    const int own = own_splits((L + kPfTile - 1) / kPfTile, a.osplits);
+    int cands = own, y = 0, blocks = 0, w = kPfCostSolo, subs = 0, c0 = 0, lrow = 0;
+    PfRanges rg = {0, 0};
+    if (gi >= 0) {
       const PfGroup q = load_group(a.group + gi);
-      const PfRanges rg = [&] {  // from the last CTA's range: its end is the list's
-        return ranges_of(load_group(a.start + a.ctas - 1).b1, a.ctas);
-      }();
+      rg = ranges_of(load_group(a.start + a.ctas - 1).b1, a.ctas);  // (the last range ends where the list does)
       const PfPrefix s = prefix_shape(q.ptiles, q.count, a.G);
       const int h = quotient(hq, a.by_g);
-      const int i = (r - q.first) * a.G + hq - h * a.G, u = i / kPfUnitRows, lrow = i % kPfUnitRows;
-      const int w = u == s.units - 1 ? s.wlast : kPfCostPair;
-      const int y = q.y0 + h * s.head_cost + u * s.step + start_cost(w);
-      const int subs = w == kPfCostPair ? 0 : 1;  // log2 of the row tiles with a partial each
-      const int c0 = rg.owner(y), c1 = rg.owner(y + (s.blocks - 1) * w);
-      const int cands = (c1 - c0 + 1) << subs;
+      const int i = (r - q.first) * a.G + hq - h * a.G, u = i / kPfUnitRows;
+      lrow = i % kPfUnitRows;
+      blocks = s.blocks;
+      w = u == s.units - 1 ? s.wlast : kPfCostPair;
+      y = q.y0 + h * s.head_cost + u * s.step + start_cost(w);
+      subs = w == kPfCostPair ? 0 : 1;  // log2 of the row tiles with a partial each
+      c0 = rg.owner(y);
+      cands += (rg.owner(y + (blocks - 1) * w) - c0 + 1) << subs;
+    }
 #pragma unroll 1
-      for (int base = 0; base < cands; base += 32) {
-        const int k = base + lane;
-        float2 ml = make_float2(-INFINITY, 0.f);
-        int64_t slot = 0;
-        if (k < cands) {
-          const int c = c0 + (k >> subs), sub = k & subs;
-          int i0, i1;
-          owned_blocks(y, s.blocks, w, rg.begin(c), rg.begin(c + 1), i0, i1);
-          slot = i0 == 0 ? sub * rows + row : 2 * rows + static_cast<int64_t>(c) * kPfUnitRows + sub * 128 + lrow;
-          if (i0 < i1) ml = __ldcg(a.part_ml + slot);
+    for (int base = 0; base < cands; base += 32) {
+      const int k = base + lane;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      int64_t slot = own_slot0(a) + k * rows + row;
+      bool there = k < own;
+      if (k >= own && k < cands) {
+        const int c = c0 + ((k - own) >> subs), sub = (k - own) & subs;
+        int i0, i1;
+        owned_blocks(y, blocks, w, rg.begin(c), rg.begin(c + 1), i0, i1);
+        slot = i0 == 0 ? sub * rows + row : 2 * rows + static_cast<int64_t>(c) * kPfUnitRows + sub * 128 + lrow;
+        there = i0 < i1;
+      }
+      if (there) ml = __ldcg(a.part_ml + slot);
+      dead = __any_sync(kFull, ml.y < 0.f) || dead;
+      float mx = ml.x;
+#pragma unroll 1
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      const float mn = fmaxf(M, mx);
+      const bool has = ml.x != -INFINITY;  // a NaN maximum counts
+      const float f = has ? fast_exp2(ml.x - mn) : 0.f;
+      float ws = ml.y * f;
+#pragma unroll 1
+      for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(kFull, ws, o);
+      const float old = M == -INFINITY ? 0.f : fast_exp2(M - mn);
+      W = W * old + ws;
+      acc.x *= old;
+      acc.y *= old;
+      acc.z *= old;
+      acc.w *= old;
+      M = mn;
+      unsigned todo = __ballot_sync(kFull, has);
+#pragma unroll 1
+      while (todo) {
+        float fk[4];
+        float4 o[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int src = todo ? __ffs(todo) - 1 : 0;
+          const float fx = __shfl_sync(kFull, f, src);
+          const int64_t sx = __shfl_sync(kFull, slot, src);
+          fk[x] = todo ? fx : 0.f;
+          o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (todo) o[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + sx * kPfDim) + lane);
+          todo &= todo - 1;
         }
-        float mx = ml.x;
-#pragma unroll 1
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-        const float mn = fmaxf(M, mx);
-        const bool has = ml.x != -INFINITY;  // a NaN maximum counts
-        const float f = has ? fast_exp2(ml.x - mn) : 0.f;
-        float ws = ml.y * f;
-#pragma unroll 1
-        for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(kFull, ws, o);
-        const float old = M == -INFINITY ? 0.f : fast_exp2(M - mn);
-        W = W * old + ws;
-        acc.x *= old;
-        acc.y *= old;
-        acc.z *= old;
-        acc.w *= old;
-        M = mn;
-        unsigned todo = __ballot_sync(kFull, has);
-#pragma unroll 1
-        while (todo) {
-          float fk[4];
-          float4 o[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int src = todo ? __ffs(todo) - 1 : 0;
-            const float fx = __shfl_sync(kFull, f, src);
-            const int64_t sx = __shfl_sync(kFull, slot, src);
-            fk[x] = todo ? fx : 0.f;
-            o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (todo) o[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + sx * kPfDim) + lane);
-            todo &= todo - 1;
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            acc.x = fmaf(o[x].x, fk[x], acc.x);
-            acc.y = fmaf(o[x].y, fk[x], acc.y);
-            acc.z = fmaf(o[x].z, fk[x], acc.z);
-            acc.w = fmaf(o[x].w, fk[x], acc.w);
-          }
+        for (int x = 0; x < 4; ++x) {
+          acc.x = fmaf(o[x].x, fk[x], acc.x);
+          acc.y = fmaf(o[x].y, fk[x], acc.y);
+          acc.z = fmaf(o[x].z, fk[x], acc.z);
+          acc.w = fmaf(o[x].w, fk[x], acc.w);
         }
       }
     }
@@ -1276,21 +1584,25 @@ int prepare_prefix(int dev) {
   return FPK_OK;
 }
 
+// Most splits of a request's own tokens per kv head: about four waves of CTAs of four per SM in all.
+int own_splits_most(int64_t B, int64_t Hkv, int64_t ctas) {
+  const int64_t n = 16 * ctas / (B * Hkv > 0 ? B * Hkv : 1);
+  return static_cast<int>(n < 1 ? 1 : n > 32 ? 32 : n);
+}
+
 struct PfLayout {
-  size_t gstart, group, start, per_request, own_out, own_lse, ml, o, total;
+  size_t gstart, group, start, per_request, ml, o, total;
 };
-// Behind the workspace of the own parts' attention (whose first word is the status word of both).
-PfLayout prefix_layout(int64_t B, int64_t Hq, int64_t ctas, size_t own_bytes) {
+// Behind the workspace of decode attention (batches without groups; its first word is the status word).
+PfLayout prefix_layout(int64_t B, int64_t Hq, int64_t Hkv, int64_t ctas, size_t decode_bytes) {
   auto up = [](int64_t x) { return (static_cast<size_t>(x) + 255) & ~static_cast<size_t>(255); };
-  const int64_t slots = 2 * B * Hq + ctas * kPfUnitRows;
+  const int64_t slots = 2 * B * Hq + ctas * kPfUnitRows + own_splits_most(B, Hkv, ctas) * B * Hq;
   PfLayout l;
-  l.gstart = up(static_cast<int64_t>(own_bytes));
+  l.gstart = up(static_cast<int64_t>(decode_bytes));
   l.group = l.gstart + up((B + 1) * 4);
   l.start = l.group + up(B * static_cast<int64_t>(sizeof(PfGroup)));
   l.per_request = l.start + up(ctas * static_cast<int64_t>(sizeof(PfGroup)));
-  l.own_out = l.per_request + up(4 * B * 4);
-  l.own_lse = l.own_out + up(B * Hq * kPfDim * 4);
-  l.ml = l.own_lse + up(B * Hq * 4);
+  l.ml = l.per_request + up(3 * B * 4);
   l.o = l.ml + up(slots * 8);
   l.total = l.o + up(slots * kPfDim * 4);
   return l;
@@ -1330,6 +1642,15 @@ int launch_dependent(void (*kernel)(Exp...), int grid, int threads, size_t smem,
   return checked_launch_status();
 }
 
+// Bytes behind the first 256 of a decode attention workspace that hold its arrival counters, for any
+// split count up to two CTAs per SM and more.
+size_t decode_counter_bytes(int64_t B, int64_t Hq, int64_t Hkv) {
+  int dev = 0;
+  const int W = cudaGetDevice(&dev) == cudaSuccess ? 4 * device_sm_count(dev) : 0;
+  const WsLayout l = layout(B, Hkv, Hq / Hkv, W);
+  return l.part_ml - l.seg_count;
+}
+
 template <bool kFp8>
 int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const float* v_scale,
                  const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
@@ -1362,9 +1683,9 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kPfMaxDevices) return FPK_ECUDA;
   const int ctas = device_sm_count(dev);
   if (ctas <= 0) return FPK_ECUDA;
-  const size_t own_bytes = own_attention_bytes(B, Hq, Hkv);
-  if (own_bytes == 0) return FPK_ECUDA;
-  const PfLayout l = prefix_layout(B, Hq, ctas, own_bytes);
+  const size_t decode_bytes = fpk_decode_workspace_bytes(B, Hq, Hkv, D, 0);
+  if (decode_bytes == 0) return FPK_ECUDA;
+  const PfLayout l = prefix_layout(B, Hq, Hkv, ctas, decode_bytes);
   if (workspace_bytes < l.total) return FPK_ENOSPC;
   const int st = prepare_prefix<kFp8>(dev);
   if (st != FPK_OK) return st;
@@ -1392,10 +1713,11 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   a.start = reinterpret_cast<PfGroup*>(ws + l.start);
   a.group_of = reinterpret_cast<int32_t*>(ws + l.per_request);
   a.own_len = a.group_of + B;
-  a.skip = a.own_len + B;
-  a.dead = a.skip + B;
-  a.own_out = reinterpret_cast<float*>(ws + l.own_out);
-  a.own_lse = reinterpret_cast<float*>(ws + l.own_lse);
+  a.dead = a.own_len + B;
+  a.all_out = reinterpret_cast<float*>(ws + l.o);
+  a.all_lse = reinterpret_cast<float*>(ws + l.ml);
+  a.kv_pool = static_cast<const uint8_t*>(kv_pool);
+  a.osplits = own_splits_most(B, Hkv, ctas);
   a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
   a.part_o = reinterpret_cast<float*>(ws + l.o);
   a.n_groups = n_groups;
@@ -1412,25 +1734,28 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   a.by_tpp = tpp == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + tpp - 1) / tpp);
   a.sm_scale_log2 = sm_scale * kPfLog2e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool groups = n_groups > 0;
-  size_t from = 0, to = 0;
-  own_attention_counters(B, Hq, Hkv, &from, &to);
-  a.counters = reinterpret_cast<uint4*>(ws + from);
-  a.n_counters = static_cast<int>((to - from) / sizeof(uint4));
-  if (!groups && cudaMemsetAsync(ws + from, 0, to - from, s) != cudaSuccess) return FPK_ECUDA;
-  if (groups) {
-    prefix_plan_kernel<<<1, kPfPlanThreads, 0, s>>>(a);
-    if (checked_launch_status() != FPK_OK) return FPK_ECUDA;
-  }
-  // without groups the own parts are all there is, and their kernel knows dead requests by itself
-  const int own = own_attention(kFp8, q, kv_pool, k_scale, v_scale, page_table, max_pages, groups ? a.own_len : seq_lens,
-                                groups ? a.skip : nullptr, groups ? nullptr : abort_mask,
-                                reinterpret_cast<float*>(ws + l.own_out), reinterpret_cast<float*>(ws + l.own_lse), ws,
-                                own_bytes, sm_scale, B, Hq, Hkv, page_size, num_pages, stream);
-  if (own != FPK_OK) return own;
-  if (groups && launch_dependent(prefix_attn_kernel<kFp8>, ctas, kPfThreads, PfCfg<kFp8>::kSmem, s, a, kmap, vmap) != FPK_OK)
-    return FPK_ECUDA;
   const int merge = static_cast<int>((static_cast<int64_t>(B) * Hq + kPfMergeWarps - 1) / kPfMergeWarps);
+  if (n_groups == 0) {
+    // the arrival counters of decode attention, which lie elsewhere for other shapes, begin at zero
+    if (cudaMemsetAsync(ws + 256, 0, decode_counter_bytes(B, Hq, Hkv), s) != cudaSuccess) return FPK_ECUDA;
+    float* all_out = reinterpret_cast<float*>(ws + l.o);
+    float* all_lse = reinterpret_cast<float*>(ws + l.ml);
+    const int done =
+        kFp8 ? fpk_paged_decode_attn_fp8(q, static_cast<const uint8_t*>(kv_pool), k_scale, v_scale, page_table, max_pages,
+                                         seq_lens, abort_mask, all_out, all_lse, ws, decode_bytes, 0, sm_scale, B, Hq,
+                                         Hkv, D, page_size, num_pages, stream)
+             : fpk_paged_decode_attn_bf16(q, kv_pool, page_table, max_pages, seq_lens, abort_mask, all_out, all_lse, ws,
+                                          decode_bytes, 0, sm_scale, B, Hq, Hkv, D, page_size, num_pages, stream);
+    if (done != FPK_OK) return done;
+    return launch_dependent(prefix_merge_kernel, merge, 32 * kPfMergeWarps, 0, s, a);
+  }
+  const int64_t own = static_cast<int64_t>(B) * Hkv * a.osplits;
+  if (own > 0x7fffffff) return FPK_EUNSUPPORTED;
+  prefix_plan_kernel<<<1, kPfPlanThreads, 0, s>>>(a);
+  if (checked_launch_status() != FPK_OK) return FPK_ECUDA;
+  if (launch_dependent(prefix_own_kernel<kFp8>, static_cast<int>(own), 32 * kOwnWarps, 0, s, a) != FPK_OK ||
+      launch_dependent(prefix_attn_kernel<kFp8>, ctas, kPfThreads, PfCfg<kFp8>::kSmem, s, a, kmap, vmap) != FPK_OK)
+    return FPK_ECUDA;
   return launch_dependent(prefix_merge_kernel, merge, 32 * kPfMergeWarps, 0, s, a);
 }
 
@@ -1442,8 +1767,8 @@ extern "C" size_t fpk_prefix_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv,
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= fpk::kPfMaxDevices) return 0;
   const int ctas = fpk::device_sm_count(dev);
-  const size_t own = fpk::own_attention_bytes(B, Hq, Hkv);
-  return ctas > 0 && own > 0 ? fpk::prefix_layout(B, Hq, ctas, own).total : 0;
+  const size_t decode = fpk_decode_workspace_bytes(B, Hq, Hkv, D, 0);
+  return ctas > 0 && decode > 0 ? fpk::prefix_layout(B, Hq, Hkv, ctas, decode).total : 0;
 }
 
 extern "C" int fpk_paged_decode_attn_fp8_prefix(const void* q, const uint8_t* kv_pool, const float* k_scale,
