@@ -528,6 +528,18 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       : "memory");
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// 32 bytes: a whole sector from one thread.
+__device__ __forceinline__ void st_global8(float* dst, const float (&x)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+               "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
+
 // Packed fp32 pairs and the three-input maximum: one instruction each on sm_103a.
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
   float2 r;
@@ -657,66 +669,88 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     ++pn;
     return __all_sync(kFull, p.i0 < p.i1 && !*s_failed);
   };
-  // query rows [row, row + n) of a unit, by one warp, into rows `at`.. of a query buffer: half a warp per row
-  // (a lane: 8 dims), the next rows' loads ahead
+  // query rows [row, row + n) of a unit, by one warp, into rows `at`.. of a query buffer: all rows are asked for
+  // at once (half a warp per row, a lane 8 dims), to where bf16 has its two halves of the dims; e4m3's two
+  // parts of a row take the same 256 bytes
   auto stage_rows = [&](const PfPiece& p, int buf, int row, int at, int n) {
-    const int c = lane & 15;
-    auto load = [&](int k) -> uint4 {
-      const int i = k + (lane >> 4), g = p.row0 + row + i;
-      if (i >= n) return make_uint4(0, 0, 0, 0);
-      const int r = quotient(g, a.by_g);
-      return __ldg(reinterpret_cast<const uint4*>(
-                       a.q + (static_cast<int64_t>(p.gfirst + r) * a.Hq + p.h * a.G + g - r * a.G) * kPfDim) + c);
-    };
+    const int c = lane & 15, hw = lane >> 4;
+    uint8_t* const tile = sm + buf * C::kQTile;
+    auto chunk = [&](int rr) -> uint8_t* { return tile + (c >> 3) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4); };
+    int g = p.row0 + row + hw, r = quotient(g, a.by_g), h = g - r * a.G;  // request and head of the row
+    const uint16_t* src = a.q + (static_cast<int64_t>(p.gfirst + r) * a.Hq + p.h * a.G + h) * kPfDim + c * 8;
+#pragma unroll 1
+    for (int i = hw; i < n; i += 2) {
+      cp_async16(smem_addr(chunk(at + i)), src);
+      h += 2;
+      src += 2 * kPfDim;
+      while (h >= a.G) {
+        h -= a.G;
+        src += static_cast<int64_t>(a.Hq - a.G) * kPfDim;
+      }
+    }
     const float base = fabsf(a.sm_scale_log2) * (kFp8 ? __ldg(a.k_scale) : 1.f);
     // a negative scale's sign goes to the query: maxima of raw scores are then those of scaled ones
     const uint32_t flip = a.sm_scale_log2 < 0.f ? 0x80008000u : 0u;
-    uint4 x0 = load(0), x1 = load(2), x2 = load(4), x3 = load(6);
+    cp_async_wait_all();
+    if (kFp8) {
 #pragma unroll 1
-    for (int k = 0; k < n; k += 2) {
-      const uint32_t w[4] = {x0.x ^ flip, x0.y ^ flip, x0.z ^ flip, x0.w ^ flip};
-      x0 = x1;
-      x1 = x2;
-      x2 = x3;
-      x3 = load(k + 8);
-      const int rr = at + k + (lane >> 4);
-      uint8_t* const dst = sm + buf * C::kQTile + rr * 128;
-      if (kFp8) {
-        uint32_t top = 0;  // largest |q|: bf16 magnitudes order as integers
+      for (int k = 0; k < n; k += 4) {
+        uint32_t w[2][4], top[2] = {0, 0};  // largest |q|: bf16 magnitudes order as integers
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+        for (int y = 0; y < 2; ++y) {
+          const int i = k + 2 * y + hw;
+          const uint4 x = i < n ? *reinterpret_cast<const uint4*>(chunk(at + i)) : make_uint4(0, 0, 0, 0);
+          w[y][0] = x.x ^ flip;
+          w[y][1] = x.y ^ flip;
+          w[y][2] = x.z ^ flip;
+          w[y][3] = x.w ^ flip;
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-        // e4m3 parts of q 2^e with its largest value in [128, 256): e = 134 - its exponent
-        const int ex = static_cast<int>(top >> 7);
-        const int e = ex == 0 ? (top == 0 ? 0 : 126) : min(max(134 - ex, -126), 126);
-        const float up = __int_as_float((127 + e) << 23);
-        uint32_t c0[2], c1[2];
+          for (int z = 0; z < 4; ++z) top[y] = max(top[y], max(w[y][z] & 0x7FFFu, (w[y][z] >> 16) & 0x7FFFu));
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float lo = __uint_as_float(w[i] << 16) * up, hi = __uint_as_float(w[i] & 0xFFFF0000u) * up;
-          const uint32_t u = f32x2_to_e4m3x2(lo, hi);
-          const float2 f = e4m3x2_to_float2(u);
-          const uint32_t v = f32x2_to_e4m3x2(lo - f.x, hi - f.y);
-          if (i & 1) {
-            c0[i >> 1] |= u << 16;
-            c1[i >> 1] |= v << 16;
-          } else {
-            c0[i >> 1] = u;
-            c1[i >> 1] = v;
+        for (int o = 1; o < 16; o <<= 1) {
+          const uint32_t t0 = __shfl_xor_sync(kFull, top[0], o), t1 = __shfl_xor_sync(kFull, top[1], o);
+          top[0] = max(top[0], t0);
+          top[1] = max(top[1], t1);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int i = k + 2 * y + hw, rr = at + i;
+          // e4m3 parts of q 2^e with its largest value in [128, 256): e = 134 - its exponent
+          const int ex = static_cast<int>(top[y] >> 7);
+          const int e = ex == 0 ? (top[y] == 0 ? 0 : 126) : min(max(134 - ex, -126), 126);
+          const float up = __int_as_float((127 + e) << 23);
+          uint32_t c0[2], c1[2];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const float lo = __uint_as_float(w[y][z] << 16) * up, hi = __uint_as_float(w[y][z] & 0xFFFF0000u) * up;
+            const uint32_t u = f32x2_to_e4m3x2(lo, hi);
+            const float2 f = e4m3x2_to_float2(u);
+            const uint32_t v = f32x2_to_e4m3x2(lo - f.x, hi - f.y);
+            if (z & 1) {
+              c0[z >> 1] |= u << 16;
+              c1[z >> 1] |= v << 16;
+            } else {
+              c0[z >> 1] = u;
+              c1[z >> 1] = v;
+            }
+          }
+          if (i < n) {  // (every lane has read its chunk: the maxima came from all)
+            uint8_t* const d = tile + rr * 128 + (((c >> 1) ^ (rr & 7)) << 4) + (c & 1) * 8;
+            *reinterpret_cast<uint2*>(d) = make_uint2(c0[0], c0[1]);
+            *reinterpret_cast<uint2*>(d + 16384) = make_uint2(c1[0], c1[1]);
+            if (c == 0)
+              s_mult[buf * 128 + rr] =
+                  ex == 255 ? __int_as_float(0x7fffffff) : fmaxf(base * __int_as_float((127 - e) << 23), kPfMinMult);
           }
         }
-        if (rr < at + n) {
-          uint8_t* const d = dst + (((c >> 1) ^ (rr & 7)) << 4) + (c & 1) * 8;
-          *reinterpret_cast<uint2*>(d) = make_uint2(c0[0], c0[1]);
-          *reinterpret_cast<uint2*>(d + 16384) = make_uint2(c1[0], c1[1]);
-          if (c == 0)
-            s_mult[buf * 128 + rr] =
-                ex == 255 ? __int_as_float(0x7fffffff) : fmaxf(base * __int_as_float((127 - e) << 23), kPfMinMult);
-        }
-      } else if (rr < at + n) {
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (c == 0) s_mult[buf * 128 + rr] = fmaxf(base, kPfMinMult);
+      }
+    } else {
+      if (lane < n) s_mult[buf * 128 + at + lane] = fmaxf(base, kPfMinMult);
+#pragma unroll 1
+      for (int i = flip ? hw : n; i < n; i += 2) {
+        uint4* const x = reinterpret_cast<uint4*>(chunk(at + i));
+        *x = make_uint4(x->x ^ flip, x->y ^ flip, x->z ^ flip, x->w ^ flip);
       }
     }
     fence_proxy_async_smem();
@@ -786,18 +820,19 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const int mx = kw ? (lane & 8) * 8 : 0, my = kw ? 0 : kFp8 ? 16 : 128;
       auto all_of_half = [&](bool x) -> bool { return (__ballot_sync(kFull, x) & group) == group; };
       const int32_t* row = nullptr;
-      int i = 0, tiles = 0, next = -2;
+      int i = 0, tiles = 0;
       uint32_t j = 0, st = 0, round = 0, idle = 0;
       bool have = false, done = false;
-      int ids[4] = {-2, -2, -2, -2};  // pages of this lane's box of the next four blocks (once it is there)
-      auto have_box = [&](int i) -> bool { return copies && i < p.i1 && i * kPfBlkTiles + box_t < tiles; };
+      // pages of 16 tiles, one per lane of the half: of this block and the next (an even number of blocks
+      // into the piece), and of the two behind them, asked for two blocks before they are needed
+      int now = -1, then = -1;
       while (!__all_sync(kFull, done)) {
         ++idle;
         if (all_of_half(!have && !done && mbar_test(bar(C::kBarPiece + pn % kPfPieces), pn / kPfPieces & 1))) {
           const PfSlot& slot = s_piece[pn % kPfPieces];
           p = slot.piece;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ids[k] = slot.pages[(k * kPfBlkTiles + box_t) & 31];
+          then = slot.pages[16 + (lane & 15)];
+          now = slot.pages[lane & 15];
           __syncwarp(group);
           if (leads) mbar_arrive(bar(C::kBarPieceFree + pn % kPfPieces));
           ++pn;
@@ -806,20 +841,22 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           i = p.i0;
           row = a.page_table + static_cast<int64_t>(p.r) * a.max_pages;
           tiles = p.tokens / kPfTile;
-          // (the slot may be written anew from here on: the ids are taken now)
-          next = have_box(i) ? ids[0] : -2;
           idle = 0;
         }
         const bool goes = all_of_half(have && (round == 0 || mbar_test(free + 8 * st, (round - 1) & 1)));
-        const bool good = goes && next >= 0 && next < a.num_pages;
-        const uint32_t boxes = __popc(__ballot_sync(kFull, good) & group);
         if (goes) {
-          const int pg = next;  // (one outside the pool is not copied: the check has it)
-          ids[0] = ids[1];
-          ids[1] = ids[2];
-          ids[2] = ids[3];
-          if (have_box(i + 4)) ids[3] = max(-1, __ldg(row + quotient((i + 4) * kPfBlkTiles + box_t, a.by_tpp)));
-          next = have_box(i + 1) ? ids[0] : -2;
+          const int behind = i - p.i0;
+          if (behind > 0 && (behind & 1) == 0) {
+            now = then;
+            then = -1;
+            const int tile = (i + 2) * kPfBlkTiles + (lane & 15);
+            if (tile < min(tiles, p.i1 * kPfBlkTiles)) then = __ldg(row + quotient(tile, a.by_tpp));
+          }
+          const int tile = i * kPfBlkTiles + box_t;
+          const int pg = __shfl_sync(group, now, (behind & 1) * 8 + box_t, 16);
+          // (one outside the pool is not copied: the check has it)
+          const bool good = copies && tile < tiles && pg >= 0 && pg < a.num_pages;
+          const uint32_t boxes = __popc(__ballot_sync(group, good));
           const uint32_t f = full + 8 * st;
           if (leads) {
             const uint32_t bytes = boxes * a.zbox * (kPfTile * (kw ? 128 : kPfDim * C::kElem));
@@ -827,11 +864,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             else mbar_arrive_expect_tx(f, bytes);
           }
           __syncwarp(group);
-          if (good) {
-            const int tile = i * kPfBlkTiles + box_t;
+          if (good)
             tma_load_3d(ring + st * C::kKStage, map, mx, my,
                         (pg * a.Hkv + p.h) * tpp + tile - quotient(tile, a.by_tpp) * tpp, f, pol);
-          }
           if (++st == stages) st = 0, ++round;
           ++j;
           if (++i == p.i1) have = false;
@@ -1133,9 +1168,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               tmem_ld64(to + 64 * c, o);
               if (valid) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  *reinterpret_cast<float4*>(dst + 64 * c + 4 * k) =
-                      make_float4(o[4 * k] * vscale, o[4 * k + 1] * vscale, o[4 * k + 2] * vscale, o[4 * k + 3] * vscale);
+                for (int k = 0; k < 64; k += 8) {
+                  const float x[8] = {o[k] * vscale,     o[k + 1] * vscale, o[k + 2] * vscale, o[k + 3] * vscale,
+                                      o[k + 4] * vscale, o[k + 5] * vscale, o[k + 6] * vscale, o[k + 7] * vscale};
+                  st_global8(dst + 64 * c + k, x);
+                }
               }
             }
           }
@@ -1222,9 +1259,13 @@ __device__ __forceinline__ int shared_pages(const PfArgs& a, int r) {
   const unsigned kFull = 0xffffffffu;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   auto start = [&](int i) -> int { return min(max(__ldg(a.group_starts + i), 0), a.B); };
-  int first = 0x7fffffff;
+  // (the first 128 starts, lengths and prefixes are asked for together; what is looked at again is in L1)
+  const int start0 = t <= a.n_groups ? start(t) : 0, live0 = t < a.B ? live_length(a, t) : 0;
+  const int prefix0 = t < a.n_groups ? __ldg(a.prefix_lens + t) : 0;
+  asm volatile("" ::"r"(prefix0));
+  int first = t <= a.n_groups && start0 > r ? t : 0x7fffffff;
 #pragma unroll 1
-  for (int i = t; i <= a.n_groups && first == 0x7fffffff; i += 32 * kOwnWarps)
+  for (int i = t + 32 * kOwnWarps; i <= a.n_groups && first == 0x7fffffff; i += 32 * kOwnWarps)
     if (start(i) > r) first = i;
   first = __reduce_min_sync(kFull, first);
   if (lane == 0) s_first[warp] = first;
@@ -1232,9 +1273,9 @@ __device__ __forceinline__ int shared_pages(const PfArgs& a, int r) {
 #pragma unroll
   for (int w = 0; w < kOwnWarps; ++w) first = min(first, s_first[w]);
   if (first == 0 || first > a.n_groups) return 0;
-  int lo = 0;
+  int lo = t < first ? start0 : 0;
 #pragma unroll 1
-  for (int i = t; i < first; i += 32 * kOwnWarps) lo = max(lo, start(i));
+  for (int i = t + 32 * kOwnWarps; i < first; i += 32 * kOwnWarps) lo = max(lo, start(i));
   lo = __reduce_max_sync(kFull, lo);
   if (lane == 0) s_lo[warp] = lo;
   __syncthreads();
@@ -1242,9 +1283,9 @@ __device__ __forceinline__ int shared_pages(const PfArgs& a, int r) {
   for (int w = 0; w < kOwnWarps; ++w) lo = max(lo, s_lo[w]);
   const int hi = start(first);
   if (hi - lo < 2) return 0;
-  int least = 0x7fffffff;
+  int least = t >= lo && t < hi && live0 > 0 ? live0 : 0x7fffffff;
 #pragma unroll 1
-  for (int i = lo + t; i < hi; i += 32 * kOwnWarps) {
+  for (int i = max(lo, 32 * kOwnWarps) + t; i < hi; i += 32 * kOwnWarps) {
     const int L = live_length(a, i);
     if (L > 0) least = min(least, L);
   }
@@ -1538,10 +1579,10 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
       unsigned todo = __ballot_sync(kFull, has);
 #pragma unroll 1
       while (todo) {
-        float fk[4];
-        float4 o[4];
+        float fk[8];
+        float4 o[8];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 8; ++x) {
           const int src = todo ? __ffs(todo) - 1 : 0;
           const float fx = __shfl_sync(kFull, f, src);
           const int64_t sx = __shfl_sync(kFull, slot, src);
@@ -1551,7 +1592,7 @@ __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const 
           todo &= todo - 1;
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 8; ++x) {
           acc.x = fmaf(o[x].x, fk[x], acc.x);
           acc.y = fmaf(o[x].y, fk[x], acc.y);
           acc.z = fmaf(o[x].z, fk[x], acc.z);
