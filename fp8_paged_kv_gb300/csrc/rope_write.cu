@@ -7,11 +7,17 @@
 // fraction of p f / (2 pi) is taken with the product's rounding error (one FMA)
 // added back, so that far positions keep the accuracy of near ones.
 //
-// One thread owns one unit of a token -- 16 values of a head, 8 pairs -- and
-// walks over heads with the unit's eight cosines and sines in registers: the
-// same unit of every head turns by the same angles.  In the half layout the
-// unit's two 16-byte chunks lie rot_dim/2 apart, interleaved or unrotated ones
-// are adjacent, and no pair ever crosses two threads.
+// A unit is 16 values of a head, 8 pairs, and belongs to one thread: in the half
+// layout its two 16-byte chunks lie rot_dim/2 apart, interleaved or unrotated
+// ones are adjacent, and no pair ever crosses two threads.  The same unit of
+// every head of a token turns by the same angles, so a thread keeps a unit's
+// eight cosines and sines in registers over the heads that it walks.
+//
+// Both kernels move bytes and are bound by HBM (or, for few tokens, by a
+// launch and three dependent loads).  Appends have a thread per (token, unit,
+// slice of the heads).  Prompts go by 16-token tiles of the cache: what a CTA
+// does is cut out of one list of (tile, eight heads) steps, as many for each
+// CTA, and values are written as whole rows of a tile's dim-major block.
 #include "step_ops.cuh"
 
 namespace fpk {
@@ -20,6 +26,10 @@ namespace {
 constexpr int kRopeDim = 128;
 constexpr int kRopeUnits = kRopeDim / 16;  // units of 16 values per head
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBatch = 4;                // heads in flight per thread
+constexpr int kRopeStep = 2 * kRopeBatch;    // heads per step of a prompt's tile
+constexpr int kRopeStage = 16 * kRopeStep * kRopeDim * 2, kRopeStages = 3;
+constexpr int kRopeWarpStage = kRopeStage / (kRopeThreads / 32);
 
 struct RopeArgs {
   WriteArgs w;               // k_src, v_src, pool, table, tags; seq_lens or cu_seqlens
@@ -110,96 +120,323 @@ __device__ __forceinline__ uint4 pack8(const float* y) {
                     pack_bf16x2(y[6], y[7]));
 }
 
-// Thread = (token, head slice, unit): the unit of heads slice, slice + hsplit,
-// ...; heads 0 .. Hq-1 are the queries', the following Hkv the cache's.
-template <bool kFp8, bool kPrefill>
-__global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeArgs a) {
+// A unit's chunks: first values of the two.
+struct Unit {
+  int d0, d1;
+  bool turns;
+};
+__device__ __forceinline__ Unit unit_of(const RopeArgs& a, int u) {
+  Unit x;
+  x.turns = 16 * u < a.rot;
+  const bool half = x.turns && !a.interleaved;
+  x.d0 = half ? 8 * u : 16 * u;
+  x.d1 = half ? 8 * u + (a.rot >> 1) : 16 * u + 8;
+  return x;
+}
+
+// A unit of a rotated key into its row of the K block.
+template <bool kFp8>
+__device__ __forceinline__ void put_key(const WriteArgs& w, int64_t row, const Unit& x, const float (&y)[16],
+                                        const Divisor& ks) {
+  if (kFp8) {
+    *reinterpret_cast<uint2*>(w.kv_pool + row + x.d0) = quant8(y, ks);
+    *reinterpret_cast<uint2*>(w.kv_pool + row + x.d1) = quant8(y + 8, ks);
+  } else {
+    uint16_t* pool = reinterpret_cast<uint16_t*>(w.kv_pool);
+    *reinterpret_cast<uint4*>(pool + row + x.d0) = pack8(y);
+    *reinterpret_cast<uint4*>(pool + row + x.d1) = pack8(y + 8);
+  }
+}
+
+// The page of position pos of request r, -1 if its token may not be written.
+__device__ __forceinline__ int page_for(const WriteArgs& w, int r, int64_t pos) {
+  if (pos < 0) return -1;
+  const int64_t pi = pos / w.page_size;
+  if (pi >= w.max_pages) return -1;
+  const int64_t e = static_cast<int64_t>(r) * w.max_pages + pi;
+  const bool guarded = w.live_tags != nullptr && w.expected_tags != nullptr;
+  const int page = __ldg(w.page_table + e);
+  const uint32_t want = guarded ? __ldg(w.expected_tags + e) : 0u;
+  if (page < 0 || page >= w.num_pages || (guarded && __ldg(w.live_tags + page) != want)) return -1;
+  return page;
+}
+
+// One token per request.  Thread = (token, slice, unit); the slice's heads are
+// slice, slice + hsplit, ... of the Hq queries, Hkv keys and Hkv values.  A
+// token's V column is strided by a tile's 16 tokens: element stores.
+template <bool kFp8>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs a) {
   const WriteArgs& w = a.w;
-  const int64_t total = w.rows * a.hsplit * kRopeUnits;
-  const Divisor ks = make_divisor(kFp8 ? __ldg(w.k_scale) : 1.f);
-  const Divisor vs = make_divisor(kFp8 ? __ldg(w.v_scale) : 1.f);
-  const int tpp = w.page_size >> 4;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(kRopeThreads) + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kRopeThreads) {
-    const int u = static_cast<int>(i % kRopeUnits);
-    const int64_t row = (i / kRopeUnits) % w.rows;
-    const int slice = static_cast<int>(i / kRopeUnits / w.rows);
-    int r, pos;
-    if (kPrefill) {
-      r = request_of_row(w.cu_seqlens, w.B, row);
-      pos = static_cast<int>(row - __ldg(w.cu_seqlens + r)) + (a.start_pos != nullptr ? __ldg(a.start_pos + r) : 0);
+  const int64_t i = blockIdx.x * static_cast<int64_t>(kRopeThreads) + threadIdx.x;
+  const int u = static_cast<int>(i % kRopeUnits);
+  const int slice = static_cast<int>(i / kRopeUnits % a.hsplit);
+  const int64_t row = i / kRopeUnits / a.hsplit;
+  if (row >= w.rows) return;
+  const Unit x = unit_of(a, u);
+  const int pos = __ldg(w.seq_lens + row) - 1;
+  // a source row of the head list; queries may be rotated in place: plain loads
+  auto source = [&](int h) -> const uint16_t* {
+    if (h < a.Hq) return a.q + (row * a.Hq + h) * kRopeDim;
+    return h < a.Hq + w.Hkv ? w.k_src + (row * w.Hkv + h - a.Hq) * kRopeDim
+                            : w.v_src + (row * w.Hkv + h - a.Hq - w.Hkv) * kRopeDim;
+  };
+  const int heads = a.Hq + 2 * w.Hkv;
+  int h = slice;
+  const uint16_t* src = source(h);
+  bool value = h >= a.Hq + w.Hkv;
+  uint4 x0 = *reinterpret_cast<const uint4*>(src + (value ? 16 * u : x.d0));
+  uint4 x1 = *reinterpret_cast<const uint4*>(src + (value ? 16 * u + 8 : x.d1));
+  if (pos < 0) return;
+  const int page = h + (heads - 1 - h) / a.hsplit * a.hsplit >= a.Hq ? page_for(w, static_cast<int>(row), pos) : -1;
+  const int tpp = w.page_size >> 4, off = pos % w.page_size;
+  Turn t;
+  if (x.turns && !value) unit_angles(a, pos, u, t);
+  for (;;) {
+    if (h < a.Hq) {
+      float y[16];
+      rotate_unit(x0, x1, t, x.turns, a.interleaved, y);
+      uint16_t* const out = a.q_out + (row * a.Hq + h) * kRopeDim;
+      *reinterpret_cast<uint4*>(out + x.d0) = pack8(y);
+      *reinterpret_cast<uint4*>(out + x.d1) = pack8(y + 8);
+    } else if (page < 0) {
+      if (w.abort_mask != nullptr) w.abort_mask[row] = 1;
+      return;
     } else {
-      r = static_cast<int>(row);
-      pos = __ldg(w.seq_lens + r) - 1;
-      if (pos < 0) continue;
-    }
-    const bool turns = 16 * u < a.rot;
-    Turn t;
-    if (turns) unit_angles(a, pos, u, t);
-    const bool half = turns && !a.interleaved;
-    const int d0 = half ? 8 * u : 16 * u;              // first value of the two chunks
-    const int d1 = half ? 8 * u + (a.rot >> 1) : 16 * u + 8;
-    int h = slice;
-#pragma unroll 4
-    for (; h < a.Hq; h += a.hsplit) {
-      const int64_t at = (row * a.Hq + h) * kRopeDim;
-      const uint4 x0 = *reinterpret_cast<const uint4*>(a.q + at + d0);
-      const uint4 x1 = *reinterpret_cast<const uint4*>(a.q + at + d1);
-      float y[16];
-      rotate_unit(x0, x1, t, turns, a.interleaved, y);
-      *reinterpret_cast<uint4*>(a.q_out + at + d0) = pack8(y);
-      *reinterpret_cast<uint4*>(a.q_out + at + d1) = pack8(y + 8);
-    }
-    if (h - a.Hq >= w.Hkv) continue;
-    // the slot of this token and its guard
-    const int pi = pos >= 0 ? pos / w.page_size : -1;
-    const int off = pos - pi * w.page_size;
-    bool ok = pi >= 0 && pi < w.max_pages;
-    int page = -1;
-    if (ok) {
-      const int64_t e = static_cast<int64_t>(r) * w.max_pages + pi;
-      page = __ldg(w.page_table + e);
-      ok = page >= 0 && page < w.num_pages;
-      if (ok && w.live_tags != nullptr && w.expected_tags != nullptr)
-        ok = __ldg(w.live_tags + page) == __ldg(w.expected_tags + e);
-    }
-    if (!ok) {
-      if (w.abort_mask != nullptr) w.abort_mask[r] = 1;
-      continue;
-    }
-    for (int hk = h - a.Hq; hk < w.Hkv; hk += a.hsplit) {
-      const int64_t at = (row * w.Hkv + hk) * kRopeDim;
-      const uint4 x0 = __ldg(reinterpret_cast<const uint4*>(w.k_src + at + d0));
-      const uint4 x1 = __ldg(reinterpret_cast<const uint4*>(w.k_src + at + d1));
-      const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(w.v_src + at + 16 * u));
-      const uint4 v1 = __ldg(reinterpret_cast<const uint4*>(w.v_src + at + 16 * u + 8));
+      const int hk = h - a.Hq - (value ? w.Hkv : 0);
       const int64_t tile = ((static_cast<int64_t>(page) * w.Hkv + hk) * tpp + (off >> 4)) * 2 * 16 * kRopeDim;
-      const int64_t krow = tile + (off & 15) * kRopeDim;
-      const int64_t vcol = tile + 16 * kRopeDim + 16 * u * 16 + (off & 15);
-      float y[16];
-      rotate_unit(x0, x1, t, turns, a.interleaved, y);
-      const uint32_t vw[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-      if (kFp8) {
-        *reinterpret_cast<uint2*>(w.kv_pool + krow + d0) = quant8(y, ks);
-        *reinterpret_cast<uint2*>(w.kv_pool + krow + d1) = quant8(y + 8, ks);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float lo = div_by(__uint_as_float(vw[j] << 16), vs);
-          const float hi = div_by(__uint_as_float(vw[j] & 0xFFFF0000u), vs);
-          const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-          w.kv_pool[vcol + 32 * j] = static_cast<uint8_t>(c & 0xFFu);
-          w.kv_pool[vcol + 32 * j + 16] = static_cast<uint8_t>(c >> 8);
-        }
+      if (!value) {
+        float y[16];
+        rotate_unit(x0, x1, t, x.turns, a.interleaved, y);
+        put_key<kFp8>(w, tile + (off & 15) * kRopeDim, x, y, make_divisor(kFp8 ? __ldg(w.k_scale) : 1.f));
       } else {
-        uint16_t* pool = reinterpret_cast<uint16_t*>(w.kv_pool);
-        *reinterpret_cast<uint4*>(pool + krow + d0) = pack8(y);
-        *reinterpret_cast<uint4*>(pool + krow + d1) = pack8(y + 8);
+        const int64_t at = tile + 16 * kRopeDim + 16 * u * 16 + (off & 15);
+        const uint32_t vw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        if (kFp8) {
+          const Divisor vs = make_divisor(__ldg(w.v_scale));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          pool[vcol + 32 * j] = static_cast<uint16_t>(vw[j] & 0xFFFFu);
-          pool[vcol + 32 * j + 16] = static_cast<uint16_t>(vw[j] >> 16);
+          for (int j = 0; j < 8; ++j) {
+            const float lo = div_by(__uint_as_float(vw[j] << 16), vs);
+            const float hi = div_by(__uint_as_float(vw[j] & 0xFFFF0000u), vs);
+            const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+            w.kv_pool[at + 32 * j] = static_cast<uint8_t>(c & 0xFFu);
+            w.kv_pool[at + 32 * j + 16] = static_cast<uint8_t>(c >> 8);
+          }
+        } else {
+          uint16_t* pool = reinterpret_cast<uint16_t*>(w.kv_pool);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            pool[at + 32 * j] = static_cast<uint16_t>(vw[j] & 0xFFFFu);
+            pool[at + 32 * j + 16] = static_cast<uint16_t>(vw[j] >> 16);
+          }
         }
       }
+    }
+    h += a.hsplit;
+    if (h >= heads) return;
+    src = source(h);
+    value = h >= a.Hq + w.Hkv;
+    x0 = *reinterpret_cast<const uint4*>(src + (value ? 16 * u : x.d0));
+    x1 = *reinterpret_cast<const uint4*>(src + (value ? 16 * u + 8 : x.d1));
+  }
+}
+
+// Values of one tile and head, by a warp: a lane has four dims of all 16 tokens
+// and writes their rows, whole where the tile's tokens are all new.
+template <bool kFp8>
+__device__ __forceinline__ void put_values(const WriteArgs& w, int64_t vblock, const uint2* src, int t0, int n,
+                                           const Divisor& vs, int lane) {
+  uint2 x[16];  // (of the tokens that are not new: whatever the stage held)
+#pragma unroll
+  for (int q = 0; q < 16; ++q) x[q] = src[q * 32];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    uint32_t e[8];  // dim 4 lane + d: tokens 2 q, 2 q + 1
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const uint32_t a = d < 2 ? x[2 * q].x : x[2 * q].y, b = d < 2 ? x[2 * q + 1].x : x[2 * q + 1].y;
+      e[q] = d & 1 ? __byte_perm(a, b, 0x7632) : __byte_perm(a, b, 0x5410);
+    }
+    const int64_t at = vblock + (4 * lane + d) * 16;
+    if (kFp8) {
+      uint32_t c[4];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t y = __nv_cvt_float2_to_fp8x2(
+            make_float2(div_by(__uint_as_float(e[q] << 16), vs), div_by(__uint_as_float(e[q] & 0xFFFF0000u), vs)),
+            __NV_SATFINITE, __NV_E4M3);
+        if (q & 1) c[q >> 1] |= y << 16;
+        else c[q >> 1] = y;
+      }
+      if (n == 16) {
+        *reinterpret_cast<uint4*>(w.kv_pool + at) = make_uint4(c[0], c[1], c[2], c[3]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          if (q >= t0 && q < t0 + n) w.kv_pool[at + q] = static_cast<uint8_t>(c[q >> 2] >> (8 * (q & 3)));
+      }
+    } else {
+      uint16_t* const row = reinterpret_cast<uint16_t*>(w.kv_pool) + at;
+      if (n == 16) {
+        reinterpret_cast<uint4*>(row)[0] = make_uint4(e[0], e[1], e[2], e[3]);
+        reinterpret_cast<uint4*>(row)[1] = make_uint4(e[4], e[5], e[6], e[7]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          if (q >= t0 && q < t0 + n) row[q] = static_cast<uint16_t>(e[q >> 1] >> (16 * (q & 1)));
+      }
+    }
+  }
+}
+
+// Tiles of request r have the places cu[r] / 16 + 2 r and on: a request of n
+// tokens touches at most n / 16 + 2 tiles wherever its first position lies, so
+// that the places need no scan over the requests, and a few stay empty.
+__host__ __device__ __forceinline__ int64_t tile_places(int64_t rows, int64_t B) { return rows / 16 + 2 * B; }
+
+// A step of a prompt: eight heads of a tile (queries, then keys: the threads of
+// the lower and the upper half take four each; then values, a warp each).
+struct Step {
+  int request, row0, t0, n;  // n new tokens from source row row0 at rows t0 .. of the tile; 0: nothing to do
+  int tile, step, page;      // tile of the request; page: -1 if refused (steps behind the queries')
+};
+
+__device__ __forceinline__ void rope_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void rope_copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The sources of the next two steps are on their way while a step is worked
+// on: 128 KiB per SM in flight, each warp's into its own part of a stage, so
+// that no warp waits for another.
+template <bool kFp8>
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const RopeArgs a) {
+  extern __shared__ __align__(16) uint8_t s_stage[];
+  const WriteArgs& w = a.w;
+  const int u = threadIdx.x % kRopeUnits, tok = threadIdx.x / kRopeUnits % 16, lane = threadIdx.x & 31;
+  const int side = threadIdx.x / (16 * kRopeUnits), warp = threadIdx.x >> 5;
+  const int qsteps = (a.Hq + kRopeStep - 1) / kRopeStep, ksteps = (w.Hkv + kRopeStep - 1) / kRopeStep;
+  const int steps = qsteps + 2 * ksteps;
+  const int64_t total = tile_places(w.rows, w.B) * steps;
+  const int64_t begin = total * blockIdx.x / gridDim.x;
+  const int count = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x - begin);
+  const Divisor ks = make_divisor(kFp8 ? __ldg(w.k_scale) : 1.f);
+  const Divisor vs = make_divisor(kFp8 ? __ldg(w.v_scale) : 1.f);
+  const Unit x = unit_of(a, u);
+  const int tpp = w.page_size >> 4;
+  int64_t place = begin / steps - 1;
+  int at = static_cast<int>(begin - (place + 1) * steps), left = count;  // the next step's place in its tile; steps not yet asked for
+  Step next = {};
+  // a warp's part of a stage: [chunk][lane] of 16 bytes, or [token][lane] of 8
+  const uint32_t stages = smem_addr(s_stage) + warp * kRopeWarpStage + lane * 16;
+
+  // the next step, and its sources asked for
+  auto ask = [&](uint32_t stage) {
+    if (left > 0) {
+      --left;
+      if (at == steps) at = 0;
+      if (at == 0 || left == count - 1) {
+        // a new place: its request is the largest r with cu[r] / 16 + 2 r at or below it
+        ++place;
+        int lo = 0, hi = w.B - 1;
+#pragma unroll 1
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if ((__ldg(w.cu_seqlens + mid) >> 4) + 2 * static_cast<int64_t>(mid) <= place) lo = mid; else hi = mid - 1;
+        }
+        const int64_t c0 = max(__ldg(w.cu_seqlens + lo), 0);
+        const int64_t c1 = min(static_cast<int64_t>(__ldg(w.cu_seqlens + lo + 1)), w.rows);
+        const int64_t start = a.start_pos != nullptr ? __ldg(a.start_pos + lo) : 0;
+        const int64_t tile = (start >> 4) + place - ((c0 >> 4) + 2 * lo);  // of the request's positions
+        const int64_t p0 = max(start, 16 * tile), p1 = min(start + c1 - c0, 16 * tile + 16);
+        next.request = lo;
+        next.tile = static_cast<int>(tile);
+        next.n = static_cast<int>(max(p1 - p0, static_cast<int64_t>(0)));
+        next.t0 = static_cast<int>(p0 - 16 * tile);
+        next.row0 = static_cast<int>(c0 + p0 - start);
+        next.page = next.n > 0 ? page_for(w, lo, p0) : -1;
+      }
+      next.step = at++;
+      const bool key = next.step >= qsteps;
+      if (next.n > 0 && next.step < qsteps + ksteps) {
+        const int heads = key ? w.Hkv : a.Hq;
+        const int h0 = (key ? next.step - qsteps : next.step) * kRopeStep + side * kRopeBatch;
+        const uint16_t* const src =
+            (key ? w.k_src : a.q) + (static_cast<int64_t>(next.row0 + tok - next.t0) * heads + h0) * kRopeDim;
+        if (tok >= next.t0 && tok < next.t0 + next.n)
+#pragma unroll
+          for (int k = 0; k < kRopeBatch; ++k)
+            if (h0 + k < heads) {
+              rope_copy16(stage + 2 * k * 512, src + k * kRopeDim + x.d0);
+              rope_copy16(stage + (2 * k + 1) * 512, src + k * kRopeDim + x.d1);
+            }
+      } else if (next.n > 0) {
+        const int h = (next.step - qsteps - ksteps) * kRopeStep + warp;
+        const uint16_t* src = w.v_src + (static_cast<int64_t>(next.row0) * w.Hkv + h) * kRopeDim + 4 * lane;
+        const uint32_t dst = stage - lane * 8;
+        if (h < w.Hkv)
+#pragma unroll 1
+          for (int q = next.t0; q < next.t0 + next.n; ++q, src += static_cast<int64_t>(w.Hkv) * kRopeDim)
+            rope_copy8(dst + q * 256, src);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  uint32_t st = 0;  // stage of the step that is worked on
+  Step s0, s1;
+  ask(stages);
+  s0 = next;
+  ask(stages + kRopeStage);
+  s1 = next;
+  Turn t;
+  int turned = -1;  // tokens' tile that t belongs to, by its request's place
+#pragma unroll 1
+  for (int done = 0; done < count; ++done) {
+    __syncwarp();  // the stage's last readers
+    ask(stages + (st == 0 ? 2 : st - 1) * kRopeStage);
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    __syncwarp();
+    const Step c = s0;
+    s0 = s1;
+    s1 = next;
+    const uint8_t* const mine = s_stage + st * kRopeStage + warp * kRopeWarpStage;
+    st = st == 2 ? 0 : st + 1;
+    if (done == 0 || c.step == 0) turned = 0;
+    if (c.n == 0) continue;
+    if (c.step >= qsteps && c.page < 0) {
+      if (threadIdx.x == 0 && w.abort_mask != nullptr) w.abort_mask[c.request] = 1;
+      continue;
+    }
+    const int64_t block = static_cast<int64_t>(c.page) * w.Hkv * tpp + c.tile % tpp;
+    if (c.step < qsteps + ksteps) {
+      if (x.turns && turned == 0) unit_angles(a, 16 * c.tile + tok, u, t);
+      turned = 1;
+      const bool key = c.step >= qsteps;
+      const int heads = key ? w.Hkv : a.Hq;
+      const int h0 = (key ? c.step - qsteps : c.step) * kRopeStep + side * kRopeBatch;
+      const int64_t row = c.row0 + tok - c.t0;
+      if (tok >= c.t0 && tok < c.t0 + c.n)
+#pragma unroll
+        for (int k = 0; k < kRopeBatch; ++k)
+          if (h0 + k < heads) {
+            const uint4* const in = reinterpret_cast<const uint4*>(mine) + lane + 2 * k * 32;
+            float y[16];
+            rotate_unit(in[0], in[32], t, x.turns, a.interleaved, y);
+            if (key) {
+              put_key<kFp8>(w, (block + static_cast<int64_t>(h0 + k) * tpp) * 2 * 16 * kRopeDim + tok * kRopeDim, x, y, ks);
+            } else {
+              uint16_t* const out = a.q_out + (row * heads + h0 + k) * kRopeDim;
+              *reinterpret_cast<uint4*>(out + x.d0) = pack8(y);
+              *reinterpret_cast<uint4*>(out + x.d1) = pack8(y + 8);
+            }
+          }
+    } else {
+      const int h = (c.step - qsteps - ksteps) * kRopeStep + warp;
+      if (h < w.Hkv)
+        put_values<kFp8>(w, (block + static_cast<int64_t>(h) * tpp) * 2 * 16 * kRopeDim + 16 * kRopeDim,
+                         reinterpret_cast<const uint2*>(mine) + lane, c.t0, c.n, vs, lane);
     }
   }
 }
@@ -248,11 +485,23 @@ int rope_entry(bool fp8, bool prefill, const void* q, const void* k, const void*
   a.rot = rot_dim;
   a.interleaved = interleaved != 0;
   a.hsplit = 1;
-  const int64_t want = (rows * a.hsplit * kRopeUnits + kRopeThreads - 1) / kRopeThreads;
-  auto kern = fp8 ? (prefill ? rope_write_kernel<true, true> : rope_write_kernel<true, false>)
-                  : (prefill ? rope_write_kernel<false, true> : rope_write_kernel<false, false>);
-  const int grid = resident_grid(reinterpret_cast<const void*>(kern), kRopeThreads, 0, want);
-  kern<<<grid, kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (prefill) {
+    auto kern = fp8 ? rope_prefill_kernel<true> : rope_prefill_kernel<false>;
+    const int64_t steps = (Hq + kRopeStep - 1) / kRopeStep + 2 * static_cast<int64_t>((Hkv + kRopeStep - 1) / kRopeStep);
+    constexpr int smem = kRopeStages * kRopeStage;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FPK_ECUDA;
+    const int grid = resident_grid(reinterpret_cast<const void*>(kern), kRopeThreads, smem, tile_places(rows, B) * steps);
+    kern<<<grid, kRopeThreads, smem, st>>>(a);
+  } else {
+    // a head per thread while that is no more than two full waves of threads; then as few slices as fill those
+    const int64_t heads = Hq + 2 * static_cast<int64_t>(Hkv), full = 2 * 152 * 1024 / kRopeUnits;
+    a.hsplit = static_cast<int>(rows * heads <= full ? heads : (full + rows - 1) / rows);
+    const int64_t ctas = (rows * a.hsplit * kRopeUnits + kRopeThreads - 1) / kRopeThreads;
+    if (ctas > 0x7fffffff) return FPK_EUNSUPPORTED;
+    auto kern = fp8 ? rope_append_kernel<true> : rope_append_kernel<false>;
+    kern<<<static_cast<int>(ctas), kRopeThreads, 0, st>>>(a);
+  }
   return checked_launch_status();
 }
 
