@@ -60,18 +60,32 @@ struct Turn {
   float c[8], s[8];
 };
 
-__device__ __forceinline__ void unit_angles(const RopeArgs& a, int pos, int u, Turn& t) {
+// The eight cosines and sines of unit u at a position, to out[0], [stride], .. [3 stride]: a short loop (the
+// unrolled one is 8 KiB of code, fetched anew each time).
+__device__ __forceinline__ void unit_angles(const RopeArgs& a, int pos, int u, float4* out, int stride) {
   // positions of more than 24 bits enter as two parts
   const float plo = static_cast<float>(pos & 0xFFFF), phi = static_cast<float>(pos - (pos & 0xFFFF));
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    float c[2], s[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float f = __ldg(a.inv_freq + 8 * u + i);
-    const float th = __fmul_rn(f, kInvTwoPiHi);
-    const float tl = __fmaf_rn(f, kInvTwoPiLo, __fmaf_rn(f, kInvTwoPiHi, -th));
-    float r = turn_fraction(plo, th, tl) + turn_fraction(phi, th, tl);
-    sincospif(2.f * r, &t.s[i], &t.c[i]);
-    t.s[i] *= a.rot_scale;
-    t.c[i] *= a.rot_scale;
+    for (int k = 0; k < 2; ++k) {
+      const float f = __ldg(a.inv_freq + 8 * u + 2 * i + k);
+      const float th = __fmul_rn(f, kInvTwoPiHi);
+      const float tl = __fmaf_rn(f, kInvTwoPiLo, __fmaf_rn(f, kInvTwoPiHi, -th));
+      sincospif(2.f * (turn_fraction(plo, th, tl) + turn_fraction(phi, th, tl)), &s[k], &c[k]);
+    }
+    out[i * stride] = make_float4(c[0] * a.rot_scale, c[1] * a.rot_scale, s[0] * a.rot_scale, s[1] * a.rot_scale);
+  }
+}
+__device__ __forceinline__ void load_turn(Turn& t, const float4* in, int stride) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 x = in[i * stride];
+    t.c[2 * i] = x.x;
+    t.c[2 * i + 1] = x.y;
+    t.s[2 * i] = x.z;
+    t.s[2 * i + 1] = x.w;
   }
 }
 
@@ -102,16 +116,21 @@ __device__ __forceinline__ void rotate_unit(const uint4& r0, const uint4& r1, co
   }
 }
 
+__device__ __forceinline__ uint32_t codes(float x, float y) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+// e4m3 codes of eight values; a divisor without a normal reciprocal is divided by out of line.
+__device__ __noinline__ uint2 quant8_slow(float4 x, float4 y, float s) {
+  return make_uint2(codes(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)) | codes(__fdiv_rn(x.z, s), __fdiv_rn(x.w, s)) << 16,
+                    codes(__fdiv_rn(y.x, s), __fdiv_rn(y.y, s)) | codes(__fdiv_rn(y.z, s), __fdiv_rn(y.w, s)) << 16);
+}
 __device__ __forceinline__ uint2 quant8(const float* y, const Divisor& s) {
+  if (!s.recip_ok) return quant8_slow(make_float4(y[0], y[1], y[2], y[3]), make_float4(y[4], y[5], y[6], y[7]), s.s);
   uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(div_by(y[4 * i], s), div_by(y[4 * i + 1], s)),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(div_by(y[4 * i + 2], s), div_by(y[4 * i + 3], s)),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    w[i] = lo | (hi << 16);
-  }
+  for (int i = 0; i < 2; ++i)
+    w[i] = codes(div_fast(y[4 * i], s), div_fast(y[4 * i + 1], s)) |
+           codes(div_fast(y[4 * i + 2], s), div_fast(y[4 * i + 3], s)) << 16;
   return make_uint2(w[0], w[1]);
 }
 
@@ -189,8 +208,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
   if (pos < 0) return;
   const int page = h + (heads - 1 - h) / a.hsplit * a.hsplit >= a.Hq ? page_for(w, static_cast<int>(row), pos) : -1;
   const int tpp = w.page_size >> 4, off = pos % w.page_size;
+  __shared__ float4 s_turn[4][kRopeThreads];  // a thread's own
+  if (x.turns && !value) unit_angles(a, pos, u, &s_turn[0][threadIdx.x], kRopeThreads);
   Turn t;
-  if (x.turns && !value) unit_angles(a, pos, u, t);
+  load_turn(t, &s_turn[0][threadIdx.x], kRopeThreads);
   for (;;) {
     if (h < a.Hq) {
       float y[16];
@@ -214,12 +235,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
         if (kFp8) {
           const Divisor vs = make_divisor(__ldg(w.v_scale));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float lo = div_by(__uint_as_float(vw[j] << 16), vs);
-            const float hi = div_by(__uint_as_float(vw[j] & 0xFFFF0000u), vs);
-            const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-            w.kv_pool[at + 32 * j] = static_cast<uint8_t>(c & 0xFFu);
-            w.kv_pool[at + 32 * j + 16] = static_cast<uint8_t>(c >> 8);
+          for (int j = 0; j < 2; ++j) {
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              y[2 * k] = __uint_as_float(vw[4 * j + k] << 16);
+              y[2 * k + 1] = __uint_as_float(vw[4 * j + k] & 0xFFFF0000u);
+            }
+            const uint2 c = quant8(y, vs);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              w.kv_pool[at + 16 * (8 * j + k)] = static_cast<uint8_t>((k < 4 ? c.x : c.y) >> (8 * (k & 3)));
           }
         } else {
           uint16_t* pool = reinterpret_cast<uint16_t*>(w.kv_pool);
@@ -240,50 +266,69 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
   }
 }
 
-// Values of one tile and head, by a warp: a lane has four dims of all 16 tokens
-// and writes their rows, whole where the tile's tokens are all new.
-template <bool kFp8>
-__device__ __forceinline__ void put_values(const WriteArgs& w, int64_t vblock, const uint2* src, int t0, int n,
-                                           const Divisor& vs, int lane) {
-  uint2 x[16];  // (of the tokens that are not new: whatever the stage held)
+// Bytes [b0, b1) of a row of 4 kWords bytes, in the widest aligned pieces: a store costs an L1 cycle per line it
+// touches whatever its width (element stores of a 15-token tile: 16 us instead of 1).
+template <int kWords, int kElem>
+__device__ __forceinline__ void put_row(uint8_t* row, const uint32_t (&c)[kWords], int b0, int b1) {
+  auto inside = [&](int b, int n) -> bool { return b0 <= b && b + n <= b1; };
 #pragma unroll
-  for (int q = 0; q < 16; ++q) x[q] = src[q * 32];
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    uint32_t e[8];  // dim 4 lane + d: tokens 2 q, 2 q + 1
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint32_t a = d < 2 ? x[2 * q].x : x[2 * q].y, b = d < 2 ? x[2 * q + 1].x : x[2 * q + 1].y;
-      e[q] = d & 1 ? __byte_perm(a, b, 0x7632) : __byte_perm(a, b, 0x5410);
+  for (int p = 0; p < kWords; p += 4) {
+    if (inside(4 * p, 16)) {
+      *reinterpret_cast<uint4*>(row + 4 * p) = make_uint4(c[p], c[p + 1], c[p + 2], c[p + 3]);
+      continue;
     }
-    const int64_t at = vblock + (4 * lane + d) * 16;
+#pragma unroll
+    for (int h = p; h < p + 4; h += 2) {
+      if (inside(4 * h, 8)) {
+        *reinterpret_cast<uint2*>(row + 4 * h) = make_uint2(c[h], c[h + 1]);
+        continue;
+      }
+#pragma unroll
+      for (int w = h; w < h + 2; ++w) {
+        if (inside(4 * w, 4)) {
+          *reinterpret_cast<uint32_t*>(row + 4 * w) = c[w];
+          continue;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e += kElem)
+          if (inside(4 * w + e, kElem)) {
+            if (kElem == 1) row[4 * w + e] = static_cast<uint8_t>(c[w] >> (8 * e));
+            else *reinterpret_cast<uint16_t*>(row + 4 * w + e) = static_cast<uint16_t>(c[w] >> (8 * e));
+          }
+      }
+    }
+  }
+}
+
+// Values of one tile and head, by a warp: src is the tile's 16 token rows (those that are not new: whatever the
+// stage held); lane l writes the rows of dims l, l + 32, l + 64, l + 96, consecutive lanes consecutive rows.
+template <bool kFp8>
+__device__ __forceinline__ void put_values(const WriteArgs& w, int64_t vblock, const uint16_t* src, int t0, int n,
+                                           const Divisor& vs, int lane) {
+#pragma unroll 1
+  for (int d = lane; d < kRopeDim; d += 32) {
+    uint32_t e[8];  // tokens 2 q, 2 q + 1
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      e[q] = src[2 * q * kRopeDim + d] | static_cast<uint32_t>(src[(2 * q + 1) * kRopeDim + d]) << 16;
+    const int64_t at = vblock + d * 16;
     if (kFp8) {
       uint32_t c[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const uint32_t y = __nv_cvt_float2_to_fp8x2(
-            make_float2(div_by(__uint_as_float(e[q] << 16), vs), div_by(__uint_as_float(e[q] & 0xFFFF0000u), vs)),
-            __NV_SATFINITE, __NV_E4M3);
-        if (q & 1) c[q >> 1] |= y << 16;
-        else c[q >> 1] = y;
-      }
-      if (n == 16) {
-        *reinterpret_cast<uint4*>(w.kv_pool + at) = make_uint4(c[0], c[1], c[2], c[3]);
-      } else {
+      for (int j = 0; j < 2; ++j) {
+        float y[8];
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
-          if (q >= t0 && q < t0 + n) w.kv_pool[at + q] = static_cast<uint8_t>(c[q >> 2] >> (8 * (q & 3)));
+        for (int k = 0; k < 4; ++k) {
+          y[2 * k] = __uint_as_float(e[4 * j + k] << 16);
+          y[2 * k + 1] = __uint_as_float(e[4 * j + k] & 0xFFFF0000u);
+        }
+        const uint2 x = quant8(y, vs);
+        c[2 * j] = x.x;
+        c[2 * j + 1] = x.y;
       }
+      put_row<4, 1>(w.kv_pool + at, c, t0, t0 + n);
     } else {
-      uint16_t* const row = reinterpret_cast<uint16_t*>(w.kv_pool) + at;
-      if (n == 16) {
-        reinterpret_cast<uint4*>(row)[0] = make_uint4(e[0], e[1], e[2], e[3]);
-        reinterpret_cast<uint4*>(row)[1] = make_uint4(e[4], e[5], e[6], e[7]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-          if (q >= t0 && q < t0 + n) row[q] = static_cast<uint16_t>(e[q >> 1] >> (16 * (q & 1)));
-      }
+      put_row<8, 2>(w.kv_pool + 2 * at, e, 2 * t0, 2 * (t0 + n));
     }
   }
 }
@@ -384,25 +429,22 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
-  uint32_t st = 0;  // stage of the step that is worked on
-  Step s0, s1;
-  ask(stages);
-  s0 = next;
-  ask(stages + kRopeStage);
-  s1 = next;
+  uint32_t st = 0;  // stage asked for; the one worked on is two steps behind it, the next in the ring
+  Step s0 = {}, s1 = {};
   Turn t;
-  int turned = -1;  // tokens' tile that t belongs to, by its request's place
+  int turned = 0;  // t belongs to the tile
 #pragma unroll 1
-  for (int done = 0; done < count; ++done) {
+  for (int done = -2; done < count; ++done) {
     __syncwarp();  // the stage's last readers
-    ask(stages + (st == 0 ? 2 : st - 1) * kRopeStage);
-    asm volatile("cp.async.wait_group 2;" ::: "memory");
-    __syncwarp();
+    ask(stages + st * kRopeStage);
     const Step c = s0;
     s0 = s1;
     s1 = next;
-    const uint8_t* const mine = s_stage + st * kRopeStage + warp * kRopeWarpStage;
     st = st == 2 ? 0 : st + 1;
+    if (done < 0) continue;
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    __syncwarp();
+    const uint8_t* const mine = s_stage + st * kRopeStage + warp * kRopeWarpStage;
     if (done == 0 || c.step == 0) turned = 0;
     if (c.n == 0) continue;
     if (c.step >= qsteps && c.page < 0) {
@@ -411,14 +453,18 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
     }
     const int64_t block = static_cast<int64_t>(c.page) * w.Hkv * tpp + c.tile % tpp;
     if (c.step < qsteps + ksteps) {
-      if (x.turns && turned == 0) unit_angles(a, 16 * c.tile + tok, u, t);
+      if (x.turns && turned == 0) {
+        float4* const turn = reinterpret_cast<float4*>(s_stage + kRopeStages * kRopeStage) + threadIdx.x;
+        unit_angles(a, 16 * c.tile + tok, u, turn, kRopeThreads);
+        load_turn(t, turn, kRopeThreads);
+      }
       turned = 1;
       const bool key = c.step >= qsteps;
       const int heads = key ? w.Hkv : a.Hq;
       const int h0 = (key ? c.step - qsteps : c.step) * kRopeStep + side * kRopeBatch;
       const int64_t row = c.row0 + tok - c.t0;
       if (tok >= c.t0 && tok < c.t0 + c.n)
-#pragma unroll
+#pragma unroll 2
         for (int k = 0; k < kRopeBatch; ++k)
           if (h0 + k < heads) {
             const uint4* const in = reinterpret_cast<const uint4*>(mine) + lane + 2 * k * 32;
@@ -436,7 +482,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
       const int h = (c.step - qsteps - ksteps) * kRopeStep + warp;
       if (h < w.Hkv)
         put_values<kFp8>(w, (block + static_cast<int64_t>(h) * tpp) * 2 * 16 * kRopeDim + 16 * kRopeDim,
-                         reinterpret_cast<const uint2*>(mine) + lane, c.t0, c.n, vs, lane);
+                         reinterpret_cast<const uint16_t*>(mine), c.t0, c.n, vs, lane);
     }
   }
 }
@@ -489,7 +535,7 @@ int rope_entry(bool fp8, bool prefill, const void* q, const void* k, const void*
   if (prefill) {
     auto kern = fp8 ? rope_prefill_kernel<true> : rope_prefill_kernel<false>;
     const int64_t steps = (Hq + kRopeStep - 1) / kRopeStep + 2 * static_cast<int64_t>((Hkv + kRopeStep - 1) / kRopeStep);
-    constexpr int smem = kRopeStages * kRopeStage;
+    constexpr int smem = kRopeStages * kRopeStage + kRopeThreads * 64;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FPK_ECUDA;
     const int grid = resident_grid(reinterpret_cast<const void*>(kern), kRopeThreads, smem, tile_places(rows, B) * steps);
     kern<<<grid, kRopeThreads, smem, st>>>(a);
