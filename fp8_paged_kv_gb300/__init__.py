@@ -148,16 +148,21 @@ def _stream(stream):
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
+
+def _launch_stream(stream, device):
+    """The handle alone: the current stream's object costs as much as a launch."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
 def _expect(t, name, shape):
-    """The tensor's shape, where the call's other arguments settle it (None: an argument left out)."""
-    if t is not None and tuple(t.shape) != shape:
+    """The tensor's shape (an int: its number of elements), where the call's other arguments settle it."""
+    if t is None or shape is None:
+        return
+    if isinstance(shape, int):
+        if t.numel() != shape:
+            raise FpkError(f"{name} has {t.numel()} elements, expected {shape}")
+    elif tuple(t.shape) != shape:
         raise FpkError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-
-
-def _expect_pool(kv_pool, layers, num_pages, Hkv, page_size, D):
-    want = 2 * layers * num_pages * Hkv * page_size * D
-    if layers < 1 or kv_pool.numel() != want:
-        raise FpkError(f"kv_pool has {kv_pool.numel()} elements, expected {want}")
 
 
 def _same_device(*tensors):
@@ -172,8 +177,37 @@ def _same_device(*tensors):
             raise FpkError(f"tensor on device {t.get_device()}, the current device is {dev}")
 
 
+def _pointers(*specs):
+    """Addresses of a call's tensors, each (tensor, dtypes, name, shape or None, optional).  One pass
+    over what nearly every call has; if anything is not as it should be, the checks by name say what."""
+    try:
+        dev, out = specs[0][0].get_device(), []
+        if dev >= 0 and dev == torch.cuda.current_device():
+            for t, dtypes, _, shape, optional in specs:
+                if t is None:
+                    if not optional:
+                        break
+                    out.append(None)
+                elif (t.dtype in dtypes and t.get_device() == dev and t.is_contiguous()
+                      and (shape is None or t.shape == shape
+                           or (shape.__class__ is int and t.numel() == shape))):
+                    out.append(t.data_ptr())
+                else:
+                    break
+            else:
+                return out
+    except AttributeError:
+        pass  # no tensor
+    for t, _, name, shape, _ in specs:
+        if t is None or isinstance(t, torch.Tensor):
+            _expect(t, name, shape)
+    _same_device(*(t for t, *_ in specs if isinstance(t, torch.Tensor)))
+    return [_ptr(t, dtypes, name, optional) for t, dtypes, name, _, optional in specs]
+
+
 _U8 = torch.uint8
 _I32T = torch.int32
+_U8S, _I32S, _F32S, _BF16S = (torch.uint8,), (torch.int32,), (torch.float32,), (torch.bfloat16,)
 _F32 = torch.float32
 _BF16 = torch.bfloat16
 _TAGS = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
@@ -405,101 +439,73 @@ def _groups(group_starts, prefix_lens):
     return n
 
 
-def _attn_shapes(q, page_table, seq_lens, abort_mask, out, lse):
+def _prefix(name, fp8, q, kv_pool, scales, page_table, seq_lens, abort_mask, group_starts, prefix_lens,
+            out, lse, workspace, Hkv, page_size, num_pages, sm_scale, stream):
     B, Hq, D = q.shape
-    _expect(page_table, "page_table", (B, page_table.shape[-1]))
-    _expect(seq_lens, "seq_lens", (B,))
-    _expect(abort_mask, "abort_mask", (B,))
-    _expect(out, "out", (B, Hq, D))
-    _expect(lse, "lse", (B, Hq))
-    return B, Hq, D
+    max_pages, n_groups = page_table.shape[-1], _groups(group_starts, prefix_lens)
+    (q_p, pool_p, table_p, lens_p, abort_p, starts_p, prefix_p, out_p, lse_p, ws_p, *scales_p) = _pointers(
+        (q, _BF16S, "q", None, False),
+        (kv_pool, _U8S if fp8 else _BF16_LIKE, "kv_pool", 2 * num_pages * Hkv * page_size * D, False),
+        (page_table, _I32S, "page_table", (B, max_pages), False), (seq_lens, _I32S, "seq_lens", (B,), False),
+        (abort_mask, _U8S, "abort_mask", (B,), True), (group_starts, _I32S, "group_starts", None, False),
+        (prefix_lens, _I32S, "prefix_lens", None, False), (out, _BF16S, "out", (B, Hq, D), False),
+        (lse, _F32S, "lse", (B, Hq), True), (workspace, _U8S, "workspace", None, False), *scales)
+    _check(getattr(_lib or load_library(), name)(
+        q_p, pool_p, *scales_p, table_p, max_pages, lens_p, abort_p, starts_p, prefix_p, n_groups, out_p, lse_p,
+        ws_p, workspace.numel(), sm_scale, B, Hq, Hkv, D, page_size, num_pages, _launch_stream(stream, kv_pool.get_device())), name)
+
+
+def _scales(k_scale, v_scale):
+    return (k_scale, _F32S, "k_scale", None, False), (v_scale, _F32S, "v_scale", None, False)
 
 
 def fpk_paged_decode_attn_fp8_prefix(q, kv_pool, k_scale, v_scale, page_table, seq_lens, abort_mask,
                                      group_starts, prefix_lens, out, lse, workspace, *, Hkv, page_size,
                                      num_pages, sm_scale, stream=None):
     """Decode attention that reads each group's shared prefix once (out: bf16)."""
-    B, Hq, D = _attn_shapes(q, page_table, seq_lens, abort_mask, out, lse)
-    n_groups = _groups(group_starts, prefix_lens)
-    _expect_pool(kv_pool, 1, num_pages, Hkv, page_size, D)
-    _same_device(q, kv_pool, k_scale, v_scale, page_table, seq_lens, abort_mask, group_starts,
-                 prefix_lens, out, lse, workspace)
-    _check(load_library().fpk_paged_decode_attn_fp8_prefix(
-        _ptr(q, _BF16, "q"), _ptr(kv_pool, _U8, "kv_pool"),
-        _ptr(k_scale, _F32, "k_scale"), _ptr(v_scale, _F32, "v_scale"),
-        _ptr(page_table, _I32T, "page_table"), page_table.shape[1], _ptr(seq_lens, _I32T, "seq_lens"),
-        _ptr(abort_mask, _U8, "abort_mask", True), _ptr(group_starts, _I32T, "group_starts"),
-        _ptr(prefix_lens, _I32T, "prefix_lens"), n_groups,
-        _ptr(out, _BF16, "out"), _ptr(lse, _F32, "lse", True), _ptr(workspace, _U8, "workspace"),
-        workspace.numel(), sm_scale, B, Hq, Hkv, D, page_size, num_pages, _stream(stream)),
-        "fpk_paged_decode_attn_fp8_prefix")
+    _prefix("fpk_paged_decode_attn_fp8_prefix", True, q, kv_pool, _scales(k_scale, v_scale), page_table, seq_lens,
+            abort_mask, group_starts, prefix_lens, out, lse, workspace, Hkv, page_size, num_pages, sm_scale, stream)
 
 
 def fpk_paged_decode_attn_bf16_prefix(q, kv_pool, page_table, seq_lens, abort_mask, group_starts,
                                       prefix_lens, out, lse, workspace, *, Hkv, page_size, num_pages,
                                       sm_scale, stream=None):
     """BF16-cache variant of fpk_paged_decode_attn_fp8_prefix."""
-    B, Hq, D = _attn_shapes(q, page_table, seq_lens, abort_mask, out, lse)
-    n_groups = _groups(group_starts, prefix_lens)
-    _expect_pool(kv_pool, 1, num_pages, Hkv, page_size, D)
-    _same_device(q, kv_pool, page_table, seq_lens, abort_mask, group_starts, prefix_lens, out, lse,
-                 workspace)
-    _check(load_library().fpk_paged_decode_attn_bf16_prefix(
-        _ptr(q, _BF16, "q"), _ptr(kv_pool, _BF16_LIKE, "kv_pool"),
-        _ptr(page_table, _I32T, "page_table"), page_table.shape[1], _ptr(seq_lens, _I32T, "seq_lens"),
-        _ptr(abort_mask, _U8, "abort_mask", True), _ptr(group_starts, _I32T, "group_starts"),
-        _ptr(prefix_lens, _I32T, "prefix_lens"), n_groups,
-        _ptr(out, _BF16, "out"), _ptr(lse, _F32, "lse", True), _ptr(workspace, _U8, "workspace"),
-        workspace.numel(), sm_scale, B, Hq, Hkv, D, page_size, num_pages, _stream(stream)),
-        "fpk_paged_decode_attn_bf16_prefix")
+    _prefix("fpk_paged_decode_attn_bf16_prefix", False, q, kv_pool, (), page_table, seq_lens, abort_mask,
+            group_starts, prefix_lens, out, lse, workspace, Hkv, page_size, num_pages, sm_scale, stream)
 
 
 # --------------------------------------------------------- rotary positions
-def _rope_shapes(q, k, v, inv_freq, q_out, page_table, live_tags, expected_tags, abort_mask, Hkv,
-                 rot_dim, rows):
-    T, _, D = k.shape
-    _expect(k, "k", (T, Hkv, D))
-    _expect(v, "v", (T, Hkv, D))
-    Hq = 0 if q is None else q.shape[1]
-    if q is not None:
-        _expect(q, "q", (T, Hq, D))
-        _expect(q_out, "q_out", (T, Hq, D))
-    _expect(inv_freq, "inv_freq", (rot_dim // 2,))
-    B = page_table.shape[0]
-    if rows is not None and T != B:
-        raise FpkError(f"k has {T} rows for {B} requests")
-    _expect(expected_tags, "expected_tags", tuple(page_table.shape))
-    _expect(abort_mask, "abort_mask", (B,))
-    _same_device(q, k, v, inv_freq, q_out, page_table, live_tags, expected_tags, abort_mask)
-    return T, B, Hq, D
-
-
 def _rope(name, fp8, q, k, v, pos, inv_freq, q_out, kv_pool, scales, page_table, live_tags,
           expected_tags, abort_mask, Hkv, page_size, num_pages, rot_dim, interleaved, rot_scale,
           stream):
     """pos: (seq_lens,) of an append or (cu_seqlens, start_pos) of a prefill."""
+    T, _, D = k.shape
+    Hq = 0 if q is None else q.shape[1]
+    B, max_pages = page_table.shape
     append = len(pos) == 1
-    T, B, Hq, D = _rope_shapes(q, k, v, inv_freq, q_out, page_table, live_tags, expected_tags,
-                               abort_mask, Hkv, rot_dim, pos[0] if append else None)
-    _expect_pool(kv_pool, 1, num_pages, Hkv, page_size, D)
-    _expect(live_tags, "live_tags", (num_pages,))
-    _same_device(kv_pool, *pos, *scales)
+    if append and T != B:
+        raise FpkError(f"k has {T} rows for {B} requests")
     if append:
-        _expect(pos[0], "seq_lens", (B,))
-        mid, places = [], [_ptr(pos[0], _I32T, "seq_lens")]
+        where = ((pos[0], _I32S, "seq_lens", (B,), False),)
     else:
-        _expect(pos[0], "cu_seqlens", (B + 1,))
-        _expect(pos[1], "start_pos", (B,))
-        mid, places = [_ptr(pos[0], _I32T, "cu_seqlens"), T, _ptr(pos[1], _I32T, "start_pos", True)], []
-    _check(getattr(load_library(), name)(
-        _ptr(q, _BF16, "q", True), _ptr(k, _BF16, "k"), _ptr(v, _BF16, "v"), *mid,
-        _ptr(inv_freq, _F32, "inv_freq"), _ptr(q_out, _BF16, "q_out", True),
-        _ptr(kv_pool, _U8 if fp8 else _BF16_LIKE, "kv_pool"),
-        *(_ptr(s, _F32, n) for s, n in zip(scales, ("k_scale", "v_scale"))),
-        _ptr(page_table, _I32T, "page_table"), page_table.shape[1], *places,
-        _ptr(live_tags, _TAGS, "live_tags", True), _ptr(expected_tags, _TAGS, "expected_tags", True),
-        _ptr(abort_mask, _U8, "abort_mask", True), rot_dim, int(interleaved), rot_scale, B, Hq, Hkv, D,
-        page_size, num_pages, _stream(stream)), name)
+        where = ((pos[0], _I32S, "cu_seqlens", (B + 1,), False), (pos[1], _I32S, "start_pos", (B,), True))
+    scales = _scales(*scales) if fp8 else ()
+    (k_p, v_p, q_p, out_p, freq_p, pool_p, table_p, live_p, expected_p, abort_p, pos_p, *rest) = _pointers(
+        (k, _BF16S, "k", (T, Hkv, D), False), (v, _BF16S, "v", (T, Hkv, D), False),
+        (q, _BF16S, "q", (T, Hq, D), True), (q_out, _BF16S, "q_out", (T, Hq, D) if Hq else None, True),
+        (inv_freq, _F32S, "inv_freq", (rot_dim // 2,), False),
+        (kv_pool, _U8S if fp8 else _BF16_LIKE, "kv_pool", 2 * num_pages * Hkv * page_size * D, False),
+        (page_table, _I32S, "page_table", None, False), (live_tags, _TAGS, "live_tags", (num_pages,), True),
+        (expected_tags, _TAGS, "expected_tags", (B, max_pages), True),
+        (abort_mask, _U8S, "abort_mask", (B,), True), *where, *scales)
+    fn = getattr(_lib or load_library(), name)
+    last = (live_p, expected_p, abort_p, rot_dim, int(interleaved), rot_scale, B, Hq, Hkv, D, page_size,
+            num_pages, _launch_stream(stream, kv_pool.get_device()))
+    if append:
+        _check(fn(q_p, k_p, v_p, freq_p, out_p, pool_p, *rest, table_p, max_pages, pos_p, *last), name)
+    else:
+        _check(fn(q_p, k_p, v_p, pos_p, T, rest[0], freq_p, out_p, pool_p, *rest[1:], table_p, max_pages, *last), name)
 
 
 def fpk_rope_append_fp8(q, k_new, v_new, inv_freq, q_out, kv_pool, k_scale, v_scale, page_table,
@@ -535,55 +541,45 @@ def fpk_rope_prefill_bf16(q, k, v, cu_seqlens, start_pos, inv_freq, q_out, kv_po
 
 
 # ---------------------------------------------------------- forks and moves
-def _pool_layers(kv_pool, layers, num_pages, Hkv, page_size, D):
-    """(element bytes, bytes from one layer's pool to the next)"""
-    _expect_pool(kv_pool, layers, num_pages, Hkv, page_size, D)
-    el = kv_pool.element_size()
-    return el, 2 * num_pages * Hkv * page_size * D * el
-
-
-def _table_shapes(page_table, expected_tags, seq_lens, live_tags, abort_mask, num_pages):
+def _moves(kv_pool, page_table, expected_tags, seq_lens, live_tags, layers, Hkv, D, page_size, num_pages, *more):
+    """(B, max_pages, element bytes, bytes from one layer's pool to the next), addresses"""
     B, max_pages = page_table.shape
-    _expect(expected_tags, "expected_tags", (B, max_pages))
-    _expect(seq_lens, "seq_lens", (B,))
-    _expect(live_tags, "live_tags", (num_pages,))
-    _expect(abort_mask, "abort_mask", (B,))
-    return B, max_pages
+    if layers < 1:
+        raise FpkError(f"kv_pool has {kv_pool.numel()} elements for {layers} layers")
+    one = 2 * num_pages * Hkv * page_size * D
+    at = _pointers((kv_pool, (torch.uint8, *_BF16_LIKE), "kv_pool", layers * one, False),
+                   (page_table, _I32S, "page_table", None, False),
+                   (expected_tags, _TAGS, "expected_tags", (B, max_pages), False),
+                   (seq_lens, _I32S, "seq_lens", (B,), False), (live_tags, _TAGS, "live_tags", (num_pages,), False),
+                   *more)
+    el = kv_pool.element_size()
+    return (B, max_pages, el, one * el), at
 
 
 def fpk_kv_fork(kv_pool, page_table, expected_tags, seq_lens, live_tags, abort_mask, parent, child,
                 fresh, *, layers=1, Hkv, D, page_size, num_pages, stream=None):
     """Rows child[i] take over rows parent[i]: full pages shared, the page in use
     copied to fresh[i] in all layers of kv_pool ([layers][one pool], contiguous)."""
-    B, max_pages = _table_shapes(page_table, expected_tags, seq_lens, live_tags, abort_mask, num_pages)
-    el, stride = _pool_layers(kv_pool, layers, num_pages, Hkv, page_size, D)
     n = parent.numel()
-    _expect(child, "child", (n,))
-    _expect(fresh, "fresh", (n,))
-    _same_device(kv_pool, page_table, expected_tags, seq_lens, live_tags, abort_mask, parent, child, fresh)
-    _check(load_library().fpk_kv_fork(
-        _ptr(kv_pool, (_U8, *_BF16_LIKE), "kv_pool"), el, layers, stride,
-        _ptr(page_table, _I32T, "page_table"), max_pages, _ptr(expected_tags, _TAGS, "expected_tags"),
-        _ptr(seq_lens, _I32T, "seq_lens"), _ptr(live_tags, _TAGS, "live_tags"),
-        _ptr(abort_mask, _U8, "abort_mask", True), _ptr(parent, _I32T, "parent"),
-        _ptr(child, _I32T, "child"), _ptr(fresh, _I32T, "fresh"), n, B, Hkv, D, page_size, num_pages,
-        _stream(stream)), "fpk_kv_fork")
+    (B, max_pages, el, stride), (pool_p, table_p, expected_p, lens_p, live_p, abort_p, parent_p, child_p, fresh_p) = _moves(
+        kv_pool, page_table, expected_tags, seq_lens, live_tags, layers, Hkv, D, page_size, num_pages,
+        (abort_mask, _U8S, "abort_mask", (page_table.shape[0],), True), (parent, _I32S, "parent", None, False),
+        (child, _I32S, "child", (n,), False), (fresh, _I32S, "fresh", (n,), False))
+    _check((_lib or load_library()).fpk_kv_fork(
+        pool_p, el, layers, stride, table_p, max_pages, expected_p, lens_p, live_p, abort_p, parent_p, child_p,
+        fresh_p, n, B, Hkv, D, page_size, num_pages, _launch_stream(stream, kv_pool.get_device())), "fpk_kv_fork")
 
 
 def fpk_kv_compact(kv_pool, page_table, expected_tags, seq_lens, live_tags, src, dst, *, layers=1,
                    Hkv, D, page_size, num_pages, stream=None):
     """Pages src[i] (ascending) move to dst[i] in all layers of kv_pool; tables and tags follow."""
-    B, max_pages = _table_shapes(page_table, expected_tags, seq_lens, live_tags, None, num_pages)
-    el, stride = _pool_layers(kv_pool, layers, num_pages, Hkv, page_size, D)
     n = src.numel()
-    _expect(dst, "dst", (n,))
-    _same_device(kv_pool, page_table, expected_tags, seq_lens, live_tags, src, dst)
-    _check(load_library().fpk_kv_compact(
-        _ptr(kv_pool, (_U8, *_BF16_LIKE), "kv_pool"), el, layers, stride,
-        _ptr(page_table, _I32T, "page_table"), max_pages, _ptr(expected_tags, _TAGS, "expected_tags"),
-        _ptr(seq_lens, _I32T, "seq_lens"), _ptr(live_tags, _TAGS, "live_tags"),
-        _ptr(src, _I32T, "src"), _ptr(dst, _I32T, "dst"), n, B, Hkv, D, page_size, num_pages,
-        _stream(stream)), "fpk_kv_compact")
+    (B, max_pages, el, stride), (pool_p, table_p, expected_p, lens_p, live_p, src_p, dst_p) = _moves(
+        kv_pool, page_table, expected_tags, seq_lens, live_tags, layers, Hkv, D, page_size, num_pages,
+        (src, _I32S, "src", None, False), (dst, _I32S, "dst", (n,), False))
+    _check((_lib or load_library()).fpk_kv_compact(
+        pool_p, el, layers, stride, table_p, max_pages, expected_p, lens_p, live_p, src_p, dst_p, n, B, Hkv, D,
+        page_size, num_pages, _launch_stream(stream, kv_pool.get_device())), "fpk_kv_compact")
 
 
 def fpk_decode_status(workspace, stream=None) -> int:

@@ -28,19 +28,25 @@ struct MoveArgs {
   int n, B, Hkv, page_size, num_pages, max_pages, layers, tile_bytes;
 };
 
-// `bytes` (a multiple of 16) from src to dst by the CTA's threads.
-__device__ __forceinline__ void copy_run(uint8_t* dst, const uint8_t* src, int64_t bytes) {
-  const int64_t n = bytes >> 4;
+// `runs` runs of `units` 16-byte units, `stride` units apart, from src to dst by the CTA's threads: eight loads of
+// a thread on their way before its first store, across the runs.
+__device__ __forceinline__ void copy_runs(uint8_t* dst, const uint8_t* src, int runs, int units, int stride) {
   const uint4* s = reinterpret_cast<const uint4*>(src);
   uint4* d = reinterpret_cast<uint4*>(dst);
-  for (int64_t i = threadIdx.x; i < n; i += kMoveThreads * kMoveUnroll) {
+  const int total = runs * units;  // (a page of one layer: some 2^20 units at most)
+#pragma unroll 1
+  for (int i = threadIdx.x; i < total; i += kMoveThreads * kMoveUnroll) {
     uint4 x[kMoveUnroll];
+    int at[kMoveUnroll];
+#pragma unroll
+    for (int k = 0; k < kMoveUnroll; ++k) {
+      const int e = i + k * kMoveThreads, run = e / units;
+      at[k] = run * stride + e - run * units;
+      if (e < total) x[k] = __ldg(s + at[k]);
+    }
 #pragma unroll
     for (int k = 0; k < kMoveUnroll; ++k)
-      if (i + k * kMoveThreads < n) x[k] = __ldg(s + i + k * kMoveThreads);
-#pragma unroll
-    for (int k = 0; k < kMoveUnroll; ++k)
-      if (i + k * kMoveThreads < n) d[i + k * kMoveThreads] = x[k];
+      if (i + k * kMoveThreads < total) d[at[k]] = x[k];
   }
 }
 
@@ -66,11 +72,9 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const MoveArgs a, co
     const int src = prow[pages - 1];
     if (src < 0 || src >= a.num_pages || src == fr) return;
     const int layer = static_cast<int>(job / a.n);
-    const int64_t head_bytes = static_cast<int64_t>(a.page_size >> 4) * a.tile_bytes;
-    const int64_t run = static_cast<int64_t>((rem + 15) >> 4) * a.tile_bytes;
+    const int head = (a.page_size >> 4) * (a.tile_bytes >> 4), used = ((rem + 15) >> 4) * (a.tile_bytes >> 4);
     uint8_t* base = a.pool + layer * a.layer_stride;
-    for (int h = 0; h < a.Hkv; ++h)
-      copy_run(base + fr * a.page_bytes + h * head_bytes, base + src * a.page_bytes + h * head_bytes, run);
+    copy_runs(base + fr * a.page_bytes, base + src * a.page_bytes, a.Hkv, used, head);
     return;
   }
   int bad = !ok;
@@ -102,37 +106,39 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const MoveArgs a, co
   }
 }
 
-// CTA = (move, layer): one page copied.
-__global__ void __launch_bounds__(kMoveThreads) move_pages_kernel(const MoveArgs a, const int32_t* __restrict__ src,
-                                                                  const int32_t* __restrict__ dst) {
-  for (int64_t job = blockIdx.x; job < static_cast<int64_t>(a.n) * a.layers; job += gridDim.x) {
-    const int i = static_cast<int>(job % a.n);
-    const int s = __ldg(src + i), d = __ldg(dst + i);
-    if (s < 0 || s >= a.num_pages || d < 0 || d >= a.num_pages) continue;
-    uint8_t* base = a.pool + job / a.n * a.layer_stride;
-    copy_run(base + d * a.page_bytes, base + s * a.page_bytes, a.page_bytes);
+// The first remaps CTAs go over the tables, the others copy: CTA = (move, layer), one page.  An entry (r, j) of a
+// moved page looks its page up in the ascending list src.  Tags are as they were before the moves.
+__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const MoveArgs a, const int32_t* __restrict__ src,
+                                                               const int32_t* __restrict__ dst, int remaps) {
+  griddep_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= remaps) {
+    const int copies = static_cast<int>(gridDim.x) - remaps;
+    for (int64_t job = static_cast<int>(blockIdx.x) - remaps; job < static_cast<int64_t>(a.n) * a.layers; job += copies) {
+      const int i = static_cast<int>(job % a.n);
+      const int s = __ldg(src + i), d = __ldg(dst + i);
+      if (s < 0 || s >= a.num_pages || d < 0 || d >= a.num_pages) continue;
+      uint8_t* base = a.pool + job / a.n * a.layer_stride;
+      const int units = static_cast<int>(a.page_bytes >> 4);
+      copy_runs(base + d * a.page_bytes, base + s * a.page_bytes, 1, units, units);
+    }
+    return;
   }
-}
-
-// Table entries of moved pages: entry (r, j) looks its page up in the ascending
-// list src.  Tags are as they were before the moves.
-__global__ void __launch_bounds__(kMoveThreads) remap_kernel(const MoveArgs a, const int32_t* __restrict__ src,
-                                                             const int32_t* __restrict__ dst) {
   const int64_t total = static_cast<int64_t>(a.B) * a.max_pages;
   for (int64_t e = blockIdx.x * static_cast<int64_t>(kMoveThreads) + threadIdx.x; e < total;
-       e += static_cast<int64_t>(gridDim.x) * kMoveThreads) {
+       e += static_cast<int64_t>(remaps) * kMoveThreads) {
     const int r = static_cast<int>(e / a.max_pages);
     const int j = static_cast<int>(e - static_cast<int64_t>(r) * a.max_pages);
+    const int p = a.page_table[e];
+    const uint32_t expected = a.expected_tags[e];
     const int L = __ldg(a.seq_lens + r);
     if (L <= 0 || j > (L - 1) / a.page_size) continue;
-    const int p = a.page_table[e];
     if (p < 0 || p >= a.num_pages) continue;
     int lo = 0, hi = a.n;  // first index whose source is not below p
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (__ldg(src + mid) < p) lo = mid + 1; else hi = mid;
     }
-    if (lo >= a.n || __ldg(src + lo) != p || a.live_tags[p] != a.expected_tags[e]) continue;
+    if (lo >= a.n || __ldg(src + lo) != p || a.live_tags[p] != expected) continue;
     const int d = __ldg(dst + lo);
     if (d < 0 || d >= a.num_pages) continue;
     a.page_table[e] = d;
@@ -140,11 +146,12 @@ __global__ void __launch_bounds__(kMoveThreads) remap_kernel(const MoveArgs a, c
   }
 }
 
+// Behind the compaction (every table entry has read the tags by then).
 __global__ void __launch_bounds__(kMoveThreads) moved_tags_kernel(const MoveArgs a, const int32_t* __restrict__ src,
                                                                   const int32_t* __restrict__ dst) {
   const int i = blockIdx.x * kMoveThreads + threadIdx.x;
-  if (i >= a.n) return;
-  const int s = __ldg(src + i), d = __ldg(dst + i);
+  const int s = i < a.n ? __ldg(src + i) : -1, d = i < a.n ? __ldg(dst + i) : -1;
+  griddep_wait();
   if (s < 0 || s >= a.num_pages || d < 0 || d >= a.num_pages) return;
   a.live_tags[d] += 1u;
 }
@@ -216,16 +223,24 @@ extern "C" int fpk_kv_compact(void* kv_pool, int32_t elem_bytes, int32_t layers,
   if (st != FPK_OK || n == 0 || B == 0) return st;
   if (!src || !dst) return FPK_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // pages: as many CTAs as are resident at once; tables: one per 256 entries, up to as many again
   const int64_t jobs = static_cast<int64_t>(n) * layers;
-  if (jobs > 0) {
-    const int grid = resident_grid(reinterpret_cast<const void*>(move_pages_kernel), kMoveThreads, 0, jobs);
-    move_pages_kernel<<<grid, kMoveThreads, 0, s>>>(a, src, dst);
+  const int64_t entries = (static_cast<int64_t>(B) * max_pages + kMoveThreads - 1) / kMoveThreads;
+  const int full = resident_grid(reinterpret_cast<const void*>(compact_kernel), kMoveThreads, 0, jobs > entries ? jobs : entries);
+  const int copies = static_cast<int>(jobs < full ? jobs : full), remaps = static_cast<int>(entries < full ? entries : full);
+  if (copies + remaps > 0) {
+    compact_kernel<<<copies + remaps, kMoveThreads, 0, s>>>(a, src, dst, remaps);
+    if (checked_launch_status() != FPK_OK) return FPK_ECUDA;
   }
-  if (max_pages > 0) {
-    const int64_t want = (static_cast<int64_t>(B) * max_pages + kMoveThreads - 1) / kMoveThreads;
-    const int grid = resident_grid(reinterpret_cast<const void*>(remap_kernel), kMoveThreads, 0, want);
-    remap_kernel<<<grid, kMoveThreads, 0, s>>>(a, src, dst);
-  }
-  moved_tags_kernel<<<(n + kMoveThreads - 1) / kMoveThreads, kMoveThreads, 0, s>>>(a, src, dst);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((n + kMoveThreads - 1) / kMoveThreads);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = copies + remaps > 0 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, moved_tags_kernel, a, src, dst) != cudaSuccess) return FPK_ECUDA;
   return checked_launch_status();
 }
