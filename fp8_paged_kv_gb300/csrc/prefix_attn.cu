@@ -95,6 +95,8 @@ struct PfArgs {
   int32_t* own_len;  // [B] tokens behind the shared prefix; 0 for a dead request
   int32_t* dead;     // [B]
   const uint8_t* kv_pool;
+  uint8_t* q_image;  // [2][Hkv][B][G][128 bytes]: query rows as the products read them (two parts, or two halves)
+  float* q_mult;     // [Hkv][B][G]: their score multipliers
   const float* all_out;  // without groups: [B][Hq][D], [B][Hq], attention over all tokens
   const float* all_lse;
   float2* part_ml;   // partials: prefixes' 2 per (request, query head) and 256 rows per CTA, then own parts' osplits
@@ -118,8 +120,7 @@ struct PfCfg {
   static constexpr int kOffK = 2 * kQTile;
   static constexpr int kOffV = kOffK + kKStages * kKStage;
   static constexpr int kOffV16 = kOffV + kVStages * kVStage;
-  static constexpr int kOffMult = kOffV16 + kV16Bufs * kV16;   // score multiplier of each query row
-  static constexpr int kOffPiece = kOffMult + 2 * 128 * 4;
+  static constexpr int kOffPiece = kOffV16 + kV16Bufs * kV16;
   static constexpr int kOffBars = kOffPiece + kPfPieces * kPfPieceBytes;
   // barriers
   static constexpr int kReady = kFp8 ? kV16Bufs : kVStages;    // V blocks ready for the MMA
@@ -528,10 +529,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       : "memory");
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // 32 bytes: a whole sector from one thread.
 __device__ __forceinline__ void st_global8(float* dst, const float (&x)[8]) {
@@ -622,7 +624,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     return;
   }
   auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8 * i; };
-  float* const s_mult = reinterpret_cast<float*>(sm + C::kOffMult);
   PfSlot* const s_piece = reinterpret_cast<PfSlot*>(sm + C::kOffPiece);
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
   volatile int* const s_failed = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 4);
@@ -639,7 +640,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (kFp8 && i >= C::kBarVFree && i < C::kBarVFree + C::kVStages) arrivals = 4;   // V warps
     if (i >= C::kBarP && i < C::kBarP + 4) arrivals = 4;                             // a tile's softmax warps
     if (i >= C::kBarOFree && i < C::kBarOFree + 2) arrivals = 4;                     // a tile's softmax warps
-    if (i >= C::kBarQ && i < C::kBarQ + 2) arrivals = 4;                             // those
     if (i >= C::kBarQFree && i < C::kBarQFree + 2) arrivals = 10;                    // MMA and softmax warps
     if (i >= C::kBarPieceFree && i < C::kBarPieceFree + kPfPieces) arrivals = 16;    // every other warp; K's and V's half of one
     mbar_init(bar(i), arrivals);
@@ -669,94 +669,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     ++pn;
     return __all_sync(kFull, p.i0 < p.i1 && !*s_failed);
   };
-  // query rows [row, row + n) of a unit, by one warp, into rows `at`.. of a query buffer: all rows are asked for
-  // at once (half a warp per row, a lane 8 dims), to where bf16 has its two halves of the dims; e4m3's two
-  // parts of a row take the same 256 bytes
-  auto stage_rows = [&](const PfPiece& p, int buf, int row, int at, int n) {
-    const int c = lane & 15, hw = lane >> 4;
-    uint8_t* const tile = sm + buf * C::kQTile;
-    auto chunk = [&](int rr) -> uint8_t* { return tile + (c >> 3) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4); };
-    int g = p.row0 + row + hw, r = quotient(g, a.by_g), h = g - r * a.G;  // request and head of the row
-    const uint16_t* src = a.q + (static_cast<int64_t>(p.gfirst + r) * a.Hq + p.h * a.G + h) * kPfDim + c * 8;
-#pragma unroll 1
-    for (int i = hw; i < n; i += 2) {
-      cp_async16(smem_addr(chunk(at + i)), src);
-      h += 2;
-      src += 2 * kPfDim;
-      while (h >= a.G) {
-        h -= a.G;
-        src += static_cast<int64_t>(a.Hq - a.G) * kPfDim;
-      }
-    }
-    const float base = fabsf(a.sm_scale_log2) * (kFp8 ? __ldg(a.k_scale) : 1.f);
-    // a negative scale's sign goes to the query: maxima of raw scores are then those of scaled ones
-    const uint32_t flip = a.sm_scale_log2 < 0.f ? 0x80008000u : 0u;
-    cp_async_wait_all();
-    if (kFp8) {
-#pragma unroll 1
-      for (int k = 0; k < n; k += 4) {
-        uint32_t w[2][4], top[2] = {0, 0};  // largest |q|: bf16 magnitudes order as integers
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int i = k + 2 * y + hw;
-          const uint4 x = i < n ? *reinterpret_cast<const uint4*>(chunk(at + i)) : make_uint4(0, 0, 0, 0);
-          w[y][0] = x.x ^ flip;
-          w[y][1] = x.y ^ flip;
-          w[y][2] = x.z ^ flip;
-          w[y][3] = x.w ^ flip;
-#pragma unroll
-          for (int z = 0; z < 4; ++z) top[y] = max(top[y], max(w[y][z] & 0x7FFFu, (w[y][z] >> 16) & 0x7FFFu));
-        }
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) {
-          const uint32_t t0 = __shfl_xor_sync(kFull, top[0], o), t1 = __shfl_xor_sync(kFull, top[1], o);
-          top[0] = max(top[0], t0);
-          top[1] = max(top[1], t1);
-        }
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int i = k + 2 * y + hw, rr = at + i;
-          // e4m3 parts of q 2^e with its largest value in [128, 256): e = 134 - its exponent
-          const int ex = static_cast<int>(top[y] >> 7);
-          const int e = ex == 0 ? (top[y] == 0 ? 0 : 126) : min(max(134 - ex, -126), 126);
-          const float up = __int_as_float((127 + e) << 23);
-          uint32_t c0[2], c1[2];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const float lo = __uint_as_float(w[y][z] << 16) * up, hi = __uint_as_float(w[y][z] & 0xFFFF0000u) * up;
-            const uint32_t u = f32x2_to_e4m3x2(lo, hi);
-            const float2 f = e4m3x2_to_float2(u);
-            const uint32_t v = f32x2_to_e4m3x2(lo - f.x, hi - f.y);
-            if (z & 1) {
-              c0[z >> 1] |= u << 16;
-              c1[z >> 1] |= v << 16;
-            } else {
-              c0[z >> 1] = u;
-              c1[z >> 1] = v;
-            }
-          }
-          if (i < n) {  // (every lane has read its chunk: the maxima came from all)
-            uint8_t* const d = tile + rr * 128 + (((c >> 1) ^ (rr & 7)) << 4) + (c & 1) * 8;
-            *reinterpret_cast<uint2*>(d) = make_uint2(c0[0], c0[1]);
-            *reinterpret_cast<uint2*>(d + 16384) = make_uint2(c1[0], c1[1]);
-            if (c == 0)
-              s_mult[buf * 128 + rr] =
-                  ex == 255 ? __int_as_float(0x7fffffff) : fmaxf(base * __int_as_float((127 - e) << 23), kPfMinMult);
-          }
-        }
-      }
-    } else {
-      if (lane < n) s_mult[buf * 128 + at + lane] = fmaxf(base, kPfMinMult);
-#pragma unroll 1
-      for (int i = flip ? hw : n; i < n; i += 2) {
-        uint4* const x = reinterpret_cast<uint4*>(chunk(at + i));
-        *x = make_uint4(x->x ^ flip, x->y ^ flip, x->z ^ flip, x->w ^ flip);
-      }
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-  };
-
   if (first.b0 < first.b1) {
     PfPiece p;
     const int tpp = a.page_size >> 4;
@@ -1049,12 +961,27 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // ---- the queries into shared memory
         if (pair || t == 0) {
           const uint32_t u = buf ? uses[1] : uses[0];
-          if (u > 0) wait(C::kBarQFree + buf, u - 1);
-          if (busy) stage_rows(p, buf, lrow - lane, row - lane, min(32, p.rows - (lrow - lane)));
-          if (lane == 0) mbar_arrive(bar(C::kBarQ + buf));
+          if ((warp & 3) == 0) {
+            if (u > 0) wait(C::kBarQFree + buf, u - 1);
+            if (lane == 0) {
+              const int n = max(0, min(128, p.rows - lrow));
+              const int64_t at = (static_cast<int64_t>(p.h) * a.B + p.gfirst) * a.G + p.row0 + lrow;
+              const uint8_t* const src = a.q_image + at * 128;
+              const uint32_t dst = sbase + buf * C::kQTile;
+              if (n > 0) {
+                mbar_arrive_expect_tx(bar(C::kBarQ + buf), n * 256);
+                bulk_copy(dst, src, n * 128, bar(C::kBarQ + buf));
+                bulk_copy(dst + 16384, src + static_cast<int64_t>(a.B) * a.Hq * 128, n * 128, bar(C::kBarQ + buf));
+              } else {
+                mbar_arrive(bar(C::kBarQ + buf));
+              }
+            }
+          }
         }
+        const float mult = valid ? __ldcg(a.q_mult + (static_cast<int64_t>(p.h) * a.B + p.gfirst) * a.G + p.row0 + lrow) : 0.f;
         wait(C::kBarQ + buf, buf ? uses[1] : uses[0]);
-        const float mult = s_mult[buf * 128 + row];   // (whatever lies there for a row that is none)
+        // (whoever asked for the rows has them before the CTA ends, whatever failed elsewhere)
+        if ((pair || t == 0) && (warp & 3) == 0) mbar_wait(bar(C::kBarQ + buf), (buf ? uses[1] : uses[0]) & 1, a.status);
         __syncwarp();
         if (pair || p.qbuf == 0) ++uses[0];
         if (pair || p.qbuf == 1) ++uses[1];
@@ -1252,49 +1179,114 @@ __device__ __forceinline__ void own_mma(float (&d)[4], const uint32_t (&a)[4], u
   else mma_bf16(d, a, b0, b1);
 }
 
-// The pages that request r shares, found by one CTA on its own (as the planning kernel finds them for all):
-// its group ends at the first start above r.
-__device__ __forceinline__ int shared_pages(const PfArgs& a, int r) {
-  __shared__ int s_first[kOwnWarps], s_lo[kOwnWarps], s_least[kOwnWarps];
+// The pages that request r shares and its group's first request, found by one warp on its own (as the planning
+// kernel finds them for all): the group ends at the first start above r.
+struct OwnShare {
+  int skip, lo;
+};
+__device__ __forceinline__ OwnShare share_of(const PfArgs& a, int r, int lane) {
   const unsigned kFull = 0xffffffffu;
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   auto start = [&](int i) -> int { return min(max(__ldg(a.group_starts + i), 0), a.B); };
-  // (the first 128 starts, lengths and prefixes are asked for together; what is looked at again is in L1)
-  const int start0 = t <= a.n_groups ? start(t) : 0, live0 = t < a.B ? live_length(a, t) : 0;
-  const int prefix0 = t < a.n_groups ? __ldg(a.prefix_lens + t) : 0;
-  asm volatile("" ::"r"(prefix0));
-  int first = t <= a.n_groups && start0 > r ? t : 0x7fffffff;
-#pragma unroll 1
-  for (int i = t + 32 * kOwnWarps; i <= a.n_groups && first == 0x7fffffff; i += 32 * kOwnWarps)
-    if (start(i) > r) first = i;
+  int live[4];  // the first 128 lengths, asked for with the starts
+#pragma unroll
+  for (int k = 0; k < 4; ++k) live[k] = lane + 32 * k < a.B ? live_length(a, lane + 32 * k) : 0;
+  int first = 0x7fffffff;
+#pragma unroll 4
+  for (int i = lane; i <= a.n_groups; i += 32)
+    if (start(i) > r) first = min(first, i);
   first = __reduce_min_sync(kFull, first);
-  if (lane == 0) s_first[warp] = first;
-  __syncthreads();
+  OwnShare s = {0, 0};
+  if (first == 0 || first > a.n_groups) return s;
+  const int prefix = __ldg(a.prefix_lens + first - 1), hi = start(first);
+#pragma unroll 4
+  for (int i = lane; i < first; i += 32) s.lo = max(s.lo, start(i));
+  s.lo = __reduce_max_sync(kFull, s.lo);
+  if (hi - s.lo < 2) return s;
+  int least = 0x7fffffff;
 #pragma unroll
-  for (int w = 0; w < kOwnWarps; ++w) first = min(first, s_first[w]);
-  if (first == 0 || first > a.n_groups) return 0;
-  int lo = t < first ? start0 : 0;
-#pragma unroll 1
-  for (int i = t + 32 * kOwnWarps; i < first; i += 32 * kOwnWarps) lo = max(lo, start(i));
-  lo = __reduce_max_sync(kFull, lo);
-  if (lane == 0) s_lo[warp] = lo;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kOwnWarps; ++w) lo = max(lo, s_lo[w]);
-  const int hi = start(first);
-  if (hi - lo < 2) return 0;
-  int least = t >= lo && t < hi && live0 > 0 ? live0 : 0x7fffffff;
-#pragma unroll 1
-  for (int i = max(lo, 32 * kOwnWarps) + t; i < hi; i += 32 * kOwnWarps) {
+  for (int k = 0; k < 4; ++k)
+    if (lane + 32 * k >= s.lo && lane + 32 * k < hi && live[k] > 0) least = min(least, live[k]);
+#pragma unroll 4
+  for (int i = max(s.lo, 128) + lane; i < hi; i += 32) {
     const int L = live_length(a, i);
     if (L > 0) least = min(least, L);
   }
   least = __reduce_min_sync(kFull, least);
-  if (lane == 0) s_least[warp] = least;
-  __syncthreads();
+  s.skip = least == 0x7fffffff ? 0 : max(0, min(prefix, least)) / a.page_size;
+  return s;
+}
+
+// The query rows of request r, kv head h, as the products of a prefix read them: 128-byte rows with the 128-byte
+// swizzle of their place in the group's units.  e4m3 scores take a query as two parts, q 2^e = p0 + p1, e such
+// that the row's largest value lies in [128, 256): p0 is the value rounded to e4m3, p1 what that left, so that
+// the pair holds eight bits of mantissa (bf16 has eight) down to 2^-6 and steps of 2^-9 below.
+template <bool kFp8>
+__device__ __forceinline__ void put_query(const PfArgs& a, int r, int h, int lo, int lane) {
+  const unsigned kFull = 0xffffffffu;
+  const int g = lane >> 2, c = lane & 3;  // head of the group, dims 32 c .. 32 c + 31
+  const int64_t at = (static_cast<int64_t>(h) * a.B + r) * a.G + g;
+  const int swizzle = ((r - lo) * a.G + g) & 7;
+  uint8_t* const p0 = a.q_image + at * 128;
+  uint8_t* const p1 = p0 + static_cast<int64_t>(a.B) * a.Hq * 128;
+  const uint4* const src = reinterpret_cast<const uint4*>(
+      a.q + (static_cast<int64_t>(r) * a.Hq + h * a.G + (g < a.G ? g : 0)) * kPfDim + 32 * c);
+  // a negative scale's sign goes to the query: maxima of raw scores are then those of scaled ones
+  const uint32_t flip = a.sm_scale_log2 < 0.f ? 0x80008000u : 0u;
+  uint32_t w[16];
 #pragma unroll
-  for (int w = 0; w < kOwnWarps; ++w) least = min(least, s_least[w]);
-  return max(0, min(__ldg(a.prefix_lens + first - 1), least)) / a.page_size;
+  for (int i = 0; i < 4; ++i) {
+    const uint4 x = __ldg(src + i);
+    w[4 * i] = x.x ^ flip;
+    w[4 * i + 1] = x.y ^ flip;
+    w[4 * i + 2] = x.z ^ flip;
+    w[4 * i + 3] = x.w ^ flip;
+  }
+  float mult = fabsf(a.sm_scale_log2) * (kFp8 ? __ldg(a.k_scale) : 1.f);
+  if (kFp8) {
+    uint32_t top = 0;  // largest |q|: bf16 magnitudes order as integers
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    top = max(top, __shfl_xor_sync(kFull, top, 1));
+    top = max(top, __shfl_xor_sync(kFull, top, 2));
+    // e = 134 - the largest value's exponent
+    const int ex = static_cast<int>(top >> 7);
+    const int e = ex == 0 ? (top == 0 ? 0 : 126) : min(max(134 - ex, -126), 126);
+    const float up = __int_as_float((127 + e) << 23);
+    mult = ex == 255 ? __int_as_float(0x7fffffff) : mult * __int_as_float((127 - e) << 23);
+    if (ex != 255) mult = fmaxf(mult, kPfMinMult);
+    if (g < a.G) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t u[4], v[4];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t x = w[8 * i + k];
+          const float x0 = __uint_as_float(x << 16) * up, x1 = __uint_as_float(x & 0xFFFF0000u) * up;
+          const uint32_t y = f32x2_to_e4m3x2(x0, x1);
+          const float2 f = e4m3x2_to_float2(y);
+          const uint32_t z = f32x2_to_e4m3x2(x0 - f.x, x1 - f.y);
+          if (k & 1) {
+            u[k >> 1] |= y << 16;
+            v[k >> 1] |= z << 16;
+          } else {
+            u[k >> 1] = y;
+            v[k >> 1] = z;
+          }
+        }
+        const int to = ((2 * c + i) ^ swizzle) * 16;
+        *reinterpret_cast<uint4*>(p0 + to) = make_uint4(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<uint4*>(p1 + to) = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+  } else if (g < a.G) {
+    uint8_t* const half = c < 2 ? p0 : p1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(half + ((((c & 1) * 4 + i) ^ swizzle) << 4)) =
+          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    mult = fmaxf(mult, kPfMinMult);
+  }
+  if (g < a.G && c == 0) a.q_mult[at] = mult;
 }
 
 template <bool kFp8>
@@ -1305,8 +1297,10 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int z = static_cast<int>(blockIdx.x) % a.osplits, seg = static_cast<int>(blockIdx.x) / a.osplits;
   const int r = seg / a.Hkv, h = seg - r * a.Hkv;
-  const int live = live_length(a, r), skip = shared_pages(a, r);
-  const int L = max(0, live - skip * a.page_size);
+  const int live = live_length(a, r);
+  const OwnShare share = share_of(a, r, lane);
+  const int skip = share.skip, L = max(0, live - skip * a.page_size);
+  if (z == 0 && skip > 0 && warp == kOwnWarps - 1) put_query<kFp8>(a, r, h, share.lo, lane);
   const int tiles = (L + kPfTile - 1) / kPfTile, n = own_splits(tiles, a.osplits);
   if (z >= n) return;
   const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * z / n);
@@ -1625,14 +1619,14 @@ int prepare_prefix(int dev) {
   return FPK_OK;
 }
 
-// Most splits of a request's own tokens per kv head: about four waves of CTAs of four per SM in all.
+// Most splits of a request's own tokens per kv head: two waves of CTAs, four per SM, in all.
 int own_splits_most(int64_t B, int64_t Hkv, int64_t ctas) {
-  const int64_t n = 16 * ctas / (B * Hkv > 0 ? B * Hkv : 1);
+  const int64_t n = 8 * ctas / (B * Hkv > 0 ? B * Hkv : 1);
   return static_cast<int>(n < 1 ? 1 : n > 32 ? 32 : n);
 }
 
 struct PfLayout {
-  size_t gstart, group, start, per_request, ml, o, total;
+  size_t gstart, group, start, per_request, ml, o, image, mult, total;
 };
 // Behind the workspace of decode attention (batches without groups; its first word is the status word).
 PfLayout prefix_layout(int64_t B, int64_t Hq, int64_t Hkv, int64_t ctas, size_t decode_bytes) {
@@ -1645,7 +1639,9 @@ PfLayout prefix_layout(int64_t B, int64_t Hq, int64_t Hkv, int64_t ctas, size_t 
   l.per_request = l.start + up(ctas * static_cast<int64_t>(sizeof(PfGroup)));
   l.ml = l.per_request + up(3 * B * 4);
   l.o = l.ml + up(slots * 8);
-  l.total = l.o + up(slots * kPfDim * 4);
+  l.image = l.o + up(slots * kPfDim * 4);
+  l.mult = l.image + up(B * Hq * 256);
+  l.total = l.mult + up(B * Hq * 4);
   return l;
 }
 
@@ -1758,6 +1754,8 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   a.all_out = reinterpret_cast<float*>(ws + l.o);
   a.all_lse = reinterpret_cast<float*>(ws + l.ml);
   a.kv_pool = static_cast<const uint8_t*>(kv_pool);
+  a.q_image = ws + l.image;
+  a.q_mult = reinterpret_cast<float*>(ws + l.mult);
   a.osplits = own_splits_most(B, Hkv, ctas);
   a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
   a.part_o = reinterpret_cast<float*>(ws + l.o);

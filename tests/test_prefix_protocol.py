@@ -34,7 +34,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
              vfull=[Bar(1) for _ in range(VST)], vfree=[Bar(4 if fp8 else 2) for _ in range(VST)],
              ready=[Bar(4) for _ in range(ready_n)], used=[Bar(2) for _ in range(V16)],
              S=[Bar(1), Bar(1)], P=[[Bar(4), Bar(4)], [Bar(4), Bar(4)]], O=[Bar(1), Bar(1)],
-             ofree=[Bar(4), Bar(4)], Q=[Bar(4), Bar(4)], qfree=[Bar(10), Bar(10)],
+             ofree=[Bar(4), Bar(4)], Q=[Bar(1), Bar(1)], qfree=[Bar(10), Bar(10)],
              piece=[Bar(1) for _ in range(pieces_ring)], piecefree=[Bar(16) for _ in range(pieces_ring)],
              turn=[Bar(1), Bar(1)])
     late = []                       # (order in its queue, effect)
@@ -196,7 +196,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
             j0 += blocks
             later(q, lambda b=mine_buf, c=2 if pair else 1: B["qfree"][b].arrive(c))
 
-    def softmax(t):
+    def softmax(t, w):
         ns = pn = 0
         uses = [0, 0]
         while True:
@@ -205,14 +205,16 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
             if not blocks:
                 return
             b = t if pair else qb
-            if pair or t == 0:
+            if (pair or t == 0) and w == 0:
                 if uses[b] > 0:
                     yield from wait(B["qfree"][b], uses[b] - 1)
-                qof[b] = k
-                yield
-                B["Q"][b].arrive()
+
+                def landed(b=b, k=k):
+                    qof[b] = k
+                    B["Q"][b].arrive()
+                later(("q", b), landed)
             yield from wait(B["Q"][b], uses[b])
-            assert qof[b] == k, "multipliers"
+            assert qof[b] == k, "queries"
             yield
             for x in (0, 1):
                 if pair or qb == x:
@@ -236,7 +238,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
                 B["ofree"][t].arrive()
 
     tasks = [plan(), loader(B["kfull"], B["kfree"], kst, kof, "k"), loader(B["vfull"], B["vfree"], VST, vof, "v"),
-             mma(0), mma(1)] + [vwarp() for _ in range(4)] + [softmax(t) for t in (0, 1) for _ in range(4)]
+             mma(0), mma(1)] + [vwarp() for _ in range(4)] + [softmax(t, w) for t in (0, 1) for w in range(4)]
     weight = [0.002 if i == slow else rng.choice([1, 1, 3, 20]) for i in range(len(tasks))]
     def state():
         return [b.phase * 1000 + b.left for v in B.values() for x in v for b in (x if isinstance(x, list) else [x])]
