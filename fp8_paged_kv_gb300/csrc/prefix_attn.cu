@@ -65,6 +65,7 @@ constexpr int kPfThreads = 512;
 constexpr int kPfVWarp = 8, kPfLoadWarp = 12, kPfMmaWarp = 13, kPfPlanWarp = 15;  // two MMA warps
 constexpr int kPfPieces = 4, kPfPieceBytes = 176;  // pieces known ahead
 constexpr int kPfPlanThreads = 1024;
+constexpr int kPfTurnSpins = 4096;  // looks at the other tile's turns, some 40 cycles each
 constexpr int kPfMergeWarps = 4;
 
 // What the planning kernel finds of each group.
@@ -139,9 +140,8 @@ struct PfCfg {
   static constexpr int kBarPiece = kBarQFree + 2;              // [kPfPieces] piece known
   static constexpr int kBarPieceFree = kBarPiece + kPfPieces;  // [kPfPieces] piece read by every warp
   static constexpr int kBarDone = kBarPieceFree + kPfPieces;   // [2] every MMA of a warp completed
-  static constexpr int kBarTurn = kBarDone + 2;                // [tile] the other tile's products of a turn are out
-  static constexpr int kBars = kBarTurn + 2;
-  static constexpr int kOffMisc = kOffBars + 8 * kBars;        // tensor memory base, failure flag
+  static constexpr int kBars = kBarDone + 2;
+  static constexpr int kOffMisc = kOffBars + 8 * kBars;        // tensor memory base, failure flag, turns taken by each tile
   static constexpr int kSmem = kOffMisc + 16;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
@@ -645,7 +645,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     mbar_init(bar(i), arrivals);
     fence_barrier_init();
   }
-  if (threadIdx.x == 0) *s_failed = 0;
+  volatile int* const s_turns = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 8);
+  if (threadIdx.x == 0) *s_failed = s_turns[0] = s_turns[1] = 0;
   if (warp == kPfMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)),
                  "r"(512)
@@ -856,7 +857,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // same block in halves as the softmax hands P over, S of the next (which overwrites S and P: the
       // products of one thread run in order).  While a tile's softmax runs the other tile has the tensor
       // cores; on a unit of both tiles the warps take turns (PV and the next S), or else the two would run
-      // in step, their softmaxes too, and leave the tensor cores idle.
+      // in step, their softmaxes too, and leave the tensor cores idle (4080 cycles a block of 256 rows, the
+      // products' own time being 2050).  An issuing warp stands still until the tensor cores take its product,
+      // so all waits of a turn come before it, and turns are counted in shared memory, not by a barrier (some
+      // 60 cycles from warp to warp against 300 to 400; no result hangs on it, a turn not seen is gone without).
       //
       // On a unit of one row tile block j belongs to tile j mod 2.  A barrier's parity tells neighbouring
       // phases apart, no others, so a warp has to see every phase of a barrier it waits for: where the
@@ -870,7 +874,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // V, 16 tokens a step: e4m3 as two columns of core matrices (8 dims x 8 tokens, 128 B apart along
       // the dims, 2 KiB along the tokens), bf16 as rows of 32 bytes with the 32-byte swizzle
       const uint64_t vdesc = kFp8 ? smem_desc(base + C::kOffV16, 2048, 128, 0) : smem_desc(base + C::kOffV, 16, 256, 6);
-      uint32_t j0 = 0, v3 = 0, v3ph = 0, n0 = 0, n1 = 0, begun = 0, uses0 = 0, uses1 = 0, turns = 0;
+      uint32_t j0 = 0, v3 = 0, v3ph = 0, n0 = 0, n1 = 0, begun = 0, uses0 = 0, uses1 = 0;
+      int turns = 0;
       static_assert(C::kKStages % 2 == 0 && (!kFp8 || C::kReady == 2), "slots that tiles own");
       while (take_piece(p)) {
         const int pair_in = __any_sync(kFull, p.pair());
@@ -895,25 +900,49 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         };
 #pragma unroll 1
         for (uint32_t i = pair_in ? 0 : (j0 ^ t) & 1; i < nb + step; i += step) {
-          // PV of this tile's block before, S of block i
+          // PV of this tile's block before, S of block i: what they need first, then the turn
           const bool pair = varying(pair_in) != 0;
-          if (pair && (t == 1 || i > 0)) wait(C::kBarTurn + t, turns++);
+          const uint32_t ks = (j0 + i) % C::kKStages, m = i - step, jm = j0 + m;
+          if (i < nb) wait(C::kBarKFull + ks, (j0 + i) / C::kKStages);
+          uint32_t vs = 0;
           if (i >= step) {
-            const uint32_t m = i - step, jm = j0 + m;
             pass_v(m);
-            const uint32_t vs = kFp8 ? jm % C::kReady : v3;
+            vs = kFp8 ? jm % C::kReady : v3;
             wait(C::kBarReady + vs, kFp8 ? jm / C::kReady : v3ph);
             if (begins && begun > 0) wait(C::kBarOFree + t, begun - 1);  // O of the piece before has been read
+            wait(C::kBarP + 2 * t, n0++);
+          }
+          if (pair) {
+#pragma unroll 1
+            for (int spins = 0; s_turns[t ^ 1] - turns < t && spins < kPfTurnSpins; ++spins) {
+            }
+          }
+          tc_fence_after();
+          if (i >= step) {
             const uint64_t vd = vdesc + vs * ((kFp8 ? C::kV16 : C::kVStage) >> 4);
 #pragma unroll 1
             for (int h = 0; h < 2 && 2 * m + h < halves; ++h) {
-              wait(C::kBarP + 2 * t + h, h ? n1++ : n0++);
-              tc_fence_after();
+              if (h == 1) {
+                wait(C::kBarP + 2 * t + 1, n1++);
+                tc_fence_after();
+              }
               issue_o(tm + 256 + t * 128, tm + t * 128 + 32 * h, vd + h * 1024, kFp8 ? kPfOF16 : kPfOBf16,
                       !begins || h > 0);
             }
             begun += begins;
             begins = false;
+          }
+          if (i < nb) issue_s<kFp8>(tm + t * 128, qd, kdesc + ks * (C::kKStage >> 4));
+          if (pair) {
+            ++turns;
+            if (lane == 0) s_turns[t] = turns;
+          }
+          if (i < nb) {
+            commit_elected(bars + 8 * (C::kBarS + t));
+            commit_elected(bars + 8 * (C::kBarKFree + ks));
+            if (!pair) commit_elected(bars + 8 * (C::kBarKFree + ks));
+          }
+          if (i >= step) {
             commit_elected(bars + 8 * (C::kBarO + t));
             const uint32_t bv = bars + 8 * ((kFp8 ? C::kBarUsed : C::kBarVFree) + vs);
             commit_elected(bv);
@@ -923,22 +952,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               if (++v3 == C::kReady) v3 = 0, v3ph ^= 1;
             }
           }
-          if (i < nb) {
-            const uint32_t ks = (j0 + i) % C::kKStages;
-            wait(C::kBarKFull + ks, (j0 + i) / C::kKStages);
-            tc_fence_after();
-            issue_s<kFp8>(tm + t * 128, qd, kdesc + ks * (C::kKStage >> 4));
-            commit_elected(bars + 8 * (C::kBarS + t));
-            commit_elected(bars + 8 * (C::kBarKFree + ks));
-            if (!pair) commit_elected(bars + 8 * (C::kBarKFree + ks));
-          }
-          if (pair && lane == 0 && (t == 0 || i < nb)) mbar_arrive(bar(C::kBarTurn + (t ^ 1)));
         }
         pass_v(nb);
         j0 += nb;
-        // the queries: both warps' S of a buffer are done
+        // the queries: this warp's S are done (of a pair it answers for both buffers: it has seen both filled)
 #pragma unroll 1
-        for (int k = 0; k <= pair_in; ++k) commit_elected(bars + 8 * (C::kBarQFree + (pair_in ? t : qb)));
+        for (uint32_t b = pair_in ? 0 : qb; b <= (pair_in ? 1 : qb); ++b) commit_elected(bars + 8 * (C::kBarQFree + b));
       }
       // every product and every arrival it owes is done before the CTA ends
       commit_elected(bars + 8 * (C::kBarDone + t));

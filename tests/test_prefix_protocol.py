@@ -35,8 +35,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
              ready=[Bar(4) for _ in range(ready_n)], used=[Bar(2) for _ in range(V16)],
              S=[Bar(1), Bar(1)], P=[[Bar(4), Bar(4)], [Bar(4), Bar(4)]], O=[Bar(1), Bar(1)],
              ofree=[Bar(4), Bar(4)], Q=[Bar(1), Bar(1)], qfree=[Bar(10), Bar(10)],
-             piece=[Bar(1) for _ in range(pieces_ring)], piecefree=[Bar(16) for _ in range(pieces_ring)],
-             turn=[Bar(1), Bar(1)])
+             piece=[Bar(1) for _ in range(pieces_ring)], piecefree=[Bar(16) for _ in range(pieces_ring)])
     late = []                       # (order in its queue, effect)
     queues = {}
     slots = [None] * pieces_ring
@@ -44,6 +43,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
     kof, vof, cof = [None] * kst, [None] * VST, [None] * ready_n
     sof, oof = [None, None], [None, None]
     nb = len(pieces)
+    turned = [0, 0]
 
     def later(queue, effect):
         queues.setdefault(queue, []).append(effect)
@@ -118,7 +118,7 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
                 yield
 
     def mma(t):
-        j0 = v3 = v3r = begun = turns = pn = 0
+        j0 = v3 = v3r = begun = pn = 0
         n = [0, 0]
         uses = [0, 0]
         q = ("mma", t)
@@ -149,20 +149,28 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
 
             i = 0 if pair else (j0 ^ t) & 1
             while i < blocks + step:
-                if pair and (t == 1 or i > 0):
-                    yield from wait(B["turn"][t], turns)
-                    turns += 1
+                m, ks = i - step, (j0 + i) % kst
+                if i < blocks:
+                    yield from wait(B["kfull"][ks], (j0 + i) // kst)
+                    assert kof[ks] == (k, i), "K block"
                 if i >= step:
-                    m = i - step
                     yield from pass_v(m)
                     vs, vr = ((j0 + m) % V16, (j0 + m) // V16) if fp8 else (v3, v3r)
                     yield from wait(B["ready"][vs], vr)
                     assert cof[vs] == (k, m), "converted block"
                     if begins and begun > 0:
                         yield from wait(B["ofree"][t], begun - 1)
-                    for h in range(tail if m == blocks - 1 else 2):
-                        yield from wait(B["P"][t][h], n[h])
-                        n[h] += 1
+                    yield from wait(B["P"][t][0], n[0])
+                    n[0] += 1
+                # (a turn is waited for a while, then gone without: nothing depends on it)
+                for _ in range(rng.randint(0, 5)):
+                    if turned[t ^ 1] - turned[t] < t:
+                        yield
+                effects = []
+                if i >= step:
+                    if m < blocks - 1 or tail == 2:
+                        yield from wait(B["P"][t][1], n[1])
+                        n[1] += 1
                     begun += begins
                     begins = False
 
@@ -171,30 +179,29 @@ def simulate(pieces, fp8, seed, slow=None, pieces_ring=PIECES):
                         oof[t] = at
                         B["O"][t].arrive()
                         freed.arrive(c)
-                    later(q, pv)
+                    effects.append(pv)
                     if not fp8:
                         passed += 1
                         v3 += 1
                         if v3 == VST:
                             v3, v3r = 0, v3r + 1
                 if i < blocks:
-                    ks = (j0 + i) % kst
-                    yield from wait(B["kfull"][ks], (j0 + i) // kst)
-                    assert kof[ks] == (k, i), "K block"
-
                     def s(at=(k, i), ks=ks, b=mine_buf, c=1 if pair else 2):
                         assert kof[ks] == at and qof[b] == at[0], "operands of S"
                         sof[t] = at
                         B["S"][t].arrive()
                         B["kfree"][ks].arrive(c)
-                    later(q, s)
-                if pair and (t == 0 or i < blocks):
-                    B["turn"][t ^ 1].arrive()
+                    effects.insert(0, s)  # (its arrivals are asked for first, and come with the products')
+                for e in effects:
+                    later(q, e)
+                turned[t] += pair
                 yield
                 i += step
             yield from pass_v(blocks)
             j0 += blocks
-            later(q, lambda b=mine_buf, c=2 if pair else 1: B["qfree"][b].arrive(c))
+            for b in (0, 1):
+                if pair or qb == b:
+                    later(q, lambda b=b: B["qfree"][b].arrive())
 
     def softmax(t, w):
         ns = pn = 0
