@@ -1638,9 +1638,9 @@ int prepare_prefix(int dev) {
   return FPK_OK;
 }
 
-// Most splits of a request's own tokens per kv head: two waves of CTAs, four per SM, in all.
+// Most splits of a request's own tokens per kv head: one wave of CTAs, four per SM, in all (two waves: 2 us more for 4 to 32 requests).
 int own_splits_most(int64_t B, int64_t Hkv, int64_t ctas) {
-  const int64_t n = 8 * ctas / (B * Hkv > 0 ? B * Hkv : 1);
+  const int64_t n = 4 * ctas / (B * Hkv > 0 ? B * Hkv : 1);
   return static_cast<int>(n < 1 ? 1 : n > 32 ? 32 : n);
 }
 
