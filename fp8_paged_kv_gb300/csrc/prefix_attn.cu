@@ -1143,14 +1143,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 // ---------------------------------------------------------------------------
 // A request's own tokens, kv head by kv head, in up to osplits splits of at
 // least 256 tokens: a CTA of four warps per split, a warp taking every fourth
-// tile of 16 tokens straight from the pool into registers (mma.sync: the rows
+// tile of 16 tokens, by bulk copies into a ring of its own (mma.sync: the rows
 // are the at most eight heads of a GQA group, which is too few for a tcgen05
-// tile, and the work is reading).  The layout of the pool suits the fragments
-// with the dims of K and the tokens of V permuted: lane (g, c) = (lane / 4,
-// lane % 4) holds dims 32 c .. 32 c + 31 of its K tokens -- step kk of S takes
-// 32 c + 4 kk .. + 3 of q and K alike -- and tokens 4 c .. 4 c + 3 of its V dims,
-// which are the very tokens of the scores that the lane holds for head g: P
-// enters the second product from the registers where S left it.
+// tile, and the work is reading: 192 KiB per SM on their way).  The layout of
+// the pool suits the fragments with the dims of K and the tokens of V permuted:
+// lane (g, c) = (lane / 4, lane % 4) holds 16-byte chunks c, c + 4, .. of its K
+// tokens -- S takes them as they come, of q and K alike -- and tokens 4 c ..
+// 4 c + 3 of its V dims, which are the very tokens of the scores that the lane
+// holds for head g: P enters the second product from the registers where S
+// left it.
 constexpr int kOwnWarps = 4;
 constexpr int kOwnMinTiles = 16;  // of a split
 constexpr float kOwnFails = -1.f;  // sum of a split with a page outside the pool
@@ -1162,35 +1163,16 @@ __device__ __forceinline__ int64_t own_slot0(const PfArgs& a) {
   return static_cast<int64_t>(2) * a.B * a.Hq + static_cast<int64_t>(a.ctas) * kPfUnitRows;
 }
 
-// K and V words of one tile as the lane needs them: K 8 (16) words of two tokens, V 16 quads of tokens.
+// The ring of a warp, and the CTA's shared memory: rings (later the warps' O), barriers, maxima and sums.
+constexpr int kOwnRing = 16384;
 template <bool kFp8>
-struct OwnTile {
-  uint4 k[2][kFp8 ? 2 : 4];
-  uint32_t v[kFp8 ? 16 : 32];
+struct OwnCfg {
+  static constexpr int kTileBytes = 2 * kPfTile * kPfDim * (kFp8 ? 1 : 2);
+  static constexpr int kStages = kOwnRing / kTileBytes;
 };
-
-template <bool kFp8>
-__device__ __forceinline__ void own_load(OwnTile<kFp8>& x, const uint8_t* tile, int lane) {
-  constexpr int el = kFp8 ? 1 : 2;
-  const int g = lane >> 2, c = lane & 3;
-  const int tok = 4 * (g >> 1) + (g & 1);  // scores' column g of either half: tokens tok, tok + 2
-#pragma unroll
-  for (int n = 0; n < 2; ++n)
-#pragma unroll
-    for (int i = 0; i < 2 * el; ++i)
-      x.k[n][i] = __ldg(reinterpret_cast<const uint4*>(tile + ((tok + 2 * n) * kPfDim + 32 * c) * el) + i);
-  const uint8_t* v = tile + kPfTile * kPfDim * el + (g * kPfTile + 4 * c) * el;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (kFp8) {
-      x.v[i] = __ldg(reinterpret_cast<const uint32_t*>(v + i * 8 * kPfTile));
-    } else {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(v + i * 8 * kPfTile * 2));
-      x.v[2 * i] = w.x;
-      x.v[2 * i + 1] = w.y;
-    }
-  }
-}
+constexpr int kOwnSmem = kOwnWarps * (kOwnRing + 4 * 8 + kPfGroupMax * 8);
+constexpr int kOwnRow = kPfDim + 4;
+static_assert(kPfGroupMax * kOwnRow * 4 <= kOwnRing, "a warp's O fits its ring");
 
 template <bool kFp8>
 __device__ __forceinline__ void own_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -1310,8 +1292,8 @@ __device__ __forceinline__ void put_query(const PfArgs& a, int r, int h, int lo,
 
 template <bool kFp8>
 __device__ __forceinline__ void own_part(const PfArgs& a) {
-  __shared__ float s_o[kOwnWarps][kPfGroupMax][kPfDim + 4];
-  __shared__ float2 s_ml[kOwnWarps][kPfGroupMax];
+  using C = OwnCfg<kFp8>;
+  extern __shared__ __align__(128) uint8_t s_own[];
   const unsigned kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int z = static_cast<int>(blockIdx.x) % a.osplits, seg = static_cast<int>(blockIdx.x) / a.osplits;
@@ -1324,20 +1306,42 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
   if (z >= n) return;
   const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * z / n);
   const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (z + 1) / n);
+  uint8_t* const ring = s_own + warp * kOwnRing;
+  const uint32_t bars = smem_addr(s_own + kOwnWarps * kOwnRing) + warp * 32;
+  float2* const s_ml = reinterpret_cast<float2*>(s_own + kOwnWarps * (kOwnRing + 32));
   const int tpp = a.page_size >> 4;
-  constexpr int tile_bytes = 2 * kPfTile * kPfDim * (kFp8 ? 1 : 2);
   const int32_t* row = a.page_table + static_cast<int64_t>(r) * a.max_pages + skip;
-  auto page_of = [&](int t) -> int { return t < t1 ? __ldg(row + quotient(t, a.by_tpp)) : -1; };
-  auto good = [&](int page) -> bool { return page >= 0 && page < a.num_pages; };
-  auto at = [&](int t, int page) -> const uint8_t* {
-    return a.kv_pool +
-           ((static_cast<int64_t>(page) * a.Hkv + h) * tpp + t - quotient(t, a.by_tpp) * tpp) * tile_bytes;
+  const int count = (t1 - t0 - warp + kOwnWarps - 1) / kOwnWarps;  // this warp's tiles: t0 + warp + 4 k
+  // pages of 32 tiles, a lane each, and of the 32 behind them
+  auto pages_of = [&](int k) -> int {
+    return k + lane < count ? __ldg(row + quotient(t0 + warp + kOwnWarps * (k + lane), a.by_tpp)) : -1;
   };
-  int t = t0 + warp;
-  int page = page_of(t), next = page_of(t + kOwnWarps);
-  OwnTile<kFp8> x;
-  bool have = good(page);
-  if (have) own_load<kFp8>(x, at(t, page), lane);
+  int pages = pages_of(0), behind = pages_of(32);
+  if (lane < C::kStages) {
+    mbar_init(bars + 8 * lane, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  uint32_t there = 0, phase = 0;  // stages with a tile on its way or landed; parities
+  auto ask = [&](int k) {
+    if (k >= count) return;
+    if (k > 0 && (k & 31) == 0) {
+      pages = behind;
+      behind = pages_of(k + 32);
+    }
+    const int page = __shfl_sync(kFull, pages, k & 31), st = k % C::kStages;
+    there &= ~(1u << st);
+    if (page < 0 || page >= a.num_pages) return;
+    there |= 1u << st;
+    const int t = t0 + warp + kOwnWarps * k;
+    if (lane == 0) {
+      const int64_t tile = (static_cast<int64_t>(page) * a.Hkv + h) * tpp + t - quotient(t, a.by_tpp) * tpp;
+      mbar_arrive_expect_tx(bars + 8 * st, C::kTileBytes);
+      bulk_copy(smem_addr(ring) + st * C::kTileBytes, a.kv_pool + tile * C::kTileBytes, C::kTileBytes, bars + 8 * st);
+    }
+  };
+#pragma unroll 1
+  for (int k = 0; k < C::kStages; ++k) ask(k);
   // ---- queries of the GQA group (head g): A fragments, rows 8 .. 15 zero; e4m3: f16 of q 2^e
   uint32_t qa[8][2];
   float mult = fabsf(a.sm_scale_log2) * (kFp8 ? __ldg(a.k_scale) : 1.f);
@@ -1346,7 +1350,8 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       w[i] = g < a.G ? __ldg(reinterpret_cast<const uint4*>(
-                                 a.q + (static_cast<int64_t>(r) * a.Hq + h * a.G + g) * kPfDim + 32 * c) + i)
+                                 a.q + (static_cast<int64_t>(r) * a.Hq + h * a.G + g) * kPfDim +
+                                 (kFp8 ? 16 * (c + 4 * (i >> 1)) + 8 * (i & 1) : 8 * (c + 4 * i))))
                      : make_uint4(0, 0, 0, 0);
     const uint32_t flip = a.sm_scale_log2 < 0.f ? 0x80008000u : 0u;
     uint32_t q[16] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w,
@@ -1378,48 +1383,56 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
     for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
   bool bad = false;
 #pragma unroll 1
-  for (; t < t1; t += kOwnWarps) {
-    if (!have) {
+  for (int k = 0; k < count; ++k) {
+    const int st = k % C::kStages, t = t0 + warp + kOwnWarps * k;
+    if ((there >> st & 1) == 0) {
       bad = true;  // a page outside the pool
-      page = next;
-      next = page_of(t + 2 * kOwnWarps);
-      have = good(page);
-      if (have) own_load<kFp8>(x, at(t + kOwnWarps, page), lane);
+      ask(k + C::kStages);
       continue;
     }
-    // ---- scores of head g, tokens 4 c .. 4 c + 3
+    mbar_wait(bars + 8 * st, phase >> st & 1, a.status);
+    __syncwarp();
+    phase ^= 1u << st;
+    const uint8_t* const tile = ring + st * C::kTileBytes;
+    // ---- scores of head g, tokens 4 c .. 4 c + 3: columns g of the halves are tokens tok, tok + 2
     float s[2][4] = {};
+    constexpr int el = kFp8 ? 1 : 2;
+    const uint8_t* const krow = tile + (4 * (g >> 1) + (g & 1)) * kPfDim * el + c * 16;
 #pragma unroll
     for (int n2 = 0; n2 < 2; ++n2) {
-      const uint32_t* kw = reinterpret_cast<const uint32_t*>(x.k[n2]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t b0, b1;
-        if (kFp8) {
-          e4m3x4_to_f16x4(kw[i], b0, b1);
-        } else {
-          b0 = kw[2 * i];
-          b1 = kw[2 * i + 1];
+      for (int i = 0; i < 2 * el; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(krow + 2 * n2 * kPfDim * el + 64 * i);
+        const uint32_t kw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int y = 0; y < 4 / el; ++y) {
+          uint32_t b0, b1;
+          if (kFp8) {
+            e4m3x4_to_f16x4(kw[y], b0, b1);
+          } else {
+            b0 = kw[2 * y];
+            b1 = kw[2 * y + 1];
+          }
+          const int step = i * (4 / el) + y;
+          const uint32_t af[4] = {qa[step][0], 0u, qa[step][1], 0u};
+          own_mma<kFp8>(s[n2], af, b0, b1);
         }
-        const uint32_t af[4] = {qa[i][0], 0u, qa[i][1], 0u};
-        own_mma<kFp8>(s[n2], af, b0, b1);
       }
     }
     uint32_t v[16][2];
+    const uint8_t* const vrow = tile + kPfTile * kPfDim * el + (g * kPfTile + 4 * c) * el;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       if (kFp8) {
-        e4m3x4_to_f16x4(x.v[i], v[i][0], v[i][1]);
+        e4m3x4_to_f16x4(*reinterpret_cast<const uint32_t*>(vrow + i * 8 * kPfTile), v[i][0], v[i][1]);
       } else {
-        v[i][0] = x.v[2 * i];
-        v[i][1] = x.v[2 * i + 1];
+        const uint2 x = *reinterpret_cast<const uint2*>(vrow + i * 8 * kPfTile * 2);
+        v[i][0] = x.x;
+        v[i][1] = x.y;
       }
     }
-    // ---- the next tile's loads under this one's softmax and second product
-    page = next;
-    next = page_of(t + 2 * kOwnWarps);
-    have = good(page);
-    if (have) own_load<kFp8>(x, at(t + kOwnWarps, page), lane);
+    __syncwarp();  // the stage has been read
+    ask(k + C::kStages);
     float e[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};
     const int left = L - t * kPfTile - 4 * c;  // tokens of this lane's four that exist
     if (L - t * kPfTile < kPfTile) {
@@ -1473,13 +1486,15 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
   // ---- the four warps' states
   l += __shfl_xor_sync(kFull, l, 1);
   l += __shfl_xor_sync(kFull, l, 2);
-  if (c == 0) s_ml[warp][g] = make_float2(m, l);
+  if (c == 0) s_ml[warp * kPfGroupMax + g] = make_float2(m, l);
+  float* const mine = reinterpret_cast<float*>(ring);  // (its last tile has been read)
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    s_o[warp][2 * c][16 * i + g] = o[i][0];
-    s_o[warp][2 * c + 1][16 * i + g] = o[i][1];
-    s_o[warp][2 * c][16 * i + 8 + g] = o[i][2];
-    s_o[warp][2 * c + 1][16 * i + 8 + g] = o[i][3];
+    mine[2 * c * kOwnRow + 16 * i + g] = o[i][0];
+    mine[(2 * c + 1) * kOwnRow + 16 * i + g] = o[i][1];
+    mine[2 * c * kOwnRow + 16 * i + 8 + g] = o[i][2];
+    mine[(2 * c + 1) * kOwnRow + 16 * i + 8 + g] = o[i][3];
   }
   const bool fails = __syncthreads_or(bad);
   const float vscale = kFp8 ? __ldg(a.v_scale) : 1.f;
@@ -1487,14 +1502,14 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
   for (int hd = warp; hd < a.G; hd += kOwnWarps) {
     float M = -INFINITY, W = 0.f;
 #pragma unroll
-    for (int w = 0; w < kOwnWarps; ++w) M = fmaxf(M, s_ml[w][hd].x);
+    for (int w = 0; w < kOwnWarps; ++w) M = fmaxf(M, s_ml[w * kPfGroupMax + hd].x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kOwnWarps; ++w) {
-      const float2 ml = s_ml[w][hd];
+      const float2 ml = s_ml[w * kPfGroupMax + hd];
       if (ml.x == -INFINITY) continue;
       const float f = fast_exp2(ml.x - M);
-      const float4 y = *reinterpret_cast<const float4*>(&s_o[w][hd][4 * lane]);
+      const float4 y = *reinterpret_cast<const float4*>(s_own + w * kOwnRing + (hd * kOwnRow + 4 * lane) * 4);
       W = fmaf(ml.y, f, W);
       acc.x = fmaf(y.x, f, acc.x);
       acc.y = fmaf(y.y, f, acc.y);
@@ -1509,7 +1524,7 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
 
 // Runs beside the planning kernel: it needs nothing of it.  Its end implies that kernel's, though: one CTA waits.
 template <bool kFp8>
-__global__ void __launch_bounds__(32 * kOwnWarps, kFp8 ? 4 : 3) prefix_own_kernel(const PfArgs a) {
+__global__ void __launch_bounds__(32 * kOwnWarps, 3) prefix_own_kernel(const PfArgs a) {
   griddep_launch_dependents();
   own_part<kFp8>(a);
   if (blockIdx.x == 0) griddep_wait();
@@ -1632,13 +1647,14 @@ int prepare_prefix(int dev) {
   std::atomic<int>& slot = g_pf_ready[kFp8][dev];
   if (slot.load(std::memory_order_relaxed) > 0) return FPK_OK;
   if (cudaFuncSetAttribute(prefix_attn_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           PfCfg<kFp8>::kSmem) != cudaSuccess)
+                           PfCfg<kFp8>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(prefix_own_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmem) != cudaSuccess)
     return FPK_ECUDA;
   slot.store(1, std::memory_order_relaxed);
   return FPK_OK;
 }
 
-// Most splits of a request's own tokens per kv head: one wave of CTAs, four per SM, in all (two waves: 2 us more for 4 to 32 requests).
+// Most splits of a request's own tokens per kv head: about a wave of CTAs, three per SM, in all (two waves: 2 us more for 4 to 32 requests).
 int own_splits_most(int64_t B, int64_t Hkv, int64_t ctas) {
   const int64_t n = 4 * ctas / (B * Hkv > 0 ? B * Hkv : 1);
   return static_cast<int>(n < 1 ? 1 : n > 32 ? 32 : n);
@@ -1811,7 +1827,7 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   if (own > 0x7fffffff) return FPK_EUNSUPPORTED;
   prefix_plan_kernel<<<1, kPfPlanThreads, 0, s>>>(a);
   if (checked_launch_status() != FPK_OK) return FPK_ECUDA;
-  if (launch_dependent(prefix_own_kernel<kFp8>, static_cast<int>(own), 32 * kOwnWarps, 0, s, a) != FPK_OK ||
+  if (launch_dependent(prefix_own_kernel<kFp8>, static_cast<int>(own), 32 * kOwnWarps, kOwnSmem, s, a) != FPK_OK ||
       launch_dependent(prefix_attn_kernel<kFp8>, ctas, kPfThreads, PfCfg<kFp8>::kSmem, s, a, kmap, vmap) != FPK_OK)
     return FPK_ECUDA;
   return launch_dependent(prefix_merge_kernel, merge, 32 * kPfMergeWarps, 0, s, a);
