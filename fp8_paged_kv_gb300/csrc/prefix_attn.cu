@@ -516,6 +516,30 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Their largest value (a NaN counts only among NaNs), found on the way: the values themselves are dropped.
+__device__ __forceinline__ float tmem_max64(uint32_t taddr) {
+  uint32_t r[64];
+  float top;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x64.max.f32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+      "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, "
+      "%42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+      "%62, %63}, %64, [%65]; "
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=f"(top)
+      : "r"(taddr)
+      : "memory");
+  return top;
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -542,7 +566,7 @@ __device__ __forceinline__ void st_global8(float* dst, const float (&x)[8]) {
                : "memory");
 }
 
-// Packed fp32 pairs and the three-input maximum: one instruction each on sm_103a.
+// Packed fp32 pairs: one instruction each on sm_103a.
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
   float2 r;
   asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
@@ -559,12 +583,6 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
       : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
   return r;
 }
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
-
 __device__ __forceinline__ void tmem_fill1(uint32_t taddr, float x) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
 }
@@ -1037,13 +1055,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             float s[64], mx = -INFINITY;
 #pragma unroll 1
             for (int h = 0; h < halves; ++h) {
-              tmem_ld64(ts + 64 * h, s);
-              float m4[4] = {max3(mx, s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
-#pragma unroll
-              for (int k = 8; k < 64; k += 8)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) m4[x] = max3(m4[x], s[k + 2 * x], s[k + 2 * x + 1]);
-              mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+              mx = fmaxf(mx, tmem_max64(ts + 64 * h));
             }
             const float mb = mx == -INFINITY ? -INFINITY : mx * mult;
             const bool grown = mb > m + kPfGrow || (m == -INFINITY && mb != -INFINITY);
