@@ -474,24 +474,6 @@ __device__ __forceinline__ void issue_o(uint32_t d, uint32_t p, uint64_t vdesc, 
       : "memory");
 }
 
-// 32 consecutive columns of this thread's tensor memory lane, waited for.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
-      "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32]; "
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // 64 consecutive columns of this thread's tensor memory lane, waited for.
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
   uint32_t r[64];
@@ -516,8 +498,8 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Their largest value (a NaN counts only among NaNs), found on the way: the values themselves are dropped.
-__device__ __forceinline__ float tmem_max64(uint32_t taddr) {
+// The same with their largest value (a NaN counts only among NaNs), found on the way.
+__device__ __forceinline__ float tmem_ld64_max(uint32_t taddr, float (&v)[64]) {
   uint32_t r[64];
   float top;
   asm volatile(
@@ -537,7 +519,29 @@ __device__ __forceinline__ float tmem_max64(uint32_t taddr) {
         "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=f"(top)
       : "r"(taddr)
       : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
   return top;
+}
+
+// 16 columns times f.
+__device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16]; "
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16}; "
+      ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -1052,10 +1056,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               }
               tmem_wait_st();
             }
-            float s[64], mx = -INFINITY;
-#pragma unroll 1
-            for (int h = 0; h < halves; ++h) {
-              mx = fmaxf(mx, tmem_max64(ts + 64 * h));
+            // the second half's maximum, then the first half with its own
+            float s[64], mx;
+            {
+              const float top = halves == 2 ? tmem_ld64_max(ts + 64, s) : -INFINITY;
+              mx = fmaxf(tmem_ld64_max(ts, s), top);
             }
             const float mb = mx == -INFINITY ? -INFINITY : mx * mult;
             const bool grown = mb > m + kPfGrow || (m == -INFINITY && mb != -INFINITY);
@@ -1065,14 +1070,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               l *= f;
               if (any) {  // O of the blocks before
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                  float o[32];
-                  tmem_ld32(to + 32 * c, o);
-                  uint32_t z[32];
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) z[k] = __float_as_uint(o[k] * f);
-                  tmem_st32(to + 32 * c, z);
-                }
+                for (int c = 0; c < 8; ++c) tmem_scale16(to + 16 * c, f);
               }
             }
             const float ref = m == -INFINITY ? 0.f : m;
@@ -1080,7 +1078,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
             for (int h = 0; h < halves; ++h) {
-              tmem_ld64(ts + 64 * h, s);
+              if (h == 1) tmem_ld64(ts + 64, s);
               uint32_t w[32];
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
