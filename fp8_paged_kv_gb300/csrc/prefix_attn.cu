@@ -1748,10 +1748,10 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   const int tpp = page_size / kPfTile;
   const int64_t tiles = static_cast<int64_t>(num_pages) * Hkv * tpp;
   // tile numbers are 32-bit tensor-map coordinates; rows and the work list's length (at most a unit
-  // of the table's width per request and kv head) are counted in 31 bits
+  // of the table's width per request and kv head) are counted in 31 bits, rows divided by reciprocals (2^28)
   const int64_t width = (static_cast<int64_t>(max_pages) * page_size + kPfBlk - 1) / kPfBlk;
   const int64_t longest = width * kPfCostPair + kPfStartPair;
-  if (tiles > 0x7fffffff || static_cast<int64_t>(B) * Hq > 0x7fffffff / 4 || width > (int64_t(1) << 24) ||
+  if (tiles > 0x7fffffff || static_cast<int64_t>(B) * Hq >= (int64_t(1) << 28) || width > (int64_t(1) << 24) ||
       longest > 0x7fffffff / (static_cast<int64_t>(B > 0 ? B : 1) * Hkv))
     return FPK_EUNSUPPORTED;
   if (B == 0) return FPK_OK;

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
   const int64_t row = i / kRopeUnits / a.hsplit;
   if (row >= w.rows) return;
   const Unit x = unit_of(a, u);
-  const int pos = __ldg(w.seq_lens + row) - 1;
+  const int length = __ldg(w.seq_lens + row), pos = max(length, 1) - 1;
   // a source row of the head list; queries may be rotated in place: plain loads
   auto source = [&](int h) -> const uint16_t* {
     if (h < a.Hq) return a.q + (row * a.Hq + h) * kRopeDim;
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
   bool value = h >= a.Hq + w.Hkv;
   uint4 x0 = *reinterpret_cast<const uint4*>(src + (value ? 16 * u : x.d0));
   uint4 x1 = *reinterpret_cast<const uint4*>(src + (value ? 16 * u + 8 : x.d1));
-  if (pos < 0) return;
+  if (length <= 0) return;
   const int page = h + (heads - 1 - h) / a.hsplit * a.hsplit >= a.Hq ? page_for(w, static_cast<int>(row), pos) : -1;
   const int tpp = w.page_size >> 4, off = pos % w.page_size;
   __shared__ float4 s_turn[4][kRopeThreads];  // a thread's own

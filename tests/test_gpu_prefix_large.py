@@ -94,3 +94,32 @@ def test_one_workspace_for_every_shape(fp8):
     graph.replay()
     for c, s, ref in zip(cases, states, refs):
         check(c, s, ref, "graph")
+
+
+@BOTH
+@pytest.mark.parametrize("G,ps", [(1, 16), (2, 32), (3, 64), (5, 256), (6, 16), (7, 128), (8, 16)])
+def test_no_groups_shapes(fp8, G, ps):
+    c = make([], fp8=fp8, Hkv=3, G=G, ps=ps, lead=13, tail=2, seed=G)
+    check(c, call(c), reference(c))
+
+
+@BOTH
+def test_no_groups_dead_requests(fp8):
+    c = make([], fp8=fp8, lead=6, seed=3)
+    table, lens = c["table"].copy(), c["lens"].copy()
+    abort = np.array([0, 1, 0, 0, 0, 0], np.uint8)
+    table[2, 1], table[3, 0], table[4, 0] = -1, c["P"], -9
+    lens[5] = table.shape[1] * c["ps"] + 1
+    lens[0] = 0
+    check(c, call(c, abort=abort, table=table, lens=lens), reference(c, abort=abort, table=table, lens=lens))
+
+
+@BOTH
+def test_more_groups_than_a_warp_looks_up_at_once(fp8):
+    groups = [(40 + i % 90, [41 + i % 90 + (7 * i + r) % 60 for r in range(2 + i % 2)]) for i in range(150)]
+    c = make(groups, fp8=fp8, Hkv=1, G=4, lead=3, seed=8)
+    assert c["B"] > 256
+    check(c, call(c), reference(c))
+    lens = c["lens"].copy()
+    lens[::5] = 0                      # groups whose first, last or all requests are dead
+    check(c, call(c, lens=lens), reference(c, lens=lens))

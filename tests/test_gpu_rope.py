@@ -297,3 +297,41 @@ def test_many_requests():
     c = scene(n, [(7 * r) % 40 for r in range(5000)], fp8=True, Hq=1, Hkv=1, ps=16, seed=9)
     f = freqs(32)
     check(c, launch(c, f, rot=32), f, rot=32)
+
+
+@BOTH
+def test_shortest_lengths_leave_everything(fp8):
+    for low in (0, -1, -2 ** 31):
+        c = scene([1, 1, 1], [3, 40, 7], fp8=fp8, Hq=4, Hkv=2, ps=16, seed=12)
+        f = freqs(64)
+        s = launch(c, f, rot=64, append=True, guard=True)
+        torch.cuda.synchronize()
+        s["pool"].copy_(dev(c["pool"]).view(s["pool"].dtype))
+        s["qo"].fill_(7.0)
+        s["abort"].zero_()
+        s["lens"].fill_(low)
+        launch(c, f, rot=64, append=True, guard=True, state=s)
+        torch.cuda.synchronize()
+        assert (s["qo"] == 7.0).all() and not s["abort"].any()
+        assert torch.equal(s["pool"].view(torch.uint8).cpu(), torch.from_numpy(c["pool"]).view(torch.uint8))
+
+
+@BOTH
+@pytest.mark.parametrize("t0,n", [(0, 1), (1, 14), (2, 13), (3, 9), (4, 8), (5, 11), (8, 8), (7, 2), (0, 15), (15, 1), (15, 33)])
+def test_ragged_tiles(fp8, t0, n):
+    # every width of piece that a tile's values may be written in
+    c = scene([n, 0, n], [t0, 5, 32 + t0], fp8=fp8, Hq=9, Hkv=9, ps=32, seed=t0 * 16 + n)
+    f = freqs(96)
+    check(c, launch(c, f, rot=96), f, rot=96)
+
+
+def test_more_tokens_than_offsets_name():
+    # rows behind the last request are nobody's: left as they are
+    c = scene([20, 5], [0, 3], fp8=True, Hq=4, Hkv=2, ps=16, seed=5)
+    f = freqs(128)
+    whole = {k: torch.cat([c[k], torch.ones(9, *c[k].shape[1:], dtype=c[k].dtype)]) for k in ("q", "k", "v")}
+    s = launch(dict(c, **whole), f, rot=128)
+    torch.cuda.synchronize()
+    assert (s["qo"][c["T"]:] == 7.0).all()
+    s["qo"] = s["qo"][:c["T"]]
+    check(c, s, f, rot=128)
