@@ -289,6 +289,7 @@ __device__ __forceinline__ bool next_piece(const PfArgs& a, PfCursor& c, PfPiece
 __global__ void __launch_bounds__(kPfPlanThreads, 1) prefix_plan_kernel(const PfArgs a) {
   __shared__ int s_sum[kPfPlanThreads / 32];
   __shared__ int s_max[kPfPlanThreads / 32];
+  griddep_wait();  // what ran before is over: the own parts, which do not wait, may start behind it
   griddep_launch_dependents();
   const unsigned kFull = 0xffffffffu;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -1835,9 +1836,8 @@ int prefix_entry(const void* q, const void* kv_pool, const float* k_scale, const
   }
   const int64_t own = static_cast<int64_t>(B) * Hkv * a.osplits;
   if (own > 0x7fffffff) return FPK_EUNSUPPORTED;
-  prefix_plan_kernel<<<1, kPfPlanThreads, 0, s>>>(a);
-  if (checked_launch_status() != FPK_OK) return FPK_ECUDA;
-  if (launch_dependent(prefix_own_kernel<kFp8>, static_cast<int>(own), 32 * kOwnWarps, kOwnSmem, s, a) != FPK_OK ||
+  if (launch_dependent(prefix_plan_kernel, 1, kPfPlanThreads, 0, s, a) != FPK_OK ||
+      launch_dependent(prefix_own_kernel<kFp8>, static_cast<int>(own), 32 * kOwnWarps, kOwnSmem, s, a) != FPK_OK ||
       launch_dependent(prefix_attn_kernel<kFp8>, ctas, kPfThreads, PfCfg<kFp8>::kSmem, s, a, kmap, vmap) != FPK_OK)
     return FPK_ECUDA;
   return launch_dependent(prefix_merge_kernel, merge, 32 * kPfMergeWarps, 0, s, a);
