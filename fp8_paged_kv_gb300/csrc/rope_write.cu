@@ -18,6 +18,8 @@
 // slice of the heads).  Prompts go by 16-token tiles of the cache: what a CTA
 // does is cut out of one list of (tile, eight heads) steps, as many for each
 // CTA, and values are written as whole rows of a tile's dim-major block.
+#include <algorithm>
+
 #include "step_ops.cuh"
 
 namespace fpk {
@@ -60,9 +62,17 @@ struct Turn {
   float c[8], s[8];
 };
 
-// The eight cosines and sines of unit u at a position, to out[0], [stride], .. [3 stride]: a short loop (the
-// unrolled one is 8 KiB of code, fetched anew each time).
-__device__ __forceinline__ void unit_angles(const RopeArgs& a, int pos, int u, float4* out, int stride) {
+// Turns per position of pair i, f / (2 pi), as the sum of two floats.
+__device__ __forceinline__ float2 turn_rate(const RopeArgs& a, int i) {
+  const float f = __ldg(a.inv_freq + i);
+  const float th = __fmul_rn(f, kInvTwoPiHi);
+  return make_float2(th, __fmaf_rn(f, kInvTwoPiLo, __fmaf_rn(f, kInvTwoPiHi, -th)));
+}
+
+// The eight cosines and sines of a unit at a position, to out[0], [stride], .. [3 stride]: a short loop (the
+// unrolled one is 8 KiB of code, fetched anew each time).  rate(i): the turns of its pair i.
+template <class Rate>
+__device__ __forceinline__ void unit_angles(const RopeArgs& a, int pos, const Rate& rate, float4* out, int stride) {
   // positions of more than 24 bits enter as two parts
   const float plo = static_cast<float>(pos & 0xFFFF), phi = static_cast<float>(pos - (pos & 0xFFFF));
 #pragma unroll 1
@@ -70,10 +80,8 @@ __device__ __forceinline__ void unit_angles(const RopeArgs& a, int pos, int u, f
     float c[2], s[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const float f = __ldg(a.inv_freq + 8 * u + 2 * i + k);
-      const float th = __fmul_rn(f, kInvTwoPiHi);
-      const float tl = __fmaf_rn(f, kInvTwoPiLo, __fmaf_rn(f, kInvTwoPiHi, -th));
-      sincospif(2.f * (turn_fraction(plo, th, tl) + turn_fraction(phi, th, tl)), &s[k], &c[k]);
+      const float2 t = rate(2 * i + k);
+      sincospif(2.f * (turn_fraction(plo, t.x, t.y) + turn_fraction(phi, t.x, t.y)), &s[k], &c[k]);
     }
     out[i * stride] = make_float4(c[0] * a.rot_scale, c[1] * a.rot_scale, s[0] * a.rot_scale, s[1] * a.rot_scale);
   }
@@ -209,7 +217,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
   const int page = h + (heads - 1 - h) / a.hsplit * a.hsplit >= a.Hq ? page_for(w, static_cast<int>(row), pos) : -1;
   const int tpp = w.page_size >> 4, off = pos % w.page_size;
   __shared__ float4 s_turn[4][kRopeThreads];  // a thread's own
-  if (x.turns && !value) unit_angles(a, pos, u, &s_turn[0][threadIdx.x], kRopeThreads);
+  if (x.turns && !value)
+    unit_angles(a, pos, [&](int i) { return turn_rate(a, 8 * u + i); }, &s_turn[0][threadIdx.x], kRopeThreads);
   Turn t;
   load_turn(t, &s_turn[0][threadIdx.x], kRopeThreads);
   for (;;) {
@@ -358,6 +367,7 @@ __device__ __forceinline__ void rope_copy8(uint32_t dst, const void* src) {
 template <bool kFp8>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) uint8_t s_stage[];
+  __shared__ float2 s_rate[kRopeDim / 2];
   const WriteArgs& w = a.w;
   const int u = threadIdx.x % kRopeUnits, tok = threadIdx.x / kRopeUnits % 16, lane = threadIdx.x & 31;
   const int side = threadIdx.x / (16 * kRopeUnits), warp = threadIdx.x >> 5;
@@ -376,9 +386,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
   // a warp's part of a stage: [chunk][lane] of 16 bytes, or [token][lane] of 8
   const uint32_t stages = smem_addr(s_stage) + warp * kRopeWarpStage + lane * 16;
 
+  if (2 * static_cast<int>(threadIdx.x) < a.rot) s_rate[threadIdx.x] = turn_rate(a, threadIdx.x);
+  __syncthreads();
+
   // the next step, and its sources asked for
   auto ask = [&](uint32_t stage) {
     if (left > 0) {
+      bool entered = false;
       --left;
       if (at == steps) at = 0;
       if (at == 0 || left == count - 1) {
@@ -400,7 +414,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
         next.n = static_cast<int>(max(p1 - p0, static_cast<int64_t>(0)));
         next.t0 = static_cast<int>(p0 - 16 * tile);
         next.row0 = static_cast<int>(c0 + p0 - start);
-        next.page = next.n > 0 ? page_for(w, lo, p0) : -1;
+        entered = true;
       }
       next.step = at++;
       const bool key = next.step >= qsteps;
@@ -425,6 +439,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
           for (int q = next.t0; q < next.t0 + next.n; ++q, src += static_cast<int64_t>(w.Hkv) * kRopeDim)
             rope_copy8(dst + q * 256, src);
       }
+      // (the page is looked up behind the copies: nothing waits for it before the step is worked on)
+      if (entered) next.page = next.n > 0 ? page_for(w, next.request, 16 * static_cast<int64_t>(next.tile) + next.t0) : -1;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -455,7 +471,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
     if (c.step < qsteps + ksteps) {
       if (x.turns && turned == 0) {
         float4* const turn = reinterpret_cast<float4*>(s_stage + kRopeStages * kRopeStage) + threadIdx.x;
-        unit_angles(a, 16 * c.tile + tok, u, turn, kRopeThreads);
+        unit_angles(a, 16 * c.tile + tok, [&](int i) { return s_rate[8 * u + i]; }, turn, kRopeThreads);
         load_turn(t, turn, kRopeThreads);
       }
       turned = 1;
@@ -537,8 +553,13 @@ int rope_entry(bool fp8, bool prefill, const void* q, const void* k, const void*
     const int64_t steps = (Hq + kRopeStep - 1) / kRopeStep + 2 * static_cast<int64_t>((Hkv + kRopeStep - 1) / kRopeStep);
     constexpr int smem = kRopeStages * kRopeStage + kRopeThreads * 64;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FPK_ECUDA;
-    const int grid = resident_grid(reinterpret_cast<const void*>(kern), kRopeThreads, smem, tile_places(rows, B) * steps);
-    kern<<<grid, kRopeThreads, smem, st>>>(a);
+    // As many CTAs as are resident at once, or up to four times as many where each still has eight steps: the SMs
+    // run at different speeds (and requests end in empty places), which only CTAs that come later can even out.
+    // 16384 tokens: one wave 117 us, four 106; 2011 tokens: one wave (three steps a CTA) 19 us, four 23.
+    const int64_t all = tile_places(rows, B) * steps;
+    const int64_t wave = resident_grid(reinterpret_cast<const void*>(kern), kRopeThreads, smem, all);
+    const int64_t ctas = std::min(std::max(wave, all / 8), 4 * wave);
+    kern<<<static_cast<int>(ctas), kRopeThreads, smem, st>>>(a);
   } else {
     // a head per thread while that is no more than two full waves of threads; then as few slices as fill those
     const int64_t heads = Hq + 2 * static_cast<int64_t>(Hkv), full = 2 * 152 * 1024 / kRopeUnits;
