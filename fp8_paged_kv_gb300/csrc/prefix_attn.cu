@@ -4,9 +4,13 @@
 // A group's shared prefix is a matrix product: the rows are the queries of all
 // its requests that read one kv head (requests x GQA group), the columns the
 // prefix's tokens.  What a request has of its own is decode attention, bound by
-// HBM.  Four launches: a plan, the own parts, the prefixes, and a merge of each
-// row's partials by log-sum-exp.  (Without groups: paged_decode_split_kernel and
-// the merge, which then only rounds.)
+// HBM.  Four launches, each a dependent of the one before:
+//   plan    the work list of the prefixes (one CTA)
+//   own     beside the plan: the own tokens, and the queries as the prefixes'
+//           products read them
+//   attn    the prefixes, a CTA per SM
+//   merge   each row's partials, by log-sum-exp
+// (Without groups: paged_decode_split_kernel and the merge, which then only rounds.)
 //
 // * Unit: (group, kv head, up to 256 query rows) over the group's shared pages.
 // * Units are laid end to end in cost (blocks of 128 tokens, dearer for units of
@@ -29,12 +33,23 @@
 // Units of more than 128 rows use both tiles on every block; smaller ones give
 // the two tiles alternate blocks of the same rows, each with its own partial.
 //
-// Precision.  bf16 cache: q, K, P and V in bf16.  e4m3 cache: K enters as it
-// lies; q x 2^e (its largest value in [128, 256)) as two e4m3 parts c0 + c1: a
-// bf16's eight bits fill exactly two parts of four, but for values below 2^-9
-// of the largest, which lose at most 2^-17 of it; the MMAs' K runs over both
-// parts against the same K rows, at the rate of one f16 product.  Scores, sums and
-// O stay in fp32.  O is rescaled only when a row's maximum has grown by more than
+// What bounds it.  A block of 256 rows is 2050 cycles of products (the two parts
+// of an e4m3 query cost what one f16 product does) and takes about 2950: a tile's
+// S, softmax, P V and next S follow one another (S and P share the tile's 128
+// columns of tensor memory, the accumulators have the other half), and two tiles
+// in turn do not quite hide the chain.  128 requests x 32768 shared tokens,
+// 64/8 heads, e4m3: the prefixes' kernel 92 us with the tensor cores at 70 %, the
+// call 123 us (72 us are the products at the measured bf16 rate); in bf16, 131 us.
+// Few rows or short prefixes are bound by the four launches' chain of dependent
+// reads: 4 requests x 512 tokens 17 us, 32 x 8192 33 us (41 where nothing is in L2).
+//
+// Precision.  bf16 cache: q, K, P and V in bf16 (the product takes one type, and V's
+// range does not fit f16).  e4m3 cache: K enters as it lies; q x 2^e (its largest
+// value in [128, 256)) as two e4m3 parts c0 + c1: a bf16's eight bits fill exactly
+// two parts of four, but for values below 2^-9 of the largest, which lose at most
+// 2^-17 of it; the MMAs' K runs over both parts against the same K rows, at the rate
+// of one f16 product; weights are rounded to f16, and V is exact in it.  Scores, sums
+// and O stay in fp32.  O is rescaled only when a row's maximum has grown by more than
 // 2^8 since the last time: weights are then at most 2^8, far inside f16.
 #include <atomic>
 
@@ -56,8 +71,9 @@ constexpr float kPfGrow = 8.f;                 // log2 growth of a maximum that 
 // A row's scale is not taken below this (a scale of 0 leaves weights of 1 all the same): -inf times
 // it is -inf still.
 constexpr float kPfMinMult = 1e-37f;
-// Costs in the work list, in some 600 cycles: of a block with both tiles at work and with one, and
-// of a unit's start (queries, first products, partials).
+// Costs in the work list, in some 500 cycles: of a block with both tiles at work and with one, and
+// of a unit's start (queries, first products, partials).  (3 for a block with one, or starts of 8 and 3: 61
+// ragged requests in five groups 60 -> 63 us, whole batches on one prompt the same.)
 constexpr int kPfCostPair = 6, kPfCostSolo = 2;
 constexpr int kPfStartPair = 12, kPfStartSolo = 5;
 
@@ -1162,7 +1178,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 // tokens -- S takes them as they come, of q and K alike -- and tokens 4 c ..
 // 4 c + 3 of its V dims, which are the very tokens of the scores that the lane
 // holds for head g: P enters the second product from the registers where S
-// left it.
+// left it.  70 MB of own tokens of 128 requests: 27 us from a cold L2, 100 MB of
+// 61 ragged requests in bf16 24 us (registers as the only buffer: 33 and 29).
 constexpr int kOwnWarps = 4;
 constexpr int kOwnMinTiles = 16;  // of a split
 constexpr float kOwnFails = -1.f;  // sum of a split with a page outside the pool
@@ -1544,7 +1561,8 @@ __global__ void __launch_bounds__(32 * kOwnWarps, 3) prefix_own_kernel(const PfA
 // ---------------------------------------------------------------------------
 // merge
 // ---------------------------------------------------------------------------
-// One warp per (request, query head): the partials of its own splits and those
+// Bound by reading the partials (256 rows x 512 bytes per CTA and piece, some 22 MB in all): 9 us from L2, and
+// 5 us for next to nothing, four dependent reads.  One warp per (request, query head): the partials of its own splits and those
 // of the pieces of its unit, in that order.  A lane finds one partial (its row in
 // the partial arrays, m, l), then all lanes add its O.
 __global__ void __launch_bounds__(32 * kPfMergeWarps) prefix_merge_kernel(const PfArgs a) {

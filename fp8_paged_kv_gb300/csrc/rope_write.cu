@@ -18,6 +18,12 @@
 // slice of the heads).  Prompts go by 16-token tiles of the cache: what a CTA
 // does is cut out of one list of (tile, eight heads) steps, as many for each
 // CTA, and values are written as whole rows of a tile's dim-major block.
+// 16384 tokens, 64/8 heads, e4m3 cache: 105 us, 6.0 TB/s of 638 MB (89 % of what a
+// copy reaches); a thread per (token, unit) over all heads with element stores of V
+// took 171 us.  2011 tokens in 7 chunks, bf16: 19 us, a launch, three dependent
+// reads and three steps per CTA.  Appends: 4 us for one token, 5 us for 64.
+//
+// Rounding: fp32 throughout, a rotated value rounded once to what it is stored as.
 #include <algorithm>
 
 #include "step_ops.cuh"

@@ -207,7 +207,8 @@ int fpk_kv_prefill_bf16(const void* k, const void* v, const int32_t* cu_seqlens,
  *            it); requests with seq_lens[r] <= 0 are left alone, q_out too.
  *   prefill: rows cu_seqlens[r] .. cu_seqlens[r+1]-1 are request r's tokens at
  *            positions start_pos[r], start_pos[r] + 1, ... (start_pos NULL: 0;
- *            a token at a negative position fails the guard).
+ *            a token at a negative position fails the guard); rows from
+ *            cu_seqlens[B] on are left alone.
  * Guard: as fpk_kv_append_fp8, per token's page -- a refused token's key and
  * value are not written and abort_mask[r] is set; its query is rotated all the
  * same.
