@@ -199,6 +199,8 @@ class DecodePool:
             self.out16 = torch.zeros((wl.B, wl.Hq, wl.D), dtype=torch.bfloat16, device=self.device)
             ws = fpk_prefix_workspace_bytes(wl.B, wl.Hq, wl.Hkv, wl.D)
             self.prefix_workspace = torch.zeros(ws, dtype=torch.uint8, device=self.device)
+            if stream is not None:  # the zeroes are on their way on the current one
+                stream.wait_stream(torch.cuda.current_stream(self.device))
         mask = self.abort_mask if use_mask else None
         args = (self.page_table, self.seq_lens, mask, group_starts, prefix_lens, self.out16, self.lse,
                 self.prefix_workspace)

@@ -94,3 +94,25 @@ def test_sampling_run(fp8, ps):
     out = pool.out16.float().cpu().numpy()
     live = np.arange(8) != 2
     assert not out[2].any() and (np.abs(out - o)[live] <= (2e-3 + (1e-2 + 2.0 ** -8) * np.abs(o))[live]).all()
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_first_shared_attention_on_another_stream(fp8):
+    # its workspace is made, and zeroed, on the current stream, which is busy
+    wl = custom(3, B=4, Hq=16, Hkv=2, ps=16, prompt_lens=[300, 310, 40, 7], steps=0)
+    pool = DecodePool(wl, fp8=fp8, device=DEV)
+    pool.prefill()
+    pool.page_table[1, :10] = pool.page_table[0, :10]
+    pool.q.copy_(torch.from_numpy(np.random.default_rng(2).standard_normal((4, 16, 128)).astype(np.float32)))
+    starts, pre = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, 2], [160]))
+    busy = torch.zeros(1 << 27, device=DEV)
+    side = torch.cuda.Stream(device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy.add_(1.0)
+    pool.attend_shared(starts, pre, use_mask=False, stream=side)
+    torch.cuda.synchronize()
+    first = pool.out16.clone(), pool.lse.clone()
+    pool.attend_shared(starts, pre, use_mask=False)
+    torch.cuda.synchronize()
+    assert torch.equal(first[0], pool.out16) and torch.equal(first[1], pool.lse) and first[0].any()
