@@ -34,12 +34,12 @@
 // the two tiles alternate blocks of the same rows, each with its own partial.
 //
 // What bounds it.  A block of 256 rows is 2050 cycles of products (the two parts
-// of an e4m3 query cost what one f16 product does) and takes about 2950: a tile's
+// of an e4m3 query cost what one f16 product does) and takes about 2900: a tile's
 // S, softmax, P V and next S follow one another (S and P share the tile's 128
 // columns of tensor memory, the accumulators have the other half), and two tiles
 // in turn do not quite hide the chain.  128 requests x 32768 shared tokens,
-// 64/8 heads, e4m3: the prefixes' kernel 92 us with the tensor cores at 70 %, the
-// call 123 us (72 us are the products at the measured bf16 rate); in bf16, 131 us.
+// 64/8 heads, e4m3: the prefixes' kernel 90 us with the tensor cores at 71 %, the
+// call 121 us (72 us are the products at the measured bf16 rate); in bf16, 127 us.
 // Few rows or short prefixes are bound by the four launches' chain of dependent
 // reads: 4 requests x 512 tokens 17 us, 32 x 8192 33 us (41 where nothing is in L2).
 //
@@ -638,6 +638,12 @@ __device__ __noinline__ void pf_wait_long(uint32_t bar, uint32_t parity, uint32_
     }
   }
 }
+// A word that another warp writes.
+__device__ __forceinline__ int load_shared(uint32_t at) {
+  int x;
+  asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
 __device__ __forceinline__ void pf_wait(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* failed) {
   if (!mbar_try_wait(bar, parity)) pf_wait_long(bar, parity, status, failed);
 }
@@ -898,8 +904,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // cores; on a unit of both tiles the warps take turns (PV and the next S), or else the two would run
       // in step, their softmaxes too, and leave the tensor cores idle (4080 cycles a block of 256 rows, the
       // products' own time being 2050).  An issuing warp stands still until the tensor cores take its product,
-      // so all waits of a turn come before it, and turns are counted in shared memory, not by a barrier (some
-      // 60 cycles from warp to warp against 300 to 400; no result hangs on it, a turn not seen is gone without).
+      // so all waits of a turn come before it, what follows is straight code (it comes cold from the instruction
+      // caches each time), and turns are counted in shared memory, not by a barrier (no result hangs on it, a turn
+      // not seen is gone without): 3820 cycles a block without these three, about 2900 with them.
       //
       // On a unit of one row tile block j belongs to tile j mod 2.  A barrier's parity tells neighbouring
       // phases apart, no others, so a warp has to see every phase of a barrier it waits for: where the
@@ -915,6 +922,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const uint64_t vdesc = kFp8 ? smem_desc(base + C::kOffV16, 2048, 128, 0) : smem_desc(base + C::kOffV, 16, 256, 6);
       uint32_t j0 = 0, v3 = 0, v3ph = 0, n0 = 0, n1 = 0, begun = 0, uses0 = 0, uses1 = 0;
       int turns = 0;
+      const uint32_t turn_of = base + C::kOffMisc + 8 + 4 * (t ^ 1);
       static_assert(C::kKStages % 2 == 0 && (!kFp8 || C::kReady == 2), "slots that tiles own");
       while (take_piece(p)) {
         const int pair_in = __any_sync(kFull, p.pair());
@@ -951,22 +959,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             if (begins && begun > 0) wait(C::kBarOFree + t, begun - 1);  // O of the piece before has been read
             wait(C::kBarP + 2 * t, n0++);
           }
+          tc_fence_after();
+          const uint64_t vd = vdesc + vs * ((kFp8 ? C::kV16 : C::kVStage) >> 4);
+          const uint32_t od = tm + 256 + t * 128, pd = tm + t * 128, acc = !begins;
+          const bool both = 2 * m + 1 < halves;
           if (pair) {
 #pragma unroll 1
-            for (int spins = 0; s_turns[t ^ 1] - turns < t && spins < kPfTurnSpins; ++spins) {
+            for (int spins = 0; load_shared(turn_of) - turns < t && spins < kPfTurnSpins; ++spins) {
             }
           }
-          tc_fence_after();
           if (i >= step) {
-            const uint64_t vd = vdesc + vs * ((kFp8 ? C::kV16 : C::kVStage) >> 4);
-#pragma unroll 1
-            for (int h = 0; h < 2 && 2 * m + h < halves; ++h) {
-              if (h == 1) {
-                wait(C::kBarP + 2 * t + 1, n1++);
-                tc_fence_after();
-              }
-              issue_o(tm + 256 + t * 128, tm + t * 128 + 32 * h, vd + h * 1024, kFp8 ? kPfOF16 : kPfOBf16,
-                      !begins || h > 0);
+            issue_o(od, pd, vd, kFp8 ? kPfOF16 : kPfOBf16, acc);
+            if (both) {
+              wait(C::kBarP + 2 * t + 1, n1++);
+              tc_fence_after();
+              issue_o(od, pd + 32, vd + 1024, kFp8 ? kPfOF16 : kPfOBf16, 1);
             }
             begun += begins;
             begins = false;
