@@ -152,7 +152,7 @@ struct PfCfg {
   static constexpr int kBarO = kBarP + 4;                      // [tile] a product added to O
   static constexpr int kBarOFree = kBarO + 2;                  // [tile] O of a piece read
   static constexpr int kBarQ = kBarOFree + 2;                  // [buffer] queries staged
-  static constexpr int kBarQFree = kBarQ + 2;                  // [buffer] queries and multipliers of a piece read
+  static constexpr int kBarQFree = kBarQ + 2;                  // [buffer] queries of a piece read
   static constexpr int kBarPiece = kBarQFree + 2;              // [kPfPieces] piece known
   static constexpr int kBarPieceFree = kBarPiece + kPfPieces;  // [kPfPieces] piece read by every warp
   static constexpr int kBarDone = kBarPieceFree + kPfPieces;   // [2] every MMA of a warp completed
@@ -911,8 +911,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // On a unit of one row tile block j belongs to tile j mod 2.  A barrier's parity tells neighbouring
       // phases apart, no others, so a warp has to see every phase of a barrier it waits for: where the
       // number of slots is even, a tile has its own slots and sees all of theirs; bf16 V has three slots,
-      // and both warps see and free every block.  (A unit of both tiles begins when all blocks before
-      // it are over: its queries are staged by the softmax warps of both.)
+      // and both warps see and free every block.  (Turns do not keep the warps in step: the CPU model
+      // of these barriers passes without them.)
       const int t = warp - kPfMmaWarp;
       const uint32_t base = __reduce_max_sync(kFull, sbase), tm = __reduce_max_sync(kFull, tmem);  // uniform registers
       const uint32_t bars = base + C::kOffBars;
