@@ -1750,11 +1750,11 @@ int launch_dependent(void (*kernel)(Exp...), int grid, int threads, size_t smem,
   return checked_launch_status();
 }
 
-// Bytes behind the first 256 of a decode attention workspace that hold its arrival counters, for any
-// split count up to two CTAs per SM and more.
+// Bytes behind the first 256 of a decode attention workspace that hold its arrival counters, for any split count
+// up to 32 resident CTAs per SM (which is more than there can be; what lies behind is written later in the call).
 size_t decode_counter_bytes(int64_t B, int64_t Hq, int64_t Hkv) {
   int dev = 0;
-  const int W = cudaGetDevice(&dev) == cudaSuccess ? 4 * device_sm_count(dev) : 0;
+  const int W = cudaGetDevice(&dev) == cudaSuccess ? 32 * device_sm_count(dev) : 0;
   const WsLayout l = layout(B, Hkv, Hq / Hkv, W);
   return l.part_ml - l.seg_count;
 }
