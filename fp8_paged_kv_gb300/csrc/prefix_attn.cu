@@ -28,29 +28,33 @@
 //   warps 13, 14  issue S = Q K^T and O += P V (tcgen05.mma, M = N = 128) of row
 //               tile 0 and 1
 //   warps 0-3, 4-7  softmax of row tile 0 and 1, a thread per row: no shuffles,
-//               the row's maximum, sum and rescale are the thread's own.  P
-//               replaces S in tensor memory as the A operand of the second product.
+//               the row's maximum, sum and rescale are the thread's own.  P (both
+//               parts of half a block in the columns of its scores) replaces S in
+//               tensor memory as the A operand of the second product.
 // Units of more than 128 rows use both tiles on every block; smaller ones give
 // the two tiles alternate blocks of the same rows, each with its own partial.
 //
-// What bounds it.  A block of 256 rows is 2050 cycles of products (the two parts
-// of an e4m3 query cost what one f16 product does) and takes about 2900: a tile's
-// S, softmax, P V and next S follow one another (S and P share the tile's 128
-// columns of tensor memory, the accumulators have the other half), and two tiles
-// in turn do not quite hide the chain.  128 requests x 32768 shared tokens,
-// 64/8 heads, e4m3: the prefixes' kernel 90 us with the tensor cores at 71 %, the
-// call 121 us (72 us are the products at the measured bf16 rate); in bf16, 127 us.
-// Few rows or short prefixes are bound by the four launches' chain of dependent
-// reads: 4 requests x 512 tokens 17 us, 32 x 8192 33 us (41 where nothing is in L2).
+// What bounds it.  A block of 256 rows is 3070 cycles of products (the two parts
+// of an e4m3 query cost what one f16 product does, the two parts of the weights
+// what two do): a tile's S, softmax, P V and next S follow one another (S and P
+// share the tile's 128 columns of tensor memory, the accumulators have the other
+// half), and two tiles in turn do not quite hide the chain.  128 requests x 32768
+// shared tokens, 64/8 heads, e4m3: the call 152 us (108 us are the products at
+// the measured bf16 rate).  Few rows or short prefixes are bound by the four
+// launches' chain of dependent reads: 4 requests x 512 tokens 18 us, 32 x 8192
+// 41 us where nothing is in L2.
 //
 // Precision.  bf16 cache: q, K, P and V in bf16 (the product takes one type, and V's
-// range does not fit f16).  e4m3 cache: K enters as it lies; q x 2^e (its largest
-// value in [128, 256)) as two e4m3 parts c0 + c1: a bf16's eight bits fill exactly
-// two parts of four, but for values below 2^-9 of the largest, which lose at most
-// 2^-17 of it; the MMAs' K runs over both parts against the same K rows, at the rate
-// of one f16 product; weights are rounded to f16, and V is exact in it.  Scores, sums
-// and O stay in fp32.  O is rescaled only when a row's maximum has grown by more than
-// 2^8 since the last time: weights are then at most 2^8, far inside f16.
+// range does not fit f16).  Weights are two parts, hi + lo, as in the framework's other
+// decode attention: one bf16 part errs by up to 2^-8 of a weight, one f16 part by 2^-11,
+// which shows where values cancel.  (With one part 128 x 32768 took 121 us.)  e4m3 cache:
+// K enters as it lies; q x 2^e (its largest value in [128, 256)) as two e4m3 parts
+// c0 + c1: a bf16's eight bits fill exactly two parts of four, but for values below
+// 2^-9 of the largest, which lose at most 2^-17 of it; the MMAs' K runs over both parts
+// against the same K rows, at the rate of one f16 product; weights are two f16 parts,
+// and V is exact in one.  Scores, sums and O stay in fp32.  O is rescaled only when a
+// row's maximum has grown by more than 2^8 since the last time: weights are then at most
+// 2^8, far inside f16.
 #include <atomic>
 
 #include "attn_plan.cuh"
@@ -478,7 +482,7 @@ __device__ __forceinline__ void issue_s(uint32_t d, uint64_t qdesc, uint64_t kde
     asm volatile(PF_S("f16")::"r"(d), "l"(qdesc), "l"(kdesc), "r"(kPfSBf16), "n"(kPfBlk * 128 >> 4) : "memory");
 }
 
-// O += P V over half a block, P from tensor memory: a step is 16 tokens, 8 columns of P and 4 KiB of V.
+// O += P V over half a block, P from tensor memory: a step is 16 tokens, 8 columns of each part of P and 4 KiB of V.
 #define PF_O_STEP(pcol, voff, acc)                                                                  \
   "add.u32 p, %1, " #pcol ";\n\tadd.s64 b, %2, " #voff ";\n\t@e tcgen05.mma.cta_group::1.kind::f16" \
   " [%0], [p], b, %3, " acc ";\n\t"
@@ -486,9 +490,23 @@ __device__ __forceinline__ void issue_o(uint32_t d, uint32_t p, uint64_t vdesc, 
   asm volatile(
       "{\n\t.reg .pred e, first, yes;\n\t.reg .b32 p;\n\t.reg .b64 b;\n\telect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.u32 first, %4, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t" PF_O_STEP(0, 0, "first") PF_O_STEP(8, 256, "yes")
-          PF_O_STEP(16, 512, "yes") PF_O_STEP(24, 768, "yes") "}" ::"r"(d),
+          PF_O_STEP(16, 512, "yes") PF_O_STEP(24, 768, "yes") PF_O_STEP(32, 0, "yes") PF_O_STEP(40, 256, "yes")
+              PF_O_STEP(48, 512, "yes") PF_O_STEP(56, 768, "yes") "}" ::"r"(d),
       "r"(p), "l"(vdesc), "r"(idesc), "r"(acc)
       : "memory");
+}
+
+// A pair of softmax weights as two parts, each of two f16 (e4m3 cache) or two bf16: rounded, and what that left.
+template <bool kFp8>
+__device__ __forceinline__ void weight_parts(float2 e, uint32_t& hi, uint32_t& lo) {
+  if (kFp8) {
+    hi = pack_f16x2(e.x, e.y);
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    lo = pack_f16x2(e.x - h.x, e.y - h.y);
+  } else {
+    hi = pack_bf16x2(e.x, e.y);
+    lo = pack_bf16x2(e.x - __uint_as_float(hi << 16), e.y - __uint_as_float(hi & 0xFFFF0000u));
+  }
 }
 
 // 64 consecutive columns of this thread's tensor memory lane, waited for.
@@ -541,6 +559,12 @@ __device__ __forceinline__ float tmem_ld64_max(uint32_t taddr, float (&v)[64]) {
   return top;
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // 16 columns times f.
 __device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
   uint32_t r[16];
@@ -558,19 +582,6 @@ __device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f) {
       ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
-      "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32}; "
-      ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 
@@ -973,7 +984,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             if (both) {
               wait(C::kBarP + 2 * t + 1, n1++);
               tc_fence_after();
-              issue_o(od, pd + 32, vd + 1024, kFp8 ? kPfOF16 : kPfOBf16, 1);
+              issue_o(od, pd + 64, vd + 1024, kFp8 ? kPfOF16 : kPfOBf16, 1);
             }
             begun += begins;
             begins = false;
@@ -1103,16 +1114,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll 1
             for (int h = 0; h < halves; ++h) {
               if (h == 1) tmem_ld64(ts + 64, s);
-              uint32_t w[32];
+              // (stored eight columns at a time: with 16 or 32 the compiler holds more than the registers can)
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                float2 e = fma2(make_float2(s[2 * k], s[2 * k + 1]), mult2, ref2);
-                e.x = fast_exp2(e.x);
-                e.y = fast_exp2(e.y);
-                sum[k & 1] = add2(sum[k & 1], e);
-                w[k] = kFp8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+              for (int g = 0; g < 4; ++g) {
+                uint32_t w[8], v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  float2 e = fma2(make_float2(s[16 * g + 2 * k], s[16 * g + 2 * k + 1]), mult2, ref2);
+                  e.x = fast_exp2(e.x);
+                  e.y = fast_exp2(e.y);
+                  sum[k & 1] = add2(sum[k & 1], e);
+                  weight_parts<kFp8>(e, w[k], v[k]);
+                }
+                tmem_st8(ts + 64 * h + 8 * g, w);  // over columns that have been read
+                tmem_st8(ts + 64 * h + 32 + 8 * g, v);
               }
-              tmem_st32(ts + 32 * h, w);  // over columns that have been read
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
@@ -1510,12 +1526,14 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
       e[k] = fast_exp2(fmaf(e[k], mul, -ref));
       l += e[k];
     }
-    const uint32_t p0 = kFp8 ? pack_f16x2(e[0], e[1]) : pack_bf16x2(e[0], e[1]);
-    const uint32_t p1 = kFp8 ? pack_f16x2(e[2], e[3]) : pack_bf16x2(e[2], e[3]);
+    uint32_t p0, p1, r0, r1;
+    weight_parts<kFp8>(make_float2(e[0], e[1]), p0, r0);
+    weight_parts<kFp8>(make_float2(e[2], e[3]), p1, r1);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t af[4] = {v[2 * i][0], v[2 * i + 1][0], v[2 * i][1], v[2 * i + 1][1]};
       own_mma<kFp8>(o[i], af, p0, p1);
+      own_mma<kFp8>(o[i], af, r0, r1);
     }
   }
   // ---- the four warps' states

@@ -513,9 +513,9 @@ int fpk_paged_decode_attn_bf16(const void* q, const void* kv_pool,
  * the group's table.
  * Precision: scores and sums in fp32; the query enters the tensor cores exactly
  * in bf16, or for the e4m3 cache as two e4m3 parts (what they leave out is below
- * 2^-17 of the largest |q| of the head); softmax weights are rounded to f16
- * (e4m3 cache) or bf16 (bf16 cache), values enter exactly.  Repeated calls
- * on the same inputs give identical bits.
+ * 2^-17 of the largest |q| of the head); softmax weights enter as the sum of two
+ * f16 (e4m3 cache) or two bf16 parts (bf16 cache), values exactly.  Repeated
+ * calls on the same inputs give identical bits.
  * D == 128, page_size a multiple of 16 in [16, 256], 1 <= Hq / Hkv <= 8, else
  * FPK_EUNSUPPORTED; n_groups is at most B, and above 0 it needs both group arrays
  * (FPK_EINVAL).
