@@ -1560,7 +1560,7 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
 #pragma unroll
     for (int w = 0; w < kOwnWarps; ++w) {
       const float2 ml = s_ml[w * kPfGroupMax + hd];
-      if (ml.x == -INFINITY) continue;
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // (no score but NaN ones: the sum is NaN, and so is the part's)
       const float f = fast_exp2(ml.x - M);
       const float4 y = *reinterpret_cast<const float4*>(s_own + w * kOwnRing + (hd * kOwnRow + 4 * lane) * 4);
       W = fmaf(ml.y, f, W);
