@@ -73,8 +73,9 @@ constexpr float kPfLog2e = 1.4426950408889634f;
 constexpr float kPfLn2 = 0.6931471805599453f;
 constexpr float kPfGrow = 8.f;                 // log2 growth of a maximum that rescales O
 // A row's scale is not taken below this (a scale of 0 leaves weights of 1 all the same): -inf times
-// it is -inf still.
+// it is -inf still.  A NaN stays one.
 constexpr float kPfMinMult = 1e-37f;
+__device__ __forceinline__ float at_least_min(float mult) { return mult < kPfMinMult ? kPfMinMult : mult; }
 // Costs in the work list, in some 500 cycles: of a block with both tiles at work and with one, and
 // of a unit's start (queries, first products, partials).  (3 for a block with one, or starts of 8 and 3: 61
 // ragged requests in five groups 60 -> 63 us, whole batches on one prompt the same.)
@@ -1305,7 +1306,7 @@ __device__ __forceinline__ void put_query(const PfArgs& a, int r, int h, int lo,
     const int e = ex == 0 ? (top == 0 ? 0 : 126) : min(max(134 - ex, -126), 126);
     const float up = __int_as_float((127 + e) << 23);
     mult = ex == 255 ? __int_as_float(0x7fffffff) : mult * __int_as_float((127 - e) << 23);
-    if (ex != 255) mult = fmaxf(mult, kPfMinMult);
+    mult = at_least_min(mult);
     if (g < a.G) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -1336,7 +1337,7 @@ __device__ __forceinline__ void put_query(const PfArgs& a, int r, int h, int lo,
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<uint4*>(half + ((((c & 1) * 4 + i) ^ swizzle) << 4)) =
           make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    mult = fmaxf(mult, kPfMinMult);
+    mult = at_least_min(mult);
   }
   if (g < a.G && c == 0) a.q_mult[at] = mult;
 }
@@ -1427,6 +1428,7 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
       qa[i][1] = q[2 * i + 1] ^ flip;
     }
   }
+  mult = at_least_min(mult);
   float m = -INFINITY, l = 0.f, o[8][4];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -1502,8 +1504,7 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
     float mx = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-    const float scale = fmaxf(mult, kPfMinMult);
-    const float mb = mx == -INFINITY ? -INFINITY : mx * (mult != mult ? mult : scale);
+    const float mb = mx == -INFINITY ? -INFINITY : mx * mult;
     const bool grown = mb > m || (m == -INFINITY && mb != -INFINITY);
     if (__any_sync(kFull, grown)) {
       const float f = !grown ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - mb);
@@ -1520,10 +1521,9 @@ __device__ __forceinline__ void own_part(const PfArgs& a) {
       }
     }
     const float ref = m == -INFINITY ? 0.f : m;
-    const float mul = mult != mult ? mult : scale;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      e[k] = fast_exp2(fmaf(e[k], mul, -ref));
+      e[k] = fast_exp2(fmaf(e[k], mult, -ref));
       l += e[k];
     }
     uint32_t p0, p1, r0, r1;

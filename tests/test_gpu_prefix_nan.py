@@ -1,5 +1,5 @@
-"""Values that are no numbers in shared-prefix attention: a NaN query, key or value
-makes the rows that meet it NaN, as the formula does, and no others, and scores
+"""Values that are no numbers in shared-prefix attention: a NaN scale, query, key or
+value makes the rows that meet it NaN, as the formula does, and no others, and scores
 of -inf have no weight.  Tolerances are those of test_gpu_prefix.py."""
 import numpy as np
 import pytest
@@ -35,6 +35,14 @@ def close(c, out, lse, ref):
     live = ~np.isnan(lse) & np.isfinite(rl)
     assert np.array_equal(np.isneginf(lse), np.isneginf(rl) & ~np.isnan(lse))
     assert (np.abs(lse - rl)[live] <= (ds + n * 2.0 ** -24 + 2.0 ** -20 * np.abs(rl))[live]).all()
+
+
+@BOTH
+def test_nan_scales(fp8):
+    c = make(GROUPS, fp8=fp8, lead=1, G=4)
+    nan = np.ones((c["B"], 8), bool)
+    for name in ("sm", "ks") if fp8 else ("sm",):
+        run({**c, name: float("nan")}, nan, name)
 
 
 @BOTH
