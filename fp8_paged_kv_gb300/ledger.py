@@ -52,7 +52,8 @@ class PageLedger:
             self.owner[page_table[m]] = rows
             for r, p in zip(rows, page_table[m]):
                 self.held[r].add(int(p))
-            np.add.at(self.refs, page_table[m], 1)
+            for pages in self.held:
+                self.refs[list(pages)] += 1
             self.lens[:] = seq_lens
         self.free = deque(int(p) for p in np.flatnonzero(self.owner < 0))
 
@@ -84,9 +85,12 @@ class PageLedger:
     def release(self, r: int) -> list[int]:
         """Request r finished (or was aborted): its pages return to the free list, but
         for those that another request still holds.  Returns the pages freed."""
-        row = self.page_table[r]
-        mine = [int(p) for p in row[row >= 0] if int(p) in self.held[r]]
-        self.held[r].clear()
+        # each page held counts once, whatever the row says of it (a stale entry may name one
+        # twice, or have taken the place of another): in the row's order, then those it lacks
+        held = self.held[r]
+        named = dict.fromkeys(int(p) for p in self.page_table[r] if int(p) in held)
+        mine = [*named, *sorted(held - named.keys())]
+        held.clear()
         pages = []
         for p in mine:
             self.refs[p] -= 1
