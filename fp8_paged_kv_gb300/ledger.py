@@ -121,15 +121,22 @@ class PageLedger:
     def fork(self, parent: int, child: int) -> int:
         """Empty slot `child` takes over request `parent`: its full pages are shared,
         and where its last page is not full the child gets a page of its own, to
-        which fpk_kv_fork copies it.  Returns that page (-1: none was needed)."""
+        which fpk_kv_fork copies it.  Returns that page (-1: none was needed).
+        Raises, and changes nothing, where fpk_kv_fork would refuse: a fork refused
+        on the device alone leaves the fresh page's tag behind the ledger's for good."""
         assert self.pages_of_table(child) == 0, "slot still holds pages"
+        if parent == child:
+            raise RuntimeError(f"request {parent}: forked to itself")
         L = int(self.lens[parent])
         full = L // self.page_size
-        row = self.page_table[parent, :full]
-        if not all(int(p) in self.held[parent] for p in row):
+        row = self.page_table[parent, :self.pages_of(parent)]
+        if row.size < self.pages_of(parent) or not all(int(p) in self.held[parent] for p in row):
             raise RuntimeError(f"request {parent}: a page it maps is not its own")
+        if not np.array_equal(self.expected[parent, :row.size], self.tags[row]):
+            raise RuntimeError(f"request {parent}: it expects a tag that its page no longer has")
         if L % self.page_size and not self.free:
             raise RuntimeError("pool exhausted")
+        row = row[:full]
         self.page_table[child, :full] = row
         self.expected[child, :full] = self.expected[parent, :full]
         self.held[child].update(int(p) for p in row)

@@ -92,3 +92,35 @@ def test_churn_with_stale_entries(seed):
     for r in range(led.B):
         led.release(r)
     assert len(led.free) == led.num_pages
+
+
+@pytest.mark.parametrize("L", [32, 40])
+@pytest.mark.parametrize("what", ["tag", "page", "range", "gone", "long"])
+def test_fork_refuses_what_the_device_refuses(L, what):
+    # the last entry is the page in use (40 tokens), which the child would copy
+    led = make()
+    led.admit(0, L)
+    led.admit(1, 64)
+    last = led.pages_of(0) - 1
+    if what == "tag":
+        led.expected[0, last] -= np.uint32(1)
+    elif what == "page":
+        led.page_table[0, last] = led.page_table[1, 0]
+        led.expected[0, last] = led.tags[led.page_table[1, 0]]
+    elif what == "long":
+        led.lens[0] = 8 * 16 + 1
+    else:
+        led.page_table[0, last] = led.num_pages if what == "range" else -1
+    state = [x.copy() for x in (led.tags, led.refs, led.owner, led.page_table, led.expected, led.lens)]
+    free, held = list(led.free), [set(h) for h in led.held]
+    with pytest.raises(RuntimeError, match="request 0"):
+        led.fork(0, 3)
+    after = led.tags, led.refs, led.owner, led.page_table, led.expected, led.lens
+    assert all(np.array_equal(x, y) for x, y in zip(state, after))
+    assert free == list(led.free) and held == led.held
+
+
+def test_fork_of_itself():
+    led = make()
+    with pytest.raises(RuntimeError, match="request 2"):
+        led.fork(2, 2)
