@@ -14,8 +14,9 @@ matches.  The ledger is that bookkeeping for one layer's pool:
 
 Requests may share pages: ``fork`` makes one request hold another's full pages
 (``fpk_kv_fork`` applies it on the device) and ``release`` frees a page when its
-last holder leaves.  ``compact`` plans the moves that bring all pages in use to
-the front of the pool (``fpk_kv_compact`` applies them).
+last holder leaves.  ``compact`` plans the moves that bring the pages in use to
+the front of the pool (``fpk_kv_compact`` applies them); pages given ahead of a
+context stay where they are.
 
 Every allocation is a reallocation and bumps the page's tag; the pages
 returned by ``allocate`` are the bump list for that step.  The ledger does no
@@ -146,16 +147,23 @@ class PageLedger:
 
     def compact(self) -> tuple[np.ndarray, np.ndarray]:
         """Moves (src ascending, dst) after which the pages in use are the pool's
-        first ones.  Tables, tags and holders follow, as fpk_kv_compact leaves
-        them on the device; stale entries stay."""
-        used = np.flatnonzero(self.refs > 0)
-        src = used[used >= used.size].astype(np.int32)
-        dst = np.flatnonzero(self.refs[:used.size] == 0).astype(np.int32)
-        to = np.arange(self.num_pages, dtype=np.int32)
-        to[src] = dst
+        first ones, but for pages given ahead of a request's context: these stay
+        where they are (fpk_kv_compact rewrites the entries of contexts alone).
+        Tables, tags and holders follow, as fpk_kv_compact leaves them on the
+        device; stale entries stay."""
         at = self.page_table
         held = np.arange(self.max_pages) < -(-self.lens[:, None] // self.page_size)
         known = held & (at >= 0) & (at < self.num_pages)
+        stays = np.zeros(self.num_pages, bool)
+        for r, j in np.argwhere(~held & (at >= 0)):
+            if int(at[r, j]) in self.held[r]:
+                stays[at[r, j]] = True
+        used = np.flatnonzero((self.refs > 0) & ~stays)
+        front = np.flatnonzero(~stays)[:used.size]
+        src = np.setdiff1d(used, front).astype(np.int32)
+        dst = np.setdiff1d(front, used).astype(np.int32)
+        to = np.arange(self.num_pages, dtype=np.int32)
+        to[src] = dst
         safe = np.where(known, at, 0)
         moved = known & (to[safe] != safe) & (self.expected == self.tags[safe])
         self.tags[dst] += np.uint32(1)

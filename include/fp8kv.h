@@ -282,7 +282,9 @@ int fpk_kv_fork(void* kv_pool, int32_t elem_bytes, int32_t layers, int64_t layer
  * ceil(seq_lens / page_size) that names src[i] and expects its live tag is
  * made to name dst[i] and to expect the new tag, in all rows that share the
  * page.  Stale entries (another expected tag) stay as they are, and so stay
- * stale; src's bytes and tag are untouched.
+ * stale; src's bytes and tag are untouched.  Entries behind a request's context
+ * stay too: a page that a row maps ahead of it must not be in src, or the row is
+ * to be counted by what it maps (seq_lens is read here for nothing else).
  * src is ascending; no page is listed twice, or in both lists.  Moves with a
  * page outside [0, num_pages) are ignored.  (An unsorted src leaves entries
  * unmoved, other breaches leave unspecified bytes; nothing out of range is

@@ -124,3 +124,62 @@ def test_fork_of_itself():
     led = make()
     with pytest.raises(RuntimeError, match="request 2"):
         led.fork(2, 2)
+
+
+def compacted(led):
+    """compact() with its promises checked: rows follow, what is ahead stays, the rest is in front."""
+    table, tags = led.page_table.copy(), led.tags.copy()
+    ahead = {int(p) for r in range(led.B) for p in table[r, led.pages_of(r):] if p >= 0}
+    src, dst = led.compact()
+    assert np.all(np.diff(src) > 0) and not set(src.tolist()) & set(dst.tolist())
+    to = dict(zip(src.tolist(), dst.tolist()))
+    assert not ahead & (set(to) | set(to.values()))
+    assert np.array_equal(led.page_table, np.vectorize(lambda p: to.get(p, p))(table))
+    assert np.array_equal(led.tags[dst], tags[dst] + np.uint32(1))
+    used = [p for p in np.flatnonzero(led.refs).tolist() if p not in ahead]
+    assert used == [p for p in range(led.num_pages) if p not in ahead][:len(used)]
+    consistent(led)
+    return src, dst
+
+
+def test_compact_leaves_pages_ahead_of_the_context():
+    led = make(num_pages=20)
+    led.admit(0, 64)
+    led.admit(1, 16)
+    ahead = led.allocate(1, 2)
+    led.release(0)
+    src, _ = compacted(led)
+    assert src.size == 1 and led.page_table[1, 1:3].tolist() == ahead
+    for _ in range(32):
+        assert led.grow(1) == []
+    consistent(led)
+    led.admit(2, 120)
+    assert not set(led.page_table[2].tolist()) & set(ahead)
+    consistent(led)
+    src, _ = compacted(led)      # the context has reached them: now they move
+    assert led.refs[:11].all()
+    led.release(1)
+    led.release(2)
+    assert len(led.free) == 20
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_compact_with_pages_ahead_in_a_churn(seed):
+    led = make(num_pages=70)
+    rng = np.random.default_rng(seed)
+    for step in range(120):
+        r = int(rng.integers(0, led.B))
+        if not led.held[r]:
+            live = [i for i in range(led.B) if led.lens[i]]
+            if live and rng.random() < 0.5:
+                led.fork(int(rng.choice(live)), r)
+            else:
+                led.admit(r, int(rng.integers(0, 100)))
+            led.allocate(r, int(rng.integers(0, 2)))
+        elif rng.random() < 0.3:
+            led.release(r)
+        elif led.lens[r] < 120:
+            led.grow(r)
+        if step % 5 == 4:
+            compacted(led)
+        consistent(led)
