@@ -41,9 +41,9 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str | None = 
         def pair_of(turns):  # the (fractional) pair that makes so many turns within original_len
             return rot_dim * math.log(original_len / (2 * math.pi * turns)) / (2 * math.log(base))
 
-        lo = max(math.floor(pair_of(beta_fast)), 0)
-        hi = min(math.ceil(pair_of(beta_slow)), rot_dim // 2 - 1)
-        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        # (either may lie before the first pair or behind the last: the ramp's slope is theirs all the same)
+        lo, hi = math.floor(pair_of(beta_fast)), math.ceil(pair_of(beta_slow))
+        ramp = ((i - lo) / max(hi - lo, 1)).clamp(0.0, 1.0)
         f = f * (1.0 - ramp) + f / factor * ramp
         scale = 0.1 * math.log(factor) + 1.0
     return f.to(torch.float32).to(device), scale
