@@ -3,9 +3,9 @@
 //
 // Pair i of a head at position p turns by the angle p f_i:
 //   (x, y) -> s (x cos a - y sin a, y cos a + x sin a),  a = p f_i.
-// The angle is reduced in turns: f / (2 pi) is held as a two-float sum and the
-// fraction of p f / (2 pi) is taken with the product's rounding error (one FMA)
-// added back, so that far positions keep the accuracy of near ones.
+// The angle is reduced in turns: f / (2 pi) is held as a fraction of 2^64, and the
+// low 64 bits of its product with p are the fraction of a turn, whatever p: far
+// positions keep the accuracy of near ones (2^-32 turns at 2^31).
 //
 // A unit is 16 values of a head, 8 pairs, and belongs to one thread: in the half
 // layout its two 16-byte chunks lie rot_dim/2 apart, interleaved or unrotated
@@ -49,46 +49,40 @@ struct RopeArgs {
   int Hq, rot, interleaved, hsplit;
 };
 
-// 1 / (2 pi) as the sum of two floats: the value rounded to 24 bits and the
-// rounded remainder (from pi to 40 digits).
-constexpr double kInvTwoPi = 0.15915494309189533576888376337251436203;
-constexpr float kInvTwoPiHi = static_cast<float>(kInvTwoPi);
-constexpr float kInvTwoPiLo = static_cast<float>(kInvTwoPi - static_cast<double>(kInvTwoPiHi));
-
-// Fraction of a turn (within about one half) of p * (th + tl), p an integer of
-// at most 24 significant bits: the product with th is split into its rounded
-// value, whose fraction is exact, and its rounding error.
-__device__ __forceinline__ float turn_fraction(float p, float th, float tl) {
-  const float a = __fmul_rn(p, th);
-  const float e = __fmaf_rn(p, th, -a);
-  return __fadd_rn(a - rintf(a), __fmaf_rn(p, tl, e));
-}
+// 2 / pi, its first 64 bits (2^64 (2 / pi), rounded down, from pi to 40 digits).
+constexpr uint32_t kTwoOverPiHi = 0xA2F9836Eu, kTwoOverPiLo = 0x4E441529u;
 
 struct Turn {
   float c[8], s[8];
 };
 
-// Turns per position of pair i, f / (2 pi), as the sum of two floats.
-__device__ __forceinline__ float2 turn_rate(const RopeArgs& a, int i) {
-  const float f = __ldg(a.inv_freq + i);
-  const float th = __fmul_rn(f, kInvTwoPiHi);
-  return make_float2(th, __fmaf_rn(f, kInvTwoPiLo, __fmaf_rn(f, kInvTwoPiHi, -th)));
+// Turns per position of pair i, f / (2 pi) modulo 1, in steps of 2^-64: the 24 bits of f times the 64 of
+// 2 / pi, the upper 64 of these shifted to their place.  Within 2 steps for |f| < 2, twice as many for each
+// doubling behind.
+__device__ __forceinline__ uint64_t turn_rate(const RopeArgs& a, int i) {
+  const uint32_t f = __float_as_uint(__ldg(a.inv_freq + i));
+  const uint32_t m = (f & 0x7FFFFFu) << 8 | 0x80000000u;
+  const uint64_t x = static_cast<uint64_t>(m) * kTwoOverPiHi + __umulhi(m, kTwoOverPiLo);
+  const int down = 128 - static_cast<int>(f >> 23 & 255u);
+  const uint64_t r = down >= 64 || down <= -64 ? 0 : down >= 0 ? x >> down : x << -down;
+  return f >> 31 ? 0 - r : r;
+}
+
+// Half turns (within 1) of a pair at a position: what lies behind the product's upper 32 bits is below 2^-32 turns.
+__device__ __forceinline__ float half_turns(int pos, uint64_t rate) {
+  const uint64_t turns = static_cast<uint64_t>(static_cast<int64_t>(pos)) * rate;
+  return static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f;
 }
 
 // The eight cosines and sines of a unit at a position, to out[0], [stride], .. [3 stride]: a short loop (the
 // unrolled one is 8 KiB of code, fetched anew each time).  rate(i): the turns of its pair i.
 template <class Rate>
 __device__ __forceinline__ void unit_angles(const RopeArgs& a, int pos, const Rate& rate, float4* out, int stride) {
-  // positions of more than 24 bits enter as two parts
-  const float plo = static_cast<float>(pos & 0xFFFF), phi = static_cast<float>(pos - (pos & 0xFFFF));
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     float c[2], s[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float2 t = rate(2 * i + k);
-      sincospif(2.f * (turn_fraction(plo, t.x, t.y) + turn_fraction(phi, t.x, t.y)), &s[k], &c[k]);
-    }
+    for (int k = 0; k < 2; ++k) sincospif(half_turns(pos, rate(2 * i + k)), &s[k], &c[k]);
     out[i * stride] = make_float4(c[0] * a.rot_scale, c[1] * a.rot_scale, s[0] * a.rot_scale, s[1] * a.rot_scale);
   }
 }
@@ -373,7 +367,7 @@ __device__ __forceinline__ void rope_copy8(uint32_t dst, const void* src) {
 template <bool kFp8>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) uint8_t s_stage[];
-  __shared__ float2 s_rate[kRopeDim / 2];
+  __shared__ uint64_t s_rate[kRopeDim / 2];
   const WriteArgs& w = a.w;
   const int u = threadIdx.x % kRopeUnits, tok = threadIdx.x / kRopeUnits % 16, lane = threadIdx.x & 31;
   const int side = threadIdx.x / (16 * kRopeUnits), warp = threadIdx.x >> 5;
