@@ -84,7 +84,10 @@ class DecodePool:
         ws = fpk_decode_workspace_bytes(wl.B, wl.Hq, wl.Hkv, wl.D, self.num_splits)
         self.workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=dev)
         self.count_aborts = True
-        self.out16 = self.prefix_workspace = None  # made by the first attend_shared()
+        # attend_shared()'s, made here: a first call may be one that a graph captures
+        self.out16 = torch.zeros((wl.B, wl.Hq, wl.D), dtype=torch.bfloat16, device=dev)
+        ws = fpk_prefix_workspace_bytes(wl.B, wl.Hq, wl.Hkv, wl.D)
+        self.prefix_workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=dev)
 
     def _new_io(self):
         wl, dev = self.wl, self.device
@@ -195,12 +198,6 @@ class DecodePool:
         device: requests [group_starts[g], group_starts[g + 1]) share their first
         prefix_lens[g] tokens' pages."""
         wl = self.wl
-        if self.out16 is None:
-            self.out16 = torch.zeros((wl.B, wl.Hq, wl.D), dtype=torch.bfloat16, device=self.device)
-            ws = fpk_prefix_workspace_bytes(wl.B, wl.Hq, wl.Hkv, wl.D)
-            self.prefix_workspace = torch.zeros(ws, dtype=torch.uint8, device=self.device)
-            if stream is not None:  # the zeroes are on their way on the current one
-                stream.wait_stream(torch.cuda.current_stream(self.device))
         mask = self.abort_mask if use_mask else None
         args = (self.page_table, self.seq_lens, mask, group_starts, prefix_lens, self.out16, self.lse,
                 self.prefix_workspace)
