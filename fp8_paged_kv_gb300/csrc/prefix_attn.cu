@@ -38,11 +38,12 @@
 // of an e4m3 query cost what one f16 product does, the two parts of the weights
 // what two do): a tile's S, softmax, P V and next S follow one another (S and P
 // share the tile's 128 columns of tensor memory, the accumulators have the other
-// half), and two tiles in turn do not quite hide the chain.  128 requests x 32768
-// shared tokens, 64/8 heads, e4m3: the call 152 us (108 us are the products at
-// the measured bf16 rate).  Few rows or short prefixes are bound by the four
-// launches' chain of dependent reads: 4 requests x 512 tokens 18 us, 32 x 8192
-// 41 us where nothing is in L2.
+// half), and two tiles in turn do not quite hide the chain: about 3700 cycles.  128
+// requests x 32768 shared tokens, 64/8 heads, e4m3: the prefixes' kernel 114 us
+// with the tensor cores at 81 %, the call 148 us (108 us are the products at the
+// measured bf16 rate); in bf16, 164 us.  Few rows or short prefixes are bound by
+// the four launches' chain of dependent reads: 4 requests x 512 tokens 18 us,
+// 32 x 8192 34 us (41 where nothing is in L2).
 //
 // Precision.  bf16 cache: q, K, P and V in bf16 (the product takes one type, and V's
 // range does not fit f16).  Weights are two parts, hi + lo, as in the framework's other
@@ -914,11 +915,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // same block in halves as the softmax hands P over, S of the next (which overwrites S and P: the
       // products of one thread run in order).  While a tile's softmax runs the other tile has the tensor
       // cores; on a unit of both tiles the warps take turns (PV and the next S), or else the two would run
-      // in step, their softmaxes too, and leave the tensor cores idle (4080 cycles a block of 256 rows, the
-      // products' own time being 2050).  An issuing warp stands still until the tensor cores take its product,
+      // in step, their softmaxes too, and leave the tensor cores idle (with weights in one part 4080 cycles a
+      // block of 256 rows, the products' own time being 2050).  An issuing warp stands still until the tensor cores take its product,
       // so all waits of a turn come before it, what follows is straight code (it comes cold from the instruction
       // caches each time), and turns are counted in shared memory, not by a barrier (no result hangs on it, a turn
-      // not seen is gone without): 3820 cycles a block without these three, about 2900 with them.
+      // not seen is gone without): 3820 cycles a block without these three, about 2900 with them (in two parts 3700).
       //
       // On a unit of one row tile block j belongs to tile j mod 2.  A barrier's parity tells neighbouring
       // phases apart, no others, so a warp has to see every phase of a barrier it waits for: where the
@@ -1708,7 +1709,10 @@ int prepare_prefix(int dev) {
   return FPK_OK;
 }
 
-// Most splits of a request's own tokens per kv head: about a wave of CTAs, three per SM, in all (two waves: 2 us more for 4 to 32 requests).
+// Most splits of a request's own tokens per kv head, from the batch's size alone: four CTAs per SM in all, of which
+// three are resident (twice as many: 2 us more for 4 to 32 requests).  Large batches have one split whatever a
+// request's length: 63 requests with 8192 shared tokens and one of 131072 tokens of its own, 8 kv heads, take
+// 1200 us (paged_decode_split_kernel, without sharing, 170).
 int own_splits_most(int64_t B, int64_t Hkv, int64_t ctas) {
   const int64_t n = 4 * ctas / (B * Hkv > 0 ? B * Hkv : 1);
   return static_cast<int>(n < 1 ? 1 : n > 32 ? 32 : n);

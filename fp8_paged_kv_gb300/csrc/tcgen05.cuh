@@ -1,6 +1,6 @@
 // tcgen05.cuh -- fifth-generation tensor core and tensor-map PTX shared by the
-// kernels that use them (sm_103a): descriptors, MMA commits and fences, tensor
-// memory loads, and the tensor-map encoder.
+// kernels that use them (sm_103a): shared-memory descriptors, MMA commits and
+// fences, e4m3 conversions, and the tensor-map encoder.
 #pragma once
 
 #include <mutex>

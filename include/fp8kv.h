@@ -518,6 +518,10 @@ int fpk_paged_decode_attn_bf16(const void* q, const void* kv_pool,
  * 2^-17 of the largest |q| of the head); softmax weights enter as the sum of two
  * f16 (e4m3 cache) or two bf16 parts (bf16 cache), values exactly.  Repeated
  * calls on the same inputs give identical bits.
+ * Meant for batches that share most of what they read.  A request's own tokens
+ * are split by the batch's size alone, so that a long context of its own in a
+ * large batch is read slowly, and a short prefix does not pay for the four
+ * launches: fpk_paged_decode_attn_* serves those batches better.
  * D == 128, page_size a multiple of 16 in [16, 256], 1 <= Hq / Hkv <= 8, else
  * FPK_EUNSUPPORTED; n_groups is at most B, and above 0 it needs both group arrays
  * (FPK_EINVAL).
