@@ -85,6 +85,26 @@ SIGNATURES = {
     "fpk_rope_prefill_bf16": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _I32,
                                              _P, _P, _P, _I32, _I32, _F, _I32, _I32, _I32, _I32, _I32,
                                              _I32, _P]),
+    "fpk_rope_append_fp8_block": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _P, _P,
+                                                 _I32, _I32, _F, _I32, _I32, _I32, _I32, _I32, _I32, _P]),
+    "fpk_rope_prefill_fp8_block": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _I32,
+                                                  _P, _P, _P, _I32, _I32, _F, _I32, _I32, _I32, _I32, _I32,
+                                                  _I32, _P]),
+    "fpk_kv_append_fp8_block": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _P, _P,
+                                               _I32, _I32, _I32, _I32, _I32, _P]),
+    "fpk_kv_prefill_fp8_block": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _P, _P, _I32, _P, _P, _P,
+                                                _I32, _I32, _I32, _I32, _I32, _P]),
+    "fpk_paged_decode_attn_fp8_block": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P,
+                                                       _SZ, _I32, _F, _I32, _I32, _I32, _I32, _I32,
+                                                       _I32, _P]),
+    "fpk_prefill_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
+    "fpk_paged_prefill_attn_fp8_block": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _I32, _P, _P, _I32,
+                                                        _P, _P, _P, _SZ, _F, _I32, _I32, _I32, _I32,
+                                                        _I32, _I32, _P]),
+    "fpk_kv_fork_block": (ctypes.c_int, [_P, _I32, _I64, _P, _I64, _P, _I32, _P, _P, _P, _P, _P, _P, _P,
+                                         _I32, _I32, _I32, _I32, _I32, _I32, _P]),
+    "fpk_kv_compact_block": (ctypes.c_int, [_P, _I32, _I64, _P, _I64, _P, _I32, _P, _P, _P, _P, _P, _I32,
+                                            _I32, _I32, _I32, _I32, _I32, _P]),
     "fpk_kv_fork": (ctypes.c_int, [_P, _I32, _I32, _I64, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _I32,
                                    _I32, _I32, _I32, _I32, _I32, _P]),
     "fpk_kv_compact": (ctypes.c_int, [_P, _I32, _I32, _I64, _P, _I32, _P, _P, _P, _P, _P, _I32,
@@ -475,6 +495,111 @@ def fpk_paged_decode_attn_bf16_prefix(q, kv_pool, page_table, seq_lens, abort_ma
             group_starts, prefix_lens, out, lse, workspace, Hkv, page_size, num_pages, sm_scale, stream)
 
 
+# ------------------------------------------------- caches with block scales
+def _block_scales(kv_scales, num_pages, Hkv, page_size):
+    return (kv_scales, _U8S, "kv_scales", 2 * num_pages * Hkv * (page_size // 16), False)
+
+
+def block_scales(num_pages, Hkv, page_size, layers=1, device="cuda"):
+    """Block scales of fresh pools: uint8 [layers][num_pages][Hkv][page_size/16][2]."""
+    return torch.zeros((layers, num_pages, Hkv, page_size // 16, 2), dtype=torch.uint8, device=device)
+
+
+def fpk_rope_append_fp8_block(q, k_new, v_new, inv_freq, q_out, kv_pool, kv_scales, page_table,
+                              seq_lens, live_tags=None, expected_tags=None, abort_mask=None, *, Hkv,
+                              page_size, num_pages, rot_dim, interleaved=False, rot_scale=1.0, stream=None):
+    """fpk_rope_append_fp8 into blocks whose scales follow their largest value (rot_dim 0: no rotation)."""
+    _rope("fpk_rope_append_fp8_block", True, q, k_new, v_new, (seq_lens,), inv_freq, q_out, kv_pool,
+          (kv_scales,), page_table, live_tags, expected_tags, abort_mask, Hkv, page_size,
+          num_pages, rot_dim, interleaved, rot_scale, stream)
+
+
+def fpk_rope_prefill_fp8_block(q, k, v, cu_seqlens, start_pos, inv_freq, q_out, kv_pool, kv_scales,
+                               page_table, live_tags=None, expected_tags=None, abort_mask=None, *, Hkv,
+                               page_size, num_pages, rot_dim, interleaved=False, rot_scale=1.0, stream=None):
+    """fpk_rope_prefill_fp8 into blocks whose scales follow their largest value (rot_dim 0: no rotation)."""
+    _rope("fpk_rope_prefill_fp8_block", True, q, k, v, (cu_seqlens, start_pos), inv_freq, q_out, kv_pool,
+          (kv_scales,), page_table, live_tags, expected_tags, abort_mask, Hkv, page_size,
+          num_pages, rot_dim, interleaved, rot_scale, stream)
+
+
+def fpk_kv_append_fp8_block(k_new, v_new, kv_pool, kv_scales, page_table, seq_lens, live_tags=None,
+                            expected_tags=None, abort_mask=None, *, Hkv, D, page_size, num_pages, stream=None):
+    """One token per request, without rotation (k_new, v_new: [B][Hkv][D])."""
+    B, max_pages = page_table.shape
+    (k_p, v_p, pool_p, scales_p, table_p, lens_p, live_p, expected_p, abort_p) = _pointers(
+        (k_new, _BF16_LIKE, "k_new", (B, Hkv, D), False), (v_new, _BF16_LIKE, "v_new", (B, Hkv, D), False),
+        (kv_pool, _U8S, "kv_pool", 2 * num_pages * Hkv * page_size * D, False),
+        _block_scales(kv_scales, num_pages, Hkv, page_size), (page_table, _I32S, "page_table", None, False),
+        (seq_lens, _I32S, "seq_lens", (B,), False), (live_tags, _TAGS, "live_tags", (num_pages,), True),
+        (expected_tags, _TAGS, "expected_tags", (B, max_pages), True), (abort_mask, _U8S, "abort_mask", (B,), True))
+    _check((_lib or load_library()).fpk_kv_append_fp8_block(
+        k_p, v_p, pool_p, scales_p, table_p, max_pages, lens_p, live_p, expected_p, abort_p, B, Hkv, D, page_size,
+        num_pages, _launch_stream(stream, kv_pool.get_device())), "fpk_kv_append_fp8_block")
+
+
+def fpk_kv_prefill_fp8_block(k, v, cu_seqlens, start_pos, kv_pool, kv_scales, page_table, live_tags=None,
+                             expected_tags=None, abort_mask=None, *, Hkv, D, page_size, num_pages, stream=None):
+    """Prompts or their chunks (from start_pos, None: 0), without rotation."""
+    T = k.shape[0]
+    B, max_pages = page_table.shape
+    (k_p, v_p, cu_p, start_p, pool_p, scales_p, table_p, live_p, expected_p, abort_p) = _pointers(
+        (k, _BF16_LIKE, "k", (T, Hkv, D), False), (v, _BF16_LIKE, "v", (T, Hkv, D), False),
+        (cu_seqlens, _I32S, "cu_seqlens", (B + 1,), False), (start_pos, _I32S, "start_pos", (B,), True),
+        (kv_pool, _U8S, "kv_pool", 2 * num_pages * Hkv * page_size * D, False),
+        _block_scales(kv_scales, num_pages, Hkv, page_size), (page_table, _I32S, "page_table", None, False),
+        (live_tags, _TAGS, "live_tags", (num_pages,), True),
+        (expected_tags, _TAGS, "expected_tags", (B, max_pages), True), (abort_mask, _U8S, "abort_mask", (B,), True))
+    _check((_lib or load_library()).fpk_kv_prefill_fp8_block(
+        k_p, v_p, cu_p, T, start_p, pool_p, scales_p, table_p, max_pages, live_p, expected_p, abort_p, B, Hkv, D,
+        page_size, num_pages, _launch_stream(stream, kv_pool.get_device())), "fpk_kv_prefill_fp8_block")
+
+
+def fpk_paged_decode_attn_fp8_block(q, kv_pool, kv_scales, page_table, seq_lens, abort_mask, out, lse,
+                                    workspace, *, Hkv, page_size, num_pages, sm_scale, num_splits=0, stream=None):
+    """fpk_paged_decode_attn_fp8 over a cache with block scales."""
+    B, Hq, D = q.shape
+    max_pages = page_table.shape[-1]
+    (q_p, pool_p, scales_p, table_p, lens_p, abort_p, out_p, lse_p, ws_p) = _pointers(
+        (q, _BF16_LIKE, "q", None, False),
+        (kv_pool, _U8S, "kv_pool", 2 * num_pages * Hkv * page_size * D, False),
+        _block_scales(kv_scales, num_pages, Hkv, page_size),
+        (page_table, _I32S, "page_table", (B, max_pages), False), (seq_lens, _I32S, "seq_lens", (B,), False),
+        (abort_mask, _U8S, "abort_mask", (B,), True), (out, _F32S, "out", (B, Hq, D), False),
+        (lse, _F32S, "lse", (B, Hq), True), (workspace, _U8S, "workspace", None, False))
+    _check((_lib or load_library()).fpk_paged_decode_attn_fp8_block(
+        q_p, pool_p, scales_p, table_p, max_pages, lens_p, abort_p, out_p, lse_p, ws_p, workspace.numel(),
+        num_splits, sm_scale, B, Hq, Hkv, D, page_size, num_pages, _launch_stream(stream, kv_pool.get_device())),
+        "fpk_paged_decode_attn_fp8_block")
+
+
+def fpk_prefill_workspace_bytes(B, n_tokens, Hq, Hkv, D=128) -> int:
+    n = load_library().fpk_prefill_workspace_bytes(B, n_tokens, Hq, Hkv, D)
+    if n == 0 and B > 0 and n_tokens > 0:
+        raise FpkError("fpk_prefill_workspace_bytes: invalid shape or no CUDA device")
+    return int(n)
+
+
+def fpk_paged_prefill_attn_fp8_block(q, cu_seqlens, kv_pool, kv_scales, page_table, seq_lens, abort_mask,
+                                     out, lse, workspace, *, causal=True, Hkv, page_size, num_pages,
+                                     sm_scale, stream=None):
+    """Attention of several query tokens per request (out: bf16): causal at the end of each
+    context, or over all of it (cross attention to an encoder's states)."""
+    T, Hq, D = q.shape
+    B, max_pages = page_table.shape
+    (q_p, cu_p, pool_p, scales_p, table_p, lens_p, abort_p, out_p, lse_p, ws_p) = _pointers(
+        (q, _BF16S, "q", None, False), (cu_seqlens, _I32S, "cu_seqlens", (B + 1,), False),
+        (kv_pool, _U8S, "kv_pool", 2 * num_pages * Hkv * page_size * D, False),
+        _block_scales(kv_scales, num_pages, Hkv, page_size), (page_table, _I32S, "page_table", None, False),
+        (seq_lens, _I32S, "seq_lens", (B,), False), (abort_mask, _U8S, "abort_mask", (B,), True),
+        (out, _BF16S, "out", (T, Hq, D), False), (lse, _F32S, "lse", (T, Hq), True),
+        (workspace, _U8S, "workspace", None, False))
+    _check((_lib or load_library()).fpk_paged_prefill_attn_fp8_block(
+        q_p, cu_p, T, pool_p, scales_p, table_p, max_pages, lens_p, abort_p, int(bool(causal)), out_p, lse_p, ws_p,
+        workspace.numel(), sm_scale, B, Hq, Hkv, D, page_size, num_pages,
+        _launch_stream(stream, kv_pool.get_device())), "fpk_paged_prefill_attn_fp8_block")
+
+
 # --------------------------------------------------------- rotary positions
 def _rope(name, fp8, q, k, v, pos, inv_freq, q_out, kv_pool, scales, page_table, live_tags,
           expected_tags, abort_mask, Hkv, page_size, num_pages, rot_dim, interleaved, rot_scale,
@@ -490,11 +615,14 @@ def _rope(name, fp8, q, k, v, pos, inv_freq, q_out, kv_pool, scales, page_table,
         where = ((pos[0], _I32S, "seq_lens", (B,), False),)
     else:
         where = ((pos[0], _I32S, "cu_seqlens", (B + 1,), False), (pos[1], _I32S, "start_pos", (B,), True))
-    scales = _scales(*scales) if fp8 else ()
+    if name.endswith("_block"):
+        scales = (_block_scales(*scales, num_pages, Hkv, page_size),)
+    else:
+        scales = _scales(*scales) if fp8 else ()
     (k_p, v_p, q_p, out_p, freq_p, pool_p, table_p, live_p, expected_p, abort_p, pos_p, *rest) = _pointers(
         (k, _BF16S, "k", (T, Hkv, D), False), (v, _BF16S, "v", (T, Hkv, D), False),
         (q, _BF16S, "q", (T, Hq, D), True), (q_out, _BF16S, "q_out", (T, Hq, D) if Hq else None, True),
-        (inv_freq, _F32S, "inv_freq", (rot_dim // 2,), False),
+        (inv_freq, _F32S, "inv_freq", (rot_dim // 2,) if rot_dim else None, rot_dim == 0),
         (kv_pool, _U8S if fp8 else _BF16_LIKE, "kv_pool", 2 * num_pages * Hkv * page_size * D, False),
         (page_table, _I32S, "page_table", None, False), (live_tags, _TAGS, "live_tags", (num_pages,), True),
         (expected_tags, _TAGS, "expected_tags", (B, max_pages), True),
@@ -580,6 +708,41 @@ def fpk_kv_compact(kv_pool, page_table, expected_tags, seq_lens, live_tags, src,
     _check((_lib or load_library()).fpk_kv_compact(
         pool_p, el, layers, stride, table_p, max_pages, expected_p, lens_p, live_p, src_p, dst_p, n, B, Hkv, D,
         page_size, num_pages, _launch_stream(stream, kv_pool.get_device())), "fpk_kv_compact")
+
+
+def _move_scales(kv_scales, layers, num_pages, Hkv, page_size):
+    one = 2 * num_pages * Hkv * (page_size // 16)
+    return one, (kv_scales, _U8S, "kv_scales", layers * one, False)
+
+
+def fpk_kv_fork_block(kv_pool, kv_scales, page_table, expected_tags, seq_lens, live_tags, abort_mask, parent,
+                      child, fresh, *, layers=1, Hkv, D, page_size, num_pages, stream=None):
+    """fpk_kv_fork of an e4m3 pool with block scales ([layers][one pool's], contiguous)."""
+    n, (one, scales) = parent.numel(), _move_scales(kv_scales, layers, num_pages, Hkv, page_size)
+    (B, max_pages, _, stride), (pool_p, table_p, expected_p, lens_p, live_p, scales_p, abort_p, parent_p, child_p, fresh_p) = _moves(
+        kv_pool, page_table, expected_tags, seq_lens, live_tags, layers, Hkv, D, page_size, num_pages, scales,
+        (abort_mask, _U8S, "abort_mask", (page_table.shape[0],), True), (parent, _I32S, "parent", None, False),
+        (child, _I32S, "child", (n,), False), (fresh, _I32S, "fresh", (n,), False))
+    if kv_pool.dtype != torch.uint8:
+        raise FpkError(f"kv_pool has dtype {kv_pool.dtype}: block scales belong to an e4m3 pool")
+    _check((_lib or load_library()).fpk_kv_fork_block(
+        pool_p, layers, stride, scales_p, one, table_p, max_pages, expected_p, lens_p, live_p, abort_p, parent_p,
+        child_p, fresh_p, n, B, Hkv, D, page_size, num_pages, _launch_stream(stream, kv_pool.get_device())),
+        "fpk_kv_fork_block")
+
+
+def fpk_kv_compact_block(kv_pool, kv_scales, page_table, expected_tags, seq_lens, live_tags, src, dst, *,
+                         layers=1, Hkv, D, page_size, num_pages, stream=None):
+    """fpk_kv_compact of an e4m3 pool with block scales ([layers][one pool's], contiguous)."""
+    n, (one, scales) = src.numel(), _move_scales(kv_scales, layers, num_pages, Hkv, page_size)
+    (B, max_pages, _, stride), (pool_p, table_p, expected_p, lens_p, live_p, scales_p, src_p, dst_p) = _moves(
+        kv_pool, page_table, expected_tags, seq_lens, live_tags, layers, Hkv, D, page_size, num_pages, scales,
+        (src, _I32S, "src", None, False), (dst, _I32S, "dst", (n,), False))
+    if kv_pool.dtype != torch.uint8:
+        raise FpkError(f"kv_pool has dtype {kv_pool.dtype}: block scales belong to an e4m3 pool")
+    _check((_lib or load_library()).fpk_kv_compact_block(
+        pool_p, layers, stride, scales_p, one, table_p, max_pages, expected_p, lens_p, live_p, src_p, dst_p, n, B,
+        Hkv, D, page_size, num_pages, _launch_stream(stream, kv_pool.get_device())), "fpk_kv_compact_block")
 
 
 def fpk_decode_status(workspace, stream=None) -> int:

@@ -43,11 +43,20 @@
 //   arrivals complete a segment's count merges its partials by log-sum-exp,
 //   in two levels above 16 partials (one launch per call; nothing ever waits
 //   on another CTA).
+// * Block scales (kBlock).  The producer fetches a tile's two exponent bytes one
+//   batch ahead, behind the table, and leaves them with the stage.  K's scale
+//   multiplies the tile's scores.  V's goes into the weights: with ev its
+//   exponent, p' = 2^(s + ev - m) with m the largest s + ev seen, so that the
+//   weights that meet the codes stay within 1 whatever the scales' order, and
+//   the sum takes p' 2^-ev, which is 2^(s - m).  m and l of partials have that
+//   meaning throughout; l stays within 2^50 per token (the scales' least
+//   exponent), and what p' loses below 2^-126 is 2^-46 of l at most.
 // * Safety.  Every wait is bounded (status word in the workspace); no barrier
 //   without a timeout is used after the prologue.
 #include <atomic>
 
 #include "attn_plan.cuh"
+#include "block_scale.cuh"
 #include "common.cuh"
 #include "step_ops.cuh"
 
@@ -99,6 +108,7 @@ struct Cfg {
   static constexpr int kMlBytes = (kConsumerWarps * kGroupMax * 4 * 2 + kConsumerWarps * 4 + 15) / 16 * 16;
   static constexpr int kBarBytes = (2 * kStages + kMergeBars) * 8;
   static constexpr int kSmemBytes = kRingBytes + kMergeBytes + kMlBytes + kBarBytes + kStages * 4 + 64;
+  static constexpr int kScaleBytes = kStages * 4;  // block scales: the exponent bytes of each stage
 };
 
 struct AttnArgs {
@@ -106,6 +116,7 @@ struct AttnArgs {
   const uint8_t* kv_pool;
   const float* k_scale;
   const float* v_scale;
+  const uint16_t* kv_scales;  // block scales: K's and V's byte of each tile, [num_pages][Hkv][tiles]
   const int32_t* page_table;
   const int32_t* seq_lens;
   const uint8_t* abort_mask;
@@ -196,7 +207,7 @@ __device__ __noinline__ int64_t tightest_split_size(const AttnArgs& a, int64_t T
   return c;
 }
 
-template <bool kFp8, bool kDeep>
+template <bool kFp8, bool kDeep, bool kBlock>
 __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const AttnArgs a) {
   using C = Cfg<kFp8, kDeep>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -207,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
   int* s_wfault = reinterpret_cast<int*>(s_l + kConsumerWarps * kGroupMax);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRingBytes + C::kMergeBytes + C::kMlBytes);
   int* s_stage_fault = reinterpret_cast<int*>(bars + 2 * C::kStages + kMergeBars);
+  uint16_t* s_stage_scale = reinterpret_cast<uint16_t*>(s_stage_fault + C::kStages);  // [stage][tile]
 
   __shared__ int64_t s_warp_sum[kThreads / 32], s_warp_splits[kThreads / 32];
   __shared__ int s_warp_nz[kThreads / 32], s_warp_min[kThreads / 32], s_warp_max[kThreads / 32];
@@ -382,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
   }
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full0 + 8 * s, 1);
+      mbar_init(full0 + 8 * s, kBlock ? 3 : 1);  // (and the two tiles' scales)
       mbar_init(empty0 + 8 * s, 1);
     }
     mbar_init(merge_free, kConsumerWarps);
@@ -462,15 +474,25 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
         }
         return pg;
       };
+      // scales of this lane's tile of the batch from k0 on page pg
+      auto load_scale = [&](int k0, int pg) -> uint32_t {
+        const int t = p.t0 + 2 * (k0 + si) + ci;
+        if (!kBlock || pg < 0 || pg >= a.num_pages) return 0u;
+        return __ldg(a.kv_scales + (static_cast<int64_t>(pg) * a.Hkv + p.h) * tpp + t % tpp);
+      };
       int pg = load_id(0);  // table reads only: harmless for an aborted request
       if (p.r != ab_r) {
         ab_r = p.r;
         ab = is_aborted(a, p.r);
       }
       if (ab) continue;  // the consumers skip it too
+      int pg1 = kBlock ? load_id(batch) : -1;  // kBlock: tables two batches ahead, scales one
+      uint32_t scale = load_scale(0, pg);
       for (int k0 = 0; k0 < nst && ok; k0 += batch) {
         const int cnt = min(batch, nst - k0);
-        const int nxt = load_id(k0 + batch);  // prefetch (unused past the piece)
+        const int nxt = kBlock ? pg1 : load_id(k0 + batch);  // prefetch (unused past the piece)
+        const uint32_t scale1 = load_scale(k0 + batch, nxt);
+        if (kBlock) pg1 = load_id(k0 + 2 * batch);
         const bool member = si < cnt;
         const int tA = p.t0 + 2 * (k0 + si);
         const bool hasB = tA + 1 < p.t1;
@@ -511,6 +533,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
             } else if (ci == 0 ? okA : okB) {
               bulk_g2s(dst, src, 2 * C::kBlockBytes, fb, pol);
             }
+            if (kBlock) {
+              s_stage_scale[2 * stage + ci] = static_cast<uint16_t>(scale);
+              mbar_arrive(fb);
+            }
           }
           // the give-up decision is taken by lane 0 for the whole warp
           const bool late = (++spins & 255u) == 0u && global_timer_ns() - t0 > kWaitLimitNs;
@@ -527,6 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
         }
         j += cnt;
         pg = nxt;
+        scale = scale1;
       }
     }
     if (!ok && lane == 0) {
@@ -547,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
   const int g = lane >> 2;   // MMA group id: A row / B column
   const int t4 = lane & 3;   // thread in group
   const int rowA = token_of_row(g);  // token of fragment row g (row g+8 is rowA + 2)
-  const float kscale = kFp8 ? __ldg(a.k_scale) : 1.f;
-  const float vscale = kFp8 ? __ldg(a.v_scale) : 1.f;
+  const float kscale = kFp8 && !kBlock ? __ldg(a.k_scale) : 1.f;
+  const float vscale = kFp8 && !kBlock ? __ldg(a.v_scale) : 1.f;
   const float vmul = kFp8 ? vscale : 1.f;
   Cursor cur = start;
   Piece p;
@@ -997,6 +1024,20 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
                         vr[tt][mt + 1][1]);
           }
         }
+      }
+      // exponents of the two tiles' scales: K's as a factor, V's as a shift of the score
+      float km[2] = {1.f, 1.f}, ve[2] = {0.f, 0.f}, vd[2] = {1.f, 1.f};
+      if (kBlock) {
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+          const uint32_t b = s_stage_scale[2 * stage + tt];
+          const int ev = scale_exponent(b >> 8);
+          km[tt] = exp2_int(scale_exponent(b & 255u));
+          ve[tt] = static_cast<float>(ev);
+          vd[tt] = exp2_int(-ev);
+        }
+      }
+      if (kFp8) {
         __syncwarp();
         if (lane == 0) mbar_arrive(empty0 + 8 * stage);
       }
@@ -1028,10 +1069,18 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
             else mma_bf16(acc0, af, qf[kk][0], qf[kk][1]);
           }
         }
-        sc[tt][0] = (acc0[0] + acc1[0]) * mult0;
-        sc[tt][1] = (acc0[1] + acc1[1]) * mult1;
-        sc[tt][2] = (acc0[2] + acc1[2]) * mult0;
-        sc[tt][3] = (acc0[3] + acc1[3]) * mult1;
+        if (kBlock) {
+          const float f0 = mult0 * km[tt], f1 = mult1 * km[tt];
+          sc[tt][0] = fmaf(acc0[0] + acc1[0], f0, ve[tt]);
+          sc[tt][1] = fmaf(acc0[1] + acc1[1], f1, ve[tt]);
+          sc[tt][2] = fmaf(acc0[2] + acc1[2], f0, ve[tt]);
+          sc[tt][3] = fmaf(acc0[3] + acc1[3], f1, ve[tt]);
+        } else {
+          sc[tt][0] = (acc0[0] + acc1[0]) * mult0;
+          sc[tt][1] = (acc0[1] + acc1[1]) * mult1;
+          sc[tt][2] = (acc0[2] + acc1[2]) * mult0;
+          sc[tt][3] = (acc0[3] + acc1[3]) * mult1;
+        }
         if (nv[tt] < kTile) {
           // select, never multiply: a stale slot may hold NaN codes
           if (rowA >= nv[tt]) sc[tt][0] = sc[tt][1] = kNegInf;
@@ -1072,8 +1121,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
       for (int tt = 0; tt < 2; ++tt) {
         const float p0 = fast_exp2(sc[tt][0] - base0), p1 = fast_exp2(sc[tt][1] - base1);
         const float p2 = fast_exp2(sc[tt][2] - base0), p3 = fast_exp2(sc[tt][3] - base1);
-        l0 += p0 + p2;
-        l1 += p1 + p3;
+        if (kBlock) {
+          l0 = fmaf(p0 + p2, vd[tt], l0);
+          l1 = fmaf(p1 + p3, vd[tt], l1);
+        } else {
+          l0 += p0 + p2;
+          l1 += p1 + p3;
+        }
         const uint32_t pr0 = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
         const uint32_t pr1 = kFp8 ? pack_f16x2(p2, p3) : pack_bf16x2(p2, p3);
         pb[tt][0] = movmatrix_trans(pr0);
@@ -1279,15 +1333,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
 // host side
 // ---------------------------------------------------------------------------
 constexpr int kMaxDevices = 64;
-std::atomic<int> g_auto_ctas[3][kMaxDevices];  // resident CTAs per SM: BF16, FP8, deep FP8
+std::atomic<int> g_auto_ctas[5][kMaxDevices];  // resident CTAs per SM: BF16, FP8, deep FP8, with block scales the two
 
-template <bool kFp8, bool kDeep = false>
+template <bool kFp8, bool kDeep = false, bool kBlock = false>
 int prepare_kernel(int dev) {
-  std::atomic<int>& slot = g_auto_ctas[kDeep ? 2 : kFp8 ? 1 : 0][dev];
+  std::atomic<int>& slot = g_auto_ctas[(kDeep ? 2 : kFp8 ? 1 : 0) + (kBlock ? 2 : 0)][dev];
   int v = slot.load(std::memory_order_relaxed);
   if (v > 0) return v;
-  auto kern = paged_decode_split_kernel<kFp8, kDeep>;
-  constexpr int smem = Cfg<kFp8, kDeep>::kSmemBytes;
+  auto kern = paged_decode_split_kernel<kFp8, kDeep, kBlock>;
+  constexpr int smem = Cfg<kFp8, kDeep>::kSmemBytes + (kBlock ? Cfg<kFp8, kDeep>::kScaleBytes : 0);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
   int per_sm = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem) !=
@@ -1330,6 +1384,7 @@ enum class AttnLaunch { kPlain, kCheckOnly, kAfterStepWrite };
 // the host cannot see the context lengths and assumes every request holds
 // tokens -- if they turn out uneven, the deep variant runs with its shallow
 // ring).  It must also fit as many CTAs per SM as the shallow one.
+template <bool kBlock>
 bool deep_ring(int dev, int W, int ctas, int B, int Hkv, bool auto_split) {
   using D = Cfg<true, true>;
   int64_t active = W < ctas ? W : ctas;
@@ -1338,16 +1393,16 @@ bool deep_ring(int dev, int W, int ctas, int B, int Hkv, bool auto_split) {
     if (u > 0) active = u;
   }
   if (active * D::kStages * D::kStageBytes > kInflightBudget) return false;
-  const int deep = prepare_kernel<true, true>(dev);
-  return deep > 0 && deep >= prepare_kernel<true, false>(dev);
+  const int deep = prepare_kernel<true, true, kBlock>(dev);
+  return deep > 0 && deep >= prepare_kernel<true, false, kBlock>(dev);
 }
 
-template <bool kFp8, bool kDeep>
+template <bool kFp8, bool kDeep, bool kBlock>
 int launch_split_kernel(const AttnArgs& a, int dev, int ctas, cudaStream_t s, bool after_step_write) {
-  constexpr int smem = Cfg<kFp8, kDeep>::kSmemBytes;
-  if (prepare_kernel<kFp8, kDeep>(dev) <= 0) return FPK_ECUDA;  // sets the kernel's shared-memory size
+  constexpr int smem = Cfg<kFp8, kDeep>::kSmemBytes + (kBlock ? Cfg<kFp8, kDeep>::kScaleBytes : 0);
+  if (prepare_kernel<kFp8, kDeep, kBlock>(dev) <= 0) return FPK_ECUDA;  // sets the kernel's shared-memory size
   if (!after_step_write) {
-    paged_decode_split_kernel<kFp8, kDeep><<<ctas, kThreads, smem, s>>>(a);
+    paged_decode_split_kernel<kFp8, kDeep, kBlock><<<ctas, kThreads, smem, s>>>(a);
     return checked_launch_status();
   }
   // launched as a programmatic dependent of the step's write + check kernel:
@@ -1363,14 +1418,14 @@ int launch_split_kernel(const AttnArgs& a, int dev, int ctas, cudaStream_t s, bo
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_decode_split_kernel<kFp8, kDeep>, a) != cudaSuccess) return FPK_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, paged_decode_split_kernel<kFp8, kDeep, kBlock>, a) != cudaSuccess) return FPK_ECUDA;
   return checked_launch_status();
 }
 
 // Shapes, required pointers and alignment of an attention call; no CUDA call
 // is made, so a rejected call has queued nothing.  need_workspace: the caller
 // supplies the workspace (the allocation-free entry point does not).
-template <bool kFp8>
+template <bool kFp8, bool kBlock = false>
 int check_attn_args(const void* q, const void* kv_pool, const float* k_scale, const float* v_scale,
                     const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
                     const float* out, const void* workspace, bool need_workspace, int32_t num_splits,
@@ -1381,26 +1436,28 @@ int check_attn_args(const void* q, const void* kv_pool, const float* k_scale, co
   if (B == 0) return FPK_OK;
   if (!q || !kv_pool || !page_table || !seq_lens || !out || (need_workspace && !workspace))
     return FPK_EINVAL;
-  if (kFp8 && (!k_scale || !v_scale)) return FPK_EINVAL;
+  if (kFp8 && !kBlock && (!k_scale || !v_scale)) return FPK_EINVAL;
   if (!aligned16(q) || !aligned16(kv_pool) || !aligned16(out) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return FPK_EINVAL;
   return FPK_OK;
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kBlock = false>
 int attn_entry(const void* q, const void* kv_pool, const float* k_scale,
                const float* v_scale, const int32_t* page_table, int32_t max_pages,
                const int32_t* seq_lens, const uint8_t* abort_mask, float* out, float* lse,
                void* workspace, size_t workspace_bytes, int32_t num_splits, float sm_scale,
                int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
-               int32_t num_pages, void* stream, AttnLaunch mode = AttnLaunch::kPlain) {
-  int st = check_attn_args<kFp8>(q, kv_pool, k_scale, v_scale, page_table, max_pages, seq_lens, out,
+               int32_t num_pages, void* stream, AttnLaunch mode = AttnLaunch::kPlain,
+               const uint8_t* kv_scales = nullptr) {
+  int st = check_attn_args<kFp8, kBlock>(q, kv_pool, k_scale, v_scale, page_table, max_pages, seq_lens, out,
                                  workspace, true, num_splits, B, Hq, Hkv, D, page_size, num_pages);
   if (st != FPK_OK || B == 0) return st;
+  if (kBlock && (!kv_scales || (reinterpret_cast<uintptr_t>(kv_scales) & 1u) != 0)) return FPK_EINVAL;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FPK_ECUDA;
-  const int per_sm = prepare_kernel<kFp8>(dev);
+  const int per_sm = prepare_kernel<kFp8, false, kBlock>(dev);
   const int wave = device_sm_count(dev) * per_sm;  // CTAs resident at once
   if (per_sm <= 0 || wave <= 0) return FPK_ECUDA;
   const int W = num_splits == 0 ? auto_splits(wave, B, Hkv) : num_splits;
@@ -1419,6 +1476,7 @@ int attn_entry(const void* q, const void* kv_pool, const float* k_scale,
   a.kv_pool = static_cast<const uint8_t*>(kv_pool);
   a.k_scale = k_scale;
   a.v_scale = v_scale;
+  a.kv_scales = reinterpret_cast<const uint16_t*>(kv_scales);
   a.page_table = page_table;
   a.seq_lens = seq_lens;
   a.abort_mask = abort_mask;
@@ -1441,9 +1499,9 @@ int attn_entry(const void* q, const void* kv_pool, const float* k_scale,
   a.sm_scale_log2 = sm_scale * kLog2e;
   if (mode == AttnLaunch::kCheckOnly) return FPK_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (kFp8 && deep_ring(dev, W, ctas, B, Hkv, num_splits == 0))
-    return launch_split_kernel<true, true>(a, dev, ctas, s, mode == AttnLaunch::kAfterStepWrite);
-  return launch_split_kernel<kFp8, false>(a, dev, ctas, s, mode == AttnLaunch::kAfterStepWrite);
+  if (kFp8 && deep_ring<kBlock>(dev, W, ctas, B, Hkv, num_splits == 0))
+    return launch_split_kernel<true, true, kBlock>(a, dev, ctas, s, mode == AttnLaunch::kAfterStepWrite);
+  return launch_split_kernel<kFp8, false, kBlock>(a, dev, ctas, s, mode == AttnLaunch::kAfterStepWrite);
 }
 
 }  // namespace
@@ -1487,6 +1545,18 @@ extern "C" int fpk_paged_decode_attn_bf16(const void* q, const void* kv_pool,
   return fpk::attn_entry<false>(q, kv_pool, nullptr, nullptr, page_table, max_pages, seq_lens,
                                 abort_mask, out, lse, workspace, workspace_bytes, num_splits,
                                 sm_scale, B, Hq, Hkv, D, page_size, num_pages, stream);
+}
+
+extern "C" int fpk_paged_decode_attn_fp8_block(const void* q, const uint8_t* kv_pool, const uint8_t* kv_scales,
+                                               const int32_t* page_table, int32_t max_pages,
+                                               const int32_t* seq_lens, const uint8_t* abort_mask,
+                                               float* out, float* lse, void* workspace,
+                                               size_t workspace_bytes, int32_t num_splits, float sm_scale,
+                                               int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                               int32_t page_size, int32_t num_pages, void* stream) {
+  return fpk::attn_entry<true, true>(q, kv_pool, nullptr, nullptr, page_table, max_pages, seq_lens, abort_mask, out,
+                                     lse, workspace, workspace_bytes, num_splits, sm_scale, B, Hq, Hkv, D, page_size,
+                                     num_pages, stream, fpk::AttnLaunch::kPlain, kv_scales);
 }
 
 extern "C" int fpk_decode_step_fp8(const void* k_new, const void* v_new, uint8_t* kv_pool,

@@ -11,7 +11,8 @@
 // request, 128 KiB of its last page in each of 32 layers: 48 us (5.7 TB/s, nearly
 // all of it writes; the source stays in L2); 4001 pages of 32 KiB in 8 layers moved:
 // 328 us, 6.4 TB/s (94 % of what a copy reaches); 3.3 us for a few pages, a launch
-// and its chain of reads.
+// and its chain of reads.  A cache with block scales has two bytes more per tile of
+// 4096: they go with the page, by the CTA that copies it.
 #include "step_ops.cuh"
 
 namespace fpk {
@@ -29,6 +30,8 @@ struct MoveArgs {
   int32_t* seq_lens;
   uint32_t* live_tags;
   uint8_t* abort_mask;
+  uint16_t* scales;       // block scales, nullable: K's and V's byte of each tile, [num_pages][Hkv][tiles]
+  int64_t scale_stride;   // from one layer's to the next, in tiles
   int n, B, Hkv, page_size, num_pages, max_pages, layers, tile_bytes;
 };
 
@@ -52,6 +55,16 @@ __device__ __forceinline__ void copy_runs(uint8_t* dst, const uint8_t* src, int 
     for (int k = 0; k < kMoveUnroll; ++k)
       if (i + k * kMoveThreads < total) d[at[k]] = x[k];
   }
+}
+
+// The scales of the first `used` of each head's tiles of page src, to page dst.
+__device__ __forceinline__ void copy_scales(const MoveArgs& a, int64_t layer, int64_t dst, int64_t src, int used) {
+  if (a.scales == nullptr) return;
+  const int tpp = a.page_size >> 4, n = a.Hkv * tpp;
+  uint16_t* const base = a.scales + layer * a.scale_stride;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n; i += kMoveThreads)
+    if (i % tpp < used) base[dst * n + i] = base[src * n + i];
 }
 
 // CTAs [0, n): the row of fork i.  The rest copy, one (fork, layer) each: the
@@ -78,6 +91,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const MoveArgs a, co
     const int layer = static_cast<int>(job / a.n);
     const int head = (a.page_size >> 4) * (a.tile_bytes >> 4), used = ((rem + 15) >> 4) * (a.tile_bytes >> 4);
     uint8_t* base = a.pool + layer * a.layer_stride;
+    copy_scales(a, layer, fr, src, (rem + 15) >> 4);
     copy_runs(base + fr * a.page_bytes, base + src * a.page_bytes, a.Hkv, used, head);
     return;
   }
@@ -123,6 +137,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const MoveArgs a,
       if (s < 0 || s >= a.num_pages || d < 0 || d >= a.num_pages) continue;
       uint8_t* base = a.pool + job / a.n * a.layer_stride;
       const int units = static_cast<int>(a.page_bytes >> 4);
+      copy_scales(a, job / a.n, d, s, a.page_size >> 4);
       copy_runs(base + d * a.page_bytes, base + s * a.page_bytes, 1, units, units);
     }
     return;
@@ -182,6 +197,8 @@ int move_args(MoveArgs& a, void* kv_pool, int32_t elem_bytes, int32_t layers, in
   a.seq_lens = seq_lens;
   a.live_tags = live_tags;
   a.abort_mask = nullptr;
+  a.scales = nullptr;
+  a.scale_stride = 0;
   a.n = n;
   a.B = B;
   a.Hkv = Hkv;
@@ -192,21 +209,27 @@ int move_args(MoveArgs& a, void* kv_pool, int32_t elem_bytes, int32_t layers, in
   return FPK_OK;
 }
 
-}  // namespace
-}  // namespace fpk
+// The block scales of a move's pool (all layers): two bytes per tile, 2-byte aligned.
+int move_scales(MoveArgs& a, uint8_t* scales, int64_t stride) {
+  const int64_t layer = 2 * static_cast<int64_t>(a.num_pages) * a.Hkv * (a.page_size >> 4);
+  if (scales == nullptr || (reinterpret_cast<uintptr_t>(scales) & 1u) != 0 || (stride & 1) != 0 || stride < 0 ||
+      (a.layers > 1 && stride < layer))
+    return FPK_EINVAL;
+  a.scales = reinterpret_cast<uint16_t*>(scales);
+  a.scale_stride = stride / 2;
+  return FPK_OK;
+}
 
-extern "C" int fpk_kv_fork(void* kv_pool, int32_t elem_bytes, int32_t layers, int64_t layer_stride,
-                           int32_t* page_table, int32_t max_pages, uint32_t* expected_tags,
-                           int32_t* seq_lens, uint32_t* live_tags, uint8_t* abort_mask,
-                           const int32_t* parent, const int32_t* child, const int32_t* fresh, int32_t n,
-                           int32_t B, int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
-                           void* stream) {
-  using namespace fpk;
+int fork_entry(void* kv_pool, int32_t elem_bytes, int32_t layers, int64_t layer_stride, bool block, uint8_t* scales,
+               int64_t scale_stride, int32_t* page_table, int32_t max_pages, uint32_t* expected_tags,
+               int32_t* seq_lens, uint32_t* live_tags, uint8_t* abort_mask, const int32_t* parent,
+               const int32_t* child, const int32_t* fresh, int32_t n, int32_t B, int32_t Hkv, int32_t D,
+               int32_t page_size, int32_t num_pages, void* stream) {
   MoveArgs a;
   const int st = move_args(a, kv_pool, elem_bytes, layers, layer_stride, page_table, max_pages, expected_tags,
                            seq_lens, live_tags, n, B, Hkv, D, page_size, num_pages);
   if (st != FPK_OK || n == 0 || B == 0) return st;
-  if (!parent || !child || !fresh) return FPK_EINVAL;
+  if (!parent || !child || !fresh || (block && move_scales(a, scales, scale_stride) != FPK_OK)) return FPK_EINVAL;
   const int64_t ctas = static_cast<int64_t>(n) * (1 + static_cast<int64_t>(layers));
   if (ctas > 0x7fffffff) return FPK_EINVAL;
   a.abort_mask = abort_mask;
@@ -215,17 +238,16 @@ extern "C" int fpk_kv_fork(void* kv_pool, int32_t elem_bytes, int32_t layers, in
   return checked_launch_status();
 }
 
-extern "C" int fpk_kv_compact(void* kv_pool, int32_t elem_bytes, int32_t layers, int64_t layer_stride,
-                              int32_t* page_table, int32_t max_pages, uint32_t* expected_tags,
-                              const int32_t* seq_lens, uint32_t* live_tags, const int32_t* src,
-                              const int32_t* dst, int32_t n, int32_t B, int32_t Hkv, int32_t D,
-                              int32_t page_size, int32_t num_pages, void* stream) {
-  using namespace fpk;
+int compact_entry(void* kv_pool, int32_t elem_bytes, int32_t layers, int64_t layer_stride, bool block,
+                  uint8_t* scales, int64_t scale_stride, int32_t* page_table, int32_t max_pages,
+                  uint32_t* expected_tags, const int32_t* seq_lens, uint32_t* live_tags, const int32_t* src,
+                  const int32_t* dst, int32_t n, int32_t B, int32_t Hkv, int32_t D, int32_t page_size,
+                  int32_t num_pages, void* stream) {
   MoveArgs a;
   const int st = move_args(a, kv_pool, elem_bytes, layers, layer_stride, page_table, max_pages, expected_tags,
                            const_cast<int32_t*>(seq_lens), live_tags, n, B, Hkv, D, page_size, num_pages);
   if (st != FPK_OK || n == 0 || B == 0) return st;
-  if (!src || !dst) return FPK_EINVAL;
+  if (!src || !dst || (block && move_scales(a, scales, scale_stride) != FPK_OK)) return FPK_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // pages: as many CTAs as are resident at once; tables: one per 256 entries, up to as many again
   const int64_t jobs = static_cast<int64_t>(n) * layers;
@@ -247,4 +269,47 @@ extern "C" int fpk_kv_compact(void* kv_pool, int32_t elem_bytes, int32_t layers,
   cfg.numAttrs = copies + remaps > 0 ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, moved_tags_kernel, a, src, dst) != cudaSuccess) return FPK_ECUDA;
   return checked_launch_status();
+}
+
+}  // namespace
+}  // namespace fpk
+
+extern "C" int fpk_kv_fork(void* kv_pool, int32_t elem_bytes, int32_t layers, int64_t layer_stride,
+                           int32_t* page_table, int32_t max_pages, uint32_t* expected_tags,
+                           int32_t* seq_lens, uint32_t* live_tags, uint8_t* abort_mask,
+                           const int32_t* parent, const int32_t* child, const int32_t* fresh, int32_t n,
+                           int32_t B, int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                           void* stream) {
+  return fpk::fork_entry(kv_pool, elem_bytes, layers, layer_stride, false, nullptr, 0, page_table, max_pages,
+                         expected_tags, seq_lens, live_tags, abort_mask, parent, child, fresh, n, B, Hkv, D,
+                         page_size, num_pages, stream);
+}
+
+extern "C" int fpk_kv_compact(void* kv_pool, int32_t elem_bytes, int32_t layers, int64_t layer_stride,
+                              int32_t* page_table, int32_t max_pages, uint32_t* expected_tags,
+                              const int32_t* seq_lens, uint32_t* live_tags, const int32_t* src,
+                              const int32_t* dst, int32_t n, int32_t B, int32_t Hkv, int32_t D,
+                              int32_t page_size, int32_t num_pages, void* stream) {
+  return fpk::compact_entry(kv_pool, elem_bytes, layers, layer_stride, false, nullptr, 0, page_table, max_pages,
+                            expected_tags, seq_lens, live_tags, src, dst, n, B, Hkv, D, page_size, num_pages, stream);
+}
+
+extern "C" int fpk_kv_fork_block(void* kv_pool, int32_t layers, int64_t layer_stride, uint8_t* kv_scales,
+                                 int64_t scale_stride, int32_t* page_table, int32_t max_pages,
+                                 uint32_t* expected_tags, int32_t* seq_lens, uint32_t* live_tags,
+                                 uint8_t* abort_mask, const int32_t* parent, const int32_t* child,
+                                 const int32_t* fresh, int32_t n, int32_t B, int32_t Hkv, int32_t D,
+                                 int32_t page_size, int32_t num_pages, void* stream) {
+  return fpk::fork_entry(kv_pool, 1, layers, layer_stride, true, kv_scales, scale_stride, page_table, max_pages,
+                         expected_tags, seq_lens, live_tags, abort_mask, parent, child, fresh, n, B, Hkv, D,
+                         page_size, num_pages, stream);
+}
+
+extern "C" int fpk_kv_compact_block(void* kv_pool, int32_t layers, int64_t layer_stride, uint8_t* kv_scales,
+                                    int64_t scale_stride, int32_t* page_table, int32_t max_pages,
+                                    uint32_t* expected_tags, const int32_t* seq_lens, uint32_t* live_tags,
+                                    const int32_t* src, const int32_t* dst, int32_t n, int32_t B, int32_t Hkv,
+                                    int32_t D, int32_t page_size, int32_t num_pages, void* stream) {
+  return fpk::compact_entry(kv_pool, 1, layers, layer_stride, true, kv_scales, scale_stride, page_table, max_pages,
+                            expected_tags, seq_lens, live_tags, src, dst, n, B, Hkv, D, page_size, num_pages, stream);
 }

@@ -23,9 +23,18 @@
 // took 171 us.  2011 tokens in 7 chunks, bf16: 19 us, a launch, three dependent
 // reads and three steps per CTA.  Appends: 4 us for one token, 5 us for 64.
 //
+// Block scales (kBlock): a block's scale follows its largest value, so a key is
+// rotated before its scale is known.  An append's head is eight neighbouring
+// lanes: they find the token's largest value by shuffles.  Of a prompt's tile the
+// keys' largest values go through shared memory (a head is four warps), those of
+// values stay within the warp that writes them.  Where a scale grows, the codes of
+// the block's earlier tokens are brought under it, all their loads in flight at
+// once; tokens that are written together have one scale from the start.
+//
 // Rounding: fp32 throughout, a rotated value rounded once to what it is stored as.
 #include <algorithm>
 
+#include "block_scale.cuh"
 #include "step_ops.cuh"
 
 namespace fpk {
@@ -45,6 +54,7 @@ struct RopeArgs {
   uint16_t* q_out;
   const float* inv_freq;
   const int32_t* start_pos;  // nullable
+  uint8_t* scales;           // kBlock: E8M0 bytes [num_pages][Hkv][tiles][2]
   float rot_scale;
   int Hq, rot, interleaved, hsplit;
 };
@@ -132,7 +142,11 @@ __device__ __noinline__ uint2 quant8_slow(float4 x, float4 y, float s) {
   return make_uint2(codes(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)) | codes(__fdiv_rn(x.z, s), __fdiv_rn(x.w, s)) << 16,
                     codes(__fdiv_rn(y.x, s), __fdiv_rn(y.y, s)) | codes(__fdiv_rn(y.z, s), __fdiv_rn(y.w, s)) << 16);
 }
+template <bool kBlock>
 __device__ __forceinline__ uint2 quant8(const float* y, const Divisor& s) {
+  if (kBlock)  // a power of two: the product is the quotient
+    return make_uint2(codes(y[0] * s.r, y[1] * s.r) | codes(y[2] * s.r, y[3] * s.r) << 16,
+                      codes(y[4] * s.r, y[5] * s.r) | codes(y[6] * s.r, y[7] * s.r) << 16);
   if (!s.recip_ok) return quant8_slow(make_float4(y[0], y[1], y[2], y[3]), make_float4(y[4], y[5], y[6], y[7]), s.s);
   uint32_t w[2];
 #pragma unroll
@@ -161,13 +175,24 @@ __device__ __forceinline__ Unit unit_of(const RopeArgs& a, int u) {
   return x;
 }
 
+// Division by the scale 2^e.
+__device__ __forceinline__ Divisor block_divisor(int e) { return {exp2_int(e), exp2_int(-e), true}; }
+
+// The largest finite magnitude of a unit.
+__device__ __forceinline__ float unit_top(const float (&y)[16]) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = fmaxf(top, finite_magnitude(y[i]));
+  return top;
+}
+
 // A unit of a rotated key into its row of the K block.
-template <bool kFp8>
+template <bool kFp8, bool kBlock>
 __device__ __forceinline__ void put_key(const WriteArgs& w, int64_t row, const Unit& x, const float (&y)[16],
                                         const Divisor& ks) {
   if (kFp8) {
-    *reinterpret_cast<uint2*>(w.kv_pool + row + x.d0) = quant8(y, ks);
-    *reinterpret_cast<uint2*>(w.kv_pool + row + x.d1) = quant8(y + 8, ks);
+    *reinterpret_cast<uint2*>(w.kv_pool + row + x.d0) = quant8<kBlock>(y, ks);
+    *reinterpret_cast<uint2*>(w.kv_pool + row + x.d1) = quant8<kBlock>(y + 8, ks);
   } else {
     uint16_t* pool = reinterpret_cast<uint16_t*>(w.kv_pool);
     *reinterpret_cast<uint4*>(pool + row + x.d0) = pack8(y);
@@ -188,10 +213,64 @@ __device__ __forceinline__ int page_for(const WriteArgs& w, int r, int64_t pos) 
   return page;
 }
 
+__device__ __forceinline__ float key_top(const RopeArgs& a, const Unit& x, const Turn& t, const uint4& x0, const uint4& x1) {
+  float y[16];
+  rotate_unit(x0, x1, t, x.turns, a.interleaved, y);
+  return unit_top(y);
+}
+__device__ __forceinline__ float values_top(const uint4& x0, const uint4& x1) {
+  const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    top = fmaxf(top, fmaxf(finite_magnitude(__uint_as_float(w[i] << 16)), finite_magnitude(__uint_as_float(w[i] & 0xFFFF0000u))));
+  return top;
+}
+
+// The block of an append's key or value, by the head's eight lanes, one per unit: its scale for a token of
+// largest value `top` (this lane's) at `slot`, the earlier tokens brought under it.  tile: the tile's first byte.
+__device__ __forceinline__ Divisor grow_block(const RopeArgs& a, int64_t tile, int slot, bool value, const Unit& x,
+                                              int u, float top) {
+  const unsigned head = 0xFFu << (threadIdx.x & 24);
+  uint8_t* const at = a.scales + tile / (16 * kRopeDim) + (value ? 1 : 0);  // (two bytes per tile of 4096)
+  int old = slot > 0 ? scale_exponent(*at) : kExpLow;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(head, top, o));
+  old = __shfl_sync(head, old, 0, 8);  // (every lane has read the byte before one writes it)
+  const int e = max(old, block_exponent(top));
+  if (u == 0) *at = static_cast<uint8_t>(e + 127);
+  if (slot > 0 && e > old) {
+    const float f = exp2_int(old - e);
+    uint8_t* const block = a.w.kv_pool + tile + (value ? 16 * kRopeDim + 16 * u * 16 : 0);
+    if (value) {
+      uint4 r[16];
+#pragma unroll
+      for (int d = 0; d < 16; ++d) r[d] = *reinterpret_cast<const uint4*>(block + 16 * d);
+#pragma unroll
+      for (int d = 0; d < 16; ++d) *reinterpret_cast<uint4*>(block + 16 * d) = rescale_first(r[d], slot, f);
+    } else {
+      uint2 r[15][2];
+#pragma unroll
+      for (int i = 0; i < 15; ++i)
+        if (i < slot) {
+          r[i][0] = *reinterpret_cast<const uint2*>(block + i * kRopeDim + x.d0);
+          r[i][1] = *reinterpret_cast<const uint2*>(block + i * kRopeDim + x.d1);
+        }
+#pragma unroll
+      for (int i = 0; i < 15; ++i)
+        if (i < slot) {
+          *reinterpret_cast<uint2*>(block + i * kRopeDim + x.d0) = make_uint2(rescale4(r[i][0].x, f), rescale4(r[i][0].y, f));
+          *reinterpret_cast<uint2*>(block + i * kRopeDim + x.d1) = make_uint2(rescale4(r[i][1].x, f), rescale4(r[i][1].y, f));
+        }
+    }
+  }
+  return block_divisor(e);
+}
+
 // One token per request.  Thread = (token, slice, unit); the slice's heads are
 // slice, slice + hsplit, ... of the Hq queries, Hkv keys and Hkv values.  A
 // token's V column is strided by a tile's 16 tokens: element stores.
-template <bool kFp8>
+template <bool kFp8, bool kBlock>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs a) {
   const WriteArgs& w = a.w;
   const int64_t i = blockIdx.x * static_cast<int64_t>(kRopeThreads) + threadIdx.x;
@@ -234,15 +313,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
     } else {
       const int hk = h - a.Hq - (value ? w.Hkv : 0);
       const int64_t tile = ((static_cast<int64_t>(page) * w.Hkv + hk) * tpp + (off >> 4)) * 2 * 16 * kRopeDim;
+      Divisor bs = {};
+      if (kBlock) bs = grow_block(a, tile, off & 15, value, x, u, value ? values_top(x0, x1) : key_top(a, x, t, x0, x1));
       if (!value) {
         float y[16];
         rotate_unit(x0, x1, t, x.turns, a.interleaved, y);
-        put_key<kFp8>(w, tile + (off & 15) * kRopeDim, x, y, make_divisor(kFp8 ? __ldg(w.k_scale) : 1.f));
+        put_key<kFp8, kBlock>(w, tile + (off & 15) * kRopeDim, x, y,
+                              kBlock ? bs : make_divisor(kFp8 ? __ldg(w.k_scale) : 1.f));
       } else {
         const int64_t at = tile + 16 * kRopeDim + 16 * u * 16 + (off & 15);
         const uint32_t vw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
         if (kFp8) {
-          const Divisor vs = make_divisor(__ldg(w.v_scale));
+          const Divisor vs = kBlock ? bs : make_divisor(__ldg(w.v_scale));
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float y[8];
@@ -251,7 +333,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
               y[2 * k] = __uint_as_float(vw[4 * j + k] << 16);
               y[2 * k + 1] = __uint_as_float(vw[4 * j + k] & 0xFFFF0000u);
             }
-            const uint2 c = quant8(y, vs);
+            const uint2 c = quant8<kBlock>(y, vs);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               w.kv_pool[at + 16 * (8 * j + k)] = static_cast<uint8_t>((k < 4 ? c.x : c.y) >> (8 * (k & 3)));
@@ -311,9 +393,9 @@ __device__ __forceinline__ void put_row(uint8_t* row, const uint32_t (&c)[kWords
 
 // Values of one tile and head, by a warp: src is the tile's 16 token rows (those that are not new: whatever the
 // stage held); lane l writes the rows of dims l, l + 32, l + 64, l + 96, consecutive lanes consecutive rows.
-template <bool kFp8>
+template <bool kFp8, bool kBlock>
 __device__ __forceinline__ void put_values(const WriteArgs& w, int64_t vblock, const uint16_t* src, int t0, int n,
-                                           const Divisor& vs, int lane) {
+                                           const Divisor& vs, int lane, float older = 1.f) {
 #pragma unroll 1
   for (int d = lane; d < kRopeDim; d += 32) {
     uint32_t e[8];  // tokens 2 q, 2 q + 1
@@ -331,9 +413,22 @@ __device__ __forceinline__ void put_values(const WriteArgs& w, int64_t vblock, c
           y[2 * k] = __uint_as_float(e[4 * j + k] << 16);
           y[2 * k + 1] = __uint_as_float(e[4 * j + k] & 0xFFFF0000u);
         }
-        const uint2 x = quant8(y, vs);
+        const uint2 x = quant8<kBlock>(y, vs);
         c[2 * j] = x.x;
         c[2 * j + 1] = x.y;
+      }
+      if (kBlock && older != 1.f) {
+        // the tokens before: their codes times `older`
+        const uint4 was = rescale_first(*reinterpret_cast<const uint4*>(w.kv_pool + at), t0, older);
+        const uint32_t o[4] = {was.x, was.y, was.z, was.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = min(max(t0 - 4 * i, 0), 4);
+          const uint32_t mine = k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1u;
+          c[i] = (o[i] & mine) | (c[i] & ~mine);
+        }
+        put_row<4, 1>(w.kv_pool + at, c, 0, t0 + n);
+        continue;
       }
       put_row<4, 1>(w.kv_pool + at, c, t0, t0 + n);
     } else {
@@ -361,13 +456,53 @@ __device__ __forceinline__ void rope_copy8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// kBlock: four heads' keys of a tile by the 128 threads of a side (a thread a unit of a token, staged at in[64 k],
+// in[64 k + 32] for head k): the blocks' largest values meet in `tops`, then the keys go out, and the tile's earlier
+// tokens where their scale has grown.  The heads behind the last one are other threads' stage: not looked at.
+__device__ __forceinline__ void put_key_blocks(const RopeArgs& a, int64_t block, int h0, int tpp, int tok, int t0, int n,
+                                               const Unit& x, const Turn& t, const uint4* in, float (*tops)[4], int side) {
+  const int heads = a.w.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5 & 3;
+  const bool fresh = tok >= t0 && tok < t0 + n;
+  int old[kRopeBatch];
+#pragma unroll
+  for (int k = 0; k < kRopeBatch; ++k) {
+    const bool there = h0 + k < heads;
+    old[k] = there && t0 > 0 ? scale_exponent(a.scales[2 * (block + static_cast<int64_t>(h0 + k) * tpp)]) : kExpLow;
+    float top = 0.f;
+    if (there && fresh) top = key_top(a, x, t, in[64 * k], in[64 * k + 32]);
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    if (lane == 0) tops[k][warp] = top;
+  }
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + side) : "memory");
+#pragma unroll
+  for (int k = 0; k < kRopeBatch; ++k) {
+    if (h0 + k >= heads) break;
+    const int64_t tile = block + static_cast<int64_t>(h0 + k) * tpp, row = tile * 2 * 16 * kRopeDim + tok * kRopeDim;
+    const int e = max(old[k], block_exponent(fmaxf(fmaxf(tops[k][0], tops[k][1]), fmaxf(tops[k][2], tops[k][3]))));
+    if (fresh) {
+      float y[16];
+      rotate_unit(in[64 * k], in[64 * k + 32], t, x.turns, a.interleaved, y);
+      put_key<true, true>(a.w, row, x, y, block_divisor(e));
+    } else if (tok < t0 && e > old[k]) {
+      const float f = exp2_int(old[k] - e);
+      uint2* const c0 = reinterpret_cast<uint2*>(a.w.kv_pool + row + x.d0);
+      uint2* const c1 = reinterpret_cast<uint2*>(a.w.kv_pool + row + x.d1);
+      const uint2 r0 = *c0, r1 = *c1;
+      *c0 = make_uint2(rescale4(r0.x, f), rescale4(r0.y, f));
+      *c1 = make_uint2(rescale4(r1.x, f), rescale4(r1.y, f));
+    }
+    if (lane == 0 && warp == 0) a.scales[2 * tile] = static_cast<uint8_t>(e + 127);
+  }
+}
+
 // The sources of the next two steps are on their way while a step is worked
 // on: 128 KiB per SM in flight, each warp's into its own part of a stage, so
 // that no warp waits for another.
-template <bool kFp8>
+template <bool kFp8, bool kBlock>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) uint8_t s_stage[];
   __shared__ uint64_t s_rate[kRopeDim / 2];
+  __shared__ float s_top[2][2][kRopeBatch][4];  // kBlock: [turn][side][head][warp]
   const WriteArgs& w = a.w;
   const int u = threadIdx.x % kRopeUnits, tok = threadIdx.x / kRopeUnits % 16, lane = threadIdx.x & 31;
   const int side = threadIdx.x / (16 * kRopeUnits), warp = threadIdx.x >> 5;
@@ -376,8 +511,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
   const int64_t total = tile_places(w.rows, w.B) * steps;
   const int64_t begin = total * blockIdx.x / gridDim.x;
   const int count = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x - begin);
-  const Divisor ks = make_divisor(kFp8 ? __ldg(w.k_scale) : 1.f);
-  const Divisor vs = make_divisor(kFp8 ? __ldg(w.v_scale) : 1.f);
+  const Divisor ks = kBlock ? Divisor{} : make_divisor(kFp8 ? __ldg(w.k_scale) : 1.f);
+  const Divisor vs = kBlock ? Divisor{} : make_divisor(kFp8 ? __ldg(w.v_scale) : 1.f);
   const Unit x = unit_of(a, u);
   const int tpp = w.page_size >> 4;
   int64_t place = begin / steps - 1;
@@ -449,6 +584,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
   Step s0 = {}, s1 = {};
   Turn t;
   int turned = 0;  // t belongs to the tile
+  int tops = 0;    // kBlock: turn of s_top
 #pragma unroll 1
   for (int done = -2; done < count; ++done) {
     __syncwarp();  // the stage's last readers
@@ -462,6 +598,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
     __syncwarp();
     const uint8_t* const mine = s_stage + st * kRopeStage + warp * kRopeWarpStage;
     if (done == 0 || c.step == 0) turned = 0;
+    // kBlock: the two sides of a keys' step meet in it, whatever the tile is
+    const bool meets = kBlock && c.step >= qsteps && c.step < qsteps + ksteps;
+    if (meets && (c.n == 0 || c.page < 0)) {
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + side) : "memory");
+      tops ^= 1;
+    }
     if (c.n == 0) continue;
     if (c.step >= qsteps && c.page < 0) {
       if (threadIdx.x == 0 && w.abort_mask != nullptr) w.abort_mask[c.request] = 1;
@@ -479,7 +621,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
       const int heads = key ? w.Hkv : a.Hq;
       const int h0 = (key ? c.step - qsteps : c.step) * kRopeStep + side * kRopeBatch;
       const int64_t row = c.row0 + tok - c.t0;
-      if (tok >= c.t0 && tok < c.t0 + c.n)
+      if (kBlock && key) {
+        put_key_blocks(a, block, h0, tpp, tok, c.t0, c.n, x, t, reinterpret_cast<const uint4*>(mine) + lane, s_top[tops][side],
+                       side);
+        tops ^= 1;
+      } else if (tok >= c.t0 && tok < c.t0 + c.n)
 #pragma unroll 2
         for (int k = 0; k < kRopeBatch; ++k)
           if (h0 + k < heads) {
@@ -487,7 +633,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
             float y[16];
             rotate_unit(in[0], in[32], t, x.turns, a.interleaved, y);
             if (key) {
-              put_key<kFp8>(w, (block + static_cast<int64_t>(h0 + k) * tpp) * 2 * 16 * kRopeDim + tok * kRopeDim, x, y, ks);
+              put_key<kFp8, kBlock>(w, (block + static_cast<int64_t>(h0 + k) * tpp) * 2 * 16 * kRopeDim + tok * kRopeDim, x, y, ks);
             } else {
               uint16_t* const out = a.q_out + (row * heads + h0 + k) * kRopeDim;
               *reinterpret_cast<uint4*>(out + x.d0) = pack8(y);
@@ -496,28 +642,48 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_prefill_kernel(const Rop
           }
     } else {
       const int h = (c.step - qsteps - ksteps) * kRopeStep + warp;
-      if (h < w.Hkv)
-        put_values<kFp8>(w, (block + static_cast<int64_t>(h) * tpp) * 2 * 16 * kRopeDim + 16 * kRopeDim,
-                         reinterpret_cast<const uint16_t*>(mine), c.t0, c.n, vs, lane);
+      const int64_t tile = block + static_cast<int64_t>(h) * tpp;
+      if (h < w.Hkv && kBlock) {
+        uint8_t* const at = a.scales + 2 * tile + 1;
+        const int old = c.t0 > 0 ? scale_exponent(*at) : kExpLow;
+        float top = 0.f;
+#pragma unroll 4
+        for (int q = c.t0; q < c.t0 + c.n; ++q) {
+          const uint2 v = *reinterpret_cast<const uint2*>(mine + q * 256 + lane * 8);
+          top = fmaxf(top, fmaxf(fmaxf(finite_magnitude(__uint_as_float(v.x << 16)), finite_magnitude(__uint_as_float(v.x & 0xFFFF0000u))),
+                                 fmaxf(finite_magnitude(__uint_as_float(v.y << 16)), finite_magnitude(__uint_as_float(v.y & 0xFFFF0000u)))));
+        }
+        // (magnitudes order as their bits; every lane has read the byte before one writes it)
+        const int e = max(old, block_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)))));
+        const float older = exp2_int(__shfl_sync(0xffffffffu, old, 0) - e);
+        if (lane == 0) *at = static_cast<uint8_t>(e + 127);
+        put_values<kFp8, true>(w, tile * 2 * 16 * kRopeDim + 16 * kRopeDim, reinterpret_cast<const uint16_t*>(mine), c.t0, c.n,
+                               block_divisor(e), lane, c.t0 > 0 ? older : 1.f);
+      } else if (h < w.Hkv) {
+        put_values<kFp8, kBlock>(w, tile * 2 * 16 * kRopeDim + 16 * kRopeDim, reinterpret_cast<const uint16_t*>(mine), c.t0,
+                                 c.n, vs, lane);
+      }
     }
   }
 }
 
+// scales != nullptr: the e4m3 cache with block scales.
 int rope_entry(bool fp8, bool prefill, const void* q, const void* k, const void* v, const int32_t* seq_lens,
                const int32_t* cu, int64_t rows, const int32_t* start_pos, const float* inv_freq, void* q_out,
                void* kv_pool, const float* k_scale, const float* v_scale, const int32_t* page_table,
                int32_t max_pages, const uint32_t* live_tags, const uint32_t* expected_tags,
                uint8_t* abort_mask, int32_t rot_dim, int32_t interleaved, float rot_scale, int32_t B,
-               int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages, void* stream) {
+               int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages, void* stream,
+               bool block = false, uint8_t* scales = nullptr) {
   if (B < 0 || Hq < 0 || Hkv <= 0 || D <= 0 || page_size <= 0 || num_pages < 0 || max_pages < 0 || rows < 0 ||
-      rot_dim <= 0)
+      rot_dim < (block ? 0 : 1))
     return FPK_EINVAL;
   if (D != kRopeDim || page_size % 16 != 0 || page_size > 256) return FPK_EUNSUPPORTED;
   if (rot_dim % 16 != 0 || rot_dim > D) return FPK_EUNSUPPORTED;
   if (rows == 0 || B == 0) return FPK_OK;
-  if (!k || !v || !inv_freq || !kv_pool || !page_table || (prefill ? !cu : !seq_lens)) return FPK_EINVAL;
+  if (!k || !v || (rot_dim > 0 && !inv_freq) || !kv_pool || !page_table || (prefill ? !cu : !seq_lens)) return FPK_EINVAL;
   if (Hq > 0 && (!q || !q_out)) return FPK_EINVAL;
-  if (fp8 && (!k_scale || !v_scale)) return FPK_EINVAL;
+  if (block ? !scales : fp8 && (!k_scale || !v_scale)) return FPK_EINVAL;
   if (!aligned16(k) || !aligned16(v) || !aligned16(kv_pool) || !aligned16(q) || !aligned16(q_out)) return FPK_EINVAL;
   RopeArgs a;
   a.w.k_src = static_cast<const uint16_t*>(k);
@@ -542,6 +708,7 @@ int rope_entry(bool fp8, bool prefill, const void* q, const void* k, const void*
   a.q_out = static_cast<uint16_t*>(q_out);
   a.inv_freq = inv_freq;
   a.start_pos = start_pos;
+  a.scales = scales;
   a.rot_scale = rot_scale;
   a.Hq = Hq;
   a.rot = rot_dim;
@@ -549,7 +716,7 @@ int rope_entry(bool fp8, bool prefill, const void* q, const void* k, const void*
   a.hsplit = 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (prefill) {
-    auto kern = fp8 ? rope_prefill_kernel<true> : rope_prefill_kernel<false>;
+    auto kern = block ? rope_prefill_kernel<true, true> : fp8 ? rope_prefill_kernel<true, false> : rope_prefill_kernel<false, false>;
     const int64_t steps = (Hq + kRopeStep - 1) / kRopeStep + 2 * static_cast<int64_t>((Hkv + kRopeStep - 1) / kRopeStep);
     constexpr int smem = kRopeStages * kRopeStage + kRopeThreads * 64;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FPK_ECUDA;
@@ -566,7 +733,7 @@ int rope_entry(bool fp8, bool prefill, const void* q, const void* k, const void*
     a.hsplit = static_cast<int>(rows * heads <= full ? heads : (full + rows - 1) / rows);
     const int64_t ctas = (rows * a.hsplit * kRopeUnits + kRopeThreads - 1) / kRopeThreads;
     if (ctas > 0x7fffffff) return FPK_EUNSUPPORTED;
-    auto kern = fp8 ? rope_append_kernel<true> : rope_append_kernel<false>;
+    auto kern = block ? rope_append_kernel<true, true> : fp8 ? rope_append_kernel<true, false> : rope_append_kernel<false, false>;
     kern<<<static_cast<int>(ctas), kRopeThreads, 0, st>>>(a);
   }
   return checked_launch_status();
@@ -620,4 +787,47 @@ extern "C" int fpk_rope_prefill_bf16(const void* q, const void* k, const void* v
   return fpk::rope_entry(false, true, q, k, v, nullptr, cu_seqlens, n_tokens, start_pos, inv_freq, q_out, kv_pool,
                          nullptr, nullptr, page_table, max_pages, live_tags, expected_tags, abort_mask, rot_dim,
                          interleaved, rot_scale, B, Hq, Hkv, D, page_size, num_pages, stream);
+}
+
+extern "C" int fpk_rope_append_fp8_block(const void* q, const void* k_new, const void* v_new, const float* inv_freq,
+                                         void* q_out, uint8_t* kv_pool, uint8_t* kv_scales, const int32_t* page_table,
+                                         int32_t max_pages, const int32_t* seq_lens, const uint32_t* live_tags,
+                                         const uint32_t* expected_tags, uint8_t* abort_mask, int32_t rot_dim,
+                                         int32_t interleaved, float rot_scale, int32_t B, int32_t Hq, int32_t Hkv,
+                                         int32_t D, int32_t page_size, int32_t num_pages, void* stream) {
+  return fpk::rope_entry(true, false, q, k_new, v_new, seq_lens, nullptr, B, nullptr, inv_freq, q_out, kv_pool,
+                         nullptr, nullptr, page_table, max_pages, live_tags, expected_tags, abort_mask, rot_dim,
+                         interleaved, rot_scale, B, Hq, Hkv, D, page_size, num_pages, stream, true, kv_scales);
+}
+
+extern "C" int fpk_rope_prefill_fp8_block(const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
+                                          int32_t n_tokens, const int32_t* start_pos, const float* inv_freq,
+                                          void* q_out, uint8_t* kv_pool, uint8_t* kv_scales, const int32_t* page_table,
+                                          int32_t max_pages, const uint32_t* live_tags, const uint32_t* expected_tags,
+                                          uint8_t* abort_mask, int32_t rot_dim, int32_t interleaved, float rot_scale,
+                                          int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
+                                          int32_t num_pages, void* stream) {
+  return fpk::rope_entry(true, true, q, k, v, nullptr, cu_seqlens, n_tokens, start_pos, inv_freq, q_out, kv_pool,
+                         nullptr, nullptr, page_table, max_pages, live_tags, expected_tags, abort_mask, rot_dim,
+                         interleaved, rot_scale, B, Hq, Hkv, D, page_size, num_pages, stream, true, kv_scales);
+}
+
+extern "C" int fpk_kv_append_fp8_block(const void* k_new, const void* v_new, uint8_t* kv_pool, uint8_t* kv_scales,
+                                       const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                                       const uint32_t* live_tags, const uint32_t* expected_tags, uint8_t* abort_mask,
+                                       int32_t B, int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                                       void* stream) {
+  return fpk_rope_append_fp8_block(nullptr, k_new, v_new, nullptr, nullptr, kv_pool, kv_scales, page_table, max_pages,
+                                   seq_lens, live_tags, expected_tags, abort_mask, 0, 0, 1.f, B, 0, Hkv, D, page_size,
+                                   num_pages, stream);
+}
+
+extern "C" int fpk_kv_prefill_fp8_block(const void* k, const void* v, const int32_t* cu_seqlens, int32_t n_tokens,
+                                        const int32_t* start_pos, uint8_t* kv_pool, uint8_t* kv_scales,
+                                        const int32_t* page_table, int32_t max_pages, const uint32_t* live_tags,
+                                        const uint32_t* expected_tags, uint8_t* abort_mask, int32_t B, int32_t Hkv,
+                                        int32_t D, int32_t page_size, int32_t num_pages, void* stream) {
+  return fpk_rope_prefill_fp8_block(nullptr, k, v, cu_seqlens, n_tokens, start_pos, nullptr, nullptr, kv_pool, kv_scales,
+                                    page_table, max_pages, live_tags, expected_tags, abort_mask, 0, 0, 1.f, B, 0, Hkv, D,
+                                    page_size, num_pages, stream);
 }

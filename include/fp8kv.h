@@ -58,6 +58,13 @@
  * Scales:         float  [1] each         per-tensor dequantisation scale:
  *                 value = decode_e4m3(code) * scale; positive and finite.
  *
+ * Block scales:    uint8  [num_pages][Hkv][page_size/16][2], the e4m3 pool of the
+ *                  *_fp8_block calls instead of the two scales: one E8M0 byte
+ *                  (exponent + 127) for the K and one for the V of each tile (16
+ *                  tokens of a kv head), value = decode_e4m3(code) * 2^(byte - 127).
+ *                  Exponents lie in [-50, 30]; bytes outside count as the nearest
+ *                  bound.  2-byte aligned.  See fpk_rope_append_fp8_block.
+ *
  * E4M3 is the OCP OFP8 E4M3 format (bias 7, no infinities, NaN = S.1111.111,
  * largest finite 448).  Quantisation computes float(x)/scale with one IEEE
  * fp32 division and rounds to nearest-even with saturation to +-448; NaN
@@ -247,6 +254,60 @@ int fpk_rope_prefill_bf16(const void* q, const void* k, const void* v, const int
                           int32_t page_size, int32_t num_pages, void* stream);
 
 /*
+ * Writes of an e4m3 cache with block scales: as fpk_rope_append_fp8,
+ * fpk_rope_prefill_fp8, fpk_kv_append_fp8 and fpk_kv_prefill_fp8 (same guard,
+ * same rotation, same rounding), but no scale is given: each block's follows its
+ * largest value.  The pages state only that the cache holds e4m3 values ("Cosa
+ * ha cambiato Cloudflare per Kimi e GLM", remio.ai); scales by block are this
+ * library's reading, for caches whose range is not known when they are written.
+ *
+ * Let E(x) be the least exponent e in [-50, 30] with |x| <= 448 * 2^e for the
+ * largest finite x of the new tokens' values (after the rotation) that one call
+ * writes into a block; larger values saturate.  A block whose slot 0 is among
+ * them gets e = E and forgets what it held; any other gets e = max(its exponent,
+ * E), and where that grows the codes of the slots before the new ones become
+ * e4m3(decode(code) * 2^(old - e)): exact, but for codes that fall below 2^-6.
+ * New codes are e4m3(x * 2^-e).  Slots behind the new ones keep their bytes
+ * (positions are written in order; a slot written again keeps the others right
+ * only while the exponent does not grow).  Repeating a call changes nothing.
+ *   kv_scales : block scales, read and written
+ *   rot_dim   : as there, or 0: no rotation (inv_freq may be NULL; queries are
+ *               copied).  The kv_* calls are those with rot_dim = Hq = 0.
+ *   start_pos : int32 [B] or NULL (0)
+ * For a decode batch on block scales: this append, fpk_page_tags_validate,
+ * fpk_paged_decode_attn_fp8_block.
+ */
+int fpk_rope_append_fp8_block(const void* q, const void* k_new, const void* v_new,
+                              const float* inv_freq, void* q_out, uint8_t* kv_pool,
+                              uint8_t* kv_scales, const int32_t* page_table, int32_t max_pages,
+                              const int32_t* seq_lens, const uint32_t* live_tags,
+                              const uint32_t* expected_tags, uint8_t* abort_mask, int32_t rot_dim,
+                              int32_t interleaved, float rot_scale, int32_t B, int32_t Hq,
+                              int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                              void* stream);
+int fpk_rope_prefill_fp8_block(const void* q, const void* k, const void* v,
+                               const int32_t* cu_seqlens, int32_t n_tokens,
+                               const int32_t* start_pos, const float* inv_freq, void* q_out,
+                               uint8_t* kv_pool, uint8_t* kv_scales, const int32_t* page_table,
+                               int32_t max_pages, const uint32_t* live_tags,
+                               const uint32_t* expected_tags, uint8_t* abort_mask, int32_t rot_dim,
+                               int32_t interleaved, float rot_scale, int32_t B, int32_t Hq,
+                               int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                               void* stream);
+int fpk_kv_append_fp8_block(const void* k_new, const void* v_new, uint8_t* kv_pool,
+                            uint8_t* kv_scales, const int32_t* page_table, int32_t max_pages,
+                            const int32_t* seq_lens, const uint32_t* live_tags,
+                            const uint32_t* expected_tags, uint8_t* abort_mask, int32_t B,
+                            int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                            void* stream);
+int fpk_kv_prefill_fp8_block(const void* k, const void* v, const int32_t* cu_seqlens,
+                             int32_t n_tokens, const int32_t* start_pos, uint8_t* kv_pool,
+                             uint8_t* kv_scales, const int32_t* page_table, int32_t max_pages,
+                             const uint32_t* live_tags, const uint32_t* expected_tags,
+                             uint8_t* abort_mask, int32_t B, int32_t Hkv, int32_t D,
+                             int32_t page_size, int32_t num_pages, void* stream);
+
+/*
  * Fork: request child[i] takes over the context of request parent[i], i < n
  * (several samples of one prompt).  Full pages are shared: the child's table
  * and expected tags name the parent's pages.  The page in use, where
@@ -295,6 +356,24 @@ int fpk_kv_compact(void* kv_pool, int32_t elem_bytes, int32_t layers, int64_t la
                    const int32_t* seq_lens, uint32_t* live_tags, const int32_t* src,
                    const int32_t* dst, int32_t n, int32_t B, int32_t Hkv, int32_t D,
                    int32_t page_size, int32_t num_pages, void* stream);
+
+/*
+ * fpk_kv_fork and fpk_kv_compact of an e4m3 pool with block scales: the scales
+ * move with the pages.
+ *   kv_scales    : block scales of layer 0; layer l's start at kv_scales + l *
+ *                  scale_stride bytes (scale_stride even)
+ */
+int fpk_kv_fork_block(void* kv_pool, int32_t layers, int64_t layer_stride, uint8_t* kv_scales,
+                      int64_t scale_stride, int32_t* page_table, int32_t max_pages,
+                      uint32_t* expected_tags, int32_t* seq_lens, uint32_t* live_tags,
+                      uint8_t* abort_mask, const int32_t* parent, const int32_t* child,
+                      const int32_t* fresh, int32_t n, int32_t B, int32_t Hkv, int32_t D,
+                      int32_t page_size, int32_t num_pages, void* stream);
+int fpk_kv_compact_block(void* kv_pool, int32_t layers, int64_t layer_stride, uint8_t* kv_scales,
+                         int64_t scale_stride, int32_t* page_table, int32_t max_pages,
+                         uint32_t* expected_tags, const int32_t* seq_lens, uint32_t* live_tags,
+                         const int32_t* src, const int32_t* dst, int32_t n, int32_t B, int32_t Hkv,
+                         int32_t D, int32_t page_size, int32_t num_pages, void* stream);
 
 /*
  * Element-wise quantiser: out[i] = e4m3(x[i] / *scale) for i < n, with the
@@ -477,6 +556,62 @@ int fpk_paged_decode_attn_bf16(const void* q, const void* kv_pool,
                                int32_t num_splits, float sm_scale, int32_t B, int32_t Hq,
                                int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
                                void* stream);
+
+/*
+ * fpk_paged_decode_attn_fp8 over a cache with block scales: same arguments but
+ * for kv_scales in place of the two scales, same results with each tile's values
+ * under its own scales, same workspace (fpk_decode_workspace_bytes), same
+ * fail-closed rules, same bits on repeated calls.
+ */
+int fpk_paged_decode_attn_fp8_block(const void* q, const uint8_t* kv_pool, const uint8_t* kv_scales,
+                                    const int32_t* page_table, int32_t max_pages,
+                                    const int32_t* seq_lens, const uint8_t* abort_mask, float* out,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    int32_t num_splits, float sm_scale, int32_t B, int32_t Hq,
+                                    int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                                    void* stream);
+
+/*
+ * Attention of several query tokens per request over a cache with block scales:
+ * a prompt's chunk behind its write (fpk_rope_prefill_fp8_block), drafted tokens
+ * that are checked in one pass, or a decoder's tokens over an encoder's states
+ * (cross attention).  The pages keep prefill in pools of its own ("Cosa ha
+ * cambiato Cloudflare per Kimi e GLM"); a decode pool needs this call where it
+ * writes prompts itself.
+ *
+ * Rows cu_seqlens[r] .. cu_seqlens[r+1]-1 of q and out are request r's n_r query
+ * tokens.  With causal != 0 they are the last n_r of its L = seq_lens[r] tokens:
+ * token i sees the cache's tokens 0 .. L - n_r + i (none where that is negative).
+ * With causal == 0 each sees all L.  Over the tokens j that it sees,
+ *   out[i][h][:] = bf16(sum_j exp(s_j - m) V_j / sum_j exp(s_j - m)),
+ *   lse[i][h] = m + ln(sum_j exp(s_j - m)), s_j = sm_scale q . K_j, m = max_j s_j,
+ * K and V the codes times their blocks' scales.  A token that sees nothing, and
+ * all tokens of a dead request (L <= 0, abort_mask[r] != 0, L > max_pages *
+ * page_size, a page id outside [0, num_pages) among the first ceil(L / page_size)
+ * entries) get out = 0 and lse = -inf.  Rows behind cu_seqlens[B] are left alone.
+ * Tokens that a row does not see have no part in it, whatever they hold.
+ *   q         : bf16 [n_tokens][Hq][D], 16-byte aligned
+ *   cu_seqlens: int32 [B+1], cu_seqlens[0] == 0, non-decreasing, cu_seqlens[B] <= n_tokens
+ *   out       : bf16 [n_tokens][Hq][D], 32-byte aligned; lse: float [n_tokens][Hq], nullable
+ *   workspace : >= fpk_prefill_workspace_bytes(...) bytes for the current device,
+ *               256-byte aligned, zeroed ONCE after allocating (its first 4 bytes
+ *               are a status word as in fpk_paged_decode_attn_fp8).  Calls that
+ *               share a workspace must not overlap on the GPU.
+ * Precision: scores, sums and O in fp32; the query enters as two e4m3 parts (what
+ * they leave out is below 2^-17 of the largest |q| of its row), K exactly; softmax
+ * weights enter in f16 (relative to the largest weight times V scale, half a step
+ * is 2^-11 of each), V exactly.  Repeated calls on the same inputs give identical
+ * bits.  One token per request is served better by fpk_paged_decode_attn_fp8_block.
+ */
+size_t fpk_prefill_workspace_bytes(int32_t B, int32_t n_tokens, int32_t Hq, int32_t Hkv, int32_t D);
+int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu_seqlens, int32_t n_tokens,
+                                     const uint8_t* kv_pool, const uint8_t* kv_scales,
+                                     const int32_t* page_table, int32_t max_pages,
+                                     const int32_t* seq_lens, const uint8_t* abort_mask,
+                                     int32_t causal, void* out, float* lse, void* workspace,
+                                     size_t workspace_bytes, float sm_scale, int32_t B, int32_t Hq,
+                                     int32_t Hkv, int32_t D, int32_t page_size, int32_t num_pages,
+                                     void* stream);
 
 /*
  * Decode attention of a batch whose requests share prefixes: each shared
