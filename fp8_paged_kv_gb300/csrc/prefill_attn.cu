@@ -1,14 +1,47 @@
 // prefill_attn.cu -- attention of several query tokens per request over an e4m3
-// cache with block scales: chunks of prompts and drafted tokens (causal), or an
-// encoder's states (all tokens).
+// cache with block scales, on the fifth-generation tensor cores: chunks of prompts
+// and drafted tokens (causal), or an encoder's states (all tokens).
 //
-// A warp takes 16 rows (a row is one query head of one token; the heads that
-// share a kv head follow one another) over all tokens they see, 16 at a time,
-// with its operands straight from the pool: lane (g, c) = (lane / 4, lane % 4)
-// holds 16-byte chunks c and c + 4 of its K tokens, and tokens 4 c .. 4 c + 3 of its
-// V dims, which are the tokens of the scores that it holds, so that the weights
-// enter the second product from the registers where the first left them.
+// The rows of a request and kv head are its query tokens' heads that read it (token
+// by token, the heads of a group one after another): one read of a block of K and V
+// serves 256 rows, and a causal border crosses few blocks (32 tokens at 8 heads per
+// group).  Three launches, each a dependent of the one before:
+//   plan    dead requests, the work list (one CTA)
+//   attn    the list, a CTA per SM
+//   merge   rows whose unit was cut between CTAs, by log-sum-exp
+//
+// * Unit: up to 256 rows of one (request, kv head) over the tokens that its last
+//   row sees.  Units are laid end to end in cost (blocks of 128 tokens, dearer for
+//   units of more than 128 rows, and a start), the kv heads one after another, and
+//   the line is cut into one equal range per CTA.  A unit that lies within a range
+//   is answered by its CTA; of the others every piece leaves a partial (m, l, O),
+//   merged in a fixed order: repeated calls give the same bits.
+//
+// Piece pipeline (one CTA per SM, 16 warps), per block of 128 tokens:
+//   warp 15     finds the pieces and the blocks' scales ahead of the others
+//   warp 12     lands K rows (128-byte swizzle) and V tiles by tensor maps
+//   warps 8-11  V codes to f16 core matrices (exact); zeroes where no token lies;
+//               between two pieces, the next one's queries: q 2^e as two e4m3 parts
+//   warps 13, 14  issue S = Q K^T (e4m3, over both parts against the same K rows) and
+//               O += P V (f16) of row tile 0 and 1, tcgen05.mma of M = N = 128
+//   warps 0-3, 4-7  softmax of row tile 0 and 1, a thread per row: no shuffles.  P
+//               (f16, in the columns of the scores it came from) is the A operand
+// Units of more than 128 rows use both tiles on every block; smaller ones give the
+// two tiles alternate blocks of the same rows, joined at the end in tensor memory.
+//
+// Scales.  Of each tile of 16 tokens (16 columns of S) K's scale multiplies the
+// scores and V's goes into the weights: with ev its exponent, P = 2^(s + ev - m), m
+// the largest s + ev (within 2^8), so that the weights that meet V's codes use f16's
+// range whatever the order of the scales; the sum takes P 2^-ev, which is 2^(s - m).
+//
+// Tokens that a row does not see have no part in it: their scores become -inf before
+// anything is taken from them, and where a block holds tokens that only some rows
+// see, their V codes that are NaN become 0 (0 NaN = NaN) and the rows that do see
+// them are given the NaN afterwards.
+#include <atomic>
+
 #include "block_scale.cuh"
+#include "tc_attn.cuh"
 
 namespace fpk {
 namespace {
@@ -16,163 +49,1154 @@ namespace {
 constexpr int kChTile = 16;
 constexpr int kChDim = 128;
 constexpr int kChGroupMax = 8;
-constexpr int kChWarps = 4;
-constexpr int kChRows = 16 * kChWarps;
+constexpr int kChBlk = 128;  // tokens of a block
+constexpr int kChBlkTiles = kChBlk / kChTile;
+constexpr int kChUnitRows = 256;
 constexpr float kChLog2e = 1.4426950408889634f;
 constexpr float kChLn2 = 0.6931471805599453f;
+constexpr float kChGrow = 8.f;  // log2 growth of a maximum that rescales O
+constexpr float kChMinMult = 1e-37f;  // of a row's scale times K's: -inf times it is -inf still
+__device__ __forceinline__ float at_least_min(float mult) { return mult < kChMinMult ? kChMinMult : mult; }  // (a NaN stays one)
+// Costs in the work list, in some 500 cycles: of a block with both tiles at work and with one, of a unit's start.
+constexpr int kChCostPair = 6, kChCostSolo = 3;
+constexpr int kChStartPair = 10, kChStartSolo = 6;
+
+constexpr int kChThreads = 512;
+constexpr int kChVWarp = 8, kChLoadWarp = 12, kChMmaWarp = 13, kChPlanWarp = 15;
+constexpr int kChPieces = 4;  // pieces known ahead
+constexpr int kChPlanThreads = 1024;
+constexpr int kChTurnSpins = 4096;
+constexpr int kChMergeWarps = 8, kChMergeParts = 8;  // merge: CTAs per cut unit
+
+struct alignas(16) ChUnit {
+  int y;       // place in a kv head's line
+  int r;
+  int row0, rows;  // of the request's rows
+  int tokens;  // that its last row sees
+  int c0;      // the request's first query token
+  int shift;   // row's token t sees min(L, max(0, shift + t + 1)) tokens
+  int L;       // 0: dead
+};
+static_assert(sizeof(ChUnit) == 32, "two 16-byte words");
+
+struct alignas(16) ChStart {  // of a CTA's range
+  int unit, h, b0, b1;
+};
 
 struct ChArgs {
   const uint16_t* q;
   const int32_t* cu_seqlens;
-  const uint8_t* kv_pool;
   const uint16_t* kv_scales;
+  const uint8_t* kv_pool;
   const int32_t* page_table;
   const int32_t* seq_lens;
   const uint8_t* abort_mask;
   uint16_t* out;
   float* lse;
-  int n_tokens, causal, B, Hq, Hkv, G, page_size, num_pages, max_pages;
+  uint32_t* status;
+  int32_t* base;    // [B + 1] first unit of each request
+  int32_t* dead;    // [B]
+  ChUnit* unit;
+  ChStart* start;   // [ctas + 1]; the last one's b0 is the line's end
+  float2* part_ml;  // partials: [2 ctas][256 rows]
+  float* part_o;
+  int n_tokens, causal, B, Hq, Hkv, G, page_size, num_pages, max_pages, ctas, zbox;
+  uint32_t by_g, by_tpp;
   float sm_scale_log2;
 };
 
-__global__ void __launch_bounds__(32 * kChWarps) prefill_attn_kernel(const ChArgs a) {
+struct ChCfg {
+  static constexpr int kQTile = 128 * 256;  // both parts of a tile's queries
+  static constexpr int kKStage = kChBlk * kChDim, kVStage = kKStage, kV16 = 2 * kVStage;
+  static constexpr int kKStages = 4, kVStages = 2, kV16Bufs = 2;
+  static constexpr int kScales = 8;         // blocks whose scales are known
+  static constexpr int kNan = 16;           // pieces with a flag of NaN values
+  static constexpr int kPieceBytes = 64 + 32 * 4;
+  static constexpr int kOffK = 2 * kQTile;
+  static constexpr int kOffV = kOffK + kKStages * kKStage;
+  static constexpr int kOffV16 = kOffV + kVStages * kVStage;
+  static constexpr int kOffPiece = kOffV16 + kV16Bufs * kV16;
+  static constexpr int kOffScale = kOffPiece + kChPieces * kPieceBytes;  // float4 [kScales][8]: K's factor, V's exponent, 1 / V's factor
+  static constexpr int kOffMult = kOffScale + kScales * kChBlkTiles * 8;
+  static constexpr int kOffBars = kOffMult + 2 * 128 * 4;
+  static constexpr int kBarKFull = 0;
+  static constexpr int kBarKFree = kBarKFull + kKStages;
+  static constexpr int kBarVFull = kBarKFree + kKStages;
+  static constexpr int kBarVFree = kBarVFull + kVStages;
+  static constexpr int kBarReady = kBarVFree + kVStages;       // converted V block
+  static constexpr int kBarUsed = kBarReady + kV16Bufs;        // .. read by the MMA
+  static constexpr int kBarS = kBarUsed + kV16Bufs;            // [tile]
+  static constexpr int kBarP = kBarS + 2;                      // [tile][half of the block]
+  static constexpr int kBarO = kBarP + 4;                      // [tile] a product added to O
+  static constexpr int kBarOFree = kBarO + 2;                  // [tile] O of a piece read
+  static constexpr int kBarQ = kBarOFree + 2;                  // [buffer] queries staged
+  static constexpr int kBarQFree = kBarQ + 2;                  // [buffer] queries of a piece read
+  static constexpr int kBarPiece = kBarQFree + 2;              // [kChPieces] piece known
+  static constexpr int kBarPieceFree = kBarPiece + kChPieces;  // [kChPieces] piece read by every warp
+  static constexpr int kBarScale = kBarPieceFree + kChPieces;  // [kScales] a block's scales known
+  static constexpr int kBarScaleFree = kBarScale + kScales;    // [kScales] .. read
+  static constexpr int kBarJoin = kBarScaleFree + kScales;     // tile 1's state of a unit of one row tile
+  static constexpr int kBarDone = kBarJoin + 1;                // [2] every MMA of a warp completed
+  static constexpr int kBars = kBarDone + 2;
+  static constexpr int kOffMisc = kOffBars + 8 * kBars;        // tensor memory base, failure flag, turns of the tiles, NaN flags
+  static constexpr int kSmem = kOffMisc + 16 + 4 * kNan;
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
+};
+
+// Context length of request r if it is alive by its length and abort flag, else 0.
+__device__ __forceinline__ int live_length(const ChArgs& a, int r) {
+  const int L = __ldg(a.seq_lens + r);
+  if (L <= 0 || static_cast<int64_t>(L) > static_cast<int64_t>(a.max_pages) * a.page_size) return 0;
+  if (a.abort_mask != nullptr && __ldg(a.abort_mask + r) != 0) return 0;
+  return L;
+}
+// First query token of request r, and behind its last (r = B: the end).
+__device__ __forceinline__ int query_start(const ChArgs& a, int r) {
+  return min(max(__ldg(a.cu_seqlens + r), 0), a.n_tokens);
+}
+__device__ __forceinline__ int seen(const ChUnit& u, int token) { return min(u.L, max(0, u.shift + token + 1)); }
+
+// ---------------------------------------------------------------------------
+// work list
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kChBlk - 1) / kChBlk; }
+__device__ __forceinline__ int block_cost(int rows) { return rows > 128 ? kChCostPair : kChCostSolo; }
+__device__ __forceinline__ int start_cost(int rows) { return rows > 128 ? kChStartPair : kChStartSolo; }
+__device__ __forceinline__ int unit_cost(const ChUnit& u) { return start_cost(u.rows) + block_cost(u.rows) * blocks_of(u.tokens); }
+// Blocks [i0, i1) of a unit at place y that a range [b0, b1) owns: those that start in it.
+__device__ __forceinline__ void owned_blocks(const ChUnit& u, int y, int b0, int b1, int& i0, int& i1) {
+  const int w = block_cost(u.rows), n = blocks_of(u.tokens), at = y + start_cost(u.rows);
+  const int lo = max(b0 - at, 0) + w - 1, hi = max(b1 - at, 0) + w - 1;
+  i0 = min(n, w == kChCostPair ? lo / kChCostPair : lo / kChCostSolo);
+  i1 = min(n, w == kChCostPair ? hi / kChCostPair : hi / kChCostSolo);
+}
+__device__ __forceinline__ ChUnit load_unit(const ChUnit* at) {
+  const int4* p = reinterpret_cast<const int4*>(at);
+  const int4 x = __ldcg(p), y = __ldcg(p + 1);
+  return {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+}
+
+// Sums of a CTA's threads: the sum of the threads before, and of all.
+__device__ __forceinline__ int block_scan(int mine, int& all, int* s_sum) {
   const unsigned kFull = 0xffffffffu;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const int h = blockIdx.y;
-  int lo = 0, hi = a.B - 1;
-  auto place_of = [&](int r) -> int64_t { return static_cast<int64_t>(__ldg(a.cu_seqlens + r)) * a.G / kChRows + r; };
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (place_of(mid) <= blockIdx.x) lo = mid; else hi = mid - 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
   }
-  const int r = lo, c0 = max(__ldg(a.cu_seqlens + r), 0), n = min(__ldg(a.cu_seqlens + r + 1), a.n_tokens) - c0;
-  const int64_t rows = static_cast<int64_t>(n) * a.G, row0 = (blockIdx.x - place_of(r)) * kChRows;
-  if (row0 >= rows) return;
-  const int L = __ldg(a.seq_lens + r), tpp = a.page_size >> 4;
-  bool dead = L <= 0 || static_cast<int64_t>(L) > static_cast<int64_t>(a.max_pages) * a.page_size ||
-              (a.abort_mask != nullptr && __ldg(a.abort_mask + r) != 0);
-  const int32_t* table = a.page_table + static_cast<int64_t>(r) * a.max_pages;
-  for (int i = threadIdx.x; !dead && i <= (L - 1) / a.page_size; i += 32 * kChWarps) {
-    const int p = __ldg(table + i);
-    dead = p < 0 || p >= a.num_pages;
+  __syncthreads();  // (s_sum's last readers)
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int sums = s_sum[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, sums, o);
+    if (lane >= o) sums += v;
   }
-  dead = __syncthreads_or(dead);
-  // this lane's rows: g and g + 8 of the warp's 16
-  int64_t at[2];
-  int limit[2];
-  bool valid[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t row = row0 + 16 * warp + g + 8 * i;
-    const int t = static_cast<int>(row / a.G);
-    valid[i] = row < rows;
-    at[i] = static_cast<int64_t>(c0 + (valid[i] ? t : 0)) * a.Hq + h * a.G + (valid[i] ? row - static_cast<int64_t>(t) * a.G : 0);
-    limit[i] = dead || !valid[i] ? 0 : a.causal ? max(0, min(L, L - n + t + 1)) : L;
-  }
-  uint32_t qa[8][4];
-  float mult[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t w[16];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.q + at[i] * kChDim + 16 * (c + 4 * (k >> 1)) + 8 * (k & 1)));
-      w[4 * k] = x.x;
-      w[4 * k + 1] = x.y;
-      w[4 * k + 2] = x.z;
-      w[4 * k + 3] = x.w;
-    }
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-    top = max(top, __shfl_xor_sync(kFull, top, 1));
-    top = max(top, __shfl_xor_sync(kFull, top, 2));
-    const int ex = static_cast<int>(top >> 7);
-    const int e = ex == 0 ? (top == 0 ? 0 : 126) : min(max(134 - ex, -126), 126);
-    const float up = exp2_int(e);
-    mult[i] = ex == 255 ? __int_as_float(0x7fffffff) : a.sm_scale_log2 * exp2_int(-e);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        qa[k][i + 2 * j] = pack_f16x2(__uint_as_float(w[2 * k + j] << 16) * up, __uint_as_float(w[2 * k + j] & 0xFFFF0000u) * up);
-  }
-  float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  int most = max(limit[0], limit[1]);
-  most = __reduce_max_sync(kFull, most);
+  const int below = __shfl_sync(kFull, sums, max(warp - 1, 0));
+  all = __shfl_sync(kFull, sums, 31);
+  return incl - mine + (warp > 0 ? below : 0);
+}
+
+__global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const ChArgs a) {
+  __shared__ int s_sum[kChPlanThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const unsigned kFull = 0xffffffffu;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  // requests that a bad page makes dead, a warp each
 #pragma unroll 1
-  for (int t = 0; t * kChTile < most; ++t) {
-    const int64_t tile = (static_cast<int64_t>(__ldg(table + t / tpp)) * a.Hkv + h) * tpp + t % tpp;
-    const uint32_t sb = __ldg(a.kv_scales + tile);
-    const float km = exp2_int(scale_exponent(sb & 255u));
-    const int ev = scale_exponent(sb >> 8);
-    const uint8_t* const block = a.kv_pool + tile * 2 * kChTile * kChDim;
-    float s[2][4] = {};
+  for (int r = warp; r < a.B; r += kChPlanThreads / 32) {
+    const int L = live_length(a, r), pages = L > 0 ? (L - 1) / a.page_size + 1 : 0;
+    const int32_t* const row = a.page_table + static_cast<int64_t>(r) * a.max_pages;
+    bool bad = false;
+#pragma unroll 8
+    for (int i = lane; i < pages; i += 32) bad |= static_cast<unsigned>(__ldg(row + i)) >= static_cast<unsigned>(a.num_pages);
+    bad = __any_sync(kFull, bad);
+    if (lane == 0) a.dead[r] = bad || L == 0;
+  }
+  // units of each request
+  int units = 0;
+#pragma unroll 1
+  for (int r0 = 0; r0 < a.B; r0 += kChPlanThreads) {
+    const int r = r0 + t;
+    const int rows = r < a.B ? max(0, query_start(a, r + 1) - query_start(a, r)) * a.G : 0;
+    int all;
+    const int before = block_scan((rows + kChUnitRows - 1) / kChUnitRows, all, s_sum);
+    if (r < a.B) a.base[r] = units + before;
+    units += all;
+  }
+  if (t == 0) a.base[a.B] = units;
+  __syncthreads();
+  // their places: each thread a run of units
+  const int chunk = (units + kChPlanThreads - 1) / kChPlanThreads;
+  const int x0 = min(units, t * chunk), x1 = min(units, x0 + chunk);
+  int lo = 0;
+  if (x0 < x1) {
+    int hi = a.B - 1;  // the last request whose first unit is not behind x0 (of empty ones the last has units)
+#pragma unroll 1
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.base[mid] <= x0) lo = mid; else hi = mid - 1;
+    }
+  }
+  auto unit_at = [&](int x, int& r) -> ChUnit {
+    while (a.base[r + 1] <= x) ++r;
+    ChUnit u;
+    u.r = r;
+    u.c0 = query_start(a, r);
+    const int n = query_start(a, r + 1) - u.c0, rows = n * a.G;
+    u.L = a.dead[r] ? 0 : __ldg(a.seq_lens + r);
+    u.shift = a.causal ? u.L - n : u.L;
+    u.row0 = (x - a.base[r]) * kChUnitRows;
+    u.rows = min(kChUnitRows, rows - u.row0);
+    u.tokens = seen(u, quotient(u.row0 + u.rows - 1, a.by_g));
+    return u;
+  };
+  int mine = 0, r = lo;
+#pragma unroll 1
+  for (int x = x0; x < x1; ++x) mine += unit_cost(unit_at(x, r));
+  int T;
+  int y = block_scan(mine, T, s_sum);
+  r = lo;
+#pragma unroll 1
+  for (int x = x0; x < x1; ++x) {
+    ChUnit u = unit_at(x, r);
+    u.y = y;
+    a.unit[x] = u;
+    y += unit_cost(u);
+  }
+  __syncthreads();
+  // every CTA's range and first unit: the last one that starts at or before it
+  const int line = T * a.Hkv, share = line / a.ctas, more = line - share * a.ctas;
+#pragma unroll 1
+  for (int c = t; c <= a.ctas; c += kChPlanThreads) {
+    ChStart s = {0, 0, c * share + min(c, more), 0};
+    s.b1 = c < a.ctas ? (c + 1) * share + min(c + 1, more) : s.b0;
+    if (T > 0) {
+      s.h = s.b0 / T;
+      const int at = s.b0 - s.h * T;
+      int l = 0, h = units - 1;
+#pragma unroll 1
+      while (l < h) {
+        const int mid = (l + h + 1) >> 1;
+        if (a.unit[mid].y <= at) l = mid; else h = mid - 1;
+      }
+      s.unit = l;
+      if (c == 0) s.h = 0;
+    }
+    a.start[c] = s;
+  }
+}
+
+struct alignas(16) ChPiece {
+  ChUnit u;
+  int h, i0, i1, blocks;  // blocks [i0, i1) of the unit's
+  int qbuf;               // query buffer of a unit of one row tile
+  int t0;                 // parity of the blocks before, and tile of the first one of a unit of one row tile
+  int last;               // no piece: the end
+  int pad;
+  __device__ __forceinline__ bool pair() const { return u.rows > 128; }
+};
+struct alignas(16) ChSlot {
+  ChPiece piece;
+  int pages[32];  // of the first four blocks' tiles, -1 where the unit has none
+};
+static_assert(sizeof(ChSlot) == ChCfg::kPieceBytes, "slot of the piece ring");
+
+// The next piece of a CTA's range; units without tokens belong to the range that holds their place.
+struct ChCursor {
+  int x, h, units, T, b0, b1;
+  ChUnit u;
+};
+__device__ __forceinline__ bool next_piece(const ChArgs& a, ChCursor& c, ChPiece& p) {
+  for (;;) {
+    if (c.x == c.units) {
+      c.x = 0;
+      if (++c.h >= a.Hkv) return false;
+      c.u = load_unit(a.unit);
+    }
+    const int y = c.h * c.T + c.u.y;
+    if (y >= c.b1) return false;
+    p.u = c.u;
+    p.h = c.h;
+    p.blocks = blocks_of(c.u.tokens);
+    owned_blocks(c.u, y, c.b0, c.b1, p.i0, p.i1);
+    if (++c.x < c.units) c.u = load_unit(a.unit + c.x);
+    if (p.i0 < p.i1 || (p.blocks == 0 && y >= c.b0)) return true;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// products
+// ---------------------------------------------------------------------------
+// O += P V over half a block, P from tensor memory: a step is 16 tokens, 8 columns of P and 4 KiB of V.
+#define CH_O_STEP(pcol, voff, acc)                                                                  \
+  "add.u32 p, %1, " #pcol ";\n\tadd.s64 b, %2, " #voff ";\n\t@e tcgen05.mma.cta_group::1.kind::f16" \
+  " [%0], [p], b, %3, " acc ";\n\t"
+__device__ __forceinline__ void issue_half_o(uint32_t d, uint32_t p, uint64_t vdesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, first, yes;\n\t.reg .b32 p;\n\t.reg .b64 b;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.u32 first, %4, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t" CH_O_STEP(0, 0, "first") CH_O_STEP(8, 256, "yes")
+          CH_O_STEP(16, 512, "yes") CH_O_STEP(24, 768, "yes") "}" ::"r"(d),
+      "r"(p), "l"(vdesc), "r"(kTcOF16), "r"(acc)
+      : "memory");
+}
+
+// 16 consecutive columns of this thread's tensor memory lane and their largest value (a NaN counts only among
+// NaNs), not waited for.
+__device__ __forceinline__ void tmem_ld16_max(uint32_t taddr, uint32_t* r, float& top) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %16, [%17];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=f"(top)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16]; "
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16}; "
+      ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Keeps the 64 registers' uses behind the wait.
+__device__ __forceinline__ void tmem_settle64(uint32_t (&r)[64]) {
+  tmem_wait_ld();
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
-      const uint8_t* const krow = block + (4 * (g >> 1) + (g & 1) + 2 * nb) * kChDim + c * 16;
+  for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// 32 bytes of bf16: a whole sector from one thread.
+__device__ __forceinline__ void st_global_u8(uint16_t* dst, const uint32_t (&x)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
+// The first n bytes (of 4) of a word.
+__device__ __forceinline__ uint32_t first_bytes(int n) {
+  return n <= 0 ? 0u : n >= 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+}
+// The bytes [from, to) of x that hold an e4m3 NaN, as 0xFF.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t x, int from, int to) {
+  const uint32_t hit = ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  return (hit >> 7) * 255u & first_bytes(to) & ~first_bytes(from);
+}
+
+// 32 columns of O of a row tile (`mine`) and of the other one's (`other`, 128 columns on), joined.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32]; "
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void join_o(uint32_t to, bool mine, bool other, float f0, float f1, float (&x)[32]) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(krow + 64 * i));
-        const uint32_t kw[4] = {x.x, x.y, x.z, x.w};
+  for (int k = 0; k < 32; ++k) x[k] = 0.f;
+  uint32_t r[32];
+  if (mine) {
+    tmem_ld32(to, r);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t b0, b1;
-          e4m3x4_to_f16x4(kw[y], b0, b1);
-          mma_f16(s[nb], qa[4 * i + y], b0, b1);
+    for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(r[k]) * f0;
+  }
+  if (other) {
+    tmem_ld32(to + 128, r);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = fmaf(__uint_as_float(r[k]), f1, x[k]);
+  }
+}
+
+// A row's NaN values: of the tokens [from, to) of its request, those that some rows of its unit do not see.
+// bf16 (out) or fp32 (a partial).
+__device__ __noinline__ void poison_row(const ChArgs& a, int r, int h, int from, int to, uint16_t* out, float* part) {
+  const int tpp = a.page_size >> 4;
+#pragma unroll 1
+  for (int j = from; j < to; ++j) {
+    const int page = __ldg(a.page_table + static_cast<int64_t>(r) * a.max_pages + j / a.page_size);
+    if (page < 0 || page >= a.num_pages) continue;
+    const int64_t tile = (static_cast<int64_t>(page) * a.Hkv + h) * tpp + j % a.page_size / kChTile;
+    const uint8_t* const v = a.kv_pool + tile * 2 * kChTile * kChDim + kChTile * kChDim + j % kChTile;
+#pragma unroll 1
+    for (int d = 0; d < kChDim; ++d)
+      if ((v[d * kChTile] & 0x7F) == 0x7F) {
+        if (out != nullptr) out[d] = 0x7FFF;
+        if (part != nullptr) part[d] = __int_as_float(0x7fffffff);
+      }
+  }
+}
+
+__global__ void __launch_bounds__(kChThreads, 1)
+    prefill_attn_kernel(const ChArgs a, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap) {
+  using C = ChCfg;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* const sm = smem_raw;
+  const uint32_t sbase = smem_addr(sm);
+  if (sbase & 1023u) {  // (cannot happen: the array is aligned, and there is no other shared memory)
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusBadStart);
+    return;
+  }
+  const unsigned kFull = 0xffffffffu;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
+  volatile int* const s_failed = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 4);
+  volatile int* const s_turns = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 8);
+  volatile int* const s_nan = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 16);
+  ChSlot* const s_piece = reinterpret_cast<ChSlot*>(sm + C::kOffPiece);
+  float2* const s_scale = reinterpret_cast<float2*>(sm + C::kOffScale);
+  float* const s_mult = reinterpret_cast<float*>(sm + C::kOffMult);
+  auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8 * i; };
+  for (int i = threadIdx.x; i < C::kBars; i += kChThreads) {
+    int arrivals = 1;
+    if (i >= C::kBarKFree && i < C::kBarKFree + C::kKStages) arrivals = 2;           // both tiles' products
+    if (i >= C::kBarVFree && i < C::kBarVFree + C::kVStages) arrivals = 4;           // converting warps
+    if (i >= C::kBarReady && i < C::kBarReady + C::kV16Bufs) arrivals = 4;
+    if (i >= C::kBarUsed && i < C::kBarUsed + C::kV16Bufs) arrivals = 2;
+    if (i >= C::kBarP && i < C::kBarP + 4) arrivals = 4;                             // a tile's softmax warps
+    if (i >= C::kBarOFree && i < C::kBarOFree + 2) arrivals = 4;
+    if (i >= C::kBarQ && i < C::kBarQ + 2) arrivals = 4;                             // converting warps
+    if (i >= C::kBarQFree && i < C::kBarQFree + 2) arrivals = 10;                    // MMA and softmax warps
+    if (i >= C::kBarPieceFree && i < C::kBarPieceFree + kChPieces) arrivals = 16;    // every other warp; K's and V's half of one
+    if (i >= C::kBarScaleFree && i < C::kBarScaleFree + C::kScales) arrivals = 8;    // softmax warps
+    if (i == C::kBarJoin) arrivals = 4;
+    mbar_init(bar(i), arrivals);
+    fence_barrier_init();
+  }
+  if (threadIdx.x < C::kNan) s_nan[threadIdx.x] = 0;
+  if (threadIdx.x == 0) *s_failed = s_turns[0] = s_turns[1] = 0;
+  if (warp == kChMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();  // the plan is there
+  griddep_launch_dependents();
+  const uint32_t tmem = *s_tmem;
+  const int4 first = __ldcg(reinterpret_cast<const int4*>(a.start + blockIdx.x));
+  auto wait = [&](int i, uint32_t parity) { tc_wait(bar(i), parity & 1u, a.status, s_failed); };
+  uint32_t pn = 0;
+  auto take_piece = [&](ChPiece& p) -> bool {
+    wait(C::kBarPiece + pn % kChPieces, pn / kChPieces);
+    p = s_piece[pn % kChPieces].piece;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::kBarPieceFree + pn % kChPieces));
+    ++pn;
+    return __all_sync(kFull, p.last == 0 && !*s_failed);
+  };
+  if (first.z < first.w) {
+    ChPiece p;
+    const int tpp = a.page_size >> 4;
+    if (warp == kChPlanWarp) {
+      // ===================== pieces and scales, ahead of the other warps =====================
+      ChCursor cur;
+      cur.x = first.x;
+      cur.h = first.y;
+      cur.b0 = first.z;
+      cur.b1 = first.w;
+      cur.units = __ldcg(a.base + a.B);
+      cur.T = __ldcg(&a.start[a.ctas].b0) / a.Hkv;  // (the last range ends where the line does)
+      cur.u = load_unit(a.unit + cur.x);
+      int qbuf = 0, t0 = 0;
+      uint32_t j = 0;  // blocks whose scales are out
+      bool more = true;
+#pragma unroll 1
+      for (uint32_t n = 0; more; ++n) {
+        more = next_piece(a, cur, p);
+        if (!more) p.i0 = p.i1 = 0;
+        p.last = !more;
+        p.qbuf = qbuf;
+        qbuf ^= 1;
+        p.t0 = t0;
+        t0 ^= (p.i1 - p.i0) & 1;
+        const int32_t* const row = a.page_table + static_cast<int64_t>(more ? p.u.r : 0) * a.max_pages;
+        const int tiles = (p.u.tokens + kChTile - 1) / kChTile;
+        // the first blocks' pages: copies need not wait for the table, which may come from far
+        auto page_of = [&](int b) -> int {
+          const int tile = b * kChBlkTiles + lane;
+          return more && tile < min(tiles, p.i1 * kChBlkTiles) ? max(-1, __ldg(row + quotient(tile, a.by_tpp))) : -1;
+        };
+        int page = page_of(p.i0);
+        if (n >= kChPieces) wait(C::kBarPieceFree + n % kChPieces, n / kChPieces - 1);
+        ChSlot* const at = s_piece + n % kChPieces;
+        at->pages[lane] = page;
+        if (lane == 0) at->piece = p;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kBarPiece + n % kChPieces));
+#pragma unroll 1
+        for (int b = p.i0; b < p.i1; b += 4) {
+          const int tile = b * kChBlkTiles + lane;
+          uint32_t raw = 0;
+          if (page >= 0 && page < a.num_pages)
+            raw = __ldg(a.kv_scales + (static_cast<int64_t>(page) * a.Hkv + p.h) * tpp + tile - quotient(tile, a.by_tpp) * tpp);
+          if (b + 4 < p.i1) page = page_of(b + 4);
+          const float2 x = make_float2(exp2_int(scale_exponent(raw & 255u)), static_cast<float>(scale_exponent(raw >> 8)));
+#pragma unroll 1
+          for (int k = 0; k < 4 && b + k < p.i1; ++k, ++j) {
+            const uint32_t st = j % C::kScales;
+            if (j >= C::kScales) wait(C::kBarScaleFree + st, j / C::kScales - 1);
+            if (lane >> 3 == k) s_scale[st * kChBlkTiles + (lane & 7)] = x;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kBarScale + st));
+          }
+        }
+        if (*s_failed) more = false;
+      }
+    } else if (warp == kChLoadWarp) {
+      // ===================== K rows, V tiles into their rings =====================
+      // The lower half-warp copies K, the upper one V, each with its own piece and place (the rings drain
+      // at different times), in one loop that looks at both and waits for neither.  Lane c of a half
+      // copies box c of a block (zbox tiles, within a page).
+      const bool kw = lane < 16;
+      const unsigned group = kw ? 0xffffu : 0xffff0000u;
+      const bool leads = (lane & 15) == 0;
+      const uint64_t pol = l2_policy_evict_normal();  // (other units and CTAs read the same pages)
+      const int c = lane & 7;
+      const int box_t = c * a.zbox;  // first tile of the box in a block
+      const bool copies = c < kChBlkTiles / a.zbox && (lane & 8) == 0;
+      const uint32_t stages = kw ? C::kKStages : C::kVStages;
+      const uint32_t full = bar(kw ? C::kBarKFull : C::kBarVFull), free = bar(kw ? C::kBarKFree : C::kBarVFree);
+      const uint32_t ring = sbase + (kw ? C::kOffK : C::kOffV) + box_t * kChTile * kChDim;
+      const void* const map = kw ? &kmap : &vmap;
+      const int my = kw ? 0 : 16;
+      auto all_of_half = [&](bool x) -> bool { return (__ballot_sync(kFull, x) & group) == group; };
+      const int32_t* row = nullptr;
+      int i = 0, tiles = 0;
+      uint32_t j = 0, st = 0, round = 0, idle = 0;
+      bool have = false, done = false;
+      // pages of 16 tiles, one per lane of the half: of this block and the next (an even number of blocks
+      // into the piece), and of the two behind them, asked for two blocks before they are needed
+      int now = -1, then = -1;
+      while (!__all_sync(kFull, done)) {
+        ++idle;
+        if (all_of_half(!have && !done && mbar_test(bar(C::kBarPiece + pn % kChPieces), pn / kChPieces & 1))) {
+          const ChSlot& slot = s_piece[pn % kChPieces];
+          p = slot.piece;
+          then = slot.pages[16 + (lane & 15)];
+          now = slot.pages[lane & 15];
+          __syncwarp(group);
+          if (leads) mbar_arrive(bar(C::kBarPieceFree + pn % kChPieces));
+          ++pn;
+          have = p.i0 < p.i1;
+          done = p.last != 0;
+          i = p.i0;
+          row = a.page_table + static_cast<int64_t>(p.u.r) * a.max_pages;
+          tiles = (p.u.tokens + kChTile - 1) / kChTile;
+          idle = 0;
+        }
+        const bool goes = all_of_half(have && (round == 0 || mbar_test(free + 8 * st, (round - 1) & 1)));
+        if (goes) {
+          const int behind = i - p.i0;
+          if (behind > 0 && (behind & 1) == 0) {
+            now = then;
+            then = -1;
+            const int tile = (i + 2) * kChBlkTiles + (lane & 15);
+            if (tile < min(tiles, p.i1 * kChBlkTiles)) then = __ldg(row + quotient(tile, a.by_tpp));
+          }
+          const int tile = i * kChBlkTiles + box_t;
+          const int pg = __shfl_sync(group, now, (behind & 1) * 8 + box_t, 16);
+          const bool good = copies && tile < tiles && pg >= 0 && pg < a.num_pages;
+          const uint32_t boxes = __popc(__ballot_sync(group, good));
+          const uint32_t f = full + 8 * st;
+          if (leads) {
+            const uint32_t bytes = boxes * a.zbox * (kChTile * kChDim);
+            if (bytes == 0) mbar_arrive(f);
+            else mbar_arrive_expect_tx(f, bytes);
+          }
+          __syncwarp(group);
+          if (good)
+            tma_load_3d(ring + st * C::kKStage, map, 0, my,
+                        (pg * a.Hkv + p.h) * tpp + tile - quotient(tile, a.by_tpp) * tpp, f, pol);
+          if (++st == stages) st = 0, ++round;
+          ++j;
+          if (++i == p.i1) have = false;
+          idle = 0;
+        }
+        // (whoever waits for a copy gives up in time)
+        if (__any_sync(kFull, (idle & 255u) == 255u && *s_failed != 0)) done = true;
+      }
+      // every copy has landed before the CTA ends
+      if (leads) {
+#pragma unroll 1
+        for (uint32_t b = j > stages ? j - stages : 0; b < j; ++b)
+          mbar_wait(full + 8 * (b % stages), (b / stages) & 1, a.status);
+      }
+    } else if (warp >= kChVWarp && warp < kChVWarp + 4) {
+      // ===================== queries, and V blocks made ready for the MMA =====================
+      const int d = threadIdx.x - kChVWarp * 32, vw = warp - kChVWarp;  // this thread's dim
+      const uint32_t flip = a.sm_scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale's sign goes to the query
+      uint32_t j = 0, uses0 = 0, uses1 = 0;
+      while (take_piece(p)) {
+        const uint32_t piece = pn - 1;
+        if (d == 0) s_nan[(piece + C::kNan / 2) % C::kNan] = 0;
+        if (p.i0 == p.i1) continue;
+        // ---- queries: a row by eight lanes, 16 dims each; warp vw rows 32 vw .. of a tile
+        {
+          const bool pair = p.pair();
+          const int b0 = pair ? 0 : p.qbuf, n = pair ? 16 : 8;  // steps of four rows
+          const int c = lane & 7;
+          auto lrow_of = [&](int s) -> int { return (s >> 3) * 128 + 32 * vw + 4 * (s & 7) + (lane >> 3); };
+          auto fetch = [&](int s, uint4& x0, uint4& x1) {
+            const int lrow = lrow_of(s), row = p.u.row0 + lrow, t = quotient(row, a.by_g);
+            x0 = x1 = make_uint4(0, 0, 0, 0);
+            if (s < n && lrow < p.u.rows) {
+              const uint4* const src = reinterpret_cast<const uint4*>(
+                  a.q + (static_cast<int64_t>(p.u.c0 + t) * a.Hq + p.h * a.G + row - t * a.G) * kChDim + 16 * c);
+              x0 = __ldg(src);
+              x1 = __ldg(src + 1);
+            }
+          };
+          uint4 x[3][2];
+#pragma unroll
+          for (int s = 0; s < 3; ++s) fetch(s, x[s][0], x[s][1]);
+#pragma unroll 1
+          for (int s = 0; s < n; ++s) {
+            const int buf = b0 + (s >> 3);
+            if ((s & 7) == 0) {
+              const uint32_t u = buf ? uses1 : uses0;
+              if (u > 0) wait(C::kBarQFree + buf, u - 1);
+              if (buf) ++uses1; else ++uses0;
+            }
+            const uint32_t w[8] = {x[0][0].x ^ flip, x[0][0].y ^ flip, x[0][0].z ^ flip, x[0][0].w ^ flip,
+                                   x[0][1].x ^ flip, x[0][1].y ^ flip, x[0][1].z ^ flip, x[0][1].w ^ flip};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              x[0][i] = x[1][i];
+              x[1][i] = x[2][i];
+            }
+            fetch(s + 3, x[2][0], x[2][1]);
+            uint32_t top = 0;  // largest |q|: bf16 magnitudes order as integers
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+            // q 2^e has its largest value in [128, 256): e = 134 - that value's exponent
+            const int ex = static_cast<int>(top >> 7);
+            const int e = ex == 0 ? (top == 0 ? 0 : 126) : min(max(134 - ex, -126), 126);
+            const float up = exp2_int(e);
+            uint32_t u[4], v[4];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float q0 = __uint_as_float(w[k] << 16) * up, q1 = __uint_as_float(w[k] & 0xFFFF0000u) * up;
+              const uint32_t y = f32x2_to_e4m3x2(q0, q1);
+              const float2 f = e4m3x2_to_float2(y);
+              const uint32_t z = f32x2_to_e4m3x2(q0 - f.x, q1 - f.y);
+              if (k & 1) {
+                u[k >> 1] |= y << 16;
+                v[k >> 1] |= z << 16;
+              } else {
+                u[k >> 1] = y;
+                v[k >> 1] = z;
+              }
+            }
+            const int row = lrow_of(s) & 127;
+            uint8_t* const dst = sm + buf * C::kQTile + row * 128 + ((c ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4*>(dst + 16384) = make_uint4(v[0], v[1], v[2], v[3]);
+            if (c == 0)
+              s_mult[buf * 128 + row] = ex == 255 ? __int_as_float(0x7fffffff) : fabsf(a.sm_scale_log2) * exp2_int(-e);
+            if ((s & 7) == 7) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(C::kBarQ + buf));
+            }
+          }
+        }
+        const int least = seen(p.u, quotient(p.u.row0, a.by_g));  // tokens that every row sees
+#pragma unroll 1
+        for (int i = p.i0; i < p.i1; ++i, ++j) {
+          const int nv = min(kChBlk, p.u.tokens - i * kChBlk);
+          const uint32_t vs = j % C::kVStages, buf = j % C::kV16Bufs;
+          uint8_t* const v = sm + C::kOffV + vs * C::kVStage;
+          wait(C::kBarVFull + vs, j / C::kVStages);
+          const int tiles = (nv + kChTile - 1) / kChTile;
+          if (least < i * kChBlk + nv) {
+            // tokens that not every row sees: a NaN would reach the others
+            uint32_t hits = 0;
+#pragma unroll 1
+            for (int t = max(0, least - i * kChBlk) / kChTile; t < tiles; ++t) {
+              uint4* const at = reinterpret_cast<uint4*>(v + t * kChTile * kChDim + d * 16);
+              uint4 x = *at;
+              const int from = least - i * kChBlk - t * kChTile, to = nv - t * kChTile;  // (behind nv: zeroed below)
+              const uint32_t n0 = nan_bytes(x.x, from, to), n1 = nan_bytes(x.y, from - 4, to - 4),
+                             n2 = nan_bytes(x.z, from - 8, to - 8), n3 = nan_bytes(x.w, from - 12, to - 12);
+              if (n0 | n1 | n2 | n3) {
+                *at = make_uint4(x.x & ~n0, x.y & ~n1, x.z & ~n2, x.w & ~n3);
+                hits = 1;
+              }
+            }
+            if (hits) s_nan[piece % C::kNan] = 1;
+          }
+          if (j >= C::kV16Bufs) wait(C::kBarUsed + buf, j / C::kV16Bufs - 1);
+          uint8_t* const o = sm + C::kOffV16 + buf * C::kV16 + d * 16;
+#pragma unroll 2
+          for (int t = 0; t < tiles; ++t) {
+            // codes of dim d, tokens 16 t .. 16 t + 15, to two rows of 8 f16
+            const uint4 x = *reinterpret_cast<const uint4*>(v + t * kChTile * kChDim + d * 16);
+            uint32_t y[8];
+            e4m3x4_to_f16x4(x.x, y[0], y[1]);
+            e4m3x4_to_f16x4(x.y, y[2], y[3]);
+            e4m3x4_to_f16x4(x.z, y[4], y[5]);
+            e4m3x4_to_f16x4(x.w, y[6], y[7]);
+            uint4* const w = reinterpret_cast<uint4*>(o + t * kChTile * kChDim * 2);
+            w[0] = make_uint4(y[0], y[1], y[2], y[3]);
+            w[128] = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+          if (nv < kChBlk) {  // f16 of token k, dim d: rows of 8 tokens, 2 KiB apart
+#pragma unroll 1
+            for (int k = nv; k & 63; k = (k | 7) + 1)
+              for (uint8_t* e = o + (k >> 3) * 2048 + (k & 7) * 2; e < o + (k >> 3) * 2048 + 16; e += 2)
+                *reinterpret_cast<uint16_t*>(e) = 0;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(C::kBarReady + buf));
+            mbar_arrive(bar(C::kBarVFree + vs));
+          }
+        }
+      }
+    } else if (warp == kChMmaWarp || warp == kChMmaWarp + 1) {
+      // ===================== MMA issue, a warp per row tile =====================
+      // The warp runs as one, an elected lane issues.  A tile's products alternate: S of a block, PV of the
+      // same block in halves as the softmax hands P over, S of the next (which overwrites S and P: the
+      // products of one thread run in order).  While a tile's softmax runs the other tile has the tensor
+      // cores; on a unit of both tiles the warps take turns (PV and the next S), or else the two would run
+      // in step.  All waits of a turn come before it, and turns are counted in shared memory, not by a
+      // barrier (no result hangs on it, a turn not seen is gone without).
+      //
+      // On a unit of one row tile block j belongs to tile j mod 2.  A barrier's parity tells neighbouring
+      // phases apart, no others, so a warp has to see every phase of a barrier it waits for: slots are even
+      // in number, and a tile has its own and sees all of theirs.
+      const int t = warp - kChMmaWarp;
+      const uint32_t base = __reduce_max_sync(kFull, sbase), tm = __reduce_max_sync(kFull, tmem);  // uniform registers
+      const uint32_t bars = base + C::kOffBars;
+      const uint64_t qdesc = smem_desc(base, 16, 1024, 2), kdesc = smem_desc(base + C::kOffK, 16, 1024, 2);
+      // V, 16 tokens a step: two columns of core matrices (8 dims x 8 tokens, 128 B apart along the dims, 2 KiB along the tokens)
+      const uint64_t vdesc = smem_desc(base + C::kOffV16, 2048, 128, 0);
+      uint32_t j0 = 0, n0 = 0, n1 = 0, begun = 0, uses0 = 0, uses1 = 0;
+      int turns = 0;
+      const uint32_t turn_of = base + C::kOffMisc + 8 + 4 * (t ^ 1);
+      static_assert(C::kKStages % 2 == 0 && C::kV16Bufs == 2 && C::kScales % 2 == 0, "slots that tiles own");
+      while (take_piece(p)) {
+        const int pair_in = __any_sync(kFull, p.pair());
+        const uint32_t nb = __reduce_max_sync(kFull, p.i1 - p.i0), qb = __reduce_max_sync(kFull, p.qbuf);
+        const uint32_t halves = __reduce_max_sync(kFull, max(0, p.u.tokens - p.i0 * kChBlk + 63) / 64);  // of the piece, and behind it
+        if (nb == 0) continue;
+        const uint32_t step = pair_in ? 1 : 2;
+        if (pair_in || qb == 0) wait(C::kBarQ, uses0++);
+        if (pair_in || qb == 1) wait(C::kBarQ + 1, uses1++);
+        const uint64_t qd = qdesc + (pair_in ? t : qb) * (C::kQTile >> 4);
+        bool begins = true;
+#pragma unroll 1
+        for (uint32_t i = pair_in ? 0 : (j0 ^ t) & 1; i < nb + step; i += step) {
+          // PV of this tile's block before, S of block i: what they need first, then the turn
+          const bool pair = varying(pair_in) != 0;
+          const uint32_t ks = (j0 + i) % C::kKStages, m = i - step, jm = j0 + m, vs = jm % C::kV16Bufs;
+          if (i < nb) wait(C::kBarKFull + ks, (j0 + i) / C::kKStages);
+          if (i >= step) {
+            wait(C::kBarReady + vs, jm / C::kV16Bufs);
+            if (begins && begun > 0) wait(C::kBarOFree + t, begun - 1);  // O of the piece before has been read
+            wait(C::kBarP + 2 * t, n0++);
+          }
+          tc_fence_after();
+          const uint64_t vd = vdesc + vs * (C::kV16 >> 4);
+          const uint32_t od = tm + 256 + t * 128, pd = tm + t * 128, acc = !begins;
+          const bool both = 2 * m + 1 < halves;
+          if (pair) {
+#pragma unroll 1
+            for (int spins = 0; load_shared(turn_of) - turns < t && spins < kChTurnSpins; ++spins) {
+            }
+          }
+          if (i >= step) {
+            issue_half_o(od, pd, vd, acc);
+            if (both) {
+              wait(C::kBarP + 2 * t + 1, n1++);
+              tc_fence_after();
+              issue_half_o(od, pd + 32, vd + 1024, 1);
+            }
+            begun += begins;
+            begins = false;
+          }
+          if (i < nb) issue_s<true>(tm + t * 128, qd, kdesc + ks * (C::kKStage >> 4));
+          if (pair) {
+            ++turns;
+            if (lane == 0) s_turns[t] = turns;
+          }
+          if (i < nb) {
+            commit_elected(bars + 8 * (C::kBarS + t));
+            commit_elected(bars + 8 * (C::kBarKFree + ks));
+            if (!pair) commit_elected(bars + 8 * (C::kBarKFree + ks));
+          }
+          if (i >= step) {
+            commit_elected(bars + 8 * (C::kBarO + t));
+            commit_elected(bars + 8 * (C::kBarUsed + vs));
+            if (!pair) commit_elected(bars + 8 * (C::kBarUsed + vs));  // for the other tile too
+          }
+        }
+        j0 += nb;
+        // the queries: this warp's S are done (of a pair it answers for both buffers: it has seen both filled)
+#pragma unroll 1
+        for (uint32_t b = pair_in ? 0 : qb; b <= (pair_in ? 1 : qb); ++b) commit_elected(bars + 8 * (C::kBarQFree + b));
+      }
+      // every product and every arrival it owes is done before the CTA ends
+      commit_elected(bars + 8 * (C::kBarDone + t));
+      mbar_wait(bar(C::kBarDone + t), 0, a.status);
+    } else {
+      // ===================== softmax, a thread per row =====================
+      const int t = warp >> 2;  // row tile
+      const int row = threadIdx.x & 127;
+      const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+      const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * 128 + lanes;
+      uint32_t ns = 0;              // S blocks taken of this tile
+      uint32_t j0 = 0;              // blocks of the pieces before
+      uint32_t uses[2] = {0, 0};    // query buffers taken
+      uint32_t joins = 0;
+      while (take_piece(p)) {
+        const bool pair = p.pair();
+        const int nb = p.i1 - p.i0;
+        const int lrow = pair ? t * 128 + row : row;  // row of the unit
+        const bool valid = lrow < p.u.rows;
+        const bool busy = lrow - lane < p.u.rows;     // some row of the warp's is
+        const int grow = p.u.row0 + min(lrow, p.u.rows - 1), token = quotient(grow, a.by_g);
+        const int limit = seen(p.u, token);
+        const int least = __reduce_min_sync(kFull, limit);  // tokens that every row of the warp sees
+        const int64_t orow = static_cast<int64_t>(p.u.c0 + token) * a.Hq + p.h * a.G + grow - token * a.G;
+        const int nan_slot = static_cast<int>((pn - 1) % C::kNan);
+        float m = -INFINITY, l = 0.f;
+        bool any = false;
+        if (nb > 0) {
+          const int buf = pair ? t : p.qbuf;
+          wait(C::kBarQ + buf, buf ? uses[1] : uses[0]);
+          if (pair || p.qbuf == 0) ++uses[0];
+          if (pair || p.qbuf == 1) ++uses[1];
+          const float mult = s_mult[buf * 128 + row];
+          __syncwarp();
+          // (of a pair each tile's warps answer for their own buffer, twice: they have seen no other filled)
+          if (lane <= (pair ? 1 : 0)) mbar_arrive(bar(C::kBarQFree + buf));
+          // ---- blocks
+#pragma unroll 1
+          for (int i = pair ? 0 : t ^ p.t0; i < nb; i += pair ? 1 : 2) {
+            const uint32_t js = j0 + i, st = js % C::kScales;
+            wait(C::kBarS + t, ns);
+            if (ns > 0) wait(C::kBarO + t, ns - 1);  // (over already: S came behind that product)
+            wait(C::kBarScale + st, js / C::kScales);
+            tc_fence_after();
+            const int at = (p.i0 + i) * kChBlk;
+            const int halves = p.u.tokens - at > 64 ? 2 : 1;  // (a half without tokens is left out)
+            const float2* const sc = s_scale + st * kChBlkTiles;
+            if (busy) {
+              if (least - at < 64 * halves) {
+                // columns that a row does not see: -inf, by a short loop over tensor memory (selects on
+                // registers would be a second copy of the code below, fetched anew each time)
+#pragma unroll 1
+                for (int k = max(0, least - at) / 16; k < 4 * halves; ++k) {
+                  uint32_t x[16];
+                  tmem_ld16(ts + 16 * k, x);
+                  const int left = limit - at - 16 * k;
+#pragma unroll
+                  for (int c = 0; c < 16; ++c) x[c] = c < left ? x[c] : 0xFF800000u;
+                  tmem_st16(ts + 16 * k, x);
+                }
+                tmem_wait_st();
+              }
+              // the second half's maximum, then the first half with its own
+              uint32_t s[64];
+              float mb = -INFINITY;
+#pragma unroll 1
+              for (int h = halves - 1; h >= 0; --h) {
+                float top[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) tmem_ld16_max(ts + 64 * h + 16 * g, s + 16 * g, top[g]);
+                tmem_settle64(s);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                  asm volatile("" : "+f"(top[g]));
+                  const float2 x = sc[4 * h + g];
+                  mb = fmaxf(mb, fmaf(top[g], at_least_min(mult * x.x), x.y));
+                }
+              }
+              if (__any_sync(kFull, mult != mult)) mb = mult != mult ? mult : mb;  // a NaN query's row is NaN
+              const bool grown = mb > m + kChGrow || (m == -INFINITY && mb != -INFINITY);
+              if (__any_sync(kFull, grown)) {
+                const float f = !grown ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - mb);
+                if (grown) m = mb;
+                l *= f;
+                if (any) {  // O of the blocks before
+#pragma unroll 1
+                  for (int c = 0; c < 8; ++c) tmem_scale16(to + 16 * c, f);
+                }
+              }
+              const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+              for (int h = 0; h < halves; ++h) {
+                if (h == 1) {
+                  float v[64];
+                  tmem_ld64(ts + 64, v);
+#pragma unroll
+                  for (int k = 0; k < 64; ++k) s[k] = __float_as_uint(v[k]);
+                }
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                  const float2 x = sc[4 * h + g];
+                  const float f = at_least_min(mult * x.x), b = x.y - ref;
+                  const float2 f2 = make_float2(f, f), b2 = make_float2(b, b);
+                  float2 sum = make_float2(0.f, 0.f);
+                  uint32_t w[8];
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) {
+                    float2 e = fma2(make_float2(__uint_as_float(s[16 * g + 2 * k]), __uint_as_float(s[16 * g + 2 * k + 1])), f2, b2);
+                    e.x = fast_exp2(e.x);
+                    e.y = fast_exp2(e.y);
+                    sum = add2(sum, e);
+                    w[k] = pack_f16x2(e.x, e.y);
+                  }
+                  tmem_st8(ts + 32 * h + 8 * g, w);  // over columns that have been read
+                  l = fmaf(sum.x + sum.y, exp2_int(-static_cast<int>(x.y)), l);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::kBarP + 2 * t + h));
+              }
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(bar(C::kBarP + 2 * t));
+                if (halves == 2) mbar_arrive(bar(C::kBarP + 2 * t + 1));
+              }
+            }
+            if (lane <= (pair ? 0 : 1)) mbar_arrive(bar(C::kBarScaleFree + st));
+            any = true;
+            ++ns;
+          }
+          if (any) {
+            wait(C::kBarO + t, ns - 1);
+            tc_fence_after();
+          }
+        }
+        j0 += nb;
+        // ---- results: a row's thread, of a unit of one row tile the one of tile 0
+        const bool whole = p.i0 == 0 && p.i1 == p.blocks;
+        const int64_t slot = static_cast<int64_t>(2 * blockIdx.x + (p.i0 == 0 ? 0 : 1)) * kChUnitRows + lrow;
+        float f0 = 1.f, f1 = 0.f;
+        bool other = false;  // tile 1's O counts too
+        if (!pair && nb > 0) {
+          other = (1 ^ p.t0) < nb;  // tile 1 has had a block
+          if (t == 1) {
+            if (any) {
+              // (to tile 0, by way of the workspace: the slot's places behind the unit's rows.  The next join's
+              // are written when O, which tile 0 reads behind these, has been freed.)
+              __stcg(a.part_ml + slot + 128, make_float2(m, l));
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(C::kBarJoin));
+            }
+            continue;
+          }
+          if (other) {
+            wait(C::kBarJoin, joins++);
+            tc_fence_after();
+            const float2 ml = __ldcg(a.part_ml + slot + 128);
+            const float M = ml.x > m || m == -INFINITY ? ml.x : m;
+            f0 = m == -INFINITY ? 0.f : fast_exp2(m - M);
+            f1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+            l = l * f0 + ml.y * f1;
+            m = M;
+          }
+        } else if (!pair && t == 1) {
+          continue;
+        }
+        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        const bool none = l == 0.f;
+        if (busy) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float x[32];
+            join_o(to + 32 * c, any, other, f0 * inv, f1 * inv, x);
+            if (valid) {
+              if (whole) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 16) {
+                  uint32_t y[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    y[i] = none ? 0u : pack_bf16x2(x[k + 2 * i], x[k + 2 * i + 1]);
+                  st_global_u8(a.out + orow * kChDim + 32 * c + k, y);
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                  float y[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) y[i] = none ? 0.f : x[k + i];
+                  st_global8(a.part_o + slot * kChDim + 32 * c + k, y);
+                }
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (any) mbar_arrive(bar(C::kBarOFree + t));
+          if (other) mbar_arrive(bar(C::kBarOFree + 1));
+        }
+        if (valid) {
+          if (s_nan[nan_slot] != 0) {
+            const int lo = max(seen(p.u, quotient(p.u.row0, a.by_g)), p.i0 * kChBlk), hi = min(limit, p.i1 * kChBlk);
+            poison_row(a, p.u.r, p.h, lo, hi, whole ? a.out + orow * kChDim : nullptr, whole ? nullptr : a.part_o + slot * kChDim);
+          }
+          if (!whole) a.part_ml[slot] = make_float2(m, l);
+          else if (a.lse != nullptr) a.lse[orow] = none ? -INFINITY : (m + __log2f(l)) * kChLn2;
         }
       }
     }
-    uint32_t p[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float e[4] = {s[0][2 * i], s[0][2 * i + 1], s[1][2 * i], s[1][2 * i + 1]};
-      float mx = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        e[k] = t * kChTile + 4 * c + k < limit[i] ? fmaf(e[k], mult[i] * km, static_cast<float>(ev)) : -INFINITY;
-        mx = fmaxf(mx, e[k]);
-      }
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-      const float mn = fmaxf(m[i], mx), f = m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - mn), ref = mn == -INFINITY ? 0.f : mn;
-      m[i] = mn;
-      l[i] *= f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        o[j][2 * i] *= f;
-        o[j][2 * i + 1] *= f;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) e[k] = fast_exp2(e[k] - ref);
-      l[i] = fmaf((e[0] + e[1]) + (e[2] + e[3]), exp2_int(-ev), l[i]);
-      p[0][i] = pack_f16x2(e[0], e[1]);
-      p[1][i] = pack_f16x2(e[2], e[3]);
-    }
-    const uint32_t pa[4] = {p[0][0], p[0][1], p[1][0], p[1][1]};
-    const int left = min(4, max(0, L - t * kChTile - 4 * c));
-    const uint32_t keep = left == 4 ? 0xFFFFFFFFu : (1u << (8 * left)) - 1u;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      uint32_t b0, b1;
-      e4m3x4_to_f16x4(__ldg(reinterpret_cast<const uint32_t*>(block + kChTile * kChDim + (8 * j + g) * kChTile + 4 * c)) & keep,
-                      b0, b1);
-      mma_f16(o[j], pa, b0, b1);
-    }
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(kFull, l[i], 1);
-    l[i] += __shfl_xor_sync(kFull, l[i], 2);
-    if (!valid[i]) continue;
-    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      *reinterpret_cast<uint32_t*>(a.out + at[i] * kChDim + 8 * j + 2 * c) = pack_bf16x2(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
-    if (c == 0 && a.lse != nullptr) a.lse[at[i]] = l[i] == 0.f ? -INFINITY : (m[i] + __log2f(l[i])) * kChLn2;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kChMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
+}
+
+// ---------------------------------------------------------------------------
+// merge
+// ---------------------------------------------------------------------------
+// kChMergeParts CTAs for each CTA of the products whose range ends within a unit that begins in it; a warp per
+// row: a lane finds one partial (its place, m, l), then all lanes add its O.
+__global__ void __launch_bounds__(32 * kChMergeWarps) prefill_merge_kernel(const ChArgs a) {
+  const unsigned kFull = 0xffffffffu;
+  const int lane = threadIdx.x & 31, c = blockIdx.x / kChMergeParts;
+  griddep_wait();
+  auto load_start = [&](int i) -> ChStart {
+    const int4 x = __ldcg(reinterpret_cast<const int4*>(a.start + i));
+    return {x.x, x.y, x.z, x.w};
+  };
+  const ChStart s0 = load_start(c), s1 = load_start(c + 1);
+  const int T = load_start(a.ctas).b0 / a.Hkv;
+  if (s0.b0 >= s0.b1 || s1.b0 >= s1.b1) return;
+  const ChUnit u = load_unit(a.unit + s1.unit);
+  const int y = s1.h * T + u.y, blocks = blocks_of(u.tokens);
+  int i0, i1;
+  owned_blocks(u, y, s0.b0, s0.b1, i0, i1);
+  if (i0 != 0 || i1 == 0 || i1 == blocks) return;
+#pragma unroll 1
+  for (int row = blockIdx.x % kChMergeParts * kChMergeWarps + (threadIdx.x >> 5); row < u.rows; row += kChMergeParts * kChMergeWarps) {
+    float M = -INFINITY, W = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool more = true;
+#pragma unroll 1
+    for (int base = c; more; base += 32) {
+      const int k = base + lane;
+      const int64_t slot = static_cast<int64_t>(2 * k + (k == c ? 0 : 1)) * kChUnitRows + row;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      int b = 0, e = blocks;
+      if (k < a.ctas) {
+        const ChStart s = load_start(k);
+        owned_blocks(u, y, s.b0, s.b1, b, e);
+        if (b < e) ml = __ldcg(a.part_ml + slot);
+      }
+      more = !__any_sync(kFull, k >= a.ctas || e == blocks);
+      float mx = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      const float mn = fmaxf(M, mx);
+      const bool has = ml.y != 0.f;  // (a NaN sum counts, whatever its maximum)
+      const float f = !has ? 0.f : ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - mn);
+      float ws = ml.y * f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(kFull, ws, o);
+      const float old = M == -INFINITY ? 0.f : fast_exp2(M - mn);
+      W = W * old + ws;
+      acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+      M = mn;
+      unsigned todo = __ballot_sync(kFull, has);
+#pragma unroll 1
+      while (todo) {
+        float fk[4];
+        float4 o[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int src = todo ? __ffs(todo) - 1 : 0;
+          const float fx = __shfl_sync(kFull, f, src);
+          const int64_t sx = __shfl_sync(kFull, slot, src);
+          fk[x] = todo ? fx : 0.f;
+          o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (todo) o[x] = __ldcg(reinterpret_cast<const float4*>(a.part_o + sx * kChDim) + lane);
+          todo &= todo - 1;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          acc = make_float4(fmaf(o[x].x, fk[x], acc.x), fmaf(o[x].y, fk[x], acc.y), fmaf(o[x].z, fk[x], acc.z),
+                            fmaf(o[x].w, fk[x], acc.w));
+      }
+    }
+    const bool none = W == 0.f;
+    const float inv = none ? 0.f : 1.f / W;
+    const int grow = u.row0 + row, token = quotient(grow, a.by_g);
+    const int64_t orow = static_cast<int64_t>(u.c0 + token) * a.Hq + y / T * a.G + grow - token * a.G;
+    reinterpret_cast<uint2*>(a.out + orow * kChDim)[lane] =
+        none ? make_uint2(0, 0) : make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0 && a.lse != nullptr) a.lse[orow] = none ? -INFINITY : (M + __log2f(W)) * kChLn2;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+constexpr int kChMaxDevices = 64;
+std::atomic<int> g_ch_ready[kChMaxDevices];
+
+int prepare_prefill(int dev) {
+  if (g_ch_ready[dev].load(std::memory_order_relaxed) > 0) return FPK_OK;
+  if (cudaFuncSetAttribute(prefill_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ChCfg::kSmem) != cudaSuccess)
+    return FPK_ECUDA;
+  g_ch_ready[dev].store(1, std::memory_order_relaxed);
+  return FPK_OK;
+}
+
+// Most units of a kv head.
+int64_t most_units(int64_t B, int64_t n_tokens, int64_t G) { return n_tokens * G / kChUnitRows + B; }
+
+struct ChLayout {
+  size_t base, dead, unit, start, ml, o, total;
+};
+ChLayout prefill_layout(int64_t B, int64_t n_tokens, int64_t G, int64_t ctas) {
+  auto up = [](int64_t x) { return (static_cast<size_t>(x) + 255) & ~static_cast<size_t>(255); };
+  ChLayout l;
+  l.base = 256;
+  l.dead = l.base + up((B + 1) * 4);
+  l.unit = l.dead + up(B * 4);
+  l.start = l.unit + up(most_units(B, n_tokens, G) * static_cast<int64_t>(sizeof(ChUnit)));
+  l.ml = l.start + up((ctas + 1) * static_cast<int64_t>(sizeof(ChStart)));
+  l.o = l.ml + up(2 * ctas * kChUnitRows * 8);
+  l.total = l.o + up(2 * ctas * kChUnitRows * kChDim * 4);
+  return l;
 }
 
 }  // namespace
@@ -180,7 +1204,10 @@ __global__ void __launch_bounds__(32 * kChWarps) prefill_attn_kernel(const ChArg
 
 extern "C" size_t fpk_prefill_workspace_bytes(int32_t B, int32_t n_tokens, int32_t Hq, int32_t Hkv, int32_t D) {
   if (B < 0 || n_tokens < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > fpk::kChGroupMax || D != fpk::kChDim) return 0;
-  return 256;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= fpk::kChMaxDevices) return 0;
+  const int ctas = fpk::device_sm_count(dev);
+  return ctas > 0 ? fpk::prefill_layout(B, n_tokens, Hq / Hkv, ctas).total : 0;
 }
 
 extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu_seqlens, int32_t n_tokens,
@@ -196,22 +1223,52 @@ extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu
     return FPK_EINVAL;
   const int G = Hq / Hkv;
   if (D != kChDim || G > kChGroupMax || page_size % kChTile != 0 || page_size > 256) return FPK_EUNSUPPORTED;
+  const int tpp = page_size / kChTile;
+  const int64_t tiles = static_cast<int64_t>(num_pages) * Hkv * tpp;
+  // tile numbers are 32-bit tensor-map coordinates; the work list's length is counted in 31 bits, rows are divided
+  // by reciprocals (2^28)
+  const int64_t width = (static_cast<int64_t>(max_pages) * page_size + kChBlk - 1) / kChBlk;
+  const int64_t units = most_units(B, n_tokens, G), longest = width * kChCostPair + kChStartPair;
+  if (tiles > 0x7fffffff || static_cast<int64_t>(n_tokens) * G >= (int64_t(1) << 28) || width > (int64_t(1) << 24) ||
+      longest > 0x7fffffff / ((units > 0 ? units : 1) * Hkv))
+    return FPK_EUNSUPPORTED;
   if (B == 0 || n_tokens == 0) return FPK_OK;
   if (!q || !cu_seqlens || !kv_pool || !kv_scales || !page_table || !seq_lens || !out || !workspace) return FPK_EINVAL;
   if (!aligned16(q) || !aligned16(kv_pool) || (reinterpret_cast<uintptr_t>(kv_scales) & 1u) != 0 ||
       (reinterpret_cast<uintptr_t>(out) & 31u) != 0 || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return FPK_EINVAL;
-  if (workspace_bytes < 256) return FPK_ENOSPC;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kChMaxDevices) return FPK_ECUDA;
+  const int ctas = device_sm_count(dev);
+  if (ctas <= 0) return FPK_ECUDA;
+  const ChLayout l = prefill_layout(B, n_tokens, G, ctas);
+  if (workspace_bytes < l.total) return FPK_ENOSPC;
+  const int st = prepare_prefill(dev);
+  if (st != FPK_OK) return st;
+  int zbox = 1;  // tiles per copy: a power of two that divides a page and a block
+  while (zbox < kChBlkTiles && tpp % (2 * zbox) == 0) zbox *= 2;
+  CUtensorMap kmap, vmap;
+  if (encode_pool_map(&kmap, kv_pool, tiles > 0 ? tiles : 1, true, false, zbox) != FPK_OK ||
+      encode_pool_map(&vmap, kv_pool, tiles > 0 ? tiles : 1, true, true, zbox) != FPK_OK)
+    return FPK_ECUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   ChArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.cu_seqlens = cu_seqlens;
-  a.kv_pool = kv_pool;
   a.kv_scales = reinterpret_cast<const uint16_t*>(kv_scales);
+  a.kv_pool = kv_pool;
   a.page_table = page_table;
   a.seq_lens = seq_lens;
   a.abort_mask = abort_mask;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.base = reinterpret_cast<int32_t*>(ws + l.base);
+  a.dead = reinterpret_cast<int32_t*>(ws + l.dead);
+  a.unit = reinterpret_cast<ChUnit*>(ws + l.unit);
+  a.start = reinterpret_cast<ChStart*>(ws + l.start);
+  a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
+  a.part_o = reinterpret_cast<float*>(ws + l.o);
   a.n_tokens = n_tokens;
   a.causal = causal != 0;
   a.B = B;
@@ -221,9 +1278,14 @@ extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu
   a.page_size = page_size;
   a.num_pages = num_pages;
   a.max_pages = max_pages;
+  a.ctas = ctas;
+  a.zbox = zbox;
+  a.by_g = G == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + G - 1) / G);
+  a.by_tpp = tpp == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + tpp - 1) / tpp);
   a.sm_scale_log2 = sm_scale * kChLog2e;
-  const int64_t places = static_cast<int64_t>(n_tokens) * G / kChRows + B;
-  if (places > 0x7fffffff || Hkv > 65535) return FPK_EUNSUPPORTED;
-  prefill_attn_kernel<<<dim3(static_cast<unsigned>(places), Hkv), 32 * kChWarps, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return checked_launch_status();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (launch_dependent(prefill_plan_kernel, 1, kChPlanThreads, 0, s, a) != FPK_OK ||
+      launch_dependent(prefill_attn_kernel, ctas, kChThreads, ChCfg::kSmem, s, a, kmap, vmap) != FPK_OK)
+    return FPK_ECUDA;
+  return ctas > 1 ? launch_dependent(prefill_merge_kernel, (ctas - 1) * kChMergeParts, 32 * kChMergeWarps, 0, s, a) : FPK_OK;
 }

@@ -207,3 +207,26 @@ def test_calls_share_a_workspace_and_repeat_their_bits():
         check(s, got, causal=True, rows=5)
         first = first or got
     assert np.array_equal(first[0], got[0]) and np.array_equal(first[1], got[1])
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(16, 2), (5, 5)])
+@pytest.mark.parametrize("where", [50, 200, 391])
+def test_nan_values_reach_only_rows_that_see_them(Hq, Hkv, where):
+    """V of one token is NaN in three dims, K of another wholly: rows before them are as without, rows behind are NaN."""
+    L, n, ps = 400, 390, 16
+    s = scene([L], [n], Hq=Hq, Hkv=Hkv, ps=ps, seed=where)
+    clean = run(s, causal=True)
+    page, t, slot = s["table"][0, where // ps], where % ps // TILE, where % TILE
+    dims = [0, 77, 127]
+    s["pool"][page, 0, t, 1].reshape(D, TILE)[dims, slot] = NAN
+    out, lse = run(s, causal=True)
+    sees = np.arange(n) + L - n >= where  # query i is token L - n + i
+    G = Hq // Hkv
+    assert np.array_equal(out[~sees], clean[0][~sees]) and np.array_equal(lse, clean[1])
+    assert np.array_equal(out[:, G:], clean[0][:, G:])
+    bad = np.isnan(out[sees][:, :G])
+    assert np.all(bad[..., dims]) and bad.sum() == bad[..., dims].size
+    s["pool"][page, 0, t, 0].reshape(TILE, D)[slot, 3] = NAN | 0x80
+    out, lse = run(s, causal=True)
+    assert np.array_equal(out[~sees], clean[0][~sees]) and np.array_equal(lse[~sees], clean[1][~sees])
+    assert np.all(np.isnan(out[sees][:, :G])) and np.all(np.isnan(lse[sees][:, :G])) and np.array_equal(lse[:, G:], clean[1][:, G:])
