@@ -19,9 +19,10 @@
 //
 // Piece pipeline (one CTA per SM, 16 warps), per block of 128 tokens:
 //   warp 15     finds the pieces and the blocks' scales ahead of the others
-//   warp 12     lands K rows (128-byte swizzle) and V tiles by tensor maps
-//   warps 8-11  V codes to f16 core matrices (exact); zeroes where no token lies;
-//               between two pieces, the next one's queries: q 2^e as two e4m3 parts
+//   warp 12     lands K rows (128-byte swizzle) by a tensor map
+//   warps 8-11  V codes from the pool to f16 core matrices (exact), a block ahead in
+//               registers, zeroes where no token lies; and, some after each block, the
+//               next piece's queries: q 2^e as two e4m3 parts
 //   warps 13, 14  issue S = Q K^T (e4m3, over both parts against the same K rows) and
 //               O += P V (f16) of row tile 0 and 1, tcgen05.mma of M = N = 128
 //   warps 0-3, 4-7  softmax of row tile 0 and 1, a thread per row: no shuffles.  P
@@ -105,33 +106,35 @@ struct ChArgs {
   float sm_scale_log2;
 };
 
+constexpr int kNanRow = -128;  // exponent of a row with a NaN or an infinity
+
 struct ChCfg {
   static constexpr int kQTile = 128 * 256;  // both parts of a tile's queries
-  static constexpr int kKStage = kChBlk * kChDim, kVStage = kKStage, kV16 = 2 * kVStage;
-  static constexpr int kKStages = 4, kVStages = 2, kV16Bufs = 2;
+  static constexpr int kKStage = kChBlk * kChDim, kV16 = 2 * kKStage;
+  static constexpr int kQTiles = 4;         // of this piece and the next
+  static constexpr int kKStages = 2, kV16Bufs = 2;
   static constexpr int kScales = 8;         // blocks whose scales are known
   static constexpr int kNan = 16;           // pieces with a flag of NaN values
   static constexpr int kPieceBytes = 64 + 32 * 4;
-  static constexpr int kOffK = 2 * kQTile;
-  static constexpr int kOffV = kOffK + kKStages * kKStage;
-  static constexpr int kOffV16 = kOffV + kVStages * kVStage;
+  static constexpr int kOffK = kQTiles * kQTile;
+  static constexpr int kOffV16 = kOffK + kKStages * kKStage;
   static constexpr int kOffPiece = kOffV16 + kV16Bufs * kV16;
-  static constexpr int kOffScale = kOffPiece + kChPieces * kPieceBytes;  // float4 [kScales][8]: K's factor, V's exponent, 1 / V's factor
-  static constexpr int kOffMult = kOffScale + kScales * kChBlkTiles * 8;
-  static constexpr int kOffBars = kOffMult + 2 * 128 * 4;
+  static constexpr int kOffScale = kOffPiece + kChPieces * kPieceBytes;  // float2 [kScales][8]: K's factor, V's exponent
+  static constexpr int kOffTile = kOffScale + kScales * kChBlkTiles * 8;  // int [kScales][8]: the pool's tiles, -1: none
+  static constexpr int kOffMult = kOffTile + kScales * kChBlkTiles * 4;
+  static constexpr int kOffBars = kOffMult + kQTiles * 128;
   static constexpr int kBarKFull = 0;
   static constexpr int kBarKFree = kBarKFull + kKStages;
-  static constexpr int kBarVFull = kBarKFree + kKStages;
-  static constexpr int kBarVFree = kBarVFull + kVStages;
-  static constexpr int kBarReady = kBarVFree + kVStages;       // converted V block
+  static constexpr int kBarReady = kBarKFree + kKStages;       // converted V block
   static constexpr int kBarUsed = kBarReady + kV16Bufs;        // .. read by the MMA
   static constexpr int kBarS = kBarUsed + kV16Bufs;            // [tile]
   static constexpr int kBarP = kBarS + 2;                      // [tile][half of the block]
-  static constexpr int kBarO = kBarP + 4;                      // [tile] a product added to O
-  static constexpr int kBarOFree = kBarO + 2;                  // [tile] O of a piece read
+  static constexpr int kBarO = kBarP + 4;                      // [tile] a block's product added to O
+  static constexpr int kBarHalf = kBarO + 2;                   // [tile] the first half's product added
+  static constexpr int kBarOFree = kBarHalf + 2;               // [tile] O of a piece read
   static constexpr int kBarQ = kBarOFree + 2;                  // [buffer] queries staged
-  static constexpr int kBarQFree = kBarQ + 2;                  // [buffer] queries of a piece read
-  static constexpr int kBarPiece = kBarQFree + 2;              // [kChPieces] piece known
+  static constexpr int kBarQFree = kBarQ + kQTiles;            // [buffer] queries of a piece read
+  static constexpr int kBarPiece = kBarQFree + kQTiles;        // [kChPieces] piece known
   static constexpr int kBarPieceFree = kBarPiece + kChPieces;  // [kChPieces] piece read by every warp
   static constexpr int kBarScale = kBarPieceFree + kChPieces;  // [kScales] a block's scales known
   static constexpr int kBarScaleFree = kBarScale + kScales;    // [kScales] .. read
@@ -139,7 +142,7 @@ struct ChCfg {
   static constexpr int kBarDone = kBarJoin + 1;                // [2] every MMA of a warp completed
   static constexpr int kBars = kBarDone + 2;
   static constexpr int kOffMisc = kOffBars + 8 * kBars;        // tensor memory base, failure flag, turns of the tiles, NaN flags
-  static constexpr int kSmem = kOffMisc + 16 + 4 * kNan;
+  static constexpr int kSmem = kOffMisc + 16 + kNan;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
 struct alignas(16) ChPiece {
   ChUnit u;
   int h, i0, i1, blocks;  // blocks [i0, i1) of the unit's
-  int qbuf;               // query buffer of a unit of one row tile
+  int qset;               // pair of query buffers: a tile's each, or the first for a unit of one row tile
   int t0;                 // parity of the blocks before, and tile of the first one of a unit of one row tile
   int last;               // no piece: the end
   int pad;
@@ -374,11 +377,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// Keeps the 64 registers' uses behind the wait.
-__device__ __forceinline__ void tmem_settle64(uint32_t (&r)[64]) {
+// Waits, and keeps the registers' uses behind the wait.
+__device__ __forceinline__ void tmem_settle64(uint32_t (&r)[64], float (&top)[4]) {
   tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < 64; ++i) asm volatile("" : "+r"(r[i]));
+  asm volatile("" : "+f"(top[0]), "+f"(top[1]), "+f"(top[2]), "+f"(top[3]));
 }
 
 // 32 bytes of bf16: a whole sector from one thread.
@@ -388,17 +392,48 @@ __device__ __forceinline__ void st_global_u8(uint16_t* dst, const uint32_t (&x)[
                : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* at, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+}
+
+// The e4m3 codes of four f16 values.
+__device__ __forceinline__ uint32_t f16x4_to_e4m3x4(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\tmov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "r"(x), "r"(y));
+  return r;
+}
+// The larger magnitudes of two pairs of bf16, signs apart; NaN if one is.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
 // The first n bytes (of 4) of a word.
 __device__ __forceinline__ uint32_t first_bytes(int n) {
   return n <= 0 ? 0u : n >= 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
 }
-// The bytes [from, to) of x that hold an e4m3 NaN, as 0xFF.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t x, int from, int to) {
+// The bytes of x from the n-th on that hold an e4m3 NaN, as 0xFF.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t x, int n) {
   const uint32_t hit = ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-  return (hit >> 7) * 255u & first_bytes(to) & ~first_bytes(from);
+  return (hit >> 7) * 255u & ~first_bytes(n);
 }
 
-// 32 columns of O of a row tile (`mine`) and of the other one's (`other`, 128 columns on), joined.
+// 16 bytes of the pool, which goes by: no line of L1 for it.
+__device__ __forceinline__ uint4 ld_stream(const uint8_t* at) {
+  uint4 x;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(at));
+  return x;
+}
+
+// 32 consecutive columns, waited for.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -411,19 +446,20 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void join_o(uint32_t to, bool mine, bool other, float f0, float f1, float (&x)[32]) {
+// 16 columns of O of a row tile (`mine`) and of the other one's (`other`, 128 columns on), joined.
+__device__ __forceinline__ void join_o(uint32_t to, bool mine, bool other, float f0, float f1, float (&x)[16]) {
 #pragma unroll
-  for (int k = 0; k < 32; ++k) x[k] = 0.f;
-  uint32_t r[32];
+  for (int k = 0; k < 16; ++k) x[k] = 0.f;
+  uint32_t r[16];
   if (mine) {
-    tmem_ld32(to, r);
+    tmem_ld16(to, r);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(r[k]) * f0;
+    for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(r[k]) * f0;
   }
   if (other) {
-    tmem_ld32(to + 128, r);
+    tmem_ld16(to + 128, r);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) x[k] = fmaf(__uint_as_float(r[k]), f1, x[k]);
+    for (int k = 0; k < 16; ++k) x[k] = fmaf(__uint_as_float(r[k]), f1, x[k]);
   }
 }
 
@@ -447,8 +483,7 @@ __device__ __noinline__ void poison_row(const ChArgs& a, int r, int h, int from,
 }
 
 __global__ void __launch_bounds__(kChThreads, 1)
-    prefill_attn_kernel(const ChArgs a, const __grid_constant__ CUtensorMap kmap,
-                        const __grid_constant__ CUtensorMap vmap) {
+    prefill_attn_kernel(const ChArgs a, const __grid_constant__ CUtensorMap kmap) {
   using C = ChCfg;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const sm = smem_raw;
@@ -462,23 +497,23 @@ __global__ void __launch_bounds__(kChThreads, 1)
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
   volatile int* const s_failed = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 4);
   volatile int* const s_turns = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 8);
-  volatile int* const s_nan = reinterpret_cast<volatile int*>(sm + C::kOffMisc + 16);
+  volatile uint8_t* const s_nan = sm + C::kOffMisc + 16;
   ChSlot* const s_piece = reinterpret_cast<ChSlot*>(sm + C::kOffPiece);
   float2* const s_scale = reinterpret_cast<float2*>(sm + C::kOffScale);
-  float* const s_mult = reinterpret_cast<float*>(sm + C::kOffMult);
+  int* const s_tile = reinterpret_cast<int*>(sm + C::kOffTile);
+  int8_t* const s_exp = reinterpret_cast<int8_t*>(sm + C::kOffMult);  // [buffer][row] e of the queries; kNanRow
   auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8 * i; };
   for (int i = threadIdx.x; i < C::kBars; i += kChThreads) {
     int arrivals = 1;
     if (i >= C::kBarKFree && i < C::kBarKFree + C::kKStages) arrivals = 2;           // both tiles' products
-    if (i >= C::kBarVFree && i < C::kBarVFree + C::kVStages) arrivals = 4;           // converting warps
-    if (i >= C::kBarReady && i < C::kBarReady + C::kV16Bufs) arrivals = 4;
+    if (i >= C::kBarReady && i < C::kBarReady + C::kV16Bufs) arrivals = 4;           // converting warps
     if (i >= C::kBarUsed && i < C::kBarUsed + C::kV16Bufs) arrivals = 2;
     if (i >= C::kBarP && i < C::kBarP + 4) arrivals = 4;                             // a tile's softmax warps
     if (i >= C::kBarOFree && i < C::kBarOFree + 2) arrivals = 4;
-    if (i >= C::kBarQ && i < C::kBarQ + 2) arrivals = 4;                             // converting warps
-    if (i >= C::kBarQFree && i < C::kBarQFree + 2) arrivals = 10;                    // MMA and softmax warps
-    if (i >= C::kBarPieceFree && i < C::kBarPieceFree + kChPieces) arrivals = 16;    // every other warp; K's and V's half of one
-    if (i >= C::kBarScaleFree && i < C::kBarScaleFree + C::kScales) arrivals = 8;    // softmax warps
+    if (i >= C::kBarQ && i < C::kBarQ + C::kQTiles) arrivals = 4;                             // converting warps
+    if (i >= C::kBarQFree && i < C::kBarQFree + C::kQTiles) arrivals = 10;                    // MMA and softmax warps
+    if (i >= C::kBarPieceFree && i < C::kBarPieceFree + kChPieces) arrivals = 15;    // every other warp
+    if (i >= C::kBarScaleFree && i < C::kBarScaleFree + C::kScales) arrivals = 12;   // softmax and converting warps
     if (i == C::kBarJoin) arrivals = 4;
     mbar_init(bar(i), arrivals);
     fence_barrier_init();
@@ -519,7 +554,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       cur.units = __ldcg(a.base + a.B);
       cur.T = __ldcg(&a.start[a.ctas].b0) / a.Hkv;  // (the last range ends where the line does)
       cur.u = load_unit(a.unit + cur.x);
-      int qbuf = 0, t0 = 0;
+      int qset = 0, t0 = 0;
       uint32_t j = 0;  // blocks whose scales are out
       bool more = true;
 #pragma unroll 1
@@ -527,8 +562,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
         more = next_piece(a, cur, p);
         if (!more) p.i0 = p.i1 = 0;
         p.last = !more;
-        p.qbuf = qbuf;
-        qbuf ^= 1;
+        p.qset = qset;
+        qset ^= 1;
         p.t0 = t0;
         t0 ^= (p.i1 - p.i0) & 1;
         const int32_t* const row = a.page_table + static_cast<int64_t>(more ? p.u.r : 0) * a.max_pages;
@@ -539,6 +574,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
           return more && tile < min(tiles, p.i1 * kChBlkTiles) ? max(-1, __ldg(row + quotient(tile, a.by_tpp))) : -1;
         };
         int page = page_of(p.i0);
+        if (more && p.i0 < p.i1) {
+          // its queries, into L2: a group's heads of each token lie together
+          const int first = quotient(p.u.row0, a.by_g), last = quotient(p.u.row0 + p.u.rows - 1, a.by_g);
+#pragma unroll 1
+          for (int i = first + lane; i <= last; i += 32)
+            prefetch_l2(a.q + (static_cast<int64_t>(p.u.c0 + i) * a.Hq + p.h * a.G) * kChDim, a.G * kChDim * 2);
+        }
         if (n >= kChPieces) wait(C::kBarPieceFree + n % kChPieces, n / kChPieces - 1);
         ChSlot* const at = s_piece + n % kChPieces;
         at->pages[lane] = page;
@@ -549,15 +591,23 @@ __global__ void __launch_bounds__(kChThreads, 1)
         for (int b = p.i0; b < p.i1; b += 4) {
           const int tile = b * kChBlkTiles + lane;
           uint32_t raw = 0;
-          if (page >= 0 && page < a.num_pages)
-            raw = __ldg(a.kv_scales + (static_cast<int64_t>(page) * a.Hkv + p.h) * tpp + tile - quotient(tile, a.by_tpp) * tpp);
+          int place = -1;
+          if (page >= 0 && page < a.num_pages) {
+            place = (page * a.Hkv + p.h) * tpp + tile - quotient(tile, a.by_tpp) * tpp;
+            raw = __ldg(a.kv_scales + place);
+            // K and V of the tile, into L2: the copies of few rows' blocks follow one another faster than HBM answers
+            prefetch_l2(a.kv_pool + static_cast<int64_t>(place) * (2 * kChTile * kChDim), 2 * kChTile * kChDim);
+          }
           if (b + 4 < p.i1) page = page_of(b + 4);
           const float2 x = make_float2(exp2_int(scale_exponent(raw & 255u)), static_cast<float>(scale_exponent(raw >> 8)));
 #pragma unroll 1
           for (int k = 0; k < 4 && b + k < p.i1; ++k, ++j) {
             const uint32_t st = j % C::kScales;
             if (j >= C::kScales) wait(C::kBarScaleFree + st, j / C::kScales - 1);
-            if (lane >> 3 == k) s_scale[st * kChBlkTiles + (lane & 7)] = x;
+            if (lane >> 3 == k) {
+              s_scale[st * kChBlkTiles + (lane & 7)] = x;
+              s_tile[st * kChBlkTiles + (lane & 7)] = place;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::kBarScale + st));
           }
@@ -565,49 +615,28 @@ __global__ void __launch_bounds__(kChThreads, 1)
         if (*s_failed) more = false;
       }
     } else if (warp == kChLoadWarp) {
-      // ===================== K rows, V tiles into their rings =====================
-      // The lower half-warp copies K, the upper one V, each with its own piece and place (the rings drain
-      // at different times), in one loop that looks at both and waits for neither.  Lane c of a half
-      // copies box c of a block (zbox tiles, within a page).
-      const bool kw = lane < 16;
-      const unsigned group = kw ? 0xffffu : 0xffff0000u;
-      const bool leads = (lane & 15) == 0;
+      // ===================== K rows into their ring =====================
+      // Lane c copies box c of a block (zbox tiles, within a page).
       const uint64_t pol = l2_policy_evict_normal();  // (other units and CTAs read the same pages)
-      const int c = lane & 7;
-      const int box_t = c * a.zbox;  // first tile of the box in a block
-      const bool copies = c < kChBlkTiles / a.zbox && (lane & 8) == 0;
-      const uint32_t stages = kw ? C::kKStages : C::kVStages;
-      const uint32_t full = bar(kw ? C::kBarKFull : C::kBarVFull), free = bar(kw ? C::kBarKFree : C::kBarVFree);
-      const uint32_t ring = sbase + (kw ? C::kOffK : C::kOffV) + box_t * kChTile * kChDim;
-      const void* const map = kw ? &kmap : &vmap;
-      const int my = kw ? 0 : 16;
-      auto all_of_half = [&](bool x) -> bool { return (__ballot_sync(kFull, x) & group) == group; };
-      const int32_t* row = nullptr;
-      int i = 0, tiles = 0;
-      uint32_t j = 0, st = 0, round = 0, idle = 0;
-      bool have = false, done = false;
-      // pages of 16 tiles, one per lane of the half: of this block and the next (an even number of blocks
-      // into the piece), and of the two behind them, asked for two blocks before they are needed
-      int now = -1, then = -1;
-      while (!__all_sync(kFull, done)) {
-        ++idle;
-        if (all_of_half(!have && !done && mbar_test(bar(C::kBarPiece + pn % kChPieces), pn / kChPieces & 1))) {
-          const ChSlot& slot = s_piece[pn % kChPieces];
-          p = slot.piece;
-          then = slot.pages[16 + (lane & 15)];
-          now = slot.pages[lane & 15];
-          __syncwarp(group);
-          if (leads) mbar_arrive(bar(C::kBarPieceFree + pn % kChPieces));
-          ++pn;
-          have = p.i0 < p.i1;
-          done = p.last != 0;
-          i = p.i0;
-          row = a.page_table + static_cast<int64_t>(p.u.r) * a.max_pages;
-          tiles = (p.u.tokens + kChTile - 1) / kChTile;
-          idle = 0;
-        }
-        const bool goes = all_of_half(have && (round == 0 || mbar_test(free + 8 * st, (round - 1) & 1)));
-        if (goes) {
+      const int box_t = (lane & 7) * a.zbox;  // first tile of the box in a block
+      const bool copies = lane < kChBlkTiles / a.zbox;
+      uint32_t j = 0;
+      for (;;) {
+        wait(C::kBarPiece + pn % kChPieces, pn / kChPieces);
+        const ChSlot& slot = s_piece[pn % kChPieces];
+        p = slot.piece;
+        // pages of 16 tiles, one per lane of a half-warp: of this block and the next (an even number of blocks
+        // into the piece), and of the two behind them, asked for two blocks before they are needed
+        int now = slot.pages[lane & 15], then = slot.pages[16 + (lane & 15)];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kBarPieceFree + pn % kChPieces));
+        ++pn;
+        if (__any_sync(kFull, p.last != 0 || *s_failed)) break;
+        const int32_t* const row = a.page_table + static_cast<int64_t>(p.u.r) * a.max_pages;
+        const int tiles = (p.u.tokens + kChTile - 1) / kChTile;
+#pragma unroll 1
+        for (int i = p.i0; i < p.i1; ++i, ++j) {
+          const uint32_t st = j % C::kKStages, f = bar(C::kBarKFull + st);
           const int behind = i - p.i0;
           if (behind > 0 && (behind & 1) == 0) {
             now = then;
@@ -616,165 +645,217 @@ __global__ void __launch_bounds__(kChThreads, 1)
             if (tile < min(tiles, p.i1 * kChBlkTiles)) then = __ldg(row + quotient(tile, a.by_tpp));
           }
           const int tile = i * kChBlkTiles + box_t;
-          const int pg = __shfl_sync(group, now, (behind & 1) * 8 + box_t, 16);
+          const int pg = __shfl_sync(kFull, now, (behind & 1) * 8 + box_t, 16);
           const bool good = copies && tile < tiles && pg >= 0 && pg < a.num_pages;
-          const uint32_t boxes = __popc(__ballot_sync(group, good));
-          const uint32_t f = full + 8 * st;
-          if (leads) {
-            const uint32_t bytes = boxes * a.zbox * (kChTile * kChDim);
-            if (bytes == 0) mbar_arrive(f);
-            else mbar_arrive_expect_tx(f, bytes);
+          const uint32_t boxes = __popc(__ballot_sync(kFull, good));
+          if (j >= C::kKStages) wait(C::kBarKFree + st, j / C::kKStages - 1);
+          if (lane == 0) {
+            if (boxes == 0) mbar_arrive(f);
+            else mbar_arrive_expect_tx(f, boxes * a.zbox * (kChTile * kChDim));
           }
-          __syncwarp(group);
+          __syncwarp();
           if (good)
-            tma_load_3d(ring + st * C::kKStage, map, 0, my,
+            tma_load_3d(sbase + C::kOffK + st * C::kKStage + box_t * kChTile * kChDim, &kmap, 0, 0,
                         (pg * a.Hkv + p.h) * tpp + tile - quotient(tile, a.by_tpp) * tpp, f, pol);
-          if (++st == stages) st = 0, ++round;
-          ++j;
-          if (++i == p.i1) have = false;
-          idle = 0;
         }
-        // (whoever waits for a copy gives up in time)
-        if (__any_sync(kFull, (idle & 255u) == 255u && *s_failed != 0)) done = true;
       }
       // every copy has landed before the CTA ends
-      if (leads) {
+      if (lane == 0) {
 #pragma unroll 1
-        for (uint32_t b = j > stages ? j - stages : 0; b < j; ++b)
-          mbar_wait(full + 8 * (b % stages), (b / stages) & 1, a.status);
+        for (uint32_t b = j > C::kKStages ? j - C::kKStages : 0; b < j; ++b)
+          mbar_wait(bar(C::kBarKFull + b % C::kKStages), (b / C::kKStages) & 1, a.status);
       }
     } else if (warp >= kChVWarp && warp < kChVWarp + 4) {
       // ===================== queries, and V blocks made ready for the MMA =====================
       const int d = threadIdx.x - kChVWarp * 32, vw = warp - kChVWarp;  // this thread's dim
-      const uint32_t flip = a.sm_scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale's sign goes to the query
-      uint32_t j = 0, uses0 = 0, uses1 = 0;
-      while (take_piece(p)) {
-        const uint32_t piece = pn - 1;
-        if (d == 0) s_nan[(piece + C::kNan / 2) % C::kNan] = 0;
-        if (p.i0 == p.i1) continue;
-        // ---- queries: a row by eight lanes, 16 dims each; warp vw rows 32 vw .. of a tile
-        {
-          const bool pair = p.pair();
-          const int b0 = pair ? 0 : p.qbuf, n = pair ? 16 : 8;  // steps of four rows
-          const int c = lane & 7;
-          auto lrow_of = [&](int s) -> int { return (s >> 3) * 128 + 32 * vw + 4 * (s & 7) + (lane >> 3); };
-          auto fetch = [&](int s, uint4& x0, uint4& x1) {
-            const int lrow = lrow_of(s), row = p.u.row0 + lrow, t = quotient(row, a.by_g);
-            x0 = x1 = make_uint4(0, 0, 0, 0);
-            if (s < n && lrow < p.u.rows) {
-              const uint4* const src = reinterpret_cast<const uint4*>(
-                  a.q + (static_cast<int64_t>(p.u.c0 + t) * a.Hq + p.h * a.G + row - t * a.G) * kChDim + 16 * c);
-              x0 = __ldg(src);
-              x1 = __ldg(src + 1);
+      const int c = lane & 7;
+      const float sign = a.sm_scale_log2 < 0.f ? -1.f : 1.f;  // a negative scale's sign goes to the query
+      uint32_t j = 0, used = 0, phases = 0;  // V blocks; query buffers used before, and the parities of their frees
+      // The piece whose blocks are converted (i .. p.i1 to go), and the next one, whose queries are: steps at .. n of
+      // four rows (eight lanes a row, 16 dims each; warp vw rows 32 vw .. of a tile).
+      ChPiece next;
+      p.i0 = p.i1 = 0;
+      int i = 0, at = 0, n = 0, least = 0;
+      uint32_t piece = 0;
+      bool known = false, ended = false;
+      uint4 x[kChBlkTiles];
+      auto fetch = [&](uint32_t b, int t) {
+        const int tile = s_tile[b % C::kScales * kChBlkTiles + t];
+        x[t] = make_uint4(0, 0, 0, 0);
+        if (tile >= 0)
+          x[t] = ld_stream(a.kv_pool + static_cast<int64_t>(tile) * (2 * kChTile * kChDim) + kChTile * kChDim + d * 16);
+      };
+      auto fetched = [&](uint32_t b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kBarScaleFree + b % C::kScales));
+      };
+      for (;;) {
+        if (i < p.i1) {
+          // ---- V: this thread's dim of a block's tiles, the next block's on their way while one is converted
+          const int nv = min(kChBlk, p.u.tokens - i * kChBlk), first_hidden = least - i * kChBlk;
+          const uint32_t buf = j % C::kV16Bufs;
+          const bool more = i + 1 < p.i1;
+          if (nv < kChBlk || first_hidden < kChBlk) {
+            // codes behind the last token: 0; and NaN in tokens that not every row sees (they would reach the others)
+            uint32_t hits = 0;
+#pragma unroll
+            for (int t = 0; t < kChBlkTiles; ++t) {
+              uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int tok = 16 * t + 4 * k;
+                w[k] &= first_bytes(nv - tok);
+                const uint32_t nans = nan_bytes(w[k], first_hidden - tok);
+                w[k] &= ~nans;
+                hits |= nans;
+              }
+              x[t] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (hits) s_nan[piece % C::kNan] = 1;
+          }
+          if (more) wait(C::kBarScale + (j + 1) % C::kScales, (j + 1) / C::kScales);
+          if (j >= C::kV16Bufs) wait(C::kBarUsed + buf, j / C::kV16Bufs - 1);
+          uint8_t* const o = sm + C::kOffV16 + buf * C::kV16 + d * 16;
+#pragma unroll
+          for (int t = 0; t < kChBlkTiles; ++t) {
+            // codes of dim d, tokens 16 t .. 16 t + 15, to two rows of 8 f16
+            uint32_t y[8];
+            e4m3x4_to_f16x4(x[t].x, y[0], y[1]);
+            e4m3x4_to_f16x4(x[t].y, y[2], y[3]);
+            e4m3x4_to_f16x4(x[t].z, y[4], y[5]);
+            e4m3x4_to_f16x4(x[t].w, y[6], y[7]);
+            uint4* const w = reinterpret_cast<uint4*>(o + t * kChTile * kChDim * 2);
+            w[0] = make_uint4(y[0], y[1], y[2], y[3]);
+            w[128] = make_uint4(y[4], y[5], y[6], y[7]);
+            if (more) fetch(j + 1, t);
+          }
+          fence_proxy_async_smem();
+          if (more) fetched(j + 1);
+          else __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kBarReady + buf));
+          ++i;
+          ++j;
+        }
+        // ---- the next piece, once it is known; it is waited for when there is nothing else to do
+        if (!known && (i == p.i1 || __all_sync(kFull, mbar_test(bar(C::kBarPiece + pn % kChPieces), pn / kChPieces & 1)))) {
+          ended = !take_piece(next);
+          known = true;
+          at = 0;
+          n = ended || next.i0 == next.i1 ? 0 : next.pair() ? 16 : 8;
+          if (d == 0) s_nan[(pn - 1 + C::kNan / 2) % C::kNan] = 0;
+        }
+        // ---- its queries, two steps at a time; each operation for all values before the next one: only the warp's
+        // own instructions hide their time
+        if (known && at < n) {
+          const int row0 = next.u.row0 + 32 * vw + (lane >> 3);  // of this lane: step s has row0 + 128 (s / 8) + 4 (s % 8)
+          const int rows = next.u.row0 + next.u.rows;
+          const uint16_t* const src = a.q + (static_cast<int64_t>(next.u.c0) * a.Hq + next.h * a.G) * kChDim + 16 * c;
+          uint4 q[2][2];
+          auto ask = [&](int s, uint4& q0, uint4& q1) {
+            const int row = row0 + 128 * (s >> 3) + 4 * (s & 7);
+            q0 = q1 = make_uint4(0, 0, 0, 0);
+            if (s < n && row < rows) {
+              // (query token row / G, head row % G of the group)
+              const uint4* const at = reinterpret_cast<const uint4*>(
+                  src + static_cast<int64_t>(row + quotient(row, a.by_g) * (a.Hq - a.G)) * kChDim);
+              q0 = __ldg(at);
+              q1 = __ldg(at + 1);
             }
           };
-          uint4 x[3][2];
 #pragma unroll
-          for (int s = 0; s < 3; ++s) fetch(s, x[s][0], x[s][1]);
+          for (int k = 0; k < 2; ++k) ask(at + k, q[k][0], q[k][1]);
+          // all that are left behind the last block, else as many as leave none for then
+          const int left = p.i1 - i, end = left == 0 ? n : min(n, at + 2 * ((n - at + 2 * left - 1) / (2 * left)));
 #pragma unroll 1
-          for (int s = 0; s < n; ++s) {
-            const int buf = b0 + (s >> 3);
-            if ((s & 7) == 0) {
-              const uint32_t u = buf ? uses1 : uses0;
-              if (u > 0) wait(C::kBarQFree + buf, u - 1);
-              if (buf) ++uses1; else ++uses0;
-            }
-            const uint32_t w[8] = {x[0][0].x ^ flip, x[0][0].y ^ flip, x[0][0].z ^ flip, x[0][0].w ^ flip,
-                                   x[0][1].x ^ flip, x[0][1].y ^ flip, x[0][1].z ^ flip, x[0][1].w ^ flip};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              x[0][i] = x[1][i];
-              x[1][i] = x[2][i];
-            }
-            fetch(s + 3, x[2][0], x[2][1]);
-            uint32_t top = 0;  // largest |q|: bf16 magnitudes order as integers
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-            // q 2^e has its largest value in [128, 256): e = 134 - that value's exponent
-            const int ex = static_cast<int>(top >> 7);
-            const int e = ex == 0 ? (top == 0 ? 0 : 126) : min(max(134 - ex, -126), 126);
-            const float up = exp2_int(e);
-            uint32_t u[4], v[4];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float q0 = __uint_as_float(w[k] << 16) * up, q1 = __uint_as_float(w[k] & 0xFFFF0000u) * up;
-              const uint32_t y = f32x2_to_e4m3x2(q0, q1);
-              const float2 f = e4m3x2_to_float2(y);
-              const uint32_t z = f32x2_to_e4m3x2(q0 - f.x, q1 - f.y);
-              if (k & 1) {
-                u[k >> 1] |= y << 16;
-                v[k >> 1] |= z << 16;
-              } else {
-                u[k >> 1] = y;
-                v[k >> 1] = z;
+          for (; at < end; at += 2) {
+            const int buf = 2 * next.qset + (at >> 3);
+            if ((at & 7) == 0) {
+              if (used >> buf & 1) {
+                wait(C::kBarQFree + buf, phases >> buf & 1);
+                phases ^= 1u << buf;
               }
+              used |= 1u << buf;
             }
-            const int row = lrow_of(s) & 127;
-            uint8_t* const dst = sm + buf * C::kQTile + row * 128 + ((c ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
-            *reinterpret_cast<uint4*>(dst + 16384) = make_uint4(v[0], v[1], v[2], v[3]);
-            if (c == 0)
-              s_mult[buf * 128 + row] = ex == 255 ? __int_as_float(0x7fffffff) : fabsf(a.sm_scale_log2) * exp2_int(-e);
-            if ((s & 7) == 7) {
+            uint32_t r[2][8], top[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              r[k][0] = q[k][0].x, r[k][1] = q[k][0].y, r[k][2] = q[k][0].z, r[k][3] = q[k][0].w;
+              r[k][4] = q[k][1].x, r[k][5] = q[k][1].y, r[k][6] = q[k][1].z, r[k][7] = q[k][1].w;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) ask(at + 2 + k, q[k][0], q[k][1]);
+            // largest |q| of the row: bf16 magnitudes order as integers
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = max_abs_bf16x2(r[k][2 * e], r[k][2 * e + 1]);
+              x[0] = max_abs_bf16x2(max_abs_bf16x2(x[0], x[1]), max_abs_bf16x2(x[2], x[3]));
+              top[k] = max(x[0] & 0x7FFFu, x[0] >> 16 & 0x7FFFu);
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) top[k] = max(top[k], __shfl_xor_sync(kFull, top[k], o));
+            // q 2^e has its largest value in [128, 256): e = 134 - that value's exponent
+            int ex[2];
+            uint32_t w[2][8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              ex[k] = static_cast<int>(top[k] >> 7);
+              ex[k] = ex[k] == 255 ? kNanRow : ex[k] == 0 ? (top[k] == 0 ? 0 : 126) : min(max(134 - ex[k], -126), 126);
+              const float up = sign * exp2_int(max(ex[k], -126));
+#pragma unroll
+              for (int e = 0; e < 8; ++e)  // (f16 holds it but for what lies below 2^-24, which neither part would)
+                w[k][e] = pack_f16x2(__uint_as_float(r[k][e] << 16) * up, __uint_as_float(r[k][e] & 0xFFFF0000u) * up);
+            }
+            uint32_t y[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[k][e] = f16x4_to_e4m3x4(w[k][2 * e], w[k][2 * e + 1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t h0, h1;
+                e4m3x4_to_f16x4(y[k][e], h0, h1);
+                w[k][2 * e] = sub_f16x2(w[k][2 * e], h0);
+                w[k][2 * e + 1] = sub_f16x2(w[k][2 * e + 1], h1);
+              }
+            uint32_t z[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) z[k][e] = f16x4_to_e4m3x4(w[k][2 * e], w[k][2 * e + 1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int row = 32 * vw + 4 * ((at + k) & 7) + (lane >> 3);  // of the tile
+              uint8_t* const dst = sm + buf * C::kQTile + row * 128 + ((c ^ (row & 7)) << 4);
+              *reinterpret_cast<uint4*>(dst) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
+              *reinterpret_cast<uint4*>(dst + 16384) = make_uint4(z[k][0], z[k][1], z[k][2], z[k][3]);
+              if (c == 0) s_exp[buf * 128 + row] = static_cast<int8_t>(ex[k]);
+            }
+            if ((at & 7) == 6) {
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(C::kBarQ + buf));
             }
           }
         }
-        const int least = seen(p.u, quotient(p.u.row0, a.by_g));  // tokens that every row sees
-#pragma unroll 1
-        for (int i = p.i0; i < p.i1; ++i, ++j) {
-          const int nv = min(kChBlk, p.u.tokens - i * kChBlk);
-          const uint32_t vs = j % C::kVStages, buf = j % C::kV16Bufs;
-          uint8_t* const v = sm + C::kOffV + vs * C::kVStage;
-          wait(C::kBarVFull + vs, j / C::kVStages);
-          const int tiles = (nv + kChTile - 1) / kChTile;
-          if (least < i * kChBlk + nv) {
-            // tokens that not every row sees: a NaN would reach the others
-            uint32_t hits = 0;
-#pragma unroll 1
-            for (int t = max(0, least - i * kChBlk) / kChTile; t < tiles; ++t) {
-              uint4* const at = reinterpret_cast<uint4*>(v + t * kChTile * kChDim + d * 16);
-              uint4 x = *at;
-              const int from = least - i * kChBlk - t * kChTile, to = nv - t * kChTile;  // (behind nv: zeroed below)
-              const uint32_t n0 = nan_bytes(x.x, from, to), n1 = nan_bytes(x.y, from - 4, to - 4),
-                             n2 = nan_bytes(x.z, from - 8, to - 8), n3 = nan_bytes(x.w, from - 12, to - 12);
-              if (n0 | n1 | n2 | n3) {
-                *at = make_uint4(x.x & ~n0, x.y & ~n1, x.z & ~n2, x.w & ~n3);
-                hits = 1;
-              }
-            }
-            if (hits) s_nan[piece % C::kNan] = 1;
-          }
-          if (j >= C::kV16Bufs) wait(C::kBarUsed + buf, j / C::kV16Bufs - 1);
-          uint8_t* const o = sm + C::kOffV16 + buf * C::kV16 + d * 16;
-#pragma unroll 2
-          for (int t = 0; t < tiles; ++t) {
-            // codes of dim d, tokens 16 t .. 16 t + 15, to two rows of 8 f16
-            const uint4 x = *reinterpret_cast<const uint4*>(v + t * kChTile * kChDim + d * 16);
-            uint32_t y[8];
-            e4m3x4_to_f16x4(x.x, y[0], y[1]);
-            e4m3x4_to_f16x4(x.y, y[2], y[3]);
-            e4m3x4_to_f16x4(x.z, y[4], y[5]);
-            e4m3x4_to_f16x4(x.w, y[6], y[7]);
-            uint4* const w = reinterpret_cast<uint4*>(o + t * kChTile * kChDim * 2);
-            w[0] = make_uint4(y[0], y[1], y[2], y[3]);
-            w[128] = make_uint4(y[4], y[5], y[6], y[7]);
-          }
-          if (nv < kChBlk) {  // f16 of token k, dim d: rows of 8 tokens, 2 KiB apart
-#pragma unroll 1
-            for (int k = nv; k & 63; k = (k | 7) + 1)
-              for (uint8_t* e = o + (k >> 3) * 2048 + (k & 7) * 2; e < o + (k >> 3) * 2048 + 16; e += 2)
-                *reinterpret_cast<uint16_t*>(e) = 0;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(C::kBarReady + buf));
-            mbar_arrive(bar(C::kBarVFree + vs));
+        // ---- on to it
+        if (i == p.i1 && known && at >= n) {
+          if (ended) break;
+          p = next;
+          piece = pn - 1;
+          known = false;
+          i = p.i0;
+          least = seen(p.u, quotient(p.u.row0, a.by_g));  // tokens that every row sees
+          if (i < p.i1) {
+            wait(C::kBarScale + j % C::kScales, j / C::kScales);
+#pragma unroll
+            for (int t = 0; t < kChBlkTiles; ++t) fetch(j, t);
+            fetched(j);
           }
         }
       }
@@ -796,19 +877,20 @@ __global__ void __launch_bounds__(kChThreads, 1)
       const uint64_t qdesc = smem_desc(base, 16, 1024, 2), kdesc = smem_desc(base + C::kOffK, 16, 1024, 2);
       // V, 16 tokens a step: two columns of core matrices (8 dims x 8 tokens, 128 B apart along the dims, 2 KiB along the tokens)
       const uint64_t vdesc = smem_desc(base + C::kOffV16, 2048, 128, 0);
-      uint32_t j0 = 0, n0 = 0, n1 = 0, begun = 0, uses0 = 0, uses1 = 0;
+      uint32_t j0 = 0, n0 = 0, n1 = 0, begun = 0, phases = 0;  // (phases: parities of the query buffers)
       int turns = 0;
       const uint32_t turn_of = base + C::kOffMisc + 8 + 4 * (t ^ 1);
       static_assert(C::kKStages % 2 == 0 && C::kV16Bufs == 2 && C::kScales % 2 == 0, "slots that tiles own");
       while (take_piece(p)) {
         const int pair_in = __any_sync(kFull, p.pair());
-        const uint32_t nb = __reduce_max_sync(kFull, p.i1 - p.i0), qb = __reduce_max_sync(kFull, p.qbuf);
+        const uint32_t nb = __reduce_max_sync(kFull, p.i1 - p.i0), qb = __reduce_max_sync(kFull, 2 * p.qset);
         const uint32_t halves = __reduce_max_sync(kFull, max(0, p.u.tokens - p.i0 * kChBlk + 63) / 64);  // of the piece, and behind it
         if (nb == 0) continue;
         const uint32_t step = pair_in ? 1 : 2;
-        if (pair_in || qb == 0) wait(C::kBarQ, uses0++);
-        if (pair_in || qb == 1) wait(C::kBarQ + 1, uses1++);
-        const uint64_t qd = qdesc + (pair_in ? t : qb) * (C::kQTile >> 4);
+        wait(C::kBarQ + qb, phases >> qb);
+        if (pair_in) wait(C::kBarQ + qb + 1, phases >> (qb + 1));
+        phases ^= (pair_in ? 3u : 1u) << qb;
+        const uint64_t qd = qdesc + (qb + (pair_in ? t : 0)) * (C::kQTile >> 4);
         bool begins = true;
 #pragma unroll 1
         for (uint32_t i = pair_in ? 0 : (j0 ^ t) & 1; i < nb + step; i += step) {
@@ -832,11 +914,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
           }
           if (i >= step) {
             issue_half_o(od, pd, vd, acc);
+            commit_elected(bars + 8 * (C::kBarHalf + t));
             if (both) {
               wait(C::kBarP + 2 * t + 1, n1++);
               tc_fence_after();
               issue_half_o(od, pd + 32, vd + 1024, 1);
             }
+            commit_elected(bars + 8 * (C::kBarO + t));  // (before S: who sees S knows O's phase to be over)
             begun += begins;
             begins = false;
           }
@@ -851,7 +935,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
             if (!pair) commit_elected(bars + 8 * (C::kBarKFree + ks));
           }
           if (i >= step) {
-            commit_elected(bars + 8 * (C::kBarO + t));
             commit_elected(bars + 8 * (C::kBarUsed + vs));
             if (!pair) commit_elected(bars + 8 * (C::kBarUsed + vs));  // for the other tile too
           }
@@ -859,7 +942,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         j0 += nb;
         // the queries: this warp's S are done (of a pair it answers for both buffers: it has seen both filled)
 #pragma unroll 1
-        for (uint32_t b = pair_in ? 0 : qb; b <= (pair_in ? 1 : qb); ++b) commit_elected(bars + 8 * (C::kBarQFree + b));
+        for (uint32_t b = qb; b <= (pair_in ? qb + 1 : qb); ++b) commit_elected(bars + 8 * (C::kBarQFree + b));
       }
       // every product and every arrival it owes is done before the CTA ends
       commit_elected(bars + 8 * (C::kBarDone + t));
@@ -870,9 +953,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
       const int row = threadIdx.x & 127;
       const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
       const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * 128 + lanes;
-      uint32_t ns = 0;              // S blocks taken of this tile
-      uint32_t j0 = 0;              // blocks of the pieces before
-      uint32_t uses[2] = {0, 0};    // query buffers taken
+      uint32_t ns = 0;            // S blocks taken of this tile
+      uint32_t j0 = 0;            // blocks of the pieces before
+      uint32_t phases = 0;        // parities of the query buffers
       uint32_t joins = 0;
       while (take_piece(p)) {
         const bool pair = p.pair();
@@ -883,30 +966,37 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const int grow = p.u.row0 + min(lrow, p.u.rows - 1), token = quotient(grow, a.by_g);
         const int limit = seen(p.u, token);
         const int least = __reduce_min_sync(kFull, limit);  // tokens that every row of the warp sees
-        const int64_t orow = static_cast<int64_t>(p.u.c0 + token) * a.Hq + p.h * a.G + grow - token * a.G;
         const int nan_slot = static_cast<int>((pn - 1) % C::kNan);
         float m = -INFINITY, l = 0.f;
         bool any = false;
         if (nb > 0) {
-          const int buf = pair ? t : p.qbuf;
-          wait(C::kBarQ + buf, buf ? uses[1] : uses[0]);
-          if (pair || p.qbuf == 0) ++uses[0];
-          if (pair || p.qbuf == 1) ++uses[1];
-          const float mult = s_mult[buf * 128 + row];
+          const int buf = 2 * p.qset + (pair ? t : 0);
+          wait(C::kBarQ + buf, phases >> buf);
+          phases ^= (pair ? 3u : 1u) << (2 * p.qset);
+          const int e = s_exp[buf * 128 + row];
+          const float mult = e == kNanRow ? __int_as_float(0x7fffffff) : fabsf(a.sm_scale_log2) * exp2_int(-e);
           __syncwarp();
           // (of a pair each tile's warps answer for their own buffer, twice: they have seen no other filled)
           if (lane <= (pair ? 1 : 0)) mbar_arrive(bar(C::kBarQFree + buf));
+          if (mult != mult) m = mult;  // a NaN query: its row is NaN
           // ---- blocks
 #pragma unroll 1
           for (int i = pair ? 0 : t ^ p.t0; i < nb; i += pair ? 1 : 2) {
             const uint32_t js = j0 + i, st = js % C::kScales;
-            wait(C::kBarS + t, ns);
-            if (ns > 0) wait(C::kBarO + t, ns - 1);  // (over already: S came behind that product)
-            wait(C::kBarScale + st, js / C::kScales);
-            tc_fence_after();
             const int at = (p.i0 + i) * kChBlk;
             const int halves = p.u.tokens - at > 64 ? 2 : 1;  // (a half without tokens is left out)
+            // the scales, before S is there: shared memory answers late while the products read it
+            wait(C::kBarScale + st, js / C::kScales);
             const float2* const sc = s_scale + st * kChBlkTiles;
+            float f[4], ev[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const float2 x = sc[g];
+              f[g] = at_least_min(mult * x.x);
+              ev[g] = x.y;
+            }
+            wait(C::kBarS + t, ns);
+            tc_fence_after();
             if (busy) {
               if (least - at < 64 * halves) {
                 // columns that a row does not see: -inf, by a short loop over tensor memory (selects on
@@ -922,59 +1012,68 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 }
                 tmem_wait_st();
               }
-              // the second half's maximum, then the first half with its own
-              uint32_t s[64];
-              float mb = -INFINITY;
-#pragma unroll 1
-              for (int h = halves - 1; h >= 0; --h) {
-                float top[4];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) tmem_ld16_max(ts + 64 * h + 16 * g, s + 16 * g, top[g]);
-                tmem_settle64(s);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                  asm volatile("" : "+f"(top[g]));
-                  const float2 x = sc[4 * h + g];
-                  mb = fmaxf(mb, fmaf(top[g], at_least_min(mult * x.x), x.y));
-                }
-              }
-              if (__any_sync(kFull, mult != mult)) mb = mult != mult ? mult : mb;  // a NaN query's row is NaN
-              const bool grown = mb > m + kChGrow || (m == -INFINITY && mb != -INFINITY);
-              if (__any_sync(kFull, grown)) {
-                const float f = !grown ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - mb);
-                if (grown) m = mb;
-                l *= f;
-                if (any) {  // O of the blocks before
-#pragma unroll 1
-                  for (int c = 0; c < 8; ++c) tmem_scale16(to + 16 * c, f);
-                }
-              }
-              const float ref = m == -INFINITY ? 0.f : m;
+              // Half a block at a time, each with a look at its own maximum: the first half's weights are on
+              // their way while the second's are made.
 #pragma unroll 1
               for (int h = 0; h < halves; ++h) {
-                if (h == 1) {
-                  float v[64];
-                  tmem_ld64(ts + 64, v);
+                uint32_t s[64];
+                float top[4];
+                float2 next[4];  // the other half's scales, asked for ahead
 #pragma unroll
-                  for (int k = 0; k < 64; ++k) s[k] = __float_as_uint(v[k]);
+                for (int g = 0; g < 4; ++g) tmem_ld16_max(ts + 64 * h + 16 * g, s + 16 * g, top[g]);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) next[g] = sc[4 + g];
+                tmem_settle64(s, top);
+                const float mb = fmaxf(fmaxf(fmaf(top[0], f[0], ev[0]), fmaf(top[1], f[1], ev[1])),
+                                       fmaxf(fmaf(top[2], f[2], ev[2]), fmaf(top[3], f[3], ev[3])));
+                const bool grown = mb > m + kChGrow || (m == -INFINITY && mb != -INFINITY);
+                if (__any_sync(kFull, grown)) {
+                  const float x = !grown ? 1.f : m == -INFINITY ? 0.f : fast_exp2(m - mb);
+                  if (grown) m = mb;
+                  l *= x;
+                  if (any || h > 0) {
+                    // O so far: of the blocks before, whose product S came behind, and of this one's first half
+                    if (h > 0) {
+                      wait(C::kBarHalf + t, ns);
+                      tc_fence_after();
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) tmem_scale16(to + 16 * c, x);
+                    tmem_wait_st();
+                  }
                 }
+                const float ref = m == -INFINITY ? 0.f : m;
+                // arguments of the next 16 columns beside the powers of these: the powers' pipe is the slow one
+                auto arguments = [&](int g) {
+                  const float2 f2 = make_float2(f[g], f[g]), b2 = make_float2(ev[g] - ref, ev[g] - ref);
+#pragma unroll
+                  for (int k = 16 * g; k < 16 * g + 16; k += 2) {
+                    const float2 e = fma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f2, b2);
+                    s[k] = __float_as_uint(e.x);
+                    s[k + 1] = __float_as_uint(e.y);
+                  }
+                };
+                arguments(0);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                  const float2 x = sc[4 * h + g];
-                  const float f = at_least_min(mult * x.x), b = x.y - ref;
-                  const float2 f2 = make_float2(f, f), b2 = make_float2(b, b);
-                  float2 sum = make_float2(0.f, 0.f);
+                  if (g < 3) arguments(g + 1);
                   uint32_t w[8];
+                  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                   for (int k = 0; k < 8; ++k) {
-                    float2 e = fma2(make_float2(__uint_as_float(s[16 * g + 2 * k]), __uint_as_float(s[16 * g + 2 * k + 1])), f2, b2);
-                    e.x = fast_exp2(e.x);
-                    e.y = fast_exp2(e.y);
-                    sum = add2(sum, e);
+                    const float2 e = make_float2(fast_exp2(__uint_as_float(s[16 * g + 2 * k])), fast_exp2(__uint_as_float(s[16 * g + 2 * k + 1])));
+                    sum[k & 1] = add2(sum[k & 1], e);
                     w[k] = pack_f16x2(e.x, e.y);
                   }
                   tmem_st8(ts + 32 * h + 8 * g, w);  // over columns that have been read
-                  l = fmaf(sum.x + sum.y, exp2_int(-static_cast<int>(x.y)), l);
+                  const float2 x = add2(sum[0], sum[1]);
+                  // 2^-ev, from the integer in the last bits of ev + 1.5 2^23
+                  l = fmaf(x.x + x.y, __int_as_float((0x4B400000 + 127 - __float_as_int(ev[g] + 12582912.f)) << 23), l);
+                }
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                  f[g] = at_least_min(mult * next[g].x);
+                  ev[g] = next[g].y;
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -1030,31 +1129,27 @@ __global__ void __launch_bounds__(kChThreads, 1)
         } else if (!pair && t == 1) {
           continue;
         }
-        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        const int64_t orow = static_cast<int64_t>(p.u.c0 + token) * a.Hq + p.h * a.G + grow - token * a.G;
         const bool none = l == 0.f;
+        const float inv = whole && !none ? 1.f / l : 1.f;
         if (busy) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float x[32];
-            join_o(to + 32 * c, any, other, f0 * inv, f1 * inv, x);
-            if (valid) {
-              if (whole) {
+          for (int c = 0; c < 8; ++c) {
+            float x[16];
+            join_o(to + 16 * c, any, other, f0 * inv, f1 * inv, x);
+            const int d = 16 * c;
+            if (valid && whole) {
+              uint32_t y[8];
 #pragma unroll
-                for (int k = 0; k < 32; k += 16) {
-                  uint32_t y[8];
+              for (int i = 0; i < 8; ++i) y[i] = none ? 0u : pack_bf16x2(x[2 * i], x[2 * i + 1]);
+              st_global_u8(a.out + orow * kChDim + d, y);
+            } else if (valid) {
 #pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    y[i] = none ? 0u : pack_bf16x2(x[k + 2 * i], x[k + 2 * i + 1]);
-                  st_global_u8(a.out + orow * kChDim + 32 * c + k, y);
-                }
-              } else {
+              for (int k = 0; k < 16; k += 8) {
+                float y[8];
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                  float y[8];
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) y[i] = none ? 0.f : x[k + i];
-                  st_global8(a.part_o + slot * kChDim + 32 * c + k, y);
-                }
+                for (int i = 0; i < 8; ++i) y[i] = none ? 0.f : x[k + i];
+                st_global8(a.part_o + slot * kChDim + d + k, y);
               }
             }
           }
@@ -1247,10 +1342,8 @@ extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu
   if (st != FPK_OK) return st;
   int zbox = 1;  // tiles per copy: a power of two that divides a page and a block
   while (zbox < kChBlkTiles && tpp % (2 * zbox) == 0) zbox *= 2;
-  CUtensorMap kmap, vmap;
-  if (encode_pool_map(&kmap, kv_pool, tiles > 0 ? tiles : 1, true, false, zbox) != FPK_OK ||
-      encode_pool_map(&vmap, kv_pool, tiles > 0 ? tiles : 1, true, true, zbox) != FPK_OK)
-    return FPK_ECUDA;
+  CUtensorMap kmap;
+  if (encode_pool_map(&kmap, kv_pool, tiles > 0 ? tiles : 1, true, false, zbox) != FPK_OK) return FPK_ECUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   ChArgs a;
   a.q = static_cast<const uint16_t*>(q);
@@ -1285,7 +1378,7 @@ extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu
   a.sm_scale_log2 = sm_scale * kChLog2e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (launch_dependent(prefill_plan_kernel, 1, kChPlanThreads, 0, s, a) != FPK_OK ||
-      launch_dependent(prefill_attn_kernel, ctas, kChThreads, ChCfg::kSmem, s, a, kmap, vmap) != FPK_OK)
+      launch_dependent(prefill_attn_kernel, ctas, kChThreads, ChCfg::kSmem, s, a, kmap) != FPK_OK)
     return FPK_ECUDA;
   return ctas > 1 ? launch_dependent(prefill_merge_kernel, (ctas - 1) * kChMergeParts, 32 * kChMergeWarps, 0, s, a) : FPK_OK;
 }
