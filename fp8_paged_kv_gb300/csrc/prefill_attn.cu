@@ -67,7 +67,8 @@ constexpr int kChVWarp = 8, kChLoadWarp = 12, kChMmaWarp = 13, kChPlanWarp = 15;
 constexpr int kChPieces = 4;  // pieces known ahead
 constexpr int kChPlanThreads = 1024;
 constexpr int kChTurnSpins = 4096;
-constexpr int kChMergeWarps = 8, kChMergeParts = 8;  // merge: CTAs per cut unit
+constexpr int kChMergeWarps = 8, kChMergeParts = 16;  // merge: CTAs per cut unit
+constexpr int kChNear = 1024, kChNearUnits = 4096;    // requests and units that the plan keeps in shared memory
 
 struct alignas(16) ChUnit {
   int y;       // place in a kv head's line
@@ -80,9 +81,15 @@ struct alignas(16) ChUnit {
 };
 static_assert(sizeof(ChUnit) == 32, "two 16-byte words");
 
-struct alignas(16) ChStart {  // of a CTA's range
+// A CTA's range [b0, b1), its first unit, and the unit that it begins and others end (cut >= 0: up to CTA cut).
+struct alignas(16) ChStart {
   int unit, h, b0, b1;
+  ChUnit u;
+  int units, T;    // of a kv head
+  int cut, cut_h;
+  ChUnit cut_u;
 };
+static_assert(sizeof(ChStart) == 96, "six 16-byte words");
 
 struct ChArgs {
   const uint16_t* q;
@@ -98,7 +105,7 @@ struct ChArgs {
   int32_t* base;    // [B + 1] first unit of each request
   int32_t* dead;    // [B]
   ChUnit* unit;
-  ChStart* start;   // [ctas + 1]; the last one's b0 is the line's end
+  ChStart* start;   // [ctas]
   float2* part_ml;  // partials: [2 ctas][256 rows]
   float* part_o;
   int n_tokens, causal, B, Hq, Hkv, G, page_size, num_pages, max_pages, ctas, zbox;
@@ -179,6 +186,24 @@ __device__ __forceinline__ ChUnit load_unit(const ChUnit* at) {
   return {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 }
 
+__device__ __forceinline__ ChUnit near_unit(const int4& x, const int4& y) { return {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}; }
+
+// CTA c owns [begin(c), begin(c + 1)) of the line: its length / n, one more for the first (its length mod n) CTAs.
+struct ChRanges {
+  int share, more;
+  __device__ __forceinline__ int begin(int c) const { return c * share + min(c, more); }
+  __device__ __forceinline__ int owner(int y) const {
+    const int big = more * (share + 1);
+    return y < big ? y / (share + 1) : more + (y - big) / share;
+  }
+};
+__device__ __forceinline__ ChRanges ranges_of(int line, int n) {
+  ChRanges r;
+  r.share = line / n;
+  r.more = line - r.share * n;
+  return r;
+}
+
 // Sums of a CTA's threads: the sum of the threads before, and of all.
 __device__ __forceinline__ int block_scan(int mine, int& all, int* s_sum) {
   const unsigned kFull = 0xffffffffu;
@@ -203,22 +228,32 @@ __device__ __forceinline__ int block_scan(int mine, int& all, int* s_sum) {
   return incl - mine + (warp > 0 ? below : 0);
 }
 
+// Few dependent reads: the requests and the units' places stay in shared memory (where there are more than fit, in
+// the workspace), and warps without a request of their own share the others' page tables.
 __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const ChArgs a) {
   __shared__ int s_sum[kChPlanThreads / 32];
+  __shared__ int s_base[kChNear + 1], s_bad[kChNear], s_y[kChNearUnits];
   griddep_wait();
   griddep_launch_dependents();
   const unsigned kFull = 0xffffffffu;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  // requests that a bad page makes dead, a warp each
+  constexpr int kWarps = kChPlanThreads / 32;
+  const bool near = a.B <= kChNear;
+  int32_t* const base = near ? s_base : a.base;
+  int32_t* const dead = near ? s_bad : a.dead;
+  if (t < kChNear) s_bad[t] = 0;
+  __syncthreads();
+  // requests that are dead, by a bad page or otherwise
+  const int ways = a.B < kWarps ? kWarps / a.B : 1;
 #pragma unroll 1
-  for (int r = warp; r < a.B; r += kChPlanThreads / 32) {
+  for (int r = warp / ways; r < a.B; r += kWarps / ways) {
     const int L = live_length(a, r), pages = L > 0 ? (L - 1) / a.page_size + 1 : 0;
     const int32_t* const row = a.page_table + static_cast<int64_t>(r) * a.max_pages;
-    bool bad = false;
+    bool bad = L == 0;
 #pragma unroll 8
-    for (int i = lane; i < pages; i += 32) bad |= static_cast<unsigned>(__ldg(row + i)) >= static_cast<unsigned>(a.num_pages);
+    for (int i = warp % ways * 32 + lane; i < pages; i += 32 * ways) bad |= static_cast<unsigned>(__ldg(row + i)) >= static_cast<unsigned>(a.num_pages);
     bad = __any_sync(kFull, bad);
-    if (lane == 0) a.dead[r] = bad || L == 0;
+    if (lane == 0 && (bad || !near)) dead[r] = bad;  // (with several ways the flags begin at 0)
   }
   // units of each request
   int units = 0;
@@ -228,10 +263,10 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
     const int rows = r < a.B ? max(0, query_start(a, r + 1) - query_start(a, r)) * a.G : 0;
     int all;
     const int before = block_scan((rows + kChUnitRows - 1) / kChUnitRows, all, s_sum);
-    if (r < a.B) a.base[r] = units + before;
+    if (r < a.B) base[r] = units + before;
     units += all;
   }
-  if (t == 0) a.base[a.B] = units;
+  if (t == 0) base[a.B] = units;
   __syncthreads();
   // their places: each thread a run of units
   const int chunk = (units + kChPlanThreads - 1) / kChPlanThreads;
@@ -242,18 +277,19 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
 #pragma unroll 1
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (a.base[mid] <= x0) lo = mid; else hi = mid - 1;
+      if (base[mid] <= x0) lo = mid; else hi = mid - 1;
     }
   }
   auto unit_at = [&](int x, int& r) -> ChUnit {
-    while (a.base[r + 1] <= x) ++r;
+    while (base[r + 1] <= x) ++r;
     ChUnit u;
+    u.y = 0;
     u.r = r;
     u.c0 = query_start(a, r);
     const int n = query_start(a, r + 1) - u.c0, rows = n * a.G;
-    u.L = a.dead[r] ? 0 : __ldg(a.seq_lens + r);
+    u.L = dead[r] ? 0 : __ldg(a.seq_lens + r);
     u.shift = a.causal ? u.L - n : u.L;
-    u.row0 = (x - a.base[r]) * kChUnitRows;
+    u.row0 = (x - base[r]) * kChUnitRows;
     u.rows = min(kChUnitRows, rows - u.row0);
     u.tokens = seen(u, quotient(u.row0 + u.rows - 1, a.by_g));
     return u;
@@ -269,26 +305,43 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
     ChUnit u = unit_at(x, r);
     u.y = y;
     a.unit[x] = u;
+    if (x < kChNearUnits) s_y[x] = y;
     y += unit_cost(u);
   }
   __syncthreads();
-  // every CTA's range and first unit: the last one that starts at or before it
-  const int line = T * a.Hkv, share = line / a.ctas, more = line - share * a.ctas;
+  // every CTA's range, its first unit (the last one that starts at or before it) and the one that it leaves to others
+  const ChRanges rg = ranges_of(T * a.Hkv, a.ctas);
+  const bool near_units = units <= kChNearUnits;
+  auto unit_of = [&](int place, int& h) -> int {
+    h = min(place / T, a.Hkv - 1);
+    const int at = place - h * T;
+    int l = 0, m = units - 1;
 #pragma unroll 1
-  for (int c = t; c <= a.ctas; c += kChPlanThreads) {
-    ChStart s = {0, 0, c * share + min(c, more), 0};
-    s.b1 = c < a.ctas ? (c + 1) * share + min(c + 1, more) : s.b0;
-    if (T > 0) {
-      s.h = s.b0 / T;
-      const int at = s.b0 - s.h * T;
-      int l = 0, h = units - 1;
+    while (l < m) {
+      const int mid = (l + m + 1) >> 1;
+      if ((near_units ? s_y[mid] : a.unit[mid].y) <= at) l = mid; else m = mid - 1;
+    }
+    return l;
+  };
 #pragma unroll 1
-      while (l < h) {
-        const int mid = (l + h + 1) >> 1;
-        if (a.unit[mid].y <= at) l = mid; else h = mid - 1;
+  for (int c = t; c < a.ctas; c += kChPlanThreads) {
+    ChStart s = {};
+    s.b0 = rg.begin(c);
+    s.b1 = rg.begin(c + 1);
+    s.units = units;
+    s.T = T;
+    s.cut = -1;
+    if (s.b0 < s.b1) {
+      s.unit = unit_of(s.b0, s.h);
+      s.u = a.unit[s.unit];
+      if (s.b1 < T * a.Hkv) {
+        s.cut_u = a.unit[unit_of(s.b1, s.cut_h)];
+        const int at = s.cut_h * T + s.cut_u.y, blocks = blocks_of(s.cut_u.tokens);
+        int i0, i1;
+        owned_blocks(s.cut_u, at, s.b0, s.b1, i0, i1);
+        if (i0 == 0 && i1 > 0 && i1 < blocks)
+          s.cut = rg.owner(at + start_cost(s.cut_u.rows) + (blocks - 1) * block_cost(s.cut_u.rows));
       }
-      s.unit = l;
-      if (c == 0) s.h = 0;
     }
     a.start[c] = s;
   }
@@ -530,7 +583,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
   griddep_wait();  // the plan is there
   griddep_launch_dependents();
   const uint32_t tmem = *s_tmem;
-  const int4 first = __ldcg(reinterpret_cast<const int4*>(a.start + blockIdx.x));
+  const int4* const start = reinterpret_cast<const int4*>(a.start + blockIdx.x);
+  const int4 first = __ldcg(start);
   auto wait = [&](int i, uint32_t parity) { tc_wait(bar(i), parity & 1u, a.status, s_failed); };
   uint32_t pn = 0;
   auto take_piece = [&](ChPiece& p) -> bool {
@@ -551,9 +605,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
       cur.h = first.y;
       cur.b0 = first.z;
       cur.b1 = first.w;
-      cur.units = __ldcg(a.base + a.B);
-      cur.T = __ldcg(&a.start[a.ctas].b0) / a.Hkv;  // (the last range ends where the line does)
-      cur.u = load_unit(a.unit + cur.x);
+      cur.u = near_unit(__ldcg(start + 1), __ldcg(start + 2));
+      const int4 more_of = __ldcg(start + 3);
+      cur.units = more_of.x;
+      cur.T = more_of.y;
       int qset = 0, t0 = 0;
       uint32_t j = 0;  // blocks whose scales are out
       bool more = true;
@@ -1182,41 +1237,32 @@ __global__ void __launch_bounds__(kChThreads, 1)
 // ---------------------------------------------------------------------------
 // merge
 // ---------------------------------------------------------------------------
-// kChMergeParts CTAs for each CTA of the products whose range ends within a unit that begins in it; a warp per
-// row: a lane finds one partial (its place, m, l), then all lanes add its O.
+// kChMergeParts CTAs for each CTA of the products that begins a unit and leaves its end to others; a warp per row: a
+// lane finds one partial (its place, m, l), then all lanes add its O.
 __global__ void __launch_bounds__(32 * kChMergeWarps) prefill_merge_kernel(const ChArgs a) {
   const unsigned kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31, c = blockIdx.x / kChMergeParts;
   griddep_wait();
-  auto load_start = [&](int i) -> ChStart {
-    const int4 x = __ldcg(reinterpret_cast<const int4*>(a.start + i));
-    return {x.x, x.y, x.z, x.w};
-  };
-  const ChStart s0 = load_start(c), s1 = load_start(c + 1);
-  const int T = load_start(a.ctas).b0 / a.Hkv;
-  if (s0.b0 >= s0.b1 || s1.b0 >= s1.b1) return;
-  const ChUnit u = load_unit(a.unit + s1.unit);
-  const int y = s1.h * T + u.y, blocks = blocks_of(u.tokens);
-  int i0, i1;
-  owned_blocks(u, y, s0.b0, s0.b1, i0, i1);
-  if (i0 != 0 || i1 == 0 || i1 == blocks) return;
+  const int4* const start = reinterpret_cast<const int4*>(a.start + c);
+  const int4 cut = __ldcg(start + 3), u0 = __ldcg(start + 4), u1 = __ldcg(start + 5);
+  if (cut.z < 0) return;
+  const ChUnit u = near_unit(u0, u1);
+  const int T = cut.y, y = cut.w * T + u.y;
+  const ChRanges rg = ranges_of(T * a.Hkv, a.ctas);
 #pragma unroll 1
   for (int row = blockIdx.x % kChMergeParts * kChMergeWarps + (threadIdx.x >> 5); row < u.rows; row += kChMergeParts * kChMergeWarps) {
     float M = -INFINITY, W = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool more = true;
 #pragma unroll 1
-    for (int base = c; more; base += 32) {
+    for (int base = c; base <= cut.z; base += 32) {
       const int k = base + lane;
       const int64_t slot = static_cast<int64_t>(2 * k + (k == c ? 0 : 1)) * kChUnitRows + row;
       float2 ml = make_float2(-INFINITY, 0.f);
-      int b = 0, e = blocks;
-      if (k < a.ctas) {
-        const ChStart s = load_start(k);
-        owned_blocks(u, y, s.b0, s.b1, b, e);
+      if (k <= cut.z) {
+        int b, e;
+        owned_blocks(u, y, rg.begin(k), rg.begin(k + 1), b, e);
         if (b < e) ml = __ldcg(a.part_ml + slot);
       }
-      more = !__any_sync(kFull, k >= a.ctas || e == blocks);
       float mx = ml.x;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
@@ -1254,7 +1300,7 @@ __global__ void __launch_bounds__(32 * kChMergeWarps) prefill_merge_kernel(const
     const bool none = W == 0.f;
     const float inv = none ? 0.f : 1.f / W;
     const int grow = u.row0 + row, token = quotient(grow, a.by_g);
-    const int64_t orow = static_cast<int64_t>(u.c0 + token) * a.Hq + y / T * a.G + grow - token * a.G;
+    const int64_t orow = static_cast<int64_t>(u.c0 + token) * a.Hq + cut.w * a.G + grow - token * a.G;
     reinterpret_cast<uint2*>(a.out + orow * kChDim)[lane] =
         none ? make_uint2(0, 0) : make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (lane == 0 && a.lse != nullptr) a.lse[orow] = none ? -INFINITY : (M + __log2f(W)) * kChLn2;
@@ -1288,7 +1334,7 @@ ChLayout prefill_layout(int64_t B, int64_t n_tokens, int64_t G, int64_t ctas) {
   l.dead = l.base + up((B + 1) * 4);
   l.unit = l.dead + up(B * 4);
   l.start = l.unit + up(most_units(B, n_tokens, G) * static_cast<int64_t>(sizeof(ChUnit)));
-  l.ml = l.start + up((ctas + 1) * static_cast<int64_t>(sizeof(ChStart)));
+  l.ml = l.start + up(ctas * static_cast<int64_t>(sizeof(ChStart)));
   l.o = l.ml + up(2 * ctas * kChUnitRows * 8);
   l.total = l.o + up(2 * ctas * kChUnitRows * kChDim * 4);
   return l;
@@ -1380,5 +1426,5 @@ extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu
   if (launch_dependent(prefill_plan_kernel, 1, kChPlanThreads, 0, s, a) != FPK_OK ||
       launch_dependent(prefill_attn_kernel, ctas, kChThreads, ChCfg::kSmem, s, a, kmap) != FPK_OK)
     return FPK_ECUDA;
-  return ctas > 1 ? launch_dependent(prefill_merge_kernel, (ctas - 1) * kChMergeParts, 32 * kChMergeWarps, 0, s, a) : FPK_OK;
+  return launch_dependent(prefill_merge_kernel, ctas * kChMergeParts, 32 * kChMergeWarps, 0, s, a);
 }
