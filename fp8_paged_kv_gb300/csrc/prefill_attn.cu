@@ -5,8 +5,9 @@
 // The rows of a request and kv head are its query tokens' heads that read it (token
 // by token, the heads of a group one after another): one read of a block of K and V
 // serves 256 rows, and a causal border crosses few blocks (32 tokens at 8 heads per
-// group).  Three launches, each a dependent of the one before:
-//   plan    dead requests, the work list (one CTA)
+// group).  Two or three launches, each a dependent of the one before:
+//   plan    dead requests, the work list (one CTA; small ones are made by every CTA of
+//           the next launch itself, which saves this one: 4 us of 18 for 16 tokens)
 //   attn    the list, a CTA per SM
 //   merge   rows whose unit was cut between CTAs, by log-sum-exp
 //
@@ -69,6 +70,7 @@ constexpr int kChPlanThreads = 1024;
 constexpr int kChTurnSpins = 4096;
 constexpr int kChMergeWarps = 8, kChMergeParts = 16;  // merge: CTAs per cut unit
 constexpr int kChNear = 1024, kChNearUnits = 4096;    // requests and units that the plan keeps in shared memory
+constexpr int kChSmallPages = 8192, kChSmallUnits = kChThreads;  // page table entries and units of a list that every CTA makes
 
 struct alignas(16) ChUnit {
   int y;       // place in a kv head's line
@@ -108,6 +110,8 @@ struct ChArgs {
   ChStart* start;   // [ctas]
   float2* part_ml;  // partials: [2 ctas][256 rows]
   float* part_o;
+  int small;        // every CTA makes the list
+  int boxed;        // 32 rows are whole tokens' heads: results go out by tensor map
   int n_tokens, causal, B, Hq, Hkv, G, page_size, num_pages, max_pages, ctas, zbox;
   uint32_t by_g, by_tpp;
   float sm_scale_log2;
@@ -205,6 +209,7 @@ __device__ __forceinline__ ChRanges ranges_of(int line, int n) {
 }
 
 // Sums of a CTA's threads: the sum of the threads before, and of all.
+template <int kThreads>
 __device__ __forceinline__ int block_scan(int mine, int& all, int* s_sum) {
   const unsigned kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -217,7 +222,7 @@ __device__ __forceinline__ int block_scan(int mine, int& all, int* s_sum) {
   __syncthreads();  // (s_sum's last readers)
   if (lane == 31) s_sum[warp] = incl;
   __syncthreads();
-  int sums = s_sum[lane];
+  int sums = lane < kThreads / 32 ? s_sum[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(kFull, sums, o);
@@ -228,20 +233,23 @@ __device__ __forceinline__ int block_scan(int mine, int& all, int* s_sum) {
   return incl - mine + (warp > 0 ? below : 0);
 }
 
-// Few dependent reads: the requests and the units' places stay in shared memory (where there are more than fit, in
-// the workspace), and warps without a request of their own share the others' page tables.
-__global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const ChArgs a) {
-  __shared__ int s_sum[kChPlanThreads / 32];
-  __shared__ int s_base[kChNear + 1], s_bad[kChNear], s_y[kChNearUnits];
-  griddep_wait();
-  griddep_launch_dependents();
+struct ChPlanSpace {
+  int sum[32];
+  int base[kChNear + 1], bad[kChNear], y[kChNearUnits];
+};
+
+// The work list, by a CTA, and the ranges of the CTAs c0, c0 + 1, .. c1 - 1.  Few dependent reads: the requests and the
+// units' places stay in shared memory (where there are more than fit, in the workspace), and warps without a request
+// of their own share the others' page tables.
+template <int kThreads>
+__device__ __forceinline__ void make_plan(const ChArgs& a, ChPlanSpace& sp, int c0, int c1) {
   const unsigned kFull = 0xffffffffu;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  constexpr int kWarps = kChPlanThreads / 32;
+  constexpr int kWarps = kThreads / 32;
   const bool near = a.B <= kChNear;
-  int32_t* const base = near ? s_base : a.base;
-  int32_t* const dead = near ? s_bad : a.dead;
-  if (t < kChNear) s_bad[t] = 0;
+  int32_t* const base = near ? sp.base : a.base;
+  int32_t* const dead = near ? sp.bad : a.dead;
+  for (int i = t; i < min(a.B, kChNear); i += kThreads) sp.bad[i] = 0;
   __syncthreads();
   // requests that are dead, by a bad page or otherwise
   const int ways = a.B < kWarps ? kWarps / a.B : 1;
@@ -258,32 +266,30 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
   // units of each request
   int units = 0;
 #pragma unroll 1
-  for (int r0 = 0; r0 < a.B; r0 += kChPlanThreads) {
+  for (int r0 = 0; r0 < a.B; r0 += kThreads) {
     const int r = r0 + t;
     const int rows = r < a.B ? max(0, query_start(a, r + 1) - query_start(a, r)) * a.G : 0;
     int all;
-    const int before = block_scan((rows + kChUnitRows - 1) / kChUnitRows, all, s_sum);
+    const int before = block_scan<kThreads>((rows + kChUnitRows - 1) / kChUnitRows, all, sp.sum);
     if (r < a.B) base[r] = units + before;
     units += all;
   }
   if (t == 0) base[a.B] = units;
   __syncthreads();
-  // their places: each thread a run of units
-  const int chunk = (units + kChPlanThreads - 1) / kChPlanThreads;
-  const int x0 = min(units, t * chunk), x1 = min(units, x0 + chunk);
-  int lo = 0;
-  if (x0 < x1) {
-    int hi = a.B - 1;  // the last request whose first unit is not behind x0 (of empty ones the last has units)
+  // the last request whose first unit is not behind x (of empty ones the last has units)
+  auto request_of = [&](int x) -> int {
+    int lo = 0, hi = a.B - 1;
 #pragma unroll 1
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (base[mid] <= x0) lo = mid; else hi = mid - 1;
+      if (base[mid] <= x) lo = mid; else hi = mid - 1;
     }
-  }
-  auto unit_at = [&](int x, int& r) -> ChUnit {
+    return lo;
+  };
+  auto unit_at = [&](int x, int& r, int y) -> ChUnit {
     while (base[r + 1] <= x) ++r;
     ChUnit u;
-    u.y = 0;
+    u.y = y;
     u.r = r;
     u.c0 = query_start(a, r);
     const int n = query_start(a, r + 1) - u.c0, rows = n * a.G;
@@ -294,37 +300,42 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
     u.tokens = seen(u, quotient(u.row0 + u.rows - 1, a.by_g));
     return u;
   };
+  // their places: each thread a run of units
+  const int chunk = (units + kThreads - 1) / kThreads;
+  const int x0 = min(units, t * chunk), x1 = min(units, x0 + chunk);
+  const int lo = x0 < x1 ? request_of(x0) : 0;
   int mine = 0, r = lo;
 #pragma unroll 1
-  for (int x = x0; x < x1; ++x) mine += unit_cost(unit_at(x, r));
+  for (int x = x0; x < x1; ++x) mine += unit_cost(unit_at(x, r, 0));
   int T;
-  int y = block_scan(mine, T, s_sum);
+  int y = block_scan<kThreads>(mine, T, sp.sum);
   r = lo;
 #pragma unroll 1
   for (int x = x0; x < x1; ++x) {
-    ChUnit u = unit_at(x, r);
-    u.y = y;
+    const ChUnit u = unit_at(x, r, y);
     a.unit[x] = u;
-    if (x < kChNearUnits) s_y[x] = y;
+    if (x < kChNearUnits) sp.y[x] = y;
     y += unit_cost(u);
   }
   __syncthreads();
-  // every CTA's range, its first unit (the last one that starts at or before it) and the one that it leaves to others
+  // the ranges, with their first unit (the last one that starts at or before it) and the one that they leave to others
   const ChRanges rg = ranges_of(T * a.Hkv, a.ctas);
   const bool near_units = units <= kChNearUnits;
-  auto unit_of = [&](int place, int& h) -> int {
+  auto unit_of = [&](int place, int& x, int& h) -> ChUnit {
     h = min(place / T, a.Hkv - 1);
     const int at = place - h * T;
     int l = 0, m = units - 1;
 #pragma unroll 1
     while (l < m) {
       const int mid = (l + m + 1) >> 1;
-      if ((near_units ? s_y[mid] : a.unit[mid].y) <= at) l = mid; else m = mid - 1;
+      if ((near_units ? sp.y[mid] : a.unit[mid].y) <= at) l = mid; else m = mid - 1;
     }
-    return l;
+    x = l;
+    int q = request_of(l);
+    return unit_at(l, q, near_units ? sp.y[l] : a.unit[l].y);
   };
 #pragma unroll 1
-  for (int c = t; c < a.ctas; c += kChPlanThreads) {
+  for (int c = c0 + t; c < c1; c += kThreads) {
     ChStart s = {};
     s.b0 = rg.begin(c);
     s.b1 = rg.begin(c + 1);
@@ -332,10 +343,10 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
     s.T = T;
     s.cut = -1;
     if (s.b0 < s.b1) {
-      s.unit = unit_of(s.b0, s.h);
-      s.u = a.unit[s.unit];
+      s.u = unit_of(s.b0, s.unit, s.h);
       if (s.b1 < T * a.Hkv) {
-        s.cut_u = a.unit[unit_of(s.b1, s.cut_h)];
+        int x;
+        s.cut_u = unit_of(s.b1, x, s.cut_h);
         const int at = s.cut_h * T + s.cut_u.y, blocks = blocks_of(s.cut_u.tokens);
         int i0, i1;
         owned_blocks(s.cut_u, at, s.b0, s.b1, i0, i1);
@@ -345,6 +356,13 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
     }
     a.start[c] = s;
   }
+}
+
+__global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const ChArgs a) {
+  __shared__ ChPlanSpace sp;
+  griddep_wait();
+  griddep_launch_dependents();
+  make_plan<kChPlanThreads>(a, sp, 0, a.ctas);
 }
 
 struct alignas(16) ChPiece {
@@ -499,6 +517,30 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
+// 32 columns of O of a row tile (`mine`) and of the other one's (`other`, 128 columns on), joined.
+__device__ __forceinline__ void join_o32(uint32_t to, bool mine, bool other, float f0, float f1, float (&x)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) x[k] = 0.f;
+  uint32_t r[32];
+  if (mine) {
+    tmem_ld32(to, r);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(r[k]) * f0;
+  }
+  if (other) {
+    tmem_ld32(to + 128, r);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = fmaf(__uint_as_float(r[k]), f1, x[k]);
+  }
+}
+
+__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+
 // 16 columns of O of a row tile (`mine`) and of the other one's (`other`, 128 columns on), joined.
 __device__ __forceinline__ void join_o(uint32_t to, bool mine, bool other, float f0, float f1, float (&x)[16]) {
 #pragma unroll
@@ -536,7 +578,8 @@ __device__ __noinline__ void poison_row(const ChArgs& a, int r, int h, int from,
 }
 
 __global__ void __launch_bounds__(kChThreads, 1)
-    prefill_attn_kernel(const ChArgs a, const __grid_constant__ CUtensorMap kmap) {
+    prefill_attn_kernel(const ChArgs a, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap omap) {
   using C = ChCfg;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const sm = smem_raw;
@@ -580,8 +623,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_wait();  // the plan is there
+  griddep_wait();  // the plan is there, or what it needs
   griddep_launch_dependents();
+  if (a.small) {
+    // (every CTA writes the same list of units; the space is the queries')
+    make_plan<kChThreads>(a, *reinterpret_cast<ChPlanSpace*>(sm), blockIdx.x, blockIdx.x + 1);
+    __syncthreads();
+  }
   const uint32_t tmem = *s_tmem;
   const int4* const start = reinterpret_cast<const int4*>(a.start + blockIdx.x);
   const int4 first = __ldcg(start);
@@ -740,12 +788,31 @@ __global__ void __launch_bounds__(kChThreads, 1)
         if (tile >= 0)
           x[t] = ld_stream(a.kv_pool + static_cast<int64_t>(tile) * (2 * kChTile * kChDim) + kChTile * kChDim + d * 16);
       };
+      uint4 q[2][2];
+      auto ask = [&](int s0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int s = s0 + k, row = next.u.row0 + 32 * vw + (lane >> 3) + 128 * (s >> 3) + 4 * (s & 7);
+          q[k][0] = q[k][1] = make_uint4(0, 0, 0, 0);
+          if (s < n && row < next.u.row0 + next.u.rows) {
+            // (query token row / G, head row % G of the group)
+            const uint4* const at = reinterpret_cast<const uint4*>(
+                a.q + (static_cast<int64_t>(next.u.c0) * a.Hq + next.h * a.G + row + static_cast<int64_t>(quotient(row, a.by_g)) * (a.Hq - a.G)) * kChDim +
+                16 * c);
+            q[k][0] = __ldg(at);
+            q[k][1] = __ldg(at + 1);
+          }
+        }
+      };
       auto fetched = [&](uint32_t b) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::kBarScaleFree + b % C::kScales));
       };
       for (;;) {
-        if (i < p.i1) {
+        // V goes first wherever its buffer is free, a step of the queries else
+        const bool queries = known && at < n;
+        if (i < p.i1 && (!queries || j < C::kV16Bufs ||
+                         __all_sync(kFull, mbar_test(bar(C::kBarUsed + j % C::kV16Bufs), (j / C::kV16Bufs - 1) & 1)))) {
           // ---- V: this thread's dim of a block's tiles, the next block's on their way while one is converted
           const int nv = min(kChBlk, p.u.tokens - i * kChBlk), first_hidden = least - i * kChBlk;
           const uint32_t buf = j % C::kV16Bufs;
@@ -790,37 +857,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (lane == 0) mbar_arrive(bar(C::kBarReady + buf));
           ++i;
           ++j;
-        }
-        // ---- the next piece, once it is known; it is waited for when there is nothing else to do
-        if (!known && (i == p.i1 || __all_sync(kFull, mbar_test(bar(C::kBarPiece + pn % kChPieces), pn / kChPieces & 1)))) {
-          ended = !take_piece(next);
-          known = true;
-          at = 0;
-          n = ended || next.i0 == next.i1 ? 0 : next.pair() ? 16 : 8;
-          if (d == 0) s_nan[(pn - 1 + C::kNan / 2) % C::kNan] = 0;
-        }
-        // ---- its queries, two steps at a time; each operation for all values before the next one: only the warp's
-        // own instructions hide their time
-        if (known && at < n) {
-          const int row0 = next.u.row0 + 32 * vw + (lane >> 3);  // of this lane: step s has row0 + 128 (s / 8) + 4 (s % 8)
-          const int rows = next.u.row0 + next.u.rows;
-          const uint16_t* const src = a.q + (static_cast<int64_t>(next.u.c0) * a.Hq + next.h * a.G) * kChDim + 16 * c;
-          uint4 q[2][2];
-          auto ask = [&](int s, uint4& q0, uint4& q1) {
-            const int row = row0 + 128 * (s >> 3) + 4 * (s & 7);
-            q0 = q1 = make_uint4(0, 0, 0, 0);
-            if (s < n && row < rows) {
-              // (query token row / G, head row % G of the group)
-              const uint4* const at = reinterpret_cast<const uint4*>(
-                  src + static_cast<int64_t>(row + quotient(row, a.by_g) * (a.Hq - a.G)) * kChDim);
-              q0 = __ldg(at);
-              q1 = __ldg(at + 1);
-            }
-          };
-#pragma unroll
-          for (int k = 0; k < 2; ++k) ask(at + k, q[k][0], q[k][1]);
-          // all that are left behind the last block, else as many as leave none for then
-          const int left = p.i1 - i, end = left == 0 ? n : min(n, at + 2 * ((n - at + 2 * left - 1) / (2 * left)));
+        } else if (queries) {
+          // ---- the next piece's queries, two steps at a time (all that are left behind the last block); each operation
+          // for all values before the next one: only the warp's own instructions hide their time
+          const int end = i == p.i1 ? n : at + 2;
 #pragma unroll 1
           for (; at < end; at += 2) {
             const int buf = 2 * next.qset + (at >> 3);
@@ -837,8 +877,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
               r[k][0] = q[k][0].x, r[k][1] = q[k][0].y, r[k][2] = q[k][0].z, r[k][3] = q[k][0].w;
               r[k][4] = q[k][1].x, r[k][5] = q[k][1].y, r[k][6] = q[k][1].z, r[k][7] = q[k][1].w;
             }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) ask(at + 2 + k, q[k][0], q[k][1]);
+            ask(at + 2);
             // largest |q| of the row: bf16 magnitudes order as integers
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -897,6 +936,15 @@ __global__ void __launch_bounds__(kChThreads, 1)
               if (lane == 0) mbar_arrive(bar(C::kBarQ + buf));
             }
           }
+        }
+        // ---- the next piece, once it is known; it is waited for when there is nothing else to do
+        if (!known && (i == p.i1 || __all_sync(kFull, mbar_test(bar(C::kBarPiece + pn % kChPieces), pn / kChPieces & 1)))) {
+          ended = !take_piece(next);
+          known = true;
+          at = 0;
+          n = ended || next.i0 == next.i1 ? 0 : next.pair() ? 16 : 8;
+          ask(0);
+          if (d == 0) s_nan[(pn - 1 + C::kNan / 2) % C::kNan] = 0;
         }
         // ---- on to it
         if (i == p.i1 && known && at >= n) {
@@ -1022,17 +1070,19 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const int limit = seen(p.u, token);
         const int least = __reduce_min_sync(kFull, limit);  // tokens that every row of the warp sees
         const int nan_slot = static_cast<int>((pn - 1) % C::kNan);
+        const int buf = 2 * p.qset + (pair ? t : 0);
+        // (of a pair each tile's warps answer for their own buffer, twice: they have seen no other filled)
+        auto free_queries = [&]() {
+          if (nb > 0 && lane <= (pair ? 1 : 0)) mbar_arrive(bar(C::kBarQFree + buf));
+        };
         float m = -INFINITY, l = 0.f;
         bool any = false;
         if (nb > 0) {
-          const int buf = 2 * p.qset + (pair ? t : 0);
           wait(C::kBarQ + buf, phases >> buf);
           phases ^= (pair ? 3u : 1u) << (2 * p.qset);
           const int e = s_exp[buf * 128 + row];
           const float mult = e == kNanRow ? __int_as_float(0x7fffffff) : fabsf(a.sm_scale_log2) * exp2_int(-e);
           __syncwarp();
-          // (of a pair each tile's warps answer for their own buffer, twice: they have seen no other filled)
-          if (lane <= (pair ? 1 : 0)) mbar_arrive(bar(C::kBarQFree + buf));
           if (mult != mult) m = mult;  // a NaN query: its row is NaN
           // ---- blocks
 #pragma unroll 1
@@ -1169,6 +1219,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(C::kBarJoin));
             }
+            free_queries();
             continue;
           }
           if (other) {
@@ -1187,7 +1238,31 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const int64_t orow = static_cast<int64_t>(p.u.c0 + token) * a.Hq + p.h * a.G + grow - token * a.G;
         const bool none = l == 0.f;
         const float inv = whole && !none ? 1.f / l : 1.f;
-        if (busy) {
+        if (whole && a.boxed && lrow - lane + 32 <= p.u.rows) {
+          // The warp's 32 rows are whole tokens' heads: by way of its rows' place in the query buffer, which has been
+          // read, as two boxes of 64 dims (rows of 128 bytes with the 128-byte swizzle).  Stores from registers touch a
+          // line per row, a cycle each, and what is asked of shared memory behind them waits as long.
+          uint8_t* const mine = sm + buf * C::kQTile + (row - lane) * 256 + lane * 128;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float x[32];
+            join_o32(to + 32 * c, any, other, f0 * inv, f1 * inv, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(mine + (c >> 1) * 4096 + ((((c & 1) * 4 + i) ^ (lane & 7)) << 4)) =
+                  none ? make_uint4(0, 0, 0, 0)
+                       : make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                                    pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const uint32_t src = smem_addr(mine);
+            tma_store_3d(&omap, src, 0, p.h * a.G, p.u.c0 + token);
+            tma_store_3d(&omap, src + 4096, 64, p.h * a.G, p.u.c0 + token);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else if (busy) {
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             float x[16];
@@ -1215,14 +1290,19 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (any) mbar_arrive(bar(C::kBarOFree + t));
           if (other) mbar_arrive(bar(C::kBarOFree + 1));
         }
+        if (s_nan[nan_slot] != 0) {
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the rows are out)
+          __syncwarp();
+          const int lo = max(seen(p.u, quotient(p.u.row0, a.by_g)), p.i0 * kChBlk), hi = min(limit, p.i1 * kChBlk);
+          if (valid) poison_row(a, p.u.r, p.h, lo, hi, whole ? a.out + orow * kChDim : nullptr, whole ? nullptr : a.part_o + slot * kChDim);
+        }
         if (valid) {
-          if (s_nan[nan_slot] != 0) {
-            const int lo = max(seen(p.u, quotient(p.u.row0, a.by_g)), p.i0 * kChBlk), hi = min(limit, p.i1 * kChBlk);
-            poison_row(a, p.u.r, p.h, lo, hi, whole ? a.out + orow * kChDim : nullptr, whole ? nullptr : a.part_o + slot * kChDim);
-          }
           if (!whole) a.part_ml[slot] = make_float2(m, l);
           else if (a.lse != nullptr) a.lse[orow] = none ? -INFINITY : (m + __log2f(l)) * kChLn2;
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+        free_queries();
       }
     }
   }
@@ -1321,6 +1401,19 @@ int prepare_prefill(int dev) {
   return FPK_OK;
 }
 
+// bf16 results [n_tokens][Hq][128]: boxes of 64 dims, G heads, 32 / G tokens.
+int encode_rows_map(CUtensorMap* m, void* out, int Hq, int n_tokens, int G) {
+  EncodeTiled enc = tensor_map_encoder();
+  if (enc == nullptr) return FPK_ECUDA;
+  const cuuint64_t dims[3] = {kChDim, static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(n_tokens)};
+  const cuuint64_t strides[2] = {kChDim * 2, static_cast<cuuint64_t>(Hq) * kChDim * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(32 / G)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FPK_OK : FPK_ECUDA;
+}
+
 // Most units of a kv head.
 int64_t most_units(int64_t B, int64_t n_tokens, int64_t G) { return n_tokens * G / kChUnitRows + B; }
 
@@ -1390,8 +1483,13 @@ extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu
   while (zbox < kChBlkTiles && tpp % (2 * zbox) == 0) zbox *= 2;
   CUtensorMap kmap;
   if (encode_pool_map(&kmap, kv_pool, tiles > 0 ? tiles : 1, true, false, zbox) != FPK_OK) return FPK_ECUDA;
+  // results: dims, heads, tokens; boxes of a warp's rows, which are whole tokens' heads where G divides 32
+  const bool boxed = 32 % G == 0;
+  CUtensorMap omap = kmap;
+  if (boxed && encode_rows_map(&omap, out, Hq, n_tokens, G) != FPK_OK) return FPK_ECUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   ChArgs a;
+  a.boxed = boxed;
   a.q = static_cast<const uint16_t*>(q);
   a.cu_seqlens = cu_seqlens;
   a.kv_scales = reinterpret_cast<const uint16_t*>(kv_scales);
@@ -1422,9 +1520,10 @@ extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu
   a.by_g = G == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + G - 1) / G);
   a.by_tpp = tpp == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + tpp - 1) / tpp);
   a.sm_scale_log2 = sm_scale * kChLog2e;
+  a.small = units <= kChSmallUnits && static_cast<int64_t>(B) * max_pages <= kChSmallPages;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (launch_dependent(prefill_plan_kernel, 1, kChPlanThreads, 0, s, a) != FPK_OK ||
-      launch_dependent(prefill_attn_kernel, ctas, kChThreads, ChCfg::kSmem, s, a, kmap) != FPK_OK)
+  if ((!a.small && launch_dependent(prefill_plan_kernel, 1, kChPlanThreads, 0, s, a) != FPK_OK) ||
+      launch_dependent(prefill_attn_kernel, ctas, kChThreads, ChCfg::kSmem, s, a, kmap, omap) != FPK_OK)
     return FPK_ECUDA;
   return launch_dependent(prefill_merge_kernel, ctas * kChMergeParts, 32 * kChMergeWarps, 0, s, a);
 }
