@@ -820,9 +820,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (nv < kChBlk || first_hidden < kChBlk) {
             // codes behind the last token: 0; and NaN in tokens that not every row sees (they would reach the others)
             uint32_t hits = 0;
-#pragma unroll
-            for (int t = 0; t < kChBlkTiles; ++t) {
-              uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+#pragma unroll 1
+            for (int t = 0; t < kChBlkTiles; ++t) {  // (tile by tile at the first place, the others moving up: short code)
+              uint32_t w[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const int tok = 16 * t + 4 * k;
@@ -831,7 +831,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 w[k] &= ~nans;
                 hits |= nans;
               }
-              x[t] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+              for (int k = 0; k + 1 < kChBlkTiles; ++k) x[k] = x[k + 1];
+              x[kChBlkTiles - 1] = make_uint4(w[0], w[1], w[2], w[3]);
             }
             if (hits) s_nan[piece % C::kNan] = 1;
           }
