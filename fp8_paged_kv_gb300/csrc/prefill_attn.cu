@@ -6,8 +6,8 @@
 // by token, the heads of a group one after another): one read of a block of K and V
 // serves 256 rows, and a causal border crosses few blocks (32 tokens at 8 heads per
 // group).  Two or three launches, each a dependent of the one before:
-//   plan    dead requests, the work list (one CTA; small ones are made by every CTA of
-//           the next launch itself, which saves this one: 4 us of 18 for 16 tokens)
+//   plan    dead requests, the work list (one CTA; of up to 32 requests and some 16384
+//           rows a warp of every CTA of the next launch makes its part of the list itself)
 //   attn    the list, a CTA per SM
 //   merge   rows whose unit was cut between CTAs, by log-sum-exp
 //
@@ -60,8 +60,8 @@ constexpr float kChGrow = 8.f;  // log2 growth of a maximum that rescales O
 constexpr float kChMinMult = 1e-37f;  // of a row's scale times K's: -inf times it is -inf still
 __device__ __forceinline__ float at_least_min(float mult) { return mult < kChMinMult ? kChMinMult : mult; }  // (a NaN stays one)
 // Costs in the work list, in some 500 cycles: of a block with both tiles at work and with one, of a unit's start.
-constexpr int kChCostPair = 6, kChCostSolo = 3;
-constexpr int kChStartPair = 10, kChStartSolo = 6;
+constexpr int kChCostPair = 6, kChCostSolo = 4;
+constexpr int kChStartPair = 20, kChStartSolo = 16;
 
 constexpr int kChThreads = 512;
 constexpr int kChVWarp = 8, kChLoadWarp = 12, kChMmaWarp = 13, kChPlanWarp = 15;
@@ -70,7 +70,7 @@ constexpr int kChPlanThreads = 1024;
 constexpr int kChTurnSpins = 4096;
 constexpr int kChMergeWarps = 8, kChMergeParts = 16;  // merge: CTAs per cut unit
 constexpr int kChNear = 1024, kChNearUnits = 4096;    // requests and units that the plan keeps in shared memory
-constexpr int kChSmallPages = 8192, kChSmallUnits = kChThreads;  // page table entries and units of a list that every CTA makes
+constexpr int64_t kChSmallRows = 16384, kChSmallPages = 32768;  // of a kv head's rows, and page table entries, without a plan
 
 struct alignas(16) ChUnit {
   int y;       // place in a kv head's line
@@ -110,7 +110,7 @@ struct ChArgs {
   ChStart* start;   // [ctas]
   float2* part_ml;  // partials: [2 ctas][256 rows]
   float* part_o;
-  int small;        // every CTA makes the list
+  int small;        // without a plan
   int boxed;        // 32 rows are whole tokens' heads: results go out by tensor map
   int n_tokens, causal, B, Hq, Hkv, G, page_size, num_pages, max_pages, ctas, zbox;
   uint32_t by_g, by_tpp;
@@ -209,7 +209,6 @@ __device__ __forceinline__ ChRanges ranges_of(int line, int n) {
 }
 
 // Sums of a CTA's threads: the sum of the threads before, and of all.
-template <int kThreads>
 __device__ __forceinline__ int block_scan(int mine, int& all, int* s_sum) {
   const unsigned kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -222,7 +221,7 @@ __device__ __forceinline__ int block_scan(int mine, int& all, int* s_sum) {
   __syncthreads();  // (s_sum's last readers)
   if (lane == 31) s_sum[warp] = incl;
   __syncthreads();
-  int sums = lane < kThreads / 32 ? s_sum[lane] : 0;
+  int sums = s_sum[lane];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(kFull, sums, o);
@@ -233,23 +232,21 @@ __device__ __forceinline__ int block_scan(int mine, int& all, int* s_sum) {
   return incl - mine + (warp > 0 ? below : 0);
 }
 
-struct ChPlanSpace {
-  int sum[32];
-  int base[kChNear + 1], bad[kChNear], y[kChNearUnits];
-};
-
-// The work list, by a CTA, and the ranges of the CTAs c0, c0 + 1, .. c1 - 1.  Few dependent reads: the requests and the
-// units' places stay in shared memory (where there are more than fit, in the workspace), and warps without a request
-// of their own share the others' page tables.
-template <int kThreads>
-__device__ __forceinline__ void make_plan(const ChArgs& a, ChPlanSpace& sp, int c0, int c1) {
+// The work list, and the CTAs' ranges, by one CTA.  Few dependent reads: the requests and the units' places stay in
+// shared memory (where there are more than fit, in the workspace), and warps without a request of their own share the
+// others' page tables.
+__global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const ChArgs a) {
+  __shared__ int s_sum[kChPlanThreads / 32];
+  __shared__ int s_base[kChNear + 1], s_bad[kChNear], s_y[kChNearUnits];
+  griddep_wait();
+  griddep_launch_dependents();
   const unsigned kFull = 0xffffffffu;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  constexpr int kWarps = kThreads / 32;
+  constexpr int kThreads = kChPlanThreads, kWarps = kThreads / 32;
   const bool near = a.B <= kChNear;
-  int32_t* const base = near ? sp.base : a.base;
-  int32_t* const dead = near ? sp.bad : a.dead;
-  for (int i = t; i < min(a.B, kChNear); i += kThreads) sp.bad[i] = 0;
+  int32_t* const base = near ? s_base : a.base;
+  int32_t* const dead = near ? s_bad : a.dead;
+  for (int i = t; i < min(a.B, kChNear); i += kThreads) s_bad[i] = 0;
   __syncthreads();
   // requests that are dead, by a bad page or otherwise
   const int ways = a.B < kWarps ? kWarps / a.B : 1;
@@ -270,7 +267,7 @@ __device__ __forceinline__ void make_plan(const ChArgs& a, ChPlanSpace& sp, int 
     const int r = r0 + t;
     const int rows = r < a.B ? max(0, query_start(a, r + 1) - query_start(a, r)) * a.G : 0;
     int all;
-    const int before = block_scan<kThreads>((rows + kChUnitRows - 1) / kChUnitRows, all, sp.sum);
+    const int before = block_scan((rows + kChUnitRows - 1) / kChUnitRows, all, s_sum);
     if (r < a.B) base[r] = units + before;
     units += all;
   }
@@ -308,13 +305,13 @@ __device__ __forceinline__ void make_plan(const ChArgs& a, ChPlanSpace& sp, int 
 #pragma unroll 1
   for (int x = x0; x < x1; ++x) mine += unit_cost(unit_at(x, r, 0));
   int T;
-  int y = block_scan<kThreads>(mine, T, sp.sum);
+  int y = block_scan(mine, T, s_sum);
   r = lo;
 #pragma unroll 1
   for (int x = x0; x < x1; ++x) {
     const ChUnit u = unit_at(x, r, y);
     a.unit[x] = u;
-    if (x < kChNearUnits) sp.y[x] = y;
+    if (x < kChNearUnits) s_y[x] = y;
     y += unit_cost(u);
   }
   __syncthreads();
@@ -328,14 +325,14 @@ __device__ __forceinline__ void make_plan(const ChArgs& a, ChPlanSpace& sp, int 
 #pragma unroll 1
     while (l < m) {
       const int mid = (l + m + 1) >> 1;
-      if ((near_units ? sp.y[mid] : a.unit[mid].y) <= at) l = mid; else m = mid - 1;
+      if ((near_units ? s_y[mid] : a.unit[mid].y) <= at) l = mid; else m = mid - 1;
     }
     x = l;
     int q = request_of(l);
-    return unit_at(l, q, near_units ? sp.y[l] : a.unit[l].y);
+    return unit_at(l, q, near_units ? s_y[l] : a.unit[l].y);
   };
 #pragma unroll 1
-  for (int c = c0 + t; c < c1; c += kThreads) {
+  for (int c = t; c < a.ctas; c += kThreads) {
     ChStart s = {};
     s.b0 = rg.begin(c);
     s.b1 = rg.begin(c + 1);
@@ -358,11 +355,85 @@ __device__ __forceinline__ void make_plan(const ChArgs& a, ChPlanSpace& sp, int 
   }
 }
 
-__global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const ChArgs a) {
-  __shared__ ChPlanSpace sp;
-  griddep_wait();
-  griddep_launch_dependents();
-  make_plan<kChPlanThreads>(a, sp, 0, a.ctas);
+// The list of up to 32 requests, a lane each, by a warp that keeps it in its registers.
+struct ChSmall {
+  int base, n, c0, L, y;  // of this lane's request: first unit, query tokens, the first of them, context (0: dead), place
+  int units, T;           // of a kv head
+};
+__device__ __forceinline__ ChUnit small_unit(const ChArgs& a, const ChSmall& s, int x) {
+  const unsigned kFull = 0xffffffffu;
+  ChUnit u;
+  u.r = 31 - __clz(__ballot_sync(kFull, s.base <= x));  // (of empty requests the last has units)
+  const int n = __shfl_sync(kFull, s.n, u.r), base = __shfl_sync(kFull, s.base, u.r);
+  u.c0 = __shfl_sync(kFull, s.c0, u.r);
+  u.L = __shfl_sync(kFull, s.L, u.r);
+  u.y = __shfl_sync(kFull, s.y, u.r);
+  u.shift = a.causal ? u.L - n : u.L;
+#pragma unroll 1
+  for (int i = base;; ++i) {
+    u.row0 = (i - base) * kChUnitRows;
+    u.rows = min(kChUnitRows, n * a.G - u.row0);
+    u.tokens = seen(u, quotient(u.row0 + u.rows - 1, a.by_g));
+    if (i == x) return u;
+    u.y += unit_cost(u);
+  }
+}
+// The unit that a place of the line belongs to: the last one that starts at or before it.
+__device__ __forceinline__ ChUnit small_unit_of(const ChArgs& a, const ChSmall& s, int place, int& x, int& h) {
+  const unsigned kFull = 0xffffffffu;
+  h = min(place / s.T, a.Hkv - 1);
+  const int at = place - h * s.T;
+  x = __shfl_sync(kFull, s.base, 31 - __clz(__ballot_sync(kFull, s.n > 0 && s.y <= at)));
+  ChUnit u = small_unit(a, s, x);
+#pragma unroll 1
+  while (x + 1 < s.units && u.y + unit_cost(u) <= at) u = small_unit(a, s, ++x);
+  return u;
+}
+__device__ __forceinline__ void small_plan(const ChArgs& a, unsigned bad, ChSmall& s, ChStart& st) {
+  const unsigned kFull = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  s.n = s.c0 = s.L = 0;
+  if (lane < a.B) {
+    s.c0 = query_start(a, lane);
+    s.n = max(0, query_start(a, lane + 1) - s.c0);
+    s.L = bad >> lane & 1 ? 0 : __ldg(a.seq_lens + lane);
+  }
+  int mine = (s.n * a.G + kChUnitRows - 1) / kChUnitRows, cost = 0;
+  ChUnit u;
+  u.L = s.L;
+  u.shift = a.causal ? s.L - s.n : s.L;
+#pragma unroll 1
+  for (int i = 0; i < mine; ++i) {
+    u.rows = min(kChUnitRows, s.n * a.G - i * kChUnitRows);
+    u.tokens = seen(u, quotient(i * kChUnitRows + u.rows - 1, a.by_g));
+    cost += unit_cost(u);
+  }
+  int x = mine, y = cost;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const int p = __shfl_up_sync(kFull, x, o), q = __shfl_up_sync(kFull, y, o);
+    if (lane >= o) x += p, y += q;
+  }
+  s.units = __shfl_sync(kFull, x, 31);
+  s.T = __shfl_sync(kFull, y, 31);
+  s.base = x - mine;
+  s.y = y - cost;
+  const ChRanges rg = ranges_of(s.T * a.Hkv, a.ctas);
+  st.b0 = rg.begin(blockIdx.x);
+  st.b1 = rg.begin(blockIdx.x + 1);
+  st.units = s.units;
+  st.T = s.T;
+  st.cut = -1;
+  st.unit = st.h = st.cut_h = 0;
+  if (st.b0 >= st.b1) return;
+  st.u = small_unit_of(a, s, st.b0, st.unit, st.h);
+  if (st.b1 == s.T * a.Hkv) return;
+  st.cut_u = small_unit_of(a, s, st.b1, x, st.cut_h);
+  const int at = st.cut_h * s.T + st.cut_u.y, blocks = blocks_of(st.cut_u.tokens);
+  int i0, i1;
+  owned_blocks(st.cut_u, at, st.b0, st.b1, i0, i1);
+  if (i0 == 0 && i1 > 0 && i1 < blocks)
+    st.cut = rg.owner(at + start_cost(st.cut_u.rows) + (blocks - 1) * block_cost(st.cut_u.rows));
 }
 
 struct alignas(16) ChPiece {
@@ -384,13 +455,15 @@ static_assert(sizeof(ChSlot) == ChCfg::kPieceBytes, "slot of the piece ring");
 struct ChCursor {
   int x, h, units, T, b0, b1;
   ChUnit u;
+  ChSmall s;
+  __device__ __forceinline__ ChUnit unit(const ChArgs& a, int i) const { return a.small ? small_unit(a, s, i) : load_unit(a.unit + i); }
 };
 __device__ __forceinline__ bool next_piece(const ChArgs& a, ChCursor& c, ChPiece& p) {
   for (;;) {
     if (c.x == c.units) {
       c.x = 0;
       if (++c.h >= a.Hkv) return false;
-      c.u = load_unit(a.unit);
+      c.u = c.unit(a, 0);
     }
     const int y = c.h * c.T + c.u.y;
     if (y >= c.b1) return false;
@@ -398,7 +471,7 @@ __device__ __forceinline__ bool next_piece(const ChArgs& a, ChCursor& c, ChPiece
     p.h = c.h;
     p.blocks = blocks_of(c.u.tokens);
     owned_blocks(c.u, y, c.b0, c.b1, p.i0, p.i1);
-    if (++c.x < c.units) c.u = load_unit(a.unit + c.x);
+    if (++c.x < c.units) c.u = c.unit(a, c.x);
     if (p.i0 < p.i1 || (p.blocks == 0 && y >= c.b0)) return true;
   }
 }
@@ -625,14 +698,51 @@ __global__ void __launch_bounds__(kChThreads, 1)
   tc_fence_after();
   griddep_wait();  // the plan is there, or what it needs
   griddep_launch_dependents();
+  ChCursor cur;
+  int4 first;
   if (a.small) {
-    // (every CTA writes the same list of units; the space is the queries')
-    make_plan<kChThreads>(a, *reinterpret_cast<ChPlanSpace*>(sm), blockIdx.x, blockIdx.x + 1);
+    // page tables by all warps, the list by one
+    unsigned bad = 0;
+    const int ways = 16 / min(a.B, 16);
+#pragma unroll 1
+    for (int r = warp / ways; r < a.B; r += 16 / ways) {
+      const int L = live_length(a, r), pages = L > 0 ? (L - 1) / a.page_size + 1 : 0;
+      const int32_t* const row = a.page_table + static_cast<int64_t>(r) * a.max_pages;
+      bool out = L == 0;
+#pragma unroll 4
+      for (int i = warp % ways * 32 + lane; i < pages; i += 32 * ways) out |= static_cast<unsigned>(__ldg(row + i)) >= static_cast<unsigned>(a.num_pages);
+      if (__any_sync(kFull, out)) bad |= 1u << r;
+    }
+    int* const s_bad = reinterpret_cast<int*>(sm);  // (the queries' place)
+    if (lane == 0) s_bad[warp] = static_cast<int>(bad);
     __syncthreads();
+    if (warp == kChPlanWarp) {
+      bad = __reduce_or_sync(kFull, lane < 16 ? static_cast<unsigned>(s_bad[lane]) : 0u);
+      ChStart st;
+      small_plan(a, bad, cur.s, st);
+      cur.u = st.u;
+      cur.units = st.units;
+      cur.T = st.T;
+      first = make_int4(st.unit, st.h, st.b0, st.b1);
+      if (lane == 0) {
+        s_bad[16] = st.b0 < st.b1;
+        a.start[blockIdx.x] = st;  // (for the merge)
+      }
+    }
+    __syncthreads();
+    if (warp != kChPlanWarp) first = make_int4(0, 0, 0, s_bad[16]);
+    __syncthreads();
+  } else {
+    const int4* const start = reinterpret_cast<const int4*>(a.start + blockIdx.x);
+    first = __ldcg(start);
+    if (warp == kChPlanWarp) {
+      cur.u = near_unit(__ldcg(start + 1), __ldcg(start + 2));
+      const int4 more_of = __ldcg(start + 3);
+      cur.units = more_of.x;
+      cur.T = more_of.y;
+    }
   }
   const uint32_t tmem = *s_tmem;
-  const int4* const start = reinterpret_cast<const int4*>(a.start + blockIdx.x);
-  const int4 first = __ldcg(start);
   auto wait = [&](int i, uint32_t parity) { tc_wait(bar(i), parity & 1u, a.status, s_failed); };
   uint32_t pn = 0;
   auto take_piece = [&](ChPiece& p) -> bool {
@@ -648,15 +758,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
     const int tpp = a.page_size >> 4;
     if (warp == kChPlanWarp) {
       // ===================== pieces and scales, ahead of the other warps =====================
-      ChCursor cur;
       cur.x = first.x;
       cur.h = first.y;
       cur.b0 = first.z;
       cur.b1 = first.w;
-      cur.u = near_unit(__ldcg(start + 1), __ldcg(start + 2));
-      const int4 more_of = __ldcg(start + 3);
-      cur.units = more_of.x;
-      cur.T = more_of.y;
       int qset = 0, t0 = 0;
       uint32_t j = 0;  // blocks whose scales are out
       bool more = true;
@@ -1522,7 +1627,7 @@ extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu
   a.by_g = G == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + G - 1) / G);
   a.by_tpp = tpp == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + tpp - 1) / tpp);
   a.sm_scale_log2 = sm_scale * kChLog2e;
-  a.small = units <= kChSmallUnits && static_cast<int64_t>(B) * max_pages <= kChSmallPages;
+  a.small = B <= 32 && static_cast<int64_t>(n_tokens) * G <= kChSmallRows && static_cast<int64_t>(B) * max_pages <= kChSmallPages;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((!a.small && launch_dependent(prefill_plan_kernel, 1, kChPlanThreads, 0, s, a) != FPK_OK) ||
       launch_dependent(prefill_attn_kernel, ctas, kChThreads, ChCfg::kSmem, s, a, kmap, omap) != FPK_OK)
