@@ -1357,8 +1357,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4*>(mine + (c >> 1) * 4096 + ((((c & 1) * 4 + i) ^ (lane & 7)) << 4)) =
-                  none ? make_uint4(0, 0, 0, 0)
-                       : make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                  make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
                                     pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
           }
           fence_proxy_async_smem();
@@ -1378,14 +1377,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
             if (valid && whole) {
               uint32_t y[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = none ? 0u : pack_bf16x2(x[2 * i], x[2 * i + 1]);
+              for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
               st_global_u8(a.out + orow * kChDim + d, y);
             } else if (valid) {
 #pragma unroll
               for (int k = 0; k < 16; k += 8) {
                 float y[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = none ? 0.f : x[k + i];
+                for (int i = 0; i < 8; ++i) y[i] = x[k + i];
                 st_global8(a.part_o + slot * kChDim + d + k, y);
               }
             }
