@@ -1,7 +1,8 @@
 """Device-resident decode pool: torch allocates, libfp8kv computes.
 
 A DecodePool holds one layer's paged KV pool (e4m3 or bf16), the page table,
-the live and expected page tags, the per-tensor scales and the output and
+the live and expected page tags, the scales (per tensor, or with block_scales one
+per 16 tokens and kv head of an e4m3 pool) and the output and
 workspace buffers of a decode batch, and runs the decode step in the order
 the pages describe: write the new token's K/V into its page, check every
 request's (page, tag) mapping in a separate batched operation, then attend
@@ -14,13 +15,16 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (fpk_decode_append_check_bf16, fpk_decode_append_check_fp8, fpk_decode_step_bf16,
-               fpk_decode_step_fp8, fpk_decode_workspace_bytes, fpk_kv_append_bf16, fpk_kv_append_fp8,
-               fpk_kv_compact, fpk_kv_fork, fpk_kv_prefill_bf16, fpk_kv_prefill_fp8,
+from . import (block_scales as new_block_scales, fpk_decode_append_check_bf16, fpk_decode_append_check_fp8,
+               fpk_decode_step_bf16, fpk_decode_step_fp8, fpk_decode_workspace_bytes, fpk_kv_append_bf16,
+               fpk_kv_append_fp8, fpk_kv_append_fp8_block, fpk_kv_compact, fpk_kv_compact_block, fpk_kv_fork,
+               fpk_kv_fork_block, fpk_kv_prefill_bf16, fpk_kv_prefill_fp8, fpk_kv_prefill_fp8_block,
                fpk_page_tags_bump, fpk_page_tags_validate, fpk_paged_decode_attn_bf16,
                fpk_paged_decode_attn_bf16_prefix, fpk_paged_decode_attn_fp8,
-               fpk_paged_decode_attn_fp8_prefix, fpk_paged_decode_attn_fp8_tc,
-               fpk_prefix_workspace_bytes, fpk_rope_append_bf16, fpk_rope_append_fp8)
+               fpk_paged_decode_attn_fp8_block, fpk_paged_decode_attn_fp8_prefix, fpk_paged_decode_attn_fp8_tc,
+               fpk_paged_prefill_attn_fp8_block, fpk_prefill_workspace_bytes, fpk_prefix_workspace_bytes,
+               fpk_rope_append_bf16, fpk_rope_append_fp8, fpk_rope_append_fp8_block, fpk_rope_prefill_bf16,
+               fpk_rope_prefill_fp8, fpk_rope_prefill_fp8_block)
 
 NAN_E4M3 = 0x7F          # e4m3 NaN code: fills slots no token was written to
 NAN_BF16 = 0x7FC0
@@ -55,9 +59,17 @@ def _arena(device, specs):
 
 class DecodePool:
     def __init__(self, wl, fp8: bool = True, device="cuda", num_splits: int | None = None,
-                 tensor_cores: bool = False):
+                 tensor_cores: bool = False, block_scales: bool = False, prompt_tokens: int = 0):
+        if block_scales and (not fp8 or tensor_cores):
+            raise ValueError("block scales belong to an e4m3 pool, read by its own attention kernels")
+        if prompt_tokens and not block_scales:
+            raise ValueError("attend_prompt() reads a pool with block scales")
         self.wl = wl
         self.fp8 = fp8
+        # a scale per 16 tokens and kv head, which the writes find (kv_scales), instead of
+        # wl.k_scale and wl.v_scale; prompt_tokens: the most query rows of one attend_prompt()
+        self.block_scales = block_scales
+        self.prompt_tokens = prompt_tokens
         # FP8 attention on the tcgen05 tensor cores (fpk_paged_decode_attn_fp8_tc)
         # instead of the warp-level kernel; attend() only
         self.tensor_cores = tensor_cores
@@ -68,6 +80,11 @@ class DecodePool:
             self.kv_pool = torch.full((n,), NAN_E4M3, dtype=torch.uint8, device=dev)
         else:
             self.kv_pool = torch.full((n,), NAN_BF16, dtype=torch.int16, device=dev).view(torch.bfloat16)
+        if block_scales:
+            self.kv_scales = new_block_scales(wl.num_pages, wl.Hkv, wl.page_size, device=dev)
+            if prompt_tokens:     # made here, as attend_shared()'s below
+                ws = fpk_prefill_workspace_bytes(wl.B, prompt_tokens, wl.Hq, wl.Hkv)
+                self.prompt_workspace = torch.zeros(ws, dtype=torch.uint8, device=dev)
         self.page_table = to_device(wl.page_table, dev)
         self.live_tags = to_device(wl.live_tags, dev)
         self.expected_tags = to_device(wl.expected_tags, dev)
@@ -113,6 +130,15 @@ class DecodePool:
         w = self.wl
         return dict(Hkv=w.Hkv, D=w.D, page_size=w.page_size, num_pages=w.num_pages)
 
+    @property
+    def kw_block(self):
+        w = self.wl
+        return dict(Hkv=w.Hkv, page_size=w.page_size, num_pages=w.num_pages)
+
+    def _per_tensor_only(self, what):
+        if self.block_scales:
+            raise ValueError(f"{what} takes a pool with per-tensor scales")
+
     # ---------------------------------------------------------------- writes
     def prefill(self, chunk_tokens: int = 1 << 22):
         """Bulk-write every request's prompt (positions 0..prompt_len-1)."""
@@ -130,7 +156,10 @@ class DecodePool:
             cu_sub = to_device((cu[r0:r1 + 1] - cu[r0]).astype(np.int32), self.device)
             pt = self.page_table[r0:r1]
             ex = self.expected_tags[r0:r1]
-            if self.fp8:
+            if self.block_scales:
+                fpk_kv_prefill_fp8_block(k, v, cu_sub, None, self.kv_pool, self.kv_scales, pt,
+                                         self.live_tags, ex, None, **self.kw)
+            elif self.fp8:
                 fpk_kv_prefill_fp8(k, v, cu_sub, self.kv_pool, self.k_scale, self.v_scale,
                                    pt, self.live_tags, ex, None, **self.kw)
             else:
@@ -157,7 +186,10 @@ class DecodePool:
 
     def append(self, stream=None, guard: bool = True):
         tags = (self.live_tags, self.expected_tags, self.abort_mask) if guard else (None, None, None)
-        if self.fp8:
+        if self.block_scales:
+            fpk_kv_append_fp8_block(self.k_new, self.v_new, self.kv_pool, self.kv_scales, self.page_table,
+                                    self.seq_lens, *tags, stream=stream, **self.kw)
+        elif self.fp8:
             fpk_kv_append_fp8(self.k_new, self.v_new, self.kv_pool, self.k_scale,
                               self.v_scale, self.page_table, self.seq_lens, *tags, stream=stream,
                               **self.kw)
@@ -184,7 +216,10 @@ class DecodePool:
         mask = self.abort_mask if use_mask else None
         kw = dict(Hkv=wl.Hkv, page_size=wl.page_size, num_pages=wl.num_pages,
                   sm_scale=wl.sm_scale, num_splits=ns, stream=stream)
-        if self.fp8:
+        if self.block_scales:
+            fpk_paged_decode_attn_fp8_block(self.q, self.kv_pool, self.kv_scales, self.page_table, self.seq_lens,
+                                            mask, self.out, self.lse, self.workspace, **kw)
+        elif self.fp8:
             attn = fpk_paged_decode_attn_fp8_tc if self.tensor_cores else fpk_paged_decode_attn_fp8
             attn(self.q, self.kv_pool, self.k_scale, self.v_scale, self.page_table, self.seq_lens,
                  mask, self.out, self.lse, self.workspace, **kw)
@@ -197,6 +232,7 @@ class DecodePool:
         lse as attend().  group_starts int32 [n + 1] and prefix_lens int32 [n] on the
         device: requests [group_starts[g], group_starts[g + 1]) share their first
         prefix_lens[g] tokens' pages."""
+        self._per_tensor_only("attend_shared()")
         wl = self.wl
         mask = self.abort_mask if use_mask else None
         args = (self.page_table, self.seq_lens, mask, group_starts, prefix_lens, self.out16, self.lse,
@@ -208,16 +244,32 @@ class DecodePool:
         else:
             fpk_paged_decode_attn_bf16_prefix(self.q, self.kv_pool, *args, **kw)
 
+    def attend_prompt(self, q, cu_seqlens, out, lse, causal: bool = True, use_mask: bool = True, stream=None):
+        """Attention of several rows per request, q[cu_seqlens[r]:cu_seqlens[r + 1]] (bf16): with
+        causal the request's last tokens, already written, so that each sees those up to itself (a
+        prompt or a chunk of one, drafts to verify); without it rows that see all seq_lens[r]
+        tokens (an encoder's states).  bf16 results in out [rows][Hq][D], lse [rows][Hq]; up to
+        prompt_tokens rows of a pool with block_scales."""
+        if q.shape[0] > self.prompt_tokens:
+            raise ValueError(f"{q.shape[0]} rows in a pool made for prompt_tokens={self.prompt_tokens}")
+        fpk_paged_prefill_attn_fp8_block(q, cu_seqlens, self.kv_pool, self.kv_scales, self.page_table, self.seq_lens,
+                                         self.abort_mask if use_mask else None, out, lse, self.prompt_workspace,
+                                         causal=causal, sm_scale=self.wl.sm_scale, stream=stream, **self.kw_block)
+
     # ------------------------------------------------ forks, moves, rotations
     def fork(self, parent, child, fresh, stream=None):
         """Rows child[i] take over rows parent[i] (int32 device tensors; fresh: PageLedger.fork)."""
-        fpk_kv_fork(self.kv_pool, self.page_table, self.expected_tags, self.seq_lens, self.live_tags,
-                    self.abort_mask, parent, child, fresh, stream=stream, **self.kw)
+        pool, fork = (((self.kv_pool, self.kv_scales), fpk_kv_fork_block) if self.block_scales
+                      else ((self.kv_pool,), fpk_kv_fork))
+        fork(*pool, self.page_table, self.expected_tags, self.seq_lens, self.live_tags,
+             self.abort_mask, parent, child, fresh, stream=stream, **self.kw)
 
     def compact(self, src, dst, stream=None):
         """Pages src[i] move to dst[i] (int32 device tensors from PageLedger.compact)."""
-        fpk_kv_compact(self.kv_pool, self.page_table, self.expected_tags, self.seq_lens, self.live_tags,
-                       src, dst, stream=stream, **self.kw)
+        pool, compact = (((self.kv_pool, self.kv_scales), fpk_kv_compact_block) if self.block_scales
+                         else ((self.kv_pool,), fpk_kv_compact))
+        compact(*pool, self.page_table, self.expected_tags, self.seq_lens, self.live_tags,
+                src, dst, stream=stream, **self.kw)
 
     def rope_append(self, inv_freq, *, rot_dim=None, interleaved=False, rot_scale=1.0, guard=True,
                     stream=None):
@@ -227,15 +279,35 @@ class DecodePool:
         kw = dict(Hkv=wl.Hkv, page_size=wl.page_size, num_pages=wl.num_pages,
                   rot_dim=wl.D if rot_dim is None else rot_dim, interleaved=interleaved,
                   rot_scale=rot_scale, stream=stream)
-        if self.fp8:
+        if self.block_scales:
+            fpk_rope_append_fp8_block(self.q, self.k_new, self.v_new, inv_freq, self.q, self.kv_pool, self.kv_scales,
+                                      self.page_table, self.seq_lens, *tags, **kw)
+        elif self.fp8:
             fpk_rope_append_fp8(self.q, self.k_new, self.v_new, inv_freq, self.q, self.kv_pool,
                                 self.k_scale, self.v_scale, self.page_table, self.seq_lens, *tags, **kw)
         else:
             fpk_rope_append_bf16(self.q, self.k_new, self.v_new, inv_freq, self.q, self.kv_pool,
                                  self.page_table, self.seq_lens, *tags, **kw)
 
+    def rope_prefill(self, q, k, v, cu_seqlens, start_pos, inv_freq, *, rot_dim=None, interleaved=False,
+                     rot_scale=1.0, guard=True, stream=None):
+        """A prompt or a chunk of one with rotary positions: request r's rows start at position
+        start_pos[r] (None: 0); q is rotated in place, k on its way into the cache."""
+        wl = self.wl
+        tags = (self.live_tags, self.expected_tags, None) if guard else (None, None, None)
+        kw = dict(rot_dim=wl.D if rot_dim is None else rot_dim, interleaved=interleaved, rot_scale=rot_scale,
+                  stream=stream, **self.kw_block)
+        rows = (q, k, v, cu_seqlens, start_pos, inv_freq, q, self.kv_pool)
+        if self.block_scales:
+            fpk_rope_prefill_fp8_block(*rows, self.kv_scales, self.page_table, *tags, **kw)
+        elif self.fp8:
+            fpk_rope_prefill_fp8(*rows, self.k_scale, self.v_scale, self.page_table, *tags, **kw)
+        else:
+            fpk_rope_prefill_bf16(*rows, self.page_table, *tags, **kw)
+
     def append_check(self, stream=None):
         """The step's cache write and batched tag check in one launch."""
+        self._per_tensor_only("append_check()")
         if self.fp8:
             fpk_decode_append_check_fp8(self.k_new, self.v_new, self.kv_pool, self.k_scale,
                                         self.v_scale, self.page_table, self.seq_lens,
@@ -253,12 +325,13 @@ class DecodePool:
         the check (fpk_decode_step_*).  Without it (the no-op tracker): the same
         two launches with no tag check -- the write unguarded, attention over
         every request.  With count_aborts the check runs as its own launch so
-        that it also produces the device-side count."""
+        that it also produces the device-side count, and so it does with block_scales."""
         main = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if validate and self.count_aborts:
-            self.append(stream=main)
-            self.validate(stream=main)
-            self.attend(use_mask=True, stream=main)
+        if self.block_scales or (validate and self.count_aborts):
+            self.append(stream=main, guard=validate)
+            if validate:
+                self.validate(stream=main)
+            self.attend(use_mask=validate, stream=main)
             return
         wl = self.wl
         kw = dict(Hkv=wl.Hkv, page_size=wl.page_size, num_pages=wl.num_pages,
@@ -361,15 +434,18 @@ class HostPipeline:
 
 
 def admission_cap(budget_bytes: int, context: int, *, Hkv: int, D: int, page_size: int,
-                  fp8: bool):
+                  fp8: bool, block_scales: bool = False):
     """Requests of `context` tokens a one-layer KV pool of `budget_bytes` admits.
 
     A page holds K and V of page_size tokens for every kv head: 2*Hkv*page_size*D
-    elements of 1 byte (e4m3) or 2 (bf16).  The pool has floor(budget / page
+    elements of 1 byte (e4m3) or 2 (bf16), and with block_scales a byte for K and
+    for V of every 16 tokens and kv head.  The pool has floor(budget / page
     bytes) pages and a request needs ceil(context / page_size) of them.
     Returns (pages in the pool, pages per request, requests admitted).
     """
     page_bytes = 2 * Hkv * page_size * D * (1 if fp8 else 2)
+    if block_scales:
+        page_bytes += 2 * Hkv * (page_size // 16)
     pages = budget_bytes // page_bytes
     per_request = -(-context // page_size)
     return pages, per_request, (pages // per_request if per_request else 0)
