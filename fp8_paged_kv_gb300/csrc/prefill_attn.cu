@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       const float sign = a.sm_scale_log2 < 0.f ? -1.f : 1.f;  // a negative scale's sign goes to the query
       uint32_t j = 0, used = 0, phases = 0;  // V blocks; query buffers used before, and the parities of their frees
       // The piece whose blocks are converted (i .. p.i1 to go), and the next one, whose queries are: steps at .. n of
-      // four rows (eight lanes a row, 16 dims each; warp vw rows 32 vw .. of a tile).
+      // 16 rows, four a warp (eight lanes a row, 16 dims each).
       ChPiece next;
       p.i0 = p.i1 = 0;
       int i = 0, at = 0, n = 0, least = 0;
@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       auto ask = [&](int s0) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int s = s0 + k, row = next.u.row0 + 32 * vw + (lane >> 3) + 128 * (s >> 3) + 4 * (s & 7);
+          const int s = s0 + k, row = next.u.row0 + 16 * s + 4 * vw + (lane >> 3);
           q[k][0] = q[k][1] = make_uint4(0, 0, 0, 0);
           if (s < n && row < next.u.row0 + next.u.rows) {
             // (query token row / G, head row % G of the group)
@@ -1031,13 +1031,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
               for (int e = 0; e < 4; ++e) z[k][e] = f16x4_to_e4m3x4(w[k][2 * e], w[k][2 * e + 1]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const int row = 32 * vw + 4 * ((at + k) & 7) + (lane >> 3);  // of the tile
+              const int row = 16 * ((at + k) & 7) + 4 * vw + (lane >> 3);  // of the tile
               uint8_t* const dst = sm + buf * C::kQTile + row * 128 + ((c ^ (row & 7)) << 4);
               *reinterpret_cast<uint4*>(dst) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
               *reinterpret_cast<uint4*>(dst + 16384) = make_uint4(z[k][0], z[k][1], z[k][2], z[k][3]);
               if (c == 0) s_exp[buf * 128 + row] = static_cast<int8_t>(ex[k]);
             }
-            if ((at & 7) == 6) {
+            if ((at & 7) == 6 || at + 2 == n) {
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(C::kBarQ + buf));
@@ -1049,7 +1049,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           ended = !take_piece(next);
           known = true;
           at = 0;
-          n = ended || next.i0 == next.i1 ? 0 : next.pair() ? 16 : 8;
+          n = ended || next.i0 == next.i1 ? 0 : (next.u.rows + 31) / 32 * 2;  // (what lies behind the last row stays what it was)
           ask(0);
           if (d == 0) s_nan[(pn - 1 + C::kNan / 2) % C::kNan] = 0;
         }
