@@ -131,7 +131,7 @@ struct ChCfg {
   static constexpr int kOffV16 = kOffK + kKStages * kKStage;
   static constexpr int kOffPiece = kOffV16 + kV16Bufs * kV16;
   static constexpr int kOffScale = kOffPiece + kChPieces * kPieceBytes;  // float2 [kScales][8]: K's factor, V's exponent
-  static constexpr int kOffTile = kOffScale + kScales * kChBlkTiles * 8;  // int [kScales][8]: the pool's tiles, -1: none
+  static constexpr int kOffTile = kOffScale + kScales * kChBlkTiles * 8;  // int [kScales][8]: the pool's tiles (0 behind the last)
   static constexpr int kOffMult = kOffTile + kScales * kChBlkTiles * 4;
   static constexpr int kOffBars = kOffMult + kQTiles * 128;
   static constexpr int kBarKFull = 0;
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             if (j >= C::kScales) wait(C::kBarScaleFree + st, j / C::kScales - 1);
             if (lane >> 3 == k) {
               s_scale[st * kChBlkTiles + (lane & 7)] = x;
-              s_tile[st * kChBlkTiles + (lane & 7)] = place;
+              s_tile[st * kChBlkTiles + (lane & 7)] = max(place, 0);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::kBarScale + st));
@@ -887,12 +887,15 @@ __global__ void __launch_bounds__(kChThreads, 1)
       uint32_t piece = 0;
       bool known = false, ended = false;
       uint4 x[kChBlkTiles];
-      auto fetch = [&](uint32_t b, int t) {
-        const int tile = s_tile[b % C::kScales * kChBlkTiles + t];
-        x[t] = make_uint4(0, 0, 0, 0);
-        if (tile >= 0)
-          x[t] = ld_stream(a.kv_pool + static_cast<int64_t>(tile) * (2 * kChTile * kChDim) + kChTile * kChDim + d * 16);
+      const uint8_t* const codes = a.kv_pool + kChTile * kChDim + d * 16;
+      int place[kChBlkTiles];  // of a block's tiles
+      auto places = [&](uint32_t b) {
+        const int4* const at = reinterpret_cast<const int4*>(s_tile + b % C::kScales * kChBlkTiles);
+        const int4 lo = at[0], hi = at[1];
+        place[0] = lo.x, place[1] = lo.y, place[2] = lo.z, place[3] = lo.w;
+        place[4] = hi.x, place[5] = hi.y, place[6] = hi.z, place[7] = hi.w;
       };
+      auto fetch = [&](int t) { x[t] = ld_stream(codes + static_cast<int64_t>(place[t]) * (2 * kChTile * kChDim)); };
       uint4 q[2][2];
       auto ask = [&](int s0) {
 #pragma unroll
@@ -942,7 +945,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
             }
             if (hits) s_nan[piece % C::kNan] = 1;
           }
-          if (more) wait(C::kBarScale + (j + 1) % C::kScales, (j + 1) / C::kScales);
+          if (more) {
+            wait(C::kBarScale + (j + 1) % C::kScales, (j + 1) / C::kScales);
+            places(j + 1);
+          }
           if (j >= C::kV16Bufs) wait(C::kBarUsed + buf, j / C::kV16Bufs - 1);
           uint8_t* const o = sm + C::kOffV16 + buf * C::kV16 + d * 16;
 #pragma unroll
@@ -956,7 +962,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             uint4* const w = reinterpret_cast<uint4*>(o + t * kChTile * kChDim * 2);
             w[0] = make_uint4(y[0], y[1], y[2], y[3]);
             w[128] = make_uint4(y[4], y[5], y[6], y[7]);
-            if (more) fetch(j + 1, t);
+            if (more) fetch(t);
           }
           fence_proxy_async_smem();
           if (more) fetched(j + 1);
@@ -1045,7 +1051,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           }
         }
         // ---- the next piece, once it is known; it is waited for when there is nothing else to do
-        if (!known && (i == p.i1 || __all_sync(kFull, mbar_test(bar(C::kBarPiece + pn % kChPieces), pn / kChPieces & 1)))) {
+        if (!known && p.i1 - i <= C::kScales && (i == p.i1 || __all_sync(kFull, mbar_test(bar(C::kBarPiece + pn % kChPieces), pn / kChPieces & 1)))) {
           ended = !take_piece(next);
           known = true;
           at = 0;
@@ -1063,8 +1069,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
           least = seen(p.u, quotient(p.u.row0, a.by_g));  // tokens that every row sees
           if (i < p.i1) {
             wait(C::kBarScale + j % C::kScales, j / C::kScales);
+            places(j);
 #pragma unroll
-            for (int t = 0; t < kChBlkTiles; ++t) fetch(j, t);
+            for (int t = 0; t < kChBlkTiles; ++t) fetch(t);
             fetched(j);
           }
         }
