@@ -150,7 +150,7 @@ def measured_peaks():
 
 
 # the sources compiled into the attention kernel's translation unit
-KERNEL_SOURCES = ("decode_attn.cu", "attn_plan.cuh", "common.cuh", "step_ops.cuh", "quant.cuh")
+KERNEL_SOURCES = ("decode_attn.cu", "attn_plan.cuh", "block_scale.cuh", "common.cuh", "step_ops.cuh", "quant.cuh")
 
 
 def _strip_comments(src: str) -> str:
