@@ -360,34 +360,55 @@ struct ChSmall {
   int base, n, c0, L, y;  // of this lane's request: first unit, query tokens, the first of them, context (0: dead), place
   int units, T;           // of a kv head
 };
-__device__ __forceinline__ ChUnit small_unit(const ChArgs& a, const ChSmall& s, int x) {
+// Unit i of request r, at place y.
+__device__ __forceinline__ ChUnit small_unit(const ChArgs& a, const ChSmall& s, int r, int i, int y) {
   const unsigned kFull = 0xffffffffu;
+  const int n = __shfl_sync(kFull, s.n, r);
   ChUnit u;
-  u.r = 31 - __clz(__ballot_sync(kFull, s.base <= x));  // (of empty requests the last has units)
-  const int n = __shfl_sync(kFull, s.n, u.r), base = __shfl_sync(kFull, s.base, u.r);
-  u.c0 = __shfl_sync(kFull, s.c0, u.r);
-  u.L = __shfl_sync(kFull, s.L, u.r);
-  u.y = __shfl_sync(kFull, s.y, u.r);
+  u.r = r;
+  u.y = y;
+  u.c0 = __shfl_sync(kFull, s.c0, r);
+  u.L = __shfl_sync(kFull, s.L, r);
   u.shift = a.causal ? u.L - n : u.L;
-#pragma unroll 1
-  for (int i = base;; ++i) {
-    u.row0 = (i - base) * kChUnitRows;
-    u.rows = min(kChUnitRows, n * a.G - u.row0);
-    u.tokens = seen(u, quotient(u.row0 + u.rows - 1, a.by_g));
-    if (i == x) return u;
-    u.y += unit_cost(u);
-  }
+  u.row0 = i * kChUnitRows;
+  u.rows = min(kChUnitRows, n * a.G - u.row0);
+  u.tokens = seen(u, quotient(u.row0 + u.rows - 1, a.by_g));
+  return u;
 }
-// The unit that a place of the line belongs to: the last one that starts at or before it.
+// The unit behind u, x of all: of the same request, or the first of the next one that has any (of several that begin
+// at x the last has units).
+__device__ __forceinline__ ChUnit small_next(const ChArgs& a, const ChSmall& s, const ChUnit& u, int x) {
+  const int r = 31 - __clz(__ballot_sync(0xffffffffu, s.base <= x));
+  return small_unit(a, s, r, r == u.r ? u.row0 / kChUnitRows + 1 : 0, u.y + unit_cost(u));
+}
+__device__ __forceinline__ ChUnit small_first(const ChArgs& a, const ChSmall& s) {
+  return small_unit(a, s, 31 - __clz(__ballot_sync(0xffffffffu, s.base <= 0)), 0, 0);
+}
+// The unit that a place of the line belongs to: the last one that starts at or before it.  A lane looks at a unit.
 __device__ __forceinline__ ChUnit small_unit_of(const ChArgs& a, const ChSmall& s, int place, int& x, int& h) {
   const unsigned kFull = 0xffffffffu;
   h = min(place / s.T, a.Hkv - 1);
-  const int at = place - h * s.T;
-  x = __shfl_sync(kFull, s.base, 31 - __clz(__ballot_sync(kFull, s.n > 0 && s.y <= at)));
-  ChUnit u = small_unit(a, s, x);
+  const int at = place - h * s.T, r = 31 - __clz(__ballot_sync(kFull, s.n > 0 && s.y <= at));
+  const int base = __shfl_sync(kFull, s.base, r), n = __shfl_sync(kFull, s.n, r);
+  int y = __shfl_sync(kFull, s.y, r), i = 0;
 #pragma unroll 1
-  while (x + 1 < s.units && u.y + unit_cost(u) <= at) u = small_unit(a, s, ++x);
-  return u;
+  for (int i0 = 0;; i0 += 32) {
+    const ChUnit mine = small_unit(a, s, r, i0 + (threadIdx.x & 31), 0);
+    const int cost = mine.rows > 0 ? unit_cost(mine) : 0;
+    int ends = cost;  // of this lane's unit
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int p = __shfl_up_sync(kFull, ends, o);
+      if ((threadIdx.x & 31) >= o) ends += p;
+    }
+    const unsigned behind = __ballot_sync(kFull, mine.rows > 0 && y + ends <= at);  // units that end at or before the place
+    const int passed = __popc(behind);
+    i = i0 + passed;
+    y += passed > 0 ? __shfl_sync(kFull, ends, passed - 1) : 0;
+    if (passed < 32 || (i0 + 32) * kChUnitRows >= n * a.G) break;
+  }
+  x = base + i;
+  return small_unit(a, s, r, i, y);
 }
 __device__ __forceinline__ void small_plan(const ChArgs& a, unsigned bad, ChSmall& s, ChStart& st) {
   const unsigned kFull = 0xffffffffu;
@@ -456,14 +477,13 @@ struct ChCursor {
   int x, h, units, T, b0, b1;
   ChUnit u;
   ChSmall s;
-  __device__ __forceinline__ ChUnit unit(const ChArgs& a, int i) const { return a.small ? small_unit(a, s, i) : load_unit(a.unit + i); }
 };
 __device__ __forceinline__ bool next_piece(const ChArgs& a, ChCursor& c, ChPiece& p) {
   for (;;) {
     if (c.x == c.units) {
       c.x = 0;
       if (++c.h >= a.Hkv) return false;
-      c.u = c.unit(a, 0);
+      c.u = a.small ? small_first(a, c.s) : load_unit(a.unit);
     }
     const int y = c.h * c.T + c.u.y;
     if (y >= c.b1) return false;
@@ -471,7 +491,7 @@ __device__ __forceinline__ bool next_piece(const ChArgs& a, ChCursor& c, ChPiece
     p.h = c.h;
     p.blocks = blocks_of(c.u.tokens);
     owned_blocks(c.u, y, c.b0, c.b1, p.i0, p.i1);
-    if (++c.x < c.units) c.u = c.unit(a, c.x);
+    if (++c.x < c.units) c.u = a.small ? small_next(a, c.s, c.u, c.x) : load_unit(a.unit + c.x);
     if (p.i0 < p.i1 || (p.blocks == 0 && y >= c.b0)) return true;
   }
 }
