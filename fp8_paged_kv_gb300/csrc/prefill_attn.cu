@@ -112,6 +112,7 @@ struct ChArgs {
   float* part_o;
   int small;        // without a plan
   int boxed;        // 32 rows are whole tokens' heads: results go out by tensor map
+  int most;         // units of a kv head that there can be
   int n_tokens, causal, B, Hq, Hkv, G, page_size, num_pages, max_pages, ctas, zbox;
   uint32_t by_g, by_tpp;
   float sm_scale_log2;
@@ -269,7 +270,11 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
     int all;
     const int before = block_scan((rows + kChUnitRows - 1) / kChUnitRows, all, s_sum);
     if (r < a.B) base[r] = units + before;
-    units += all;
+    units = min(units + all, a.most + 1);
+  }
+  if (units > a.most) {  // cu_seqlens that decrease: the list has no place for them, nothing is answered
+    if (t == 0) atomicOr(a.status, kStatusBadStart);
+    units = 0;
   }
   if (t == 0) base[a.B] = units;
   __syncthreads();
@@ -437,6 +442,10 @@ __device__ __forceinline__ void small_plan(const ChArgs& a, unsigned bad, ChSmal
   }
   s.units = __shfl_sync(kFull, x, 31);
   s.T = __shfl_sync(kFull, y, 31);
+  if (s.units > a.most) {  // (as in the plan)
+    if (lane == 0 && blockIdx.x == 0) atomicOr(a.status, kStatusBadStart);
+    s.units = s.T = 0;
+  }
   s.base = x - mine;
   s.y = y - cost;
   const ChRanges rg = ranges_of(s.T * a.Hkv, a.ctas);
@@ -1639,6 +1648,7 @@ extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu
   a.start = reinterpret_cast<ChStart*>(ws + l.start);
   a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
   a.part_o = reinterpret_cast<float*>(ws + l.o);
+  a.most = static_cast<int>(units);
   a.n_tokens = n_tokens;
   a.causal = causal != 0;
   a.B = B;

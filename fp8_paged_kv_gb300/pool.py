@@ -250,7 +250,7 @@ class DecodePool:
         prompt or a chunk of one, drafts to verify); without it rows that see all seq_lens[r]
         tokens (an encoder's states).  bf16 results in out [rows][Hq][D], lse [rows][Hq]; up to
         prompt_tokens rows of a pool with block_scales."""
-        if q.shape[0] > self.prompt_tokens:
+        if not self.prompt_tokens or q.shape[0] > self.prompt_tokens:
             raise ValueError(f"{q.shape[0]} rows in a pool made for prompt_tokens={self.prompt_tokens}")
         fpk_paged_prefill_attn_fp8_block(q, cu_seqlens, self.kv_pool, self.kv_scales, self.page_table, self.seq_lens,
                                          self.abort_mask if use_mask else None, out, lse, self.prompt_workspace,

@@ -149,6 +149,15 @@ def test_decode_dead_requests():
     check(s, run(s, mask=[0, 0, 1, 0, 0]), dead=(1, 2, 3, 4))
 
 
+@pytest.mark.parametrize("spread", [0, 10, 40])
+@pytest.mark.parametrize("causal", [True, False])
+def test_chunks_scales_far_apart(spread, causal):
+    s = scene([400, 100], [150, 40], Hq=16, Hkv=2, ps=16, seed=spread, spread=0)
+    rng = np.random.default_rng(spread)
+    s["scales"][..., 1] = 127 + rng.integers(-spread - 7, spread - 7 + 1, s["scales"].shape[:-1]).clip(-50, 30)
+    check(s, run(s, causal=causal), causal=causal)
+
+
 GEOMETRIES = [(64, 8, 16), (10, 2, 64), (7, 7, 48), (7, 1, 256), (32, 8, 32), (6, 1, 16)]
 
 

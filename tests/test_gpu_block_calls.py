@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from block_helpers import D, bf16
-from fp8_paged_kv_gb300 import (FpkError, block_scales, fpk_decode_workspace_bytes, fpk_kv_compact_block, fpk_kv_fork_block,
+from fp8_paged_kv_gb300 import (FpkError, block_scales, fpk_decode_status, fpk_decode_workspace_bytes, fpk_kv_compact_block, fpk_kv_fork_block,
                                 fpk_paged_decode_attn_fp8_block, fpk_paged_prefill_attn_fp8_block,
                                 fpk_prefill_workspace_bytes, fpk_rope_append_fp8_block, fpk_rope_prefill_fp8_block)
 from fp8_paged_kv_gb300.rope import rope_inv_freq
@@ -263,3 +263,18 @@ def test_small_workspace_and_wrong_buffers_are_refused():
     fpk_paged_prefill_attn_fp8_block(**good, Hkv=2, page_size=16, num_pages=s["P"], sm_scale=SM)
     torch.cuda.synchronize()
     check(s, (bf16(good["out"]), run(s, causal=True)[1]), causal=True)
+
+
+@pytest.mark.parametrize("B", [5, 41])
+def test_query_starts_that_decrease(B):
+    """More rows than there are: the status word says so, and no row is written."""
+    n = 256       # tokens, 8 units; every second request has them all
+    s = scene([40], [1], Hq=64, Hkv=8, ps=16, seed=3)
+    cu = np.tile(np.array([0, n], np.int32), B)[:B + 1]
+    q, out = dev(s["q"]).expand(n, -1, -1).contiguous(), torch.full((n, 64, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = torch.zeros(fpk_prefill_workspace_bytes(B, n, 64, 8), dtype=torch.uint8, device=DEV)
+    table, lens = dev(s["table"]).expand(B, -1).contiguous(), dev(s["lens"]).expand(B).contiguous()
+    fpk_paged_prefill_attn_fp8_block(q, dev(cu), dev(s["pool"]).reshape(-1), dev(s["scales"]), table, lens, None, out, None, ws,
+                                     Hkv=8, page_size=16, num_pages=s["P"], sm_scale=SM)
+    torch.cuda.synchronize()
+    assert fpk_decode_status(ws) != 0 and torch.all(out == 7)
