@@ -161,11 +161,10 @@ def simulate(pieces, seed, slow=None):
             if blocks == 0:
                 continue
             assert t0 == j0 % 2
-            bufs = [2 * qset, 2 * qset + 1][:1 + pair]
-            for b in bufs:
-                yield from wait(B["Q"][b], phases[b])
-                phases[b] += 1
             mine, begins, step = 2 * qset + (t if pair else 0), True, 1 if pair else 2
+            yield from wait(B["Q"][mine], phases[mine])
+            for b in (2 * qset, 2 * qset + 1)[:1 + pair]:
+                phases[b] += 1
             i = 0 if pair else (j0 ^ t) & 1
             while i < blocks + step:
                 m, ks = i - step, (j0 + i) % KST
@@ -211,8 +210,7 @@ def simulate(pieces, seed, slow=None):
                 yield
                 i += step
             j0 += blocks
-            for b in bufs:
-                later(q, lambda b=b: B["qfree"][b].arrive())
+            later(q, lambda b=mine, c=1 + pair: B["qfree"][b].arrive(c))
 
     def softmax(t, w):
         ns = pn = joins = j0 = 0
