@@ -505,7 +505,7 @@ __device__ __forceinline__ bool next_piece(const ChArgs& a, ChCursor& c, ChPiece
   }
 }
 
-// tc_wait of the softmax warps, which are most of the warps: the hardware may hold one back for a microsecond, so
+// tc_wait of the softmax warps and of those that work ahead: the hardware may hold one back for a microsecond, so
 // that their looking leaves the issue slots to the others (8192-token prompt 798 -> 776 us; the other warps answer
 // sooner without).
 __device__ __forceinline__ void idle_wait(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* failed) {
@@ -802,6 +802,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     const int tpp = a.page_size >> 4;
     if (warp == kChPlanWarp) {
       // ===================== pieces and scales, ahead of the other warps =====================
+      auto wait = [&](int i, uint32_t parity) { idle_wait(bar(i), parity & 1u, a.status, s_failed); };
       cur.x = first.x;
       cur.h = first.y;
       cur.b0 = first.z;
@@ -868,6 +869,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       }
     } else if (warp == kChLoadWarp) {
       // ===================== K rows into their ring =====================
+      auto wait = [&](int i, uint32_t parity) { idle_wait(bar(i), parity & 1u, a.status, s_failed); };
       // Lane c copies box c of a block (zbox tiles, within a page).
       const uint64_t pol = l2_policy_evict_normal();  // (other units and CTAs read the same pages)
       const int box_t = (lane & 7) * a.zbox;  // first tile of the box in a block
