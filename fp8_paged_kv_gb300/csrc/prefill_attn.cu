@@ -16,7 +16,8 @@
 //   units of more than 128 rows, and a start), the kv heads one after another, and
 //   the line is cut into one equal range per CTA.  A unit that lies within a range
 //   is answered by its CTA; of the others every piece leaves a partial (m, l, O),
-//   merged in a fixed order: repeated calls give the same bits.
+//   merged in a fixed order: repeated calls give the same bits.  Where whole units,
+//   as many to each CTA, come out sooner than cut ones and their merge, none is cut.
 //
 // Piece pipeline (one CTA per SM, 16 warps), per block of 128 tokens:
 //   warp 15     finds the pieces and the blocks' scales ahead of the others
@@ -62,6 +63,9 @@ __device__ __forceinline__ float at_least_min(float mult) { return mult < kChMin
 // Costs in the work list, in some 500 cycles: of a block with both tiles at work and with one, of a unit's start.
 constexpr int kChCostPair = 6, kChCostSolo = 4;
 constexpr int kChStartPair = 20, kChStartSolo = 16;
+// What cutting units costs a call: another start, partials, their merge (16 requests of 4 tokens over 2048: 32.8 us cut,
+// 28.7 whole; 24 of them, 2 units to a CTA then: 43.0 cut, 48.7 whole; 3 of 300 over 1000: 52.6 and 46.1).
+constexpr int kChCut = 48;
 
 constexpr int kChThreads = 512;
 constexpr int kChVWarp = 8, kChLoadWarp = 12, kChMmaWarp = 13, kChPlanWarp = 15;
@@ -209,6 +213,13 @@ __device__ __forceinline__ ChRanges ranges_of(int line, int n) {
   return r;
 }
 
+// Whether the units, the dearest of which costs `top`, are dealt out whole, as many to each CTA: the ranges end with
+// units then.
+__device__ __forceinline__ bool uncut(const ChArgs& a, int units, int T, int top) {
+  const int all = units * a.Hkv;
+  return (all + a.ctas - 1) / a.ctas * top <= T * a.Hkv / a.ctas + kChCut;
+}
+
 // Sums of a CTA's threads: the sum of the threads before, and of all.
 __device__ __forceinline__ int block_scan(int mine, int& all, int* s_sum) {
   const unsigned kFull = 0xffffffffu;
@@ -238,7 +249,7 @@ __device__ __forceinline__ int block_scan(int mine, int& all, int* s_sum) {
 // others' page tables.
 __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const ChArgs a) {
   __shared__ int s_sum[kChPlanThreads / 32];
-  __shared__ int s_base[kChNear + 1], s_bad[kChNear], s_y[kChNearUnits];
+  __shared__ int s_base[kChNear + 1], s_bad[kChNear], s_y[kChNearUnits], s_top;
   griddep_wait();
   griddep_launch_dependents();
   const unsigned kFull = 0xffffffffu;
@@ -248,6 +259,7 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
   int32_t* const base = near ? s_base : a.base;
   int32_t* const dead = near ? s_bad : a.dead;
   for (int i = t; i < min(a.B, kChNear); i += kThreads) s_bad[i] = 0;
+  if (t == 0) s_top = 0;
   __syncthreads();
   // requests that are dead, by a bad page or otherwise
   const int ways = a.B < kWarps ? kWarps / a.B : 1;
@@ -306,9 +318,14 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
   const int chunk = (units + kThreads - 1) / kThreads;
   const int x0 = min(units, t * chunk), x1 = min(units, x0 + chunk);
   const int lo = x0 < x1 ? request_of(x0) : 0;
-  int mine = 0, r = lo;
+  int mine = 0, top = 0, r = lo;
 #pragma unroll 1
-  for (int x = x0; x < x1; ++x) mine += unit_cost(unit_at(x, r, 0));
+  for (int x = x0; x < x1; ++x) {
+    const int cost = unit_cost(unit_at(x, r, 0));
+    mine += cost;
+    top = max(top, cost);
+  }
+  if (top > 0) atomicMax(&s_top, top);
   int T;
   int y = block_scan(mine, T, s_sum);
   r = lo;
@@ -322,6 +339,8 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
   __syncthreads();
   // the ranges, with their first unit (the last one that starts at or before it) and the one that they leave to others
   const ChRanges rg = ranges_of(T * a.Hkv, a.ctas);
+  const bool whole = uncut(a, units, T, s_top);
+  const ChRanges by = ranges_of(units * a.Hkv, a.ctas);
   const bool near_units = units <= kChNearUnits;
   auto unit_of = [&](int place, int& x, int& h) -> ChUnit {
     h = min(place / T, a.Hkv - 1);
@@ -336,17 +355,22 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
     int q = request_of(l);
     return unit_at(l, q, near_units ? s_y[l] : a.unit[l].y);
   };
+  // unit `of` of all heads'
+  auto place_of = [&](int of) -> int {
+    const int h = of / units, x = of - h * units;
+    return h == a.Hkv ? a.Hkv * T : h * T + (near_units ? s_y[x] : a.unit[x].y);
+  };
 #pragma unroll 1
   for (int c = t; c < a.ctas; c += kThreads) {
     ChStart s = {};
-    s.b0 = rg.begin(c);
-    s.b1 = rg.begin(c + 1);
+    s.b0 = !whole ? rg.begin(c) : units > 0 ? place_of(by.begin(c)) : 0;
+    s.b1 = !whole ? rg.begin(c + 1) : units > 0 ? place_of(by.begin(c + 1)) : 0;
     s.units = units;
     s.T = T;
     s.cut = -1;
     if (s.b0 < s.b1) {
       s.u = unit_of(s.b0, s.unit, s.h);
-      if (s.b1 < T * a.Hkv) {
+      if (!whole && s.b1 < T * a.Hkv) {
         int x;
         s.cut_u = unit_of(s.b1, x, s.cut_h);
         const int at = s.cut_h * T + s.cut_u.y, blocks = blocks_of(s.cut_u.tokens);
@@ -389,11 +413,10 @@ __device__ __forceinline__ ChUnit small_next(const ChArgs& a, const ChSmall& s, 
 __device__ __forceinline__ ChUnit small_first(const ChArgs& a, const ChSmall& s) {
   return small_unit(a, s, 31 - __clz(__ballot_sync(0xffffffffu, s.base <= 0)), 0, 0);
 }
-// The unit that a place of the line belongs to: the last one that starts at or before it.  A lane looks at a unit.
-__device__ __forceinline__ ChUnit small_unit_of(const ChArgs& a, const ChSmall& s, int place, int& x, int& h) {
+// The unit of request r behind those that end at or before place `at`, or behind the first x - its first.  A lane
+// looks at a unit.
+__device__ __forceinline__ ChUnit small_find(const ChArgs& a, const ChSmall& s, int r, int at, int& x) {
   const unsigned kFull = 0xffffffffu;
-  h = min(place / s.T, a.Hkv - 1);
-  const int at = place - h * s.T, r = 31 - __clz(__ballot_sync(kFull, s.n > 0 && s.y <= at));
   const int base = __shfl_sync(kFull, s.base, r), n = __shfl_sync(kFull, s.n, r);
   int y = __shfl_sync(kFull, s.y, r), i = 0;
 #pragma unroll 1
@@ -406,14 +429,26 @@ __device__ __forceinline__ ChUnit small_unit_of(const ChArgs& a, const ChSmall& 
       const int p = __shfl_up_sync(kFull, ends, o);
       if ((threadIdx.x & 31) >= o) ends += p;
     }
-    const unsigned behind = __ballot_sync(kFull, mine.rows > 0 && y + ends <= at);  // units that end at or before the place
-    const int passed = __popc(behind);
+    const bool behind = y + ends <= at || base + i0 + static_cast<int>(threadIdx.x & 31) < x;
+    const int passed = __popc(__ballot_sync(kFull, mine.rows > 0 && behind));
     i = i0 + passed;
     y += passed > 0 ? __shfl_sync(kFull, ends, passed - 1) : 0;
     if (passed < 32 || (i0 + 32) * kChUnitRows >= n * a.G) break;
   }
   x = base + i;
   return small_unit(a, s, r, i, y);
+}
+// The unit that a place of the line belongs to: the last one that starts at or before it.
+__device__ __forceinline__ ChUnit small_unit_of(const ChArgs& a, const ChSmall& s, int place, int& x, int& h) {
+  h = min(place / s.T, a.Hkv - 1);
+  x = 0;
+  return small_find(a, s, 31 - __clz(__ballot_sync(0xffffffffu, s.n > 0 && s.y <= place - h * s.T)), place - h * s.T, x);
+}
+// Unit `of` of all heads'.
+__device__ __forceinline__ ChUnit small_unit_at(const ChArgs& a, const ChSmall& s, int of, int& x, int& h) {
+  h = of / s.units;
+  x = of - h * s.units;
+  return small_find(a, s, 31 - __clz(__ballot_sync(0xffffffffu, s.base <= x)), -1, x);
 }
 __device__ __forceinline__ void small_plan(const ChArgs& a, unsigned bad, ChSmall& s, ChStart& st) {
   const unsigned kFull = 0xffffffffu;
@@ -424,7 +459,7 @@ __device__ __forceinline__ void small_plan(const ChArgs& a, unsigned bad, ChSmal
     s.n = max(0, query_start(a, lane + 1) - s.c0);
     s.L = bad >> lane & 1 ? 0 : __ldg(a.seq_lens + lane);
   }
-  int mine = (s.n * a.G + kChUnitRows - 1) / kChUnitRows, cost = 0;
+  int mine = (s.n * a.G + kChUnitRows - 1) / kChUnitRows, cost = 0, top = 0;
   ChUnit u;
   u.L = s.L;
   u.shift = a.causal ? s.L - s.n : s.L;
@@ -433,6 +468,7 @@ __device__ __forceinline__ void small_plan(const ChArgs& a, unsigned bad, ChSmal
     u.rows = min(kChUnitRows, s.n * a.G - i * kChUnitRows);
     u.tokens = seen(u, quotient(i * kChUnitRows + u.rows - 1, a.by_g));
     cost += unit_cost(u);
+    top = max(top, unit_cost(u));
   }
   int x = mine, y = cost;
 #pragma unroll 1
@@ -448,13 +484,28 @@ __device__ __forceinline__ void small_plan(const ChArgs& a, unsigned bad, ChSmal
   }
   s.base = x - mine;
   s.y = y - cost;
-  const ChRanges rg = ranges_of(s.T * a.Hkv, a.ctas);
-  st.b0 = rg.begin(blockIdx.x);
-  st.b1 = rg.begin(blockIdx.x + 1);
+  st.b0 = st.b1 = 0;
   st.units = s.units;
   st.T = s.T;
   st.cut = -1;
   st.unit = st.h = st.cut_h = 0;
+  if (uncut(a, s.units, s.T, __reduce_max_sync(kFull, top))) {
+    const int all = s.units * a.Hkv;
+    const ChRanges by = ranges_of(all, a.ctas);
+    const int from = by.begin(blockIdx.x), to = by.begin(blockIdx.x + 1);
+    if (from == to) return;
+    st.u = small_unit_at(a, s, from, st.unit, st.h);
+    st.b0 = st.h * s.T + st.u.y;
+    st.b1 = s.T * a.Hkv;
+    if (to == all) return;
+    int h;
+    const int y_to = small_unit_at(a, s, to, x, h).y;
+    st.b1 = h * s.T + y_to;
+    return;
+  }
+  const ChRanges rg = ranges_of(s.T * a.Hkv, a.ctas);
+  st.b0 = rg.begin(blockIdx.x);
+  st.b1 = rg.begin(blockIdx.x + 1);
   if (st.b0 >= st.b1) return;
   st.u = small_unit_of(a, s, st.b0, st.unit, st.h);
   if (st.b1 == s.T * a.Hkv) return;

@@ -1,12 +1,12 @@
 """CPU model of the prompt attention's work list: every block of every unit belongs to exactly
 one CTA, a unit without tokens to the one that holds its place, at most one of a CTA's pieces
 continues a unit and at most one leaves its end to others, and the merge of a unit visits
-exactly the partials that the pieces wrote, in slots of their own."""
+exactly the partials that the pieces wrote, in slots of their own; or the units are dealt out whole."""
 import random
 
 import pytest
 
-PAIR, SOLO, START_PAIR, START_SOLO, ROWS, BLK = 6, 4, 20, 16, 256, 128
+PAIR, SOLO, START_PAIR, START_SOLO, CUT, ROWS, BLK = 6, 4, 20, 16, 48, 256, 128
 
 
 def units_of(requests, G, causal):
@@ -46,13 +46,22 @@ def owned(rows, blocks, y, b0, b1):
     return tuple(min(blocks, (max(b - at, 0) + w - 1) // w) for b in (b0, b1))
 
 
+def ranges(units, T, Hkv, ctas):
+    """Where the CTAs' ranges of the line begin, and its end; whether they end with units."""
+    every = len(units) * Hkv
+    top = max((start(u[2]) + cost(u[2]) * u[3] for u in units), default=0)
+    if -(-every // ctas) * top <= T * Hkv // ctas + CUT:
+        places = [h * T + u[0] for h in range(Hkv) for u in units] + [T * Hkv]
+        return [places[begin(c, every, ctas)] for c in range(ctas + 1)], True
+    return [begin(c, T * Hkv, ctas) for c in range(ctas + 1)], False
+
+
 def unit_at(units, T, Hkv, place):
     h = min(place // T, Hkv - 1)
     return max(x for x, u in enumerate(units) if u[0] <= place - h * T), h
 
 
-def pieces(units, T, Hkv, ctas, c):
-    b0, b1 = begin(c, T * Hkv, ctas), begin(c + 1, T * Hkv, ctas)
+def pieces(units, T, Hkv, b0, b1):
     if b0 >= b1:
         return
     x, h = unit_at(units, T, Hkv, b0)
@@ -74,10 +83,11 @@ def pieces(units, T, Hkv, ctas, c):
 def check(requests, G, Hkv, ctas, causal):
     units, T = units_of(requests, G, causal)
     line, done, slots, cuts = T * Hkv, {}, {}, []
+    at, uncut = ranges(units, T, Hkv, ctas)
     for c in range(ctas):
-        b0, b1 = begin(c, line, ctas), begin(c + 1, line, ctas)
+        b0, b1 = at[c], at[c + 1]
         whole = []
-        for x, h, i0, i1 in pieces(units, T, Hkv, ctas, c):
+        for x, h, i0, i1 in pieces(units, T, Hkv, b0, b1):
             blocks = units[x][3]
             assert done.get((x, h), 0) == i0, "blocks in order, none twice"
             assert blocks or (x, h) not in done
@@ -88,13 +98,14 @@ def check(requests, G, Hkv, ctas, causal):
                 assert slot not in slots, "one partial per slot"
                 slots[slot] = (x, h)
         assert sum(not first for first, _ in whole) <= 1 and sum(not last for _, last in whole) <= 1
-        if b0 < b1 < line:
+        assert not uncut or all(x == (True, True) for x in whole)
+        if b0 < b1 < line and not uncut:
             x, h = unit_at(units, T, Hkv, b1)
             y0, _, rows, blocks = units[x]
-            at = h * T + y0
-            i0, i1 = owned(rows, blocks, at, b0, b1)
+            y = h * T + y0
+            i0, i1 = owned(rows, blocks, y, b0, b1)
             if i0 == 0 and 0 < i1 < blocks:
-                cuts.append((c, owner(at + start(rows) + (blocks - 1) * cost(rows), line, ctas), x, h))
+                cuts.append((c, owner(y + start(rows) + (blocks - 1) * cost(rows), line, ctas), x, h))
     assert done == {(x, h): u[3] for h in range(Hkv) for x, u in enumerate(units)}
     merged = {}
     for c, to, x, h in cuts:
