@@ -662,14 +662,12 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t x, uint32_t y) {
   return r;
 }
 
-// The first n bytes (of 4) of a word.
-__device__ __forceinline__ uint32_t first_bytes(int n) {
-  return n <= 0 ? 0u : n >= 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
-}
-// The bytes of x from the n-th on that hold an e4m3 NaN, as 0xFF.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t x, int n) {
-  const uint32_t hit = ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-  return (hit >> 7) * 255u & ~first_bytes(n);
+// The first n halves (of 2) of a word.
+__device__ __forceinline__ uint32_t first_halves(int n) { return n <= 0 ? 0u : n == 1 ? 0xFFFFu : 0xFFFFFFFFu; }
+// The halves of x that hold an f16 NaN, as 0xFFFF.
+__device__ __forceinline__ uint32_t nan_halves(uint32_t x) {
+  const uint32_t hit = ((x & 0x7FFF7FFFu) + 0x03FF03FFu) & 0x80008000u;
+  return (hit >> 15) * 65535u;
 }
 
 // 16 bytes of the pool, which goes by: no line of L1 for it.
@@ -1029,26 +1027,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
           const int nv = min(kChBlk, p.u.tokens - i * kChBlk), first_hidden = least - i * kChBlk;
           const uint32_t buf = j % C::kV16Bufs;
           const bool more = i + 1 < p.i1;
-          if (nv < kChBlk || first_hidden < kChBlk) {
-            // codes behind the last token: 0; and NaN in tokens that not every row sees (they would reach the others)
-            uint32_t hits = 0;
-#pragma unroll 1
-            for (int t = 0; t < kChBlkTiles; ++t) {  // (tile by tile at the first place, the others moving up: short code)
-              uint32_t w[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int tok = 16 * t + 4 * k;
-                w[k] &= first_bytes(nv - tok);
-                const uint32_t nans = nan_bytes(w[k], first_hidden - tok);
-                w[k] &= ~nans;
-                hits |= nans;
-              }
-#pragma unroll
-              for (int k = 0; k + 1 < kChBlkTiles; ++k) x[k] = x[k + 1];
-              x[kChBlkTiles - 1] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            if (hits) s_nan[piece % C::kNan] = 1;
-          }
           if (more) {
             wait(C::kBarScale + (j + 1) % C::kScales, (j + 1) / C::kScales);
             places(j + 1);
@@ -1067,6 +1045,25 @@ __global__ void __launch_bounds__(kChThreads, 1)
             w[0] = make_uint4(y[0], y[1], y[2], y[3]);
             w[128] = make_uint4(y[4], y[5], y[6], y[7]);
             if (more) fetch(t);
+          }
+          if (nv < kChBlk || first_hidden < kChBlk) {
+            // what lies behind the last token: 0; and NaN in tokens that not every row sees (they would reach the others)
+            uint32_t hits = 0;
+#pragma unroll 1
+            for (int tok = max(0, min(nv, first_hidden)) & ~7; tok < kChBlk; tok += 8) {
+              uint4* const w = reinterpret_cast<uint4*>(o + (tok >> 4) * (kChTile * kChDim * 2) + (tok & 8) * 256);
+              const uint4 v = *w;
+              uint32_t y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                y[k] &= first_halves(nv - tok - 2 * k);
+                const uint32_t nans = nan_halves(y[k]) & ~first_halves(first_hidden - tok - 2 * k);
+                y[k] &= ~nans;
+                hits |= nans;
+              }
+              *w = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+            if (hits) s_nan[piece % C::kNan] = 1;
           }
           fence_proxy_async_smem();
           if (more) fetched(j + 1);
