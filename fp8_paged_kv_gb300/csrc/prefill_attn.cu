@@ -1277,14 +1277,20 @@ __global__ void __launch_bounds__(kChThreads, 1)
       uint32_t j0 = 0;            // blocks of the pieces before
       uint32_t phases = 0;        // parities of the query buffers
       uint32_t joins = 0;
-      while (take_piece(p)) {
+      // (a piece's slot is read twice, here and for its results: what those need would take registers from the blocks)
+      auto piece_read = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kBarPieceFree + (pn - 1) % kChPieces));
+      };
+      for (;;) {
+        wait(C::kBarPiece + pn % kChPieces, pn / kChPieces);
+        p = s_piece[pn++ % kChPieces].piece;
+        if (__any_sync(kFull, p.last != 0 || *s_failed)) break;
         const bool pair = p.pair();
         const int nb = p.i1 - p.i0;
         const int lrow = pair ? t * 128 + row : row;  // row of the unit
-        const bool valid = lrow < p.u.rows;
         const bool busy = lrow - lane < p.u.rows;     // some row of the warp's is
-        const int grow = p.u.row0 + min(lrow, p.u.rows - 1), token = quotient(grow, a.by_g);
-        const int limit = seen(p.u, token);
+        const int limit = seen(p.u, quotient(p.u.row0 + min(lrow, p.u.rows - 1), a.by_g));
         const int least = __reduce_min_sync(kFull, limit);  // tokens that every row of the warp sees
         const int nan_slot = static_cast<int>((pn - 1) % C::kNan);
         const int buf = 2 * p.qset + (pair ? t : 0);
@@ -1421,6 +1427,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         j0 += nb;
         // ---- results: a row's thread, of a unit of one row tile the one of tile 0
+        p = s_piece[(pn - 1) % kChPieces].piece;
+        piece_read();
+        const int grow = p.u.row0 + min(lrow, p.u.rows - 1), token = quotient(grow, a.by_g);
+        const int ends = seen(p.u, token);
+        const bool valid = lrow < p.u.rows;
         const bool whole = p.i0 == 0 && p.i1 == p.blocks;
         const int64_t slot = static_cast<int64_t>(2 * blockIdx.x + (p.i0 == 0 ? 0 : 1)) * kChUnitRows + lrow;
         float f0 = 1.f, f1 = 0.f;
@@ -1509,7 +1520,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         if (s_nan[nan_slot] != 0) {
           if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the rows are out)
           __syncwarp();
-          const int lo = max(seen(p.u, quotient(p.u.row0, a.by_g)), p.i0 * kChBlk), hi = min(limit, p.i1 * kChBlk);
+          const int lo = max(seen(p.u, quotient(p.u.row0, a.by_g)), p.i0 * kChBlk), hi = min(ends, p.i1 * kChBlk);
           if (valid) poison_row(a, p.u.r, p.h, lo, hi, whole ? a.out + orow * kChDim : nullptr, whole ? nullptr : a.part_o + slot * kChDim);
         }
         if (valid) {

@@ -48,12 +48,13 @@ def simulate(pieces, seed, slow=None):
         while not bar.done(phase):
             yield
 
-    def take(pn):
+    def take(pn, keep=False):
         yield from wait(B["piece"][pn % PIECES], pn // PIECES)
         p = slots[pn % PIECES]
         assert p is not None and p[0] == pn, "piece slot"
         yield
-        B["piecefree"][pn % PIECES].arrive()
+        if not keep:
+            B["piecefree"][pn % PIECES].arrive()
         return p
 
     def plan():
@@ -216,7 +217,7 @@ def simulate(pieces, seed, slow=None):
         ns = pn = joins = j0 = 0
         phases = [0] * 4
         while True:
-            k, qset, t0, pair, blocks, tail, _, last = yield from take(pn)
+            k, qset, t0, pair, blocks, tail, _, last = yield from take(pn, keep=True)
             pn += 1
             if last:
                 return
@@ -248,6 +249,9 @@ def simulate(pieces, seed, slow=None):
                     yield from wait(B["O"][t], ns - 1)
                     assert oof[t][0] == k, "O"
             j0 += blocks
+            assert slots[(pn - 1) % PIECES][0] == k, "piece slot, read again"
+            yield
+            B["piecefree"][(pn - 1) % PIECES].arrive()
             if not pair and t == 1:
                 if blocks:
                     if some:
