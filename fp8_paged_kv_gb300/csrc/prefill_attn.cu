@@ -461,15 +461,11 @@ __device__ __forceinline__ ChUnit small_unit_at(const ChArgs& a, const ChSmall& 
   x = of - h * s.units;
   return small_find(a, s, 31 - __clz(__ballot_sync(0xffffffffu, s.base <= x)), -1, x);
 }
+// (s.n, s.c0 and s.L are given)
 __device__ __forceinline__ void small_plan(const ChArgs& a, unsigned bad, ChSmall& s, ChStart& st) {
   const unsigned kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  s.n = s.c0 = s.L = 0;
-  if (lane < a.B) {
-    s.c0 = query_start(a, lane);
-    s.n = max(0, query_start(a, lane + 1) - s.c0);
-    s.L = bad >> lane & 1 ? 0 : __ldg(a.seq_lens + lane);
-  }
+  if (bad >> lane & 1) s.L = 0;
   int mine = (s.n * a.G + kChUnitRows - 1) / kChUnitRows, cost = 0, top = 0;
   ChUnit u;
   u.L = s.L;
@@ -805,8 +801,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
   ChCursor cur;
   int4 first;
   if (a.small) {
-    // page tables by all warps, the list by one
+    // page tables by all warps, the list by one (what it needs of the requests is asked for ahead)
     unsigned bad = 0;
+    cur.s.n = cur.s.c0 = cur.s.L = 0;
+    if (warp == kChPlanWarp && lane < a.B) {
+      cur.s.c0 = query_start(a, lane);
+      cur.s.n = max(0, query_start(a, lane + 1) - cur.s.c0);
+      cur.s.L = __ldg(a.seq_lens + lane);
+    }
     const int ways = 16 / min(a.B, 16);
 #pragma unroll 1
     for (int r = warp / ways; r < a.B; r += 16 / ways) {
