@@ -37,7 +37,7 @@
 // the next scores overwrite those weights: about 3100, in which both tiles' products are 2280.  64/8 heads: a prompt of
 // 8192 tokens 757 us (1450 TFLOP/s, three quarters of a plain library product's rate), 8192 rows over all of 8192 tokens
 // 1410 us (1560), the last 1024 of 32768 703 us (1540).  Few rows: a start (list, queries, pipeline; 6 us), some
-// 2000 cycles for 128 tokens, an end (3 us): 16 requests of 4 tokens over 2048 29 us, 4 tokens over 131072 80 us.
+// 2000 cycles for 128 tokens, an end (3 us): 16 requests of 4 tokens over 2048 27 us, 4 tokens over 131072 77 us.
 // Short prompts: queries in, results out and the piece's start and end come on top (16 x 512: 181 us, of which 40 go
 // when neither queries nor results touch HBM).
 //
