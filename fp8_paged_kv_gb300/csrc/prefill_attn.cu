@@ -1472,10 +1472,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const int64_t orow = static_cast<int64_t>(p.u.c0 + token) * a.Hq + p.h * a.G + grow - token * a.G;
         const bool none = l == 0.f;
         const float inv = whole && !none ? 1.f / l : 1.f;
-        if (whole && a.boxed && lrow - lane + 32 <= p.u.rows) {
+        if (whole && nb > 0 && a.boxed && lrow - lane + 32 <= p.u.rows) {
           // The warp's 32 rows are whole tokens' heads: by way of its rows' place in the query buffer, which has been
           // read, as two boxes of 64 dims (rows of 128 bytes with the 128-byte swizzle).  Stores from registers touch a
-          // line per row, a cycle each, and what is asked of shared memory behind them waits as long.
+          // line per row, a cycle each, and what is asked of shared memory behind them waits as long.  (A piece without
+          // blocks has no buffer: that of its turn may hold a later piece's queries by now.  Its zeroes go from registers.)
           uint8_t* const mine = sm + buf * C::kQTile + (row - lane) * 256 + lane * 128;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
