@@ -1310,9 +1310,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
           wait(C::kBarQ + buf, phases >> buf);
           phases ^= (pair ? 3u : 1u) << (2 * p.qset);
           const int e = s_exp[buf * 128 + row];
-          const float mult = e == kNanRow ? __int_as_float(0x7fffffff) : fabsf(a.sm_scale_log2) * exp2_int(-e);
+          // a NaN query: its row is NaN, unless it sees nothing (all its scores are -inf then, and have to stay so)
+          const float mult = limit == 0 ? 1.f : e == kNanRow ? __int_as_float(0x7fffffff) : fabsf(a.sm_scale_log2) * exp2_int(-e);
           __syncwarp();
-          if (mult != mult) m = mult;  // a NaN query: its row is NaN
+          if (mult != mult) m = mult;
           // ---- blocks
 #pragma unroll 1
           for (int i = pair ? 0 : t ^ p.t0; i < nb; i += pair ? 1 : 2) {
