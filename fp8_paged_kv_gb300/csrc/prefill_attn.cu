@@ -286,16 +286,21 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
   }
   // units of each request
   int units = 0;
+  bool down = false;
 #pragma unroll 1
   for (int r0 = 0; r0 < a.B; r0 += kThreads) {
     const int r = r0 + t;
-    const int rows = r < a.B ? max(0, query_start(a, r + 1) - query_start(a, r)) * a.G : 0;
+    const int n = r < a.B ? query_start(a, r + 1) - query_start(a, r) : 0;
+    const int rows = max(0, n) * a.G;
+    down |= n < 0;
     int all;
     const int before = block_scan((rows + kChUnitRows - 1) / kChUnitRows, all, s_sum);
     if (r < a.B) base[r] = units + before;
     units = min(units + all, a.most + 1);
   }
-  if (units > a.most) {  // cu_seqlens that decrease: the list has no place for them, nothing is answered
+  if (__syncthreads_or(down)) {
+    // cu_seqlens that decrease: rows of several requests, and more units than the list may have places for; nothing is
+    // answered.  (Without, a request's rows are its own and the units no more than a.most.)
     if (t == 0) atomicOr(a.status, kStatusBadStart);
     units = 0;
   }
@@ -461,11 +466,16 @@ __device__ __forceinline__ ChUnit small_unit_at(const ChArgs& a, const ChSmall& 
   x = of - h * s.units;
   return small_find(a, s, 31 - __clz(__ballot_sync(0xffffffffu, s.base <= x)), -1, x);
 }
-// (s.n, s.c0 and s.L are given)
+// (s.n, s.c0 and s.L are given; s.n below 0 where cu_seqlens decrease)
 __device__ __forceinline__ void small_plan(const ChArgs& a, unsigned bad, ChSmall& s, ChStart& st) {
   const unsigned kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   if (bad >> lane & 1) s.L = 0;
+  const bool down = __any_sync(kFull, s.n < 0);  // (as in the plan)
+  if (down) {
+    if (lane == 0 && blockIdx.x == 0) atomicOr(a.status, kStatusBadStart);
+    s.n = 0;
+  }
   int mine = (s.n * a.G + kChUnitRows - 1) / kChUnitRows, cost = 0, top = 0;
   ChUnit u;
   u.L = s.L;
@@ -485,10 +495,6 @@ __device__ __forceinline__ void small_plan(const ChArgs& a, unsigned bad, ChSmal
   }
   s.units = __shfl_sync(kFull, x, 31);
   s.T = __shfl_sync(kFull, y, 31);
-  if (s.units > a.most) {  // (as in the plan)
-    if (lane == 0 && blockIdx.x == 0) atomicOr(a.status, kStatusBadStart);
-    s.units = s.T = 0;
-  }
   s.base = x - mine;
   s.y = y - cost;
   st.b0 = st.b1 = 0;
@@ -806,7 +812,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     cur.s.n = cur.s.c0 = cur.s.L = 0;
     if (warp == kChPlanWarp && lane < a.B) {
       cur.s.c0 = query_start(a, lane);
-      cur.s.n = max(0, query_start(a, lane + 1) - cur.s.c0);
+      cur.s.n = query_start(a, lane + 1) - cur.s.c0;
       cur.s.L = __ldg(a.seq_lens + lane);
     }
     const int ways = 16 / min(a.B, 16);

@@ -596,9 +596,8 @@ int fpk_paged_decode_attn_fp8_block(const void* q, const uint8_t* kv_pool, const
  *   workspace : >= fpk_prefill_workspace_bytes(...) bytes for the current device,
  *               256-byte aligned, zeroed ONCE after allocating (its first 4 bytes
  *               are a status word as in fpk_paged_decode_attn_fp8; cu_seqlens
- *               that decrease set it too, where their rows number more than
- *               n_tokens, and then no row is written).  Calls that share a
- *               workspace must not overlap on the GPU.
+ *               that decrease set it too, and then no row is written).  Calls
+ *               that share a workspace must not overlap on the GPU.
  * D is 128, Hq / Hkv at most 8, page_size a multiple of 16 up to 256; a pool of
  * 2^31 tiles, n_tokens * Hq / Hkv of 2^28, a table of 2^31 tokens, or a work list
  * (a table's blocks of 128 tokens, times some 6, for each 256 rows and kv head) of
