@@ -1701,11 +1701,11 @@ extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu
   if (D != kChDim || G > kChGroupMax || page_size % kChTile != 0 || page_size > 256) return FPK_EUNSUPPORTED;
   const int tpp = page_size / kChTile;
   const int64_t tiles = static_cast<int64_t>(num_pages) * Hkv * tpp;
-  // tile numbers are 32-bit tensor-map coordinates; the work list's length is counted in 31 bits, rows are divided
-  // by reciprocals (2^28)
+  // tile numbers are 32-bit tensor-map coordinates; the work list's length is counted in 31 bits, tokens are rounded up
+  // to blocks in them (a context of at most 2^31 - 128), rows are divided by reciprocals (2^28)
   const int64_t width = (static_cast<int64_t>(max_pages) * page_size + kChBlk - 1) / kChBlk;
   const int64_t units = most_units(B, n_tokens, G), longest = width * kChCostPair + kChStartPair;
-  if (tiles > 0x7fffffff || static_cast<int64_t>(n_tokens) * G >= (int64_t(1) << 28) || width > (int64_t(1) << 24) ||
+  if (tiles > 0x7fffffff || static_cast<int64_t>(n_tokens) * G >= (int64_t(1) << 28) || width >= (int64_t(1) << 24) ||
       longest > 0x7fffffff / ((units > 0 ? units : 1) * Hkv))
     return FPK_EUNSUPPORTED;
   if (B == 0 || n_tokens == 0) return FPK_OK;

@@ -599,9 +599,9 @@ int fpk_paged_decode_attn_fp8_block(const void* q, const uint8_t* kv_pool, const
  *               that decrease set it too, and then no row is written).  Calls
  *               that share a workspace must not overlap on the GPU.
  * D is 128, Hq / Hkv at most 8, page_size a multiple of 16 up to 256; a pool of
- * 2^31 tiles, n_tokens * Hq / Hkv of 2^28, a table of 2^31 tokens, or a work list
- * (a table's blocks of 128 tokens, times some 6, for each 256 rows and kv head) of
- * 2^31 is FPK_EUNSUPPORTED.
+ * 2^31 tiles, n_tokens * Hq / Hkv of 2^28, a table of more than 2^31 - 128 tokens,
+ * or a work list (a table's blocks of 128 tokens, times some 6, for each 256 rows
+ * and kv head) of 2^31 is FPK_EUNSUPPORTED.
  * Precision: scores, sums and O in fp32; the query enters as two e4m3 parts (what
  * they leave out is below 2^-17 of the largest |q| of its row), K exactly; softmax
  * weights enter in f16 (relative to the largest weight times V scale, half a step
