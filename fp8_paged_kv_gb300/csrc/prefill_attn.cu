@@ -93,7 +93,7 @@ struct alignas(16) ChUnit {
   int row0, rows;  // of the request's rows
   int tokens;  // that its last row sees
   int c0;      // the request's first query token
-  int shift;   // row's token t sees min(L, max(0, shift + t + 1)) tokens
+  int behind;  // query tokens behind the first one, of those that see fewer: token t sees L - max(0, behind - t), or none
   int L;       // 0: dead
 };
 static_assert(sizeof(ChUnit) == 32, "two 16-byte words");
@@ -184,7 +184,8 @@ __device__ __forceinline__ int live_length(const ChArgs& a, int r) {
 __device__ __forceinline__ int query_start(const ChArgs& a, int r) {
   return min(max(__ldg(a.cu_seqlens + r), 0), a.n_tokens);
 }
-__device__ __forceinline__ int seen(const ChUnit& u, int token) { return min(u.L, max(0, u.shift + token + 1)); }
+// (L may be near 2^31: nothing is added to it)
+__device__ __forceinline__ int seen(const ChUnit& u, int token) { return max(0, u.L - max(0, u.behind - token)); }
 
 // ---------------------------------------------------------------------------
 // work list
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kChPlanThreads, 1) prefill_plan_kernel(const C
     u.c0 = query_start(a, r);
     const int n = query_start(a, r + 1) - u.c0, rows = n * a.G;
     u.L = dead[r] ? 0 : __ldg(a.seq_lens + r);
-    u.shift = a.causal ? u.L - n : u.L;
+    u.behind = a.causal ? n - 1 : 0;
     u.row0 = (x - base[r]) * kChUnitRows;
     u.rows = min(kChUnitRows, rows - u.row0);
     u.tokens = seen(u, quotient(u.row0 + u.rows - 1, a.by_g));
@@ -414,7 +415,7 @@ __device__ __forceinline__ ChUnit small_unit(const ChArgs& a, const ChSmall& s, 
   u.y = y;
   u.c0 = __shfl_sync(kFull, s.c0, r);
   u.L = __shfl_sync(kFull, s.L, r);
-  u.shift = a.causal ? u.L - n : u.L;
+  u.behind = a.causal ? n - 1 : 0;
   u.row0 = i * kChUnitRows;
   u.rows = min(kChUnitRows, n * a.G - u.row0);
   u.tokens = seen(u, quotient(u.row0 + u.rows - 1, a.by_g));
@@ -479,7 +480,7 @@ __device__ __forceinline__ void small_plan(const ChArgs& a, unsigned bad, ChSmal
   int mine = (s.n * a.G + kChUnitRows - 1) / kChUnitRows, cost = 0, top = 0;
   ChUnit u;
   u.L = s.L;
-  u.shift = a.causal ? s.L - s.n : s.L;
+  u.behind = a.causal ? s.n - 1 : 0;
 #pragma unroll 1
   for (int i = 0; i < mine; ++i) {
     u.rows = min(kChUnitRows, s.n * a.G - i * kChUnitRows);
