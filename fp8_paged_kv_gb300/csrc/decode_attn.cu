@@ -46,11 +46,15 @@
 // * Block scales (kBlock).  The producer fetches a tile's two exponent bytes one
 //   batch ahead, behind the table, and leaves them with the stage.  K's scale
 //   multiplies the tile's scores.  V's goes into the weights: with ev its
-//   exponent, p' = 2^(s + ev - m) with m the largest s + ev seen, so that the
-//   weights that meet the codes stay within 1 whatever the scales' order, and
-//   the sum takes p' 2^-ev, which is 2^(s - m).  m and l of partials have that
-//   meaning throughout; l stays within 2^50 per token (the scales' least
-//   exponent), and what p' loses below 2^-126 is 2^-46 of l at most.
+//   exponent, p' = 2^(s + ev - m + 14) with m the largest s + ev seen, so that
+//   the weights that meet the codes stay within 2^14 whatever the scales' order
+//   and fill f16's range: its two parts keep 2^-22 of a weight down to 2^-17 of
+//   the largest, and are off by 2^-39 of that below (without the 14 bits 2^-25,
+//   which is all that a block has left beside one whose scale is 2^24 as
+//   large).  The sum takes p' 2^(-ev - 14), which is 2^(s - m), and results are
+//   taken back by 2^-14: m and l of partials have that meaning throughout; l
+//   stays within 2^50 per token (the scales' least exponent), and what p' loses
+//   below 2^-126 is 2^-60 of l at most.
 //   64/8 heads: 32 x 8192 tokens 85.4 us (6.3 TB/s, 93 % of a copy's rate), 4 x
 //   131072 160 us (6.7 TB/s): bound by HBM as with one scale for all.
 // * Safety.  Every wait is bounded (status word in the workspace); no barrier
@@ -208,6 +212,8 @@ __device__ __noinline__ int64_t tightest_split_size(const AttnArgs& a, int64_t T
   __syncthreads();  // s_warp is reused by the caller
   return c;
 }
+
+constexpr int kBlockLift = 14;  // block scales: log2 of the largest weight that meets V's codes
 
 template <bool kFp8, bool kDeep, bool kBlock>
 __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const AttnArgs a) {
@@ -578,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
   const int rowA = token_of_row(g);  // token of fragment row g (row g+8 is rowA + 2)
   const float kscale = kFp8 && !kBlock ? __ldg(a.k_scale) : 1.f;
   const float vscale = kFp8 && !kBlock ? __ldg(a.v_scale) : 1.f;
-  const float vmul = kFp8 ? vscale : 1.f;
+  const float vmul = kBlock ? exp2_int(-kBlockLift) : kFp8 ? vscale : 1.f;
   Cursor cur = start;
   Piece p;
   uint32_t jbase = 0;
@@ -1036,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
           const int ev = scale_exponent(b >> 8);
           km[tt] = exp2_int(scale_exponent(b & 255u));
           ve[tt] = static_cast<float>(ev);
-          vd[tt] = exp2_int(-ev);
+          vd[tt] = exp2_int(-ev - kBlockLift);
         }
       }
       if (kFp8) {
@@ -1113,7 +1119,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_split_kernel(const A
         m0 = mn0;
         m1 = mn1;
       }
-      const float base0 = m0 == kNegInf ? 0.f : m0, base1 = m1 == kNegInf ? 0.f : m1;
+      const float lift = kBlock ? kBlockLift : 0.f;
+      const float base0 = m0 == kNegInf ? 0.f : m0 - lift, base1 = m1 == kNegInf ? 0.f : m1 - lift;
       // ---- P^T as the B operand of O^T = V^T P^T, per tile, as P = hi + lo:
       // two f16 (FP8 cache) or bf16 (BF16 cache) parts.  One f16 P alone
       // errs by up to 2^-12 of each p, which reaches the 2e-3 absolute
