@@ -28,7 +28,7 @@
 //   warps 13, 14  issue S = Q K^T (e4m3, over both parts against the same K rows) and
 //               O += P V (f16) of row tile 0 and 1, tcgen05.mma of M = N = 128
 //   warps 0-3, 4-7  softmax of row tile 0 and 1, a thread per row: no shuffles.  P
-//               (f16, in the columns of the scores it came from) is the A operand
+//               (two f16 parts, in the columns of the scores it came from) is the A operand
 // Units of more than 128 rows use both tiles on every block; smaller ones give the
 // two tiles alternate blocks of the same rows, joined at the end in tensor memory.
 //
@@ -42,9 +42,17 @@
 // when neither queries nor results touch HBM).
 //
 // Scales.  Of each tile of 16 tokens (16 columns of S) K's scale multiplies the
-// scores and V's goes into the weights: with ev its exponent, P = 2^(s + ev - m), m
-// the largest s + ev (within 2^8), so that the weights that meet V's codes use f16's
-// range whatever the order of the scales; the sum takes P 2^-ev, which is 2^(s - m).
+// scores and V's goes into the weights: with ev its exponent, P = 2^(s + ev - m + 7),
+// m the largest s + ev (within 2^8), so that the weights that meet V's codes use f16's
+// range (up to 2^15) whatever the order of the scales; the sum takes P 2^(-ev - 7),
+// which is 2^(s - m), and O is taken back by 2^-7 on its way out.
+//
+// Weights are two f16 parts, rounded, and what that left, as in the framework's other
+// attention: 2^-22 of a weight is lost, or 2^-32 of the largest where that is more.
+// With one part 2^-11 of each was: where values cancel, results were 4 times outside
+// what two parts allow, beside a block whose V scale is 2^24 as large 9 times.  It
+// cost a prompt of 8192 tokens 763 -> 953 us (two thirds of that the products), 4 tokens
+// over 131072 79 -> 87, 16 x 4 over 2048 29 -> 34.
 //
 // Tokens that a row does not see have no part in it: their scores become -inf before
 // anything is taken from them, and where a block holds tokens that only some rows
@@ -67,6 +75,7 @@ constexpr int kChUnitRows = 256;
 constexpr float kChLog2e = 1.4426950408889634f;
 constexpr float kChLn2 = 0.6931471805599453f;
 constexpr float kChGrow = 8.f;  // log2 growth of a maximum that rescales O
+constexpr int kChLift = 7;      // log2 of a weight with the score m: up to 2^15 with that growth, which f16 holds
 constexpr float kChMinMult = 1e-37f;  // of a row's scale times K's: -inf times it is -inf still
 __device__ __forceinline__ float at_least_min(float mult) { return mult < kChMinMult ? kChMinMult : mult; }  // (a NaN stays one)
 // Costs in the work list, in some 500 cycles: of a block with both tiles at work and with one, of a unit's start.
@@ -588,7 +597,7 @@ __device__ __forceinline__ void idle_wait(uint32_t bar, uint32_t parity, uint32_
 // ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
-// O += P V over half a block, P from tensor memory: a step is 16 tokens, 8 columns of P and 4 KiB of V.
+// O += P V over half a block, P from tensor memory: a step is 16 tokens, 8 columns of each part of P and 4 KiB of V.
 #define CH_O_STEP(pcol, voff, acc)                                                                  \
   "add.u32 p, %1, " #pcol ";\n\tadd.s64 b, %2, " #voff ";\n\t@e tcgen05.mma.cta_group::1.kind::f16" \
   " [%0], [p], b, %3, " acc ";\n\t"
@@ -596,9 +605,21 @@ __device__ __forceinline__ void issue_half_o(uint32_t d, uint32_t p, uint64_t vd
   asm volatile(
       "{\n\t.reg .pred e, first, yes;\n\t.reg .b32 p;\n\t.reg .b64 b;\n\telect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.u32 first, %4, 0;\n\tsetp.eq.u32 yes, 0, 0;\n\t" CH_O_STEP(0, 0, "first") CH_O_STEP(8, 256, "yes")
-          CH_O_STEP(16, 512, "yes") CH_O_STEP(24, 768, "yes") "}" ::"r"(d),
+          CH_O_STEP(16, 512, "yes") CH_O_STEP(24, 768, "yes") CH_O_STEP(32, 0, "yes") CH_O_STEP(40, 256, "yes")
+              CH_O_STEP(48, 512, "yes") CH_O_STEP(56, 768, "yes") "}" ::"r"(d),
       "r"(p), "l"(vdesc), "r"(kTcOF16), "r"(acc)
       : "memory");
+}
+
+// What rounding to the two f16 of hi left of e, as two f16.  (Mixed-precision products: 8192-token prompt 953 us, with
+// conversions of hi and a packed subtraction 1021.)
+__device__ __forceinline__ uint32_t left_f16x2(float2 e, uint32_t hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b, n;\n\t.reg .f32 x, y;\n\tmov.b32 {a, b}, %1;\n\tmov.b16 n, 0xBC00;\n\t"
+      "fma.rn.f32.f16 x, a, n, %2;\n\tfma.rn.f32.f16 y, b, n, %3;\n\tcvt.rn.f16x2.f32 %0, y, x;\n\t}"
+      : "=r"(r)
+      : "r"(hi), "f"(e.x), "f"(e.y));
+  return r;
 }
 
 // 16 consecutive columns of this thread's tensor memory lane and their largest value (a NaN counts only among
@@ -1250,7 +1271,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             if (both) {
               wait(C::kBarP + 2 * t + 1, n1++);
               tc_fence_after();
-              issue_half_o(od, pd + 32, vd + 1024, 1);
+              issue_half_o(od, pd + 64, vd + 1024, 1);
             }
             commit_elected(bars + 8 * (C::kBarO + t));  // (before S: who sees S knows O's phase to be over)
             begun += begins;
@@ -1384,7 +1405,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
                     tmem_wait_st();
                   }
                 }
-                const float ref = m == -INFINITY ? 0.f : m;
+                const float ref = m == -INFINITY ? 0.f : m - kChLift;
                 // arguments of the next 16 columns beside the powers of these: the powers' pipe is the slow one
                 auto arguments = [&](int g) {
                   const float2 f2 = make_float2(f[g], f[g]), b2 = make_float2(ev[g] - ref, ev[g] - ref);
@@ -1399,18 +1420,20 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                   if (g < 3) arguments(g + 1);
-                  uint32_t w[8];
+                  uint32_t w[8], v[8];
                   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                   for (int k = 0; k < 8; ++k) {
                     const float2 e = make_float2(fast_exp2(__uint_as_float(s[16 * g + 2 * k])), fast_exp2(__uint_as_float(s[16 * g + 2 * k + 1])));
                     sum[k & 1] = add2(sum[k & 1], e);
                     w[k] = pack_f16x2(e.x, e.y);
+                    v[k] = left_f16x2(e, w[k]);
                   }
-                  tmem_st8(ts + 32 * h + 8 * g, w);  // over columns that have been read
+                  tmem_st8(ts + 64 * h + 8 * g, w);  // over columns that have been read
+                  tmem_st8(ts + 64 * h + 32 + 8 * g, v);
                   const float2 x = add2(sum[0], sum[1]);
-                  // 2^-ev, from the integer in the last bits of ev + 1.5 2^23
-                  l = fmaf(x.x + x.y, __int_as_float((0x4B400000 + 127 - __float_as_int(ev[g] + 12582912.f)) << 23), l);
+                  // 2^(-ev - lift), from the integer in the last bits of ev + 1.5 2^23
+                  l = fmaf(x.x + x.y, __int_as_float((0x4B400000 + 127 - kChLift - __float_as_int(ev[g] + 12582912.f)) << 23), l);
                 }
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
@@ -1479,7 +1502,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         const int64_t orow = static_cast<int64_t>(p.u.c0 + token) * a.Hq + p.h * a.G + grow - token * a.G;
         const bool none = l == 0.f;
-        const float inv = whole && !none ? 1.f / l : 1.f;
+        const float inv = exp2_int(-kChLift) * (whole && !none ? 1.f / l : 1.f);
         if (whole && nb > 0 && a.boxed && lrow - lane + 32 <= p.u.rows) {
           // The warp's 32 rows are whole tokens' heads: by way of its rows' place in the query buffer, which has been
           // read, as two boxes of 64 dims (rows of 128 bytes with the 128-byte swizzle).  Stores from registers touch a

@@ -561,7 +561,8 @@ int fpk_paged_decode_attn_bf16(const void* q, const void* kv_pool,
  * fpk_paged_decode_attn_fp8 over a cache with block scales: same arguments but
  * for kv_scales in place of the two scales, same results with each tile's values
  * under its own scales, same workspace (fpk_decode_workspace_bytes), same
- * fail-closed rules, same bits on repeated calls.
+ * fail-closed rules, same bits on repeated calls.  Softmax weights enter as two f16
+ * parts: off by 2^-22 of each, or by 2^-39 of the largest weight times V scale.
  */
 int fpk_paged_decode_attn_fp8_block(const void* q, const uint8_t* kv_pool, const uint8_t* kv_scales,
                                     const int32_t* page_table, int32_t max_pages,
@@ -604,8 +605,9 @@ int fpk_paged_decode_attn_fp8_block(const void* q, const uint8_t* kv_pool, const
  * and kv head) of 2^31 is FPK_EUNSUPPORTED.
  * Precision: scores, sums and O in fp32; the query enters as two e4m3 parts (what
  * they leave out is below 2^-17 of the largest |q| of its row), K exactly; softmax
- * weights enter in f16 (relative to the largest weight times V scale, half a step
- * is 2^-11 of each), V exactly.  Repeated calls on the same inputs give identical
+ * weights enter as two f16 parts (off by 2^-22 of each, or by 2^-32 of the largest
+ * weight times V scale where that is more: below that nothing is left of tokens
+ * under much smaller scales), V exactly.  Repeated calls on the same inputs give identical
  * bits.  One token per request is served better by fpk_paged_decode_attn_fp8_block.
  */
 size_t fpk_prefill_workspace_bytes(int32_t B, int32_t n_tokens, int32_t Hq, int32_t Hkv, int32_t D);
