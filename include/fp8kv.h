@@ -603,12 +603,14 @@ int fpk_paged_decode_attn_fp8_block(const void* q, const uint8_t* kv_pool, const
  * 2^31 tiles, n_tokens * Hq / Hkv of 2^28, a table of more than 2^31 - 128 tokens,
  * or a work list (a table's blocks of 128 tokens, times some 6, for each 256 rows
  * and kv head) of 2^31 is FPK_EUNSUPPORTED.
- * Precision: scores, sums and O in fp32; the query enters as two e4m3 parts (what
- * they leave out is below 2^-17 of the largest |q| of its row), K exactly; softmax
- * weights enter as two f16 parts (off by 2^-22 of each, or by 2^-32 of the largest
- * weight times V scale where that is more: below that nothing is left of tokens
- * under much smaller scales), V exactly.  Repeated calls on the same inputs give identical
- * bits.  One token per request is served better by fpk_paged_decode_attn_fp8_block.
+ * Precision: scores, sums and O in fp32, added up by the tensor cores over 8192
+ * tokens at most, which cut 2^-13 of O off at most, one way; the query enters as
+ * two e4m3 parts (what they leave out is below 2^-17 of the largest |q| of its
+ * row), K exactly; softmax weights enter as two f16 parts (off by 2^-22 of each, or
+ * by 2^-32 of the largest weight times V scale where that is more: below that
+ * nothing is left of tokens under much smaller scales), V exactly.  Repeated calls
+ * on the same inputs give identical bits.  One token per request is served better
+ * by fpk_paged_decode_attn_fp8_block.
  */
 size_t fpk_prefill_workspace_bytes(int32_t B, int32_t n_tokens, int32_t Hq, int32_t Hkv, int32_t D);
 int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu_seqlens, int32_t n_tokens,
