@@ -32,14 +32,14 @@
 // Units of more than 128 rows use both tiles on every block; smaller ones give the
 // two tiles alternate blocks of the same rows, joined at the end in tensor memory.
 //
-// What bounds it: a row tile's chain.  Of 128 tokens its scores take 569 cycles of products, its softmax some 2300
-// (powers, 4 cycles each for a warp, and one warp's latencies), the products of the second half's weights 285, and
-// the next scores overwrite those weights: about 3100, in which both tiles' products are 2280.  64/8 heads: a prompt of
-// 8192 tokens 757 us (1450 TFLOP/s, three quarters of a plain library product's rate), 8192 rows over all of 8192 tokens
-// 1410 us (1560), the last 1024 of 32768 703 us (1540).  Few rows: a start (list, queries, pipeline; 6 us), some
-// 2000 cycles for 128 tokens, an end (3 us): 16 requests of 4 tokens over 2048 27 us, 4 tokens over 131072 77 us.
-// Short prompts: queries in, results out and the piece's start and end come on top (16 x 512: 181 us, of which 40 go
-// when neither queries nor results touch HBM).
+// What bounds it: a row tile's chain.  Of 128 tokens its scores take 569 cycles of products, its softmax some 2700
+// (powers, 4 cycles each for a warp, the weights' second parts, and one warp's latencies), the products of the second
+// half's weights 570, and the next scores overwrite those weights: about 3900, in which both tiles' products are 3420.
+// Replayed from a graph, 64/8 heads: a prompt of 8192 tokens 990 us (1110 TFLOP/s, 58 % of a plain library product's
+// rate; 965 where calls share their inputs), 8192 rows over all of 8192 tokens 1870 us (1180), the last 1024 of 32768
+// 950 us (1140).  Few rows: a start (list, queries, pipeline; 6 us), some 2300 cycles for 128 tokens, an end (3 us):
+// 16 requests of 4 tokens over 2048 33 us, 4 tokens over 131072 85 us.  Short prompts: queries in, results out and the
+// piece's start and end come on top (16 x 512: 212 us, of which some 40 go when neither queries nor results touch HBM).
 //
 // Scales.  Of each tile of 16 tokens (16 columns of S) K's scale multiplies the
 // scores and V's goes into the weights: with ev its exponent, P = 2^(s + ev - m + 7),
@@ -51,7 +51,7 @@
 // attention: 2^-22 of a weight is lost, or 2^-32 of the largest where that is more.
 // With one part 2^-11 of each was: where values cancel, results were 4 times outside
 // what two parts allow, beside a block whose V scale is 2^24 as large 9 times.  It
-// cost a prompt of 8192 tokens 763 -> 953 us (two thirds of that the products), 4 tokens
+// cost a prompt of 8192 tokens 763 -> 953 us (three quarters of that the products), 4 tokens
 // over 131072 79 -> 87, 16 x 4 over 2048 29 -> 34.
 //
 // Tokens that a row does not see have no part in it: their scores become -inf before
@@ -82,11 +82,13 @@ constexpr int kChFold = 64;
 constexpr int kChLift = 7;      // log2 of a weight with the score m: up to 2^15 with that growth, which f16 holds
 constexpr float kChMinMult = 1e-37f;  // of a row's scale times K's: -inf times it is -inf still
 __device__ __forceinline__ float at_least_min(float mult) { return mult < kChMinMult ? kChMinMult : mult; }  // (a NaN stays one)
-// Costs in the work list, in some 500 cycles: of a block with both tiles at work and with one, of a unit's start.
+// Costs in the work list, in some 600 cycles: of a block with both tiles at work and with one, of a unit's start.  (8 and 5,
+// 7 and 4, or starts of 24 and 20: within 2 % where many units are cut, 3 requests of 300 rows over 1000 55 -> 64 us.)
 constexpr int kChCostPair = 6, kChCostSolo = 4;
 constexpr int kChStartPair = 20, kChStartSolo = 16;
-// What cutting units costs a call: another start, partials, their merge (16 requests of 4 tokens over 2048: 32.8 us cut,
-// 28.7 whole; 24 of them, 2 units to a CTA then: 43.0 cut, 48.7 whole; 3 of 300 over 1000: 52.6 and 46.1).
+// What cutting units costs a call: another start, partials, their merge (16 requests of 4 tokens over 2048: 37.2 us cut,
+// 33.0 whole; 24 of them, 2 units to a CTA then: 48.5 cut, 54.5 whole; 3 of 300 over 1000: 62.4 and 55.5; cut by this rule
+// although whole ones would be sooner: 16 prompts of 512, 212 and 190).
 constexpr int kChCut = 48;
 
 constexpr int kChThreads = 512;
@@ -94,9 +96,11 @@ constexpr int kChVWarp = 8, kChLoadWarp = 12, kChMmaWarp = 13, kChPlanWarp = 15;
 constexpr int kChPieces = 4;  // pieces known ahead
 constexpr int kChPlanThreads = 1024;
 constexpr int kChTurnSpins = 4096;
-// Merge: CTAs per cut unit, few where requests have few rows on average.  (4: 16 requests of 32 rows over 2048 tokens
-// 27.2 -> 26.0 us, 32 rows over 131072 79 -> 76, one row 12.5 -> 11.4; 512 rows over 4000 32 -> 48.)
-constexpr int kChMergeWarps = 8, kChMergeFew = 4, kChMergeMany = 16, kChMergeRows = 128;
+// Merge: CTAs per cut unit, few where a call has few rows, or its requests on average.  (4 instead of 16: 16 requests of
+// 32 rows over 2048 tokens 35.0 -> 33.1 us, one token over 4096 22.1 -> 20.7, 16 tokens over 16 18.6 -> 16.5; 512 rows over
+// 4000 39.6 -> 56.3.)  An average says little of a batch of drafts and a chunk: with 128 for both, 60 drafts of 32 rows and
+// a chunk of 4000 rows took 190.8 us instead of 180.5, 20 and one of 1600 98.5 instead of 92.2; 8 of 128 rows lose 33.2 -> 34.9.
+constexpr int kChMergeWarps = 8, kChMergeFew = 4, kChMergeMany = 16, kChMergeAll = 128, kChMergeMean = 64;
 constexpr int kChNear = 1024, kChNearUnits = 4096;    // requests and units that the plan keeps in shared memory
 constexpr int64_t kChSmallRows = 16384, kChSmallPages = 32768;  // of a kv head's rows, and page table entries, without a plan
 
@@ -584,8 +588,8 @@ __device__ __forceinline__ bool next_piece(const ChArgs& a, ChCursor& c, ChPiece
 }
 
 // tc_wait of the softmax warps and of those that work ahead: the hardware may hold one back for a microsecond, so
-// that their looking leaves the issue slots to the others (8192-token prompt 798 -> 776 us; the other warps answer
-// sooner without).
+// that their looking leaves the issue slots to the others (8192-token prompt 798 -> 776 us, with weights in one part; the
+// other warps answer sooner without).
 __device__ __forceinline__ void idle_wait(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* failed) {
   uint32_t ok;
   asm volatile(
@@ -1843,7 +1847,8 @@ extern "C" int fpk_paged_prefill_attn_fp8_block(const void* q, const int32_t* cu
   if ((!a.small && launch_dependent(prefill_plan_kernel, 1, kChPlanThreads, 0, s, a) != FPK_OK) ||
       launch_dependent(prefill_attn_kernel, ctas, kChThreads, ChCfg::kSmem, s, a, kmap, omap) != FPK_OK)
     return FPK_ECUDA;
-  if (static_cast<int64_t>(n_tokens) * G <= static_cast<int64_t>(kChMergeRows) * B)
+  const int64_t rows = static_cast<int64_t>(n_tokens) * G;
+  if (rows <= kChMergeAll || rows <= static_cast<int64_t>(kChMergeMean) * B)
     return launch_dependent(prefill_merge_kernel<kChMergeFew>, ctas * kChMergeFew, 32 * kChMergeWarps, 0, s, a);
   return launch_dependent(prefill_merge_kernel<kChMergeMany>, ctas * kChMergeMany, 32 * kChMergeWarps, 0, s, a);
 }
